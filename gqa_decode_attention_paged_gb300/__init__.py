@@ -91,6 +91,11 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.kv_pool_set_cascade_mode.argtypes = [P, c.c_int32]
         lib.kv_pool_reserve_workspace.argtypes = [P, c.c_int32, c.c_int32, c.c_int32]
         lib.paged_kv_append.argtypes = [P, P, P, P, c.c_int64, P]
+        lib.pkv_rope_create.argtypes = [c.c_int32, c.c_int32, c.c_int32, P, P, c.POINTER(P)]
+        lib.pkv_rope_destroy.argtypes = [P]
+        lib.paged_rope_append.argtypes = [P, P, P, c.c_int64, c.c_int32, P, c.c_int64, P, c.c_int64, P, P, c.c_int64,
+                                          P, c.c_int64, P]
+        lib.paged_kv_gather.argtypes = [P, P, P, c.c_int32, P, c.c_int32, c.c_int64, P, P, P]
         lib.paged_decode_attention.argtypes = [P, P, c.c_int32, P, c.c_int32, P, c.c_int32,
                                                c.c_float, P, P]
         lib.paged_decode_attention_noalloc.argtypes = [P, P, c.c_int32, P, c.c_int32, P, c.c_int32,
@@ -133,8 +138,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         for name in ("kv_pool_create", "kv_pool_destroy", "kv_pool_set_fp8_scales", "kv_pool_set_int4_key_params",
                      "kv_pool_layout",
                      "kv_pool_set_partition_tokens", "kv_pool_set_cascade_mode", "kv_pool_reserve_workspace",
-                     "paged_kv_append",
-                     "paged_decode_attention", "paged_decode_attention_noalloc", "paged_decode_step",
+                     "paged_kv_append", "pkv_rope_create", "pkv_rope_destroy", "paged_rope_append",
+                     "paged_kv_gather", "paged_decode_attention", "paged_decode_attention_noalloc", "paged_decode_step",
                      "paged_decode_attention_csr", "paged_prefill_attention",
                      "paged_decode_step_host", "paged_decode_attention_prefix", "pkv_get_error", "pkv_timing_enable", "pkv_timing_read",
                      "pkv_selftest_wait_timeout", "kv_block_copy", "kv_swap_out", "kv_swap_in", "kv_alloc_create",
@@ -182,6 +187,34 @@ def _dev_ptr(t, name, dtype=None, ndim=None, shape=None):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _pool_ptr(pool, t, name, dtype=None, ndim=None, shape=None):
+    """_dev_ptr, for a tensor that has to be on the pool's device."""
+    p = _dev_ptr(t, name, dtype, ndim, shape)
+    if t.device.index != pool.device:
+        raise ValueError(f"{name} is on {t.device}, the pool on cuda:{pool.device}")
+    return p
+
+
+def _rows_ptr(pool, t, name, heads=None, rows=None):
+    """Pointer and token stride of a bf16 [rows, heads, d_head] tensor whose
+    heads lie side by side (a slice of a wider row is fine)."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda or t.device.index != pool.device:
+        raise ValueError(f"{name} must be on the pool's device cuda:{pool.device}")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    n, h, d = t.shape if t.dim() == 3 else (-1, -1, -1)
+    if d != pool.d_head or (heads is not None and h != heads) or (rows is not None and n != rows):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {heads}, {pool.d_head})")
+    sn, sh, sd = t.stride()
+    if sd != 1 or (h > 1 and sh != d):
+        raise ValueError(f"{name} must hold each token's heads side by side (strides {t.stride()})")
+    return t.data_ptr(), sn if n > 1 else h * d
+
+
 def kv_bytes_per_token(layers: int, n_kv: int, d_head: int, bytes_per_value: float) -> float:
     """2 x layers x n_kv x d_head x bytes_per_value (host arithmetic in the library)."""
     return float(load().kv_bytes_per_token(layers, n_kv, d_head, float(bytes_per_value)))
@@ -194,6 +227,9 @@ class Pool:
         self._h = handle
         self.num_blocks, self.block_size, self.n_kv, self.d_head, self.dtype = (
             num_blocks, block_size, n_kv, d_head, dtype)
+        import torch
+
+        self.device = torch.cuda.current_device()  # where the library allocated it
 
     @property
     def handle(self):
@@ -331,6 +367,109 @@ def paged_kv_append(pool: Pool, k_new, v_new, slot_mapping, stream=None):
     vp = _dev_ptr(v_new, "v_new", torch.bfloat16, 3, shape)
     sp = _dev_ptr(slot_mapping, "slot_mapping", torch.int64, 1)
     _check(load().paged_kv_append(pool.handle, kp, vp, sp, T, _stream_handle(stream)))
+
+
+class Rope:
+    """A rotary embedding: ``inv_freq`` radians per position for each channel
+    pair (rot_dim / 2 numbers, kept in 64 bits), ``pair_axis`` the position
+    axis each pair follows (default: all 0), ``interleaved`` pairs (2i, 2i+1)
+    instead of (i, i + rot_dim / 2)."""
+
+    def __init__(self, inv_freq, pair_axis=None, interleaved: bool = False, n_axes=None):
+        import numpy as np
+
+        self._h = None
+        f = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64).reshape(-1))
+        ax = np.zeros(f.size, np.int32) if pair_axis is None else np.ascontiguousarray(
+            np.asarray(pair_axis, dtype=np.int32).reshape(-1))
+        if ax.size != f.size:
+            raise ValueError(f"pair_axis has {ax.size} entries, inv_freq {f.size}")
+        self.rot_dim, self.interleaved = 2 * f.size, bool(interleaved)
+        self.n_axes = int(n_axes) if n_axes is not None else int(ax.max(initial=0)) + 1
+        h = ctypes.c_void_p()
+        _check(load().pkv_rope_create(self.rot_dim, int(self.interleaved), self.n_axes, f.ctypes.data, ax.ctypes.data,
+                                      ctypes.byref(h)))
+        self._h = h
+
+    @property
+    def handle(self):
+        if not self._h:
+            raise ValueError("rope is closed")
+        return self._h
+
+    def close(self):
+        if getattr(self, "_h", None):
+            load().pkv_rope_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def paged_rope_append(pool: Pool, rope: Rope, q, k_new, v_new, positions, slot_mapping, q_out=None, stream=None):
+    """Turn q [T, n_q, d_head] and k_new [T, n_kv, d_head] by positions
+    (int32 [n_axes, T]), append the turned keys and v_new to slot_mapping
+    (int64 [T]) and return the turned queries (``q_out``, allocated if not
+    given; q itself turns in place).  q may be None: keys and values only.
+    Tokens may be slices of wider rows (a fused projection's output)."""
+    import torch
+
+    T = int(slot_mapping.shape[0])
+    kp, ks = _rows_ptr(pool, k_new, "k_new", pool.n_kv, T)
+    vp, vs = _rows_ptr(pool, v_new, "v_new", pool.n_kv, T)
+    pp = _pool_ptr(pool, positions, "positions", torch.int32, 2, (rope.n_axes, T))
+    sp = _pool_ptr(pool, slot_mapping, "slot_mapping", torch.int64, 1)
+    qp = op = None
+    qs = os_ = n_q = 0
+    if q is not None:
+        n_q = int(q.shape[1]) if q.dim() == 3 else -1
+        qp, qs = _rows_ptr(pool, q, "q", n_q, T)
+        if q_out is None:
+            q_out = torch.empty((T, n_q, pool.d_head), dtype=q.dtype, device=q.device)
+        op, os_ = _rows_ptr(pool, q_out, "q_out", n_q, T)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _check(load().paged_rope_append(pool.handle, rope.handle, qp, qs, n_q, kp, ks, vp, vs, pp, sp, T, op, os_,
+                                    _stream_handle(stream)))
+    return q_out
+
+
+def paged_kv_gather(pool: Pool, out_indptr, block_tables, starts=None, n_rows=None, k_out=None, v_out=None,
+                    stream=None):
+    """Read sequences back: rows out_indptr[b]:out_indptr[b+1] (int32 [B + 1])
+    of the returned bf16 (k, v) [n_rows, n_kv, d_head] are sequence b's
+    positions starts[b] + 0, 1, ... (int32 [B]; None: 0) through
+    block_tables[b] (int32 [B, W]).  ``n_rows`` or ``k_out`` and ``v_out`` have
+    to be given; rows no sequence covers are left as they were (whatever
+    was there, in arrays allocated here)."""
+    import torch
+
+    ip = _pool_ptr(pool, out_indptr, "out_indptr", torch.int32, 1)
+    B = int(out_indptr.shape[0]) - 1
+    if B < 0:
+        raise ValueError("out_indptr must have at least one entry")
+    tp = _pool_ptr(pool, block_tables, "block_tables", torch.int32, 2, (B, None))
+    st = None if starts is None else _pool_ptr(pool, starts, "starts", torch.int32, 1, (B,))
+    if (k_out is None) != (v_out is None):
+        raise ValueError("give both k_out and v_out, or neither")
+    if k_out is None:
+        if n_rows is None:
+            raise ValueError("give n_rows, or k_out and v_out")
+        shape = (int(n_rows), pool.n_kv, pool.d_head)
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=out_indptr.device)
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=out_indptr.device)
+    n = int(k_out.shape[0])
+    if n_rows is not None and n != int(n_rows):
+        raise ValueError(f"k_out has {n} rows, n_rows is {n_rows}")
+    shape = (n, pool.n_kv, pool.d_head)
+    kp = _pool_ptr(pool, k_out, "k_out", torch.bfloat16, 3, shape)
+    vp = _pool_ptr(pool, v_out, "v_out", torch.bfloat16, 3, shape)
+    _check(load().paged_kv_gather(pool.handle, ip, tp, int(block_tables.shape[1]), st, B, n, kp, vp,
+                                  _stream_handle(stream)))
+    return k_out, v_out
 
 
 def paged_decode_attention(pool: Pool, q, block_tables, context_lens, scale: float, out=None,
@@ -650,6 +789,6 @@ class BlockAllocator:
 __all__ = ["BF16", "FP8_E4M3", "INT4", "Pool", "PagedKVError", "kv_pool_create", "paged_kv_append",
            "paged_decode_attention", "paged_decode_attention_noalloc", "paged_decode_step",
            "paged_decode_step_host", "paged_decode_attention_prefix", "paged_decode_attention_csr",
-           "paged_prefill_attention",
+           "paged_prefill_attention", "Rope", "paged_rope_append", "paged_kv_gather",
            "kv_bytes_per_token", "kv_block_bytes", "kv_swap_entry_bytes",
            "kv_block_copy", "kv_swap_out", "kv_swap_in", "BlockAllocator", "load", "library_path"]

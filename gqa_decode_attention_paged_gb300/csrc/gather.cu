@@ -1,0 +1,273 @@
+// Reading the cache back: the rows of a batch of sequences, found through
+// their block tables, widened to bf16 and laid one after the other.
+//
+// Mathematics: bf16(x) of what a stored row stands for -- the row itself
+// (bf16 pools), E4M3 * scale[g] (FP8), code * scale + zero point (4-bit:
+// per-channel parameters for keys, the row's own for values) -- in fp32,
+// rounded once.
+//
+// What bounds it: HBM.  A row is read once and written once.  A CTA takes a
+// tile of consecutive output rows and up to 32 KV heads; its first threads
+// find their rows' sequences (binary search in out_indptr) and pool entries
+// all at once, then every thread keeps one (head, 16 channels) for all rows
+// of the tile, so that its scales and, for 4-bit pools, its 32 channel
+// parameters stay in registers and no index is divided in the loop.
+#include <algorithm>
+
+#include "pkv_internal.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kGatherThreads = 256;
+constexpr int kMaxTile = 64;   // output rows of a CTA
+constexpr int kMaxHeads = 32;  // KV heads of a CTA
+
+struct GatherArgs {
+    const uint8_t *pool;
+    int64_t num_blocks;
+    int n_kv;
+    const int32_t *out_indptr;  // [batch + 1]
+    const int32_t *block_tables;
+    int W;
+    const int32_t *starts;      // [batch], or null: 0
+    int batch;
+    int64_t n_rows;
+    const float *scales, *k_params;
+    __nv_bfloat16 *k_out, *v_out;  // [n_rows][n_kv][D]
+    int tile, heads;               // rows and heads of a CTA
+    unsigned *err;
+};
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Four E4M3 bytes times s, as two bf16 pairs.
+__device__ __forceinline__ uint2 e4m3x4_to_bf16x4(uint32_t x, float s)
+{
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    return make_uint2(bf16x2(f.x * s, f.y * s), bf16x2(h.x * s, h.y * s));
+}
+
+// 16 channels of one stored row, as they are read: 32, 16 or 8 bytes.
+template <int KV>
+struct Raw {
+    uint4 a, b;
+};
+
+template <int KV>
+__device__ __forceinline__ void load_raw(Raw<KV> &x, const uint8_t *p)
+{
+    if constexpr (KV == PKV_BF16) {
+        x.a = ldg_nc_v4(p);
+        x.b = ldg_nc_v4(p + 16);
+    } else if constexpr (KV == PKV_FP8_E4M3) {
+        x.a = ldg_nc_v4(p);
+    } else {
+        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+        x.a = make_uint4(v.x, v.y, 0, 0);
+    }
+}
+
+template <int D, int KV>
+__global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_constant__ GatherArgs a)
+{
+    constexpr int LPR = D / 16;  // lanes per (row, head)
+    constexpr int ROWB = KV == PKV_BF16 ? 2 * D : KV == PKV_FP8_E4M3 ? D : D / 2;
+    constexpr int64_t ENTRY = kv_entry_bytes(KV, D);
+    constexpr int UNROLL = 4;
+    __shared__ int64_t place[kMaxTile];  // block * n_kv * 16 + offset in the block; -1: zeros; -2: no row of any sequence
+    griddep_wait();
+    griddep_launch_dependents();
+    const int tid = threadIdx.x;
+    const int64_t row0 = (int64_t)blockIdx.x * a.tile;
+    const int n = (int)min((int64_t)a.tile, a.n_rows - row0);
+    if (tid < n) {
+        const int32_t row = (int32_t)(row0 + tid);
+        // the last sequence that begins at or before this row: empty ones before it begin there too
+        int lo = 0, hi = a.batch;  // out_indptr[lo] <= row < out_indptr[hi], where the rows are covered
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.out_indptr[mid] <= row) lo = mid; else hi = mid;
+        }
+        const int32_t first = a.out_indptr[lo];
+        int64_t at = -2;
+        if (first <= row && row < a.out_indptr[lo + 1]) {
+            at = -1;
+            const int64_t pos = (int64_t)(a.starts ? a.starts[lo] : 0) + ((int64_t)row - first);
+            if (pos < 0 || pos >= (int64_t)a.W * kBlockSize) {
+                atomicOr(a.err, PKV_DEVERR_CTX_RANGE);
+            } else {
+                const int32_t blk = a.block_tables[(int64_t)lo * a.W + pos / kBlockSize];
+                if (blk < 0 || blk >= a.num_blocks) atomicOr(a.err, PKV_DEVERR_BLOCK_RANGE);
+                else at = (int64_t)blk * a.n_kv * kBlockSize + pos % kBlockSize;
+            }
+        }
+        place[tid] = at;
+    }
+    __syncthreads();
+
+    const int h0 = blockIdx.y * a.heads;
+    const int hn = min(a.heads, a.n_kv - h0);
+    const int lanes = hn * LPR;               // threads of one output row
+    const int per = kGatherThreads / lanes;   // rows a step takes
+    const int sub = tid / lanes;
+    if (sub >= per) return;
+    const int u = tid - sub * lanes;
+    const int g = h0 + u / LPR, c = 16 * (u % LPR);
+    [[maybe_unused]] float ks[16], kz[16];
+    [[maybe_unused]] float fk = 1.0f, fv = 1.0f;
+    if constexpr (KV == PKV_INT4) {
+        const float *p = a.k_params + (int64_t)g * D + c;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            ks[i] = p[i];
+            kz[i] = p[(int64_t)a.n_kv * D + i];
+        }
+    } else if constexpr (KV == PKV_FP8_E4M3) {
+        fk = a.scales[g];
+        fv = a.scales[a.n_kv + g];
+    }
+    for (int i0 = sub; i0 < n; i0 += UNROLL * per) {
+        Raw<KV> k[UNROLL], v[UNROLL];
+        [[maybe_unused]] float2 vp[UNROLL];
+        int64_t at[UNROLL];
+#pragma unroll
+        for (int x = 0; x < UNROLL; ++x) {
+            const int i = i0 + x * per;
+            at[x] = i < n ? place[i] : -2;
+            if (at[x] < 0) continue;
+            const int64_t blk_u = at[x] / kBlockSize;  // block * n_kv
+            const int off = (int)(at[x] % kBlockSize);
+            const uint8_t *entry = a.pool + (blk_u + g) * ENTRY;
+            const uint8_t *src = entry + off * ROWB + c * ROWB / D;
+            load_raw<KV>(k[x], src);
+            load_raw<KV>(v[x], src + kBlockSize * ROWB);
+            if constexpr (KV == PKV_INT4)
+                vp[x] = __ldg(reinterpret_cast<const float2 *>(entry + i4_params_offset(D) + 8 * off));
+        }
+#pragma unroll
+        for (int x = 0; x < UNROLL; ++x) {
+            if (at[x] == -2) continue;
+            uint4 ko[2], vo[2];
+            if (at[x] < 0) {
+                ko[0] = ko[1] = vo[0] = vo[1] = make_uint4(0, 0, 0, 0);
+            } else if constexpr (KV == PKV_BF16) {
+                ko[0] = k[x].a;
+                ko[1] = k[x].b;
+                vo[0] = v[x].a;
+                vo[1] = v[x].b;
+            } else if constexpr (KV == PKV_FP8_E4M3) {
+                const uint32_t kw[4] = {k[x].a.x, k[x].a.y, k[x].a.z, k[x].a.w};
+                const uint32_t vw[4] = {v[x].a.x, v[x].a.y, v[x].a.z, v[x].a.w};
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint2 k0 = e4m3x4_to_bf16x4(kw[2 * i], fk), k1 = e4m3x4_to_bf16x4(kw[2 * i + 1], fk);
+                    const uint2 v0 = e4m3x4_to_bf16x4(vw[2 * i], fv), v1 = e4m3x4_to_bf16x4(vw[2 * i + 1], fv);
+                    ko[i] = make_uint4(k0.x, k0.y, k1.x, k1.y);
+                    vo[i] = make_uint4(v0.x, v0.y, v1.x, v1.y);
+                }
+            } else {
+                const uint32_t kw[2] = {k[x].a.x, k[x].a.y}, vw[2] = {v[x].a.x, v[x].a.y};
+                uint32_t kp[8], vq[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t kb = kw[i / 4] >> (8 * (i % 4)), vb = vw[i / 4] >> (8 * (i % 4));
+                    kp[i] = bf16x2(fmaf((float)(kb & 15u), ks[2 * i], kz[2 * i]),
+                                   fmaf((float)((kb >> 4) & 15u), ks[2 * i + 1], kz[2 * i + 1]));
+                    vq[i] = bf16x2(fmaf((float)(vb & 15u), vp[x].x, vp[x].y),
+                                   fmaf((float)((vb >> 4) & 15u), vp[x].x, vp[x].y));
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    ko[i] = make_uint4(kp[4 * i], kp[4 * i + 1], kp[4 * i + 2], kp[4 * i + 3]);
+                    vo[i] = make_uint4(vq[4 * i], vq[4 * i + 1], vq[4 * i + 2], vq[4 * i + 3]);
+                }
+            }
+            const int64_t dst = ((row0 + i0 + x * per) * a.n_kv + g) * D + c;
+            *reinterpret_cast<uint4 *>(a.k_out + dst) = ko[0];
+            *reinterpret_cast<uint4 *>(a.k_out + dst + 8) = ko[1];
+            *reinterpret_cast<uint4 *>(a.v_out + dst) = vo[0];
+            *reinterpret_cast<uint4 *>(a.v_out + dst + 8) = vo[1];
+        }
+    }
+}
+
+template <int D>
+cudaError_t launch_gather(const GatherArgs &a, int kv, dim3 grid, cudaStream_t s)
+{
+    if (kv == PKV_BF16) return launch_pdl(gather_kernel<D, PKV_BF16>, grid, dim3(kGatherThreads), 0, s, a);
+    if (kv == PKV_FP8_E4M3) return launch_pdl(gather_kernel<D, PKV_FP8_E4M3>, grid, dim3(kGatherThreads), 0, s, a);
+    return launch_pdl(gather_kernel<D, PKV_INT4>, grid, dim3(kGatherThreads), 0, s, a);
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" pkv_status paged_kv_gather(pkv_pool *pool, const int32_t *out_indptr, const int32_t *block_tables,
+                                      int32_t max_blocks_per_seq, const int32_t *starts, int32_t batch,
+                                      int64_t n_rows, void *k_out, void *v_out, void *stream)
+{
+    const char *who = "paged_kv_gather";
+    if (!pool) return fail(PKV_EINVAL, "%s: NULL pool", who);
+    if (batch < 0) return fail(PKV_EINVAL, "%s: batch < 0", who);
+    if (n_rows < 0) return fail(PKV_EINVAL, "%s: n_rows < 0", who);
+    if (n_rows > INT32_MAX) return fail(PKV_EUNSUPPORTED, "%s: more than 2^31 rows", who);
+    if (max_blocks_per_seq <= 0 || max_blocks_per_seq > (1 << 24))
+        return fail(PKV_EINVAL, "%s: max_blocks_per_seq %d out of range", who, max_blocks_per_seq);
+    if (pool->dtype != PKV_BF16 && !pool->scales_set)
+        return fail(PKV_EINVAL, "%s: quantised pool needs its scales first (kv_pool_set_fp8_scales or "
+                    "kv_pool_set_int4_key_params)", who);
+    if (batch == 0 || n_rows == 0) return PKV_OK;
+    if (!out_indptr || !block_tables || !k_out || !v_out) return fail(PKV_EINVAL, "%s: NULL device pointer", who);
+    if (((uintptr_t)k_out | (uintptr_t)v_out) & 15u)
+        return fail(PKV_EINVAL, "%s: k_out and v_out must be 16-byte aligned", who);
+    if (((uintptr_t)out_indptr | (uintptr_t)block_tables | (uintptr_t)starts) & 3u)
+        return fail(PKV_EINVAL, "%s: indptr, tables and starts must be 4-byte aligned", who);
+    const uint64_t out_bytes = (uint64_t)n_rows * pool->n_kv * pool->d_head * 2;
+    if ((uintptr_t)k_out < (uintptr_t)v_out + out_bytes && (uintptr_t)v_out < (uintptr_t)k_out + out_bytes)
+        return fail(PKV_EINVAL, "%s: k_out and v_out overlap", who);
+    pkv_status st = check_pool_device(pool, who);
+    if (st != PKV_OK) return st;
+    GatherArgs a;
+    a.pool = static_cast<const uint8_t *>(pool->k);
+    a.num_blocks = pool->num_blocks;
+    a.n_kv = pool->n_kv;
+    a.out_indptr = out_indptr;
+    a.block_tables = block_tables;
+    a.W = max_blocks_per_seq;
+    a.starts = starts;
+    a.batch = batch;
+    a.n_rows = n_rows;
+    a.scales = pool->scales;
+    a.k_params = pool->k_params;
+    a.k_out = static_cast<__nv_bfloat16 *>(k_out);
+    a.v_out = static_cast<__nv_bfloat16 *>(v_out);
+    a.err = pool->err;
+    a.heads = std::min(pool->n_kv, kMaxHeads);
+    // Tile: one step of rows (as many as the CTA's threads hold at once) while that gives no more
+    // than two CTAs per SM, then longer tiles, which pay the search for the rows' places less often.
+    const int per = kGatherThreads / (a.heads * (pool->d_head / 16));
+    const int64_t target = (int64_t)pool->num_sms * 2;
+    const int64_t tile = std::max<int64_t>(per, n_rows / target);
+    a.tile = (int)std::min<int64_t>(kMaxTile, tile);
+    const dim3 grid((unsigned)((n_rows + a.tile - 1) / a.tile), (unsigned)((pool->n_kv + a.heads - 1) / a.heads));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    LaunchScope ls(pool, kBlocks, s);
+    cudaError_t e = pool->d_head == 128 ? launch_gather<128>(a, pool->dtype, grid, s)
+                                        : launch_gather<64>(a, pool->dtype, grid, s);
+    ls.done();
+    if (e != cudaSuccess) return cuda_fail(e, "paged_kv_gather launch");
+    return PKV_OK;
+}

@@ -166,6 +166,10 @@ constexpr unsigned kFull = 0xffffffffu;
 pkv_status check_step_args(const pkv_pool *pool, const char *who, int n_q, int max_blocks_per_seq, int batch,
                            float scale);
 
+// PKV_EINVAL unless the pool's device is the current one: a launch goes to the
+// current device, where the pool's memory is not.
+pkv_status check_pool_device(const pkv_pool *pool, const char *who);
+
 // ---------------------------------------------------------------------------
 // Device helpers (inline PTX)
 // ---------------------------------------------------------------------------

@@ -55,6 +55,16 @@ void LaunchScope::done()
     pool->pending.push_back(EventPair{a, b, kind});
 }
 
+pkv_status check_pool_device(const pkv_pool *pool, const char *who)
+{
+    int cur = -1;
+    cudaError_t e = cudaGetDevice(&cur);
+    if (e != cudaSuccess) return cuda_fail(e, who);
+    if (cur != pool->device)
+        return fail(PKV_EINVAL, "%s: make the pool's device (%d) current, not %d", who, pool->device, cur);
+    return PKV_OK;
+}
+
 pkv_status ensure_workspace(pkv_pool *pool, size_t bytes)
 {
     if (bytes <= pool->ws_bytes) return PKV_OK;

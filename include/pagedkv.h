@@ -199,6 +199,85 @@ pkv_status kv_pool_reserve_workspace(pkv_pool *pool, int32_t batch, int32_t n_q,
 pkv_status paged_kv_append(pkv_pool *pool, const void *k_new, const void *v_new,
                            const int64_t *slot_mapping, int64_t n_tokens, void *stream);
 
+/* A rotary embedding: which channel pairs of a head turn, how fast, and with
+ * which of a token's positions.  Opaque host handle; may be shared by pools
+ * and threads once created. */
+typedef struct pkv_rope pkv_rope;
+
+/* Create a rotary embedding over the first rot_dim channels of each head
+ * (the rest pass through unturned).  Pair i, 0 <= i < rot_dim / 2, is the
+ * channels (i, i + rot_dim / 2), or (2i, 2i + 1) where interleaved is 1.  It
+ * turns by positions[pair_axis[i]] * inv_freq[i] radians: with one axis, the
+ * usual rotary embedding; with several, each pair follows its own axis, for
+ * instance time, height and width of an image or video token, in whatever
+ * sections or interleaving pair_axis gives.
+ *   rot_dim    16, 32, ..., 128.
+ *   n_axes     1 .. 8.
+ *   inv_freq   host, rot_dim / 2 doubles; finite, at most 2^20 in size.
+ *   pair_axis  host, rot_dim / 2 axis numbers in [0, n_axes); NULL: all 0.
+ * Errors: EINVAL, EUNSUPPORTED (rot_dim), ENOMEM. */
+pkv_status pkv_rope_create(int32_t rot_dim, int32_t interleaved, int32_t n_axes, const double *inv_freq,
+                           const int32_t *pair_axis, pkv_rope **out);
+/* NULL is accepted.  Calls already enqueued hold their own copy. */
+pkv_status pkv_rope_destroy(pkv_rope *rope);
+
+/* Append with rotary positions: turn each token's queries and keys by its
+ * positions, write the turned key row and the value row into the token's
+ * slot as paged_kv_append does, and write the turned queries to q_out.  One
+ * launch in place of a rotation and an append.
+ *   q, k_new, v_new  device bf16: token t's heads at t * (q|k|v)_stride
+ *                 elements, each head's d_head values side by side, heads
+ *                 one after the other ([n_q][d_head], [n_kv][d_head] twice):
+ *                 slices of one fused projection output are fine.  16-byte
+ *                 aligned, strides multiples of 8 and at least the token's
+ *                 heads.  n_q need not be a multiple of n_kv; n_q == 0: keys
+ *                 and values only (q and q_out may be NULL).
+ *   positions     device int32 [n_axes][n_tokens], any values (negative and
+ *                 far ones too: angles are good to 2^-32 of a turn).
+ *   slot_mapping  device int64 [n_tokens], as paged_kv_append: a negative
+ *                 slot writes no cache row, a slot past the pool neither and
+ *                 sets PKV_DEVERR_SLOT_RANGE.  The queries of such tokens are
+ *                 turned all the same.  Two tokens with the same slot in one
+ *                 call leave each of its parts from either one (unspecified).
+ *   q_out         device bf16, rows at q_out_stride elements; may be q itself
+ *                 with the same stride (in place), and must not share memory
+ *                 with q, k_new or v_new otherwise.
+ * The rotation is computed in fp32 and rounded once, to bf16 or, in FP8 and
+ * 4-bit pools, straight to E4M3(x / scale[g]) or the 4-bit code; values are
+ * stored exactly as paged_kv_append stores them.  n_tokens == 0 is a no-op.
+ * Counted with the append launches (pkv_timing).
+ * Errors: EINVAL (null, misaligned or overlapping arrays, strides, rot_dim
+ * above the pool's d_head, scales unset, the pool's device not current),
+ * EUNSUPPORTED (2^31 tokens or more), ECUDA. */
+pkv_status paged_rope_append(pkv_pool *pool, const pkv_rope *rope, const void *q, int64_t q_stride, int32_t n_q,
+                             const void *k_new, int64_t k_stride, const void *v_new, int64_t v_stride,
+                             const int32_t *positions, const int64_t *slot_mapping, int64_t n_tokens, void *q_out,
+                             int64_t q_out_stride, void *stream);
+
+/* Read the cache back: the keys and values of a batch of sequences, found
+ * through their block tables, as bf16 rows one after the other (the inverse
+ * of an append: to hand a cache to another kernel, to check or to move it).
+ *   out_indptr    device int32 [batch + 1], ascending: sequence b fills rows
+ *                 out_indptr[b] .. out_indptr[b+1]; row out_indptr[b] + i is
+ *                 its position starts[b] + i.
+ *   block_tables  device int32 [batch][max_blocks_per_seq]; entries no row
+ *                 needs are not read.
+ *   starts        device int32 [batch]; NULL: all 0.
+ *   k_out, v_out  device bf16 [n_rows][n_kv][d_head], 16-byte aligned, not
+ *                 overlapping.  Rows that no sequence covers (behind
+ *                 out_indptr[batch] or before out_indptr[0]) stay as they
+ *                 were; rows past n_rows are not written.
+ * A row is what its stored form stands for, computed in fp32 and rounded once
+ * to bf16: the row itself (bf16 pools), E4M3 * scale[g] (FP8), code * scale +
+ * zero point (4-bit).  A position outside [0, max_blocks_per_seq * 16) gives
+ * a row of zeros and sets PKV_DEVERR_CTX_RANGE; a block id outside the pool
+ * gives zeros and sets PKV_DEVERR_BLOCK_RANGE.  One launch, counted with the
+ * block launches (pkv_timing).  batch == 0 or n_rows == 0 is a no-op.
+ * Errors: EINVAL, EUNSUPPORTED (2^31 rows or more), ECUDA. */
+pkv_status paged_kv_gather(pkv_pool *pool, const int32_t *out_indptr, const int32_t *block_tables,
+                           int32_t max_blocks_per_seq, const int32_t *starts, int32_t batch, int64_t n_rows,
+                           void *k_out, void *v_out, void *stream);
+
 /* Decode attention for one new query token per sequence:
  *   out[b][h] = sum_p softmax_p(scale * q[b][h] . K_b[p][g]) V_b[p][g]
  * over positions p < context_lens[b] of sequence b, with g = h / (n_q/n_kv)
