@@ -63,6 +63,11 @@ class _Timing(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_int64)]
 
 
+class _DiffParams(ctypes.Structure):
+    _fields_ = [("lambdas", ctypes.c_void_p), ("norm_weight", ctypes.c_void_p), ("lambda_init", ctypes.c_float),
+                ("eps", ctypes.c_float)]
+
+
 def library_path() -> str:
     return _build.LIB
 
@@ -105,6 +110,9 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.paged_decode_attention_csr.argtypes = [P, P, c.c_int32, P, P, c.c_int64, P, c.c_int32, c.c_float, P, P]
         lib.paged_prefill_attention.argtypes = [P, P, c.c_int64, c.c_int32, P, P, c.c_int32, P, c.c_int32,
                                                 c.c_float, P, P]
+        lib.paged_diff_decode_attention.argtypes = [P, P, c.c_int32, P, c.c_int32, P, c.c_int32, c.c_float,
+                                                    c.POINTER(_DiffParams), P, P]
+        lib.paged_diff_reserve_workspace.argtypes = [P, c.c_int32, c.c_int32, c.c_int32]
         lib.paged_decode_step.argtypes = [P, P, P, P, c.c_int32, P, c.c_int32, P, c.c_int32, c.c_float, P, P]
         lib.paged_decode_step_host.argtypes = [P, P, P, P, c.c_int32, P, c.c_int32, P, c.c_int32, c.c_float,
                                                P, P]
@@ -139,7 +147,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                      "kv_pool_layout",
                      "kv_pool_set_partition_tokens", "kv_pool_set_cascade_mode", "kv_pool_reserve_workspace",
                      "paged_kv_append", "pkv_rope_create", "pkv_rope_destroy", "paged_rope_append",
-                     "paged_kv_gather", "paged_decode_attention", "paged_decode_attention_noalloc", "paged_decode_step",
+                     "paged_kv_gather", "paged_diff_decode_attention", "paged_diff_reserve_workspace",
+                     "paged_decode_attention", "paged_decode_attention_noalloc", "paged_decode_step",
                      "paged_decode_attention_csr", "paged_prefill_attention",
                      "paged_decode_step_host", "paged_decode_attention_prefix", "pkv_get_error", "pkv_timing_enable", "pkv_timing_read",
                      "pkv_selftest_wait_timeout", "kv_block_copy", "kv_swap_out", "kv_swap_in", "kv_alloc_create",
@@ -300,6 +309,10 @@ class Pool:
 
     def reserve_workspace(self, batch: int, n_q: int, max_blocks_per_seq: int):
         _check(load().kv_pool_reserve_workspace(self.handle, batch, n_q, max_blocks_per_seq))
+
+    def reserve_diff_workspace(self, batch: int, n_q: int, max_blocks_per_seq: int):
+        """Grow the workspace for paged_diff_decode_attention calls up to these sizes (before capturing one)."""
+        _check(load().paged_diff_reserve_workspace(self.handle, batch, n_q, max_blocks_per_seq))
 
     def get_error(self, clear: bool = False) -> int:
         bits = ctypes.c_uint32(0)
@@ -528,6 +541,58 @@ def paged_prefill_attention(pool: Pool, q, qo_indptr, block_tables, context_lens
     op = _dev_ptr(out, "out", torch.bfloat16, 3, tuple(q.shape))
     _check(load().paged_prefill_attention(pool.handle, qp, rows, n_q, ip, tp, int(block_tables.shape[1]), cp, B,
                                           float(scale), op, _stream_handle(stream)))
+    return out
+
+
+class DiffParams:
+    """The learned weights of a layer's differential attention: ``lambdas``
+    fp32 CUDA [4, d_head], ``lambda_init``, ``norm_weight`` fp32 CUDA
+    [2 * d_head] (None: ones) and the norm's ``eps``.  Holds the tensors."""
+
+    def __init__(self, lambdas, lambda_init: float, norm_weight=None, eps: float = 1e-5):
+        import torch
+
+        lp = _dev_ptr(lambdas, "lambdas", torch.float32, 2, (4, None))
+        self.d_head = int(lambdas.shape[1])
+        wp = None if norm_weight is None else _dev_ptr(norm_weight, "norm_weight", torch.float32, 1, (2 * self.d_head,))
+        if norm_weight is not None and norm_weight.device != lambdas.device:
+            raise ValueError("lambdas and norm_weight are on different devices")
+        self.lambdas, self.norm_weight, self.lambda_init, self.eps = lambdas, norm_weight, float(lambda_init), float(eps)
+        self._c = _DiffParams(lp, wp, self.lambda_init, self.eps)
+        self._ref = ctypes.byref(self._c)
+
+
+def _diff_args(pool, q, params, rows):
+    """Checks shared by the differential calls; (q pointer, n_q, out shape)."""
+    import torch
+
+    qp = _pool_ptr(pool, q, "q", torch.bfloat16, 3, (rows, None, pool.d_head))
+    if not isinstance(params, DiffParams):
+        raise TypeError("params must be a DiffParams")
+    if params.d_head != pool.d_head or params.lambdas.device.index != pool.device:
+        raise ValueError(f"params are for d_head {params.d_head} on {params.lambdas.device}, the pool has d_head "
+                         f"{pool.d_head} on cuda:{pool.device}")
+    n_q = int(q.shape[1])
+    return qp, n_q, (int(q.shape[0]), n_q // 2, 2 * pool.d_head)
+
+
+def paged_diff_decode_attention(pool: Pool, q, block_tables, context_lens, scale: float, params: DiffParams,
+                                out=None, stream=None):
+    """Differential decode attention.  q: bf16 [B, n_q, d_head], rows 2h and
+    2h + 1 the two queries of head h; block_tables: int32 [B, W];
+    context_lens: int32 [B].  Returns ``out`` (bf16 [B, n_q / 2, 2 * d_head],
+    allocated if not given)."""
+    import torch
+
+    cp = _pool_ptr(pool, context_lens, "context_lens", torch.int32, 1)
+    B = int(context_lens.shape[0])
+    qp, n_q, shape = _diff_args(pool, q, params, B)
+    tp = _pool_ptr(pool, block_tables, "block_tables", torch.int32, 2, (B, None))
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+    op = _pool_ptr(pool, out, "out", torch.bfloat16, 3, shape)
+    _check(load().paged_diff_decode_attention(pool.handle, qp, n_q, tp, int(block_tables.shape[1]), cp, B,
+                                              float(scale), params._ref, op, _stream_handle(stream)))
     return out
 
 
@@ -790,5 +855,6 @@ __all__ = ["BF16", "FP8_E4M3", "INT4", "Pool", "PagedKVError", "kv_pool_create",
            "paged_decode_attention", "paged_decode_attention_noalloc", "paged_decode_step",
            "paged_decode_step_host", "paged_decode_attention_prefix", "paged_decode_attention_csr",
            "paged_prefill_attention", "Rope", "paged_rope_append", "paged_kv_gather",
+           "DiffParams", "paged_diff_decode_attention",
            "kv_bytes_per_token", "kv_block_bytes", "kv_swap_entry_bytes",
            "kv_block_copy", "kv_swap_out", "kv_swap_in", "BlockAllocator", "load", "library_path"]

@@ -93,6 +93,7 @@ struct pkv_pool {
     unsigned *err = nullptr;          // device sticky error word
     void *ws = nullptr;               // split-KV workspace (grow-only)
     size_t ws_bytes = 0;
+    std::vector<void *> old_ws;       // workspaces replaced by larger ones (graphs may use them)
     void *stage = nullptr;            // device staging for paged_decode_step_host (grow-only)
     size_t stage_bytes = 0;
     int partition_tokens = pkv::kDefaultPartitionTokens;
@@ -133,7 +134,11 @@ struct LaunchScope {
     void done();
 };
 
+// Grows the workspace to `bytes` at least.  The one it replaces is kept until
+// the pool is destroyed: a captured graph may still use it.
 pkv_status ensure_workspace(pkv_pool *pool, size_t bytes);
+// The same, refused (PKV_EINVAL) where it would have to allocate while `s` is captured.
+pkv_status ensure_workspace(pkv_pool *pool, size_t bytes, cudaStream_t s, const char *who);
 // The device address of paged_decode_attention_noalloc's scratch array on the
 // current device (cudaGetSymbolAddress; loads the decode code if it is not
 // loaded yet, which reserves the array's memory).

@@ -5,6 +5,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
 #include <new>
 
 #include <cudaTypedefs.h>
@@ -68,21 +69,28 @@ pkv_status check_pool_device(const pkv_pool *pool, const char *who)
 pkv_status ensure_workspace(pkv_pool *pool, size_t bytes)
 {
     if (bytes <= pool->ws_bytes) return PKV_OK;
-    size_t want = bytes + bytes / 4;  // grow with headroom
+    // grow with headroom; at least doubling keeps all replaced workspaces together below the current one
+    size_t want = std::max(bytes + bytes / 4, 2 * pool->ws_bytes);
     want = (want + (1u << 20) - 1) & ~size_t((1u << 20) - 1);
-    if (pool->ws) {
-        cudaError_t e = cudaFree(pool->ws);  // synchronises: no kernel still uses it
-        pool->ws = nullptr;
-        pool->ws_bytes = 0;
-        if (e != cudaSuccess) return cuda_fail(e, "cudaFree(workspace)");
-    }
-    cudaError_t e = cudaMalloc(&pool->ws, want);
-    if (e != cudaSuccess) {
-        pool->ws = nullptr;
-        return cuda_fail(e, "cudaMalloc(workspace)");
-    }
+    void *fresh = nullptr;
+    cudaError_t e = cudaMalloc(&fresh, want);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(workspace)");
+    if (pool->ws) pool->old_ws.push_back(pool->ws);  // captured graphs may still use it
+    pool->ws = fresh;
     pool->ws_bytes = want;
     return PKV_OK;
+}
+
+pkv_status ensure_workspace(pkv_pool *pool, size_t bytes, cudaStream_t s, const char *who)
+{
+    if (bytes <= pool->ws_bytes) return PKV_OK;
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(s, &cap);
+    if (e != cudaSuccess) cudaGetLastError();
+    if (e != cudaSuccess || cap != cudaStreamCaptureStatusNone)
+        return fail(PKV_EINVAL, "%s: the workspace has to grow to %zu bytes while the stream is captured; reserve it "
+                    "first", who, bytes);
+    return ensure_workspace(pool, bytes);
 }
 
 pkv_status ensure_staging(pkv_pool *pool, size_t bytes)
@@ -316,6 +324,7 @@ pkv_status kv_pool_destroy(pkv_pool *pool)
     cudaFree(pool->k_params);
     cudaFree(pool->err);
     cudaFree(pool->ws);
+    for (void *w : pool->old_ws) cudaFree(w);
     cudaFree(pool->stage);
     if (pool->host_graph) cudaGraphExecDestroy(pool->host_graph);
     if (pool->capture_stream) cudaStreamDestroy(pool->capture_stream);

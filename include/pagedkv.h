@@ -438,6 +438,58 @@ pkv_status paged_prefill_attention(pkv_pool *pool, const void *q, int64_t n_rows
                                    const int32_t *qo_indptr, const int32_t *block_tables, int32_t max_blocks_per_seq,
                                    const int32_t *context_lens, int32_t batch, float scale, void *out, void *stream);
 
+/* ---------------------------------------------------------------------
+ * Differential attention over the paged cache: each head is the difference
+ * of two softmax maps, the second weighted by a learned lambda, followed by a
+ * norm of the head's output.  KV heads come in pairs (2p, 2p + 1), so the
+ * pool's n_kv must be even: the pair's two key heads are the keys of the two
+ * maps, its two value heads side by side are one value head of 2 d_head
+ * channels ([n_kv][d_head] rows of keys and values are what a projection to
+ * n_kv / 2 such heads gives, so appends need nothing special).  Query rows
+ * 2h and 2h + 1 are the two queries of head h, h < n_q / 2, which reads pair
+ * p = h / (n_q / n_kv):
+ *   o_h   = softmax(scale q_2h . K_2p) V - lambda softmax(scale q_2h+1 . K_2p+1) V,
+ *           V = [V_2p | V_2p+1]
+ *   out_h = (1 - lambda_init) * norm_weight * o_h / sqrt(mean(o_h^2) + eps)
+ *   lambda = exp(lambdas[0] . lambdas[1]) - exp(lambdas[2] . lambdas[3]) + lambda_init
+ * The softmax statistics, the sums, lambda and the norm are held in fp32;
+ * the weights of a map enter the products with V as bf16 (bf16 pools) or f16
+ * (FP8 pools), and out is rounded once, to bf16.
+ * --------------------------------------------------------------------- */
+typedef struct {
+    const float *lambdas;      /* device fp32 [4][d_head] */
+    const float *norm_weight;  /* device fp32 [2 d_head]; NULL: ones */
+    float lambda_init;         /* finite */
+    float eps;                 /* finite, > 0 */
+} pkv_diff_params;
+
+/* Differential decode attention for one new query token per sequence.
+ *   q       device bf16 [batch][n_q][d_head], 16-byte aligned.
+ *   params  host struct (its pointers are device memory); read at the call.
+ *   out     device bf16 [batch][n_q / 2][2 d_head], 16-byte aligned.
+ * block_tables, context_lens, scale, limits and range errors as
+ * paged_decode_attention (a context of 0 gives a row of zeros, a block id
+ * outside the pool counts as masked).  bf16 and FP8 pools; on FP8 pools the
+ * products run in f16 (|q| must stay in f16's range).  Two launches, like
+ * paged_decode_attention; uses the same workspace (grown outside stream
+ * captures: see paged_diff_reserve_workspace) and the pool's partition
+ * setting.
+ * Errors: as paged_decode_attention, plus EUNSUPPORTED (4-bit pools, odd
+ * n_kv), EINVAL (params, the pool's device not current, a workspace that
+ * would have to grow while `stream` is captured). */
+pkv_status paged_diff_decode_attention(pkv_pool *pool, const void *q, int32_t n_q, const int32_t *block_tables,
+                                       int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t batch,
+                                       float scale, const pkv_diff_params *params, void *out, void *stream);
+
+/* Grow the pool's workspace now, so that later paged_diff_decode_attention
+ * calls with at most `batch` sequences, `n_q` query heads and
+ * `max_blocks_per_seq` table entries allocate nothing and may be captured.
+ * Memory that captured graphs may use stays valid: a workspace that is
+ * replaced by a larger one is kept until the pool is destroyed.  Graphs of
+ * one pool share its workspace: replay them one after the other.
+ * Errors: EINVAL, EUNSUPPORTED, ENOMEM. */
+pkv_status paged_diff_reserve_workspace(pkv_pool *pool, int32_t batch, int32_t n_q, int32_t max_blocks_per_seq);
+
 /* paged_decode_attention without any allocation.  The pages have no
  * counterpart to this call; it exists for callers that cannot allocate
  * device memory when they decode: an engine that reserved nearly all free
