@@ -112,6 +112,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                                                 c.c_float, P, P]
         lib.paged_diff_decode_attention.argtypes = [P, P, c.c_int32, P, c.c_int32, P, c.c_int32, c.c_float,
                                                     c.POINTER(_DiffParams), P, P]
+        lib.paged_diff_prefill_attention.argtypes = [P, P, c.c_int64, c.c_int32, P, P, c.c_int32, P, c.c_int32,
+                                                     c.c_float, c.POINTER(_DiffParams), P, P]
         lib.paged_diff_reserve_workspace.argtypes = [P, c.c_int32, c.c_int32, c.c_int32]
         lib.paged_decode_step.argtypes = [P, P, P, P, c.c_int32, P, c.c_int32, P, c.c_int32, c.c_float, P, P]
         lib.paged_decode_step_host.argtypes = [P, P, P, P, c.c_int32, P, c.c_int32, P, c.c_int32, c.c_float,
@@ -147,7 +149,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                      "kv_pool_layout",
                      "kv_pool_set_partition_tokens", "kv_pool_set_cascade_mode", "kv_pool_reserve_workspace",
                      "paged_kv_append", "pkv_rope_create", "pkv_rope_destroy", "paged_rope_append",
-                     "paged_kv_gather", "paged_diff_decode_attention", "paged_diff_reserve_workspace",
+                     "paged_kv_gather", "paged_diff_decode_attention", "paged_diff_prefill_attention",
+                     "paged_diff_reserve_workspace",
                      "paged_decode_attention", "paged_decode_attention_noalloc", "paged_decode_step",
                      "paged_decode_attention_csr", "paged_prefill_attention",
                      "paged_decode_step_host", "paged_decode_attention_prefix", "pkv_get_error", "pkv_timing_enable", "pkv_timing_read",
@@ -596,6 +599,28 @@ def paged_diff_decode_attention(pool: Pool, q, block_tables, context_lens, scale
     return out
 
 
+def paged_diff_prefill_attention(pool: Pool, q, qo_indptr, block_tables, context_lens, scale: float,
+                                 params: DiffParams, out=None, stream=None):
+    """Differential attention of each sequence's chunk of new tokens over its
+    cache (causal).  q: bf16 [rows, n_q, d_head], the chunks sequence by
+    sequence; qo_indptr: int32 [B + 1]; block_tables: int32 [B, W];
+    context_lens: int32 [B] (including the chunk).  Returns ``out`` (bf16
+    [rows, n_q / 2, 2 * d_head], allocated if not given)."""
+    import torch
+
+    qp, n_q, shape = _diff_args(pool, q, params, None)
+    cp = _pool_ptr(pool, context_lens, "context_lens", torch.int32, 1)
+    B = int(context_lens.shape[0])
+    ip = _pool_ptr(pool, qo_indptr, "qo_indptr", torch.int32, 1, (B + 1,))
+    tp = _pool_ptr(pool, block_tables, "block_tables", torch.int32, 2, (B, None))
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+    op = _pool_ptr(pool, out, "out", torch.bfloat16, 3, shape)
+    _check(load().paged_diff_prefill_attention(pool.handle, qp, shape[0], n_q, ip, tp, int(block_tables.shape[1]), cp, B,
+                                               float(scale), params._ref, op, _stream_handle(stream)))
+    return out
+
+
 def paged_decode_attention_prefix(pool: Pool, q, prefix_blocks, block_tables, context_lens, scale: float,
                                   out=None, stream=None):
     """Cascade decode: every sequence starts with the shared prefix whose
@@ -855,6 +880,6 @@ __all__ = ["BF16", "FP8_E4M3", "INT4", "Pool", "PagedKVError", "kv_pool_create",
            "paged_decode_attention", "paged_decode_attention_noalloc", "paged_decode_step",
            "paged_decode_step_host", "paged_decode_attention_prefix", "paged_decode_attention_csr",
            "paged_prefill_attention", "Rope", "paged_rope_append", "paged_kv_gather",
-           "DiffParams", "paged_diff_decode_attention",
+           "DiffParams", "paged_diff_decode_attention", "paged_diff_prefill_attention",
            "kv_bytes_per_token", "kv_block_bytes", "kv_swap_entry_bytes",
            "kv_block_copy", "kv_swap_out", "kv_swap_in", "BlockAllocator", "load", "library_path"]

@@ -1,0 +1,908 @@
+// Differential attention of a chunk of new tokens over the paged cache, on the
+// tcgen05 tensor cores.
+//
+// Mathematics (see diff.cu for the head layout): for the rows of a pair's G
+// heads, o = P1 V - lambda P2 V with P_m = softmax(s Q_m K_m^T) and V the
+// pair's two value heads side by side.  Both products go into ONE accumulator:
+// a first sweep over the keys finds each row's maximum m and sum l of both
+// maps, a second one recomputes the scores and adds
+//   c1 2^(s1 - m1) V  and  -+ c2 2^(s2 - m2) V,   c1 / c2 = l2 / (|lambda| l1),
+// the larger of c1, c2 being 2^8 (weights stay within f16's range whatever
+// the two sums are), so that o = accumulator / (c1 l1).  All statistics are
+// final before the first weight is formed: no accumulator is ever rescaled,
+// and the two maps' weights need nothing from each other inside the sweep.
+// Separate accumulators for the two maps would take all 512 columns of tensor
+// memory at d_head 128 and leave none for scores; the price of one is the
+// second Q K^T (4 of 16 MMA units where 12 are the least).
+//
+// Design (one persistent CTA per SM, warp-specialised, as prefill.cu):
+//   * a tile is 128 query rows (token, head) of one (sequence, pair): both
+//     maps' queries.  A step is 128 keys; its units are (map 1), (map 2).
+//   * warp 8 streams Q and the K_m tiles (one unit each, both sweeps), warp 9
+//     the V tiles (second sweep; units of 64 keys x 2 d channels, used by both
+//     maps), warp 10 issues S_m = Q_m K_m^T, warp 11 O += P_m V.
+//   * warps 0-3 take map 1's scores, warps 4-7 map 2's, a thread a row: the
+//     statistics are the thread's own, and while one map's weights are formed
+//     the tensor cores work on the other's.  P_m overwrites the scores it came
+//     from.  The two threads of a row swap l (through shared memory) between
+//     the sweeps, and half sums of squares at the end, where each normalises
+//     and stores one value head's half of the row.
+//   * value rows behind the sequence's end (a page that ends inside a tile)
+//     are zeroed in shared memory before their product: a weight of 0 does not
+//     cancel what is not finite.
+// Every mbarrier wait is bounded; on a timeout the CTA records
+// PKV_DEVERR_TIMEOUT, every role stops, the MMA and copy pipes are drained
+// (bounded) and the tensor memory is released before the CTA exits.
+#include <algorithm>
+#include <mutex>
+
+#include "diff_common.cuh"
+#include "tcgen05.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kRows = 128;  // query rows per tile (= TMEM lanes)
+constexpr int kKeys = 128;  // keys per step
+constexpr int kStepBlocks = kKeys / kBlockSize;
+constexpr int kVKeys = 64;  // keys of a V unit
+constexpr int kUnitBlocks = kVKeys / kBlockSize;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kKWarp = 8, kVWarp = 9, kQkWarp = 10, kPvWarp = 11;
+constexpr int kThreads = 12 * 32;
+// Tensor memory: S_1 at 0, S_2 at 128 (fp32 scores; P_m over the first 64 columns of S_m), O at 256 (2 d).
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 256;
+constexpr uint32_t kKHalf = kKeys * 128;   // a 64-column range of a Q or K tile
+constexpr uint32_t kVChunk = kVKeys * 128; // a 64-channel range of a V unit
+constexpr float kBoost = 8.0f;             // log2 of the larger of c1, c2
+
+struct Args {
+    const int32_t *qo_indptr;  // [batch + 1]
+    const int32_t *block_tables;
+    int W;
+    const int32_t *context_lens;
+    int batch, n_q, n_kv, n_pairs;
+    int64_t num_blocks, n_rows;
+    int oob_row;          // a row index past the end of the pool's entry rows (zero-filled box)
+    float qscale;         // scale * log2(e)
+    const float *scales;  // FP8 pools: [2 * n_kv] fp32, K scales then V scales
+    DiffWeights w;
+    __nv_bfloat16 *out;   // [n_rows][n_q / 2][2 D]
+    unsigned *err;
+};
+
+template <int D>
+struct Layout {
+    static constexpr uint32_t QT = kRows * D * 2;       // one map's queries
+    static constexpr uint32_t KT = kKeys * D * 2;       // one K unit
+    static constexpr uint32_t VT = kVKeys * 2 * D * 2;  // one V unit
+    static constexpr int kKStages = D == 128 ? 2 : 4, kVStages = D == 128 ? 3 : 6;
+    static constexpr uint32_t kQ = 0;
+    static constexpr uint32_t kK = kQ + 2 * QT;
+    static constexpr uint32_t kV = kK + kKStages * KT;
+    static constexpr uint32_t kX = kV + kVStages * VT;  // [2 maps][kRows] float: l, then sums of squares
+    static constexpr uint32_t kBar = kX + 2 * kRows * 4;
+    // *_RAW: FP8 pools' copies complete there; K_FULL, V_FULL and Q_FULL follow when the rows are f16
+    enum { Q_RAW = 0, Q_FULL, Q_FREE, K_RAW, K_FULL = K_RAW + kKStages, K_EMPTY = K_FULL + kKStages,
+           V_RAW = K_EMPTY + kKStages, V_FULL = V_RAW + kVStages, V_EMPTY = V_FULL + kVStages,
+           S_FULL = V_EMPTY + kVStages,  // per map
+           S_READ = S_FULL + 2,          // per map: a first-sweep unit's scores are in registers
+           P_FULL = S_READ + 2,          // per (map, key half)
+           PV_DONE = P_FULL + 4,         // per map: a second-sweep unit's product has run
+           O_FULL = PV_DONE + 2, O_FREE, PAIR, DRAIN = PAIR + 4, NBARS = DRAIN + 2 };
+    static constexpr uint32_t kTmemSlot = kBar + NBARS * 8;
+    static constexpr uint32_t kAbort = kTmemSlot + 4;
+    static constexpr uint32_t kEnd = kAbort + 4;
+    static constexpr size_t bytes = 1024 + kEnd;
+    static_assert(bytes <= 232448, "shared memory beyond the 227 KiB a CTA may use");
+};
+
+// ------------------------------------------------------------- FP8 pools: E4M3 -> f16 in shared memory
+
+// A tile of R rows x D, converted in place by one warp: rows [row0, row0 + rows).
+// Before: E4M3 rows of D bytes in the tile's upper half (the copies' swizzle:
+// 16-byte chunk c of row r at c ^ (r & 7) for 128-byte rows, c ^ ((r >> 1) & 3)
+// for 64-byte rows).  After: per 64 columns, f16 row r at r * 128 bytes, chunk
+// j at j ^ (r & 7).  For D = 128 row r's second 64 columns land exactly on its
+// own E4M3 row; for D = 64 f16 row r covers E4M3 rows 2 r - R and 2 r - R + 1,
+// none above r (so one warp takes all rows there, in order).  Rows are read
+// before any lane writes.
+template <int D, int R>
+__device__ __forceinline__ void convert_f16(uint32_t tile, int lane, int row0, int rows)
+{
+    constexpr int CPR = D / 16;      // 16-byte chunks of an E4M3 row
+    constexpr int RPI = 32 / CPR;    // rows per step of a warp
+    constexpr int U = 4;
+    const uint32_t in = tile + R * D;
+    const int c = lane % CPR;
+#pragma unroll 1
+    for (int i = row0; i < row0 + rows; i += U * RPI) {
+        uint4 x[U];
+        int r[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            r[u] = i + u * RPI + lane / CPR;
+            const int sw = D == 128 ? r[u] & 7 : (r[u] >> 1) & 3;
+            x[u] = lds128(in + r[u] * D + ((c ^ sw) << 4));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            uint4 lo, hi;
+            e4m3x4_to_f16x4(x[u].x, lo.x, lo.y);
+            e4m3x4_to_f16x4(x[u].y, lo.z, lo.w);
+            e4m3x4_to_f16x4(x[u].z, hi.x, hi.y);
+            e4m3x4_to_f16x4(x[u].w, hi.z, hi.w);
+            const uint32_t row = tile + (c >> 2) * (R * 128) + r[u] * 128;
+            const int j = 2 * (c & 3);
+            sts128(row + ((j ^ (r[u] & 7)) << 4), lo);
+            sts128(row + (((j + 1) ^ (r[u] & 7)) << 4), hi);
+        }
+        __syncwarp();
+    }
+}
+
+// One map's queries (bf16, as the copy left them) -> f16 in place, element by element.
+template <int D>
+__device__ __forceinline__ void convert_q(uint32_t base, int lane)
+{
+#pragma unroll 4
+    for (uint32_t off = 16u * lane; off < Layout<D>::QT; off += 16u * 32) {
+        uint4 v = lds128(base + off);
+        uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 f = bf16x2_to_f32x2(w[k]);
+            w[k] = pack_f16x2(f.x, f.y);
+        }
+        sts128(base + off, v);
+    }
+}
+
+// ------------------------------------------------------------- packed fp32
+
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// ------------------------------------------------------------- tile walk
+
+struct Tile {
+    int b, p, rt0;  // sequence, pair, first local row
+    int R;          // rows of (b, p): T * G
+    int row0, T, C; // first query token row of b, chunk length, context length (clamped)
+    int n_blocks, n_steps;
+    bool bad_ctx;
+};
+
+// A window of 32 sequences, one per lane: each warp walks the tile list itself
+// (sequence, then pair, then row tile), with the same arithmetic.
+struct Walker {
+    int wb = 0, wbase = 0;           // the window's first sequence, tiles before it
+    int incl = 0, tot = 0;
+    int nt = 0, row0 = 0, T = 0, C = 0;  // this lane's sequence: row tiles per pair, rows, context
+};
+
+template <int G>
+__device__ __forceinline__ void load_window(Walker &w, const Args &a, int lane)
+{
+    const int bl = w.wb + lane;
+    w.row0 = w.T = w.C = w.nt = 0;
+    if (bl < a.batch) {
+        const int32_t lo = a.qo_indptr[bl], hi = a.qo_indptr[bl + 1];
+        if (lo < 0 || hi < lo || hi > a.n_rows) {  // rows that are not the caller's: skip the sequence
+            atomicOr(a.err, PKV_DEVERR_CTX_RANGE);
+        } else {
+            w.row0 = lo;
+            w.T = hi - lo;
+            w.C = a.context_lens[bl];
+            w.nt = (w.T * G + kRows - 1) / kRows;
+        }
+    }
+    int x = w.nt * a.n_pairs;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, x, o);
+        if (lane >= o) x += y;
+    }
+    w.incl = x;
+    w.tot = __shfl_sync(kFull, x, 31);
+}
+
+// Tile x of the list; false past its end.  Warp-wide, uniform result.
+template <int G>
+__device__ __forceinline__ bool find_tile(Walker &w, const Args &a, int x, Tile &t, int lane)
+{
+    while (x >= w.wbase + w.tot) {
+        if (w.wb + 32 >= a.batch) return false;
+        w.wbase += w.tot;
+        w.wb += 32;
+        load_window<G>(w, a, lane);
+    }
+    const unsigned hit = __ballot_sync(kFull, w.wbase + w.incl > x);
+    const int l = __ffs(hit) - 1;
+    const int nt = __shfl_sync(kFull, w.nt, l);
+    const int before = __shfl_sync(kFull, w.incl - w.nt * a.n_pairs, l);
+    t.b = w.wb + l;
+    t.row0 = __shfl_sync(kFull, w.row0, l);
+    t.T = __shfl_sync(kFull, w.T, l);
+    int C = __shfl_sync(kFull, w.C, l);
+    const int within = x - w.wbase - before;
+    t.p = within / nt;
+    t.rt0 = (within - t.p * nt) * kRows;
+    t.R = t.T * G;
+    const int cap = a.W * kBlockSize;
+    t.bad_ctx = C < t.T || C > cap;
+    if (t.bad_ctx) C = max(t.T, min(C, cap));
+    t.C = C;
+    if (C > cap) {  // a chunk longer than the whole table: nothing sensible to attend to
+        t.n_blocks = t.n_steps = 0;
+        return true;
+    }
+    const int last_row = min(t.R, t.rt0 + kRows) - 1;
+    t.n_blocks = (C - t.T + last_row / G) / kBlockSize + 1;
+    t.n_steps = (t.n_blocks + kStepBlocks - 1) / kStepBlocks;
+    return true;
+}
+
+// ------------------------------------------------------------- the kernel
+
+template <int D, int G, bool F8>
+__global__ void __launch_bounds__(kThreads, 1)
+    diff_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
+                        const __grid_constant__ Args a)
+{
+    using L = Layout<D>;
+    constexpr int NH = D / 64;  // 64-column ranges of a row
+    constexpr int KS = L::kKStages, VS = L::kVStages;
+    constexpr bool kSplitK = F8 && D == 128;  // the K rows' conversion is shared by the K and the Q K^T warp
+    extern __shared__ __align__(1024) uint8_t dp_smem[];
+    uint8_t *sm = dp_smem + ((1024u - (smem_u32(dp_smem) & 1023u)) & 1023u);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::kBar);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::kAbort);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        prefetch_tensormap(&tm_q);
+        prefetch_tensormap(&tm_kv);
+        for (int i = 0; i < L::NBARS; ++i) {
+            uint32_t n = 1;
+            if (i >= L::S_READ && i < L::PV_DONE) n = 4;        // S_READ, P_FULL: a map's four warps
+            if (i == L::O_FREE) n = kSoftmaxWarps;
+            if (i >= L::PAIR && i < L::PAIR + 4) n = 2;         // the two warps of a lane quarter
+            if (i == L::Q_FULL && F8) n = 2;                    // a warp converts each map's queries
+            mbar_init(&bar[i], n);
+        }
+        *abort_flag = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == kQkWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(sm + L::kTmemSlot)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + L::kTmemSlot);
+    griddep_wait();
+    griddep_launch_dependents();
+
+    auto set_abort = [&]() {
+        if (lane == 0) {
+            atomicOr(a.err, PKV_DEVERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+    };
+    Walker wk;
+    load_window<G>(wk, a, lane);
+    const uint32_t base = smem_u32(sm);
+
+    if (warp == kKWarp) {
+        // ---------------------------------------------------------- Q and K copies
+        const uint64_t policy = l2_policy_evict_normal();
+        int u = 0, n = 0;  // units, tiles
+        int issued = 0;    // units whose copies were issued
+        int pend = -1;     // FP8: the unit awaiting conversion
+        bool pend_q = false;
+        bool ok = true;
+        [[maybe_unused]] auto convert_pending = [&]() -> bool {
+            if (pend_q) {
+                if (!wait_all(&bar[L::Q_RAW], (n - 1) & 1)) return false;
+                convert_q<D>(base + L::kQ, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[L::Q_FULL]);
+                pend_q = false;
+            }
+            if (pend < 0) return true;
+            const int st = pend % KS;
+            if (!wait_all(&bar[L::K_RAW + st], (pend / KS) & 1)) return false;
+            convert_f16<D, kKeys>(base + L::kK + st * L::KT, lane, 0, kSplitK ? kKeys / 2 : kKeys);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[L::K_FULL + st]);
+            pend = -1;
+            return true;
+        };
+        for (int x = blockIdx.x; ok; x += gridDim.x) {
+            Tile t;
+            if (!find_tile<G>(wk, a, x, t, lane)) break;
+            if (t.n_steps == 0) continue;
+            if (*abort_flag) break;
+            if constexpr (F8) {  // the last unit of the tile before
+                if (!(ok = convert_pending())) break;
+            }
+            if (n > 0 && !(ok = wait_all(&bar[L::Q_FREE], (n - 1) & 1))) break;
+            if (lane == 0) {
+                uint64_t *qb = &bar[F8 ? L::Q_RAW : L::Q_FULL];
+                mbar_arrive_expect_tx(qb, 2 * L::QT);
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int h = 0; h < NH; ++h)
+                        tma_load_4d(sm + L::kQ + m * L::QT + h * kKHalf, &tm_q, 64 * h, m, t.p * G, t.row0 + t.rt0 / G,
+                                    qb, policy);
+            }
+            ++n;
+            pend_q = F8;
+            const int32_t *trow = a.block_tables + (int64_t)t.b * a.W;
+            for (int sweep = 0; sweep < 2 && ok; ++sweep) {
+                int nxt = lane < kStepBlocks && lane < t.n_blocks ? trow[lane] : -1;
+                for (int s = 0; s < t.n_steps && ok; ++s) {
+                    const int cur = nxt;
+                    const int nb = (s + 1) * kStepBlocks + lane;
+                    if (s + 1 < t.n_steps) nxt = lane < kStepBlocks && nb < t.n_blocks ? trow[nb] : -1;
+                    const bool present = lane < kStepBlocks && s * kStepBlocks + lane < t.n_blocks;
+                    const bool valid = present && cur >= 0 && cur < a.num_blocks;
+                    if (present && !valid && sweep == 0) atomicOr(a.err, PKV_DEVERR_BLOCK_RANGE);
+                    for (int m = 0; m < 2; ++m, ++u) {
+                        const int st = u % KS, use = u / KS;
+                        if (use > 0 && !(ok = wait_all(&bar[L::K_EMPTY + st], (use - 1) & 1))) break;
+                        uint64_t *kb = &bar[(F8 ? L::K_RAW : L::K_FULL) + st];
+                        if (lane == 0) mbar_arrive_expect_tx(kb, F8 ? L::KT / 2 : L::KT);
+                        __syncwarp();
+                        if (lane < kStepBlocks) {
+                            const int y = valid ? (int)((cur * (int64_t)a.n_kv + 2 * t.p + m) * 2 * kBlockSize) : a.oob_row;
+                            uint8_t *dst = sm + L::kK + st * L::KT;
+                            if constexpr (F8) {
+                                tma_load_2d(dst + L::KT / 2 + lane * (kBlockSize * D), &tm_kv, 0, y, kb, policy);
+                            } else {
+#pragma unroll
+                                for (int h = 0; h < NH; ++h)
+                                    tma_load_2d(dst + h * kKHalf + lane * (kBlockSize * 128), &tm_kv, 64 * h, y, kb, policy);
+                            }
+                        }
+                        issued = u + 1;
+                        if constexpr (F8) {
+                            if (!(ok = convert_pending())) break;
+                            pend = u;
+                        }
+                    }
+                }
+            }
+        }
+        if constexpr (F8) {
+            if (ok && !*abort_flag) ok = convert_pending();
+        }
+        // copies still in flight (after an abort) land before the CTA exits
+        for (int i = max(0, issued - KS); i < issued; ++i)
+            mbar_wait_bounded(&bar[(F8 ? L::K_RAW : L::K_FULL) + i % KS], (i / KS) & 1);
+        if (n > 0) mbar_wait_bounded(&bar[F8 ? L::Q_RAW : L::Q_FULL], (n - 1) & 1);
+        if (!ok) set_abort();
+    } else if (warp == kVWarp) {
+        // ---------------------------------------------------------- V copies
+        const uint64_t policy = l2_policy_evict_normal();
+        int u = 0, n = 0, issued = 0, pend = -1;
+        bool ok = true;
+        [[maybe_unused]] auto convert_pending = [&]() -> bool {  // value head 0's rows
+            if (pend < 0) return true;
+            const int st = pend % VS;
+            if (!wait_all(&bar[L::V_RAW + st], (pend / VS) & 1)) return false;
+            convert_f16<D, kVKeys>(base + L::kV + st * L::VT, lane, 0, kVKeys);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[L::V_FULL + st]);
+            pend = -1;
+            return true;
+        };
+        for (int x = blockIdx.x; ok; x += gridDim.x) {
+            Tile t;
+            if (!find_tile<G>(wk, a, x, t, lane)) break;
+            if (t.n_steps == 0) continue;
+            if (*abort_flag) break;
+            if constexpr (F8) {
+                if (!(ok = convert_pending())) break;
+                if (!(ok = wait_all(&bar[L::Q_RAW], n & 1))) break;
+                convert_q<D>(base + L::kQ + L::QT, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[L::Q_FULL]);
+            }
+            ++n;
+            const int32_t *trow = a.block_tables + (int64_t)t.b * a.W;
+            // lane: block (lane & 3) of a unit, value head lane >> 2
+            const int k = lane & 3, head = lane >> 2;
+            const int units = 2 * t.n_steps;
+            int nxt = lane < 8 && k < t.n_blocks ? trow[k] : -1;
+            for (int i = 0; i < units && ok; ++i, ++u) {
+                const int cur = nxt;
+                const int nb = (i + 1) * kUnitBlocks + k;
+                if (i + 1 < units) nxt = lane < 8 && nb < t.n_blocks ? trow[nb] : -1;
+                const int st = u % VS, use = u / VS;
+                if (use > 0 && !(ok = wait_all(&bar[L::V_EMPTY + st], (use - 1) & 1))) break;
+                const bool valid = lane < 8 && i * kUnitBlocks + k < t.n_blocks && cur >= 0 && cur < a.num_blocks;
+                uint64_t *vb = &bar[(F8 ? L::V_RAW : L::V_FULL) + st];
+                if (lane == 0) mbar_arrive_expect_tx(vb, F8 ? L::VT / 2 : L::VT);
+                __syncwarp();
+                if (lane < 8) {
+                    const int y = valid ? (int)((cur * (int64_t)a.n_kv + 2 * t.p + head) * 2 * kBlockSize + kBlockSize)
+                                        : a.oob_row;
+                    uint8_t *dst = sm + L::kV + st * L::VT + head * NH * kVChunk;
+                    if constexpr (F8) {
+                        tma_load_2d(dst + kVKeys * D + k * (kBlockSize * D), &tm_kv, 0, y, vb, policy);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < NH; ++h)
+                            tma_load_2d(dst + h * kVChunk + k * (kBlockSize * 128), &tm_kv, 64 * h, y, vb, policy);
+                    }
+                }
+                issued = u + 1;
+                if constexpr (F8) {
+                    if (!(ok = convert_pending())) break;
+                    pend = u;
+                }
+            }
+        }
+        if constexpr (F8) {
+            if (ok && !*abort_flag) ok = convert_pending();
+        }
+        for (int i = max(0, issued - VS); i < issued; ++i)
+            mbar_wait_bounded(&bar[(F8 ? L::V_RAW : L::V_FULL) + i % VS], (i / VS) & 1);
+        if (!ok) set_abort();
+    } else if (warp == kQkWarp) {
+        // ---------------------------------------------------------- S_m = Q_m K_m^T
+        constexpr uint32_t idesc = mma_idesc(kRows, kKeys, 0, F8);
+        int u = 0, n = 0;                // K units, tiles
+        int reads = 0, prods = 0;        // first- and second-sweep units of each map so far
+        int prev = -1;                   // what the units before these were: 0 first sweep, 1 second
+        bool ok = true;
+        for (int x = blockIdx.x; ok; x += gridDim.x) {
+            Tile t;
+            if (!find_tile<G>(wk, a, x, t, lane)) break;
+            if (t.n_steps == 0) continue;
+            if (*abort_flag) break;
+            if (!(ok = wait_all(&bar[L::Q_FULL], n & 1))) break;
+            ++n;
+            for (int sweep = 0; sweep < 2 && ok; ++sweep)
+                for (int s = 0; s < t.n_steps && ok; ++s) {
+                    for (int m = 0; m < 2; ++m, ++u) {
+                        const int st = u % KS;
+                        if constexpr (kSplitK) {  // this warp's rows of the unit
+                            if (!(ok = wait_all(&bar[L::K_RAW + st], (u / KS) & 1))) break;
+                            convert_f16<D, kKeys>(base + L::kK + st * L::KT, lane, kKeys / 2, kKeys / 2);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                        if (!(ok = wait_all(&bar[L::K_FULL + st], (u / KS) & 1))) break;
+                        // S_m is free: its scores are in registers (first sweep), or its product has run
+                        if (prev == 0 && !(ok = wait_all(&bar[L::S_READ + m], (reads - 1) & 1))) break;
+                        if (prev == 1 && !(ok = wait_all(&bar[L::PV_DONE + m], (prods - 1) & 1))) break;
+                        tc_fence_after();
+                        if (lane == 0) {
+                            const uint32_t qb = base + L::kQ + m * L::QT, kb = base + L::kK + st * L::KT;
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t off = (kk >> 2) * kKHalf + (kk & 3) * 32;
+                                umma(tmem + m * kKeys, smem_desc(qb + off, 16, 1024), smem_desc(kb + off, 16, 1024),
+                                     idesc, kk > 0 ? 1u : 0u);
+                            }
+                            umma_commit(&bar[L::S_FULL + m]);
+                            umma_commit(&bar[L::K_EMPTY + st]);
+                            if (sweep == 1 && s == t.n_steps - 1 && m == 1) umma_commit(&bar[L::Q_FREE]);
+                        }
+                        __syncwarp();
+                    }
+                    prev = sweep;
+                    if (sweep == 0) ++reads;
+                    else ++prods;
+                }
+        }
+        if (lane == 0) umma_commit(&bar[L::DRAIN]);
+        __syncwarp();
+        mbar_wait_bounded(&bar[L::DRAIN], 0);
+        if (!ok) set_abort();
+    } else if (warp == kPvWarp) {
+        // ---------------------------------------------------------- O += P_m V
+        constexpr uint32_t idesc = mma_idesc(kRows, 2 * D, 1, F8);
+        int u = 0, n = 0, steps = 0;  // V units, tiles, steps so far
+        bool ok = true;
+        for (int x = blockIdx.x; ok; x += gridDim.x) {
+            Tile t;
+            if (!find_tile<G>(wk, a, x, t, lane)) break;
+            if (t.n_steps == 0) continue;
+            if (*abort_flag) break;
+            if (n > 0 && !(ok = wait_all(&bar[L::O_FREE], (n - 1) & 1))) break;
+            ++n;
+            // the block the sequence ends inside of, where this tile reaches it
+            const int end_blk = (t.C % kBlockSize) && t.C / kBlockSize < t.n_blocks ? t.C / kBlockSize : -1;
+            for (int s = 0; s < t.n_steps && ok; ++s, ++steps, u += 2) {
+                for (int m = 0; m < 2 && ok; ++m) {
+                    for (int h = 0; h < 2; ++h) {
+                        const int st = (u + h) % VS;
+                        if (m == 0) {
+                            if constexpr (F8) {  // value head 1's rows
+                                if (!(ok = wait_all(&bar[L::V_RAW + st], ((u + h) / VS) & 1))) break;
+                                convert_f16<D, kVKeys>(base + L::kV + st * L::VT + NH * kVChunk, lane, 0, kVKeys);
+                                fence_proxy_async_smem();
+                                __syncwarp();
+                            }
+                            if (!(ok = wait_all(&bar[L::V_FULL + st], ((u + h) / VS) & 1))) break;
+                            if (end_blk >= 0 && end_blk / kUnitBlocks == 2 * s + h) {
+                                const int r0 = (end_blk % kUnitBlocks) * kBlockSize;
+                                const int first = r0 + t.C % kBlockSize, rows = r0 + kBlockSize - first;
+                                for (int i = lane; i < rows * 8 * 2 * NH; i += 32) {
+                                    const int row = first + (i >> 3) % rows, ch = (i >> 3) / rows;
+                                    sts128(base + L::kV + st * L::VT + ch * kVChunk + row * 128 + (i & 7) * 16,
+                                           make_uint4(0, 0, 0, 0));
+                                }
+                                fence_proxy_async_smem();
+                                __syncwarp();
+                            }
+                        }
+                        if (!(ok = wait_all(&bar[L::P_FULL + 2 * m + h], steps & 1))) break;
+                        tc_fence_after();
+                        if (lane == 0) {
+                            const uint32_t vb = base + L::kV + st * L::VT;
+#pragma unroll
+                            for (int kk = 0; kk < kVKeys / 16; ++kk)
+                                umma_ts(tmem + kColO, tmem + m * kKeys + h * (kVKeys / 2) + 8 * kk,
+                                        smem_desc(vb + kk * 2048, kVChunk, 1024), idesc,
+                                        (s > 0 || m > 0 || h > 0 || kk > 0) ? 1u : 0u);
+                            if (m == 1) umma_commit(&bar[L::V_EMPTY + st]);
+                            if (h == 1) umma_commit(&bar[L::PV_DONE + m]);
+                            if (h == 1 && m == 1 && s == t.n_steps - 1) umma_commit(&bar[L::O_FULL]);
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+        }
+        if (lane == 0) umma_commit(&bar[L::DRAIN + 1]);
+        __syncwarp();
+        mbar_wait_bounded(&bar[L::DRAIN + 1], 0);
+        if (!ok) set_abort();
+    } else {
+        // ---------------------------------------------------------- statistics, weights, norm
+        const int m = warp >> 2, quarter = warp & 3;  // this warp's map, its TMEM lanes 32 quarter ..
+        const int row = quarter * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        const uint32_t ts = tmem + lane_off + m * kKeys;       // this map's scores
+        const uint32_t to = tmem + lane_off + kColO + m * D;   // value head m's half of O
+        uint64_t *pair = &bar[L::PAIR + quarter];
+        float *xs = reinterpret_cast<float *>(sm + L::kX);
+        const float lam = diff_lambda<D>(a.w, lane);
+        const float abs_lam = fabsf(lam);
+        const uint32_t flip = m == 1 && !(lam < 0.0f) ? 0x80008000u : 0u;  // the second map is subtracted
+        int gs = 0, n = 0, pph = 0;  // units of this map, tiles, phases of the pair barrier
+        bool ok = true;
+        for (int x = blockIdx.x; ok; x += gridDim.x) {
+            Tile t;
+            if (!find_tile<G>(wk, a, x, t, lane)) break;
+            if (t.bad_ctx && tid == 0 && t.rt0 == 0 && t.p == 0) atomicOr(a.err, PKV_DEVERR_CTX_RANGE);
+            if (t.n_steps == 0) continue;
+            if (*abort_flag) break;
+            const int r = t.rt0 + row;
+            const int pos = t.C - t.T + min(r, t.R - 1) / G;  // this row sees keys 0 .. pos
+            const float qs = F8 ? a.qscale * a.scales[2 * t.p + m] : a.qscale;
+            const int32_t *trow = a.block_tables + (int64_t)t.b * a.W;
+            auto ids_of = [&](int s) -> int {
+                const int nb = s * kStepBlocks + lane;
+                return lane < kStepBlocks && nb < t.n_blocks ? trow[nb] : -1;
+            };
+            // valid blocks of a step, as the copies decided
+            auto mask_of = [&](int id) -> uint32_t {
+                return __ballot_sync(kFull, lane < kStepBlocks && id >= 0 && id < a.num_blocks);
+            };
+            // keys 64 h .. + 63 of the step: loaded, and what this row does not see set to -inf
+            auto load_half = [&](uint32_t (&sr)[64], int h) {
+                tmem_ld32(ts + 64 * h, sr);
+                tmem_ld32(ts + 64 * h + 32, sr + 32);
+                tmem_wait_ld();
+            };
+            auto hide = [&](uint32_t (&sr)[64], int h, int s, uint32_t mask) {
+                const int key0 = s * kKeys + 64 * h;
+                const uint32_t mh = (mask >> (4 * h)) & 15u;
+                if (!(mh == 15u && key0 + 63 <= pos)) {
+#pragma unroll
+                    for (int k = 0; k < 64; ++k)
+                        if (!(((mh >> (k / kBlockSize)) & 1u) && key0 + k <= pos)) sr[k] = 0xff800000u;
+                }
+            };
+            // ---- first sweep: maximum and sum of this map's row ----
+            float mx = -INFINITY, l = 0.0f;
+            int nxt = ids_of(0);
+            for (int s = 0; s < t.n_steps; ++s, ++gs) {
+                const uint32_t mask = mask_of(nxt);
+                if (s + 1 < t.n_steps) nxt = ids_of(s + 1);
+                if (!(ok = wait_all(&bar[L::S_FULL + m], gs & 1))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t sr[64];
+                    load_half(sr, h);
+                    if (h == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar[L::S_READ + m]);
+                    }
+                    float2 v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = fmul2(make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])),
+                                     make_float2(qs, qs));
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        sr[2 * i] = __float_as_uint(v[i].x);
+                        sr[2 * i + 1] = __float_as_uint(v[i].y);
+                    }
+                    hide(sr, h, s, mask);
+                    float mc[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        auto e = [&](int q) { return __uint_as_float(sr[j + 8 * q]); };
+                        mc[j] = fmaxf(fmax3(fmax3(fmax3(e(0), e(1), e(2)), e(3), e(4)), e(5), e(6)), e(7));
+                    }
+                    const float mn = fmaxf(mx, fmax3(fmax3(mc[0], mc[1], mc[2]), fmax3(mc[3], mc[4], mc[5]),
+                                                     fmaxf(mc[6], mc[7])));
+                    const float neg = mn == -INFINITY ? 0.0f : -mn;
+                    float2 sum[4] = {};
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float2 d = fadd2(make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])),
+                                               make_float2(neg, neg));
+                        sum[i & 3] = fadd2(sum[i & 3], make_float2(ex2(d.x), ex2(d.y)));
+                    }
+                    const float2 q0 = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
+                    l = (mx == -INFINITY ? 0.0f : l * ex2(mx - mn)) + (q0.x + q0.y);
+                    mx = mn;
+                }
+            }
+            if (!ok) break;
+            // ---- both maps' sums give the weights' factors ----
+            if (n > 0) {  // the partner has read the last tile's sums of squares
+                if (!(ok = wait_all(pair, pph & 1))) break;
+                ++pph;
+            }
+            xs[m * kRows + row] = l;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pair);
+            if (!(ok = wait_all(pair, pph & 1))) break;
+            ++pph;
+            const float l_ot = xs[(m ^ 1) * kRows + row];
+            const float l1 = m == 0 ? l : l_ot, l2 = m == 0 ? l_ot : l;
+            float neg = 0.0f, inv = 0.0f;  // P = 2^(s qs + neg); o = inv * accumulator
+            if (!(l1 == 0.0f)) {  // (a row none of whose blocks could be read stays all zero)
+                const float f = abs_lam * l1 / l2;  // c2 / c1
+                const float c = m == 0 ? (f <= 1.0f ? 1.0f : 1.0f / f) : (f <= 1.0f ? f : 1.0f);
+                neg = log2f(c) + kBoost - mx;
+                inv = (f <= 1.0f ? 1.0f / l1 : abs_lam / l2) * (1.0f / 256.0f);
+            }
+            // ---- second sweep: weights ----
+            nxt = ids_of(0);
+            for (int s = 0; s < t.n_steps; ++s, ++gs) {
+                const uint32_t mask = mask_of(nxt);
+                if (s + 1 < t.n_steps) nxt = ids_of(s + 1);
+                if (!(ok = wait_all(&bar[L::S_FULL + m], gs & 1))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t sr[64];
+                    load_half(sr, h);
+                    uint32_t pk[32];
+                    const int key0 = s * kKeys + 64 * h;
+                    const bool all = ((mask >> (4 * h)) & 15u) == 15u && key0 + 63 <= pos;
+                    float2 v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = ffma2(make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])),
+                                     make_float2(qs, qs), make_float2(neg, neg));
+                    if (!all) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            sr[2 * i] = __float_as_uint(v[i].x);
+                            sr[2 * i + 1] = __float_as_uint(v[i].y);
+                        }
+                        hide(sr, h, s, mask);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1]));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float px = ex2(v[i].x), py = ex2(v[i].y);
+                        pk[i] = (F8 ? pack_f16x2(px, py) : pack_bf16x2(px, py)) ^ flip;
+                    }
+                    tmem_st32(ts + 32 * h, pk);  // over scores of this step that are already read
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[L::P_FULL + 2 * m + h]);
+                }
+            }
+            if (!ok) break;
+            // ---- norm and store: this thread's row, value head m's half ----
+            if (!(ok = wait_all(&bar[L::O_FULL], n & 1))) break;
+            tc_fence_after();
+            const float f = inv * (F8 ? a.scales[a.n_kv + 2 * t.p + m] : 1.0f);
+            float ss = 0.0f;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(to + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float v = __uint_as_float(o[i]) * f;
+                    ss = fmaf(v, v, ss);
+                }
+            }
+            xs[m * kRows + row] = ss;  // the partner took l before it formed the weights of this O
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pair);
+            if (!(ok = wait_all(pair, pph & 1))) break;
+            ++pph;
+            const float tot = xs[row] + xs[kRows + row];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pair);  // read: waited for before the next tile's l
+            const float rn = f * a.w.out_scale * rsqrtf(tot * (1.0f / (2 * D)) + a.w.eps);
+            const bool live = r < t.R;
+            const int64_t tok = (int64_t)t.row0 + r / G;
+            __nv_bfloat16 *dst = a.out + ((tok * (a.n_q / 2) + t.p * G + r % G) * 2 + m) * D;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(to + c, o);
+                tmem_wait_ld();
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float4 g = make_float4(1.f, 1.f, 1.f, 1.f);
+                    if (a.w.norm_weight) {
+                        const float *nw = a.w.norm_weight + m * D + c + 4 * i;
+                        g = make_float4(nw[0], nw[1], nw[2], nw[3]);
+                    }
+                    w[2 * i] = pack_bf16x2(__uint_as_float(o[4 * i]) * rn * g.x, __uint_as_float(o[4 * i + 1]) * rn * g.y);
+                    w[2 * i + 1] = pack_bf16x2(__uint_as_float(o[4 * i + 2]) * rn * g.z, __uint_as_float(o[4 * i + 3]) * rn * g.w);
+                }
+                if (live) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4 *>(dst + c + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[L::O_FREE]);
+            ++n;
+        }
+        if (!ok) set_abort();
+    }
+
+    tc_fence_before();
+    __syncthreads();  // every role is done with the tensor memory
+    tc_fence_after();
+    if (warp == kQkWarp)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+// ------------------------------------------------------------- launch
+
+template <int D, int G, bool F8>
+pkv_status launch(pkv_pool *pool, const void *q, int64_t tiles, const Args &a, cudaStream_t s)
+{
+    using L = Layout<D>;
+    static std::mutex mu;
+    static bool ready[64];
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (pool->device >= 64 || !ready[pool->device]) {
+            cudaError_t e = cudaFuncSetAttribute(diff_prefill_kernel<D, G, F8>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::bytes);
+            if (e != cudaSuccess) return cuda_fail(e, "paged_diff_prefill_attention: kernel attributes");
+            if (pool->device < 64) ready[pool->device] = true;
+        }
+    }
+    CUtensorMap tm_q;
+    pkv_status st = make_q_pair_map(&tm_q, q, a.n_rows, a.n_q, D, G, kRows / G);
+    if (st != PKV_OK) return st;
+    const int grid = (int)std::min<int64_t>(tiles, pool->num_sms);
+    LaunchScope ls(pool, kDecode, s);
+    cudaError_t e = launch_pdl(diff_prefill_kernel<D, G, F8>, dim3(grid), dim3(kThreads), L::bytes, s, tm_q,
+                               pool->tm_block, a);
+    ls.done();
+    if (e != cudaSuccess) return cuda_fail(e, "paged_diff_prefill_attention launch");
+    return PKV_OK;
+}
+
+template <int D, bool F8>
+pkv_status dispatch_g(pkv_pool *pool, const void *q, int G, int64_t tiles, const Args &a, cudaStream_t s)
+{
+    switch (G) {
+    case 1: return launch<D, 1, F8>(pool, q, tiles, a, s);
+    case 2: return launch<D, 2, F8>(pool, q, tiles, a, s);
+    case 4: return launch<D, 4, F8>(pool, q, tiles, a, s);
+    case 8: return launch<D, 8, F8>(pool, q, tiles, a, s);
+    }
+    return fail(PKV_EUNSUPPORTED, "differential prefill: group size %d unsupported (1, 2, 4 or 8)", G);
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" pkv_status paged_diff_prefill_attention(pkv_pool *pool, const void *q, int64_t n_rows, int32_t n_q,
+                                                   const int32_t *qo_indptr, const int32_t *block_tables,
+                                                   int32_t max_blocks_per_seq, const int32_t *context_lens,
+                                                   int32_t batch, float scale, const pkv_diff_params *params, void *out,
+                                                   void *stream)
+{
+    const char *who = "paged_diff_prefill_attention";
+    pkv_status st = check_step_args(pool, who, n_q, max_blocks_per_seq, batch, scale);
+    Args a;
+    if (st == PKV_OK) st = check_diff_args(pool, who, params, &a.w);
+    if (st != PKV_OK) return st;
+    if (n_rows < 0) return fail(PKV_EINVAL, "%s: n_rows < 0", who);
+    if (batch == 0 || n_rows == 0) return PKV_OK;
+    const int G = n_q / pool->n_kv;
+    if (n_rows > INT32_MAX / G) return fail(PKV_EUNSUPPORTED, "%s: more than 2^31 query rows x group size", who);
+    if (!q || !qo_indptr || !block_tables || !context_lens || !out)
+        return fail(PKV_EINVAL, "%s: NULL device pointer", who);
+    if (((uintptr_t)q | (uintptr_t)out) & 15u) return fail(PKV_EINVAL, "%s: q and out must be 16-byte aligned", who);
+    if (((uintptr_t)qo_indptr | (uintptr_t)block_tables | (uintptr_t)context_lens) & 3u)
+        return fail(PKV_EINVAL, "%s: indptr, tables and lengths must be 4-byte aligned", who);
+    st = check_pool_device(pool, who);
+    if (st != PKV_OK) return st;
+    // an upper bound on the tiles: every sequence may end with a partial one
+    const int64_t tiles = ((n_rows * G + kRows - 1) / kRows + batch) * (pool->n_kv / 2);
+    if (tiles > INT32_MAX) return fail(PKV_EUNSUPPORTED, "%s: too many query rows", who);
+    a.qo_indptr = qo_indptr;
+    a.block_tables = block_tables;
+    a.W = max_blocks_per_seq;
+    a.context_lens = context_lens;
+    a.batch = batch;
+    a.n_q = n_q;
+    a.n_kv = pool->n_kv;
+    a.n_pairs = pool->n_kv / 2;
+    a.num_blocks = pool->num_blocks;
+    a.n_rows = n_rows;
+    a.oob_row = (int)(pool->num_blocks * pool->n_kv * 2 * kBlockSize);
+    a.qscale = scale * kLog2e;
+    a.scales = pool->scales;
+    a.out = static_cast<__nv_bfloat16 *>(out);
+    a.err = pool->err;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool f8 = pool->dtype == PKV_FP8_E4M3;
+    if (pool->d_head == 128)
+        return f8 ? dispatch_g<128, true>(pool, q, G, tiles, a, s) : dispatch_g<128, false>(pool, q, G, tiles, a, s);
+    return f8 ? dispatch_g<64, true>(pool, q, G, tiles, a, s) : dispatch_g<64, false>(pool, q, G, tiles, a, s);
+}

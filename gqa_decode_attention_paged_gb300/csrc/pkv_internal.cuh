@@ -153,6 +153,9 @@ void *mapped_host_ptr(const void *p);
 // A 3-D tiled TMA map over a query array [n_rows][n_q][d_head] bf16: box of
 // min(d_head, 64) columns x `heads` heads x `tokens` rows, 128-byte swizzle.
 pkv_status make_q_map(CUtensorMap *map, const void *q, int64_t n_rows, int n_q, int d_head, int heads, int tokens);
+// The same rows as [n_rows][n_q / 2][2][d_head] (a head's two queries apart):
+// a 4-D map with boxes of min(d_head, 64) columns x 1 query x `heads` x `tokens`.
+pkv_status make_q_pair_map(CUtensorMap *map, const void *q, int64_t n_rows, int n_q, int d_head, int heads, int tokens);
 
 // The cascade's prefix stage on the tensor cores (the prefill kernel in
 // partial mode): every query row of every KV head against the shared blocks,
@@ -279,6 +282,17 @@ __device__ __forceinline__ void tma_load_3d(void *dst_smem, const CUtensorMap *m
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
         "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst_smem)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
+// Tiled 4-D TMA load of one box at element coordinates (x, y, z, w).
+__device__ __forceinline__ void tma_load_4d(void *dst_smem, const CUtensorMap *map, int x, int y, int z, int w,
+                                            uint64_t *bar, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_u32(dst_smem)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
 }
 

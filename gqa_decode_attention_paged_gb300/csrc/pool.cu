@@ -158,6 +158,22 @@ pkv_status make_q_map(CUtensorMap *map, const void *q, int64_t n_rows, int n_q, 
     return PKV_OK;
 }
 
+pkv_status make_q_pair_map(CUtensorMap *map, const void *q, int64_t n_rows, int n_q, int d_head, int heads, int tokens)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    pkv_status st = tiled_encoder(&encode);
+    if (st != PKV_OK) return st;
+    cuuint64_t dims[4] = {(cuuint64_t)d_head, 2, (cuuint64_t)n_q / 2, (cuuint64_t)n_rows};
+    cuuint64_t strides[3] = {(cuuint64_t)d_head * 2, (cuuint64_t)d_head * 4, (cuuint64_t)n_q * d_head * 2};
+    cuuint32_t box[4] = {(cuuint32_t)(d_head < 64 ? d_head : 64), 1, (cuuint32_t)heads, (cuuint32_t)tokens};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(q), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(PKV_ECUDA, "cuTensorMapEncodeTiled (query pairs) failed (%d)", (int)r);
+    return PKV_OK;
+}
+
 pkv_status make_tensor_maps(pkv_pool *pool)
 {
     PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;

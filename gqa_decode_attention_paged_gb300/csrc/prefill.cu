@@ -49,7 +49,7 @@
 #include <algorithm>
 #include <mutex>
 
-#include "pkv_internal.cuh"
+#include "tcgen05.cuh"
 
 namespace pkv {
 namespace {
@@ -120,145 +120,6 @@ struct Layout {
     static_assert(bytes <= 232448, "shared memory beyond the 227 KiB a CTA may use");
 };
 
-// ------------------------------------------------------------- tcgen05 PTX
-
-// Shared-memory matrix descriptor: 128-byte swizzled canonical layout.  For a
-// K-major operand `sbo` is the stride between 8-row groups (1024 B) and the
-// leading offset is unused; for an MN-major operand `lbo` is the stride
-// between 64-element chunks of the M/N dimension and `sbo` the stride
-// between 8-row groups of the K dimension.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo)
-{
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
-}
-
-// Instruction descriptor, kind::f16: bf16 (f16 = false) or f16 (f16 = true)
-// A and B, f32 accumulator, M x N, A K-major, B K-major (b_mn = 0) or
-// MN-major (b_mn = 1).
-__host__ __device__ constexpr uint32_t mma_idesc(int M, int N, int b_mn, bool f16 = false)
-{
-    const uint32_t ab = f16 ? 0u : 1u;  // operand format: 0 f16, 1 bf16
-    return (1u << 4) | (ab << 7) | (ab << 10) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
-           ((uint32_t)(M >> 4) << 24);
-}
-
-// A from tensor memory (M rows in lanes, K packed along columns), B from shared memory.
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc)
-{
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
-                 : "memory");
-}
-
-__device__ __forceinline__ void umma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
-{
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc)
-                 : "memory");
-}
-
-// Arrive once on `bar` when every tcgen05 MMA this thread issued so far has completed.
-__device__ __forceinline__ void umma_commit(uint64_t *bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// 32 consecutive columns of this warp's 32 TMEM lanes, one lane per thread.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r)
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-                   "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-                   "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-                 : "r"(taddr)
-                 : "memory");
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r)
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-                 "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-                 ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-                   "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-                   "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-                   "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-                   "r"(r[29]), "r"(r[30]), "r"(r[31])
-                 : "memory");
-}
-
-
-
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// acc += the two bf16 halves of `pk` (each widened exactly, added in fp32).
-__device__ __forceinline__ void add_bf16x2_to(float &acc, uint32_t pk)
-{
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\t"
-        "add.rn.f32.bf16 %0, lo, %0;\n\tadd.rn.f32.bf16 %0, hi, %0;\n\t}"
-        : "+f"(acc)
-        : "r"(pk));
-}
-
-// max(a, b, c) in one instruction
-__device__ __forceinline__ float fmax3(float a, float b, float c)
-{
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
-// (a.x b.x + c.x, a.y b.y + c.y), each rounded as fmaf, in one paired instruction
-__device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c)
-{
-    float2 d;
-    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-        "mov.b64 rc, {%6, %7};\n\tfma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-// acc += the two f16 halves of `pk` (each widened exactly, added in fp32).
-__device__ __forceinline__ void add_f16x2_to(float &acc, uint32_t pk)
-{
-    asm("{\n\t.reg .b16 lo, hi;\n\t.reg .f32 a, b;\n\tmov.b32 {lo, hi}, %1;\n\t"
-        "cvt.f32.f16 a, lo;\n\tcvt.f32.f16 b, hi;\n\tadd.rn.f32 %0, a, %0;\n\tadd.rn.f32 %0, b, %0;\n\t}"
-        : "+f"(acc)
-        : "r"(pk));
-}
-
 // P as the operand the P V product takes: bf16 pairs, or f16 pairs for FP8 pools
 // (whose MMAs run in f16); the row sum adds the rounded values.
 template <bool F16>
@@ -275,29 +136,6 @@ __device__ __forceinline__ void add_p_to(float &acc, uint32_t pk)
 }
 
 // ------------------------------------------------------------- FP8 pools: E4M3 -> f16 in shared memory
-
-// Four E4M3 bytes -> two f16x2 words (bytes 0, 1 -> lo; bytes 2, 3 -> hi); exact.
-__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t x, uint32_t &lo, uint32_t &hi)
-{
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(x));
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr)
-                 : "memory");
-    return v;
-}
-
-__device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
-{
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                 : "memory");
-}
 
 // One step's K (or V) tile of an FP8 pool, converted in place by one warp.
 // The copies put the 128 E4M3 rows (row r = key r of the step, D bytes, the
@@ -504,11 +342,6 @@ template <bool PARTIAL>
 __device__ __forceinline__ const int32_t *tile_blocks(const Args &a, const Tile &t)
 {
     return PARTIAL ? a.shared_blocks + (int64_t)t.b * a.chunk_blocks : a.block_tables + (int64_t)t.b * a.W;
-}
-
-__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity)
-{
-    return __all_sync(kFull, mbar_wait_bounded(bar, parity));
 }
 
 // ------------------------------------------------------------- the kernel

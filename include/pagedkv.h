@@ -481,6 +481,32 @@ pkv_status paged_diff_decode_attention(pkv_pool *pool, const void *q, int32_t n_
                                        int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t batch,
                                        float scale, const pkv_diff_params *params, void *out, void *stream);
 
+/* Differential attention of a chunk of new tokens per sequence over the
+ * cache: the differential form of paged_prefill_attention.  Token i of the
+ * chunk sees cached positions 0 .. C_b - T_b + i (C_b = context_lens[b]
+ * including the chunk, which is already appended).
+ *   q          device bf16 [n_rows][n_q][d_head], 16-byte aligned.
+ *   qo_indptr  device int32 [batch + 1]: sequence b's tokens are rows
+ *              qo_indptr[b] .. qo_indptr[b+1].  A sequence whose rows run
+ *              backwards or leave [0, n_rows) is skipped and sets
+ *              PKV_DEVERR_CTX_RANGE.
+ *   context_lens  device int32 [batch].  A chunk longer than its cache, or a
+ *              length past the table, is clamped and sets
+ *              PKV_DEVERR_CTX_RANGE; a chunk longer than its whole table is
+ *              skipped.
+ *   out        device bf16 [n_rows][n_q / 2][2 d_head], 16-byte aligned; rows
+ *              of no sequence, or of one that is skipped, stay as they were.
+ * A block id outside the pool counts as masked and sets
+ * PKV_DEVERR_BLOCK_RANGE; a row that sees nothing is zero.  Cached rows
+ * behind C_b are never used, whatever they hold.  bf16 and FP8 pools; one
+ * launch on the tcgen05 tensor cores, no workspace.
+ * Errors: EINVAL, EUNSUPPORTED (4-bit pools, odd n_kv, group size, 2^31 query
+ * rows x group size or more), ECUDA. */
+pkv_status paged_diff_prefill_attention(pkv_pool *pool, const void *q, int64_t n_rows, int32_t n_q,
+                                        const int32_t *qo_indptr, const int32_t *block_tables,
+                                        int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t batch,
+                                        float scale, const pkv_diff_params *params, void *out, void *stream);
+
 /* Grow the pool's workspace now, so that later paged_diff_decode_attention
  * calls with at most `batch` sequences, `n_q` query heads and
  * `max_blocks_per_seq` table entries allocate nothing and may be captured.
