@@ -233,7 +233,9 @@ def kv_bytes_per_token(layers: int, n_kv: int, d_head: int, bytes_per_value: flo
 
 
 class Pool:
-    """A K/V block pool owned by the library (one layer).  Use kv_pool_create()."""
+    """A K/V block pool owned by the library (one layer).  Use kv_pool_create().
+    Its memory lives until close() (or the end of the ``with`` block), or until
+    neither the pool nor a view of it is referenced."""
 
     def __init__(self, handle, num_blocks, block_size, n_kv, d_head, dtype):
         self._h = handle
@@ -342,13 +344,13 @@ class Pool:
     def v_view(self):
         return self._view("v")
 
-    @staticmethod
-    def _bytes_view(ptr, n):
+    def _bytes_view(self, ptr, n):
         import torch
 
         class _Holder:  # exposes the pool's memory through the CUDA array interface
             __cuda_array_interface__ = {"shape": (n,), "typestr": "|u1", "data": (ptr, False),
                                         "version": 3, "strides": None}
+            pool = self  # the tensor holds this object, so the memory outlives every view of it
 
         return torch.as_tensor(_Holder(), device="cuda")
 

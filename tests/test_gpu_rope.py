@@ -414,3 +414,21 @@ def test_write_and_read_back_on_a_side_stream_and_in_a_graph(kv):
         side.synchronize()
         for x, y in zip(want, (o, kk, vv)):
             assert torch.equal(x, y)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "int4"])
+def test_a_view_keeps_its_pool_alive(kv):
+    import gc
+    import weakref
+
+    pool, _ = make(kv, 2, 64, 3)
+    alive = weakref.ref(pool)
+    views = [pool.k_view(), pool.v_view()[1:].view(torch.int8)] + ([pool.v_params_view()] if kv == "int4" else [])
+    del pool
+    gc.collect()
+    while views:
+        assert alive() is not None
+        views.pop()
+    gc.collect()
+    assert alive() is None
