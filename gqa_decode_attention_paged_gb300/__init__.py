@@ -75,6 +75,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = True) -> ctypes.CDLL:
     """Load libpagedkv.so (building it first if it is missing and nvcc exists)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -199,6 +201,26 @@ def _dev_ptr(t, name, dtype=None, ndim=None, shape=None):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _raw_stream(pool, stream):
+    """The stream a call on this pool goes to: the given one, or the current one of the pool's device."""
+    import torch
+
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(pool.device)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _fast_ptr(pool, t, name, dtype, shape):
+    """Address of a contiguous tensor of this exact shape and type on the pool's device (cheap checks
+    first: small calls are bound by the host; what fails them gets _pool_ptr's message)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == pool.device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _pool_ptr(pool, t, name, dtype, len(shape), shape)
+
+
 def _pool_ptr(pool, t, name, dtype=None, ndim=None, shape=None):
     """_dev_ptr, for a tensor that has to be on the pool's device."""
     p = _dev_ptr(t, name, dtype, ndim, shape)
@@ -207,20 +229,20 @@ def _pool_ptr(pool, t, name, dtype=None, ndim=None, shape=None):
     return p
 
 
-def _rows_ptr(pool, t, name, heads=None, rows=None):
+def _rows_ptr(pool, t, name, heads, rows):
     """Pointer and token stride of a bf16 [rows, heads, d_head] tensor whose
     heads lie side by side (a slice of a wider row is fine)."""
     import torch
 
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if not t.is_cuda or t.device.index != pool.device:
+    if t.get_device() != pool.device:
         raise ValueError(f"{name} must be on the pool's device cuda:{pool.device}")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    n, h, d = t.shape if t.dim() == 3 else (-1, -1, -1)
-    if d != pool.d_head or (heads is not None and h != heads) or (rows is not None and n != rows):
+    if t.shape != (rows, heads, pool.d_head):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {heads}, {pool.d_head})")
+    n, h, d = t.shape
     sn, sh, sd = t.stride()
     if sd != 1 or (h > 1 and sh != d):
         raise ValueError(f"{name} must hold each token's heads side by side (strides {t.stride()})")
@@ -438,20 +460,22 @@ def paged_rope_append(pool: Pool, rope: Rope, q, k_new, v_new, positions, slot_m
     T = int(slot_mapping.shape[0])
     kp, ks = _rows_ptr(pool, k_new, "k_new", pool.n_kv, T)
     vp, vs = _rows_ptr(pool, v_new, "v_new", pool.n_kv, T)
-    pp = _pool_ptr(pool, positions, "positions", torch.int32, 2, (rope.n_axes, T))
-    sp = _pool_ptr(pool, slot_mapping, "slot_mapping", torch.int64, 1)
+    pp = _fast_ptr(pool, positions, "positions", torch.int32, (rope.n_axes, T))
+    sp = _fast_ptr(pool, slot_mapping, "slot_mapping", torch.int64, (T,))
     qp = op = None
     qs = os_ = n_q = 0
     if q is not None:
         n_q = int(q.shape[1]) if q.dim() == 3 else -1
         qp, qs = _rows_ptr(pool, q, "q", n_q, T)
         if q_out is None:
-            q_out = torch.empty((T, n_q, pool.d_head), dtype=q.dtype, device=q.device)
-        op, os_ = _rows_ptr(pool, q_out, "q_out", n_q, T)
+            q_out = q.new_empty((T, n_q, pool.d_head))
+            op, os_ = q_out.data_ptr(), n_q * pool.d_head
+        else:
+            op, os_ = _rows_ptr(pool, q_out, "q_out", n_q, T)
     elif q_out is not None:
         raise ValueError("q_out without q")
     _check(load().paged_rope_append(pool.handle, rope.handle, qp, qs, n_q, kp, ks, vp, vs, pp, sp, T, op, os_,
-                                    _stream_handle(stream)))
+                                    _raw_stream(pool, stream)))
     return q_out
 
 
@@ -465,28 +489,28 @@ def paged_kv_gather(pool: Pool, out_indptr, block_tables, starts=None, n_rows=No
     was there, in arrays allocated here)."""
     import torch
 
-    ip = _pool_ptr(pool, out_indptr, "out_indptr", torch.int32, 1)
     B = int(out_indptr.shape[0]) - 1
     if B < 0:
         raise ValueError("out_indptr must have at least one entry")
-    tp = _pool_ptr(pool, block_tables, "block_tables", torch.int32, 2, (B, None))
-    st = None if starts is None else _pool_ptr(pool, starts, "starts", torch.int32, 1, (B,))
+    W = int(block_tables.shape[-1])
+    ip = _fast_ptr(pool, out_indptr, "out_indptr", torch.int32, (B + 1,))
+    tp = _fast_ptr(pool, block_tables, "block_tables", torch.int32, (B, W))
+    st = None if starts is None else _fast_ptr(pool, starts, "starts", torch.int32, (B,))
     if (k_out is None) != (v_out is None):
         raise ValueError("give both k_out and v_out, or neither")
     if k_out is None:
         if n_rows is None:
             raise ValueError("give n_rows, or k_out and v_out")
-        shape = (int(n_rows), pool.n_kv, pool.d_head)
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=out_indptr.device)
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=out_indptr.device)
-    n = int(k_out.shape[0])
-    if n_rows is not None and n != int(n_rows):
-        raise ValueError(f"k_out has {n} rows, n_rows is {n_rows}")
+        n = int(n_rows)
+        k_out, v_out = torch.empty((2, n, pool.n_kv, pool.d_head), dtype=torch.bfloat16, device=out_indptr.device)
+    else:
+        n = int(k_out.shape[0])
+        if n_rows is not None and n != int(n_rows):
+            raise ValueError(f"k_out has {n} rows, n_rows is {n_rows}")
     shape = (n, pool.n_kv, pool.d_head)
-    kp = _pool_ptr(pool, k_out, "k_out", torch.bfloat16, 3, shape)
-    vp = _pool_ptr(pool, v_out, "v_out", torch.bfloat16, 3, shape)
-    _check(load().paged_kv_gather(pool.handle, ip, tp, int(block_tables.shape[1]), st, B, n, kp, vp,
-                                  _stream_handle(stream)))
+    kp = _fast_ptr(pool, k_out, "k_out", torch.bfloat16, shape)
+    vp = _fast_ptr(pool, v_out, "v_out", torch.bfloat16, shape)
+    _check(load().paged_kv_gather(pool.handle, ip, tp, W, st, B, n, kp, vp, _raw_stream(pool, stream)))
     return k_out, v_out
 
 
@@ -563,22 +587,29 @@ class DiffParams:
         if norm_weight is not None and norm_weight.device != lambdas.device:
             raise ValueError("lambdas and norm_weight are on different devices")
         self.lambdas, self.norm_weight, self.lambda_init, self.eps = lambdas, norm_weight, float(lambda_init), float(eps)
+        self.device = lambdas.get_device()
         self._c = _DiffParams(lp, wp, self.lambda_init, self.eps)
         self._ref = ctypes.byref(self._c)
 
 
-def _diff_args(pool, q, params, rows):
-    """Checks shared by the differential calls; (q pointer, n_q, out shape)."""
+def _diff_args(pool, q, params, rows, out):
+    """Checks shared by the differential calls; (q pointer, n_q, out, out pointer)."""
     import torch
 
-    qp = _pool_ptr(pool, q, "q", torch.bfloat16, 3, (rows, None, pool.d_head))
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise TypeError("q must be a torch tensor [rows, n_q, d_head]")
+    n_q = int(q.shape[1])
+    qp = _fast_ptr(pool, q, "q", torch.bfloat16, (rows, n_q, pool.d_head))
     if not isinstance(params, DiffParams):
         raise TypeError("params must be a DiffParams")
-    if params.d_head != pool.d_head or params.lambdas.device.index != pool.device:
-        raise ValueError(f"params are for d_head {params.d_head} on {params.lambdas.device}, the pool has d_head "
+    if params.d_head != pool.d_head or params.device != pool.device:
+        raise ValueError(f"params are for d_head {params.d_head} on cuda:{params.device}, the pool has d_head "
                          f"{pool.d_head} on cuda:{pool.device}")
-    n_q = int(q.shape[1])
-    return qp, n_q, (int(q.shape[0]), n_q // 2, 2 * pool.d_head)
+    shape = (rows, n_q // 2, 2 * pool.d_head)
+    if out is None:
+        out = q.new_empty(shape)
+        return qp, n_q, out, out.data_ptr()
+    return qp, n_q, out, _fast_ptr(pool, out, "out", torch.bfloat16, shape)
 
 
 def paged_diff_decode_attention(pool: Pool, q, block_tables, context_lens, scale: float, params: DiffParams,
@@ -589,15 +620,12 @@ def paged_diff_decode_attention(pool: Pool, q, block_tables, context_lens, scale
     allocated if not given)."""
     import torch
 
-    cp = _pool_ptr(pool, context_lens, "context_lens", torch.int32, 1)
-    B = int(context_lens.shape[0])
-    qp, n_q, shape = _diff_args(pool, q, params, B)
-    tp = _pool_ptr(pool, block_tables, "block_tables", torch.int32, 2, (B, None))
-    if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
-    op = _pool_ptr(pool, out, "out", torch.bfloat16, 3, shape)
-    _check(load().paged_diff_decode_attention(pool.handle, qp, n_q, tp, int(block_tables.shape[1]), cp, B,
-                                              float(scale), params._ref, op, _stream_handle(stream)))
+    B, W = int(context_lens.shape[0]), int(block_tables.shape[-1])
+    qp, n_q, out, op = _diff_args(pool, q, params, B, out)
+    cp = _fast_ptr(pool, context_lens, "context_lens", torch.int32, (B,))
+    tp = _fast_ptr(pool, block_tables, "block_tables", torch.int32, (B, W))
+    _check(load().paged_diff_decode_attention(pool.handle, qp, n_q, tp, W, cp, B, float(scale), params._ref, op,
+                                              _raw_stream(pool, stream)))
     return out
 
 
@@ -610,16 +638,14 @@ def paged_diff_prefill_attention(pool: Pool, q, qo_indptr, block_tables, context
     [rows, n_q / 2, 2 * d_head], allocated if not given)."""
     import torch
 
-    qp, n_q, shape = _diff_args(pool, q, params, None)
-    cp = _pool_ptr(pool, context_lens, "context_lens", torch.int32, 1)
-    B = int(context_lens.shape[0])
-    ip = _pool_ptr(pool, qo_indptr, "qo_indptr", torch.int32, 1, (B + 1,))
-    tp = _pool_ptr(pool, block_tables, "block_tables", torch.int32, 2, (B, None))
-    if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
-    op = _pool_ptr(pool, out, "out", torch.bfloat16, 3, shape)
-    _check(load().paged_diff_prefill_attention(pool.handle, qp, shape[0], n_q, ip, tp, int(block_tables.shape[1]), cp, B,
-                                               float(scale), params._ref, op, _stream_handle(stream)))
+    B, W = int(context_lens.shape[0]), int(block_tables.shape[-1])
+    rows = int(q.shape[0])
+    qp, n_q, out, op = _diff_args(pool, q, params, rows, out)
+    cp = _fast_ptr(pool, context_lens, "context_lens", torch.int32, (B,))
+    ip = _fast_ptr(pool, qo_indptr, "qo_indptr", torch.int32, (B + 1,))
+    tp = _fast_ptr(pool, block_tables, "block_tables", torch.int32, (B, W))
+    _check(load().paged_diff_prefill_attention(pool.handle, qp, rows, n_q, ip, tp, W, cp, B, float(scale), params._ref,
+                                               op, _raw_stream(pool, stream)))
     return out
 
 

@@ -2,31 +2,34 @@
 // tcgen05 tensor cores.
 //
 // Mathematics (see diff.cu for the head layout): for the rows of a pair's G
-// heads, o = P1 V - lambda P2 V with P_m = softmax(s Q_m K_m^T) and V the
-// pair's two value heads side by side.  Both products go into ONE accumulator:
-// a first sweep over the keys finds each row's maximum m and sum l of both
-// maps, a second one recomputes the scores and adds
-//   c1 2^(s1 - m1) V  and  -+ c2 2^(s2 - m2) V,   c1 / c2 = l2 / (|lambda| l1),
+// heads, o = (P1 - lambda P2) V with P_m = softmax(s Q_m K_m^T) and V the
+// pair's two value heads side by side.  A first sweep over the keys finds each
+// row's maximum m and sum l of both maps; a second one recomputes the scores,
+// forms ONE weight per key,
+//   w = c1 2^(s1 - m1) -+ c2 2^(s2 - m2),   c1 / c2 = l2 / (|lambda| l1),
 // the larger of c1, c2 being 2^8 (weights stay within f16's range whatever
-// the two sums are), so that o = accumulator / (c1 l1).  All statistics are
-// final before the first weight is formed: no accumulator is ever rescaled,
-// and the two maps' weights need nothing from each other inside the sweep.
-// Separate accumulators for the two maps would take all 512 columns of tensor
-// memory at d_head 128 and leave none for scores; the price of one is the
-// second Q K^T (4 of 16 MMA units where 12 are the least).
+// the two sums are), and adds w V; o = accumulator / (c1 l1).  The difference
+// is taken in fp32 before the rounding to the product's type, so what the two
+// maps share never enters it, and V is multiplied once instead of once per
+// map: with the second Q K^T the MMA work is that of separate products of both
+// maps (12 d per row and key), in half the accumulator -- two accumulators of
+// 2 d columns would take all of tensor memory at d_head 128 and leave none for
+// scores.  All statistics are final before the first weight is formed: no
+// accumulator is ever rescaled.
 //
 // Design (one persistent CTA per SM, warp-specialised, as prefill.cu):
 //   * a tile is 128 query rows (token, head) of one (sequence, pair): both
-//     maps' queries.  A step is 128 keys; its units are (map 1), (map 2).
-//   * warp 8 streams Q and the K_m tiles (one unit each, both sweeps), warp 9
-//     the V tiles (second sweep; units of 64 keys x 2 d channels, used by both
-//     maps), warp 10 issues S_m = Q_m K_m^T, warp 11 O += P_m V.
-//   * warps 0-3 take map 1's scores, warps 4-7 map 2's, a thread a row: the
-//     statistics are the thread's own, and while one map's weights are formed
-//     the tensor cores work on the other's.  P_m overwrites the scores it came
-//     from.  The two threads of a row swap l (through shared memory) between
-//     the sweeps, and half sums of squares at the end, where each normalises
-//     and stores one value head's half of the row.
+//     maps' queries.  A step is 128 keys.
+//   * warp 8 streams Q and the K_m tiles (one unit each; the second sweep
+//     takes map 2 first, whose scores are free sooner), warp 9 the V tiles
+//     (second sweep; units of 64 keys x 2 d channels), warp 10 issues
+//     S_m = Q_m K_m^T, warp 11 O += W V.
+//   * first sweep: warps 0-3 take map 1's scores, warps 4-7 map 2's, a thread
+//     a row, so the statistics are the thread's own.  Between the sweeps the
+//     two threads of a row swap (m, l) through shared memory.  Second sweep:
+//     warps 0-3 take the first 64 keys of a step, warps 4-7 the others, of
+//     both maps; the weights overwrite the first map's scores.  At the end
+//     each thread normalises and stores one value head's half of its row.
 //   * value rows behind the sequence's end (a page that ends inside a tile)
 //     are zeroed in shared memory before their product: a weight of 0 does not
 //     cancel what is not finite.
@@ -50,7 +53,8 @@ constexpr int kUnitBlocks = kVKeys / kBlockSize;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kKWarp = 8, kVWarp = 9, kQkWarp = 10, kPvWarp = 11;
 constexpr int kThreads = 12 * 32;
-// Tensor memory: S_1 at 0, S_2 at 128 (fp32 scores; P_m over the first 64 columns of S_m), O at 256 (2 d).
+// Tensor memory: S_1 at 0, S_2 at 128 (fp32 scores of 128 keys; the weights of keys 64 h .. + 63, packed in
+// pairs, over the first 32 columns of their S_1), O at 256 (2 d).
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;
 constexpr uint32_t kKHalf = kKeys * 128;   // a 64-column range of a Q or K tile
@@ -81,16 +85,18 @@ struct Layout {
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kK = kQ + 2 * QT;
     static constexpr uint32_t kV = kK + kKStages * KT;
-    static constexpr uint32_t kX = kV + kVStages * VT;  // [2 maps][kRows] float: l, then sums of squares
-    static constexpr uint32_t kBar = kX + 2 * kRows * 4;
+    static constexpr uint32_t kX = kV + kVStages * VT;   // [2][kRows] float: l of a map, then sums of squares
+    static constexpr uint32_t kXm = kX + 2 * kRows * 4;  // [2][kRows] bf16: m of a map
+    static constexpr uint32_t kBar = kXm + 2 * kRows * 2;
     // *_RAW: FP8 pools' copies complete there; K_FULL, V_FULL and Q_FULL follow when the rows are f16
     enum { Q_RAW = 0, Q_FULL, Q_FREE, K_RAW, K_FULL = K_RAW + kKStages, K_EMPTY = K_FULL + kKStages,
            V_RAW = K_EMPTY + kKStages, V_FULL = V_RAW + kVStages, V_EMPTY = V_FULL + kVStages,
            S_FULL = V_EMPTY + kVStages,  // per map
-           S_READ = S_FULL + 2,          // per map: a first-sweep unit's scores are in registers
-           P_FULL = S_READ + 2,          // per (map, key half)
-           PV_DONE = P_FULL + 4,         // per map: a second-sweep unit's product has run
-           O_FULL = PV_DONE + 2, O_FREE, PAIR, DRAIN = PAIR + 4, NBARS = DRAIN + 2 };
+           S_READ = S_FULL + 2,          // per map: a first-sweep step's scores are in registers
+           S2_READ = S_READ + 2,         // map 2: a second-sweep step's scores are in registers
+           P_FULL = S2_READ + 1,         // per key half: the weights are in tensor memory
+           PV_DONE = P_FULL + 2,         // a second-sweep step's product has run
+           O_FULL = PV_DONE + 1, O_FREE, PAIR, DRAIN = PAIR + 4, NBARS = DRAIN + 2 };
     static constexpr uint32_t kTmemSlot = kBar + NBARS * 8;
     static constexpr uint32_t kAbort = kTmemSlot + 4;
     static constexpr uint32_t kEnd = kAbort + 4;
@@ -160,18 +166,7 @@ __device__ __forceinline__ void convert_q(uint32_t base, int lane)
     }
 }
 
-// ------------------------------------------------------------- packed fp32
-
-__device__ __forceinline__ float2 fmul2(float2 a, float2 b)
-{
-    float2 d;
-    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-
+// (a.x + b.x, a.y + b.y) in one paired instruction
 __device__ __forceinline__ float2 fadd2(float2 a, float2 b)
 {
     float2 d;
@@ -284,8 +279,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&tm_kv);
         for (int i = 0; i < L::NBARS; ++i) {
             uint32_t n = 1;
-            if (i >= L::S_READ && i < L::PV_DONE) n = 4;        // S_READ, P_FULL: a map's four warps
-            if (i == L::O_FREE) n = kSoftmaxWarps;
+            if (i == L::S_READ || i == L::S_READ + 1 || i == L::P_FULL || i == L::P_FULL + 1) n = 4;
+            if (i == L::S2_READ || i == L::O_FREE) n = kSoftmaxWarps;
             if (i >= L::PAIR && i < L::PAIR + 4) n = 2;         // the two warps of a lane quarter
             if (i == L::Q_FULL && F8) n = 2;                    // a warp converts each map's queries
             mbar_init(&bar[i], n);
@@ -375,7 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool present = lane < kStepBlocks && s * kStepBlocks + lane < t.n_blocks;
                     const bool valid = present && cur >= 0 && cur < a.num_blocks;
                     if (present && !valid && sweep == 0) atomicOr(a.err, PKV_DEVERR_BLOCK_RANGE);
-                    for (int m = 0; m < 2; ++m, ++u) {
+                    for (int i = 0; i < 2; ++i, ++u) {
+                        const int m = i ^ sweep;  // the second sweep takes map 2 first
                         const int st = u % KS, use = u / KS;
                         if (use > 0 && !(ok = wait_all(&bar[L::K_EMPTY + st], (use - 1) & 1))) break;
                         uint64_t *kb = &bar[(F8 ? L::K_RAW : L::K_FULL) + st];
@@ -495,7 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++n;
             for (int sweep = 0; sweep < 2 && ok; ++sweep)
                 for (int s = 0; s < t.n_steps && ok; ++s) {
-                    for (int m = 0; m < 2; ++m, ++u) {
+                    for (int i = 0; i < 2; ++i, ++u) {
+                        const int m = i ^ sweep;
                         const int st = u % KS;
                         if constexpr (kSplitK) {  // this warp's rows of the unit
                             if (!(ok = wait_all(&bar[L::K_RAW + st], (u / KS) & 1))) break;
@@ -504,9 +501,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             __syncwarp();
                         }
                         if (!(ok = wait_all(&bar[L::K_FULL + st], (u / KS) & 1))) break;
-                        // S_m is free: its scores are in registers (first sweep), or its product has run
+                        // S_m is free: its scores are in registers, or (second sweep, map 1, where the
+                        // weights overwrite them) its product has run
                         if (prev == 0 && !(ok = wait_all(&bar[L::S_READ + m], (reads - 1) & 1))) break;
-                        if (prev == 1 && !(ok = wait_all(&bar[L::PV_DONE + m], (prods - 1) & 1))) break;
+                        if (prev == 1 && !(ok = wait_all(&bar[m == 0 ? L::PV_DONE : L::S2_READ], (prods - 1) & 1))) break;
                         tc_fence_after();
                         if (lane == 0) {
                             const uint32_t qb = base + L::kQ + m * L::QT, kb = base + L::kK + st * L::KT;
@@ -518,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             umma_commit(&bar[L::S_FULL + m]);
                             umma_commit(&bar[L::K_EMPTY + st]);
-                            if (sweep == 1 && s == t.n_steps - 1 && m == 1) umma_commit(&bar[L::Q_FREE]);
+                            if (sweep == 1 && s == t.n_steps - 1 && i == 1) umma_commit(&bar[L::Q_FREE]);
                         }
                         __syncwarp();
                     }
@@ -545,45 +543,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++n;
             // the block the sequence ends inside of, where this tile reaches it
             const int end_blk = (t.C % kBlockSize) && t.C / kBlockSize < t.n_blocks ? t.C / kBlockSize : -1;
-            for (int s = 0; s < t.n_steps && ok; ++s, ++steps, u += 2) {
-                for (int m = 0; m < 2 && ok; ++m) {
-                    for (int h = 0; h < 2; ++h) {
-                        const int st = (u + h) % VS;
-                        if (m == 0) {
-                            if constexpr (F8) {  // value head 1's rows
-                                if (!(ok = wait_all(&bar[L::V_RAW + st], ((u + h) / VS) & 1))) break;
-                                convert_f16<D, kVKeys>(base + L::kV + st * L::VT + NH * kVChunk, lane, 0, kVKeys);
-                                fence_proxy_async_smem();
-                                __syncwarp();
-                            }
-                            if (!(ok = wait_all(&bar[L::V_FULL + st], ((u + h) / VS) & 1))) break;
-                            if (end_blk >= 0 && end_blk / kUnitBlocks == 2 * s + h) {
-                                const int r0 = (end_blk % kUnitBlocks) * kBlockSize;
-                                const int first = r0 + t.C % kBlockSize, rows = r0 + kBlockSize - first;
-                                for (int i = lane; i < rows * 8 * 2 * NH; i += 32) {
-                                    const int row = first + (i >> 3) % rows, ch = (i >> 3) / rows;
-                                    sts128(base + L::kV + st * L::VT + ch * kVChunk + row * 128 + (i & 7) * 16,
-                                           make_uint4(0, 0, 0, 0));
-                                }
-                                fence_proxy_async_smem();
-                                __syncwarp();
-                            }
-                        }
-                        if (!(ok = wait_all(&bar[L::P_FULL + 2 * m + h], steps & 1))) break;
-                        tc_fence_after();
-                        if (lane == 0) {
-                            const uint32_t vb = base + L::kV + st * L::VT;
-#pragma unroll
-                            for (int kk = 0; kk < kVKeys / 16; ++kk)
-                                umma_ts(tmem + kColO, tmem + m * kKeys + h * (kVKeys / 2) + 8 * kk,
-                                        smem_desc(vb + kk * 2048, kVChunk, 1024), idesc,
-                                        (s > 0 || m > 0 || h > 0 || kk > 0) ? 1u : 0u);
-                            if (m == 1) umma_commit(&bar[L::V_EMPTY + st]);
-                            if (h == 1) umma_commit(&bar[L::PV_DONE + m]);
-                            if (h == 1 && m == 1 && s == t.n_steps - 1) umma_commit(&bar[L::O_FULL]);
-                        }
+            for (int s = 0; s < t.n_steps && ok; ++s, ++steps) {
+                for (int h = 0; h < 2; ++h, ++u) {
+                    const int st = u % VS;
+                    if constexpr (F8) {  // value head 1's rows
+                        if (!(ok = wait_all(&bar[L::V_RAW + st], (u / VS) & 1))) break;
+                        convert_f16<D, kVKeys>(base + L::kV + st * L::VT + NH * kVChunk, lane, 0, kVKeys);
+                        fence_proxy_async_smem();
                         __syncwarp();
                     }
+                    if (!(ok = wait_all(&bar[L::V_FULL + st], (u / VS) & 1))) break;
+                    if (end_blk >= 0 && end_blk / kUnitBlocks == 2 * s + h) {
+                        const int r0 = (end_blk % kUnitBlocks) * kBlockSize;
+                        const int first = r0 + t.C % kBlockSize, rows = r0 + kBlockSize - first;
+                        for (int i = lane; i < rows * 8 * 2 * NH; i += 32) {
+                            const int row = first + (i >> 3) % rows, ch = (i >> 3) / rows;
+                            sts128(base + L::kV + st * L::VT + ch * kVChunk + row * 128 + (i & 7) * 16,
+                                   make_uint4(0, 0, 0, 0));
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (!(ok = wait_all(&bar[L::P_FULL + h], steps & 1))) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint32_t vb = base + L::kV + st * L::VT;
+#pragma unroll
+                        for (int kk = 0; kk < kVKeys / 16; ++kk)
+                            umma_ts(tmem + kColO, tmem + h * kVKeys + 8 * kk, smem_desc(vb + kk * 2048, kVChunk, 1024),
+                                    idesc, (s > 0 || h > 0 || kk > 0) ? 1u : 0u);
+                        umma_commit(&bar[L::V_EMPTY + st]);
+                        if (h == 1) umma_commit(&bar[L::PV_DONE]);
+                        if (h == 1 && s == t.n_steps - 1) umma_commit(&bar[L::O_FULL]);
+                    }
+                    __syncwarp();
                 }
             }
         }
@@ -593,17 +586,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) set_abort();
     } else {
         // ---------------------------------------------------------- statistics, weights, norm
-        const int m = warp >> 2, quarter = warp & 3;  // this warp's map, its TMEM lanes 32 quarter ..
+        // m: this warp's map (first sweep), key half (second sweep) and value head (the end)
+        const int m = warp >> 2, quarter = warp & 3;
         const int row = quarter * 32 + lane;
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-        const uint32_t ts = tmem + lane_off + m * kKeys;       // this map's scores
+        const uint32_t ts = tmem + lane_off;
         const uint32_t to = tmem + lane_off + kColO + m * D;   // value head m's half of O
         uint64_t *pair = &bar[L::PAIR + quarter];
         float *xs = reinterpret_cast<float *>(sm + L::kX);
+        uint16_t *xm = reinterpret_cast<uint16_t *>(sm + L::kXm);
         const float lam = diff_lambda<D>(a.w, lane);
         const float abs_lam = fabsf(lam);
-        const uint32_t flip = m == 1 && !(lam < 0.0f) ? 0x80008000u : 0u;  // the second map is subtracted
-        int gs = 0, n = 0, pph = 0;  // units of this map, tiles, phases of the pair barrier
+        const float sign = lam < 0.0f ? 1.0f : -1.0f;  // of the second map's weights
+        const bool rising = a.qscale >= 0.0f;          // the largest score has the largest q . k (else the smallest)
+        int gs = 0, n = 0, pph = 0;  // steps of both sweeps, tiles, phases of the pair barrier
         bool ok = true;
         for (int x = blockIdx.x; ok; x += gridDim.x) {
             Tile t;
@@ -613,7 +609,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (*abort_flag) break;
             const int r = t.rt0 + row;
             const int pos = t.C - t.T + min(r, t.R - 1) / G;  // this row sees keys 0 .. pos
-            const float qs = F8 ? a.qscale * a.scales[2 * t.p + m] : a.qscale;
+            const float qs0 = F8 ? a.qscale * a.scales[2 * t.p] : a.qscale;
+            const float qs1 = F8 ? a.qscale * a.scales[2 * t.p + 1] : a.qscale;
+            const float qs = m == 0 ? qs0 : qs1;
             const int32_t *trow = a.block_tables + (int64_t)t.b * a.W;
             auto ids_of = [&](int s) -> int {
                 const int nb = s * kStepBlocks + lane;
@@ -623,22 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto mask_of = [&](int id) -> uint32_t {
                 return __ballot_sync(kFull, lane < kStepBlocks && id >= 0 && id < a.num_blocks);
             };
-            // keys 64 h .. + 63 of the step: loaded, and what this row does not see set to -inf
-            auto load_half = [&](uint32_t (&sr)[64], int h) {
-                tmem_ld32(ts + 64 * h, sr);
-                tmem_ld32(ts + 64 * h + 32, sr + 32);
-                tmem_wait_ld();
-            };
-            auto hide = [&](uint32_t (&sr)[64], int h, int s, uint32_t mask) {
-                const int key0 = s * kKeys + 64 * h;
-                const uint32_t mh = (mask >> (4 * h)) & 15u;
-                if (!(mh == 15u && key0 + 63 <= pos)) {
-#pragma unroll
-                    for (int k = 0; k < 64; ++k)
-                        if (!(((mh >> (k / kBlockSize)) & 1u) && key0 + k <= pos)) sr[k] = 0xff800000u;
-                }
-            };
-            // ---- first sweep: maximum and sum of this map's row ----
+            // ---- first sweep: maximum and sum of map m's row ----
             float mx = -INFINITY, l = 0.0f;
             int nxt = ids_of(0);
             for (int s = 0; s < t.n_steps; ++s, ++gs) {
@@ -649,37 +632,48 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t sr[64];
-                    load_half(sr, h);
+                    tmem_ld32(ts + m * kKeys + 64 * h, sr);
+                    tmem_ld32(ts + m * kKeys + 64 * h + 32, sr + 32);
+                    tmem_wait_ld();
                     if (h == 1) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bar[L::S_READ + m]);
                     }
-                    float2 v[32];
+                    const int key0 = s * kKeys + 64 * h;
+                    const uint32_t mh = (mask >> (4 * h)) & 15u;
+                    if (!(mh == 15u && key0 + 63 <= pos)) {  // what this row does not see never has the largest score
+                        const uint32_t never = rising ? 0xff800000u : 0x7f800000u;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        v[i] = fmul2(make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])),
-                                     make_float2(qs, qs));
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        sr[2 * i] = __float_as_uint(v[i].x);
-                        sr[2 * i + 1] = __float_as_uint(v[i].y);
+                        for (int k = 0; k < 64; ++k)
+                            if (!(((mh >> (k / kBlockSize)) & 1u) && key0 + k <= pos)) sr[k] = never;
                     }
-                    hide(sr, h, s, mask);
                     float mc[8];
+                    if (rising) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        auto e = [&](int q) { return __uint_as_float(sr[j + 8 * q]); };
-                        mc[j] = fmaxf(fmax3(fmax3(fmax3(e(0), e(1), e(2)), e(3), e(4)), e(5), e(6)), e(7));
+                        for (int j = 0; j < 8; ++j) {
+                            auto e = [&](int q) { return __uint_as_float(sr[j + 8 * q]); };
+                            mc[j] = fmaxf(fmax3(fmax3(fmax3(e(0), e(1), e(2)), e(3), e(4)), e(5), e(6)), e(7));
+                        }
+                        mc[0] = fmax3(fmax3(mc[0], mc[1], mc[2]), fmax3(mc[3], mc[4], mc[5]), fmaxf(mc[6], mc[7]));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            mc[j] = __uint_as_float(sr[j]);
+#pragma unroll
+                            for (int q = 1; q < 8; ++q) mc[j] = fminf(mc[j], __uint_as_float(sr[j + 8 * q]));
+                        }
+#pragma unroll
+                        for (int j = 1; j < 8; ++j) mc[0] = fminf(mc[0], mc[j]);
                     }
-                    const float mn = fmaxf(mx, fmax3(fmax3(mc[0], mc[1], mc[2]), fmax3(mc[3], mc[4], mc[5]),
-                                                     fmaxf(mc[6], mc[7])));
+                    const bool none = mc[0] == (rising ? -INFINITY : INFINITY);
+                    const float mn = none ? mx : fmaxf(mx, mc[0] * qs);
                     const float neg = mn == -INFINITY ? 0.0f : -mn;
                     float2 sum[4] = {};
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        const float2 d = fadd2(make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])),
-                                               make_float2(neg, neg));
+                        const float2 d = ffma2(make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])),
+                                               make_float2(qs, qs), make_float2(neg, neg));
                         sum[i & 3] = fadd2(sum[i & 3], make_float2(ex2(d.x), ex2(d.y)));
                     }
                     const float2 q0 = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
@@ -688,65 +682,71 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!ok) break;
-            // ---- both maps' sums give the weights' factors ----
+            // ---- both maps' statistics give the weights' factors ----
             if (n > 0) {  // the partner has read the last tile's sums of squares
                 if (!(ok = wait_all(pair, pph & 1))) break;
                 ++pph;
             }
-            xs[m * kRows + row] = l;
+            const __nv_bfloat16 mb = __float2bfloat16_ru(mx);  // the reference both threads use: l is put against it
+            xm[m * kRows + row] = __bfloat16_as_ushort(mb);
+            xs[m * kRows + row] = mx == -INFINITY ? l : l * ex2(mx - __bfloat162float(mb));
             __syncwarp();
             if (lane == 0) mbar_arrive(pair);
             if (!(ok = wait_all(pair, pph & 1))) break;
             ++pph;
-            const float l_ot = xs[(m ^ 1) * kRows + row];
-            const float l1 = m == 0 ? l : l_ot, l2 = m == 0 ? l_ot : l;
-            float neg = 0.0f, inv = 0.0f;  // P = 2^(s qs + neg); o = inv * accumulator
+            const float l1 = xs[row], l2 = xs[kRows + row];
+            float n0 = 0.0f, n1 = 0.0f, inv = 0.0f;  // weights 2^(s qs + n); o = inv * accumulator
             if (!(l1 == 0.0f)) {  // (a row none of whose blocks could be read stays all zero)
                 const float f = abs_lam * l1 / l2;  // c2 / c1
-                const float c = m == 0 ? (f <= 1.0f ? 1.0f : 1.0f / f) : (f <= 1.0f ? f : 1.0f);
-                neg = log2f(c) + kBoost - mx;
+                n0 = log2f(f <= 1.0f ? 1.0f : 1.0f / f) + kBoost - __bfloat162float(__ushort_as_bfloat16(xm[row]));
+                n1 = log2f(f <= 1.0f ? f : 1.0f) + kBoost - __bfloat162float(__ushort_as_bfloat16(xm[kRows + row]));
                 inv = (f <= 1.0f ? 1.0f / l1 : abs_lam / l2) * (1.0f / 256.0f);
             }
-            // ---- second sweep: weights ----
+            // ---- second sweep: the weights of keys 64 m .. + 63 of every step ----
             nxt = ids_of(0);
             for (int s = 0; s < t.n_steps; ++s, ++gs) {
                 const uint32_t mask = mask_of(nxt);
                 if (s + 1 < t.n_steps) nxt = ids_of(s + 1);
-                if (!(ok = wait_all(&bar[L::S_FULL + m], gs & 1))) break;
+                const int key0 = s * kKeys + 64 * m;
+                const uint32_t mh = (mask >> (4 * m)) & 15u;
+                const bool all = mh == 15u && key0 + 63 <= pos;
+                if (!(ok = wait_all(&bar[L::S_FULL + 1], gs & 1))) break;
+                if (!(ok = wait_all(&bar[L::S_FULL], gs & 1))) break;
                 tc_fence_after();
+                uint32_t pk[32];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t sr[64];
-                    load_half(sr, h);
-                    uint32_t pk[32];
-                    const int key0 = s * kKeys + 64 * h;
-                    const bool all = ((mask >> (4 * h)) & 15u) == 15u && key0 + 63 <= pos;
-                    float2 v[32];
+                for (int h = 0; h < 2; ++h) {  // 32 keys at a time
+                    uint32_t s0[32], s1[32];
+                    tmem_ld32(ts + 64 * m + 32 * h, s0);
+                    tmem_ld32(ts + kKeys + 64 * m + 32 * h, s1);
+                    tmem_wait_ld();
+                    if (h == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar[L::S2_READ]);
+                    }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        v[i] = ffma2(make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])),
-                                     make_float2(qs, qs), make_float2(neg, neg));
-                    if (!all) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            sr[2 * i] = __float_as_uint(v[i].x);
-                            sr[2 * i + 1] = __float_as_uint(v[i].y);
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 u0 = ffma2(make_float2(__uint_as_float(s0[2 * i]), __uint_as_float(s0[2 * i + 1])),
+                                                make_float2(qs0, qs0), make_float2(n0, n0));
+                        const float2 u1 = ffma2(make_float2(__uint_as_float(s1[2 * i]), __uint_as_float(s1[2 * i + 1])),
+                                                make_float2(qs1, qs1), make_float2(n1, n1));
+                        float2 w = ffma2(make_float2(ex2(u1.x), ex2(u1.y)), make_float2(sign, sign),
+                                         make_float2(ex2(u0.x), ex2(u0.y)));
+                        if (!all) {
+                            const int k = 32 * h + 2 * i;
+                            const bool seen = (mh >> (k / kBlockSize)) & 1u;
+                            if (!(seen && key0 + k <= pos)) w.x = 0.0f;
+                            if (!(seen && key0 + k + 1 <= pos)) w.y = 0.0f;
                         }
-                        hide(sr, h, s, mask);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1]));
+                        pk[16 * h + i] = F8 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
                     }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float px = ex2(v[i].x), py = ex2(v[i].y);
-                        pk[i] = (F8 ? pack_f16x2(px, py) : pack_bf16x2(px, py)) ^ flip;
-                    }
-                    tmem_st32(ts + 32 * h, pk);  // over scores of this step that are already read
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar[L::P_FULL + 2 * m + h]);
                 }
+                tmem_st32(ts + 64 * m, pk);  // over this warp's own scores of map 1, which are read
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[L::P_FULL + m]);
             }
             if (!ok) break;
             // ---- norm and store: this thread's row, value head m's half ----
@@ -765,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ss = fmaf(v, v, ss);
                 }
             }
-            xs[m * kRows + row] = ss;  // the partner took l before it formed the weights of this O
+            xs[m * kRows + row] = ss;  // the partner took l before it formed the weights behind this O
             __syncwarp();
             if (lane == 0) mbar_arrive(pair);
             if (!(ok = wait_all(pair, pph & 1))) break;
@@ -896,7 +896,8 @@ extern "C" pkv_status paged_diff_prefill_attention(pkv_pool *pool, const void *q
     a.num_blocks = pool->num_blocks;
     a.n_rows = n_rows;
     a.oob_row = (int)(pool->num_blocks * pool->n_kv * 2 * kBlockSize);
-    a.qscale = scale * kLog2e;
+    // (0 as 1e-30: the same scores to fp32, but -inf for hidden ones stays -inf)
+    a.qscale = scale == 0.0f ? 1e-30f : scale * kLog2e;
     a.scales = pool->scales;
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.err = pool->err;

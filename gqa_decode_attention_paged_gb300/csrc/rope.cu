@@ -257,7 +257,9 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_append_kernel(const __gr
                     uint8_t *entry = a.pool + (blk * a.n_kv + g) * i4_entry_bytes(D);
                     uint32_t w0 = 0, w1 = 0;
                     if (is_v) {
-                        float sc = __fdiv_rn(__fsub_rn(mx, mn), 15.0f);
+                        // (max - min) / 15 as one product with fp32(1/15): at most a step of the last place
+                        // from paged_kv_append's quotient
+                        float sc = __fmul_rn(__fsub_rn(mx, mn), 1.0f / 15.0f);
                         if (sc == 0.0f) sc = 1.0f;
                         const float z = __fadd_rn(mn, 0.0f);  // no negative zero
 #pragma unroll

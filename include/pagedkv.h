@@ -244,7 +244,10 @@ pkv_status pkv_rope_destroy(pkv_rope *rope);
  *                 with q, k_new or v_new otherwise.
  * The rotation is computed in fp32 and rounded once, to bf16 or, in FP8 and
  * 4-bit pools, straight to E4M3(x / scale[g]) or the 4-bit code; values are
- * stored exactly as paged_kv_append stores them.  n_tokens == 0 is a no-op.
+ * stored as paged_kv_append stores them (bf16 and FP8: the same bytes; 4-bit:
+ * the row's scale is (max - min) * fp32(1/15), at most one step of its last
+ * place from the append's quotient, so that a value halfway between two codes
+ * may take the other one).  n_tokens == 0 is a no-op.
  * Counted with the append launches (pkv_timing).
  * Errors: EINVAL (null, misaligned or overlapping arrays, strides, rot_dim
  * above the pool's d_head, scales unset, the pool's device not current),

@@ -61,6 +61,27 @@ def raw(pool):
     return pool.k_view().cpu().numpy(), pool.v_view().cpu().numpy()
 
 
+def value_rows4(v):
+    """Codes and (scale, zero point) of 4-bit value rows [T, n_kv, d] bf16, in 32-bit arithmetic:
+    scale = (max - min) * fp32(1/15) (1 if 0), zero point = min, code = rint((v - min) / scale)."""
+    x = v.float().cpu().numpy()
+    z = x.min(-1, keepdims=True) + np.float32(0)
+    s = (x.max(-1, keepdims=True) - z) * np.float32(1 / 15)
+    s = np.where(s == 0, np.float32(1), s)
+    c = np.clip(np.rint((x - z) / s), 0, 15).astype(np.uint8)
+    return c[..., 0::2] | (c[..., 1::2] << 4), np.concatenate((s, z), -1)
+
+
+def expect_values(m, v, slots):
+    """The mirror's values after v went to slots, as paged_rope_append stores them."""
+    if m.dtype != oracle.INT4:
+        return
+    codes, params = value_rows4(v)
+    for t, s in enumerate(slots):
+        if 0 <= s < m.num_blocks * BS:
+            m.v[s // BS, :, s % BS], m.v_params[s // BS, :, s % BS] = codes[t], params[t]
+
+
 def dev(a, dt):
     return torch.from_numpy(np.ascontiguousarray(a)).to("cuda").to(dt)
 
@@ -110,7 +131,8 @@ def test_rope_append_matches_the_64_bit_form(case, far):
         got = pkv.paged_rope_append(pool, rope, q, k, v, dev(pos, torch.int32), dev(slots, torch.int64))
         kb, vb = raw(pool)
         assert pool.get_error() == 0
-        m.append(bits(k), bits(v), slots)  # values: exactly what an append stores
+        m.append(bits(k), bits(v), slots)  # values: what an append stores
+        expect_values(m, v, slots)
         assert np.array_equal(vb, m.v.view(np.uint8).reshape(vb.shape))
         if kv == "int4":
             assert np.array_equal(pool.v_params_view().cpu().numpy(), m.v_params)
@@ -147,6 +169,7 @@ def test_rope_append_at_position_zero_is_the_plain_append(kv):
         got = pkv.paged_rope_append(pool, pkv.Rope(inv), q, k, v, dev(pos * 0, torch.int32), dev(slots, torch.int64))
         kb, vb = raw(pool)
     m.append(bits(k), bits(v), slots)
+    expect_values(m, v, slots)
     assert torch.equal(got, q)
     assert np.array_equal(kb, m.k.view(np.uint8).reshape(kb.shape))
     assert np.array_equal(vb, m.v.view(np.uint8).reshape(vb.shape))
@@ -193,6 +216,7 @@ def test_rope_append_skips_padding_and_flags_slots_past_the_pool(kv):
         kb, vb = raw(pool)
         assert pool.get_error(clear=True) == pkv.DEVERR_SLOT_RANGE
         assert m.append(bits(k), bits(v), slots) == 2
+        expect_values(m, v, slots)
         assert np.array_equal(vb, m.v.view(np.uint8).reshape(vb.shape))
         assert (kb[0, :, [0, 3, 7]] == 0).all() and (kb[1, :, 4:] == 0).all()  # rows no token wrote
         ref, size = turned64(f32(q), pos, inv, axis, False)
