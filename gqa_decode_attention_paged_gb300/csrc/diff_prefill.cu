@@ -20,16 +20,18 @@
 // Design (one persistent CTA per SM, warp-specialised, as prefill.cu):
 //   * a tile is 128 query rows (token, head) of one (sequence, pair): both
 //     maps' queries.  A step is 128 keys.
-//   * warp 8 streams Q and the K_m tiles (one unit each; the second sweep
-//     takes map 2 first, whose scores are free sooner), warp 9 the V tiles
-//     (second sweep; units of 64 keys x 2 d channels), warp 10 issues
-//     S_m = Q_m K_m^T, warp 11 O += W V.
-//   * first sweep: warps 0-3 take map 1's scores, warps 4-7 map 2's, a thread
-//     a row, so the statistics are the thread's own.  Between the sweeps the
-//     two threads of a row swap (m, l) through shared memory.  Second sweep:
-//     warps 0-3 take the first 64 keys of a step, warps 4-7 the others, of
-//     both maps; the weights overwrite the first map's scores.  At the end
-//     each thread normalises and stores one value head's half of its row.
+//   * warp 16 streams Q and the K_m tiles (one unit each; the second sweep
+//     takes map 2 first, whose scores are free sooner), warp 17 the V tiles
+//     (second sweep; units of 64 keys x 2 d channels), warp 18 issues
+//     S_m = Q_m K_m^T, warp 19 O += W V.
+//   * sixteen warps work on scores, four threads a row (a step's exponentials
+//     are many, and short dependent chains need several warps per scheduler to
+//     fill it: with eight warps a step took twice as long).  First sweep: each
+//     keeps (m, l) of one map and one half of every step's keys; second sweep:
+//     each forms the weights of 32 keys of a step from both maps' scores, over
+//     which the weights are written; at the end each holds a quarter of its
+//     row of O.  The four threads swap statistics, and later sums of squares,
+//     through columns of O that are not in use at that moment.
 //   * value rows behind the sequence's end (a page that ends inside a tile)
 //     are zeroed in shared memory before their product: a weight of 0 does not
 //     cancel what is not finite.
@@ -50,13 +52,15 @@ constexpr int kKeys = 128;  // keys per step
 constexpr int kStepBlocks = kKeys / kBlockSize;
 constexpr int kVKeys = 64;  // keys of a V unit
 constexpr int kUnitBlocks = kVKeys / kBlockSize;
-constexpr int kSoftmaxWarps = 8;
-constexpr int kKWarp = 8, kVWarp = 9, kQkWarp = 10, kPvWarp = 11;
-constexpr int kThreads = 12 * 32;
-// Tensor memory: S_1 at 0, S_2 at 128 (fp32 scores of 128 keys; the weights of keys 64 h .. + 63, packed in
-// pairs, over the first 32 columns of their S_1), O at 256 (2 d).
+constexpr int kSoftmaxWarps = 16;
+constexpr int kKWarp = 16, kVWarp = 17, kQkWarp = 18, kPvWarp = 19;
+constexpr int kThreads = 20 * 32;
+// Tensor memory: S_1 at 0, S_2 at 128 (fp32 scores of 128 keys; the weights of keys 32 g .. + 31, packed in
+// pairs, over the first 16 columns of their S_1), O at 256 (2 d).  While a tile has no product in O yet, its
+// columns kColStat + 2 g hold thread g's (m, l); when O is in registers, the first column of each thread's
+// quarter holds its sum of squares (neither place is the other's).
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 256;
+constexpr uint32_t kColO = 256, kColStat = kColO + 8;
 constexpr uint32_t kKHalf = kKeys * 128;   // a 64-column range of a Q or K tile
 constexpr uint32_t kVChunk = kVKeys * 128; // a 64-channel range of a V unit
 constexpr float kBoost = 8.0f;             // log2 of the larger of c1, c2
@@ -85,9 +89,7 @@ struct Layout {
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kK = kQ + 2 * QT;
     static constexpr uint32_t kV = kK + kKStages * KT;
-    static constexpr uint32_t kX = kV + kVStages * VT;   // [2][kRows] float: l of a map, then sums of squares
-    static constexpr uint32_t kXm = kX + 2 * kRows * 4;  // [2][kRows] bf16: m of a map
-    static constexpr uint32_t kBar = kXm + 2 * kRows * 2;
+    static constexpr uint32_t kBar = kV + kVStages * VT;
     // *_RAW: FP8 pools' copies complete there; K_FULL, V_FULL and Q_FULL follow when the rows are f16
     enum { Q_RAW = 0, Q_FULL, Q_FREE, K_RAW, K_FULL = K_RAW + kKStages, K_EMPTY = K_FULL + kKStages,
            V_RAW = K_EMPTY + kKStages, V_FULL = V_RAW + kVStages, V_EMPTY = V_FULL + kVStages,
@@ -96,7 +98,7 @@ struct Layout {
            S2_READ = S_READ + 2,         // map 2: a second-sweep step's scores are in registers
            P_FULL = S2_READ + 1,         // per key half: the weights are in tensor memory
            PV_DONE = P_FULL + 2,         // a second-sweep step's product has run
-           O_FULL = PV_DONE + 1, O_FREE, PAIR, DRAIN = PAIR + 4, NBARS = DRAIN + 2 };
+           O_FULL = PV_DONE + 1, O_FREE, QUAD, DRAIN = QUAD + 4, NBARS = DRAIN + 2 };
     static constexpr uint32_t kTmemSlot = kBar + NBARS * 8;
     static constexpr uint32_t kAbort = kTmemSlot + 4;
     static constexpr uint32_t kEnd = kAbort + 4;
@@ -279,10 +281,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&tm_kv);
         for (int i = 0; i < L::NBARS; ++i) {
             uint32_t n = 1;
-            if (i == L::S_READ || i == L::S_READ + 1 || i == L::P_FULL || i == L::P_FULL + 1) n = 4;
+            if (i == L::S_READ || i == L::S_READ + 1 || i == L::P_FULL || i == L::P_FULL + 1) n = kSoftmaxWarps / 2;
             if (i == L::S2_READ || i == L::O_FREE) n = kSoftmaxWarps;
-            if (i >= L::PAIR && i < L::PAIR + 4) n = 2;         // the two warps of a lane quarter
-            if (i == L::Q_FULL && F8) n = 2;                    // a warp converts each map's queries
+            if (i >= L::QUAD && i < L::QUAD + 4) n = 4;  // the four warps of a lane quarter
+            if (i == L::Q_FULL && F8) n = 2;             // a warp converts each map's queries
             mbar_init(&bar[i], n);
         }
         *abort_flag = 0;
@@ -570,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t vb = base + L::kV + st * L::VT;
 #pragma unroll
                         for (int kk = 0; kk < kVKeys / 16; ++kk)
-                            umma_ts(tmem + kColO, tmem + h * kVKeys + 8 * kk, smem_desc(vb + kk * 2048, kVChunk, 1024),
+                            umma_ts(tmem + kColO, tmem + h * kVKeys + (kk >> 1) * 32 + (kk & 1) * 8, smem_desc(vb + kk * 2048, kVChunk, 1024),
                                     idesc, (s > 0 || h > 0 || kk > 0) ? 1u : 0u);
                         umma_commit(&bar[L::V_EMPTY + st]);
                         if (h == 1) umma_commit(&bar[L::PV_DONE]);
@@ -586,21 +588,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) set_abort();
     } else {
         // ---------------------------------------------------------- statistics, weights, norm
-        // m: this warp's map (first sweep), key half (second sweep) and value head (the end)
-        const int m = warp >> 2, quarter = warp & 3;
+        const int quarter = warp & 3, grp = warp >> 2;  // TMEM lanes 32 quarter ..; which of the row's four threads
+        const int m = grp & 1, half = grp >> 1;         // first sweep: map, half of a step's keys
+        constexpr int QD = D / 2;                       // a thread's channels of the row (of value head grp / 2)
         const int row = quarter * 32 + lane;
-        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-        const uint32_t ts = tmem + lane_off;
-        const uint32_t to = tmem + lane_off + kColO + m * D;   // value head m's half of O
-        uint64_t *pair = &bar[L::PAIR + quarter];
-        float *xs = reinterpret_cast<float *>(sm + L::kX);
-        uint16_t *xm = reinterpret_cast<uint16_t *>(sm + L::kXm);
+        const uint32_t ts = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t to = ts + kColO + grp * QD;
+        uint64_t *quad = &bar[L::QUAD + quarter];
         const float lam = diff_lambda<D>(a.w, lane);
         const float abs_lam = fabsf(lam);
         const float sign = lam < 0.0f ? 1.0f : -1.0f;  // of the second map's weights
         const bool rising = a.qscale >= 0.0f;          // the largest score has the largest q . k (else the smallest)
-        int gs = 0, n = 0, pph = 0;  // steps of both sweeps, tiles, phases of the pair barrier
+        int gs = 0, n = 0, qph = 0;  // steps of both sweeps, tiles, phases of the quad barrier
         bool ok = true;
+        // every warp of the quarter is here (and what it wrote to tensor memory is visible)
+        auto meet = [&]() -> bool {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(quad);
+            const bool done = wait_all(quad, qph & 1);
+            ++qph;
+            tc_fence_after();
+            return done;
+        };
         for (int x = blockIdx.x; ok; x += gridDim.x) {
             Tile t;
             if (!find_tile<G>(wk, a, x, t, lane)) break;
@@ -621,59 +631,56 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto mask_of = [&](int id) -> uint32_t {
                 return __ballot_sync(kFull, lane < kStepBlocks && id >= 0 && id < a.num_blocks);
             };
-            // ---- first sweep: maximum and sum of map m's row ----
+            // ---- first sweep: maximum and sum of map m over this half's keys ----
             float mx = -INFINITY, l = 0.0f;
             int nxt = ids_of(0);
             for (int s = 0; s < t.n_steps; ++s, ++gs) {
-                const uint32_t mask = mask_of(nxt);
+                const uint32_t mask = mask_of(nxt) >> (4 * half);
                 if (s + 1 < t.n_steps) nxt = ids_of(s + 1);
                 if (!(ok = wait_all(&bar[L::S_FULL + m], gs & 1))) break;
                 tc_fence_after();
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t sr[64];
-                    tmem_ld32(ts + m * kKeys + 64 * h, sr);
-                    tmem_ld32(ts + m * kKeys + 64 * h + 32, sr + 32);
+                for (int c = 0; c < 2; ++c) {  // 32 keys at a time
+                    uint32_t sr[32];
+                    tmem_ld32(ts + m * kKeys + 64 * half + 32 * c, sr);
                     tmem_wait_ld();
-                    if (h == 1) {
+                    if (c == 1) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bar[L::S_READ + m]);
                     }
-                    const int key0 = s * kKeys + 64 * h;
-                    const uint32_t mh = (mask >> (4 * h)) & 15u;
-                    if (!(mh == 15u && key0 + 63 <= pos)) {  // what this row does not see never has the largest score
+                    const int key0 = s * kKeys + 64 * half + 32 * c;
+                    const uint32_t mh = (mask >> (2 * c)) & 3u;
+                    if (!(mh == 3u && key0 + 31 <= pos)) {  // what this row does not see never has the largest score
                         const uint32_t never = rising ? 0xff800000u : 0x7f800000u;
 #pragma unroll
-                        for (int k = 0; k < 64; ++k)
+                        for (int k = 0; k < 32; ++k)
                             if (!(((mh >> (k / kBlockSize)) & 1u) && key0 + k <= pos)) sr[k] = never;
                     }
-                    float mc[8];
+                    auto e = [&](int q) { return __uint_as_float(sr[q]); };
+                    float mc[4];
                     if (rising) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            auto e = [&](int q) { return __uint_as_float(sr[j + 8 * q]); };
-                            mc[j] = fmaxf(fmax3(fmax3(fmax3(e(0), e(1), e(2)), e(3), e(4)), e(5), e(6)), e(7));
-                        }
-                        mc[0] = fmax3(fmax3(mc[0], mc[1], mc[2]), fmax3(mc[3], mc[4], mc[5]), fmaxf(mc[6], mc[7]));
+                        for (int j = 0; j < 4; ++j)
+                            mc[j] = fmaxf(fmax3(fmax3(fmax3(e(j), e(j + 4), e(j + 8)), e(j + 12), e(j + 16)), e(j + 20), e(j + 24)),
+                                          e(j + 28));
+                        mc[0] = fmaxf(fmax3(mc[0], mc[1], mc[2]), mc[3]);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            mc[j] = __uint_as_float(sr[j]);
+                        for (int j = 0; j < 4; ++j) {
+                            mc[j] = e(j);
 #pragma unroll
-                            for (int q = 1; q < 8; ++q) mc[j] = fminf(mc[j], __uint_as_float(sr[j + 8 * q]));
+                            for (int q = 1; q < 8; ++q) mc[j] = fminf(mc[j], e(j + 4 * q));
                         }
-#pragma unroll
-                        for (int j = 1; j < 8; ++j) mc[0] = fminf(mc[0], mc[j]);
+                        mc[0] = fminf(fminf(mc[0], mc[1]), fminf(mc[2], mc[3]));
                     }
                     const bool none = mc[0] == (rising ? -INFINITY : INFINITY);
                     const float mn = none ? mx : fmaxf(mx, mc[0] * qs);
                     const float neg = mn == -INFINITY ? 0.0f : -mn;
                     float2 sum[4] = {};
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float2 d = ffma2(make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])),
-                                               make_float2(qs, qs), make_float2(neg, neg));
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 d = ffma2(make_float2(e(2 * i), e(2 * i + 1)), make_float2(qs, qs), make_float2(neg, neg));
                         sum[i & 3] = fadd2(sum[i & 3], make_float2(ex2(d.x), ex2(d.y)));
                     }
                     const float2 q0 = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
@@ -682,126 +689,114 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!ok) break;
-            // ---- both maps' statistics give the weights' factors ----
-            if (n > 0) {  // the partner has read the last tile's sums of squares
-                if (!(ok = wait_all(pair, pph & 1))) break;
-                ++pph;
+            // ---- the row's statistics of both maps give the weights' factors ----
+            float l1, l2, n0 = 0.0f, n1 = 0.0f, inv = 0.0f;  // weights 2^(s qs + n); o = inv * accumulator
+            {
+                uint32_t st[8] = {__float_as_uint(mx), __float_as_uint(l)};
+                tmem_st2(ts + kColStat + 2 * grp, st);
+                tmem_wait_st();
+                if (!(ok = meet())) break;
+                tmem_ld8(ts + kColStat, st);  // (m, l) of threads 0 .. 3: map 1, map 2, map 1, map 2
+                tmem_wait_ld();
+                auto f = [&](int i) { return __uint_as_float(st[i]); };
+                const float m1 = fmaxf(f(0), f(4)), m2 = fmaxf(f(2), f(6));
+                auto part = [&](int i, float top) { return f(i) == -INFINITY ? f(i + 1) : f(i + 1) * ex2(f(i) - top); };
+                l1 = part(0, m1) + part(4, m1);
+                l2 = part(2, m2) + part(6, m2);
+                if (!(l1 == 0.0f)) {  // (a row none of whose blocks could be read stays all zero)
+                    const float c = abs_lam * l1 / l2;  // c2 / c1
+                    n0 = log2f(c <= 1.0f ? 1.0f : 1.0f / c) + kBoost - m1;
+                    n1 = log2f(c <= 1.0f ? c : 1.0f) + kBoost - m2;
+                    inv = (c <= 1.0f ? 1.0f / l1 : abs_lam / l2) * (1.0f / 256.0f);
+                }
             }
-            const __nv_bfloat16 mb = __float2bfloat16_ru(mx);  // the reference both threads use: l is put against it
-            xm[m * kRows + row] = __bfloat16_as_ushort(mb);
-            xs[m * kRows + row] = mx == -INFINITY ? l : l * ex2(mx - __bfloat162float(mb));
-            __syncwarp();
-            if (lane == 0) mbar_arrive(pair);
-            if (!(ok = wait_all(pair, pph & 1))) break;
-            ++pph;
-            const float l1 = xs[row], l2 = xs[kRows + row];
-            float n0 = 0.0f, n1 = 0.0f, inv = 0.0f;  // weights 2^(s qs + n); o = inv * accumulator
-            if (!(l1 == 0.0f)) {  // (a row none of whose blocks could be read stays all zero)
-                const float f = abs_lam * l1 / l2;  // c2 / c1
-                n0 = log2f(f <= 1.0f ? 1.0f : 1.0f / f) + kBoost - __bfloat162float(__ushort_as_bfloat16(xm[row]));
-                n1 = log2f(f <= 1.0f ? f : 1.0f) + kBoost - __bfloat162float(__ushort_as_bfloat16(xm[kRows + row]));
-                inv = (f <= 1.0f ? 1.0f / l1 : abs_lam / l2) * (1.0f / 256.0f);
-            }
-            // ---- second sweep: the weights of keys 64 m .. + 63 of every step ----
+            // ---- second sweep: the weights of keys 32 grp .. + 31 of every step ----
             nxt = ids_of(0);
             for (int s = 0; s < t.n_steps; ++s, ++gs) {
-                const uint32_t mask = mask_of(nxt);
+                const uint32_t mh = (mask_of(nxt) >> (2 * grp)) & 3u;
                 if (s + 1 < t.n_steps) nxt = ids_of(s + 1);
-                const int key0 = s * kKeys + 64 * m;
-                const uint32_t mh = (mask >> (4 * m)) & 15u;
-                const bool all = mh == 15u && key0 + 63 <= pos;
+                const int key0 = s * kKeys + 32 * grp;
+                const bool all = mh == 3u && key0 + 31 <= pos;
                 if (!(ok = wait_all(&bar[L::S_FULL + 1], gs & 1))) break;
                 if (!(ok = wait_all(&bar[L::S_FULL], gs & 1))) break;
                 tc_fence_after();
-                uint32_t pk[32];
+                uint32_t s0[32], s1[32];
+                tmem_ld32(ts + kKeys + 32 * grp, s1);
+                tmem_ld32(ts + 32 * grp, s0);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[L::S2_READ]);
+                uint32_t pk[16];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {  // 32 keys at a time
-                    uint32_t s0[32], s1[32];
-                    tmem_ld32(ts + 64 * m + 32 * h, s0);
-                    tmem_ld32(ts + kKeys + 64 * m + 32 * h, s1);
-                    tmem_wait_ld();
-                    if (h == 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar[L::S2_READ]);
+                for (int i = 0; i < 16; ++i) {
+                    const float2 u0 = ffma2(make_float2(__uint_as_float(s0[2 * i]), __uint_as_float(s0[2 * i + 1])),
+                                            make_float2(qs0, qs0), make_float2(n0, n0));
+                    const float2 u1 = ffma2(make_float2(__uint_as_float(s1[2 * i]), __uint_as_float(s1[2 * i + 1])),
+                                            make_float2(qs1, qs1), make_float2(n1, n1));
+                    float2 w = ffma2(make_float2(ex2(u1.x), ex2(u1.y)), make_float2(sign, sign),
+                                     make_float2(ex2(u0.x), ex2(u0.y)));
+                    if (!all) {
+                        const bool seen = (mh >> (2 * i / kBlockSize)) & 1u;
+                        if (!(seen && key0 + 2 * i <= pos)) w.x = 0.0f;
+                        if (!(seen && key0 + 2 * i + 1 <= pos)) w.y = 0.0f;
                     }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float2 u0 = ffma2(make_float2(__uint_as_float(s0[2 * i]), __uint_as_float(s0[2 * i + 1])),
-                                                make_float2(qs0, qs0), make_float2(n0, n0));
-                        const float2 u1 = ffma2(make_float2(__uint_as_float(s1[2 * i]), __uint_as_float(s1[2 * i + 1])),
-                                                make_float2(qs1, qs1), make_float2(n1, n1));
-                        float2 w = ffma2(make_float2(ex2(u1.x), ex2(u1.y)), make_float2(sign, sign),
-                                         make_float2(ex2(u0.x), ex2(u0.y)));
-                        if (!all) {
-                            const int k = 32 * h + 2 * i;
-                            const bool seen = (mh >> (k / kBlockSize)) & 1u;
-                            if (!(seen && key0 + k <= pos)) w.x = 0.0f;
-                            if (!(seen && key0 + k + 1 <= pos)) w.y = 0.0f;
-                        }
-                        pk[16 * h + i] = F8 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
-                    }
+                    pk[i] = F8 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
                 }
-                tmem_st32(ts + 64 * m, pk);  // over this warp's own scores of map 1, which are read
+                tmem_st16(ts + 32 * grp, pk);  // over this warp's own scores of map 1, which are read
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[L::P_FULL + m]);
+                if (lane == 0) mbar_arrive(&bar[L::P_FULL + half]);
             }
             if (!ok) break;
-            // ---- norm and store: this thread's row, value head m's half ----
+            // ---- norm and store: this thread's quarter of its row ----
             if (!(ok = wait_all(&bar[L::O_FULL], n & 1))) break;
             tc_fence_after();
-            const float f = inv * (F8 ? a.scales[a.n_kv + 2 * t.p + m] : 1.0f);
-            float ss = 0.0f;
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(to + c, o);
-                tmem_wait_ld();
+            const float f = inv * (F8 ? a.scales[a.n_kv + 2 * t.p + half] : 1.0f);
+            uint32_t o[QD];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float v = __uint_as_float(o[i]) * f;
-                    ss = fmaf(v, v, ss);
-                }
+            for (int c = 0; c < QD; c += 32) tmem_ld32(to + c, o + c);
+            tmem_wait_ld();
+            float2 sq[2] = {};
+#pragma unroll
+            for (int i = 0; i < QD / 2; ++i) {
+                const float2 v = make_float2(__uint_as_float(o[2 * i]) * f, __uint_as_float(o[2 * i + 1]) * f);
+                o[2 * i] = __float_as_uint(v.x);
+                o[2 * i + 1] = __float_as_uint(v.y);
+                sq[i & 1] = ffma2(v, v, sq[i & 1]);
             }
-            xs[m * kRows + row] = ss;  // the partner took l before it formed the weights behind this O
-            __syncwarp();
-            if (lane == 0) mbar_arrive(pair);
-            if (!(ok = wait_all(pair, pph & 1))) break;
-            ++pph;
-            const float tot = xs[row] + xs[kRows + row];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(pair);  // read: waited for before the next tile's l
-            const float rn = f * a.w.out_scale * rsqrtf(tot * (1.0f / (2 * D)) + a.w.eps);
-            const bool live = r < t.R;
-            const int64_t tok = (int64_t)t.row0 + r / G;
-            __nv_bfloat16 *dst = a.out + ((tok * (a.n_q / 2) + t.p * G + r % G) * 2 + m) * D;
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(to + c, o);
+            float ss = (sq[0].x + sq[0].y) + (sq[1].x + sq[1].y);
+            {
+                uint32_t z = __float_as_uint(ss);
+                tmem_st1(to, z);  // this thread's part of O is in registers
+                tmem_wait_st();
+                if (!(ok = meet())) break;
+                uint32_t y[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) tmem_ld1(ts + kColO + g * QD, y[g]);
                 tmem_wait_ld();
-                uint32_t w[16];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float4 g = make_float4(1.f, 1.f, 1.f, 1.f);
-                    if (a.w.norm_weight) {
-                        const float *nw = a.w.norm_weight + m * D + c + 4 * i;
-                        g = make_float4(nw[0], nw[1], nw[2], nw[3]);
-                    }
-                    w[2 * i] = pack_bf16x2(__uint_as_float(o[4 * i]) * rn * g.x, __uint_as_float(o[4 * i + 1]) * rn * g.y);
-                    w[2 * i + 1] = pack_bf16x2(__uint_as_float(o[4 * i + 2]) * rn * g.z, __uint_as_float(o[4 * i + 3]) * rn * g.w);
-                }
-                if (live) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<uint4 *>(dst + c + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-                }
+                ss = (__uint_as_float(y[0]) + __uint_as_float(y[1])) + (__uint_as_float(y[2]) + __uint_as_float(y[3]));
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[L::O_FREE]);
+            const float rn = a.w.out_scale * rsqrtf(ss * (1.0f / (2 * D)) + a.w.eps);
+            if (r < t.R) {
+                const int64_t tok = (int64_t)t.row0 + r / G;
+                __nv_bfloat16 *dst = a.out + (tok * (a.n_q / 2) + t.p * G + r % G) * (2 * D) + grp * QD;
+                const float *nw = a.w.norm_weight ? a.w.norm_weight + grp * QD : nullptr;
+#pragma unroll
+                for (int c = 0; c < QD; c += 8) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float g0 = nw ? nw[c + 2 * i] : 1.0f, g1 = nw ? nw[c + 2 * i + 1] : 1.0f;
+                        w[i] = pack_bf16x2(__uint_as_float(o[c + 2 * i]) * rn * g0, __uint_as_float(o[c + 2 * i + 1]) * rn * g1);
+                    }
+                    *reinterpret_cast<uint4 *>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
             ++n;
         }
         if (!ok) set_abort();
