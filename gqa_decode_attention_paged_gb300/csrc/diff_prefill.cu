@@ -20,10 +20,19 @@
 // Design (one persistent CTA per SM, warp-specialised, as prefill.cu):
 //   * a tile is 128 query rows (token, head) of one (sequence, pair): both
 //     maps' queries.  A step is 128 keys.
-//   * warp 16 streams Q and the K_m tiles (one unit each; the second sweep
-//     takes map 2 first, whose scores are free sooner), warp 17 the V tiles
-//     (second sweep; units of 64 keys x 2 d channels), warp 18 issues
-//     S_m = Q_m K_m^T, warp 19 O += W V.
+//   * warp 16 streams Q and, through one ring, what the MMAs take in the order
+//     they take it: K_m units (128 keys of one map) and, in the second sweep, V
+//     units (64 keys x 2 d channels).  One ring for both: in the first sweep
+//     all of it holds keys.  Warp 17 issues every MMA, as one warp from uniform
+//     registers (from inside a lane's branch an MMA took 80 cycles to issue,
+//     640 a unit, and that bound the kernel).
+//     The first sweep alternates between the maps' scores.  In the second one
+//     the halves of a step (64 keys) are half a step apart: the issue order is
+//     W V of the first half, S_2 of the next step, S_1 of its first half, W V
+//     of the second half, S_1 of the next step's second half, so that one
+//     half's weights are formed while the tensor cores work for the other,
+//     although scores and weights have one place each.  Warps 18 and 19 prepare units: FP8 ones are
+//     widened to f16, and value rows behind the sequence's end are zeroed.
 //   * sixteen warps work on scores, four threads a row (a step's exponentials
 //     are many, and short dependent chains need several warps per scheduler to
 //     fill it: with eight warps a step took twice as long).  First sweep: each
@@ -53,7 +62,7 @@ constexpr int kStepBlocks = kKeys / kBlockSize;
 constexpr int kVKeys = 64;  // keys of a V unit
 constexpr int kUnitBlocks = kVKeys / kBlockSize;
 constexpr int kSoftmaxWarps = 16;
-constexpr int kKWarp = 16, kVWarp = 17, kQkWarp = 18, kPvWarp = 19;
+constexpr int kCopyWarp = 16, kMmaWarp = 17, kPrepWarp = 18;  // kPrepWarp and the next
 constexpr int kThreads = 20 * 32;
 // Tensor memory: S_1 at 0, S_2 at 128 (fp32 scores of 128 keys; the weights of keys 32 g .. + 31, packed in
 // pairs, over the first 16 columns of their S_1), O at 256 (2 d).  While a tile has no product in O yet, its
@@ -82,23 +91,22 @@ struct Args {
 
 template <int D>
 struct Layout {
-    static constexpr uint32_t QT = kRows * D * 2;       // one map's queries
-    static constexpr uint32_t KT = kKeys * D * 2;       // one K unit
-    static constexpr uint32_t VT = kVKeys * 2 * D * 2;  // one V unit
-    static constexpr int kKStages = D == 128 ? 2 : 4, kVStages = D == 128 ? 3 : 6;
+    static constexpr uint32_t QT = kRows * D * 2;  // one map's queries
+    static constexpr uint32_t UT = kKeys * D * 2;  // a unit: 128 keys x d, or 64 keys x 2 d values
+    static constexpr int kStages = D == 128 ? 5 : 10;
     static constexpr uint32_t kQ = 0;
-    static constexpr uint32_t kK = kQ + 2 * QT;
-    static constexpr uint32_t kV = kK + kKStages * KT;
-    static constexpr uint32_t kBar = kV + kVStages * VT;
-    // *_RAW: FP8 pools' copies complete there; K_FULL, V_FULL and Q_FULL follow when the rows are f16
-    enum { Q_RAW = 0, Q_FULL, Q_FREE, K_RAW, K_FULL = K_RAW + kKStages, K_EMPTY = K_FULL + kKStages,
-           V_RAW = K_EMPTY + kKStages, V_FULL = V_RAW + kVStages, V_EMPTY = V_FULL + kVStages,
-           S_FULL = V_EMPTY + kVStages,  // per map
-           S_READ = S_FULL + 2,          // per map: a first-sweep step's scores are in registers
-           S2_READ = S_READ + 2,         // map 2: a second-sweep step's scores are in registers
-           P_FULL = S2_READ + 1,         // per key half: the weights are in tensor memory
-           PV_DONE = P_FULL + 2,         // a second-sweep step's product has run
-           O_FULL = PV_DONE + 1, O_FREE, QUAD, DRAIN = QUAD + 4, NBARS = DRAIN + 2 };
+    static constexpr uint32_t kRing = kQ + 2 * QT;
+    static constexpr uint32_t kBar = kRing + kStages * UT;
+    // RAW, Q_RAW: FP8 pools' copies complete there; FULL and Q_FULL follow when the rows are f16
+    enum { Q_RAW = 0, Q_FULL, Q_FREE, RAW, FULL = RAW + kStages, EMPTY = FULL + kStages,
+           ST_FULL = EMPTY + kStages,    // first sweep, per map: scores of a step
+           ST_READ = ST_FULL + 2,        // they are in registers
+           S2_FULL = ST_READ + 2,        // second sweep: map 2's scores of a step
+           S1_FULL = S2_FULL + 1,        // map 1's, per half of the step
+           S2_READ = S1_FULL + 2,        // map 2's are in registers
+           P_FULL = S2_READ + 1,         // per half: the weights are in tensor memory
+           PV_DONE = P_FULL + 2,         // per half: their product has run
+           O_FULL = PV_DONE + 2, O_FREE, END_CLEAR, QUAD, DRAIN = QUAD + 4, NBARS };
     static constexpr uint32_t kTmemSlot = kBar + NBARS * 8;
     static constexpr uint32_t kAbort = kTmemSlot + 4;
     static constexpr uint32_t kEnd = kAbort + 4;
@@ -151,12 +159,13 @@ __device__ __forceinline__ void convert_f16(uint32_t tile, int lane, int row0, i
     }
 }
 
-// One map's queries (bf16, as the copy left them) -> f16 in place, element by element.
+// The tile's queries (bf16, as the copies left them) -> f16 in place, element by element: this warp's share.
 template <int D>
-__device__ __forceinline__ void convert_q(uint32_t base, int lane)
+__device__ __forceinline__ void convert_q(uint32_t base, int warp, int lane)
 {
+    constexpr uint32_t share = 2 * Layout<D>::QT / kSoftmaxWarps;
 #pragma unroll 4
-    for (uint32_t off = 16u * lane; off < Layout<D>::QT; off += 16u * 32) {
+    for (uint32_t off = warp * share + 16u * lane; off < (warp + 1) * share; off += 16u * 32) {
         uint4 v = lds128(base + off);
         uint32_t *w = reinterpret_cast<uint32_t *>(&v);
 #pragma unroll
@@ -259,6 +268,12 @@ __device__ __forceinline__ bool find_tile(Walker &w, const Args &a, int x, Tile 
     return true;
 }
 
+// The V unit (of the tile's 2 n_steps) in which the sequence ends inside a block, or -1.
+__device__ __forceinline__ int end_unit(const Tile &t)
+{
+    return t.C % kBlockSize && t.C / kBlockSize < t.n_blocks ? t.C / kBlockSize / kUnitBlocks : -1;
+}
+
 // ------------------------------------------------------------- the kernel
 
 template <int D, int G, bool F8>
@@ -268,29 +283,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 {
     using L = Layout<D>;
     constexpr int NH = D / 64;  // 64-column ranges of a row
-    constexpr int KS = L::kKStages, VS = L::kVStages;
-    constexpr bool kSplitK = F8 && D == 128;  // the K rows' conversion is shared by the K and the Q K^T warp
+    constexpr int NS = L::kStages;
+    // FP8 pools: at d_head 128 the two preparing warps take half of every unit, at 64 (where a K unit's
+    // rows overlap in place) every other unit; NS is even there, so a warp sees every phase of its slots
+    constexpr bool kSplit = F8 && D == 128;
+    static_assert(!F8 || kSplit || NS % 2 == 0, "a preparing warp would miss phases of its slots");
     extern __shared__ __align__(1024) uint8_t dp_smem[];
     uint8_t *sm = dp_smem + ((1024u - (smem_u32(dp_smem) & 1023u)) & 1023u);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::kBar);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::kAbort);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(kFull, tid >> 5, 0);  // the same in all lanes, and known to be
 
     if (tid == 0) {
         prefetch_tensormap(&tm_q);
         prefetch_tensormap(&tm_kv);
         for (int i = 0; i < L::NBARS; ++i) {
             uint32_t n = 1;
-            if (i == L::S_READ || i == L::S_READ + 1 || i == L::P_FULL || i == L::P_FULL + 1) n = kSoftmaxWarps / 2;
+            if (i == L::ST_READ || i == L::ST_READ + 1 || i == L::P_FULL || i == L::P_FULL + 1) n = kSoftmaxWarps / 2;
             if (i == L::S2_READ || i == L::O_FREE) n = kSoftmaxWarps;
             if (i >= L::QUAD && i < L::QUAD + 4) n = 4;  // the four warps of a lane quarter
-            if (i == L::Q_FULL && F8) n = 2;             // a warp converts each map's queries
+            if (i == L::Q_FULL && F8) n = kSoftmaxWarps;  // each widens its share of the queries
+            if (i >= L::FULL && i < L::EMPTY && kSplit) n = 2;
             mbar_init(&bar[i], n);
         }
         *abort_flag = 0;
         fence_mbarrier_init();
     }
-    if (warp == kQkWarp) {
+    if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(sm + L::kTmemSlot)),
                      "r"(kTmemCols)
@@ -314,31 +334,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     load_window<G>(wk, a, lane);
     const uint32_t base = smem_u32(sm);
 
-    if (warp == kKWarp) {
-        // ---------------------------------------------------------- Q and K copies
+    if (warp == kCopyWarp) {
+        // ---------------------------------------------------------- copies
         const uint64_t policy = l2_policy_evict_normal();
-        int u = 0, n = 0;  // units, tiles
-        int issued = 0;    // units whose copies were issued
-        int pend = -1;     // FP8: the unit awaiting conversion
-        bool pend_q = false;
+        int u = 0, n = 0;  // units issued, tiles
         bool ok = true;
-        [[maybe_unused]] auto convert_pending = [&]() -> bool {
-            if (pend_q) {
-                if (!wait_all(&bar[L::Q_RAW], (n - 1) & 1)) return false;
-                convert_q<D>(base + L::kQ, lane);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[L::Q_FULL]);
-                pend_q = false;
-            }
-            if (pend < 0) return true;
-            const int st = pend % KS;
-            if (!wait_all(&bar[L::K_RAW + st], (pend / KS) & 1)) return false;
-            convert_f16<D, kKeys>(base + L::kK + st * L::KT, lane, 0, kSplitK ? kKeys / 2 : kKeys);
-            fence_proxy_async_smem();
+        // the next unit: its slot is free, lane 0 announces the bytes
+        auto open = [&](uint64_t *&land, uint8_t *&dst) -> bool {
+            const int st = u % NS, use = u / NS;
+            if (use > 0 && !wait_all(&bar[L::EMPTY + st], (use - 1) & 1)) return false;
+            land = &bar[(F8 ? L::RAW : L::FULL) + st];
+            dst = sm + L::kRing + st * L::UT;
+            if (lane == 0) mbar_arrive_expect_tx(land, F8 ? L::UT / 2 : L::UT);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[L::K_FULL + st]);
-            pend = -1;
+            ++u;
             return true;
         };
         for (int x = blockIdx.x; ok; x += gridDim.x) {
@@ -346,9 +355,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!find_tile<G>(wk, a, x, t, lane)) break;
             if (t.n_steps == 0) continue;
             if (*abort_flag) break;
-            if constexpr (F8) {  // the last unit of the tile before
-                if (!(ok = convert_pending())) break;
-            }
             if (n > 0 && !(ok = wait_all(&bar[L::Q_FREE], (n - 1) & 1))) break;
             if (lane == 0) {
                 uint64_t *qb = &bar[F8 ? L::Q_RAW : L::Q_FULL];
@@ -361,230 +367,237 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     qb, policy);
             }
             ++n;
-            pend_q = F8;
             const int32_t *trow = a.block_tables + (int64_t)t.b * a.W;
-            for (int sweep = 0; sweep < 2 && ok; ++sweep) {
-                int nxt = lane < kStepBlocks && lane < t.n_blocks ? trow[lane] : -1;
-                for (int s = 0; s < t.n_steps && ok; ++s) {
-                    const int cur = nxt;
-                    const int nb = (s + 1) * kStepBlocks + lane;
-                    if (s + 1 < t.n_steps) nxt = lane < kStepBlocks && nb < t.n_blocks ? trow[nb] : -1;
-                    const bool present = lane < kStepBlocks && s * kStepBlocks + lane < t.n_blocks;
-                    const bool valid = present && cur >= 0 && cur < a.num_blocks;
-                    if (present && !valid && sweep == 0) atomicOr(a.err, PKV_DEVERR_BLOCK_RANGE);
-                    for (int i = 0; i < 2; ++i, ++u) {
-                        const int m = i ^ sweep;  // the second sweep takes map 2 first
-                        const int st = u % KS, use = u / KS;
-                        if (use > 0 && !(ok = wait_all(&bar[L::K_EMPTY + st], (use - 1) & 1))) break;
-                        uint64_t *kb = &bar[(F8 ? L::K_RAW : L::K_FULL) + st];
-                        if (lane == 0) mbar_arrive_expect_tx(kb, F8 ? L::KT / 2 : L::KT);
-                        __syncwarp();
-                        if (lane < kStepBlocks) {
-                            const int y = valid ? (int)((cur * (int64_t)a.n_kv + 2 * t.p + m) * 2 * kBlockSize) : a.oob_row;
-                            uint8_t *dst = sm + L::kK + st * L::KT;
-                            if constexpr (F8) {
-                                tma_load_2d(dst + L::KT / 2 + lane * (kBlockSize * D), &tm_kv, 0, y, kb, policy);
-                            } else {
+            // lane k < 8: the entry rows of block k's pair of step s, or rows past the pool (zero filled)
+            auto rows_of = [&](int s, bool flag) -> int {
+                const int nb = s * kStepBlocks + lane;
+                const bool present = lane < kStepBlocks && nb < t.n_blocks;
+                const int id = present ? trow[nb] : -1;
+                const bool valid = id >= 0 && id < a.num_blocks;
+                if (present && !valid && flag) atomicOr(a.err, PKV_DEVERR_BLOCK_RANGE);
+                return valid ? (int)((id * (int64_t)a.n_kv + 2 * t.p) * 2 * kBlockSize) : a.oob_row;
+            };
+            auto copy_k = [&](int y0, int m) -> bool {
+                uint64_t *land;
+                uint8_t *dst;
+                if (!open(land, dst)) return false;
+                if (lane < kStepBlocks) {
+                    const int y = y0 == a.oob_row ? y0 : y0 + m * 2 * kBlockSize;
+                    if constexpr (F8) {
+                        tma_load_2d(dst + L::UT / 2 + lane * (kBlockSize * D), &tm_kv, 0, y, land, policy);
+                    } else {
 #pragma unroll
-                                for (int h = 0; h < NH; ++h)
-                                    tma_load_2d(dst + h * kKHalf + lane * (kBlockSize * 128), &tm_kv, 64 * h, y, kb, policy);
-                            }
+                        for (int h = 0; h < NH; ++h)
+                            tma_load_2d(dst + h * kKHalf + lane * (kBlockSize * 128), &tm_kv, 64 * h, y, land, policy);
+                    }
+                }
+                return true;
+            };
+            auto copy_v = [&](int y0, int h) -> bool {  // lane: block lane & 3 of the half, value head lane >> 2
+                uint64_t *land;
+                uint8_t *dst;
+                const int k = lane & 3, head = (lane >> 2) & 1;
+                const int yk = __shfl_sync(kFull, y0, h * kUnitBlocks + k);
+                if (!open(land, dst)) return false;
+                if (lane < 8) {
+                    const int y = yk == a.oob_row ? yk : yk + head * 2 * kBlockSize + kBlockSize;
+                    dst += head * NH * kVChunk;
+                    if constexpr (F8) {
+                        tma_load_2d(dst + kVKeys * D + k * (kBlockSize * D), &tm_kv, 0, y, land, policy);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < NH; ++c)
+                            tma_load_2d(dst + c * kVChunk + k * (kBlockSize * 128), &tm_kv, 64 * c, y, land, policy);
+                    }
+                }
+                return true;
+            };
+            int nxt = rows_of(0, true);
+            for (int s = 0; s < t.n_steps && ok; ++s) {
+                const int y0 = nxt;
+                if (s + 1 < t.n_steps) nxt = rows_of(s + 1, true);
+                ok = copy_k(y0, 0) && copy_k(y0, 1);
+            }
+            if (!ok) break;
+            int y0 = rows_of(0, false);
+            ok = copy_k(y0, 1) && copy_k(y0, 0);
+            for (int s = 0; s < t.n_steps && ok; ++s) {  // in the order of the MMAs
+                if (s + 1 < t.n_steps) nxt = rows_of(s + 1, false);
+                ok = copy_v(y0, 0);
+                if (s + 1 < t.n_steps) ok = ok && copy_k(nxt, 1) && copy_k(nxt, 0);
+                ok = ok && copy_v(y0, 1);
+                y0 = nxt;
+            }
+        }
+        // copies still in flight (after an abort) land before the CTA exits
+        for (int i = max(0, u - NS); i < u; ++i)
+            mbar_wait_bounded(&bar[(F8 ? L::RAW : L::FULL) + i % NS], (i / NS) & 1);
+        if (n > 0) mbar_wait_bounded(&bar[F8 ? L::Q_RAW : L::Q_FULL], (n - 1) & 1);
+        if (!ok) set_abort();
+    } else if (warp >= kPrepWarp) {
+        // ---------------------------------------------------------- units made ready
+        const int which = warp - kPrepWarp;
+        if (F8 || which == 0) {
+            int u = 0;
+            bool ok = true;
+            for (int x = blockIdx.x; ok; x += gridDim.x) {
+                Tile t;
+                if (!find_tile<G>(wk, a, x, t, lane)) break;
+                if (t.n_steps == 0) continue;
+                if (*abort_flag) break;
+                const int end = end_unit(t);  // the V unit the sequence ends inside of
+                for (int i = 0; i < 6 * t.n_steps; ++i, ++u) {
+                    const int st = u % NS;
+                    if (F8 && !kSplit && (u & 1) != which) continue;
+                    if (!(ok = wait_all(&bar[(F8 ? L::RAW : L::FULL) + st], (u / NS) & 1))) break;
+                    // second sweep: K, K of the first step, then of each step V, K, K (the next step's, if
+                    // there is one), V
+                    const int iv = i - 2 * t.n_steps - 2;
+                    const int vs = iv >> 2, vp = iv & 3;
+                    const bool is_v = iv >= 0 && (vp == 0 || vp == 3 || (vp == 1 && vs == t.n_steps - 1));
+                    const uint32_t unit = base + L::kRing + st * L::UT;
+                    if constexpr (F8) {
+                        if (is_v) {
+                            if (!kSplit || which == 0) convert_f16<D, kVKeys>(unit, lane, 0, kVKeys);
+                            if (!kSplit || which == 1) convert_f16<D, kVKeys>(unit + NH * kVChunk, lane, 0, kVKeys);
+                        } else {
+                            convert_f16<D, kKeys>(unit, lane, kSplit ? which * (kKeys / 2) : 0, kSplit ? kKeys / 2 : kKeys);
                         }
-                        issued = u + 1;
-                        if constexpr (F8) {
-                            if (!(ok = convert_pending())) break;
-                            pend = u;
+                    }
+                    const bool ends = is_v && 2 * vs + (vp != 0) == end;
+                    if (ends) {  // this warp's value heads: rows behind the end
+                        const int heads = kSplit ? 1 : 2, h0 = kSplit ? which : 0;
+                        const int r0 = (t.C / kBlockSize % kUnitBlocks) * kBlockSize;
+                        const int first = r0 + t.C % kBlockSize, rows = r0 + kBlockSize - first;
+                        for (int e = lane; e < rows * 8 * heads * NH; e += 32) {
+                            const int row = first + (e >> 3) % rows, ch = h0 * NH + (e >> 3) / rows;
+                            sts128(unit + ch * kVChunk + row * 128 + (e & 7) * 16, make_uint4(0, 0, 0, 0));
                         }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (F8) mbar_arrive(&bar[L::FULL + st]);
+                        else if (ends) mbar_arrive(&bar[L::END_CLEAR]);
                     }
                 }
             }
+            if (!ok) set_abort();
         }
-        if constexpr (F8) {
-            if (ok && !*abort_flag) ok = convert_pending();
-        }
-        // copies still in flight (after an abort) land before the CTA exits
-        for (int i = max(0, issued - KS); i < issued; ++i)
-            mbar_wait_bounded(&bar[(F8 ? L::K_RAW : L::K_FULL) + i % KS], (i / KS) & 1);
-        if (n > 0) mbar_wait_bounded(&bar[F8 ? L::Q_RAW : L::Q_FULL], (n - 1) & 1);
-        if (!ok) set_abort();
-    } else if (warp == kVWarp) {
-        // ---------------------------------------------------------- V copies
-        const uint64_t policy = l2_policy_evict_normal();
-        int u = 0, n = 0, issued = 0, pend = -1;
+    } else if (warp == kMmaWarp) {
+        // ---------------------------------------------------------- S_m = Q_m K_m^T and O += W V
+        constexpr uint32_t idesc_qk = mma_idesc(kRows, kKeys, 0, F8), idesc_half = mma_idesc(kRows, 64, 0, F8);
+        constexpr uint32_t idesc_pv = mma_idesc(kRows, 2 * D, 1, F8);
+        const uint64_t qd = smem_desc(base + L::kQ, 16, 1024), kd = smem_desc(base + L::kRing, 16, 1024);
+        const uint64_t vd = smem_desc(base + L::kRing, kVChunk, 1024);
+        int u = 0, n = 0;               // the ring's next unit, tiles
+        int reads = 0, steps = 0, ends = 0;  // first- and second-sweep steps, sequence ends
         bool ok = true;
-        [[maybe_unused]] auto convert_pending = [&]() -> bool {  // value head 0's rows
-            if (pend < 0) return true;
-            const int st = pend % VS;
-            if (!wait_all(&bar[L::V_RAW + st], (pend / VS) & 1)) return false;
-            convert_f16<D, kVKeys>(base + L::kV + st * L::VT, lane, 0, kVKeys);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[L::V_FULL + st]);
-            pend = -1;
-            return true;
+        const uint32_t go = elect_one();
+        const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+        auto unit = [&](int v) -> bool { return wait_all(&bar[L::FULL + v % NS], (v / NS) & 1); };
+        // keys [64 part, 64 part + N) of ring unit v against map m's queries
+        auto scores = [&](int m, int v, int part, uint32_t idesc) {
+            tc_fence_after();
+            const uint64_t qm = qd + ((m * L::QT) >> 4), km = kd + ((v % NS * L::UT + part * 64 * 128) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * kKHalf + (kk & 3) * 32) >> 4;
+                umma_if(go, tm + m * kKeys + part * 64, qm + off, km + off, idesc, kk > 0 ? 1u : 0u);
+            }
         };
         for (int x = blockIdx.x; ok; x += gridDim.x) {
             Tile t;
             if (!find_tile<G>(wk, a, x, t, lane)) break;
             if (t.n_steps == 0) continue;
             if (*abort_flag) break;
-            if constexpr (F8) {
-                if (!(ok = convert_pending())) break;
-                if (!(ok = wait_all(&bar[L::Q_RAW], n & 1))) break;
-                convert_q<D>(base + L::kQ + L::QT, lane);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[L::Q_FULL]);
-            }
-            ++n;
-            const int32_t *trow = a.block_tables + (int64_t)t.b * a.W;
-            // lane: block (lane & 3) of a unit, value head lane >> 2
-            const int k = lane & 3, head = lane >> 2;
-            const int units = 2 * t.n_steps;
-            int nxt = lane < 8 && k < t.n_blocks ? trow[k] : -1;
-            for (int i = 0; i < units && ok; ++i, ++u) {
-                const int cur = nxt;
-                const int nb = (i + 1) * kUnitBlocks + k;
-                if (i + 1 < units) nxt = lane < 8 && nb < t.n_blocks ? trow[nb] : -1;
-                const int st = u % VS, use = u / VS;
-                if (use > 0 && !(ok = wait_all(&bar[L::V_EMPTY + st], (use - 1) & 1))) break;
-                const bool valid = lane < 8 && i * kUnitBlocks + k < t.n_blocks && cur >= 0 && cur < a.num_blocks;
-                uint64_t *vb = &bar[(F8 ? L::V_RAW : L::V_FULL) + st];
-                if (lane == 0) mbar_arrive_expect_tx(vb, F8 ? L::VT / 2 : L::VT);
-                __syncwarp();
-                if (lane < 8) {
-                    const int y = valid ? (int)((cur * (int64_t)a.n_kv + 2 * t.p + head) * 2 * kBlockSize + kBlockSize)
-                                        : a.oob_row;
-                    uint8_t *dst = sm + L::kV + st * L::VT + head * NH * kVChunk;
-                    if constexpr (F8) {
-                        tma_load_2d(dst + kVKeys * D + k * (kBlockSize * D), &tm_kv, 0, y, vb, policy);
+            {
+                const int S = __shfl_sync(kFull, t.n_steps, 0);
+                const int end = end_unit(t);
+                auto first_sweep = [&](int s, int m) -> bool {
+                    // S_m is free: its last scores are in registers, and the weights over S_1 have been used
+                    if (s > 0) {
+                        if (!wait_all(&bar[L::ST_READ + m], (reads - 1) & 1)) return false;
+                    } else if (n > 0) {
+                        if (m == 0 && !(wait_all(&bar[L::PV_DONE], (steps - 1) & 1) &&
+                                        wait_all(&bar[L::PV_DONE + 1], (steps - 1) & 1)))
+                            return false;
+                        if (m == 1 && !wait_all(&bar[L::S2_READ], (steps - 1) & 1)) return false;
+                    }
+                    if (!unit(u)) return false;
+                    scores(m, u, 0, idesc_qk);
+                    umma_commit_if(go, &bar[L::ST_FULL + m]);
+                    umma_commit_if(go, &bar[L::EMPTY + u++ % NS]);
+                    return true;
+                };
+                auto product = [&](int s, int h) -> bool {
+                    const int v = u++;
+                    if (!unit(v)) return false;
+                    if (!F8 && 2 * s + h == end) {
+                        if (!wait_all(&bar[L::END_CLEAR], ends & 1)) return false;
+                        ++ends;
+                    }
+                    if (!wait_all(&bar[L::P_FULL + h], steps & 1)) return false;
+                    tc_fence_after();
+                    const uint64_t vm = vd + ((v % NS * L::UT) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < kVKeys / 16; ++kk)
+                        umma_ts_if(go, tm + kColO, tm + h * kVKeys + (kk >> 1) * 32 + (kk & 1) * 8, vm + ((kk * 2048) >> 4),
+                                idesc_pv, (s > 0 || h > 0 || kk > 0) ? 1u : 0u);
+                    umma_commit_if(go, &bar[L::EMPTY + v % NS]);
+                    umma_commit_if(go, &bar[L::PV_DONE + h]);
+                    return true;
+                };
+                ok = wait_all(&bar[L::Q_FULL], n & 1);
+                for (int s = 0; s < S && ok; ++s, ++reads) ok = first_sweep(s, 0) && first_sweep(s, 1);
+                // second sweep: the first step's scores
+                ok = ok && wait_all(&bar[L::ST_READ + 1], (reads - 1) & 1) && unit(u);
+                if (ok) {
+                    scores(1, u, 0, idesc_qk);
+                    umma_commit_if(go, &bar[L::S2_FULL]);
+                    umma_commit_if(go, &bar[L::EMPTY + u++ % NS]);
+                    ok = wait_all(&bar[L::ST_READ], (reads - 1) & 1) && unit(u);
+                }
+                if (ok) {
+                    scores(0, u, 0, idesc_half);
+                    umma_commit_if(go, &bar[L::S1_FULL]);
+                    scores(0, u, 1, idesc_half);
+                    umma_commit_if(go, &bar[L::S1_FULL + 1]);
+                    umma_commit_if(go, &bar[L::EMPTY + u++ % NS]);
+                    if (n > 0) ok = wait_all(&bar[L::O_FREE], (n - 1) & 1);
+                }
+                for (int s = 0; s < S && ok; ++s, ++steps) {
+                    const bool more = s + 1 < S;
+                    int k1 = 0;  // the next step's K_1 unit
+                    if (!(ok = product(s, 0))) break;
+                    if (more) {
+                        if (!(ok = wait_all(&bar[L::S2_READ], steps & 1) && unit(u))) break;
+                        scores(1, u, 0, idesc_qk);
+                        umma_commit_if(go, &bar[L::S2_FULL]);
+                        umma_commit_if(go, &bar[L::EMPTY + u++ % NS]);
+                        k1 = u++;
+                        if (!(ok = wait_all(&bar[L::PV_DONE], steps & 1) && unit(k1))) break;
+                        scores(0, k1, 0, idesc_half);
+                        umma_commit_if(go, &bar[L::S1_FULL]);
                     } else {
-#pragma unroll
-                        for (int h = 0; h < NH; ++h)
-                            tma_load_2d(dst + h * kVChunk + k * (kBlockSize * 128), &tm_kv, 64 * h, y, vb, policy);
+                        umma_commit_if(go, &bar[L::Q_FREE]);
                     }
-                }
-                issued = u + 1;
-                if constexpr (F8) {
-                    if (!(ok = convert_pending())) break;
-                    pend = u;
+                    if (!(ok = product(s, 1))) break;
+                    if (more) {
+                        if (!(ok = wait_all(&bar[L::PV_DONE + 1], steps & 1))) break;
+                        scores(0, k1, 1, idesc_half);
+                        umma_commit_if(go, &bar[L::S1_FULL + 1]);
+                        umma_commit_if(go, &bar[L::EMPTY + k1 % NS]);
+                    } else {
+                        umma_commit_if(go, &bar[L::O_FULL]);
+                    }
                 }
             }
-        }
-        if constexpr (F8) {
-            if (ok && !*abort_flag) ok = convert_pending();
-        }
-        for (int i = max(0, issued - VS); i < issued; ++i)
-            mbar_wait_bounded(&bar[(F8 ? L::V_RAW : L::V_FULL) + i % VS], (i / VS) & 1);
-        if (!ok) set_abort();
-    } else if (warp == kQkWarp) {
-        // ---------------------------------------------------------- S_m = Q_m K_m^T
-        constexpr uint32_t idesc = mma_idesc(kRows, kKeys, 0, F8);
-        int u = 0, n = 0;                // K units, tiles
-        int reads = 0, prods = 0;        // first- and second-sweep units of each map so far
-        int prev = -1;                   // what the units before these were: 0 first sweep, 1 second
-        bool ok = true;
-        for (int x = blockIdx.x; ok; x += gridDim.x) {
-            Tile t;
-            if (!find_tile<G>(wk, a, x, t, lane)) break;
-            if (t.n_steps == 0) continue;
-            if (*abort_flag) break;
-            if (!(ok = wait_all(&bar[L::Q_FULL], n & 1))) break;
             ++n;
-            for (int sweep = 0; sweep < 2 && ok; ++sweep)
-                for (int s = 0; s < t.n_steps && ok; ++s) {
-                    for (int i = 0; i < 2; ++i, ++u) {
-                        const int m = i ^ sweep;
-                        const int st = u % KS;
-                        if constexpr (kSplitK) {  // this warp's rows of the unit
-                            if (!(ok = wait_all(&bar[L::K_RAW + st], (u / KS) & 1))) break;
-                            convert_f16<D, kKeys>(base + L::kK + st * L::KT, lane, kKeys / 2, kKeys / 2);
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                        }
-                        if (!(ok = wait_all(&bar[L::K_FULL + st], (u / KS) & 1))) break;
-                        // S_m is free: its scores are in registers, or (second sweep, map 1, where the
-                        // weights overwrite them) its product has run
-                        if (prev == 0 && !(ok = wait_all(&bar[L::S_READ + m], (reads - 1) & 1))) break;
-                        if (prev == 1 && !(ok = wait_all(&bar[m == 0 ? L::PV_DONE : L::S2_READ], (prods - 1) & 1))) break;
-                        tc_fence_after();
-                        if (lane == 0) {
-                            const uint32_t qb = base + L::kQ + m * L::QT, kb = base + L::kK + st * L::KT;
-#pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk) {
-                                const uint32_t off = (kk >> 2) * kKHalf + (kk & 3) * 32;
-                                umma(tmem + m * kKeys, smem_desc(qb + off, 16, 1024), smem_desc(kb + off, 16, 1024),
-                                     idesc, kk > 0 ? 1u : 0u);
-                            }
-                            umma_commit(&bar[L::S_FULL + m]);
-                            umma_commit(&bar[L::K_EMPTY + st]);
-                            if (sweep == 1 && s == t.n_steps - 1 && i == 1) umma_commit(&bar[L::Q_FREE]);
-                        }
-                        __syncwarp();
-                    }
-                    prev = sweep;
-                    if (sweep == 0) ++reads;
-                    else ++prods;
-                }
         }
-        if (lane == 0) umma_commit(&bar[L::DRAIN]);
+        umma_commit_if(go, &bar[L::DRAIN]);
         __syncwarp();
         mbar_wait_bounded(&bar[L::DRAIN], 0);
-        if (!ok) set_abort();
-    } else if (warp == kPvWarp) {
-        // ---------------------------------------------------------- O += P_m V
-        constexpr uint32_t idesc = mma_idesc(kRows, 2 * D, 1, F8);
-        int u = 0, n = 0, steps = 0;  // V units, tiles, steps so far
-        bool ok = true;
-        for (int x = blockIdx.x; ok; x += gridDim.x) {
-            Tile t;
-            if (!find_tile<G>(wk, a, x, t, lane)) break;
-            if (t.n_steps == 0) continue;
-            if (*abort_flag) break;
-            if (n > 0 && !(ok = wait_all(&bar[L::O_FREE], (n - 1) & 1))) break;
-            ++n;
-            // the block the sequence ends inside of, where this tile reaches it
-            const int end_blk = (t.C % kBlockSize) && t.C / kBlockSize < t.n_blocks ? t.C / kBlockSize : -1;
-            for (int s = 0; s < t.n_steps && ok; ++s, ++steps) {
-                for (int h = 0; h < 2; ++h, ++u) {
-                    const int st = u % VS;
-                    if constexpr (F8) {  // value head 1's rows
-                        if (!(ok = wait_all(&bar[L::V_RAW + st], (u / VS) & 1))) break;
-                        convert_f16<D, kVKeys>(base + L::kV + st * L::VT + NH * kVChunk, lane, 0, kVKeys);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    if (!(ok = wait_all(&bar[L::V_FULL + st], (u / VS) & 1))) break;
-                    if (end_blk >= 0 && end_blk / kUnitBlocks == 2 * s + h) {
-                        const int r0 = (end_blk % kUnitBlocks) * kBlockSize;
-                        const int first = r0 + t.C % kBlockSize, rows = r0 + kBlockSize - first;
-                        for (int i = lane; i < rows * 8 * 2 * NH; i += 32) {
-                            const int row = first + (i >> 3) % rows, ch = (i >> 3) / rows;
-                            sts128(base + L::kV + st * L::VT + ch * kVChunk + row * 128 + (i & 7) * 16,
-                                   make_uint4(0, 0, 0, 0));
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    if (!(ok = wait_all(&bar[L::P_FULL + h], steps & 1))) break;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t vb = base + L::kV + st * L::VT;
-#pragma unroll
-                        for (int kk = 0; kk < kVKeys / 16; ++kk)
-                            umma_ts(tmem + kColO, tmem + h * kVKeys + (kk >> 1) * 32 + (kk & 1) * 8, smem_desc(vb + kk * 2048, kVChunk, 1024),
-                                    idesc, (s > 0 || h > 0 || kk > 0) ? 1u : 0u);
-                        umma_commit(&bar[L::V_EMPTY + st]);
-                        if (h == 1) umma_commit(&bar[L::PV_DONE]);
-                        if (h == 1 && s == t.n_steps - 1) umma_commit(&bar[L::O_FULL]);
-                    }
-                    __syncwarp();
-                }
-            }
-        }
-        if (lane == 0) umma_commit(&bar[L::DRAIN + 1]);
-        __syncwarp();
-        mbar_wait_bounded(&bar[L::DRAIN + 1], 0);
         if (!ok) set_abort();
     } else {
         // ---------------------------------------------------------- statistics, weights, norm
@@ -599,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float abs_lam = fabsf(lam);
         const float sign = lam < 0.0f ? 1.0f : -1.0f;  // of the second map's weights
         const bool rising = a.qscale >= 0.0f;          // the largest score has the largest q . k (else the smallest)
-        int gs = 0, n = 0, qph = 0;  // steps of both sweeps, tiles, phases of the quad barrier
+        int gs = 0, ps = 0, n = 0, qph = 0;  // first- and second-sweep steps, tiles, phases of the quad barrier
         bool ok = true;
         // every warp of the quarter is here (and what it wrote to tensor memory is visible)
         auto meet = [&]() -> bool {
@@ -617,6 +630,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (t.bad_ctx && tid == 0 && t.rt0 == 0 && t.p == 0) atomicOr(a.err, PKV_DEVERR_CTX_RANGE);
             if (t.n_steps == 0) continue;
             if (*abort_flag) break;
+            if constexpr (F8) {
+                if (!(ok = wait_all(&bar[L::Q_RAW], n & 1))) break;
+                convert_q<D>(base + L::kQ, warp, lane);
+                fence_proxy_async_smem();  // the MMAs read it through the async proxy
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[L::Q_FULL]);
+            }
             const int r = t.rt0 + row;
             const int pos = t.C - t.T + min(r, t.R - 1) / G;  // this row sees keys 0 .. pos
             const float qs0 = F8 ? a.qscale * a.scales[2 * t.p] : a.qscale;
@@ -637,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int s = 0; s < t.n_steps; ++s, ++gs) {
                 const uint32_t mask = mask_of(nxt) >> (4 * half);
                 if (s + 1 < t.n_steps) nxt = ids_of(s + 1);
-                if (!(ok = wait_all(&bar[L::S_FULL + m], gs & 1))) break;
+                if (!(ok = wait_all(&bar[L::ST_FULL + m], gs & 1))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {  // 32 keys at a time
@@ -647,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (c == 1) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar[L::S_READ + m]);
+                        if (lane == 0) mbar_arrive(&bar[L::ST_READ + m]);
                     }
                     const int key0 = s * kKeys + 64 * half + 32 * c;
                     const uint32_t mh = (mask >> (2 * c)) & 3u;
@@ -712,13 +732,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // ---- second sweep: the weights of keys 32 grp .. + 31 of every step ----
             nxt = ids_of(0);
-            for (int s = 0; s < t.n_steps; ++s, ++gs) {
+            for (int s = 0; s < t.n_steps; ++s, ++ps) {
                 const uint32_t mh = (mask_of(nxt) >> (2 * grp)) & 3u;
                 if (s + 1 < t.n_steps) nxt = ids_of(s + 1);
                 const int key0 = s * kKeys + 32 * grp;
                 const bool all = mh == 3u && key0 + 31 <= pos;
-                if (!(ok = wait_all(&bar[L::S_FULL + 1], gs & 1))) break;
-                if (!(ok = wait_all(&bar[L::S_FULL], gs & 1))) break;
+                if (!(ok = wait_all(&bar[L::S2_FULL], ps & 1))) break;
+                if (!(ok = wait_all(&bar[L::S1_FULL + half], ps & 1))) break;
                 tc_fence_after();
                 uint32_t s0[32], s1[32];
                 tmem_ld32(ts + kKeys + 32 * grp, s1);
@@ -805,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();  // every role is done with the tensor memory
     tc_fence_after();
-    if (warp == kQkWarp)
+    if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
