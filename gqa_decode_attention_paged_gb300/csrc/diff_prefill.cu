@@ -339,13 +339,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t policy = l2_policy_evict_normal();
         int u = 0, n = 0;  // units issued, tiles
         bool ok = true;
-        // the next unit: its slot is free, lane 0 announces the bytes
-        auto open = [&](uint64_t *&land, uint8_t *&dst) -> bool {
+        // One lane issues all copies of a unit, the warp running as one: sixteen copies that lanes issued for
+        // themselves went out one lane after the other, each moving its operands to uniform registers (1300
+        // cycles a unit, which bound the kernel).
+        const uint32_t go = elect_one();
+        // the next unit: its slot is free, its bytes are announced
+        auto open = [&](uint32_t &land, uint32_t &dst) -> bool {
             const int st = u % NS, use = u / NS;
             if (use > 0 && !wait_all(&bar[L::EMPTY + st], (use - 1) & 1)) return false;
-            land = &bar[(F8 ? L::RAW : L::FULL) + st];
-            dst = sm + L::kRing + st * L::UT;
-            if (lane == 0) mbar_arrive_expect_tx(land, F8 ? L::UT / 2 : L::UT);
+            uint64_t *b = &bar[(F8 ? L::RAW : L::FULL) + st];
+            land = smem_u32(b);
+            dst = base + L::kRing + st * L::UT;
+            if (go) mbar_arrive_expect_tx(b, F8 ? L::UT / 2 : L::UT);
             __syncwarp();
             ++u;
             return true;
@@ -378,36 +383,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return valid ? (int)((id * (int64_t)a.n_kv + 2 * t.p) * 2 * kBlockSize) : a.oob_row;
             };
             auto copy_k = [&](int y0, int m) -> bool {
-                uint64_t *land;
-                uint8_t *dst;
+                uint32_t land, dst;
                 if (!open(land, dst)) return false;
-                if (lane < kStepBlocks) {
-                    const int y = y0 == a.oob_row ? y0 : y0 + m * 2 * kBlockSize;
+#pragma unroll
+                for (int k = 0; k < kStepBlocks; ++k) {
+                    const int yk = __shfl_sync(kFull, y0, k);
+                    const int y = yk == a.oob_row ? yk : yk + m * 2 * kBlockSize;
                     if constexpr (F8) {
-                        tma_load_2d(dst + L::UT / 2 + lane * (kBlockSize * D), &tm_kv, 0, y, land, policy);
+                        tma_load_2d_if(go, dst + L::UT / 2 + k * (kBlockSize * D), &tm_kv, 0, y, land, policy);
                     } else {
 #pragma unroll
                         for (int h = 0; h < NH; ++h)
-                            tma_load_2d(dst + h * kKHalf + lane * (kBlockSize * 128), &tm_kv, 64 * h, y, land, policy);
+                            tma_load_2d_if(go, dst + h * kKHalf + k * (kBlockSize * 128), &tm_kv, 64 * h, y, land, policy);
                     }
                 }
                 return true;
             };
-            auto copy_v = [&](int y0, int h) -> bool {  // lane: block lane & 3 of the half, value head lane >> 2
-                uint64_t *land;
-                uint8_t *dst;
-                const int k = lane & 3, head = (lane >> 2) & 1;
-                const int yk = __shfl_sync(kFull, y0, h * kUnitBlocks + k);
+            auto copy_v = [&](int y0, int h) -> bool {
+                uint32_t land, dst;
                 if (!open(land, dst)) return false;
-                if (lane < 8) {
-                    const int y = yk == a.oob_row ? yk : yk + head * 2 * kBlockSize + kBlockSize;
-                    dst += head * NH * kVChunk;
-                    if constexpr (F8) {
-                        tma_load_2d(dst + kVKeys * D + k * (kBlockSize * D), &tm_kv, 0, y, land, policy);
-                    } else {
 #pragma unroll
-                        for (int c = 0; c < NH; ++c)
-                            tma_load_2d(dst + c * kVChunk + k * (kBlockSize * 128), &tm_kv, 64 * c, y, land, policy);
+                for (int k = 0; k < kUnitBlocks; ++k) {
+                    const int yk = __shfl_sync(kFull, y0, h * kUnitBlocks + k);
+#pragma unroll
+                    for (int head = 0; head < 2; ++head) {
+                        const int y = yk == a.oob_row ? yk : yk + head * 2 * kBlockSize + kBlockSize;
+                        const uint32_t to = dst + head * NH * kVChunk;
+                        if constexpr (F8) {
+                            tma_load_2d_if(go, to + kVKeys * D + k * (kBlockSize * D), &tm_kv, 0, y, land, policy);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < NH; ++c)
+                                tma_load_2d_if(go, to + c * kVChunk + k * (kBlockSize * 128), &tm_kv, 64 * c, y, land, policy);
+                        }
                     }
                 }
                 return true;
@@ -806,12 +814,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t tok = (int64_t)t.row0 + r / G;
                 __nv_bfloat16 *dst = a.out + (tok * (a.n_q / 2) + t.p * G + r % G) * (2 * D) + grp * QD;
                 const float *nw = a.w.norm_weight ? a.w.norm_weight + grp * QD : nullptr;
+                // (read through the read-only path: as plain loads they wait for the stores between them)
 #pragma unroll
                 for (int c = 0; c < QD; c += 8) {
                     uint32_t w[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float g0 = nw ? nw[c + 2 * i] : 1.0f, g1 = nw ? nw[c + 2 * i + 1] : 1.0f;
+                        const float g0 = nw ? __ldg(nw + c + 2 * i) : 1.0f, g1 = nw ? __ldg(nw + c + 2 * i + 1) : 1.0f;
                         w[i] = pack_bf16x2(__uint_as_float(o[c + 2 * i]) * rn * g0, __uint_as_float(o[c + 2 * i + 1]) * rn * g1);
                     }
                     *reinterpret_cast<uint4 *>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
