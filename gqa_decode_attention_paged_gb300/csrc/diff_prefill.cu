@@ -17,9 +17,14 @@
 // scores.  All statistics are final before the first weight is formed: no
 // accumulator is ever rescaled.
 //
-// Design (one persistent CTA per SM, warp-specialised, as prefill.cu):
+// Design (persistent clusters of two CTAs, one per SM, warp-specialised):
 //   * a tile is 128 query rows (token, head) of one (sequence, pair): both
-//     maps' queries.  A step is 128 keys.
+//     maps' queries.  A step is 128 keys.  The two CTAs of a cluster take
+//     neighbouring tiles of the same (sequence, pair) and walk the same keys:
+//     each copies half of every unit into both CTAs' shared memory (multicast).
+//     A step moves 6 units of 32 KiB into each SM for 3 of MMA work each, and
+//     single copies (20 bytes a cycle and SM) bound the kernel: 602 us at 16
+//     prompts of 700..1024 tokens.
 //   * warp 16 streams Q and, through one ring, what the MMAs take in the order
 //     they take it: K_m units (128 keys of one map) and, in the second sweep, V
 //     units (64 keys x 2 d channels).  One ring for both: in the first sweep
@@ -106,7 +111,7 @@ struct Layout {
            S2_READ = S1_FULL + 2,        // map 2's are in registers
            P_FULL = S2_READ + 1,         // per half: the weights are in tensor memory
            PV_DONE = P_FULL + 2,         // per half: their product has run
-           O_FULL = PV_DONE + 2, O_FREE, END_CLEAR, QUAD, DRAIN = QUAD + 4, NBARS };
+           O_FULL = PV_DONE + 2, O_FREE, END_ASK, END_CLEAR, QUAD, DRAIN = QUAD + 4, NBARS };
     static constexpr uint32_t kTmemSlot = kBar + NBARS * 8;
     static constexpr uint32_t kAbort = kTmemSlot + 4;
     static constexpr uint32_t kEnd = kAbort + 4;
@@ -191,7 +196,7 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b)
 // ------------------------------------------------------------- tile walk
 
 struct Tile {
-    int b, p, rt0;  // sequence, pair, first local row
+    int b, p, rt0;  // sequence, pair, this CTA's first local row (past R: no rows, it helps to copy)
     int R;          // rows of (b, p): T * G
     int row0, T, C; // first query token row of b, chunk length, context length (clamped)
     int n_blocks, n_steps;
@@ -201,9 +206,9 @@ struct Tile {
 // A window of 32 sequences, one per lane: each warp walks the tile list itself
 // (sequence, then pair, then row tile), with the same arithmetic.
 struct Walker {
-    int wb = 0, wbase = 0;           // the window's first sequence, tiles before it
+    int wb = 0, wbase = 0;           // the window's first sequence, tile pairs before it
     int incl = 0, tot = 0;
-    int nt = 0, row0 = 0, T = 0, C = 0;  // this lane's sequence: row tiles per pair, rows, context
+    int nt = 0, row0 = 0, T = 0, C = 0;  // this lane's sequence: tile pairs per KV pair, rows, context
 };
 
 template <int G>
@@ -219,7 +224,7 @@ __device__ __forceinline__ void load_window(Walker &w, const Args &a, int lane)
             w.row0 = lo;
             w.T = hi - lo;
             w.C = a.context_lens[bl];
-            w.nt = (w.T * G + kRows - 1) / kRows;
+            w.nt = (w.T * G + 2 * kRows - 1) / (2 * kRows);
         }
     }
     int x = w.nt * a.n_pairs;
@@ -232,9 +237,9 @@ __device__ __forceinline__ void load_window(Walker &w, const Args &a, int lane)
     w.tot = __shfl_sync(kFull, x, 31);
 }
 
-// Tile x of the list; false past its end.  Warp-wide, uniform result.
+// Tile pair x of the list, and in it CTA `rank`'s tile; false past its end.  Warp-wide, uniform result.
 template <int G>
-__device__ __forceinline__ bool find_tile(Walker &w, const Args &a, int x, Tile &t, int lane)
+__device__ __forceinline__ bool find_tile(Walker &w, const Args &a, int x, int rank, Tile &t, int lane)
 {
     while (x >= w.wbase + w.tot) {
         if (w.wb + 32 >= a.batch) return false;
@@ -252,7 +257,8 @@ __device__ __forceinline__ bool find_tile(Walker &w, const Args &a, int x, Tile 
     int C = __shfl_sync(kFull, w.C, l);
     const int within = x - w.wbase - before;
     t.p = within / nt;
-    t.rt0 = (within - t.p * nt) * kRows;
+    const int pair0 = (within - t.p * nt) * 2 * kRows;
+    t.rt0 = pair0 + rank * kRows;
     t.R = t.T * G;
     const int cap = a.W * kBlockSize;
     t.bad_ctx = C < t.T || C > cap;
@@ -262,7 +268,7 @@ __device__ __forceinline__ bool find_tile(Walker &w, const Args &a, int x, Tile 
         t.n_blocks = t.n_steps = 0;
         return true;
     }
-    const int last_row = min(t.R, t.rt0 + kRows) - 1;
+    const int last_row = min(t.R, pair0 + 2 * kRows) - 1;  // the pair walks the same keys
     t.n_blocks = (C - t.T + last_row / G) / kBlockSize + 1;
     t.n_steps = (t.n_blocks + kStepBlocks - 1) / kStepBlocks;
     return true;
@@ -294,6 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::kAbort);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(kFull, tid >> 5, 0);  // the same in all lanes, and known to be
+    const int rank = (int)cluster_rank();
+    constexpr uint16_t kBoth = 3;
 
     if (tid == 0) {
         prefetch_tensormap(&tm_q);
@@ -305,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i >= L::QUAD && i < L::QUAD + 4) n = 4;  // the four warps of a lane quarter
             if (i == L::Q_FULL && F8) n = kSoftmaxWarps;  // each widens its share of the queries
             if (i >= L::FULL && i < L::EMPTY && kSplit) n = 2;
+            if (i >= L::EMPTY && i < L::EMPTY + NS) n = 2;  // both CTAs have used the slot
             mbar_init(&bar[i], n);
         }
         *abort_flag = 0;
@@ -319,6 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // both CTAs' barriers are ready
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + L::kTmemSlot);
     griddep_wait();
@@ -355,9 +365,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++u;
             return true;
         };
-        for (int x = blockIdx.x; ok; x += gridDim.x) {
+        for (int x = blockIdx.x / 2; ok; x += gridDim.x / 2) {
             Tile t;
-            if (!find_tile<G>(wk, a, x, t, lane)) break;
+            if (!find_tile<G>(wk, a, x, rank, t, lane)) break;
             if (t.n_steps == 0) continue;
             if (*abort_flag) break;
             if (n > 0 && !(ok = wait_all(&bar[L::Q_FREE], (n - 1) & 1))) break;
@@ -386,15 +396,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t land, dst;
                 if (!open(land, dst)) return false;
 #pragma unroll
-                for (int k = 0; k < kStepBlocks; ++k) {
+                for (int i = 0; i < kStepBlocks / 2; ++i) {  // this CTA's blocks, into both CTAs
+                    const int k = 2 * i + rank;
                     const int yk = __shfl_sync(kFull, y0, k);
                     const int y = yk == a.oob_row ? yk : yk + m * 2 * kBlockSize;
                     if constexpr (F8) {
-                        tma_load_2d_if(go, dst + L::UT / 2 + k * (kBlockSize * D), &tm_kv, 0, y, land, policy);
+                        tma_load_2d_multicast_if(go, dst + L::UT / 2 + k * (kBlockSize * D), &tm_kv, 0, y, land, kBoth, policy);
                     } else {
 #pragma unroll
                         for (int h = 0; h < NH; ++h)
-                            tma_load_2d_if(go, dst + h * kKHalf + k * (kBlockSize * 128), &tm_kv, 64 * h, y, land, policy);
+                            tma_load_2d_multicast_if(go, dst + h * kKHalf + k * (kBlockSize * 128), &tm_kv, 64 * h, y, land, kBoth, policy);
                     }
                 }
                 return true;
@@ -403,18 +414,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t land, dst;
                 if (!open(land, dst)) return false;
 #pragma unroll
-                for (int k = 0; k < kUnitBlocks; ++k) {
+                for (int i = 0; i < kUnitBlocks / 2; ++i) {
+                    const int k = 2 * i + rank;
                     const int yk = __shfl_sync(kFull, y0, h * kUnitBlocks + k);
 #pragma unroll
                     for (int head = 0; head < 2; ++head) {
                         const int y = yk == a.oob_row ? yk : yk + head * 2 * kBlockSize + kBlockSize;
                         const uint32_t to = dst + head * NH * kVChunk;
                         if constexpr (F8) {
-                            tma_load_2d_if(go, to + kVKeys * D + k * (kBlockSize * D), &tm_kv, 0, y, land, policy);
+                            tma_load_2d_multicast_if(go, to + kVKeys * D + k * (kBlockSize * D), &tm_kv, 0, y, land, kBoth, policy);
                         } else {
 #pragma unroll
                             for (int c = 0; c < NH; ++c)
-                                tma_load_2d_if(go, to + c * kVChunk + k * (kBlockSize * 128), &tm_kv, 64 * c, y, land, policy);
+                                tma_load_2d_multicast_if(go, to + c * kVChunk + k * (kBlockSize * 128), &tm_kv, 64 * c, y, land, kBoth, policy);
                         }
                     }
                 }
@@ -440,53 +452,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         // copies still in flight (after an abort) land before the CTA exits
         for (int i = max(0, u - NS); i < u; ++i)
             mbar_wait_bounded(&bar[(F8 ? L::RAW : L::FULL) + i % NS], (i / NS) & 1);
+        // and the other CTA's arrivals on this one's barriers (none comes after the last units')
+        for (int i = max(0, u - NS); i < u && ok && !*abort_flag; ++i)
+            ok = wait_all(&bar[L::EMPTY + i % NS], (i / NS) & 1);
         if (n > 0) mbar_wait_bounded(&bar[F8 ? L::Q_RAW : L::Q_FULL], (n - 1) & 1);
         if (!ok) set_abort();
     } else if (warp >= kPrepWarp) {
         // ---------------------------------------------------------- units made ready
         const int which = warp - kPrepWarp;
         if (F8 || which == 0) {
-            int u = 0;
+            int u = 0, ends = 0;
             bool ok = true;
-            for (int x = blockIdx.x; ok; x += gridDim.x) {
+            for (int x = blockIdx.x / 2; ok; x += gridDim.x / 2) {
                 Tile t;
-                if (!find_tile<G>(wk, a, x, t, lane)) break;
+                if (!find_tile<G>(wk, a, x, rank, t, lane)) break;
                 if (t.n_steps == 0) continue;
                 if (*abort_flag) break;
-                const int end = end_unit(t);  // the V unit the sequence ends inside of
-                for (int i = 0; i < 6 * t.n_steps; ++i, ++u) {
-                    const int st = u % NS;
-                    if (F8 && !kSplit && (u & 1) != which) continue;
-                    if (!(ok = wait_all(&bar[(F8 ? L::RAW : L::FULL) + st], (u / NS) & 1))) break;
-                    // second sweep: K, K of the first step, then of each step V, K, K (the next step's, if
-                    // there is one), V
-                    const int iv = i - 2 * t.n_steps - 2;
-                    const int vs = iv >> 2, vp = iv & 3;
-                    const bool is_v = iv >= 0 && (vp == 0 || vp == 3 || (vp == 1 && vs == t.n_steps - 1));
-                    const uint32_t unit = base + L::kRing + st * L::UT;
-                    if constexpr (F8) {
+                // the V unit the sequence ends inside of: zero the rows behind the end (value heads h0 ..)
+                const int end = end_unit(t);
+                auto clear = [&](uint32_t unit, int h0, int heads) {
+                    const int r0 = (t.C / kBlockSize % kUnitBlocks) * kBlockSize;
+                    const int first = r0 + t.C % kBlockSize, rows = r0 + kBlockSize - first;
+                    for (int e = lane; e < rows * 8 * heads * NH; e += 32) {
+                        const int row = first + (e >> 3) % rows, ch = h0 * NH + (e >> 3) / rows;
+                        sts128(unit + ch * kVChunk + row * 128 + (e & 7) * 16, make_uint4(0, 0, 0, 0));
+                    }
+                };
+                if constexpr (!F8) {  // the MMA warp asks when the unit has landed
+                    if (end >= 0) {
+                        const int vs = end / 2, S = t.n_steps;
+                        const int v = u + 2 * S + 2 + 4 * vs + ((end & 1) == 0 ? 0 : vs == S - 1 ? 1 : 3);
+                        if (!(ok = wait_all(&bar[L::END_ASK], ends & 1))) break;
+                        ++ends;
+                        clear(base + L::kRing + v % NS * L::UT, 0, 2);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar[L::END_CLEAR]);
+                    }
+                    u += 6 * t.n_steps;
+                } else {
+                    for (int i = 0; i < 6 * t.n_steps; ++i, ++u) {
+                        const int st = u % NS;
+                        if (!kSplit && (u & 1) != which) continue;
+                        if (!(ok = wait_all(&bar[L::RAW + st], (u / NS) & 1))) break;
+                        // second sweep: K, K of the first step, then of each step V, K, K (the next step's, if
+                        // there is one), V
+                        const int iv = i - 2 * t.n_steps - 2;
+                        const int vs = iv >> 2, vp = iv & 3;
+                        const bool is_v = iv >= 0 && (vp == 0 || vp == 3 || (vp == 1 && vs == t.n_steps - 1));
+                        const uint32_t unit = base + L::kRing + st * L::UT;
                         if (is_v) {
                             if (!kSplit || which == 0) convert_f16<D, kVKeys>(unit, lane, 0, kVKeys);
                             if (!kSplit || which == 1) convert_f16<D, kVKeys>(unit + NH * kVChunk, lane, 0, kVKeys);
+                            if (2 * vs + (vp != 0) == end) clear(unit, kSplit ? which : 0, kSplit ? 1 : 2);
                         } else {
                             convert_f16<D, kKeys>(unit, lane, kSplit ? which * (kKeys / 2) : 0, kSplit ? kKeys / 2 : kKeys);
                         }
-                    }
-                    const bool ends = is_v && 2 * vs + (vp != 0) == end;
-                    if (ends) {  // this warp's value heads: rows behind the end
-                        const int heads = kSplit ? 1 : 2, h0 = kSplit ? which : 0;
-                        const int r0 = (t.C / kBlockSize % kUnitBlocks) * kBlockSize;
-                        const int first = r0 + t.C % kBlockSize, rows = r0 + kBlockSize - first;
-                        for (int e = lane; e < rows * 8 * heads * NH; e += 32) {
-                            const int row = first + (e >> 3) % rows, ch = h0 * NH + (e >> 3) / rows;
-                            sts128(unit + ch * kVChunk + row * 128 + (e & 7) * 16, make_uint4(0, 0, 0, 0));
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (F8) mbar_arrive(&bar[L::FULL + st]);
-                        else if (ends) mbar_arrive(&bar[L::END_CLEAR]);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar[L::FULL + st]);
                     }
                 }
             }
@@ -514,9 +538,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 umma_if(go, tm + m * kKeys + part * 64, qm + off, km + off, idesc, kk > 0 ? 1u : 0u);
             }
         };
-        for (int x = blockIdx.x; ok; x += gridDim.x) {
+        for (int x = blockIdx.x / 2; ok; x += gridDim.x / 2) {
             Tile t;
-            if (!find_tile<G>(wk, a, x, t, lane)) break;
+            if (!find_tile<G>(wk, a, x, rank, t, lane)) break;
             if (t.n_steps == 0) continue;
             if (*abort_flag) break;
             {
@@ -535,13 +559,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!unit(u)) return false;
                     scores(m, u, 0, idesc_qk);
                     umma_commit_if(go, &bar[L::ST_FULL + m]);
-                    umma_commit_if(go, &bar[L::EMPTY + u++ % NS]);
+                    umma_commit_multicast_if(go, &bar[L::EMPTY + u++ % NS], kBoth);
                     return true;
                 };
                 auto product = [&](int s, int h) -> bool {
                     const int v = u++;
                     if (!unit(v)) return false;
                     if (!F8 && 2 * s + h == end) {
+                        if (go) mbar_arrive(&bar[L::END_ASK]);
+                        __syncwarp();
                         if (!wait_all(&bar[L::END_CLEAR], ends & 1)) return false;
                         ++ends;
                     }
@@ -552,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kk = 0; kk < kVKeys / 16; ++kk)
                         umma_ts_if(go, tm + kColO, tm + h * kVKeys + (kk >> 1) * 32 + (kk & 1) * 8, vm + ((kk * 2048) >> 4),
                                 idesc_pv, (s > 0 || h > 0 || kk > 0) ? 1u : 0u);
-                    umma_commit_if(go, &bar[L::EMPTY + v % NS]);
+                    umma_commit_multicast_if(go, &bar[L::EMPTY + v % NS], kBoth);
                     umma_commit_if(go, &bar[L::PV_DONE + h]);
                     return true;
                 };
@@ -563,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ok) {
                     scores(1, u, 0, idesc_qk);
                     umma_commit_if(go, &bar[L::S2_FULL]);
-                    umma_commit_if(go, &bar[L::EMPTY + u++ % NS]);
+                    umma_commit_multicast_if(go, &bar[L::EMPTY + u++ % NS], kBoth);
                     ok = wait_all(&bar[L::ST_READ], (reads - 1) & 1) && unit(u);
                 }
                 if (ok) {
@@ -571,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     umma_commit_if(go, &bar[L::S1_FULL]);
                     scores(0, u, 1, idesc_half);
                     umma_commit_if(go, &bar[L::S1_FULL + 1]);
-                    umma_commit_if(go, &bar[L::EMPTY + u++ % NS]);
+                    umma_commit_multicast_if(go, &bar[L::EMPTY + u++ % NS], kBoth);
                     if (n > 0) ok = wait_all(&bar[L::O_FREE], (n - 1) & 1);
                 }
                 for (int s = 0; s < S && ok; ++s, ++steps) {
@@ -582,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!(ok = wait_all(&bar[L::S2_READ], steps & 1) && unit(u))) break;
                         scores(1, u, 0, idesc_qk);
                         umma_commit_if(go, &bar[L::S2_FULL]);
-                        umma_commit_if(go, &bar[L::EMPTY + u++ % NS]);
+                        umma_commit_multicast_if(go, &bar[L::EMPTY + u++ % NS], kBoth);
                         k1 = u++;
                         if (!(ok = wait_all(&bar[L::PV_DONE], steps & 1) && unit(k1))) break;
                         scores(0, k1, 0, idesc_half);
@@ -595,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!(ok = wait_all(&bar[L::PV_DONE + 1], steps & 1))) break;
                         scores(0, k1, 1, idesc_half);
                         umma_commit_if(go, &bar[L::S1_FULL + 1]);
-                        umma_commit_if(go, &bar[L::EMPTY + k1 % NS]);
+                        umma_commit_multicast_if(go, &bar[L::EMPTY + k1 % NS], kBoth);
                     } else {
                         umma_commit_if(go, &bar[L::O_FULL]);
                     }
@@ -632,9 +658,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             return done;
         };
-        for (int x = blockIdx.x; ok; x += gridDim.x) {
+        for (int x = blockIdx.x / 2; ok; x += gridDim.x / 2) {
             Tile t;
-            if (!find_tile<G>(wk, a, x, t, lane)) break;
+            if (!find_tile<G>(wk, a, x, rank, t, lane)) break;
             if (t.bad_ctx && tid == 0 && t.rt0 == 0 && t.p == 0) atomicOr(a.err, PKV_DEVERR_CTX_RANGE);
             if (t.n_steps == 0) continue;
             if (*abort_flag) break;
@@ -833,6 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     tc_fence_before();
     __syncthreads();  // every role is done with the tensor memory
+    cluster_sync();   // the other CTA's last commits and copies have reached this one
     tc_fence_after();
     if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
@@ -858,10 +885,22 @@ pkv_status launch(pkv_pool *pool, const void *q, int64_t tiles, const Args &a, c
     CUtensorMap tm_q;
     pkv_status st = make_q_pair_map(&tm_q, q, a.n_rows, a.n_q, D, G, kRows / G);
     if (st != PKV_OK) return st;
-    const int grid = (int)std::min<int64_t>(tiles, pool->num_sms);
+    const int grid = 2 * (int)std::min<int64_t>(tiles, pool->num_sms / 2);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = L::bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     LaunchScope ls(pool, kDecode, s);
-    cudaError_t e = launch_pdl(diff_prefill_kernel<D, G, F8>, dim3(grid), dim3(kThreads), L::bytes, s, tm_q,
-                               pool->tm_block, a);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, diff_prefill_kernel<D, G, F8>, tm_q, pool->tm_block, a);
     ls.done();
     if (e != cudaSuccess) return cuda_fail(e, "paged_diff_prefill_attention launch");
     return PKV_OK;
@@ -906,8 +945,8 @@ extern "C" pkv_status paged_diff_prefill_attention(pkv_pool *pool, const void *q
         return fail(PKV_EINVAL, "%s: indptr, tables and lengths must be 4-byte aligned", who);
     st = check_pool_device(pool, who);
     if (st != PKV_OK) return st;
-    // an upper bound on the tiles: every sequence may end with a partial one
-    const int64_t tiles = ((n_rows * G + kRows - 1) / kRows + batch) * (pool->n_kv / 2);
+    // an upper bound on the tile pairs: every sequence may end with a partial one
+    const int64_t tiles = ((n_rows * G + 2 * kRows - 1) / (2 * kRows) + batch) * (pool->n_kv / 2);
     if (tiles > INT32_MAX) return fail(PKV_EUNSUPPORTED, "%s: too many query rows", who);
     a.qo_indptr = qo_indptr;
     a.block_tables = block_tables;
