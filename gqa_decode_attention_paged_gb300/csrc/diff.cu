@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(DCfg<D, G, KV>::kThreads, 2)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const int d = (t / NT) * D + chan(t % NT, i);
-                            const float wt = a.w.norm_weight ? a.w.norm_weight[d] : 1.0f;
+                            const float wt = a.w.norm_weight ? __ldg(a.w.norm_weight + d) : 1.0f;
                             ob[d] = __float2bfloat16_rn(o[nb][t][2 * i] * r * wt);
                         }
                 }
@@ -607,10 +607,8 @@ __global__ void __launch_bounds__(kDiffMergeWarps * 32, 2) diff_merge_kernel(con
 #pragma unroll
             for (int c = 0; c < HK; ++c) {
                 const int d = 4 * (lane + 32 * c);
-                float4 wt = make_float4(1.f, 1.f, 1.f, 1.f);
-                if (a.w.norm_weight)
-                    wt = make_float4(a.w.norm_weight[d], a.w.norm_weight[d + 1], a.w.norm_weight[d + 2],
-                                     a.w.norm_weight[d + 3]);
+                const float4 wt = a.w.norm_weight ? __ldg(reinterpret_cast<const float4 *>(a.w.norm_weight + d))
+                                                  : make_float4(1.f, 1.f, 1.f, 1.f);
                 *reinterpret_cast<uint2 *>(ob + d) = make_uint2(pack2<false>(acc[c].x * r * wt.x, acc[c].y * r * wt.y),
                                                                 pack2<false>(acc[c].z * r * wt.z, acc[c].w * r * wt.w));
             }
@@ -757,8 +755,8 @@ pkv_status check_diff_args(const pkv_pool *pool, const char *who, const pkv_diff
     if (st != PKV_OK) return st;
     if (!params) return fail(PKV_EINVAL, "%s: NULL params", who);
     if (!params->lambdas) return fail(PKV_EINVAL, "%s: NULL lambdas", who);
-    if (((uintptr_t)params->lambdas | (uintptr_t)params->norm_weight) & 3u)
-        return fail(PKV_EINVAL, "%s: lambdas and norm_weight must be 4-byte aligned", who);
+    if (((uintptr_t)params->lambdas & 3u) || ((uintptr_t)params->norm_weight & 15u))
+        return fail(PKV_EINVAL, "%s: lambdas must be 4-byte and norm_weight 16-byte aligned", who);
     if (!isfinite(params->lambda_init)) return fail(PKV_EINVAL, "%s: lambda_init is not finite", who);
     if (!(params->eps > 0.0f) || !isfinite(params->eps)) return fail(PKV_EINVAL, "%s: eps must be finite and above 0", who);
     w->lambdas = params->lambdas;

@@ -693,16 +693,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (s + 1 < t.n_steps) nxt = ids_of(s + 1);
                 if (!(ok = wait_all(&bar[L::ST_FULL + m], gs & 1))) break;
                 tc_fence_after();
+                uint32_t both[64];
+                tmem_ld32(ts + m * kKeys + 64 * half, both);
+                tmem_ld32(ts + m * kKeys + 64 * half + 32, both + 32);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[L::ST_READ + m]);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {  // 32 keys at a time
-                    uint32_t sr[32];
-                    tmem_ld32(ts + m * kKeys + 64 * half + 32 * c, sr);
-                    tmem_wait_ld();
-                    if (c == 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar[L::ST_READ + m]);
-                    }
+                    uint32_t *sr = both + 32 * c;
                     const int key0 = s * kKeys + 64 * half + 32 * c;
                     const uint32_t mh = (mask >> (2 * c)) & 3u;
                     if (!(mh == 3u && key0 + 31 <= pos)) {  // what this row does not see never has the largest score
@@ -840,16 +840,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t tok = (int64_t)t.row0 + r / G;
                 __nv_bfloat16 *dst = a.out + (tok * (a.n_q / 2) + t.p * G + r % G) * (2 * D) + grp * QD;
                 const float *nw = a.w.norm_weight ? a.w.norm_weight + grp * QD : nullptr;
-                // (read through the read-only path: as plain loads they wait for the stores between them)
+                // 32 bytes a store: a lane's row is a line of its own, so each store instruction takes the
+                // load-store unit 32 passes whatever its width.  The norm's weights come through the read-only
+                // path (plain loads would wait for the stores between them).
 #pragma unroll
-                for (int c = 0; c < QD; c += 8) {
-                    uint32_t w[4];
+                for (int c = 0; c < QD; c += 16) {
+                    uint32_t w[8];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float g0 = nw ? __ldg(nw + c + 2 * i) : 1.0f, g1 = nw ? __ldg(nw + c + 2 * i + 1) : 1.0f;
-                        w[i] = pack_bf16x2(__uint_as_float(o[c + 2 * i]) * rn * g0, __uint_as_float(o[c + 2 * i + 1]) * rn * g1);
+                        const float4 g = nw ? __ldg(reinterpret_cast<const float4 *>(nw + c) + i) : make_float4(1.f, 1.f, 1.f, 1.f);
+                        const uint32_t *x4 = o + c + 4 * i;
+                        w[2 * i] = pack_bf16x2(__uint_as_float(x4[0]) * rn * g.x, __uint_as_float(x4[1]) * rn * g.y);
+                        w[2 * i + 1] = pack_bf16x2(__uint_as_float(x4[2]) * rn * g.z, __uint_as_float(x4[3]) * rn * g.w);
                     }
-                    *reinterpret_cast<uint4 *>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+                    stg256(dst + c, w);
                 }
             }
             ++n;
@@ -940,7 +944,8 @@ extern "C" pkv_status paged_diff_prefill_attention(pkv_pool *pool, const void *q
     if (n_rows > INT32_MAX / G) return fail(PKV_EUNSUPPORTED, "%s: more than 2^31 query rows x group size", who);
     if (!q || !qo_indptr || !block_tables || !context_lens || !out)
         return fail(PKV_EINVAL, "%s: NULL device pointer", who);
-    if (((uintptr_t)q | (uintptr_t)out) & 15u) return fail(PKV_EINVAL, "%s: q and out must be 16-byte aligned", who);
+    if (((uintptr_t)q & 15u) || ((uintptr_t)out & 31u))
+        return fail(PKV_EINVAL, "%s: q must be 16-byte and out 32-byte aligned", who);
     if (((uintptr_t)qo_indptr | (uintptr_t)block_tables | (uintptr_t)context_lens) & 3u)
         return fail(PKV_EINVAL, "%s: indptr, tables and lengths must be 4-byte aligned", who);
     st = check_pool_device(pool, who);

@@ -202,6 +202,14 @@ __device__ __forceinline__ void add_bf16x2_to(float &acc, uint32_t pk)
         : "r"(pk));
 }
 
+// 32 bytes to a 32-byte aligned global address in one store.
+__device__ __forceinline__ void stg256(void *p, const uint32_t *w)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 // max(a, b, c) in one instruction
 __device__ __forceinline__ float fmax3(float a, float b, float c)
 {

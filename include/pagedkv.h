@@ -461,7 +461,7 @@ pkv_status paged_prefill_attention(pkv_pool *pool, const void *q, int64_t n_rows
  * --------------------------------------------------------------------- */
 typedef struct {
     const float *lambdas;      /* device fp32 [4][d_head] */
-    const float *norm_weight;  /* device fp32 [2 d_head]; NULL: ones */
+    const float *norm_weight;  /* device fp32 [2 d_head], 16-byte aligned; NULL: ones */
     float lambda_init;         /* finite */
     float eps;                 /* finite, > 0 */
 } pkv_diff_params;
@@ -497,7 +497,7 @@ pkv_status paged_diff_decode_attention(pkv_pool *pool, const void *q, int32_t n_
  *              length past the table, is clamped and sets
  *              PKV_DEVERR_CTX_RANGE; a chunk longer than its whole table is
  *              skipped.
- *   out        device bf16 [n_rows][n_q / 2][2 d_head], 16-byte aligned; rows
+ *   out        device bf16 [n_rows][n_q / 2][2 d_head], 32-byte aligned; rows
  *              of no sequence, or of one that is skipped, stay as they were.
  * A block id outside the pool counts as masked and sets
  * PKV_DEVERR_BLOCK_RANGE; a row that sees nothing is zero.  Cached rows
