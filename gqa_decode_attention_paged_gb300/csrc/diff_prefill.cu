@@ -101,7 +101,8 @@ struct Layout {
     static constexpr int kStages = D == 128 ? 5 : 10;
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kRing = kQ + 2 * QT;
-    static constexpr uint32_t kBar = kRing + kStages * UT;
+    static constexpr uint32_t kNorm = kRing + kStages * UT;  // [2 D] float: the norm's weights
+    static constexpr uint32_t kBar = kNorm + 2 * D * 4;
     // RAW, Q_RAW: FP8 pools' copies complete there; FULL and Q_FULL follow when the rows are f16
     enum { Q_RAW = 0, Q_FULL, Q_FREE, RAW, FULL = RAW + kStages, EMPTY = FULL + kStages,
            ST_FULL = EMPTY + kStages,    // first sweep, per map: scores of a step
@@ -340,6 +341,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             *abort_flag = 1;
         }
     };
+    for (int i = tid; i < 2 * D; i += kThreads)
+        reinterpret_cast<float *>(sm + L::kNorm)[i] = a.w.norm_weight ? a.w.norm_weight[i] : 1.0f;
+    __syncthreads();
     Walker wk;
     load_window<G>(wk, a, lane);
     const uint32_t base = smem_u32(sm);
@@ -443,9 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = copy_k(y0, 1) && copy_k(y0, 0);
             for (int s = 0; s < t.n_steps && ok; ++s) {  // in the order of the MMAs
                 if (s + 1 < t.n_steps) nxt = rows_of(s + 1, false);
-                ok = copy_v(y0, 0);
-                if (s + 1 < t.n_steps) ok = ok && copy_k(nxt, 1) && copy_k(nxt, 0);
-                ok = ok && copy_v(y0, 1);
+                const bool more = s + 1 < t.n_steps;
+                ok = copy_v(y0, 0) && (!more || (copy_k(nxt, 1) && copy_k(nxt, 0))) && copy_v(y0, 1);
                 y0 = nxt;
             }
         }
@@ -481,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (!F8) {  // the MMA warp asks when the unit has landed
                     if (end >= 0) {
                         const int vs = end / 2, S = t.n_steps;
-                        const int v = u + 2 * S + 2 + 4 * vs + ((end & 1) == 0 ? 0 : vs == S - 1 ? 1 : 3);
+                        const int v = u + 2 * S + 2 + 4 * vs + (end & 1) * (vs == S - 1 ? 1 : 3);
                         if (!(ok = wait_all(&bar[L::END_ASK], ends & 1))) break;
                         ++ends;
                         clear(base + L::kRing + v % NS * L::UT, 0, 2);
@@ -495,16 +498,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int st = u % NS;
                         if (!kSplit && (u & 1) != which) continue;
                         if (!(ok = wait_all(&bar[L::RAW + st], (u / NS) & 1))) break;
-                        // second sweep: K, K of the first step, then of each step V, K, K (the next step's, if
-                        // there is one), V
+                        // second sweep: K, K of the first step, then of each step V, K, K, V (the next step's
+                        // keys; the last step has V, V)
                         const int iv = i - 2 * t.n_steps - 2;
                         const int vs = iv >> 2, vp = iv & 3;
-                        const bool is_v = iv >= 0 && (vp == 0 || vp == 3 || (vp == 1 && vs == t.n_steps - 1));
+                        const bool tail = vs == t.n_steps - 1;
+                        const bool is_v = iv >= 0 && (tail || vp == 0 || vp == 3);
+                        const int vh = vp != 0;  // the V unit's half
                         const uint32_t unit = base + L::kRing + st * L::UT;
                         if (is_v) {
                             if (!kSplit || which == 0) convert_f16<D, kVKeys>(unit, lane, 0, kVKeys);
                             if (!kSplit || which == 1) convert_f16<D, kVKeys>(unit + NH * kVChunk, lane, 0, kVKeys);
-                            if (2 * vs + (vp != 0) == end) clear(unit, kSplit ? which : 0, kSplit ? 1 : 2);
+                            if (2 * vs + vh == end) clear(unit, kSplit ? which : 0, kSplit ? 1 : 2);
                         } else {
                             convert_f16<D, kKeys>(unit, lane, kSplit ? which * (kKeys / 2) : 0, kSplit ? kKeys / 2 : kKeys);
                         }
@@ -658,11 +663,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             return done;
         };
-        for (int x = blockIdx.x / 2; ok; x += gridDim.x / 2) {
-            Tile t;
-            if (!find_tile<G>(wk, a, x, rank, t, lane)) break;
-            if (t.bad_ctx && tid == 0 && t.rt0 == 0 && t.p == 0) atomicOr(a.err, PKV_DEVERR_CTX_RANGE);
-            if (t.n_steps == 0) continue;
+        // the next tile that has keys, and this lane's block id of its first step, are found while the tensor
+        // cores finish the tile before
+        int x = blockIdx.x / 2;
+        Tile tn;
+        int first_id = -1;
+        auto find_next = [&]() -> bool {
+            for (;; x += gridDim.x / 2) {
+                if (!find_tile<G>(wk, a, x, rank, tn, lane)) return false;
+                if (tn.bad_ctx && tid == 0 && tn.rt0 == 0 && tn.p == 0) atomicOr(a.err, PKV_DEVERR_CTX_RANGE);
+                if (tn.n_steps > 0) break;
+            }
+            x += gridDim.x / 2;
+            first_id = lane < kStepBlocks && lane < tn.n_blocks ? a.block_tables[(int64_t)tn.b * a.W + lane] : -1;
+            return true;
+        };
+        bool have = find_next();
+        while (have && ok) {
+            const Tile t = tn;
+            const int id0 = first_id;
             if (*abort_flag) break;
             if constexpr (F8) {
                 if (!(ok = wait_all(&bar[L::Q_RAW], n & 1))) break;
@@ -687,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // ---- first sweep: maximum and sum of map m over this half's keys ----
             float mx = -INFINITY, l = 0.0f;
-            int nxt = ids_of(0);
+            int nxt = id0;
             for (int s = 0; s < t.n_steps; ++s, ++gs) {
                 const uint32_t mask = mask_of(nxt) >> (4 * half);
                 if (s + 1 < t.n_steps) nxt = ids_of(s + 1);
@@ -765,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // ---- second sweep: the weights of keys 32 grp .. + 31 of every step ----
-            nxt = ids_of(0);
+            nxt = id0;
             for (int s = 0; s < t.n_steps; ++s, ++ps) {
                 const uint32_t mh = (mask_of(nxt) >> (2 * grp)) & 3u;
                 if (s + 1 < t.n_steps) nxt = ids_of(s + 1);
@@ -805,6 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             // ---- norm and store: this thread's quarter of its row ----
+            have = find_next();
             if (!(ok = wait_all(&bar[L::O_FULL], n & 1))) break;
             tc_fence_after();
             const float f = inv * (F8 ? a.scales[a.n_kv + 2 * t.p + half] : 1.0f);
@@ -839,16 +859,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (r < t.R) {
                 const int64_t tok = (int64_t)t.row0 + r / G;
                 __nv_bfloat16 *dst = a.out + (tok * (a.n_q / 2) + t.p * G + r % G) * (2 * D) + grp * QD;
-                const float *nw = a.w.norm_weight ? a.w.norm_weight + grp * QD : nullptr;
+                const float4 *nw = reinterpret_cast<const float4 *>(sm + L::kNorm) + grp * (QD / 4);
                 // 32 bytes a store: a lane's row is a line of its own, so each store instruction takes the
-                // load-store unit 32 passes whatever its width.  The norm's weights come through the read-only
-                // path (plain loads would wait for the stores between them).
+                // load-store unit 32 passes whatever its width
 #pragma unroll
                 for (int c = 0; c < QD; c += 16) {
                     uint32_t w[8];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float4 g = nw ? __ldg(reinterpret_cast<const float4 *>(nw + c) + i) : make_float4(1.f, 1.f, 1.f, 1.f);
+                        const float4 g = nw[c / 4 + i];
                         const uint32_t *x4 = o + c + 4 * i;
                         w[2 * i] = pack_bf16x2(__uint_as_float(x4[0]) * rn * g.x, __uint_as_float(x4[1]) * rn * g.y);
                         w[2 * i + 1] = pack_bf16x2(__uint_as_float(x4[2]) * rn * g.z, __uint_as_float(x4[3]) * rn * g.w);
