@@ -54,6 +54,7 @@
 // (bounded) and the tensor memory is released before the CTA exits.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "diff_common.cuh"
 #include "tcgen05.cuh"
@@ -724,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t *sr = both + 32 * c;
                     const int key0 = s * kKeys + 64 * half + 32 * c;
                     const uint32_t mh = (mask >> (2 * c)) & 3u;
-                    if (!(mh == 3u && key0 + 31 <= pos)) {  // what this row does not see never has the largest score
+                    if (!__all_sync(kFull, mh == 3u && key0 + 31 <= pos)) {  // what this row does not see never has the largest score
                         const uint32_t never = rising ? 0xff800000u : 0x7f800000u;
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
@@ -789,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t mh = (mask_of(nxt) >> (2 * grp)) & 3u;
                 if (s + 1 < t.n_steps) nxt = ids_of(s + 1);
                 const int key0 = s * kKeys + 32 * grp;
-                const bool all = mh == 3u && key0 + 31 <= pos;
+                const bool all = __all_sync(kFull, mh == 3u && key0 + 31 <= pos);
                 if (!(ok = wait_all(&bar[L::S2_FULL], ps & 1))) break;
                 if (!(ok = wait_all(&bar[L::S1_FULL + half], ps & 1))) break;
                 tc_fence_after();
@@ -801,21 +802,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[L::S2_READ]);
                 uint32_t pk[16];
+                auto weigh = [&](auto masked) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float2 u0 = ffma2(make_float2(__uint_as_float(s0[2 * i]), __uint_as_float(s0[2 * i + 1])),
-                                            make_float2(qs0, qs0), make_float2(n0, n0));
-                    const float2 u1 = ffma2(make_float2(__uint_as_float(s1[2 * i]), __uint_as_float(s1[2 * i + 1])),
-                                            make_float2(qs1, qs1), make_float2(n1, n1));
-                    float2 w = ffma2(make_float2(ex2(u1.x), ex2(u1.y)), make_float2(sign, sign),
-                                     make_float2(ex2(u0.x), ex2(u0.y)));
-                    if (!all) {
-                        const bool seen = (mh >> (2 * i / kBlockSize)) & 1u;
-                        if (!(seen && key0 + 2 * i <= pos)) w.x = 0.0f;
-                        if (!(seen && key0 + 2 * i + 1 <= pos)) w.y = 0.0f;
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 u0 = ffma2(make_float2(__uint_as_float(s0[2 * i]), __uint_as_float(s0[2 * i + 1])),
+                                                make_float2(qs0, qs0), make_float2(n0, n0));
+                        const float2 u1 = ffma2(make_float2(__uint_as_float(s1[2 * i]), __uint_as_float(s1[2 * i + 1])),
+                                                make_float2(qs1, qs1), make_float2(n1, n1));
+                        float2 w = ffma2(make_float2(ex2(u1.x), ex2(u1.y)), make_float2(sign, sign),
+                                         make_float2(ex2(u0.x), ex2(u0.y)));
+                        if constexpr (decltype(masked)::value) {
+                            const bool seen = (mh >> (2 * i / kBlockSize)) & 1u;
+                            if (!(seen && key0 + 2 * i <= pos)) w.x = 0.0f;
+                            if (!(seen && key0 + 2 * i + 1 <= pos)) w.y = 0.0f;
+                        }
+                        pk[i] = F8 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
                     }
-                    pk[i] = F8 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
-                }
+                };
+                if (all) weigh(std::false_type{});
+                else weigh(std::true_type{});
                 tmem_st16(ts + 32 * grp, pk);  // over this warp's own scores of map 1, which are read
                 tmem_wait_st();
                 tc_fence_before();
