@@ -36,6 +36,7 @@ struct GatherArgs {
     const float *scales, *k_params;
     __nv_bfloat16 *k_out, *v_out;  // [n_rows][n_kv][D]
     int tile, heads;               // rows and heads of a CTA
+    bool wide;                     // both outputs are 32-byte aligned
     unsigned *err;
 };
 
@@ -56,6 +57,20 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16x4(uint32_t x, float s)
     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
     const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
     return make_uint2(bf16x2(f.x * s, f.y * s), bf16x2(h.x * s, h.y * s));
+}
+
+// 16 channels of an output row: one 32-byte store (a lane's channels are a whole sector, which two 16-byte
+// stores write in halves), or two where the caller's arrays are aligned to 16 bytes only.
+__device__ __forceinline__ void store_row(__nv_bfloat16 *p, const uint4 (&x)[2], bool wide)
+{
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0].x), "r"(x[0].y),
+                     "r"(x[0].z), "r"(x[0].w), "r"(x[1].x), "r"(x[1].y), "r"(x[1].z), "r"(x[1].w)
+                     : "memory");
+    } else {
+        *reinterpret_cast<uint4 *>(p) = x[0];
+        *reinterpret_cast<uint4 *>(p + 8) = x[1];
+    }
 }
 
 // 16 channels of one stored row, as they are read: 32, 16 or 8 bytes.
@@ -91,6 +106,28 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
     const int tid = threadIdx.x;
     const int64_t row0 = (int64_t)blockIdx.x * a.tile;
     const int n = (int)min((int64_t)a.tile, a.n_rows - row0);
+    const int h0 = blockIdx.y * a.heads;
+    const int hn = min(a.heads, a.n_kv - h0);
+    const int lanes = hn * LPR;               // threads of one output row
+    const int per = kGatherThreads / lanes;   // rows a step takes
+    const int sub = tid / lanes;
+    const bool works = sub < per;  // the threads past the last whole row only help to search
+    const int u = tid - sub * lanes;
+    const int g = works ? h0 + u / LPR : h0, c = 16 * (u % LPR);
+    [[maybe_unused]] float ks[16], kz[16];
+    [[maybe_unused]] float fk = 1.0f, fv = 1.0f;
+    if constexpr (KV == PKV_INT4) {
+        const float4 *p = reinterpret_cast<const float4 *>(a.k_params + (int64_t)g * D + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 s = __ldg(p + i), z = __ldg(p + (int64_t)a.n_kv * D / 4 + i);
+            ks[4 * i] = s.x; ks[4 * i + 1] = s.y; ks[4 * i + 2] = s.z; ks[4 * i + 3] = s.w;
+            kz[4 * i] = z.x; kz[4 * i + 1] = z.y; kz[4 * i + 2] = z.z; kz[4 * i + 3] = z.w;
+        }
+    } else if constexpr (KV == PKV_FP8_E4M3) {
+        fk = a.scales[g];
+        fv = a.scales[a.n_kv + g];
+    }
     if (tid < n) {
         const int32_t row = (int32_t)(row0 + tid);
         // the last sequence that begins at or before this row: empty ones before it begin there too
@@ -115,28 +152,8 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
         place[tid] = at;
     }
     __syncthreads();
+    if (!works) return;
 
-    const int h0 = blockIdx.y * a.heads;
-    const int hn = min(a.heads, a.n_kv - h0);
-    const int lanes = hn * LPR;               // threads of one output row
-    const int per = kGatherThreads / lanes;   // rows a step takes
-    const int sub = tid / lanes;
-    if (sub >= per) return;
-    const int u = tid - sub * lanes;
-    const int g = h0 + u / LPR, c = 16 * (u % LPR);
-    [[maybe_unused]] float ks[16], kz[16];
-    [[maybe_unused]] float fk = 1.0f, fv = 1.0f;
-    if constexpr (KV == PKV_INT4) {
-        const float *p = a.k_params + (int64_t)g * D + c;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            ks[i] = p[i];
-            kz[i] = p[(int64_t)a.n_kv * D + i];
-        }
-    } else if constexpr (KV == PKV_FP8_E4M3) {
-        fk = a.scales[g];
-        fv = a.scales[a.n_kv + g];
-    }
     for (int i0 = sub; i0 < n; i0 += UNROLL * per) {
         Raw<KV> k[UNROLL], v[UNROLL];
         [[maybe_unused]] float2 vp[UNROLL];
@@ -194,10 +211,8 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
                 }
             }
             const int64_t dst = ((row0 + i0 + x * per) * a.n_kv + g) * D + c;
-            *reinterpret_cast<uint4 *>(a.k_out + dst) = ko[0];
-            *reinterpret_cast<uint4 *>(a.k_out + dst + 8) = ko[1];
-            *reinterpret_cast<uint4 *>(a.v_out + dst) = vo[0];
-            *reinterpret_cast<uint4 *>(a.v_out + dst + 8) = vo[1];
+            store_row(a.k_out + dst, ko, a.wide);
+            store_row(a.v_out + dst, vo, a.wide);
         }
     }
 }
@@ -254,6 +269,7 @@ extern "C" pkv_status paged_kv_gather(pkv_pool *pool, const int32_t *out_indptr,
     a.k_params = pool->k_params;
     a.k_out = static_cast<__nv_bfloat16 *>(k_out);
     a.v_out = static_cast<__nv_bfloat16 *>(v_out);
+    a.wide = (((uintptr_t)k_out | (uintptr_t)v_out) & 31u) == 0;
     a.err = pool->err;
     a.heads = std::min(pool->n_kv, kMaxHeads);
     // Tile: one step of rows (as many as the CTA's threads hold at once) while that gives no more

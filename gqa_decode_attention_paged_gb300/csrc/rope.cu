@@ -60,11 +60,36 @@ struct RopeArgs {
     unsigned *err;
 };
 
-// 4-bit code of x: clamp(rint((x - z) / s), 0, 15), each step correctly rounded in fp32, NaN to 0.
-__device__ __forceinline__ uint32_t code4(float x, float s, float z)
+// 4-bit code of x: clamp(rint((x - z) / s), 0, 15), each step correctly rounded in fp32, NaN to 0.  `r` is
+// 1 / s to a few units of its last place: the product with it is off by less than 2^-17 where the code is
+// not clamped, so the correctly rounded quotient is needed only next to a border between two codes (or
+// where the product is not finite); everywhere else both round to the same code.
+__device__ __forceinline__ uint32_t code4(float x, float s, float z, float r)
 {
-    const float r = rintf(__fdiv_rn(__fsub_rn(x, z), s));
-    return r >= 0.0f ? (uint32_t)fminf(r, 15.0f) : 0u;
+    const float d = __fsub_rn(x, z);
+    float q = d * r, c = rintf(q);
+    if (!(fabsf(q - c) < 0.49998f)) c = rintf(__fdiv_rn(d, s));
+    return c >= 0.0f ? (uint32_t)fminf(c, 15.0f) : 0u;
+}
+
+__device__ __forceinline__ float rcp_approx(float s)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return r;
+}
+
+// Codes of 8 channels whose scales and zero points lie one after the other (16-byte aligned).
+__device__ __forceinline__ uint32_t key_codes(const float *x, const float *ks, const float *kz)
+{
+    const float4 s[2] = {__ldg(reinterpret_cast<const float4 *>(ks)), __ldg(reinterpret_cast<const float4 *>(ks) + 1)};
+    const float4 z[2] = {__ldg(reinterpret_cast<const float4 *>(kz)), __ldg(reinterpret_cast<const float4 *>(kz) + 1)};
+    const float sv[8] = {s[0].x, s[0].y, s[0].z, s[0].w, s[1].x, s[1].y, s[1].z, s[1].w};
+    const float zv[8] = {z[0].x, z[0].y, z[0].z, z[0].w, z[1].x, z[1].y, z[1].z, z[1].w};
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w |= code4(x[i], sv[i], zv[i], rcp_approx(sv[i])) << (4 * i);
+    return w;
 }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
@@ -133,19 +158,16 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_append_kernel(const __gr
     };
     const int step = a.splits * RPW;
     uint4 x0[kUnroll], x1[kUnroll];
-    auto fetch = [&](int row0) {
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int row = row0 + u * step;
-            if (row < rows) {
-                const __nv_bfloat16 *src = source(row);
-                x0[u] = *reinterpret_cast<const uint4 *>(src + 8 * c0);
-                x1[u] = *reinterpret_cast<const uint4 *>(src + 8 * c1);
-            }
+    auto fetch = [&](int u, int row) {
+        if (row < rows) {
+            const __nv_bfloat16 *src = source(row);
+            x0[u] = *reinterpret_cast<const uint4 *>(src + 8 * c0);
+            x1[u] = *reinterpret_cast<const uint4 *>(src + 8 * c1);
         }
     };
-    const int first = part * RPW + r;
-    fetch(first);  // in flight while the sines and cosines are computed
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+        fetch(u, part * RPW + r + u * step);  // in flight while the sines and cosines are computed
 
     // pairs 8 j .. 8 j + 7 are this lane's; lane r of the RPW lanes with the same j computes PPL of them
     float cs[8], sn[8];
@@ -191,10 +213,12 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_append_kernel(const __gr
             const int kvrow = row - a.n_q;  // < 0: a query; < n_kv: a key; else a value
             const bool is_v = kvrow >= a.n_kv;
             float y0[8], y1[8];
+            const uint4 r0 = x0[u], r1 = x1[u];
+            fetch(u, row + kUnroll * step);  // the place is free: the row kUnroll steps on
             if (live) {
                 float lo[8], hi[8];
-                widen(x0[u], lo);
-                widen(x1[u], hi);
+                widen(r0, lo);
+                widen(r1, hi);
                 if (!is_v && turns) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -262,28 +286,25 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_append_kernel(const __gr
                         float sc = __fmul_rn(__fsub_rn(mx, mn), 1.0f / 15.0f);
                         if (sc == 0.0f) sc = 1.0f;
                         const float z = __fadd_rn(mn, 0.0f);  // no negative zero
+                        const float rc = rcp_approx(sc);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            w0 |= code4(y0[i], sc, z) << (4 * i);
-                            w1 |= code4(y1[i], sc, z) << (4 * i);
+                            w0 |= code4(y0[i], sc, z, rc) << (4 * i);
+                            w1 |= code4(y1[i], sc, z, rc) << (4 * i);
                         }
                         if (j == 0)
                             *reinterpret_cast<float2 *>(entry + i4_params_offset(D) + off * 8) = make_float2(sc, z);
                         entry += i4_v_offset(D);
                     } else {
                         const float *ks = a.k_params + (int64_t)g * D, *kz = ks + (int64_t)a.n_kv * D;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            w0 |= code4(y0[i], ks[8 * c0 + i], kz[8 * c0 + i]) << (4 * i);
-                            w1 |= code4(y1[i], ks[8 * c1 + i], kz[8 * c1 + i]) << (4 * i);
-                        }
+                        w0 = key_codes(y0, ks + 8 * c0, kz + 8 * c0);
+                        w1 = key_codes(y1, ks + 8 * c1, kz + 8 * c1);
                     }
                     *reinterpret_cast<uint32_t *>(entry + off * (D / 2) + 4 * c0) = w0;
                     *reinterpret_cast<uint32_t *>(entry + off * (D / 2) + 4 * c1) = w1;
                 }
             }
         }
-        fetch(base + kUnroll * step + r);
     }
 }
 
