@@ -234,6 +234,12 @@ def _rows_ptr(pool, t, name, heads, rows):
     heads lie side by side (a slice of a wider row is fine)."""
     import torch
 
+    try:
+        if t.dtype is torch.bfloat16 and t.shape == (rows, heads, pool.d_head) and t.get_device() == pool.device \
+                and t.is_contiguous():
+            return t.data_ptr(), heads * pool.d_head
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.get_device() != pool.device:
@@ -457,7 +463,7 @@ def paged_rope_append(pool: Pool, rope: Rope, q, k_new, v_new, positions, slot_m
     Tokens may be slices of wider rows (a fused projection's output)."""
     import torch
 
-    T = int(slot_mapping.shape[0])
+    T = slot_mapping.shape[0]
     kp, ks = _rows_ptr(pool, k_new, "k_new", pool.n_kv, T)
     vp, vs = _rows_ptr(pool, v_new, "v_new", pool.n_kv, T)
     pp = _fast_ptr(pool, positions, "positions", torch.int32, (rope.n_axes, T))
@@ -465,7 +471,7 @@ def paged_rope_append(pool: Pool, rope: Rope, q, k_new, v_new, positions, slot_m
     qp = op = None
     qs = os_ = n_q = 0
     if q is not None:
-        n_q = int(q.shape[1]) if q.dim() == 3 else -1
+        n_q = q.shape[1] if q.dim() == 3 else -1
         qp, qs = _rows_ptr(pool, q, "q", n_q, T)
         if q_out is None:
             q_out = q.new_empty((T, n_q, pool.d_head))
@@ -502,7 +508,9 @@ def paged_kv_gather(pool: Pool, out_indptr, block_tables, starts=None, n_rows=No
         if n_rows is None:
             raise ValueError("give n_rows, or k_out and v_out")
         n = int(n_rows)
-        k_out, v_out = torch.empty((2, n, pool.n_kv, pool.d_head), dtype=torch.bfloat16, device=out_indptr.device)
+        shape, dev = (n, pool.n_kv, pool.d_head), out_indptr.device
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     else:
         n = int(k_out.shape[0])
         if n_rows is not None and n != int(n_rows):
