@@ -74,8 +74,11 @@ struct DGeo {
 template <int D, int G, int KV>
 struct DCfg {
     using Gm = DGeo<D, KV>;
-    // 96 KiB of stages per CTA, two CTAs per SM.
-    static constexpr int NW = KV == PKV_BF16 && D == 128 ? 3 : 4;
+    // 96 KiB of stages per CTA, two CTAs per SM.  bf16 at d_head 128 (16 KiB a stage): two warps with three
+    // stages each; three with two read long contexts of 8 heads a KV head slower (16 x 32768 tokens: 328
+    // against 347 us; one sequence of 32768: 41 against 47) and 64 x 1024..2048 tokens no faster (72 us).
+    // E4M3 (8 KiB): four with three (256 sequences of 16..4096: 188 us; six with two 195, three with four 191).
+    static constexpr int NW = KV == PKV_BF16 && D == 128 ? 2 : 4;
     static constexpr int kThreads = NW * 32;
     static constexpr int kStages = std::min(8, 96 * 1024 / (NW * Gm::STAGE));
     static constexpr int kRing = NW * kStages * Gm::STAGE;
@@ -620,8 +623,10 @@ __global__ void __launch_bounds__(kDiffMergeWarps * 32, 2) diff_merge_kernel(con
 // Launches
 // ---------------------------------------------------------------------------
 
-constexpr int kMergeResident = 4;  // merge CTAs per SM
-constexpr int kDiffMinBlocks = 4;  // blocks a warp should have before another is used
+constexpr int kMergeResident = 2;  // merge CTAs per SM (4: 72.1 us at 64 x 1024..2048 tokens, 2: 71.8)
+// Blocks a warp should have before another is used.  One: a short sequence is bound by the chain of its warps
+// (300 tokens: 10.3 us; with 2 blocks 11.1, with 4 12.2).
+constexpr int kDiffMinBlocks = 1;
 
 constexpr int kMaxDevices = 64;
 
