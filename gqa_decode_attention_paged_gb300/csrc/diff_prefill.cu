@@ -49,6 +49,13 @@
 //   * value rows behind the sequence's end (a page that ends inside a tile)
 //     are zeroed in shared memory before their product: a weight of 0 does not
 //     cancel what is not finite.
+//   * few rows (kSums, kWeights): when the call's tiles would leave most SMs
+//     idle (a few drafted tokens on long caches), the keys of a tile are cut
+//     into ranges, one CTA each, and the sweeps become two launches: the first
+//     leaves (m, l) of both maps per row and range, the second merges them (so
+//     its weights are the final ones) and leaves its range's part of o, and a
+//     third adds the parts in order -- plain sums, since all share the row's
+//     scaling -- and applies the norm.
 // Every mbarrier wait is bounded; on a timeout the CTA records
 // PKV_DEVERR_TIMEOUT, every role stops, the MMA and copy pipes are drained
 // (bounded) and the tensor memory is released before the CTA exits.
@@ -93,7 +100,15 @@ struct Args {
     DiffWeights w;
     __nv_bfloat16 *out;   // [n_rows][n_q / 2][2 D]
     unsigned *err;
+    // ranges of keys (kSums, kWeights): how many of a tile, and per (tile, range) and row (m, l) of both
+    // maps and the range's part of o, [tile][range][kRows] and [tile][range][kRows][2 D]
+    int ranges;
+    float4 *ws_stat;
+    float *ws_o;
 };
+
+// What a launch does: both sweeps on pairs of tiles, or one of them on ranges of a tile's keys.
+enum Mode { kWhole = 0, kSums = 1, kWeights = 2 };
 
 template <int D>
 struct Layout {
@@ -201,19 +216,25 @@ struct Tile {
     int b, p, rt0;  // sequence, pair, this CTA's first local row (past R: no rows, it helps to copy)
     int R;          // rows of (b, p): T * G
     int row0, T, C; // first query token row of b, chunk length, context length (clamped)
-    int n_blocks, n_steps;
+    int n_blocks, n_steps;  // blocks the tile sees; steps of this CTA's range
+    int s0;                 // its first step
+    int slot;               // (tile, range) in the workspace
     bool bad_ctx;
 };
 
-// A window of 32 sequences, one per lane: each warp walks the tile list itself
-// (sequence, then pair, then row tile), with the same arithmetic.
+// A window of 32 sequences, one per lane: each warp walks the list itself
+// (sequence, then pair, then row tile), with the same arithmetic.  The list's
+// entries are pairs of tiles (kWhole) or ranges of a tile.
 struct Walker {
-    int wb = 0, wbase = 0;           // the window's first sequence, tile pairs before it
+    int wb = 0, wbase = 0;           // the window's first sequence, entries before it
     int incl = 0, tot = 0;
-    int nt = 0, row0 = 0, T = 0, C = 0;  // this lane's sequence: tile pairs per KV pair, rows, context
+    int nt = 0, row0 = 0, T = 0, C = 0;  // this lane's sequence: (pairs of) tiles per KV pair, rows, context
 };
 
-template <int G>
+// Steps [range_first(k), range_first(k + 1)) of a tile's S are range k's.
+__device__ __forceinline__ int range_first(int S, int ranges, int k) { return (int)((int64_t)S * k / ranges); }
+
+template <int G, int MODE>
 __device__ __forceinline__ void load_window(Walker &w, const Args &a, int lane)
 {
     const int bl = w.wb + lane;
@@ -226,7 +247,8 @@ __device__ __forceinline__ void load_window(Walker &w, const Args &a, int lane)
             w.row0 = lo;
             w.T = hi - lo;
             w.C = a.context_lens[bl];
-            w.nt = (w.T * G + 2 * kRows - 1) / (2 * kRows);
+            constexpr int per = MODE == kWhole ? 2 * kRows : kRows;
+            w.nt = (w.T * G + per - 1) / per;
         }
     }
     int x = w.nt * a.n_pairs;
@@ -239,15 +261,17 @@ __device__ __forceinline__ void load_window(Walker &w, const Args &a, int lane)
     w.tot = __shfl_sync(kFull, x, 31);
 }
 
-// Tile pair x of the list, and in it CTA `rank`'s tile; false past its end.  Warp-wide, uniform result.
-template <int G>
-__device__ __forceinline__ bool find_tile(Walker &w, const Args &a, int x, int rank, Tile &t, int lane)
+// Entry e of the list: CTA `rank`'s tile of the pair, or a range of a tile; false past its end.  Warp-wide,
+// uniform result.
+template <int G, int MODE>
+__device__ __forceinline__ bool find_tile(Walker &w, const Args &a, int e, int rank, Tile &t, int lane)
 {
+    const int x = MODE == kWhole ? e : e / a.ranges;
     while (x >= w.wbase + w.tot) {
         if (w.wb + 32 >= a.batch) return false;
         w.wbase += w.tot;
         w.wb += 32;
-        load_window<G>(w, a, lane);
+        load_window<G, MODE>(w, a, lane);
     }
     const unsigned hit = __ballot_sync(kFull, w.wbase + w.incl > x);
     const int l = __ffs(hit) - 1;
@@ -259,8 +283,10 @@ __device__ __forceinline__ bool find_tile(Walker &w, const Args &a, int x, int r
     int C = __shfl_sync(kFull, w.C, l);
     const int within = x - w.wbase - before;
     t.p = within / nt;
-    const int pair0 = (within - t.p * nt) * 2 * kRows;
-    t.rt0 = pair0 + rank * kRows;
+    const int pair0 = (within - t.p * nt) * (MODE == kWhole ? 2 : 1) * kRows;
+    t.rt0 = pair0 + (MODE == kWhole ? rank * kRows : 0);
+    t.s0 = 0;
+    t.slot = e;
     t.R = t.T * G;
     const int cap = a.W * kBlockSize;
     t.bad_ctx = C < t.T || C > cap;
@@ -270,21 +296,73 @@ __device__ __forceinline__ bool find_tile(Walker &w, const Args &a, int x, int r
         t.n_blocks = t.n_steps = 0;
         return true;
     }
-    const int last_row = min(t.R, pair0 + 2 * kRows) - 1;  // the pair walks the same keys
+    const int last_row = min(t.R, pair0 + (MODE == kWhole ? 2 : 1) * kRows) - 1;  // a pair walks the same keys
     t.n_blocks = (C - t.T + last_row / G) / kBlockSize + 1;
     t.n_steps = (t.n_blocks + kStepBlocks - 1) / kStepBlocks;
+    if constexpr (MODE != kWhole) {
+        const int k = e - x * a.ranges;
+        t.s0 = range_first(t.n_steps, a.ranges, k);
+        t.n_steps = range_first(t.n_steps, a.ranges, k + 1) - t.s0;
+    }
     return true;
 }
 
-// The V unit (of the tile's 2 n_steps) in which the sequence ends inside a block, or -1.
+// The V unit (of this CTA's 2 n_steps) in which the sequence ends inside a block, or -1.
 __device__ __forceinline__ int end_unit(const Tile &t)
 {
-    return t.C % kBlockSize && t.C / kBlockSize < t.n_blocks ? t.C / kBlockSize / kUnitBlocks : -1;
+    if (t.C % kBlockSize == 0 || t.C / kBlockSize >= t.n_blocks) return -1;
+    const int v = t.C / kBlockSize / kUnitBlocks - 2 * t.s0;
+    return v >= 0 && v < 2 * t.n_steps ? v : -1;
+}
+
+// ------------------------------------------------------------- statistics of a row
+
+// (m, l) of both maps, gathered from parts; a part without visible keys has m = -inf, l = 0.
+struct RowStat {
+    float m1 = -INFINITY, l1 = 0.0f, m2 = -INFINITY, l2 = 0.0f;
+    static __device__ __forceinline__ void join(float &m, float &l, float pm, float pl)
+    {
+        const float top = fmaxf(m, pm);
+        const float a = m == -INFINITY ? l : l * ex2(m - top), b = pm == -INFINITY ? pl : pl * ex2(pm - top);
+        l = a + b;
+        m = top;
+    }
+    __device__ __forceinline__ void add(float pm1, float pl1, float pm2, float pl2)
+    {
+        join(m1, l1, pm1, pl1);
+        join(m2, l2, pm2, pl2);
+    }
+    // Weights 2^(s + n0) and 2^(s + n1) of the two maps' scores in log2 units, and o = inv * their sums.
+    __device__ __forceinline__ void factors(float abs_lam, float &n0, float &n1, float &inv) const
+    {
+        if (l1 == 0.0f) {  // a row none of whose blocks could be read stays all zero
+            n0 = n1 = inv = 0.0f;
+            return;
+        }
+        const float c = abs_lam * l1 / l2;  // c2 / c1
+        n0 = log2f(c <= 1.0f ? 1.0f : 1.0f / c) + kBoost - m1;
+        n1 = log2f(c <= 1.0f ? c : 1.0f) + kBoost - m2;
+        inv = (c <= 1.0f ? 1.0f / l1 : abs_lam / l2) * (1.0f / 256.0f);
+    }
+};
+
+// A row's statistics over all ranges of its tile (`slot` is one of them).
+__device__ __forceinline__ RowStat merged_stats(const Args &a, const Tile &t, int row, bool live)
+{
+    RowStat rs;
+    const int S = (t.n_blocks + kStepBlocks - 1) / kStepBlocks;
+    const int first = t.slot / a.ranges * a.ranges;
+    for (int k = 0; k < a.ranges && live; ++k) {
+        if (range_first(S, a.ranges, k) == range_first(S, a.ranges, k + 1)) continue;  // an empty range wrote nothing
+        const float4 v = __ldcg(a.ws_stat + (int64_t)(first + k) * kRows + row);
+        rs.add(v.x, v.y, v.z, v.w);
+    }
+    return rs;
 }
 
 // ------------------------------------------------------------- the kernel
 
-template <int D, int G, bool F8>
+template <int D, int G, bool F8, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     diff_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
                         const __grid_constant__ Args a)
@@ -302,8 +380,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::kAbort);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(kFull, tid >> 5, 0);  // the same in all lanes, and known to be
-    const int rank = (int)cluster_rank();
+    constexpr bool kPair = MODE == kWhole;  // clusters of two
+    constexpr bool kFirst = MODE != kWeights, kSecond = MODE != kSums;
+    const int rank = kPair ? (int)cluster_rank() : 0;
     constexpr uint16_t kBoth = 3;
+    const int e0 = (int)(kPair ? blockIdx.x / 2 : blockIdx.x), stride = (int)(kPair ? gridDim.x / 2 : gridDim.x);
 
     if (tid == 0) {
         prefetch_tensormap(&tm_q);
@@ -315,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i >= L::QUAD && i < L::QUAD + 4) n = 4;  // the four warps of a lane quarter
             if (i == L::Q_FULL && F8) n = kSoftmaxWarps;  // each widens its share of the queries
             if (i >= L::FULL && i < L::EMPTY && kSplit) n = 2;
-            if (i >= L::EMPTY && i < L::EMPTY + NS) n = 2;  // both CTAs have used the slot
+            if (i >= L::EMPTY && i < L::EMPTY + NS && kPair) n = 2;  // both CTAs have used the slot
             mbar_init(&bar[i], n);
         }
         *abort_flag = 0;
@@ -330,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();  // both CTAs' barriers are ready
+    if constexpr (kPair) cluster_sync();  // both CTAs' barriers are ready
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + L::kTmemSlot);
     griddep_wait();
@@ -346,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         reinterpret_cast<float *>(sm + L::kNorm)[i] = a.w.norm_weight ? a.w.norm_weight[i] : 1.0f;
     __syncthreads();
     Walker wk;
-    load_window<G>(wk, a, lane);
+    load_window<G, MODE>(wk, a, lane);
     const uint32_t base = smem_u32(sm);
 
     if (warp == kCopyWarp) {
@@ -370,9 +451,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++u;
             return true;
         };
-        for (int x = blockIdx.x / 2; ok; x += gridDim.x / 2) {
+        for (int x = e0; ok; x += stride) {
             Tile t;
-            if (!find_tile<G>(wk, a, x, rank, t, lane)) break;
+            if (!find_tile<G, MODE>(wk, a, x, rank, t, lane)) break;
             if (t.n_steps == 0) continue;
             if (*abort_flag) break;
             if (n > 0 && !(ok = wait_all(&bar[L::Q_FREE], (n - 1) & 1))) break;
@@ -390,27 +471,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t *trow = a.block_tables + (int64_t)t.b * a.W;
             // lane k < 8: the entry rows of block k's pair of step s, or rows past the pool (zero filled)
             auto rows_of = [&](int s, bool flag) -> int {
-                const int nb = s * kStepBlocks + lane;
+                const int nb = (t.s0 + s) * kStepBlocks + lane;
                 const bool present = lane < kStepBlocks && nb < t.n_blocks;
                 const int id = present ? trow[nb] : -1;
                 const bool valid = id >= 0 && id < a.num_blocks;
                 if (present && !valid && flag) atomicOr(a.err, PKV_DEVERR_BLOCK_RANGE);
                 return valid ? (int)((id * (int64_t)a.n_kv + 2 * t.p) * 2 * kBlockSize) : a.oob_row;
             };
+            auto copy_box = [&](uint32_t to, int c, int y, uint32_t land) {
+                if constexpr (kPair) tma_load_2d_multicast_if(go, to, &tm_kv, c, y, land, kBoth, policy);
+                else tma_load_2d_if(go, to, &tm_kv, c, y, land, policy);
+            };
+            constexpr int kShare = kPair ? 2 : 1;  // this CTA's blocks of a unit: every kShare-th
             auto copy_k = [&](int y0, int m) -> bool {
                 uint32_t land, dst;
                 if (!open(land, dst)) return false;
 #pragma unroll
-                for (int i = 0; i < kStepBlocks / 2; ++i) {  // this CTA's blocks, into both CTAs
-                    const int k = 2 * i + rank;
+                for (int i = 0; i < kStepBlocks / kShare; ++i) {
+                    const int k = kShare * i + rank;
                     const int yk = __shfl_sync(kFull, y0, k);
                     const int y = yk == a.oob_row ? yk : yk + m * 2 * kBlockSize;
                     if constexpr (F8) {
-                        tma_load_2d_multicast_if(go, dst + L::UT / 2 + k * (kBlockSize * D), &tm_kv, 0, y, land, kBoth, policy);
+                        copy_box(dst + L::UT / 2 + k * (kBlockSize * D), 0, y, land);
                     } else {
 #pragma unroll
                         for (int h = 0; h < NH; ++h)
-                            tma_load_2d_multicast_if(go, dst + h * kKHalf + k * (kBlockSize * 128), &tm_kv, 64 * h, y, land, kBoth, policy);
+                            copy_box(dst + h * kKHalf + k * (kBlockSize * 128), 64 * h, y, land);
                     }
                 }
                 return true;
@@ -419,31 +505,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t land, dst;
                 if (!open(land, dst)) return false;
 #pragma unroll
-                for (int i = 0; i < kUnitBlocks / 2; ++i) {
-                    const int k = 2 * i + rank;
+                for (int i = 0; i < kUnitBlocks / kShare; ++i) {
+                    const int k = kShare * i + rank;
                     const int yk = __shfl_sync(kFull, y0, h * kUnitBlocks + k);
 #pragma unroll
                     for (int head = 0; head < 2; ++head) {
                         const int y = yk == a.oob_row ? yk : yk + head * 2 * kBlockSize + kBlockSize;
                         const uint32_t to = dst + head * NH * kVChunk;
                         if constexpr (F8) {
-                            tma_load_2d_multicast_if(go, to + kVKeys * D + k * (kBlockSize * D), &tm_kv, 0, y, land, kBoth, policy);
+                            copy_box(to + kVKeys * D + k * (kBlockSize * D), 0, y, land);
                         } else {
 #pragma unroll
                             for (int c = 0; c < NH; ++c)
-                                tma_load_2d_multicast_if(go, to + c * kVChunk + k * (kBlockSize * 128), &tm_kv, 64 * c, y, land, kBoth, policy);
+                                copy_box(to + c * kVChunk + k * (kBlockSize * 128), 64 * c, y, land);
                         }
                     }
                 }
                 return true;
             };
-            int nxt = rows_of(0, true);
-            for (int s = 0; s < t.n_steps && ok; ++s) {
+            int nxt = kFirst ? rows_of(0, true) : 0;
+            for (int s = 0; kFirst && s < t.n_steps && ok; ++s) {
                 const int y0 = nxt;
                 if (s + 1 < t.n_steps) nxt = rows_of(s + 1, true);
                 ok = copy_k(y0, 0) && copy_k(y0, 1);
             }
-            if (!ok) break;
+            if (!ok || !kSecond) continue;
             int y0 = rows_of(0, false);
             ok = copy_k(y0, 1) && copy_k(y0, 0);
             for (int s = 0; s < t.n_steps && ok; ++s) {  // in the order of the MMAs
@@ -464,16 +550,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= kPrepWarp) {
         // ---------------------------------------------------------- units made ready
         const int which = warp - kPrepWarp;
-        if (F8 || which == 0) {
+        // units of a tile: 2 a step in the first sweep, 4 in the second
+        auto first_units = [&](const Tile &t) -> int { return kFirst ? 2 * t.n_steps : 0; };
+        if (F8 || (which == 0 && kSecond)) {
             int u = 0, ends = 0;
             bool ok = true;
-            for (int x = blockIdx.x / 2; ok; x += gridDim.x / 2) {
+            for (int x = e0; ok; x += stride) {
                 Tile t;
-                if (!find_tile<G>(wk, a, x, rank, t, lane)) break;
+                if (!find_tile<G, MODE>(wk, a, x, rank, t, lane)) break;
                 if (t.n_steps == 0) continue;
                 if (*abort_flag) break;
                 // the V unit the sequence ends inside of: zero the rows behind the end (value heads h0 ..)
-                const int end = end_unit(t);
+                const int end = kSecond ? end_unit(t) : -1;
                 auto clear = [&](uint32_t unit, int h0, int heads) {
                     const int r0 = (t.C / kBlockSize % kUnitBlocks) * kBlockSize;
                     const int first = r0 + t.C % kBlockSize, rows = r0 + kBlockSize - first;
@@ -485,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (!F8) {  // the MMA warp asks when the unit has landed
                     if (end >= 0) {
                         const int vs = end / 2, S = t.n_steps;
-                        const int v = u + 2 * S + 2 + 4 * vs + (end & 1) * (vs == S - 1 ? 1 : 3);
+                        const int v = u + first_units(t) + 2 + 4 * vs + (end & 1) * (vs == S - 1 ? 1 : 3);
                         if (!(ok = wait_all(&bar[L::END_ASK], ends & 1))) break;
                         ++ends;
                         clear(base + L::kRing + v % NS * L::UT, 0, 2);
@@ -493,15 +581,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bar[L::END_CLEAR]);
                     }
-                    u += 6 * t.n_steps;
+                    u += first_units(t) + 4 * t.n_steps;
                 } else {
-                    for (int i = 0; i < 6 * t.n_steps; ++i, ++u) {
+                    const int units = first_units(t) + (kSecond ? 4 * t.n_steps : 0);
+                    for (int i = 0; i < units; ++i, ++u) {
                         const int st = u % NS;
                         if (!kSplit && (u & 1) != which) continue;
                         if (!(ok = wait_all(&bar[L::RAW + st], (u / NS) & 1))) break;
                         // second sweep: K, K of the first step, then of each step V, K, K, V (the next step's
                         // keys; the last step has V, V)
-                        const int iv = i - 2 * t.n_steps - 2;
+                        const int iv = i - first_units(t) - 2;
                         const int vs = iv >> 2, vp = iv & 3;
                         const bool tail = vs == t.n_steps - 1;
                         const bool is_v = iv >= 0 && (tail || vp == 0 || vp == 3);
@@ -534,6 +623,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t go = elect_one();
         const uint32_t tm = __shfl_sync(kFull, tmem, 0);
         auto unit = [&](int v) -> bool { return wait_all(&bar[L::FULL + v % NS], (v / NS) & 1); };
+        // ring unit v has been used when the MMAs so far have run
+        auto release = [&](int v) {
+            if constexpr (kPair) umma_commit_multicast_if(go, &bar[L::EMPTY + v % NS], kBoth);
+            else umma_commit_if(go, &bar[L::EMPTY + v % NS]);
+        };
         // keys [64 part, 64 part + N) of ring unit v against map m's queries
         auto scores = [&](int m, int v, int part, uint32_t idesc) {
             tc_fence_after();
@@ -544,9 +638,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 umma_if(go, tm + m * kKeys + part * 64, qm + off, km + off, idesc, kk > 0 ? 1u : 0u);
             }
         };
-        for (int x = blockIdx.x / 2; ok; x += gridDim.x / 2) {
+        for (int x = e0; ok; x += stride) {
             Tile t;
-            if (!find_tile<G>(wk, a, x, rank, t, lane)) break;
+            if (!find_tile<G, MODE>(wk, a, x, rank, t, lane)) break;
             if (t.n_steps == 0) continue;
             if (*abort_flag) break;
             {
@@ -554,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int end = end_unit(t);
                 auto first_sweep = [&](int s, int m) -> bool {
                     // S_m is free: its last scores are in registers, and the weights over S_1 have been used
-                    if (s > 0) {
+                    if (s > 0 || (!kSecond && n > 0)) {
                         if (!wait_all(&bar[L::ST_READ + m], (reads - 1) & 1)) return false;
                     } else if (n > 0) {
                         if (m == 0 && !(wait_all(&bar[L::PV_DONE], (steps - 1) & 1) &&
@@ -565,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!unit(u)) return false;
                     scores(m, u, 0, idesc_qk);
                     umma_commit_if(go, &bar[L::ST_FULL + m]);
-                    umma_commit_multicast_if(go, &bar[L::EMPTY + u++ % NS], kBoth);
+                    release(u++);
                     return true;
                 };
                 auto product = [&](int s, int h) -> bool {
@@ -584,26 +678,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kk = 0; kk < kVKeys / 16; ++kk)
                         umma_ts_if(go, tm + kColO, tm + h * kVKeys + (kk >> 1) * 32 + (kk & 1) * 8, vm + ((kk * 2048) >> 4),
                                 idesc_pv, (s > 0 || h > 0 || kk > 0) ? 1u : 0u);
-                    umma_commit_multicast_if(go, &bar[L::EMPTY + v % NS], kBoth);
+                    release(v);
                     umma_commit_if(go, &bar[L::PV_DONE + h]);
                     return true;
                 };
                 ok = wait_all(&bar[L::Q_FULL], n & 1);
-                for (int s = 0; s < S && ok; ++s, ++reads) ok = first_sweep(s, 0) && first_sweep(s, 1);
+                for (int s = 0; kFirst && s < S && ok; ++s, ++reads) ok = first_sweep(s, 0) && first_sweep(s, 1);
+                if constexpr (!kSecond) {
+                    umma_commit_if(go, &bar[L::Q_FREE]);
+                    ++n;
+                    continue;
+                }
                 // second sweep: the first step's scores
-                ok = ok && wait_all(&bar[L::ST_READ + 1], (reads - 1) & 1) && unit(u);
+                if constexpr (kFirst) ok = ok && wait_all(&bar[L::ST_READ + 1], (reads - 1) & 1);
+                else if (n > 0) ok = ok && wait_all(&bar[L::S2_READ], (steps - 1) & 1);
+                ok = ok && unit(u);
                 if (ok) {
                     scores(1, u, 0, idesc_qk);
                     umma_commit_if(go, &bar[L::S2_FULL]);
-                    umma_commit_multicast_if(go, &bar[L::EMPTY + u++ % NS], kBoth);
-                    ok = wait_all(&bar[L::ST_READ], (reads - 1) & 1) && unit(u);
+                    release(u++);
+                    if constexpr (kFirst) ok = wait_all(&bar[L::ST_READ], (reads - 1) & 1);
+                    else if (n > 0)
+                        ok = wait_all(&bar[L::PV_DONE], (steps - 1) & 1) && wait_all(&bar[L::PV_DONE + 1], (steps - 1) & 1);
+                    ok = ok && unit(u);
                 }
                 if (ok) {
                     scores(0, u, 0, idesc_half);
                     umma_commit_if(go, &bar[L::S1_FULL]);
                     scores(0, u, 1, idesc_half);
                     umma_commit_if(go, &bar[L::S1_FULL + 1]);
-                    umma_commit_multicast_if(go, &bar[L::EMPTY + u++ % NS], kBoth);
+                    release(u++);
                     if (n > 0) ok = wait_all(&bar[L::O_FREE], (n - 1) & 1);
                 }
                 for (int s = 0; s < S && ok; ++s, ++steps) {
@@ -614,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!(ok = wait_all(&bar[L::S2_READ], steps & 1) && unit(u))) break;
                         scores(1, u, 0, idesc_qk);
                         umma_commit_if(go, &bar[L::S2_FULL]);
-                        umma_commit_multicast_if(go, &bar[L::EMPTY + u++ % NS], kBoth);
+                        release(u++);
                         k1 = u++;
                         if (!(ok = wait_all(&bar[L::PV_DONE], steps & 1) && unit(k1))) break;
                         scores(0, k1, 0, idesc_half);
@@ -627,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!(ok = wait_all(&bar[L::PV_DONE + 1], steps & 1))) break;
                         scores(0, k1, 1, idesc_half);
                         umma_commit_if(go, &bar[L::S1_FULL + 1]);
-                        umma_commit_multicast_if(go, &bar[L::EMPTY + k1 % NS], kBoth);
+                        release(k1);
                     } else {
                         umma_commit_if(go, &bar[L::O_FULL]);
                     }
@@ -666,17 +770,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // the next tile that has keys, and this lane's block id of its first step, are found while the tensor
         // cores finish the tile before
-        int x = blockIdx.x / 2;
+        int x = e0;
         Tile tn;
         int first_id = -1;
         auto find_next = [&]() -> bool {
-            for (;; x += gridDim.x / 2) {
-                if (!find_tile<G>(wk, a, x, rank, tn, lane)) return false;
+            for (;; x += stride) {
+                if (!find_tile<G, MODE>(wk, a, x, rank, tn, lane)) return false;
                 if (tn.bad_ctx && tid == 0 && tn.rt0 == 0 && tn.p == 0) atomicOr(a.err, PKV_DEVERR_CTX_RANGE);
                 if (tn.n_steps > 0) break;
             }
-            x += gridDim.x / 2;
-            first_id = lane < kStepBlocks && lane < tn.n_blocks ? a.block_tables[(int64_t)tn.b * a.W + lane] : -1;
+            x += stride;
+            const int nb = tn.s0 * kStepBlocks + lane;
+            first_id = lane < kStepBlocks && nb < tn.n_blocks ? a.block_tables[(int64_t)tn.b * a.W + nb] : -1;
             return true;
         };
         bool have = find_next();
@@ -698,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float qs = m == 0 ? qs0 : qs1;
             const int32_t *trow = a.block_tables + (int64_t)t.b * a.W;
             auto ids_of = [&](int s) -> int {
-                const int nb = s * kStepBlocks + lane;
+                const int nb = (t.s0 + s) * kStepBlocks + lane;
                 return lane < kStepBlocks && nb < t.n_blocks ? trow[nb] : -1;
             };
             // valid blocks of a step, as the copies decided
@@ -706,9 +811,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return __ballot_sync(kFull, lane < kStepBlocks && id >= 0 && id < a.num_blocks);
             };
             // ---- first sweep: maximum and sum of map m over this half's keys ----
-            float mx = -INFINITY, l = 0.0f;
+            [[maybe_unused]] float mx = -INFINITY, l = 0.0f;
             int nxt = id0;
-            for (int s = 0; s < t.n_steps; ++s, ++gs) {
+            for (int s = 0; kFirst && s < t.n_steps; ++s, ++gs) {
                 const uint32_t mask = mask_of(nxt) >> (4 * half);
                 if (s + 1 < t.n_steps) nxt = ids_of(s + 1);
                 if (!(ok = wait_all(&bar[L::ST_FULL + m], gs & 1))) break;
@@ -723,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {  // 32 keys at a time
                     uint32_t *sr = both + 32 * c;
-                    const int key0 = s * kKeys + 64 * half + 32 * c;
+                    const int key0 = (t.s0 + s) * kKeys + 64 * half + 32 * c;
                     const uint32_t mh = (mask >> (2 * c)) & 3u;
                     if (!__all_sync(kFull, mh == 3u && key0 + 31 <= pos)) {  // what this row does not see never has the largest score
                         const uint32_t never = rising ? 0xff800000u : 0x7f800000u;
@@ -764,8 +869,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             // ---- the row's statistics of both maps give the weights' factors ----
-            float l1, l2, n0 = 0.0f, n1 = 0.0f, inv = 0.0f;  // weights 2^(s qs + n); o = inv * accumulator
-            {
+            float n0 = 0.0f, n1 = 0.0f, inv = 0.0f;  // weights 2^(s qs + n); o = inv * accumulator
+            RowStat rs;
+            if constexpr (kFirst) {
                 uint32_t st[8] = {__float_as_uint(mx), __float_as_uint(l)};
                 tmem_st2(ts + kColStat + 2 * grp, st);
                 tmem_wait_st();
@@ -773,23 +879,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld8(ts + kColStat, st);  // (m, l) of threads 0 .. 3: map 1, map 2, map 1, map 2
                 tmem_wait_ld();
                 auto f = [&](int i) { return __uint_as_float(st[i]); };
-                const float m1 = fmaxf(f(0), f(4)), m2 = fmaxf(f(2), f(6));
-                auto part = [&](int i, float top) { return f(i) == -INFINITY ? f(i + 1) : f(i + 1) * ex2(f(i) - top); };
-                l1 = part(0, m1) + part(4, m1);
-                l2 = part(2, m2) + part(6, m2);
-                if (!(l1 == 0.0f)) {  // (a row none of whose blocks could be read stays all zero)
-                    const float c = abs_lam * l1 / l2;  // c2 / c1
-                    n0 = log2f(c <= 1.0f ? 1.0f : 1.0f / c) + kBoost - m1;
-                    n1 = log2f(c <= 1.0f ? c : 1.0f) + kBoost - m2;
-                    inv = (c <= 1.0f ? 1.0f / l1 : abs_lam / l2) * (1.0f / 256.0f);
-                }
+                rs.add(f(0), f(1), f(2), f(3));
+                rs.add(f(4), f(5), f(6), f(7));
             }
+            if constexpr (!kSecond) {  // the range's statistics, for the launch that forms the weights
+                if (grp == 0 && r < t.R) a.ws_stat[(int64_t)t.slot * kRows + row] = make_float4(rs.m1, rs.l1, rs.m2, rs.l2);
+                have = find_next();
+                if (!(ok = meet())) break;  // the four threads have read the columns before the next tile's are written
+                ++n;
+                continue;
+            }
+            if constexpr (!kFirst) rs = merged_stats(a, t, row, r < t.R);
+            rs.factors(abs_lam, n0, n1, inv);
             // ---- second sweep: the weights of keys 32 grp .. + 31 of every step ----
             nxt = id0;
             for (int s = 0; s < t.n_steps; ++s, ++ps) {
                 const uint32_t mh = (mask_of(nxt) >> (2 * grp)) & 3u;
                 if (s + 1 < t.n_steps) nxt = ids_of(s + 1);
-                const int key0 = s * kKeys + 32 * grp;
+                const int key0 = (t.s0 + s) * kKeys + 32 * grp;
                 const bool all = __all_sync(kFull, mh == 3u && key0 + 31 <= pos);
                 if (!(ok = wait_all(&bar[L::S2_FULL], ps & 1))) break;
                 if (!(ok = wait_all(&bar[L::S1_FULL + half], ps & 1))) break;
@@ -832,6 +939,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             have = find_next();
             if (!(ok = wait_all(&bar[L::O_FULL], n & 1))) break;
             tc_fence_after();
+            if constexpr (!kFirst) {  // the range's part of o
+                const float vs = F8 ? a.scales[a.n_kv + 2 * t.p + half] : 1.0f;
+                float *dst = a.ws_o + ((int64_t)t.slot * kRows + row) * (2 * D) + grp * QD;
+#pragma unroll
+                for (int c = 0; c < QD; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(to + c, o);
+                    tmem_wait_ld();
+                    if (r < t.R) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * vs);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) stg256(dst + c + i, o + i);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[L::O_FREE]);
+                ++n;
+                continue;
+            }
             const float f = inv * (F8 ? a.scales[a.n_kv + 2 * t.p + half] : 1.0f);
             uint32_t o[QD];
 #pragma unroll
@@ -887,16 +1015,81 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     tc_fence_before();
     __syncthreads();  // every role is done with the tensor memory
-    cluster_sync();   // the other CTA's last commits and copies have reached this one
+    if constexpr (kPair) cluster_sync();  // the other CTA's last commits and copies have reached this one
     tc_fence_after();
     if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
+// ------------------------------------------------------------- ranges joined
+
+constexpr int kJoinWarps = 8;
+
+// One warp per row of a tile: the ranges' parts of o added in order, normalised and stored.
+template <int D, int G>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ Args a)
+{
+    constexpr int KW = 2 * D / 128;  // 16-byte pieces of a row that a lane holds
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    griddep_wait();
+    griddep_launch_dependents();
+    const float abs_lam = fabsf(diff_lambda<D>(a.w, lane));
+    Walker wk;
+    load_window<G, kWeights>(wk, a, lane);
+    for (int x = blockIdx.x;; x += gridDim.x) {
+        Tile t;
+        if (!find_tile<G, kWeights>(wk, a, x * a.ranges, 0, t, lane)) break;
+        if (t.n_blocks == 0) continue;
+        const int S = (t.n_blocks + kStepBlocks - 1) / kStepBlocks;
+        // rows of this tile, dealt to the CTAs of its column of the grid
+        for (int row = blockIdx.y * kJoinWarps + warp; row < min(kRows, t.R - t.rt0); row += gridDim.y * kJoinWarps) {
+            float4 o[KW];
+#pragma unroll
+            for (int c = 0; c < KW; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < a.ranges; ++k) {
+                if (range_first(S, a.ranges, k) == range_first(S, a.ranges, k + 1)) continue;
+                const float4 *src = reinterpret_cast<const float4 *>(a.ws_o + ((int64_t)(t.slot + k) * kRows + row) * (2 * D));
+#pragma unroll
+                for (int c = 0; c < KW; ++c) {
+                    const float4 v = __ldcg(src + lane + 32 * c);
+                    o[c].x += v.x;
+                    o[c].y += v.y;
+                    o[c].z += v.z;
+                    o[c].w += v.w;
+                }
+            }
+            float n0, n1, inv;
+            merged_stats(a, t, row, true).factors(abs_lam, n0, n1, inv);
+            float ss = 0.0f;
+#pragma unroll
+            for (int c = 0; c < KW; ++c) {
+                o[c].x *= inv;
+                o[c].y *= inv;
+                o[c].z *= inv;
+                o[c].w *= inv;
+                ss += o[c].x * o[c].x + o[c].y * o[c].y + o[c].z * o[c].z + o[c].w * o[c].w;
+            }
+#pragma unroll
+            for (int s = 16; s >= 1; s >>= 1) ss += __shfl_xor_sync(kFull, ss, s);
+            const float rn = a.w.out_scale * rsqrtf(ss * (1.0f / (2 * D)) + a.w.eps);
+            const int r = t.rt0 + row;
+            __nv_bfloat16 *dst = a.out + (((int64_t)t.row0 + r / G) * (a.n_q / 2) + t.p * G + r % G) * (2 * D);
+#pragma unroll
+            for (int c = 0; c < KW; ++c) {
+                const int d = 4 * (lane + 32 * c);
+                const float4 g = a.w.norm_weight ? __ldg(reinterpret_cast<const float4 *>(a.w.norm_weight + d))
+                                                 : make_float4(1.f, 1.f, 1.f, 1.f);
+                *reinterpret_cast<uint2 *>(dst + d) = make_uint2(pack_bf16x2(o[c].x * rn * g.x, o[c].y * rn * g.y),
+                                                                 pack_bf16x2(o[c].z * rn * g.z, o[c].w * rn * g.w));
+            }
+        }
+    }
+}
+
 // ------------------------------------------------------------- launch
 
-template <int D, int G, bool F8>
-pkv_status launch(pkv_pool *pool, const void *q, int64_t tiles, const Args &a, cudaStream_t s)
+template <int D, int G, bool F8, int MODE>
+pkv_status launch_mode(pkv_pool *pool, const CUtensorMap &tm_q, int grid, const Args &a, cudaStream_t s)
 {
     using L = Layout<D>;
     static std::mutex mu;
@@ -904,16 +1097,12 @@ pkv_status launch(pkv_pool *pool, const void *q, int64_t tiles, const Args &a, c
     {
         std::lock_guard<std::mutex> lock(mu);
         if (pool->device >= 64 || !ready[pool->device]) {
-            cudaError_t e = cudaFuncSetAttribute(diff_prefill_kernel<D, G, F8>,
+            cudaError_t e = cudaFuncSetAttribute(diff_prefill_kernel<D, G, F8, MODE>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::bytes);
             if (e != cudaSuccess) return cuda_fail(e, "paged_diff_prefill_attention: kernel attributes");
             if (pool->device < 64) ready[pool->device] = true;
         }
     }
-    CUtensorMap tm_q;
-    pkv_status st = make_q_pair_map(&tm_q, q, a.n_rows, a.n_q, D, G, kRows / G);
-    if (st != PKV_OK) return st;
-    const int grid = 2 * (int)std::min<int64_t>(tiles, pool->num_sms / 2);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
@@ -926,22 +1115,63 @@ pkv_status launch(pkv_pool *pool, const void *q, int64_t tiles, const Args &a, c
     attr[1].val.clusterDim.x = 2;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = MODE == kWhole ? 2 : 1;
     LaunchScope ls(pool, kDecode, s);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, diff_prefill_kernel<D, G, F8>, tm_q, pool->tm_block, a);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, diff_prefill_kernel<D, G, F8, MODE>, tm_q, pool->tm_block, a);
     ls.done();
     if (e != cudaSuccess) return cuda_fail(e, "paged_diff_prefill_attention launch");
     return PKV_OK;
 }
 
+// How many ranges to cut a tile's keys into: as many as give every SM a CTA (counting the most tiles the call
+// can have), none with less than one step of the longest sequence the table can hold, 16 at most.
+int ranges_of(const pkv_pool *pool, int64_t tiles, int W)
+{
+    const int64_t steps = (W + kStepBlocks - 1) / kStepBlocks;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, steps), pool->num_sms / std::max<int64_t>(1, tiles)));
+}
+
+template <int D, int G, bool F8>
+pkv_status launch(pkv_pool *pool, const void *q, Args a, cudaStream_t s)
+{
+    CUtensorMap tm_q;
+    pkv_status st = make_q_pair_map(&tm_q, q, a.n_rows, a.n_q, D, G, kRows / G);
+    if (st != PKV_OK) return st;
+    // upper bounds on the tiles and pairs of them: every sequence may end with a partial one
+    const int64_t tiles = ((a.n_rows * G + kRows - 1) / kRows + a.batch) * a.n_pairs;
+    const int64_t pairs = ((a.n_rows * G + 2 * kRows - 1) / (2 * kRows) + a.batch) * a.n_pairs;
+    a.ranges = ranges_of(pool, tiles, a.W);
+    if (a.ranges > 1) {
+        const size_t slots = (size_t)tiles * a.ranges;
+        const size_t stat_bytes = slots * kRows * sizeof(float4), bytes = stat_bytes + slots * kRows * 2 * D * sizeof(float);
+        // (a call that would have to allocate while its stream is captured runs whole instead)
+        if (ensure_workspace(pool, bytes, s, "paged_diff_prefill_attention") == PKV_OK) {
+            a.ws_stat = static_cast<float4 *>(pool->ws);
+            a.ws_o = reinterpret_cast<float *>(static_cast<uint8_t *>(pool->ws) + stat_bytes);
+            st = launch_mode<D, G, F8, kSums>(pool, tm_q, (int)slots, a, s);
+            if (st == PKV_OK) st = launch_mode<D, G, F8, kWeights>(pool, tm_q, (int)slots, a, s);
+            if (st != PKV_OK) return st;
+            LaunchScope ls(pool, kMerge, s);
+            cudaError_t e = launch_pdl(join_kernel<D, G>, dim3((unsigned)tiles, std::max(1, (int)(pool->num_sms / tiles))),
+                                       dim3(kJoinWarps * 32), 0, s, a);
+            ls.done();
+            if (e != cudaSuccess) return cuda_fail(e, "paged_diff_prefill_attention: join launch");
+            return PKV_OK;
+        }
+        cudaGetLastError();  // a failed allocation is not this call's failure
+        a.ranges = 1;
+    }
+    return launch_mode<D, G, F8, kWhole>(pool, tm_q, 2 * (int)std::min<int64_t>(pairs, pool->num_sms / 2), a, s);
+}
+
 template <int D, bool F8>
-pkv_status dispatch_g(pkv_pool *pool, const void *q, int G, int64_t tiles, const Args &a, cudaStream_t s)
+pkv_status dispatch_g(pkv_pool *pool, const void *q, int G, const Args &a, cudaStream_t s)
 {
     switch (G) {
-    case 1: return launch<D, 1, F8>(pool, q, tiles, a, s);
-    case 2: return launch<D, 2, F8>(pool, q, tiles, a, s);
-    case 4: return launch<D, 4, F8>(pool, q, tiles, a, s);
-    case 8: return launch<D, 8, F8>(pool, q, tiles, a, s);
+    case 1: return launch<D, 1, F8>(pool, q, a, s);
+    case 2: return launch<D, 2, F8>(pool, q, a, s);
+    case 4: return launch<D, 4, F8>(pool, q, a, s);
+    case 8: return launch<D, 8, F8>(pool, q, a, s);
     }
     return fail(PKV_EUNSUPPORTED, "differential prefill: group size %d unsupported (1, 2, 4 or 8)", G);
 }
@@ -974,9 +1204,7 @@ extern "C" pkv_status paged_diff_prefill_attention(pkv_pool *pool, const void *q
         return fail(PKV_EINVAL, "%s: indptr, tables and lengths must be 4-byte aligned", who);
     st = check_pool_device(pool, who);
     if (st != PKV_OK) return st;
-    // an upper bound on the tile pairs: every sequence may end with a partial one
-    const int64_t tiles = ((n_rows * G + 2 * kRows - 1) / (2 * kRows) + batch) * (pool->n_kv / 2);
-    if (tiles > INT32_MAX) return fail(PKV_EUNSUPPORTED, "%s: too many query rows", who);
+    if (((n_rows * G + kRows - 1) / kRows + batch) * (pool->n_kv / 2) > INT32_MAX) return fail(PKV_EUNSUPPORTED, "%s: too many query rows", who);
     a.qo_indptr = qo_indptr;
     a.block_tables = block_tables;
     a.W = max_blocks_per_seq;
@@ -993,9 +1221,12 @@ extern "C" pkv_status paged_diff_prefill_attention(pkv_pool *pool, const void *q
     a.scales = pool->scales;
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.err = pool->err;
+    a.ranges = 1;
+    a.ws_stat = nullptr;
+    a.ws_o = nullptr;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool f8 = pool->dtype == PKV_FP8_E4M3;
     if (pool->d_head == 128)
-        return f8 ? dispatch_g<128, true>(pool, q, G, tiles, a, s) : dispatch_g<128, false>(pool, q, G, tiles, a, s);
-    return f8 ? dispatch_g<64, true>(pool, q, G, tiles, a, s) : dispatch_g<64, false>(pool, q, G, tiles, a, s);
+        return f8 ? dispatch_g<128, true>(pool, q, G, a, s) : dispatch_g<128, false>(pool, q, G, a, s);
+    return f8 ? dispatch_g<64, true>(pool, q, G, a, s) : dispatch_g<64, false>(pool, q, G, a, s);
 }

@@ -88,8 +88,19 @@ __device__ __forceinline__ void umma_commit_if(uint32_t go, uint64_t *bar)
                  : "memory");
 }
 
-// tma_load_2d by the lane whose `go` is set (see umma_if), into every CTA of the cluster named by `mask`, at
-// the same place of its shared memory and completing on its barrier there.
+// tma_load_2d by the lane whose `go` is set (see umma_if).
+__device__ __forceinline__ void tma_load_2d_if(uint32_t go, uint32_t dst_smem, const CUtensorMap *map, int x, int y,
+                                               uint32_t bar, uint64_t policy)
+{
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+                 "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+                 "[%0], [%1, {%2, %3}], [%4], %5;\n\t}"
+                 ::"r"(dst_smem), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy), "r"(go)
+                 : "memory");
+}
+
+// The same into every CTA of the cluster named by `mask`, at the same place of its shared memory and
+// completing on its barrier there.
 __device__ __forceinline__ void tma_load_2d_multicast_if(uint32_t go, uint32_t dst_smem, const CUtensorMap *map, int x,
                                                          int y, uint32_t bar, uint16_t mask, uint64_t policy)
 {

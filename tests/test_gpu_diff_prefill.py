@@ -19,8 +19,16 @@ def i32(x):
     return torch.tensor(np.asarray(x), dtype=torch.int32).cuda()
 
 
-def prefill(c, q, chunks, params, lens=None, tables=None, indptr=None, **kw):
+PAD = 160  # sequences without rows behind the others: so many tiles may follow that the call runs whole
+
+
+def prefill(c, q, chunks, params, lens=None, tables=None, indptr=None, pad=0, **kw):
     indptr = np.concatenate([[0], np.cumsum(chunks)]) if indptr is None else indptr
+    if pad:
+        indptr = np.concatenate([indptr, np.full(pad, indptr[-1])])
+        lens = list(c.lens if lens is None else lens) + [0, 5] * (pad // 2)
+        tables = c.tables if tables is None else tables
+        tables = torch.cat((tables, torch.full((pad, tables.shape[1]), -1, dtype=torch.int32)))
     return pkv.paged_diff_prefill_attention(c.pool, q, i32(indptr), (c.tables if tables is None else tables).cuda(),
                                             i32(c.lens if lens is None else lens), 1 / np.sqrt(c.d), params, **kw)
 
@@ -44,7 +52,8 @@ CASES = [  # n_kv, G, d, lens, chunks
 @pytest.mark.gpu
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c[:3])) + f"-{len(c[3])}")
-def test_diff_prefill_matches_the_64_bit_form(kv, case):
+@pytest.mark.parametrize("pad", [0, PAD])
+def test_diff_prefill_matches_the_64_bit_form(kv, case, pad):
     n_kv, G, d, lens, chunks = case
     with Cache(kv, n_kv, d, lens, seed=G) as c:
         for b in range(len(lens)):
@@ -53,11 +62,11 @@ def test_diff_prefill_matches_the_64_bit_form(kv, case):
         rows = sum(chunks)
         q, params = queries(rows, n_kv * G, d, G), weights(d, G, norm=G != 2)
         out = torch.full((rows, n_kv * G // 2, 2 * d), 5.0, dtype=torch.bfloat16, device="cuda")
-        got = prefill(c, q, chunks, params, out=out)
+        got = prefill(c, q, chunks, params, out=out, pad=pad)
         torch.cuda.synchronize()
         assert got is out and c.pool.get_error() == 0
         check(got, *plain(c, q, ptr(chunks), lens, 1 / np.sqrt(d), params))
-        assert torch.equal(got, prefill(c, q, chunks, params))  # the same bits again
+        assert torch.equal(got, prefill(c, q, chunks, params, pad=pad))  # the same bits again
 
 
 @pytest.mark.gpu
@@ -67,6 +76,10 @@ def test_diff_prefill_matches_the_64_bit_form(kv, case):
     ("bf16", 16, 2, 64, [150] * 70, [7] * 70),
     ("bf16", 64, 1, 128, [260, 40], [130, 40]),
     ("fp8", 2, 8, 128, [1900, 10], [64, 10]),
+    ("bf16", 2, 4, 128, [20000], [9]),                              # a few drafted tokens on a long cache
+    ("fp8", 4, 2, 64, [9000, 17, 3], [3, 17, 1]),
+    ("bf16", 4, 1, 64, [1030], [1030]),
+    ("fp8", 16, 4, 128, [129] * 24, [100] * 24),                    # whole: single tiles of their pairs
 ])
 def test_diff_prefill_shapes(kv, n_kv, G, d, lens, chunks):
     with Cache(kv, n_kv, d, lens, seed=8) as c:
@@ -80,7 +93,8 @@ def test_diff_prefill_shapes(kv, n_kv, G, d, lens, chunks):
 @pytest.mark.gpu
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 @pytest.mark.parametrize("lam", ["zero", "negative", "large", "tiny"])
-def test_diff_prefill_lambdas(kv, lam):
+@pytest.mark.parametrize("pad", [0, PAD])
+def test_diff_prefill_lambdas(kv, lam, pad):
     """lambda 0, below 0, far above 1 (the second map's factor is then the larger) and far below 1."""
     d, lens, chunks = 64, [70, 300], [70, 33]
     a = torch.zeros(4, d, device="cuda")
@@ -89,7 +103,7 @@ def test_diff_prefill_lambdas(kv, lam):
         a[0, 0] = a[1, 0] = 2.0  # e^4 - 1
     with Cache(kv, 2, d, lens, seed=1) as c:
         q, params = queries(sum(chunks), 8, d), pkv.DiffParams(a, init)
-        got = prefill(c, q, chunks, params)
+        got = prefill(c, q, chunks, params, pad=pad)
         torch.cuda.synchronize()
         check(got, *plain(c, q, ptr(chunks), lens, 1 / np.sqrt(d), params))
 
@@ -109,7 +123,8 @@ def test_diff_prefill_and_decode_scales_at_or_below_zero(kv, scale):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
-def test_diff_prefill_one_map_sharp_the_other_flat(kv):
+@pytest.mark.parametrize("pad", [0, PAD])
+def test_diff_prefill_one_map_sharp_the_other_flat(kv, pad):
     """The two maps' sums differ by the whole length: one map's scores are 0 everywhere (its queries are
     0), the other's are dominated by single keys; both ways round."""
     d, lens, chunks = 64, [1500], [200]
@@ -118,20 +133,21 @@ def test_diff_prefill_one_map_sharp_the_other_flat(kv):
             q = 3 * queries(200, 4, d)
             q[:, flat::2] = 0
             params = weights(d)
-            got = prefill(c, q, chunks, params)
+            got = prefill(c, q, chunks, params, pad=pad)
             torch.cuda.synchronize()
             check(got, *plain(c, q, ptr(chunks), lens, 1 / np.sqrt(d), params), norm2=False)
 
 
 @pytest.mark.gpu
-def test_diff_prefill_bad_blocks_are_masked_and_flagged():
+@pytest.mark.parametrize("pad", [0, PAD])
+def test_diff_prefill_bad_blocks_are_masked_and_flagged(pad):
     lens, chunks = [300, 64, 200], [150, 20, 200]
     with Cache("bf16", 2, 64, lens, seed=2) as c:
         tables = c.tables.clone()
         tables[0, 2], tables[2, 0] = c.blocks, -5
         tables[1, :4] = 10 ** 6
         q, params = queries(sum(chunks), 4, 64), weights(64)
-        got = prefill(c, q, chunks, params, tables=tables)
+        got = prefill(c, q, chunks, params, tables=tables, pad=pad)
         torch.cuda.synchronize()
         assert c.pool.get_error(clear=True) == pkv.DEVERR_BLOCK_RANGE
         skip = [(0, 2), (2, 0)] + [(1, j) for j in range(4)]
@@ -172,11 +188,12 @@ def test_diff_prefill_lengths_out_of_range():
         torch.cuda.synchronize()
         assert c.pool.get_error(clear=True) == pkv.DEVERR_CTX_RANGE
         check(got, *plain(c, q, [0, 30, 70], [64, 40], 1 / np.sqrt(64), params))
-        out = torch.full((70, 2, 128), 3.0, dtype=torch.bfloat16, device="cuda")
-        prefill(c, q, [65, 5], params, lens=[65, 60], out=out)  # 65 tokens in 4 blocks: skipped
-        torch.cuda.synchronize()
-        assert c.pool.get_error(clear=True) == pkv.DEVERR_CTX_RANGE
-        assert (out[:65] == 3).all() and (out[65:] != 3).any()
+        for pad in (0, PAD):
+            out = torch.full((70, 2, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+            prefill(c, q, [65, 5], params, lens=[65, 60], out=out, pad=pad)  # 65 tokens in 4 blocks: skipped
+            torch.cuda.synchronize()
+            assert c.pool.get_error(clear=True) == pkv.DEVERR_CTX_RANGE
+            assert (out[:65] == 3).all() and (out[65:] != 3).any()
 
 
 @pytest.mark.gpu
@@ -185,7 +202,8 @@ def test_diff_prefill_on_a_side_stream_and_in_a_graph():
     with Cache("bf16", 4, 128, lens, seed=6) as c:
         q, params = queries(170, 8, 128), weights(128)
         want = prefill(c, q, chunks, params)
-        args = (i32(ptr(chunks)), c.tables.cuda(), i32(lens), 1 / np.sqrt(128), params)
+        i32_kept = (i32(ptr(chunks)), c.tables.cuda(), i32(lens))
+        args = (*i32_kept, 1 / np.sqrt(128), params)
         static = torch.zeros_like(q)
         torch.cuda.synchronize()
         side = torch.cuda.Stream()
@@ -199,6 +217,21 @@ def test_diff_prefill_on_a_side_stream_and_in_a_graph():
                 g.replay()
         side.synchronize()
         assert torch.equal(out, want)
+    # a pool whose workspace would have to grow inside the capture: the call runs whole
+    with Cache("bf16", 4, 128, lens, seed=6) as c:
+        before = c.pool.timing_read()["workspace_bytes"]
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=side):
+            out = pkv.paged_diff_prefill_attention(c.pool, static, *i32_kept, 1 / np.sqrt(128), params)
+        assert c.pool.timing_read()["workspace_bytes"] == before
+        g.replay()
+        torch.cuda.synchronize()
+        check(out, *plain(c, q, ptr(chunks), lens, 1 / np.sqrt(128), params))
+        c.pool.reserve_diff_workspace(2, 8, c.W)
+        assert c.pool.timing_read()["workspace_bytes"] > before
+        got = pkv.paged_diff_prefill_attention(c.pool, static, *i32_kept, 1 / np.sqrt(128), params)
+        assert torch.equal(got, want)
 
 
 @pytest.mark.gpu
