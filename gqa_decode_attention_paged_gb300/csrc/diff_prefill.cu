@@ -386,10 +386,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint16_t kBoth = 3;
     const int e0 = (int)(kPair ? blockIdx.x / 2 : blockIdx.x), stride = (int)(kPair ? gridDim.x / 2 : gridDim.x);
 
-    if (tid == 0) {
+    if (warp == kCopyWarp && lane == 0) {
         prefetch_tensormap(&tm_q);
         prefetch_tensormap(&tm_kv);
-        for (int i = 0; i < L::NBARS; ++i) {
+        *abort_flag = 0;
+    }
+    static_assert(L::NBARS <= 16 * 32, "a thread per barrier");
+    {
+        const int i = tid;
+        if (i < L::NBARS) {
             uint32_t n = 1;
             if (i == L::ST_READ || i == L::ST_READ + 1 || i == L::P_FULL || i == L::P_FULL + 1) n = kSoftmaxWarps / 2;
             if (i == L::S2_READ || i == L::O_FREE) n = kSoftmaxWarps;
@@ -398,9 +403,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i >= L::FULL && i < L::EMPTY && kSplit) n = 2;
             if (i >= L::EMPTY && i < L::EMPTY + NS && kPair) n = 2;  // both CTAs have used the slot
             mbar_init(&bar[i], n);
+            fence_mbarrier_init();
         }
-        *abort_flag = 0;
-        fence_mbarrier_init();
     }
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -423,9 +427,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             *abort_flag = 1;
         }
     };
-    for (int i = tid; i < 2 * D; i += kThreads)
-        reinterpret_cast<float *>(sm + L::kNorm)[i] = a.w.norm_weight ? a.w.norm_weight[i] : 1.0f;
-    __syncthreads();
+    if constexpr (kPair) {
+        for (int i = tid; i < 2 * D; i += kThreads)
+            reinterpret_cast<float *>(sm + L::kNorm)[i] = a.w.norm_weight ? a.w.norm_weight[i] : 1.0f;
+        __syncthreads();
+    }
     Walker wk;
     load_window<G, MODE>(wk, a, lane);
     const uint32_t base = smem_u32(sm);
@@ -752,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ts = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t to = ts + kColO + grp * QD;
         uint64_t *quad = &bar[L::QUAD + quarter];
-        const float lam = diff_lambda<D>(a.w, lane);
+        const float lam = kSecond ? diff_lambda<D>(a.w, lane) : 0.0f;
         const float abs_lam = fabsf(lam);
         const float sign = lam < 0.0f ? 1.0f : -1.0f;  // of the second map's weights
         const bool rising = a.qscale >= 0.0f;          // the largest score has the largest q . k (else the smallest)
@@ -1033,33 +1039,51 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     griddep_wait();
     griddep_launch_dependents();
-    const float abs_lam = fabsf(diff_lambda<D>(a.w, lane));
     Walker wk;
     load_window<G, kWeights>(wk, a, lane);
+    const float abs_lam = fabsf(diff_lambda<D>(a.w, lane));
     for (int x = blockIdx.x;; x += gridDim.x) {
         Tile t;
         if (!find_tile<G, kWeights>(wk, a, x * a.ranges, 0, t, lane)) break;
         if (t.n_blocks == 0) continue;
         const int S = (t.n_blocks + kStepBlocks - 1) / kStepBlocks;
+        const bool full = lane < a.ranges && range_first(S, a.ranges, lane) < range_first(S, a.ranges, lane + 1);
+        const uint32_t parts = __ballot_sync(kFull, full);  // the ranges that have steps (16 at most)
         // rows of this tile, dealt to the CTAs of its column of the grid
         for (int row = blockIdx.y * kJoinWarps + warp; row < min(kRows, t.R - t.rt0); row += gridDim.y * kJoinWarps) {
+            // lane k has range k's statistics
+            const float4 v = full ? __ldcg(a.ws_stat + (int64_t)(t.slot + lane) * kRows + row)
+                                  : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
             float4 o[KW];
 #pragma unroll
             for (int c = 0; c < KW; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 *src = reinterpret_cast<const float4 *>(a.ws_o + ((int64_t)t.slot * kRows + row) * (2 * D)) + lane;
+            constexpr int64_t kStep = (int64_t)kRows * 2 * D / 4;
+#pragma unroll 4
             for (int k = 0; k < a.ranges; ++k) {
-                if (range_first(S, a.ranges, k) == range_first(S, a.ranges, k + 1)) continue;
-                const float4 *src = reinterpret_cast<const float4 *>(a.ws_o + ((int64_t)(t.slot + k) * kRows + row) * (2 * D));
+                if (!((parts >> k) & 1u)) continue;
 #pragma unroll
                 for (int c = 0; c < KW; ++c) {
-                    const float4 v = __ldcg(src + lane + 32 * c);
-                    o[c].x += v.x;
-                    o[c].y += v.y;
-                    o[c].z += v.z;
-                    o[c].w += v.w;
+                    const float4 y = __ldcg(src + k * kStep + 32 * c);
+                    o[c].x += y.x;
+                    o[c].y += y.y;
+                    o[c].z += y.z;
+                    o[c].w += y.w;
                 }
             }
+            RowStat rs;
+            rs.add(v.x, v.y, v.z, v.w);
+#pragma unroll
+            for (int s = 8; s >= 1; s >>= 1)
+                rs.add(__shfl_xor_sync(kFull, rs.m1, s), __shfl_xor_sync(kFull, rs.l1, s), __shfl_xor_sync(kFull, rs.m2, s),
+                       __shfl_xor_sync(kFull, rs.l2, s));
+            RowStat all;
+            all.m1 = __shfl_sync(kFull, rs.m1, 0);
+            all.l1 = __shfl_sync(kFull, rs.l1, 0);
+            all.m2 = __shfl_sync(kFull, rs.m2, 0);
+            all.l2 = __shfl_sync(kFull, rs.l2, 0);
             float n0, n1, inv;
-            merged_stats(a, t, row, true).factors(abs_lam, n0, n1, inv);
+            all.factors(abs_lam, n0, n1, inv);
             float ss = 0.0f;
 #pragma unroll
             for (int c = 0; c < KW; ++c) {
@@ -1123,6 +1147,14 @@ pkv_status launch_mode(pkv_pool *pool, const CUtensorMap &tm_q, int grid, const 
     return PKV_OK;
 }
 
+// The most tiles of `per` rows that n_rows tokens of `batch` sequences can make: each sequence that has rows one,
+// and one for every `per` rows beyond its first row (sum of 1 + floor((x_i - 1) / per) over x_i > 0).
+int64_t most_tiles(int64_t n_rows, int G, int batch, int per)
+{
+    const int64_t begun = std::min<int64_t>(batch, n_rows);
+    return begun + (n_rows * G - begun) / per;
+}
+
 // How many ranges to cut a tile's keys into: as many as give every SM a CTA (counting the most tiles the call
 // can have), none with less than one step of the longest sequence the table can hold, 16 at most.
 int ranges_of(const pkv_pool *pool, int64_t tiles, int W)
@@ -1137,9 +1169,8 @@ pkv_status launch(pkv_pool *pool, const void *q, Args a, cudaStream_t s)
     CUtensorMap tm_q;
     pkv_status st = make_q_pair_map(&tm_q, q, a.n_rows, a.n_q, D, G, kRows / G);
     if (st != PKV_OK) return st;
-    // upper bounds on the tiles and pairs of them: every sequence may end with a partial one
-    const int64_t tiles = ((a.n_rows * G + kRows - 1) / kRows + a.batch) * a.n_pairs;
-    const int64_t pairs = ((a.n_rows * G + 2 * kRows - 1) / (2 * kRows) + a.batch) * a.n_pairs;
+    const int64_t tiles = most_tiles(a.n_rows, G, a.batch, kRows) * a.n_pairs;
+    const int64_t pairs = most_tiles(a.n_rows, G, a.batch, 2 * kRows) * a.n_pairs;
     a.ranges = ranges_of(pool, tiles, a.W);
     if (a.ranges > 1) {
         const size_t slots = (size_t)tiles * a.ranges;
@@ -1152,7 +1183,7 @@ pkv_status launch(pkv_pool *pool, const void *q, Args a, cudaStream_t s)
             if (st == PKV_OK) st = launch_mode<D, G, F8, kWeights>(pool, tm_q, (int)slots, a, s);
             if (st != PKV_OK) return st;
             LaunchScope ls(pool, kMerge, s);
-            cudaError_t e = launch_pdl(join_kernel<D, G>, dim3((unsigned)tiles, std::max(1, (int)(pool->num_sms / tiles))),
+            cudaError_t e = launch_pdl(join_kernel<D, G>, dim3((unsigned)tiles, std::max(2, (int)(4 * pool->num_sms / tiles))),
                                        dim3(kJoinWarps * 32), 0, s, a);
             ls.done();
             if (e != cudaSuccess) return cuda_fail(e, "paged_diff_prefill_attention: join launch");
@@ -1204,7 +1235,7 @@ extern "C" pkv_status paged_diff_prefill_attention(pkv_pool *pool, const void *q
         return fail(PKV_EINVAL, "%s: indptr, tables and lengths must be 4-byte aligned", who);
     st = check_pool_device(pool, who);
     if (st != PKV_OK) return st;
-    if (((n_rows * G + kRows - 1) / kRows + batch) * (pool->n_kv / 2) > INT32_MAX) return fail(PKV_EUNSUPPORTED, "%s: too many query rows", who);
+    if (most_tiles(n_rows, G, batch, kRows) * (pool->n_kv / 2) > INT32_MAX) return fail(PKV_EUNSUPPORTED, "%s: too many query rows", who);
     a.qo_indptr = qo_indptr;
     a.block_tables = block_tables;
     a.W = max_blocks_per_seq;
