@@ -821,7 +821,5 @@ extern "C" pkv_status paged_diff_reserve_workspace(pkv_pool *pool, int32_t batch
     st = check_pool_device(pool, who);
     Plan pl;
     if (st == PKV_OK) st = for_config<PlanCall>(pool, n_q / pool->n_kv, pool, batch, max_blocks_per_seq, &pl);
-    // a chunk call's ranges: at most one per SM
-    const size_t chunk = (size_t)pool->num_sms * 128 * (sizeof(float4) + 2 * (size_t)pool->d_head * sizeof(float));
-    return st == PKV_OK ? ensure_workspace(pool, std::max(pl.bytes, chunk)) : st;
+    return st == PKV_OK ? ensure_workspace(pool, pl.bytes) : st;
 }

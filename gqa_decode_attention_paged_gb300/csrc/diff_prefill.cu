@@ -49,17 +49,17 @@
 //   * value rows behind the sequence's end (a page that ends inside a tile)
 //     are zeroed in shared memory before their product: a weight of 0 does not
 //     cancel what is not finite.
-//   * few rows (kSums, kWeights): when the call's tiles would leave most SMs
-//     idle (a few drafted tokens on long caches), the keys of a tile are cut
-//     into ranges, one CTA each, and the sweeps become two launches: the first
-//     leaves (m, l) of both maps per row and range, the second merges them (so
-//     its weights are the final ones) and leaves its range's part of o, and a
-//     third adds the parts in order -- plain sums, since all share the row's
-//     scaling -- and applies the norm.
+//   * few rows (kRange): when the call's tiles would leave most SMs idle (a few
+//     drafted tokens on long caches), a cluster of 2 to 16 CTAs takes one tile,
+//     a range of its keys each.  Between the sweeps every CTA reads the others'
+//     statistics (distributed shared memory), so all form their weights with
+//     the row's final factors, and at the end the parts of o are plain sums:
+//     each CTA adds, in order, and normalises its share of the rows.
 // Every mbarrier wait is bounded; on a timeout the CTA records
 // PKV_DEVERR_TIMEOUT, every role stops, the MMA and copy pipes are drained
 // (bounded) and the tensor memory is released before the CTA exits.
 #include <algorithm>
+#include <climits>
 #include <mutex>
 #include <type_traits>
 
@@ -100,15 +100,10 @@ struct Args {
     DiffWeights w;
     __nv_bfloat16 *out;   // [n_rows][n_q / 2][2 D]
     unsigned *err;
-    // ranges of keys (kSums, kWeights): how many of a tile, and per (tile, range) and row (m, l) of both
-    // maps and the range's part of o, [tile][range][kRows] and [tile][range][kRows][2 D]
-    int ranges;
-    float4 *ws_stat;
-    float *ws_o;
 };
 
-// What a launch does: both sweeps on pairs of tiles, or one of them on ranges of a tile's keys.
-enum Mode { kWhole = 0, kSums = 1, kWeights = 2 };
+// What a cluster does: two CTAs a pair of tiles, or several CTAs the ranges of one tile's keys.
+enum Mode { kWhole = 0, kRange = 1 };
 
 template <int D>
 struct Layout {
@@ -117,8 +112,10 @@ struct Layout {
     static constexpr int kStages = D == 128 ? 5 : 10;
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kRing = kQ + 2 * QT;
-    static constexpr uint32_t kNorm = kRing + kStages * UT;  // [2 D] float: the norm's weights
-    static constexpr uint32_t kBar = kNorm + 2 * D * 4;
+    static constexpr uint32_t kNorm = kRing + kStages * UT;  // kWhole: [2 D] float, the norm's weights
+    // kRange: each row's statistics of both maps, as l = 2^g, [2][kRows] bf16, and m, [2][kRows] float
+    static constexpr uint32_t kStatM = kNorm, kStatG = kStatM + 2 * kRows * 4;
+    static constexpr uint32_t kBar = kStatG + 2 * kRows * 2;
     // RAW, Q_RAW: FP8 pools' copies complete there; FULL and Q_FULL follow when the rows are f16
     enum { Q_RAW = 0, Q_FULL, Q_FREE, RAW, FULL = RAW + kStages, EMPTY = FULL + kStages,
            ST_FULL = EMPTY + kStages,    // first sweep, per map: scores of a step
@@ -128,7 +125,7 @@ struct Layout {
            S2_READ = S1_FULL + 2,        // map 2's are in registers
            P_FULL = S2_READ + 1,         // per half: the weights are in tensor memory
            PV_DONE = P_FULL + 2,         // per half: their product has run
-           O_FULL = PV_DONE + 2, O_FREE, END_ASK, END_CLEAR, QUAD, DRAIN = QUAD + 4, NBARS };
+           O_FULL = PV_DONE + 2, O_FREE, END_ASK, END_CLEAR, STAT, PARTS, QUAD, DRAIN = QUAD + 4, NBARS };
     static constexpr uint32_t kTmemSlot = kBar + NBARS * 8;
     static constexpr uint32_t kAbort = kTmemSlot + 4;
     static constexpr uint32_t kEnd = kAbort + 4;
@@ -217,14 +214,13 @@ struct Tile {
     int R;          // rows of (b, p): T * G
     int row0, T, C; // first query token row of b, chunk length, context length (clamped)
     int n_blocks, n_steps;  // blocks the tile sees; steps of this CTA's range
-    int s0;                 // its first step
-    int slot;               // (tile, range) in the workspace
+    int s0, S;              // its first step; the tile's steps
     bool bad_ctx;
 };
 
 // A window of 32 sequences, one per lane: each warp walks the list itself
 // (sequence, then pair, then row tile), with the same arithmetic.  The list's
-// entries are pairs of tiles (kWhole) or ranges of a tile.
+// entries are pairs of tiles (kWhole) or tiles.
 struct Walker {
     int wb = 0, wbase = 0;           // the window's first sequence, entries before it
     int incl = 0, tot = 0;
@@ -261,12 +257,11 @@ __device__ __forceinline__ void load_window(Walker &w, const Args &a, int lane)
     w.tot = __shfl_sync(kFull, x, 31);
 }
 
-// Entry e of the list: CTA `rank`'s tile of the pair, or a range of a tile; false past its end.  Warp-wide,
-// uniform result.
+// Entry x of the list: CTA `rank`'s tile of the pair, or its range (of `ranges`) of the tile; false past its
+// end.  Warp-wide, uniform result.
 template <int G, int MODE>
-__device__ __forceinline__ bool find_tile(Walker &w, const Args &a, int e, int rank, Tile &t, int lane)
+__device__ __forceinline__ bool find_tile(Walker &w, const Args &a, int x, int rank, int ranges, Tile &t, int lane)
 {
-    const int x = MODE == kWhole ? e : e / a.ranges;
     while (x >= w.wbase + w.tot) {
         if (w.wb + 32 >= a.batch) return false;
         w.wbase += w.tot;
@@ -285,8 +280,7 @@ __device__ __forceinline__ bool find_tile(Walker &w, const Args &a, int e, int r
     t.p = within / nt;
     const int pair0 = (within - t.p * nt) * (MODE == kWhole ? 2 : 1) * kRows;
     t.rt0 = pair0 + (MODE == kWhole ? rank * kRows : 0);
-    t.s0 = 0;
-    t.slot = e;
+    t.s0 = t.S = 0;
     t.R = t.T * G;
     const int cap = a.W * kBlockSize;
     t.bad_ctx = C < t.T || C > cap;
@@ -299,10 +293,10 @@ __device__ __forceinline__ bool find_tile(Walker &w, const Args &a, int e, int r
     const int last_row = min(t.R, pair0 + (MODE == kWhole ? 2 : 1) * kRows) - 1;  // a pair walks the same keys
     t.n_blocks = (C - t.T + last_row / G) / kBlockSize + 1;
     t.n_steps = (t.n_blocks + kStepBlocks - 1) / kStepBlocks;
-    if constexpr (MODE != kWhole) {
-        const int k = e - x * a.ranges;
-        t.s0 = range_first(t.n_steps, a.ranges, k);
-        t.n_steps = range_first(t.n_steps, a.ranges, k + 1) - t.s0;
+    t.S = t.n_steps;
+    if constexpr (MODE == kRange) {
+        t.s0 = range_first(t.S, ranges, rank);
+        t.n_steps = range_first(t.S, ranges, rank + 1) - t.s0;
     }
     return true;
 }
@@ -346,18 +340,26 @@ struct RowStat {
     }
 };
 
-// A row's statistics over all ranges of its tile (`slot` is one of them).
-__device__ __forceinline__ RowStat merged_stats(const Args &a, const Tile &t, int row, bool live)
+// Of one map and row (index i), into this CTA's shared memory.  l goes as 2^g with g = log2(l) rounded to bf16
+// (there is no room for four floats a row); what the rounding leaves is added to m, so nothing but m's own fp32
+// rounding is lost: m + log2(l) is what the weights depend on.
+template <typename L>
+__device__ __forceinline__ void put_stat(uint8_t *sm, int i, float m, float l)
 {
-    RowStat rs;
-    const int S = (t.n_blocks + kStepBlocks - 1) / kStepBlocks;
-    const int first = t.slot / a.ranges * a.ranges;
-    for (int k = 0; k < a.ranges && live; ++k) {
-        if (range_first(S, a.ranges, k) == range_first(S, a.ranges, k + 1)) continue;  // an empty range wrote nothing
-        const float4 v = __ldcg(a.ws_stat + (int64_t)(first + k) * kRows + row);
-        rs.add(v.x, v.y, v.z, v.w);
-    }
-    return rs;
+    const float g = log2f(l);
+    const __nv_bfloat16 r = __float2bfloat16_rn(m == -INFINITY ? 0.0f : g);
+    reinterpret_cast<float *>(sm + L::kStatM)[i] = m == -INFINITY ? m : m + (g - __bfloat162float(r));
+    reinterpret_cast<__nv_bfloat16 *>(sm + L::kStatG)[i] = r;
+}
+
+// Adds CTA k's of both maps of a row.
+template <typename L>
+__device__ __forceinline__ void add_stat(RowStat &rs, uint32_t base, int row, int k)
+{
+    const uint32_t xm = smem_of(base + L::kStatM + row * 4, k), xg = smem_of(base + L::kStatG + row * 2, k);
+    const float m1 = ld_cluster_f32(xm), m2 = ld_cluster_f32(xm + 4 * kRows);
+    const float g1 = ld_cluster_bf16(xg), g2 = ld_cluster_bf16(xg + 2 * kRows);
+    rs.add(m1, m1 == -INFINITY ? 0.0f : ex2(g1), m2, m2 == -INFINITY ? 0.0f : ex2(g2));
 }
 
 // ------------------------------------------------------------- the kernel
@@ -380,11 +382,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::kAbort);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(kFull, tid >> 5, 0);  // the same in all lanes, and known to be
-    constexpr bool kPair = MODE == kWhole;  // clusters of two
-    constexpr bool kFirst = MODE != kWeights, kSecond = MODE != kSums;
-    const int rank = kPair ? (int)cluster_rank() : 0;
+    constexpr bool kPair = MODE == kWhole;
+    const int rank = (int)cluster_rank(), ranges = kPair ? 2 : (int)cluster_size();
     constexpr uint16_t kBoth = 3;
-    const int e0 = (int)(kPair ? blockIdx.x / 2 : blockIdx.x), stride = (int)(kPair ? gridDim.x / 2 : gridDim.x);
+    // the cluster's entries of the list: its own and every stride-th from there (kWhole), or its own alone
+    const int e0 = (int)(kPair ? blockIdx.x / 2 : blockIdx.x / ranges);
+    const int stride = (int)(kPair ? gridDim.x / 2 : gridDim.x / ranges);
+    const int e_end = kPair ? INT_MAX : e0 + 1;
 
     if (warp == kCopyWarp && lane == 0) {
         prefetch_tensormap(&tm_q);
@@ -402,6 +406,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i == L::Q_FULL && F8) n = kSoftmaxWarps;  // each widens its share of the queries
             if (i >= L::FULL && i < L::EMPTY && kSplit) n = 2;
             if (i >= L::EMPTY && i < L::EMPTY + NS && kPair) n = 2;  // both CTAs have used the slot
+            if (i == L::STAT) n = 4 * ranges;              // of every CTA, the warps that hold a row's statistics
+            if (i == L::PARTS) n = kSoftmaxWarps * ranges;
             mbar_init(&bar[i], n);
             fence_mbarrier_init();
         }
@@ -415,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if constexpr (kPair) cluster_sync();  // both CTAs' barriers are ready
+    cluster_sync();  // all CTAs' barriers are ready
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + L::kTmemSlot);
     griddep_wait();
@@ -457,9 +463,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++u;
             return true;
         };
-        for (int x = e0; ok; x += stride) {
+        for (int x = e0; ok && x < e_end; x += stride) {
             Tile t;
-            if (!find_tile<G, MODE>(wk, a, x, rank, t, lane)) break;
+            if (!find_tile<G, MODE>(wk, a, x, rank, ranges, t, lane)) break;
             if (t.n_steps == 0) continue;
             if (*abort_flag) break;
             if (n > 0 && !(ok = wait_all(&bar[L::Q_FREE], (n - 1) & 1))) break;
@@ -494,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!open(land, dst)) return false;
 #pragma unroll
                 for (int i = 0; i < kStepBlocks / kShare; ++i) {
-                    const int k = kShare * i + rank;
+                    const int k = kShare * i + (kPair ? rank : 0);
                     const int yk = __shfl_sync(kFull, y0, k);
                     const int y = yk == a.oob_row ? yk : yk + m * 2 * kBlockSize;
                     if constexpr (F8) {
@@ -512,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!open(land, dst)) return false;
 #pragma unroll
                 for (int i = 0; i < kUnitBlocks / kShare; ++i) {
-                    const int k = kShare * i + rank;
+                    const int k = kShare * i + (kPair ? rank : 0);
                     const int yk = __shfl_sync(kFull, y0, h * kUnitBlocks + k);
 #pragma unroll
                     for (int head = 0; head < 2; ++head) {
@@ -529,13 +535,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 return true;
             };
-            int nxt = kFirst ? rows_of(0, true) : 0;
-            for (int s = 0; kFirst && s < t.n_steps && ok; ++s) {
+            int nxt = rows_of(0, true);
+            for (int s = 0; s < t.n_steps && ok; ++s) {
                 const int y0 = nxt;
                 if (s + 1 < t.n_steps) nxt = rows_of(s + 1, true);
                 ok = copy_k(y0, 0) && copy_k(y0, 1);
             }
-            if (!ok || !kSecond) continue;
+            if (!ok) break;
             int y0 = rows_of(0, false);
             ok = copy_k(y0, 1) && copy_k(y0, 0);
             for (int s = 0; s < t.n_steps && ok; ++s) {  // in the order of the MMAs
@@ -556,18 +562,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= kPrepWarp) {
         // ---------------------------------------------------------- units made ready
         const int which = warp - kPrepWarp;
-        // units of a tile: 2 a step in the first sweep, 4 in the second
-        auto first_units = [&](const Tile &t) -> int { return kFirst ? 2 * t.n_steps : 0; };
-        if (F8 || (which == 0 && kSecond)) {
+        if (F8 || which == 0) {
             int u = 0, ends = 0;
             bool ok = true;
-            for (int x = e0; ok; x += stride) {
+            for (int x = e0; ok && x < e_end; x += stride) {
                 Tile t;
-                if (!find_tile<G, MODE>(wk, a, x, rank, t, lane)) break;
+                if (!find_tile<G, MODE>(wk, a, x, rank, ranges, t, lane)) break;
                 if (t.n_steps == 0) continue;
                 if (*abort_flag) break;
                 // the V unit the sequence ends inside of: zero the rows behind the end (value heads h0 ..)
-                const int end = kSecond ? end_unit(t) : -1;
+                const int end = end_unit(t);
                 auto clear = [&](uint32_t unit, int h0, int heads) {
                     const int r0 = (t.C / kBlockSize % kUnitBlocks) * kBlockSize;
                     const int first = r0 + t.C % kBlockSize, rows = r0 + kBlockSize - first;
@@ -579,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (!F8) {  // the MMA warp asks when the unit has landed
                     if (end >= 0) {
                         const int vs = end / 2, S = t.n_steps;
-                        const int v = u + first_units(t) + 2 + 4 * vs + (end & 1) * (vs == S - 1 ? 1 : 3);
+                        const int v = u + 2 * S + 2 + 4 * vs + (end & 1) * (vs == S - 1 ? 1 : 3);
                         if (!(ok = wait_all(&bar[L::END_ASK], ends & 1))) break;
                         ++ends;
                         clear(base + L::kRing + v % NS * L::UT, 0, 2);
@@ -587,16 +591,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bar[L::END_CLEAR]);
                     }
-                    u += first_units(t) + 4 * t.n_steps;
+                    u += 6 * t.n_steps;
                 } else {
-                    const int units = first_units(t) + (kSecond ? 4 * t.n_steps : 0);
-                    for (int i = 0; i < units; ++i, ++u) {
+                    for (int i = 0; i < 6 * t.n_steps; ++i, ++u) {
                         const int st = u % NS;
                         if (!kSplit && (u & 1) != which) continue;
                         if (!(ok = wait_all(&bar[L::RAW + st], (u / NS) & 1))) break;
                         // second sweep: K, K of the first step, then of each step V, K, K, V (the next step's
                         // keys; the last step has V, V)
-                        const int iv = i - first_units(t) - 2;
+                        const int iv = i - 2 * t.n_steps - 2;
                         const int vs = iv >> 2, vp = iv & 3;
                         const bool tail = vs == t.n_steps - 1;
                         const bool is_v = iv >= 0 && (tail || vp == 0 || vp == 3);
@@ -644,9 +647,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 umma_if(go, tm + m * kKeys + part * 64, qm + off, km + off, idesc, kk > 0 ? 1u : 0u);
             }
         };
-        for (int x = e0; ok; x += stride) {
+        for (int x = e0; ok && x < e_end; x += stride) {
             Tile t;
-            if (!find_tile<G, MODE>(wk, a, x, rank, t, lane)) break;
+            if (!find_tile<G, MODE>(wk, a, x, rank, ranges, t, lane)) break;
             if (t.n_steps == 0) continue;
             if (*abort_flag) break;
             {
@@ -654,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int end = end_unit(t);
                 auto first_sweep = [&](int s, int m) -> bool {
                     // S_m is free: its last scores are in registers, and the weights over S_1 have been used
-                    if (s > 0 || (!kSecond && n > 0)) {
+                    if (s > 0) {
                         if (!wait_all(&bar[L::ST_READ + m], (reads - 1) & 1)) return false;
                     } else if (n > 0) {
                         if (m == 0 && !(wait_all(&bar[L::PV_DONE], (steps - 1) & 1) &&
@@ -689,24 +692,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return true;
                 };
                 ok = wait_all(&bar[L::Q_FULL], n & 1);
-                for (int s = 0; kFirst && s < S && ok; ++s, ++reads) ok = first_sweep(s, 0) && first_sweep(s, 1);
-                if constexpr (!kSecond) {
-                    umma_commit_if(go, &bar[L::Q_FREE]);
-                    ++n;
-                    continue;
-                }
+                for (int s = 0; s < S && ok; ++s, ++reads) ok = first_sweep(s, 0) && first_sweep(s, 1);
                 // second sweep: the first step's scores
-                if constexpr (kFirst) ok = ok && wait_all(&bar[L::ST_READ + 1], (reads - 1) & 1);
-                else if (n > 0) ok = ok && wait_all(&bar[L::S2_READ], (steps - 1) & 1);
-                ok = ok && unit(u);
+                ok = ok && wait_all(&bar[L::ST_READ + 1], (reads - 1) & 1) && unit(u);
                 if (ok) {
                     scores(1, u, 0, idesc_qk);
                     umma_commit_if(go, &bar[L::S2_FULL]);
                     release(u++);
-                    if constexpr (kFirst) ok = wait_all(&bar[L::ST_READ], (reads - 1) & 1);
-                    else if (n > 0)
-                        ok = wait_all(&bar[L::PV_DONE], (steps - 1) & 1) && wait_all(&bar[L::PV_DONE + 1], (steps - 1) & 1);
-                    ok = ok && unit(u);
+                    ok = wait_all(&bar[L::ST_READ], (reads - 1) & 1) && unit(u);
                 }
                 if (ok) {
                     scores(0, u, 0, idesc_half);
@@ -715,6 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     umma_commit_if(go, &bar[L::S1_FULL + 1]);
                     release(u++);
                     if (n > 0) ok = wait_all(&bar[L::O_FREE], (n - 1) & 1);
+                    // the statistics in O's columns have been read by all (each warp's scores come after its own)
+                    ok = ok && wait_all(&bar[L::S2_READ], steps & 1);
                 }
                 for (int s = 0; s < S && ok; ++s, ++steps) {
                     const bool more = s + 1 < S;
@@ -758,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ts = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t to = ts + kColO + grp * QD;
         uint64_t *quad = &bar[L::QUAD + quarter];
-        const float lam = kSecond ? diff_lambda<D>(a.w, lane) : 0.0f;
+        const float lam = diff_lambda<D>(a.w, lane);
         const float abs_lam = fabsf(lam);
         const float sign = lam < 0.0f ? 1.0f : -1.0f;  // of the second map's weights
         const bool rising = a.qscale >= 0.0f;          // the largest score has the largest q . k (else the smallest)
@@ -781,9 +776,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int first_id = -1;
         auto find_next = [&]() -> bool {
             for (;; x += stride) {
-                if (!find_tile<G, MODE>(wk, a, x, rank, tn, lane)) return false;
+                if ((!kPair && x >= e_end) || !find_tile<G, MODE>(wk, a, x, rank, ranges, tn, lane)) return false;
                 if (tn.bad_ctx && tid == 0 && tn.rt0 == 0 && tn.p == 0) atomicOr(a.err, PKV_DEVERR_CTX_RANGE);
-                if (tn.n_steps > 0) break;
+                if ((kPair ? tn.n_steps : tn.S) > 0) break;
             }
             x += stride;
             const int nb = tn.s0 * kStepBlocks + lane;
@@ -795,7 +790,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Tile t = tn;
             const int id0 = first_id;
             if (*abort_flag) break;
-            if constexpr (F8) {
+            const bool some = kPair || t.n_steps > 0;  // a range may be empty
+            if (F8 && some) {
                 if (!(ok = wait_all(&bar[L::Q_RAW], n & 1))) break;
                 convert_q<D>(base + L::kQ, warp, lane);
                 fence_proxy_async_smem();  // the MMAs read it through the async proxy
@@ -817,9 +813,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return __ballot_sync(kFull, lane < kStepBlocks && id >= 0 && id < a.num_blocks);
             };
             // ---- first sweep: maximum and sum of map m over this half's keys ----
-            [[maybe_unused]] float mx = -INFINITY, l = 0.0f;
+            float mx = -INFINITY, l = 0.0f;
             int nxt = id0;
-            for (int s = 0; kFirst && s < t.n_steps; ++s, ++gs) {
+            for (int s = 0; s < t.n_steps; ++s, ++gs) {
                 const uint32_t mask = mask_of(nxt) >> (4 * half);
                 if (s + 1 < t.n_steps) nxt = ids_of(s + 1);
                 if (!(ok = wait_all(&bar[L::ST_FULL + m], gs & 1))) break;
@@ -877,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- the row's statistics of both maps give the weights' factors ----
             float n0 = 0.0f, n1 = 0.0f, inv = 0.0f;  // weights 2^(s qs + n); o = inv * accumulator
             RowStat rs;
-            if constexpr (kFirst) {
+            if (some) {
                 uint32_t st[8] = {__float_as_uint(mx), __float_as_uint(l)};
                 tmem_st2(ts + kColStat + 2 * grp, st);
                 tmem_wait_st();
@@ -888,14 +884,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 rs.add(f(0), f(1), f(2), f(3));
                 rs.add(f(4), f(5), f(6), f(7));
             }
-            if constexpr (!kSecond) {  // the range's statistics, for the launch that forms the weights
-                if (grp == 0 && r < t.R) a.ws_stat[(int64_t)t.slot * kRows + row] = make_float4(rs.m1, rs.l1, rs.m2, rs.l2);
-                have = find_next();
-                if (!(ok = meet())) break;  // the four threads have read the columns before the next tile's are written
-                ++n;
-                continue;
+            if constexpr (!kPair) {  // every range's
+                if (grp == 0) {
+                    put_stat<L>(sm, row, rs.m1, rs.l1);
+                    put_stat<L>(sm, kRows + row, rs.m2, rs.l2);
+                    __syncwarp();
+                    if (lane < ranges) mbar_arrive_remote(&bar[L::STAT], lane);
+                }
+                if (!(ok = wait_all_cluster(&bar[L::STAT], 0))) break;
+                rs = RowStat{};
+                for (int k = 0; k < ranges; ++k) add_stat<L>(rs, base, row, k);
             }
-            if constexpr (!kFirst) rs = merged_stats(a, t, row, r < t.R);
             rs.factors(abs_lam, n0, n1, inv);
             // ---- second sweep: the weights of keys 32 grp .. + 31 of every step ----
             nxt = id0;
@@ -943,28 +942,80 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             // ---- norm and store: this thread's quarter of its row ----
             have = find_next();
-            if (!(ok = wait_all(&bar[L::O_FULL], n & 1))) break;
+            if (some && !(ok = wait_all(&bar[L::O_FULL], n & 1))) break;
             tc_fence_after();
-            if constexpr (!kFirst) {  // the range's part of o
-                const float vs = F8 ? a.scales[a.n_kv + 2 * t.p + half] : 1.0f;
-                float *dst = a.ws_o + ((int64_t)t.slot * kRows + row) * (2 * D) + grp * QD;
+            if constexpr (!kPair) {
+                // this range's part of the row into shared memory (the ring's, idle now), 16-byte pieces swizzled
+                float4 *part = reinterpret_cast<float4 *>(sm + L::kRing);
+                if (some) {
+                    const float vs = F8 ? a.scales[a.n_kv + 2 * t.p + half] : 1.0f;
 #pragma unroll
-                for (int c = 0; c < QD; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(to + c, o);
-                    tmem_wait_ld();
-                    if (r < t.R) {
+                    for (int c = 0; c < QD; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(to + c, o);
+                        tmem_wait_ld();
+                        if (r < t.R) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * vs);
-#pragma unroll
-                        for (int i = 0; i < 32; i += 8) stg256(dst + c + i, o + i);
+                            for (int i = 0; i < 8; ++i) {
+                                const int piece = (grp * QD + c) / 4 + i;
+                                part[row * (2 * D / 4) + (piece ^ (row & 7))] =
+                                    make_float4(__uint_as_float(o[4 * i]) * vs, __uint_as_float(o[4 * i + 1]) * vs,
+                                                __uint_as_float(o[4 * i + 2]) * vs, __uint_as_float(o[4 * i + 3]) * vs);
+                            }
+                        }
                     }
                 }
-                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[L::O_FREE]);
-                ++n;
-                continue;
+                if (lane < ranges) mbar_arrive_remote(&bar[L::PARTS], lane);
+                if (!(ok = wait_all_cluster(&bar[L::PARTS], 0))) break;
+                // rows rank, rank + ranges, ...: a warp adds the ranges' parts in order, normalises and stores
+                const int live = min(kRows, t.R - t.rt0);
+                for (int q = rank + warp * ranges; q < live; q += kSoftmaxWarps * ranges) {
+                    constexpr int KW = 2 * D / 128;
+                    float4 o[KW];
+#pragma unroll
+                    for (int c = 0; c < KW; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    RowStat all;
+                    for (int k = 0; k < ranges; ++k) {
+                        add_stat<L>(all, base, q, k);
+                        if (range_first(t.S, ranges, k) == range_first(t.S, ranges, k + 1)) continue;  // no steps
+#pragma unroll
+                        for (int c = 0; c < KW; ++c) {
+                            const int piece = lane + 32 * c;
+                            const float4 y = ld_cluster_f32x4(
+                                smem_of(base + L::kRing + (q * (2 * D / 4) + (piece ^ (q & 7))) * 16, k));
+                            o[c].x += y.x;
+                            o[c].y += y.y;
+                            o[c].z += y.z;
+                            o[c].w += y.w;
+                        }
+                    }
+                    float x0, x1, fac;
+                    all.factors(abs_lam, x0, x1, fac);
+                    float ss = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < KW; ++c) {
+                        o[c].x *= fac;
+                        o[c].y *= fac;
+                        o[c].z *= fac;
+                        o[c].w *= fac;
+                        ss += o[c].x * o[c].x + o[c].y * o[c].y + o[c].z * o[c].z + o[c].w * o[c].w;
+                    }
+#pragma unroll
+                    for (int s = 16; s >= 1; s >>= 1) ss += __shfl_xor_sync(kFull, ss, s);
+                    const float rn = a.w.out_scale * rsqrtf(ss * (1.0f / (2 * D)) + a.w.eps);
+                    const int rq = t.rt0 + q;
+                    __nv_bfloat16 *dst = a.out + (((int64_t)t.row0 + rq / G) * (a.n_q / 2) + t.p * G + rq % G) * (2 * D);
+#pragma unroll
+                    for (int c = 0; c < KW; ++c) {
+                        const int d = 4 * (lane + 32 * c);
+                        const float4 g = a.w.norm_weight ? __ldg(reinterpret_cast<const float4 *>(a.w.norm_weight + d))
+                                                         : make_float4(1.f, 1.f, 1.f, 1.f);
+                        *reinterpret_cast<uint2 *>(dst + d) = make_uint2(pack_bf16x2(o[c].x * rn * g.x, o[c].y * rn * g.y),
+                                                                         pack_bf16x2(o[c].z * rn * g.z, o[c].w * rn * g.w));
+                    }
+                }
+                break;
             }
             const float f = inv * (F8 ? a.scales[a.n_kv + 2 * t.p + half] : 1.0f);
             uint32_t o[QD];
@@ -1021,127 +1072,73 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     tc_fence_before();
     __syncthreads();  // every role is done with the tensor memory
-    if constexpr (kPair) cluster_sync();  // the other CTA's last commits and copies have reached this one
+    cluster_sync();   // the others' last commits, copies and reads of this CTA's shared memory are done
     tc_fence_after();
     if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
-// ------------------------------------------------------------- ranges joined
-
-constexpr int kJoinWarps = 8;
-
-// One warp per row of a tile: the ranges' parts of o added in order, normalised and stored.
-template <int D, int G>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ Args a)
-{
-    constexpr int KW = 2 * D / 128;  // 16-byte pieces of a row that a lane holds
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    griddep_wait();
-    griddep_launch_dependents();
-    Walker wk;
-    load_window<G, kWeights>(wk, a, lane);
-    const float abs_lam = fabsf(diff_lambda<D>(a.w, lane));
-    for (int x = blockIdx.x;; x += gridDim.x) {
-        Tile t;
-        if (!find_tile<G, kWeights>(wk, a, x * a.ranges, 0, t, lane)) break;
-        if (t.n_blocks == 0) continue;
-        const int S = (t.n_blocks + kStepBlocks - 1) / kStepBlocks;
-        const bool full = lane < a.ranges && range_first(S, a.ranges, lane) < range_first(S, a.ranges, lane + 1);
-        const uint32_t parts = __ballot_sync(kFull, full);  // the ranges that have steps (16 at most)
-        // rows of this tile, dealt to the CTAs of its column of the grid
-        for (int row = blockIdx.y * kJoinWarps + warp; row < min(kRows, t.R - t.rt0); row += gridDim.y * kJoinWarps) {
-            // lane k has range k's statistics
-            const float4 v = full ? __ldcg(a.ws_stat + (int64_t)(t.slot + lane) * kRows + row)
-                                  : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-            float4 o[KW];
-#pragma unroll
-            for (int c = 0; c < KW; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-            const float4 *src = reinterpret_cast<const float4 *>(a.ws_o + ((int64_t)t.slot * kRows + row) * (2 * D)) + lane;
-            constexpr int64_t kStep = (int64_t)kRows * 2 * D / 4;
-#pragma unroll 4
-            for (int k = 0; k < a.ranges; ++k) {
-                if (!((parts >> k) & 1u)) continue;
-#pragma unroll
-                for (int c = 0; c < KW; ++c) {
-                    const float4 y = __ldcg(src + k * kStep + 32 * c);
-                    o[c].x += y.x;
-                    o[c].y += y.y;
-                    o[c].z += y.z;
-                    o[c].w += y.w;
-                }
-            }
-            RowStat rs;
-            rs.add(v.x, v.y, v.z, v.w);
-#pragma unroll
-            for (int s = 8; s >= 1; s >>= 1)
-                rs.add(__shfl_xor_sync(kFull, rs.m1, s), __shfl_xor_sync(kFull, rs.l1, s), __shfl_xor_sync(kFull, rs.m2, s),
-                       __shfl_xor_sync(kFull, rs.l2, s));
-            RowStat all;
-            all.m1 = __shfl_sync(kFull, rs.m1, 0);
-            all.l1 = __shfl_sync(kFull, rs.l1, 0);
-            all.m2 = __shfl_sync(kFull, rs.m2, 0);
-            all.l2 = __shfl_sync(kFull, rs.l2, 0);
-            float n0, n1, inv;
-            all.factors(abs_lam, n0, n1, inv);
-            float ss = 0.0f;
-#pragma unroll
-            for (int c = 0; c < KW; ++c) {
-                o[c].x *= inv;
-                o[c].y *= inv;
-                o[c].z *= inv;
-                o[c].w *= inv;
-                ss += o[c].x * o[c].x + o[c].y * o[c].y + o[c].z * o[c].z + o[c].w * o[c].w;
-            }
-#pragma unroll
-            for (int s = 16; s >= 1; s >>= 1) ss += __shfl_xor_sync(kFull, ss, s);
-            const float rn = a.w.out_scale * rsqrtf(ss * (1.0f / (2 * D)) + a.w.eps);
-            const int r = t.rt0 + row;
-            __nv_bfloat16 *dst = a.out + (((int64_t)t.row0 + r / G) * (a.n_q / 2) + t.p * G + r % G) * (2 * D);
-#pragma unroll
-            for (int c = 0; c < KW; ++c) {
-                const int d = 4 * (lane + 32 * c);
-                const float4 g = a.w.norm_weight ? __ldg(reinterpret_cast<const float4 *>(a.w.norm_weight + d))
-                                                 : make_float4(1.f, 1.f, 1.f, 1.f);
-                *reinterpret_cast<uint2 *>(dst + d) = make_uint2(pack_bf16x2(o[c].x * rn * g.x, o[c].y * rn * g.y),
-                                                                 pack_bf16x2(o[c].z * rn * g.z, o[c].w * rn * g.w));
-            }
-        }
-    }
-}
-
 // ------------------------------------------------------------- launch
 
+// A launch of clusters of `size` CTAs.
 template <int D, int G, bool F8, int MODE>
-pkv_status launch_mode(pkv_pool *pool, const CUtensorMap &tm_q, int grid, const Args &a, cudaStream_t s)
-{
-    using L = Layout<D>;
-    static std::mutex mu;
-    static bool ready[64];
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        if (pool->device >= 64 || !ready[pool->device]) {
-            cudaError_t e = cudaFuncSetAttribute(diff_prefill_kernel<D, G, F8, MODE>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::bytes);
-            if (e != cudaSuccess) return cuda_fail(e, "paged_diff_prefill_attention: kernel attributes");
-            if (pool->device < 64) ready[pool->device] = true;
-        }
-    }
+struct ClusterLaunch {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = L::bytes;
-    cfg.stream = s;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = MODE == kWhole ? 2 : 1;
+    ClusterLaunch(int clusters, int size, cudaStream_t s)
+    {
+        cfg.gridDim = dim3(clusters * size);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = Layout<D>::bytes;
+        cfg.stream = s;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = size;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+    }
+};
+
+// Per device, found once: the kernel's attributes are set, and resident[i] clusters of 2^(i + 1) CTAs are
+// resident at once (kRange).
+template <int D, int G, bool F8, int MODE>
+pkv_status prepare(const pkv_pool *pool, int (&resident)[4])
+{
+    struct Known {
+        bool ready;
+        int resident[4];
+    };
+    static std::mutex mu;
+    static Known known[64];
+    std::lock_guard<std::mutex> lock(mu);
+    Known local = {}, *k = pool->device < 64 ? &known[pool->device] : &local;
+    if (!k->ready) {
+        auto kern = diff_prefill_kernel<D, G, F8, MODE>;
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::bytes);
+        if (e == cudaSuccess && MODE == kRange) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return cuda_fail(e, "paged_diff_prefill_attention: kernel attributes");
+        for (int i = 0; i < 4 && MODE == kRange; ++i) {
+            ClusterLaunch<D, G, F8, MODE> cl(1, 2 << i, nullptr);
+            cl.cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&k->resident[i], kern, &cl.cfg) != cudaSuccess) {
+                cudaGetLastError();  // a size the device does not take
+                k->resident[i] = 0;
+            }
+        }
+        k->ready = true;
+    }
+    for (int i = 0; i < 4; ++i) resident[i] = k->resident[i];
+    return PKV_OK;
+}
+
+template <int D, int G, bool F8, int MODE>
+pkv_status launch_mode(pkv_pool *pool, const CUtensorMap &tm_q, int clusters, int size, const Args &a, cudaStream_t s)
+{
+    ClusterLaunch<D, G, F8, MODE> cl(clusters, size, s);
     LaunchScope ls(pool, kDecode, s);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, diff_prefill_kernel<D, G, F8, MODE>, tm_q, pool->tm_block, a);
+    cudaError_t e = cudaLaunchKernelEx(&cl.cfg, diff_prefill_kernel<D, G, F8, MODE>, tm_q, pool->tm_block, a);
     ls.done();
     if (e != cudaSuccess) return cuda_fail(e, "paged_diff_prefill_attention launch");
     return PKV_OK;
@@ -1155,44 +1152,27 @@ int64_t most_tiles(int64_t n_rows, int G, int batch, int per)
     return begun + (n_rows * G - begun) / per;
 }
 
-// How many ranges to cut a tile's keys into: as many as give every SM a CTA (counting the most tiles the call
-// can have), none with less than one step of the longest sequence the table can hold, 16 at most.
-int ranges_of(const pkv_pool *pool, int64_t tiles, int W)
-{
-    const int64_t steps = (W + kStepBlocks - 1) / kStepBlocks;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, steps), pool->num_sms / std::max<int64_t>(1, tiles)));
-}
-
 template <int D, int G, bool F8>
-pkv_status launch(pkv_pool *pool, const void *q, Args a, cudaStream_t s)
+pkv_status launch(pkv_pool *pool, const void *q, const Args &a, cudaStream_t s)
 {
     CUtensorMap tm_q;
     pkv_status st = make_q_pair_map(&tm_q, q, a.n_rows, a.n_q, D, G, kRows / G);
     if (st != PKV_OK) return st;
     const int64_t tiles = most_tiles(a.n_rows, G, a.batch, kRows) * a.n_pairs;
     const int64_t pairs = most_tiles(a.n_rows, G, a.batch, 2 * kRows) * a.n_pairs;
-    a.ranges = ranges_of(pool, tiles, a.W);
-    if (a.ranges > 1) {
-        const size_t slots = (size_t)tiles * a.ranges;
-        const size_t stat_bytes = slots * kRows * sizeof(float4), bytes = stat_bytes + slots * kRows * 2 * D * sizeof(float);
-        // (a call that would have to allocate while its stream is captured runs whole instead)
-        if (ensure_workspace(pool, bytes, s, "paged_diff_prefill_attention") == PKV_OK) {
-            a.ws_stat = static_cast<float4 *>(pool->ws);
-            a.ws_o = reinterpret_cast<float *>(static_cast<uint8_t *>(pool->ws) + stat_bytes);
-            st = launch_mode<D, G, F8, kSums>(pool, tm_q, (int)slots, a, s);
-            if (st == PKV_OK) st = launch_mode<D, G, F8, kWeights>(pool, tm_q, (int)slots, a, s);
-            if (st != PKV_OK) return st;
-            LaunchScope ls(pool, kMerge, s);
-            cudaError_t e = launch_pdl(join_kernel<D, G>, dim3((unsigned)tiles, std::max(2, (int)(4 * pool->num_sms / tiles))),
-                                       dim3(kJoinWarps * 32), 0, s, a);
-            ls.done();
-            if (e != cudaSuccess) return cuda_fail(e, "paged_diff_prefill_attention: join launch");
-            return PKV_OK;
-        }
-        cudaGetLastError();  // a failed allocation is not this call's failure
-        a.ranges = 1;
+    const int64_t steps = (a.W + kStepBlocks - 1) / kStepBlocks;  // of the longest sequence the table can hold
+    int resident[4];
+    // ranges: the largest cluster of which all tiles' (counting the most the call can have) run at once
+    if (tiles <= pool->num_sms / 2 && steps > 1) {
+        st = prepare<D, G, F8, kRange>(pool, resident);
+        if (st != PKV_OK) return st;
+        for (int i = 3; i >= 0; --i)
+            if (tiles <= resident[i] && (2 << i) <= std::max<int64_t>(2, steps))
+                return launch_mode<D, G, F8, kRange>(pool, tm_q, (int)tiles, 2 << i, a, s);
     }
-    return launch_mode<D, G, F8, kWhole>(pool, tm_q, 2 * (int)std::min<int64_t>(pairs, pool->num_sms / 2), a, s);
+    st = prepare<D, G, F8, kWhole>(pool, resident);
+    if (st != PKV_OK) return st;
+    return launch_mode<D, G, F8, kWhole>(pool, tm_q, (int)std::min<int64_t>(pairs, pool->num_sms / 2), 2, a, s);
 }
 
 template <int D, bool F8>
@@ -1252,9 +1232,6 @@ extern "C" pkv_status paged_diff_prefill_attention(pkv_pool *pool, const void *q
     a.scales = pool->scales;
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.err = pool->err;
-    a.ranges = 1;
-    a.ws_stat = nullptr;
-    a.ws_o = nullptr;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool f8 = pool->dtype == PKV_FP8_E4M3;
     if (pool->d_head == 128)

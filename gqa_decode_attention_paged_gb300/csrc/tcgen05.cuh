@@ -128,6 +128,52 @@ __device__ __forceinline__ uint32_t cluster_rank()
     return r;
 }
 
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+// Address, in the cluster's shared memory, of what is at `addr` in CTA `rank`'s.
+__device__ __forceinline__ uint32_t smem_of(uint32_t addr, int rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float ld_cluster_bf16(uint32_t addr)
+{
+    uint16_t v;
+    asm volatile("ld.shared::cluster.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+    return __uint_as_float((uint32_t)v << 16);
+}
+
+// Arrive on the barrier at the same place in CTA `rank`; what this thread (and those it has synchronised with)
+// wrote is visible to the threads of the cluster that wait for the phase with wait_all_cluster.
+__device__ __forceinline__ void mbar_arrive_remote(uint64_t *bar, int rank)
+{
+    asm volatile("fence.acq_rel.cluster;\n\tmbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                     smem_of(smem_u32(bar), rank))
+                 : "memory");
+}
+
 // Every thread of the cluster is here, and what each wrote to shared memory before is visible to all.
 __device__ __forceinline__ void cluster_sync()
 {
@@ -289,6 +335,14 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
 __device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity)
 {
     return __all_sync(kFull, mbar_wait_bounded(bar, parity));
+}
+
+// wait_all for a barrier that other CTAs of the cluster arrive on.
+__device__ __forceinline__ bool wait_all_cluster(uint64_t *bar, uint32_t parity)
+{
+    const bool ok = wait_all(bar, parity);
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    return ok;
 }
 
 }  // namespace pkv

@@ -501,11 +501,11 @@ pkv_status paged_diff_decode_attention(pkv_pool *pool, const void *q, int32_t n_
  *              of no sequence, or of one that is skipped, stay as they were.
  * A block id outside the pool counts as masked and sets
  * PKV_DEVERR_BLOCK_RANGE; a row that sees nothing is zero.  Cached rows
- * behind C_b are never used, whatever they hold.  bf16 and FP8 pools, on the
- * tcgen05 tensor cores: one launch, or, where the call's rows fill few tiles
- * of 128 (short chunks, few sequences), three that cut the keys into ranges
- * and use the pool's workspace (a call that would have to grow it while
- * `stream` is captured runs as one launch instead).
+ * behind C_b are never used, whatever they hold.  bf16 and FP8 pools; one
+ * launch on the tcgen05 tensor cores, no workspace.  Where the call's rows
+ * fill few tiles of 128 (short chunks, few sequences), several thread blocks
+ * share a tile's keys; results of a call do not depend on timing, but may
+ * differ in rounding between calls of different batch sizes.
  * Errors: EINVAL, EUNSUPPORTED (4-bit pools, odd n_kv, group size, 2^31 query
  * rows x group size or more), ECUDA. */
 pkv_status paged_diff_prefill_attention(pkv_pool *pool, const void *q, int64_t n_rows, int32_t n_q,
@@ -515,8 +515,7 @@ pkv_status paged_diff_prefill_attention(pkv_pool *pool, const void *q, int64_t n
 
 /* Grow the pool's workspace now, so that later paged_diff_decode_attention
  * calls with at most `batch` sequences, `n_q` query heads and
- * `max_blocks_per_seq` table entries, and any paged_diff_prefill_attention
- * call, allocate nothing and may be captured.
+ * `max_blocks_per_seq` table entries allocate nothing and may be captured.
  * Memory that captured graphs may use stays valid: a workspace that is
  * replaced by a larger one is kept until the pool is destroyed.  Graphs of
  * one pool share its workspace: replay them one after the other.
