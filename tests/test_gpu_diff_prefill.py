@@ -140,6 +140,32 @@ def test_diff_prefill_one_map_sharp_the_other_flat(kv, pad):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("pad", [0, PAD])
+def test_diff_prefill_scores_of_large_magnitude(pad):
+    """Scores of +-32768: a map's weights lie on a few equal keys, or on all of them, far below zero.
+
+    The scores are exact, but four sums take place at their size in units of log2 (s - m, twice; the factor's
+    exponent; m with the part of log2(l) that is not passed on): each is off by 2^-24 of it at most, and so is
+    the exponent.  The bound's 2^-12 is for small scores; this is added to it."""
+    d, lens, chunks = 64, [4000, 90], [20, 60]
+    with Cache("bf16", 2, d, lens, seed=14) as c:
+        c.k[..., 0] = -1
+        for j in (3, 60, 200):
+            c.k[int(c.tables[0, j]), :, j % BS, 0] = 1
+        c.k64 = c.k.double()
+        c.upload()
+        q, params = torch.zeros(80, 8, d, dtype=torch.bfloat16, device="cuda"), weights(d)
+        for h in range(8):
+            q[:, h, 0] = 2.0 ** 18 * (-1 if h % 3 else 1)
+        got = prefill(c, q, chunks, params, pad=pad)
+        torch.cuda.synchronize()
+        ref, bound = plain(c, q, ptr(chunks), lens, 1 / np.sqrt(d), params)
+        exact = 2.0 ** -8 + 2.0 ** -12
+        extra = 4 * 2.0 ** -24 * 32768  # (log2 units x ln 2)
+        check(got, ref, bound * (exact + extra) / exact, norm2=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("pad", [0, PAD])
 def test_diff_prefill_bad_blocks_are_masked_and_flagged(pad):
     lens, chunks = [300, 64, 200], [150, 20, 200]
     with Cache("bf16", 2, 64, lens, seed=2) as c:
