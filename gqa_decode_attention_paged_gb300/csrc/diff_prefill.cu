@@ -75,8 +75,17 @@ constexpr int kStepBlocks = kKeys / kBlockSize;
 constexpr int kVKeys = 64;  // keys of a V unit
 constexpr int kUnitBlocks = kVKeys / kBlockSize;
 constexpr int kSoftmaxWarps = 16;
-constexpr int kCopyWarp = 16, kMmaWarp = 17, kPrepWarp = 18;  // kPrepWarp and the next
-constexpr int kThreads = 20 * 32;
+constexpr int kCopyWarp = 16, kScoreWarp = 17, kPrepWarp = 18;
+template <bool F8>
+struct Warps {
+    static constexpr int kPreps = F8 ? 4 : 1;  // warps kPrepWarp .. make units ready
+    static constexpr int kProduct = kPrepWarp + kPreps;
+    static constexpr int kThreads = (F8 ? 24 : 20) * 32;
+    // FP8 pools: registers a thread at the launch, then of the warps on scores and of the others
+    static constexpr int kLaunchRegs = 80, kScoreRegs = 96, kWorkRegs = 48;
+    static_assert(kSoftmaxWarps * kScoreRegs + (24 - kSoftmaxWarps) * kWorkRegs <= 24 * kLaunchRegs,
+                  "more registers than the launch has");
+};
 // Tensor memory: S_1 at 0, S_2 at 128 (fp32 scores of 128 keys; the weights of keys 32 g .. + 31, packed in
 // pairs, over the first 16 columns of their S_1), O at 256 (2 d).  While a tile has no product in O yet, its
 // columns kColStat + 2 g hold thread g's (m, l); when O is in registers, the first column of each thread's
@@ -365,17 +374,18 @@ __device__ __forceinline__ void add_stat(RowStat &rs, uint32_t base, int row, in
 // ------------------------------------------------------------- the kernel
 
 template <int D, int G, bool F8, int MODE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
     diff_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
                         const __grid_constant__ Args a)
 {
     using L = Layout<D>;
     constexpr int NH = D / 64;  // 64-column ranges of a row
     constexpr int NS = L::kStages;
-    // FP8 pools: at d_head 128 the two preparing warps take half of every unit, at 64 (where a K unit's
-    // rows overlap in place) every other unit; NS is even there, so a warp sees every phase of its slots
-    constexpr bool kSplit = F8 && D == 128;
-    static_assert(!F8 || kSplit || NS % 2 == 0, "a preparing warp would miss phases of its slots");
+    using Wp = Warps<F8>;
+    // FP8 pools: the preparing warps take a quarter of every unit at d_head 128, and half of every other unit at 64
+    // (NS is even there, so a warp sees every phase of its slots)
+    constexpr int kSplit = !F8 ? 1 : D == 128 ? 4 : 2;  // warps on a unit
+    static_assert(Wp::kPreps == kSplit || NS % 2 == 0, "a preparing warp would miss phases of its slots");
     extern __shared__ __align__(1024) uint8_t dp_smem[];
     uint8_t *sm = dp_smem + ((1024u - (smem_u32(dp_smem) & 1023u)) & 1023u);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::kBar);
@@ -404,15 +414,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i == L::S2_READ || i == L::O_FREE) n = kSoftmaxWarps;
             if (i >= L::QUAD && i < L::QUAD + 4) n = 4;  // the four warps of a lane quarter
             if (i == L::Q_FULL && F8) n = kSoftmaxWarps;  // each widens its share of the queries
-            if (i >= L::FULL && i < L::EMPTY && kSplit) n = 2;
+            if (i >= L::FULL && i < L::EMPTY) n = kSplit;
             if (i >= L::EMPTY && i < L::EMPTY + NS && kPair) n = 2;  // both CTAs have used the slot
             if (i == L::STAT) n = 4 * ranges;              // of every CTA, the warps that hold a row's statistics
             if (i == L::PARTS) n = kSoftmaxWarps * ranges;
+            if (i == L::DRAIN) n = 2;
             mbar_init(&bar[i], n);
             fence_mbarrier_init();
         }
     }
-    if (warp == kMmaWarp) {
+    if (warp == kScoreWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(sm + L::kTmemSlot)),
                      "r"(kTmemCols)
@@ -434,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     };
     if constexpr (kPair) {
-        for (int i = tid; i < 2 * D; i += kThreads)
+        for (int i = tid; i < 2 * D; i += Wp::kThreads)
             reinterpret_cast<float *>(sm + L::kNorm)[i] = a.w.norm_weight ? a.w.norm_weight[i] : 1.0f;
         __syncthreads();
     }
@@ -442,6 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     load_window<G, MODE>(wk, a, lane);
     const uint32_t base = smem_u32(sm);
 
+    if (warp >= kSoftmaxWarps) {
+    if constexpr (F8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Wp::kWorkRegs));
     if (warp == kCopyWarp) {
         // ---------------------------------------------------------- copies
         const uint64_t policy = l2_policy_evict_normal();
@@ -494,6 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (kPair) tma_load_2d_multicast_if(go, to, &tm_kv, c, y, land, kBoth, policy);
                 else tma_load_2d_if(go, to, &tm_kv, c, y, land, policy);
             };
+            constexpr int kTileRows = D == 128 ? kKeys : kVKeys;  // of a K unit's tiles, FP8 pools
             constexpr int kShare = kPair ? 2 : 1;  // this CTA's blocks of a unit: every kShare-th
             auto copy_k = [&](int y0, int m) -> bool {
                 uint32_t land, dst;
@@ -504,7 +518,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int yk = __shfl_sync(kFull, y0, k);
                     const int y = yk == a.oob_row ? yk : yk + m * 2 * kBlockSize;
                     if constexpr (F8) {
-                        copy_box(dst + L::UT / 2 + k * (kBlockSize * D), 0, y, land);
+                        copy_box(dst + (k * kBlockSize / kTileRows) * (kTileRows * 2 * D) + kTileRows * D +
+                                     (k * kBlockSize % kTileRows) * D,
+                                 0, y, land);
                     } else {
 #pragma unroll
                         for (int h = 0; h < NH; ++h)
@@ -559,10 +575,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = wait_all(&bar[L::EMPTY + i % NS], (i / NS) & 1);
         if (n > 0) mbar_wait_bounded(&bar[F8 ? L::Q_RAW : L::Q_FULL], (n - 1) & 1);
         if (!ok) set_abort();
-    } else if (warp >= kPrepWarp) {
+    } else if (warp >= kPrepWarp && warp < Wp::kProduct) {
         // ---------------------------------------------------------- units made ready
         const int which = warp - kPrepWarp;
-        if (F8 || which == 0) {
+        {
             int u = 0, ends = 0;
             bool ok = true;
             for (int x = e0; ok && x < e_end; x += stride) {
@@ -571,10 +587,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (t.n_steps == 0) continue;
                 if (*abort_flag) break;
                 // the V unit the sequence ends inside of: zero the rows behind the end (value heads h0 ..)
-                const int end = end_unit(t);
+                const int end = end_unit(t), end_row = (t.C / kBlockSize % kUnitBlocks) * kBlockSize;
                 auto clear = [&](uint32_t unit, int h0, int heads) {
-                    const int r0 = (t.C / kBlockSize % kUnitBlocks) * kBlockSize;
-                    const int first = r0 + t.C % kBlockSize, rows = r0 + kBlockSize - first;
+                    const int first = end_row + t.C % kBlockSize, rows = end_row + kBlockSize - first;
                     for (int e = lane; e < rows * 8 * heads * NH; e += 32) {
                         const int row = first + (e >> 3) % rows, ch = h0 * NH + (e >> 3) / rows;
                         sts128(unit + ch * kVChunk + row * 128 + (e & 7) * 16, make_uint4(0, 0, 0, 0));
@@ -595,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     for (int i = 0; i < 6 * t.n_steps; ++i, ++u) {
                         const int st = u % NS;
-                        if (!kSplit && (u & 1) != which) continue;
+                        if (D == 64 && (u & 1) != which >> 1) continue;
                         if (!(ok = wait_all(&bar[L::RAW + st], (u / NS) & 1))) break;
                         // second sweep: K, K of the first step, then of each step V, K, K, V (the next step's
                         // keys; the last step has V, V)
@@ -605,12 +620,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const bool is_v = iv >= 0 && (tail || vp == 0 || vp == 3);
                         const int vh = vp != 0;  // the V unit's half
                         const uint32_t unit = base + L::kRing + st * L::UT;
-                        if (is_v) {
-                            if (!kSplit || which == 0) convert_f16<D, kVKeys>(unit, lane, 0, kVKeys);
-                            if (!kSplit || which == 1) convert_f16<D, kVKeys>(unit + NH * kVChunk, lane, 0, kVKeys);
-                            if (2 * vs + vh == end) clear(unit, kSplit ? which : 0, kSplit ? 1 : 2);
-                        } else {
-                            convert_f16<D, kKeys>(unit, lane, kSplit ? which * (kKeys / 2) : 0, kSplit ? kKeys / 2 : kKeys);
+                        if constexpr (D == 128) {  // this warp's 32 rows
+                            if (is_v) {
+                                const int head = which >> 1, row0 = (which & 1) * 32;
+                                convert_f16<D, kVKeys>(unit + head * NH * kVChunk, lane, row0, 32);
+                                if (2 * vs + vh == end && end_row / 32 == (which & 1)) clear(unit, head, 1);
+                            } else {
+                                convert_f16<D, kKeys>(unit, lane, which * 32, 32);
+                            }
+                        } else {  // half of the keys, or a value head
+                            convert_f16<D, kVKeys>(unit + (which & 1) * kVChunk, lane, 0, kVKeys);
+                            if (is_v && 2 * vs + vh == end) clear(unit, which & 1, 1);
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
@@ -620,132 +640,148 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) set_abort();
         }
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kScoreWarp || warp == Wp::kProduct) {
         // ---------------------------------------------------------- S_m = Q_m K_m^T and O += W V
         constexpr uint32_t idesc_qk = mma_idesc(kRows, kKeys, 0, F8), idesc_half = mma_idesc(kRows, 64, 0, F8);
         constexpr uint32_t idesc_pv = mma_idesc(kRows, 2 * D, 1, F8);
         const uint64_t qd = smem_desc(base + L::kQ, 16, 1024), kd = smem_desc(base + L::kRing, 16, 1024);
         const uint64_t vd = smem_desc(base + L::kRing, kVChunk, 1024);
-        int u = 0, n = 0;               // the ring's next unit, tiles
+        int slot = 0, n = 0;  // of the ring's next unit; tiles
+        uint32_t ph = 0;      // the parity of its phase
         int reads = 0, steps = 0, ends = 0;  // first- and second-sweep steps, sequence ends
-        bool ok = true;
         const uint32_t go = elect_one();
         const uint32_t tm = __shfl_sync(kFull, tmem, 0);
-        auto unit = [&](int v) -> bool { return wait_all(&bar[L::FULL + v % NS], (v / NS) & 1); };
-        // ring unit v has been used when the MMAs so far have run
-        auto release = [&](int v) {
-            if constexpr (kPair) umma_commit_multicast_if(go, &bar[L::EMPTY + v % NS], kBoth);
-            else umma_commit_if(go, &bar[L::EMPTY + v % NS]);
+        auto skip = [&](int k) {
+            slot += k;
+            if (slot >= NS) {
+                slot -= NS;
+                ph ^= 1u;
+            }
         };
-        // keys [64 part, 64 part + N) of ring unit v against map m's queries
-        auto scores = [&](int m, int v, int part, uint32_t idesc) {
+        // A slot's barrier has a phase per use.  The two warps wait each for its own units alone, and
+        // after what tells it that the slot's use before had been filled: the NS-th unit before is older than
+        // those that the weights (or the products) it has just waited for were made from.
+        auto unit = [&]() -> bool { return wait_all(&bar[L::FULL + slot], ph); };
+        // the unit in slot v has been used when this warp's MMAs so far have run
+        auto release = [&](int v) {
+            if constexpr (kPair) umma_commit_multicast_if(go, &bar[L::EMPTY + v], kBoth);
+            else umma_commit_if(go, &bar[L::EMPTY + v]);
+        };
+        // keys [64 half, 64 half + N) of the unit in slot v against map m's queries
+        auto scores = [&](int m, int v, int half, uint32_t idesc) {
             tc_fence_after();
-            const uint64_t qm = qd + ((m * L::QT) >> 4), km = kd + ((v % NS * L::UT + part * 64 * 128) >> 4);
+            const uint64_t qm = qd + ((m * L::QT) >> 4), km = kd + ((v * L::UT + half * 64 * 128) >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off = ((kk >> 2) * kKHalf + (kk & 3) * 32) >> 4;
-                umma_if(go, tm + m * kKeys + part * 64, qm + off, km + off, idesc, kk > 0 ? 1u : 0u);
+                umma_if(go, tm + m * kKeys + half * 64, qm + off, km + off, idesc, kk > 0 ? 1u : 0u);
             }
         };
-        for (int x = e0; ok && x < e_end; x += stride) {
-            Tile t;
-            if (!find_tile<G, MODE>(wk, a, x, rank, ranges, t, lane)) break;
-            if (t.n_steps == 0) continue;
-            if (*abort_flag) break;
-            {
-                const int S = __shfl_sync(kFull, t.n_steps, 0);
-                const int end = end_unit(t);
-                auto first_sweep = [&](int s, int m) -> bool {
-                    // S_m is free: its last scores are in registers, and the weights over S_1 have been used
-                    if (s > 0) {
-                        if (!wait_all(&bar[L::ST_READ + m], (reads - 1) & 1)) return false;
-                    } else if (n > 0) {
-                        if (m == 0 && !(wait_all(&bar[L::PV_DONE], (steps - 1) & 1) &&
-                                        wait_all(&bar[L::PV_DONE + 1], (steps - 1) & 1)))
-                            return false;
-                        if (m == 1 && !wait_all(&bar[L::S2_READ], (steps - 1) & 1)) return false;
-                    }
-                    if (!unit(u)) return false;
-                    scores(m, u, 0, idesc_qk);
-                    umma_commit_if(go, &bar[L::ST_FULL + m]);
-                    release(u++);
-                    return true;
-                };
-                auto product = [&](int s, int h) -> bool {
-                    const int v = u++;
-                    if (!unit(v)) return false;
-                    if (!F8 && 2 * s + h == end) {
-                        if (go) mbar_arrive(&bar[L::END_ASK]);
-                        __syncwarp();
-                        if (!wait_all(&bar[L::END_CLEAR], ends & 1)) return false;
-                        ++ends;
-                    }
-                    if (!wait_all(&bar[L::P_FULL + h], steps & 1)) return false;
-                    tc_fence_after();
-                    const uint64_t vm = vd + ((v % NS * L::UT) >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < kVKeys / 16; ++kk)
-                        umma_ts_if(go, tm + kColO, tm + h * kVKeys + (kk >> 1) * 32 + (kk & 1) * 8, vm + ((kk * 2048) >> 4),
-                                idesc_pv, (s > 0 || h > 0 || kk > 0) ? 1u : 0u);
-                    release(v);
-                    umma_commit_if(go, &bar[L::PV_DONE + h]);
-                    return true;
-                };
-                ok = wait_all(&bar[L::Q_FULL], n & 1);
-                for (int s = 0; s < S && ok; ++s, ++reads) ok = first_sweep(s, 0) && first_sweep(s, 1);
-                // second sweep: the first step's scores
-                ok = ok && wait_all(&bar[L::ST_READ + 1], (reads - 1) & 1) && unit(u);
-                if (ok) {
-                    scores(1, u, 0, idesc_qk);
-                    umma_commit_if(go, &bar[L::S2_FULL]);
-                    release(u++);
-                    ok = wait_all(&bar[L::ST_READ], (reads - 1) & 1) && unit(u);
-                }
-                if (ok) {
-                    scores(0, u, 0, idesc_half);
-                    umma_commit_if(go, &bar[L::S1_FULL]);
-                    scores(0, u, 1, idesc_half);
-                    umma_commit_if(go, &bar[L::S1_FULL + 1]);
-                    release(u++);
-                    if (n > 0) ok = wait_all(&bar[L::O_FREE], (n - 1) & 1);
-                    // the statistics in O's columns have been read by all (each warp's scores come after its own)
-                    ok = ok && wait_all(&bar[L::S2_READ], steps & 1);
-                }
-                for (int s = 0; s < S && ok; ++s, ++steps) {
-                    const bool more = s + 1 < S;
-                    int k1 = 0;  // the next step's K_1 unit
-                    if (!(ok = product(s, 0))) break;
-                    if (more) {
-                        if (!(ok = wait_all(&bar[L::S2_READ], steps & 1) && unit(u))) break;
-                        scores(1, u, 0, idesc_qk);
-                        umma_commit_if(go, &bar[L::S2_FULL]);
-                        release(u++);
-                        k1 = u++;
-                        if (!(ok = wait_all(&bar[L::PV_DONE], steps & 1) && unit(k1))) break;
-                        scores(0, k1, 0, idesc_half);
-                        umma_commit_if(go, &bar[L::S1_FULL]);
-                    } else {
-                        umma_commit_if(go, &bar[L::Q_FREE]);
-                    }
-                    if (!(ok = product(s, 1))) break;
-                    if (more) {
-                        if (!(ok = wait_all(&bar[L::PV_DONE + 1], steps & 1))) break;
-                        scores(0, k1, 1, idesc_half);
-                        umma_commit_if(go, &bar[L::S1_FULL + 1]);
-                        release(k1);
-                    } else {
-                        umma_commit_if(go, &bar[L::O_FULL]);
-                    }
-                }
+        // all of map m's scores of a step
+        auto whole = [&](int m, uint64_t *full) -> bool {
+            if (!unit()) return false;
+            scores(m, slot, 0, idesc_qk);
+            umma_commit_if(go, full);
+            release(slot);
+            skip(1);
+            return true;
+        };
+        auto first_sweep = [&](int s, int m) -> bool {
+            // S_m is free: its last scores are in registers, and the weights over S_1 have been used
+            if (s > 0) {
+                if (!wait_all(&bar[L::ST_READ + m], (reads - 1) & 1)) return false;
+            } else if (n > 0) {
+                if (m == 0 && !(wait_all(&bar[L::PV_DONE], (steps - 1) & 1) && wait_all(&bar[L::PV_DONE + 1], (steps - 1) & 1)))
+                    return false;
+                if (m == 1 && !wait_all(&bar[L::S2_READ], (steps - 1) & 1)) return false;
             }
-            ++n;
-        }
+            return whole(m, &bar[L::ST_FULL + m]);
+        };
+        // map 1's scores of a half, in the second sweep
+        auto half_of = [&](int half) {
+            scores(0, slot, half, idesc_half);
+            umma_commit_if(go, &bar[L::S1_FULL + half]);
+            if (half == 1) release(slot);
+        };
+        auto product = [&](int s, int h, int end) -> bool {
+            // (before the unit's wait, see there)
+            if (!wait_all(&bar[L::P_FULL + h], steps & 1)) return false;
+            if (s == 0 && h == 0 && !wait_all(&bar[L::O_FREE], n & 1)) return false;
+            if (!unit()) return false;
+            if (!F8 && 2 * s + h == end) {
+                if (go) mbar_arrive(&bar[L::END_ASK]);
+                __syncwarp();
+                if (!wait_all(&bar[L::END_CLEAR], ends & 1)) return false;
+                ++ends;
+            }
+            tc_fence_after();
+            const uint64_t vm = vd + ((slot * L::UT) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kVKeys / 16; ++kk)
+                umma_ts_if(go, tm + kColO, tm + h * kVKeys + (kk >> 1) * 32 + (kk & 1) * 8, vm + ((kk * 2048) >> 4), idesc_pv,
+                           (s > 0 || h > 0 || kk > 0) ? 1u : 0u);
+            umma_commit_if(go, &bar[L::PV_DONE + h]);
+            release(slot);
+            skip(1);
+            return true;
+        };
+        auto walk = [&](auto on_scores) -> bool {
+            constexpr bool kScores = decltype(on_scores)::value;
+            for (int x = e0; x < e_end; x += stride) {
+                Tile t;
+                if (!find_tile<G, MODE>(wk, a, x, rank, ranges, t, lane)) break;
+                if (t.n_steps == 0) continue;
+                if (*abort_flag) break;
+                const int S = __shfl_sync(kFull, t.n_steps, 0);
+                if constexpr (kScores) {
+                    if (!wait_all(&bar[L::Q_FULL], n & 1)) return false;
+                    for (int s = 0; s < S; ++s, ++reads)
+                        if (!(first_sweep(s, 0) && first_sweep(s, 1))) return false;
+                    // second sweep: the first step's scores
+                    if (!(wait_all(&bar[L::ST_READ + 1], (reads - 1) & 1) && whole(1, &bar[L::S2_FULL]))) return false;
+                    if (!(wait_all(&bar[L::ST_READ], (reads - 1) & 1) && unit())) return false;
+                    half_of(0);
+                    half_of(1);
+                    skip(1);
+                    for (int s = 0; s + 1 < S; ++s, ++steps) {
+                        skip(1);  // V
+                        if (!(wait_all(&bar[L::S2_READ], steps & 1) && whole(1, &bar[L::S2_FULL]))) return false;
+                        if (!(wait_all(&bar[L::PV_DONE], steps & 1) && unit())) return false;
+                        half_of(0);
+                        if (!wait_all(&bar[L::PV_DONE + 1], steps & 1)) return false;
+                        half_of(1);
+                        skip(2);  // and V
+                    }
+                    umma_commit_if(go, &bar[L::Q_FREE]);
+                    ++steps;
+                    skip(2);  // V, V
+                } else {
+                    const int end = end_unit(t);
+                    const int at = (slot + (int)ph * NS + 2 * S + 2) % (2 * NS);  // the first sweep's keys, the first step's
+                    slot = at % NS;
+                    ph = at >= NS;
+                    for (int s = 0; s < S; ++s, ++steps) {
+                        if (!product(s, 0, end)) return false;
+                        if (s + 1 < S) skip(2);  // keys
+                        if (!product(s, 1, end)) return false;
+                    }
+                    umma_commit_if(go, &bar[L::O_FULL]);
+                }
+                ++n;
+            }
+            return true;
+        };
+        bool ok;
+        if (warp == kScoreWarp) ok = walk(std::true_type{});
+        else ok = walk(std::false_type{});
         umma_commit_if(go, &bar[L::DRAIN]);
         __syncwarp();
         mbar_wait_bounded(&bar[L::DRAIN], 0);
         if (!ok) set_abort();
+    }
     } else {
         // ---------------------------------------------------------- statistics, weights, norm
+        if constexpr (F8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Wp::kScoreRegs));
         const int quarter = warp & 3, grp = warp >> 2;  // TMEM lanes 32 quarter ..; which of the row's four threads
         const int m = grp & 1, half = grp >> 1;         // first sweep: map, half of a step's keys
         constexpr int QD = D / 2;                       // a thread's channels of the row (of value head grp / 2)
@@ -883,6 +919,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto f = [&](int i) { return __uint_as_float(st[i]); };
                 rs.add(f(0), f(1), f(2), f(3));
                 rs.add(f(4), f(5), f(6), f(7));
+                // O is free: the statistics in its columns, and the tile before, are in registers
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[L::O_FREE]);
             }
             if constexpr (!kPair) {  // every range's
                 if (grp == 0) {
@@ -903,26 +943,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (s + 1 < t.n_steps) nxt = ids_of(s + 1);
                 const int key0 = (t.s0 + s) * kKeys + 32 * grp;
                 const bool all = __all_sync(kFull, mh == 3u && key0 + 31 <= pos);
+                // map 2's weights first: its scores are there before map 1's, and their place is wanted soonest
                 if (!(ok = wait_all(&bar[L::S2_FULL], ps & 1))) break;
-                if (!(ok = wait_all(&bar[L::S1_FULL + half], ps & 1))) break;
                 tc_fence_after();
                 uint32_t s0[32], s1[32];
                 tmem_ld32(ts + kKeys + 32 * grp, s1);
-                tmem_ld32(ts + 32 * grp, s0);
                 tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[L::S2_READ]);
+                float2 w2[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 u1 = ffma2(make_float2(__uint_as_float(s1[2 * i]), __uint_as_float(s1[2 * i + 1])),
+                                            make_float2(qs1, qs1), make_float2(n1, n1));
+                    w2[i] = make_float2(ex2(u1.x), ex2(u1.y));
+                }
+                if (!(ok = wait_all(&bar[L::S1_FULL + half], ps & 1))) break;
+                tc_fence_after();
+                tmem_ld32(ts + 32 * grp, s0);
+                tmem_wait_ld();
                 uint32_t pk[16];
                 auto weigh = [&](auto masked) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float2 u0 = ffma2(make_float2(__uint_as_float(s0[2 * i]), __uint_as_float(s0[2 * i + 1])),
                                                 make_float2(qs0, qs0), make_float2(n0, n0));
-                        const float2 u1 = ffma2(make_float2(__uint_as_float(s1[2 * i]), __uint_as_float(s1[2 * i + 1])),
-                                                make_float2(qs1, qs1), make_float2(n1, n1));
-                        float2 w = ffma2(make_float2(ex2(u1.x), ex2(u1.y)), make_float2(sign, sign),
-                                         make_float2(ex2(u0.x), ex2(u0.y)));
+                        float2 w = ffma2(w2[i], make_float2(sign, sign), make_float2(ex2(u0.x), ex2(u0.y)));
                         if constexpr (decltype(masked)::value) {
                             const bool seen = (mh >> (2 * i / kBlockSize)) & 1u;
                             if (!(seen && key0 + 2 * i <= pos)) w.x = 0.0f;
@@ -1042,9 +1089,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_ld();
                 ss = (__uint_as_float(y[0]) + __uint_as_float(y[1])) + (__uint_as_float(y[2]) + __uint_as_float(y[3]));
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[L::O_FREE]);
             const float rn = a.w.out_scale * rsqrtf(ss * (1.0f / (2 * D)) + a.w.eps);
             if (r < t.R) {
                 const int64_t tok = (int64_t)t.row0 + r / G;
@@ -1074,7 +1118,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();  // every role is done with the tensor memory
     cluster_sync();   // the others' last commits, copies and reads of this CTA's shared memory are done
     tc_fence_after();
-    if (warp == kMmaWarp)
+    if (warp == kScoreWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
@@ -1088,7 +1132,7 @@ struct ClusterLaunch {
     ClusterLaunch(int clusters, int size, cudaStream_t s)
     {
         cfg.gridDim = dim3(clusters * size);
-        cfg.blockDim = dim3(kThreads);
+        cfg.blockDim = dim3(Warps<F8>::kThreads);
         cfg.dynamicSmemBytes = Layout<D>::bytes;
         cfg.stream = s;
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1118,7 +1162,12 @@ pkv_status prepare(const pkv_pool *pool, int (&resident)[4])
         auto kern = diff_prefill_kernel<D, G, F8, MODE>;
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::bytes);
         if (e == cudaSuccess && MODE == kRange) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        cudaFuncAttributes fa;
+        if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kern);
         if (e != cudaSuccess) return cuda_fail(e, "paged_diff_prefill_attention: kernel attributes");
+        // (with fewer registers at the launch, the warps on scores would wait for theirs)
+        if (F8 && fa.numRegs < Warps<F8>::kLaunchRegs)
+            return fail(PKV_EUNSUPPORTED, "paged_diff_prefill_attention: built with %d registers a thread", fa.numRegs);
         for (int i = 0; i < 4 && MODE == kRange; ++i) {
             ClusterLaunch<D, G, F8, MODE> cl(1, 2 << i, nullptr);
             cl.cfg.numAttrs = 1;
