@@ -102,6 +102,7 @@ struct Args {
     int W;
     const int32_t *context_lens;
     int batch, n_q, n_kv, n_pairs;
+    int window;           // sequences whose tiles are ordered among themselves (32 at most)
     int64_t num_blocks, n_rows;
     int oob_row;          // a row index past the end of the pool's entry rows (zero-filled box)
     float qscale;         // scale * log2(e)
@@ -226,7 +227,7 @@ struct Tile {
     int s0, S;              // its first step; the tile's steps
 };
 
-// A window of 32 sequences, one per lane: each warp walks the list itself, with the same arithmetic.  The list's
+// A window of 32 sequences or fewer, one per lane: each warp walks the list itself, with the same arithmetic.  The list's
 // entries are tiles, sequence by sequence, pair by pair (kRange), or pairs of tiles, within a window those of the
 // most steps first (kWhole): dealt out in turns, there and back, they give every cluster close to the same work
 // (the 880 entries of 16 prompts of 700 .. 1024 tokens: the longest cluster has 2 % more than the mean, 14 % in the
@@ -277,7 +278,7 @@ __device__ __forceinline__ void load_window(Walker &w, const Args &a, int lane)
 {
     const int bl = w.wb + lane;
     w.row0 = w.T = w.C = w.left = 0;
-    if (bl < a.batch) {
+    if (lane < a.window && bl < a.batch) {
         const int32_t lo = a.qo_indptr[bl], hi = a.qo_indptr[bl + 1];
         if (lo < 0 || hi < lo || hi > a.n_rows) {  // rows that are not the caller's: skip the sequence
             atomicOr(a.err, PKV_DEVERR_CTX_RANGE);
@@ -305,9 +306,9 @@ template <int G, int MODE>
 __device__ __forceinline__ bool find_tile(Walker &w, const Args &a, int x, int rank, int ranges, Tile &t, int lane)
 {
     while (x >= w.wbase + w.tot) {
-        if (w.wb + 32 >= a.batch) return false;
+        if (w.wb + a.window >= a.batch) return false;
         w.wbase += w.tot;
-        w.wb += 32;
+        w.wb += a.window;
         load_window<G, MODE>(w, a, lane);
     }
     int at = x - w.wbase;
@@ -1241,7 +1242,7 @@ int64_t most_tiles(int64_t n_rows, int G, int batch, int per)
 }
 
 template <int D, int G, bool F8>
-pkv_status launch(pkv_pool *pool, const void *q, const Args &a, cudaStream_t s)
+pkv_status launch(pkv_pool *pool, const void *q, Args a, cudaStream_t s)
 {
     CUtensorMap tm_q;
     pkv_status st = make_q_pair_map(&tm_q, q, a.n_rows, a.n_q, D, G, kRows / G);
@@ -1250,6 +1251,7 @@ pkv_status launch(pkv_pool *pool, const void *q, const Args &a, cudaStream_t s)
     const int64_t pairs = most_tiles(a.n_rows, G, a.batch, 2 * kRows) * a.n_pairs;
     const int64_t steps = (a.W + kStepBlocks - 1) / kStepBlocks;  // of the longest sequence the table can hold
     int resident[4];
+    a.window = 32;
     // ranges: the largest cluster of which all tiles' (counting the most the call can have) run at once
     if (tiles <= pool->num_sms / 2 && steps > 1) {
         st = prepare<D, G, F8, kRange>(pool, resident);
@@ -1260,7 +1262,12 @@ pkv_status launch(pkv_pool *pool, const void *q, const Args &a, cudaStream_t s)
     }
     st = prepare<D, G, F8, kWhole>(pool, resident);
     if (st != PKV_OK) return st;
-    return launch_mode<D, G, F8, kWhole>(pool, tm_q, (int)std::min<int64_t>(pairs, pool->num_sms / 2), 2, a, s);
+    // Windows of few sequences keep what runs together within the L2, those of many entries even out the clusters'
+    // work: four entries a cluster (16 prompts of 700 .. 1024 tokens: 357 us with 8 sequences, 370 with 16; 24 of
+    // 129 .. 1023 at d_head 64: 103 with 8, 91 with 16, 93 with 32).
+    const int clusters = (int)std::min<int64_t>(pairs, pool->num_sms / 2);
+    for (a.window = 4; a.window < 32 && pairs * a.window < (int64_t)4 * clusters * a.batch;) a.window *= 2;
+    return launch_mode<D, G, F8, kWhole>(pool, tm_q, clusters, 2, a, s);
 }
 
 template <int D, bool F8>
