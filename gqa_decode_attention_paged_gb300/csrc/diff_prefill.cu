@@ -17,27 +17,35 @@
 // scores.  All statistics are final before the first weight is formed: no
 // accumulator is ever rescaled.
 //
-// Design (persistent clusters of two CTAs, one per SM, warp-specialised):
+// Design (persistent clusters of two CTAs, one per SM, warp-specialised; the
+// times are of 16 prompts of 700..1024 tokens on contexts of up to 2048, bf16,
+// d_head 128, 32 query heads: 355 us in all, 200 for the MMAs alone):
 //   * a tile is 128 query rows (token, head) of one (sequence, pair): both
 //     maps' queries.  A step is 128 keys.  The two CTAs of a cluster take
 //     neighbouring tiles of the same (sequence, pair) and walk the same keys:
 //     each copies half of every unit into both CTAs' shared memory (multicast).
-//     A step moves 6 units of 32 KiB into each SM for 3 of MMA work each, and
-//     single copies (20 bytes a cycle and SM) bound the kernel: 602 us at 16
-//     prompts of 700..1024 tokens.
+//     A step moves 6 units of 32 KiB into each SM for 3 of MMA work each;
+//     with each CTA copying for itself that bound the kernel (602 us against
+//     435 at that stage).
 //   * warp 16 streams Q and, through one ring, what the MMAs take in the order
 //     they take it: K_m units (128 keys of one map) and, in the second sweep, V
 //     units (64 keys x 2 d channels).  One ring for both: in the first sweep
-//     all of it holds keys.  Warp 17 issues every MMA, as one warp from uniform
-//     registers (from inside a lane's branch an MMA took 80 cycles to issue,
-//     640 a unit, and that bound the kernel).
+//     all of it holds keys.
+//   * warp 17 issues the MMAs of the scores, another warp those of the products,
+//     each as one warp from uniform registers (from inside a lane's branch an
+//     MMA took 80 cycles to issue, 640 a unit, and that bound the kernel).
 //     The first sweep alternates between the maps' scores.  In the second one
-//     the halves of a step (64 keys) are half a step apart: the issue order is
-//     W V of the first half, S_2 of the next step, S_1 of its first half, W V
-//     of the second half, S_1 of the next step's second half, so that one
-//     half's weights are formed while the tensor cores work for the other,
-//     although scores and weights have one place each.  Warps 18 and 19 prepare units: FP8 ones are
-//     widened to f16, and value rows behind the sequence's end are zeroed.
+//     the halves of a step (64 keys) are half a step apart, so that one half's
+//     weights are formed while the tensor cores work for the other, although
+//     scores and weights have one place each: S_2 of the next step follows as
+//     soon as this one's is in registers, S_1 of its halves when the products
+//     of this one's are done.  One warp for all of it held products back behind
+//     the scores' waits (397 us against 377).
+//   * the warps after that prepare units: value rows behind the sequence's end
+//     are zeroed, and FP8 units are widened to f16 in place, by four warps (two
+//     bound the kernel: 596 us against 504 at d_head 128).  Widening writes and
+//     reads shared memory once more than the MMAs alone, which keep it busy as
+//     it is: FP8 prompts at d_head 128 take 457 us.
 //   * sixteen warps work on scores, four threads a row (a step's exponentials
 //     are many, and short dependent chains need several warps per scheduler to
 //     fill it: with eight warps a step took twice as long).  First sweep: each
@@ -383,10 +391,12 @@ struct RowStat {
             n0 = n1 = inv = 0.0f;
             return;
         }
-        const float c = abs_lam * l1 / l2;  // c2 / c1
-        n0 = log2f(c <= 1.0f ? 1.0f : 1.0f / c) + kBoost - m1;
-        n1 = log2f(c <= 1.0f ? c : 1.0f) + kBoost - m2;
-        inv = (c <= 1.0f ? 1.0f / l1 : abs_lam / l2) * (1.0f / 256.0f);
+        // (the approximate forms are off by 2^-21 at most, of what is rounded to 11 bits or fewer; the exact ones
+        // take 2 us of 90 where tiles are short.  l1 and l2 are far from 2^126, beyond which __fdividef gives 0.)
+        const float c = __fdividef(abs_lam * l1, l2);  // c2 / c1
+        n0 = __log2f(c <= 1.0f ? 1.0f : __fdividef(1.0f, c)) + kBoost - m1;
+        n1 = __log2f(c <= 1.0f ? c : 1.0f) + kBoost - m2;
+        inv = (c <= 1.0f ? __fdividef(1.0f, l1) : __fdividef(abs_lam, l2)) * (1.0f / 256.0f);
     }
 };
 
@@ -495,331 +505,331 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
     const uint32_t base = smem_u32(sm);
 
     if (warp >= kSoftmaxWarps) {
-    if constexpr (F8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Wp::kWorkRegs));
-    if (warp == kCopyWarp) {
-        // ---------------------------------------------------------- copies
-        const uint64_t policy = l2_policy_evict_normal();
-        int u = 0, n = 0;  // units issued, tiles
-        bool ok = true;
-        // One lane issues all copies of a unit, the warp running as one: sixteen copies that lanes issued for
-        // themselves went out one lane after the other, each moving its operands to uniform registers (1300
-        // cycles a unit, which bound the kernel).
-        const uint32_t go = elect_one();
-        // the next unit: its slot is free, its bytes are announced
-        auto open = [&](uint32_t &land, uint32_t &dst) -> bool {
-            const int st = u % NS, use = u / NS;
-            if (use > 0 && !wait_all(&bar[L::EMPTY + st], (use - 1) & 1)) return false;
-            uint64_t *b = &bar[(F8 ? L::RAW : L::FULL) + st];
-            land = smem_u32(b);
-            dst = base + L::kRing + st * L::UT;
-            if (go) mbar_arrive_expect_tx(b, F8 ? L::UT / 2 : L::UT);
-            __syncwarp();
-            ++u;
-            return true;
-        };
-        for (int x = e0, hop = hop0; ok && x < e_end; x += hop, hop = turn - hop) {
-            Tile t;
-            if (!find_tile<G, MODE>(wk, a, x, rank, ranges, t, lane)) break;
-            if (t.n_steps == 0) continue;
-            if (*abort_flag) break;
-            if (n > 0 && !(ok = wait_all(&bar[L::Q_FREE], (n - 1) & 1))) break;
-            if (lane == 0) {
-                uint64_t *qb = &bar[F8 ? L::Q_RAW : L::Q_FULL];
-                mbar_arrive_expect_tx(qb, 2 * L::QT);
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int h = 0; h < NH; ++h)
-                        tma_load_4d(sm + L::kQ + m * L::QT + h * kKHalf, &tm_q, 64 * h, m, t.p * G, t.row0 + t.rt0 / G,
-                                    qb, policy);
-            }
-            ++n;
-            const int32_t *trow = a.block_tables + (int64_t)t.b * a.W;
-            // lane k < 8: the entry rows of block k's pair of step s, or rows past the pool (zero filled)
-            auto rows_of = [&](int s, bool flag) -> int {
-                const int nb = (t.s0 + s) * kStepBlocks + lane;
-                const bool present = lane < kStepBlocks && nb < t.n_blocks;
-                const int id = present ? trow[nb] : -1;
-                const bool valid = id >= 0 && id < a.num_blocks;
-                if (present && !valid && flag) atomicOr(a.err, PKV_DEVERR_BLOCK_RANGE);
-                return valid ? (int)((id * (int64_t)a.n_kv + 2 * t.p) * 2 * kBlockSize) : a.oob_row;
-            };
-            auto copy_box = [&](uint32_t to, int c, int y, uint32_t land) {
-                if constexpr (kPair) tma_load_2d_multicast_if(go, to, &tm_kv, c, y, land, kBoth, policy);
-                else tma_load_2d_if(go, to, &tm_kv, c, y, land, policy);
-            };
-            constexpr int kTileRows = D == 128 ? kKeys : kVKeys;  // of a K unit's tiles, FP8 pools
-            constexpr int kShare = kPair ? 2 : 1;  // this CTA's blocks of a unit: every kShare-th
-            auto copy_k = [&](int y0, int m) -> bool {
-                uint32_t land, dst;
-                if (!open(land, dst)) return false;
-#pragma unroll
-                for (int i = 0; i < kStepBlocks / kShare; ++i) {
-                    const int k = kShare * i + (kPair ? rank : 0);
-                    const int yk = __shfl_sync(kFull, y0, k);
-                    const int y = yk == a.oob_row ? yk : yk + m * 2 * kBlockSize;
-                    if constexpr (F8) {
-                        copy_box(dst + (k * kBlockSize / kTileRows) * (kTileRows * 2 * D) + kTileRows * D +
-                                     (k * kBlockSize % kTileRows) * D,
-                                 0, y, land);
-                    } else {
-#pragma unroll
-                        for (int h = 0; h < NH; ++h)
-                            copy_box(dst + h * kKHalf + k * (kBlockSize * 128), 64 * h, y, land);
-                    }
-                }
-                return true;
-            };
-            auto copy_v = [&](int y0, int h) -> bool {
-                uint32_t land, dst;
-                if (!open(land, dst)) return false;
-#pragma unroll
-                for (int i = 0; i < kUnitBlocks / kShare; ++i) {
-                    const int k = kShare * i + (kPair ? rank : 0);
-                    const int yk = __shfl_sync(kFull, y0, h * kUnitBlocks + k);
-#pragma unroll
-                    for (int head = 0; head < 2; ++head) {
-                        const int y = yk == a.oob_row ? yk : yk + head * 2 * kBlockSize + kBlockSize;
-                        const uint32_t to = dst + head * NH * kVChunk;
-                        if constexpr (F8) {
-                            copy_box(to + kVKeys * D + k * (kBlockSize * D), 0, y, land);
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < NH; ++c)
-                                copy_box(to + c * kVChunk + k * (kBlockSize * 128), 64 * c, y, land);
-                        }
-                    }
-                }
-                return true;
-            };
-            int nxt = rows_of(0, true);
-            for (int s = 0; s < t.n_steps && ok; ++s) {
-                const int y0 = nxt;
-                if (s + 1 < t.n_steps) nxt = rows_of(s + 1, true);
-                ok = copy_k(y0, 0) && copy_k(y0, 1);
-            }
-            if (!ok) break;
-            int y0 = rows_of(0, false);
-            ok = copy_k(y0, 1) && copy_k(y0, 0);
-            for (int s = 0; s < t.n_steps && ok; ++s) {  // in the order of the MMAs
-                if (s + 1 < t.n_steps) nxt = rows_of(s + 1, false);
-                const bool more = s + 1 < t.n_steps;
-                ok = copy_v(y0, 0) && (!more || (copy_k(nxt, 1) && copy_k(nxt, 0))) && copy_v(y0, 1);
-                y0 = nxt;
-            }
-        }
-        // copies still in flight (after an abort) land before the CTA exits
-        for (int i = max(0, u - NS); i < u; ++i)
-            mbar_wait_bounded(&bar[(F8 ? L::RAW : L::FULL) + i % NS], (i / NS) & 1);
-        // and the other CTA's arrivals on this one's barriers (none comes after the last units')
-        for (int i = max(0, u - NS); i < u && ok && !*abort_flag; ++i)
-            ok = wait_all(&bar[L::EMPTY + i % NS], (i / NS) & 1);
-        if (n > 0) mbar_wait_bounded(&bar[F8 ? L::Q_RAW : L::Q_FULL], (n - 1) & 1);
-        if (!ok) set_abort();
-    } else if (warp >= kPrepWarp && warp < Wp::kProduct) {
-        // ---------------------------------------------------------- units made ready
-        const int which = warp - kPrepWarp;
-        {
-            int u = 0, ends = 0;
+        if constexpr (F8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Wp::kWorkRegs));
+        if (warp == kCopyWarp) {
+            // ---------------------------------------------------------- copies
+            const uint64_t policy = l2_policy_evict_normal();
+            int u = 0, n = 0;  // units issued, tiles
             bool ok = true;
+            // One lane issues all copies of a unit, the warp running as one: sixteen copies that lanes issued for
+            // themselves went out one lane after the other, each moving its operands to uniform registers (1300
+            // cycles a unit, which bound the kernel).
+            const uint32_t go = elect_one();
+            // the next unit: its slot is free, its bytes are announced
+            auto open = [&](uint32_t &land, uint32_t &dst) -> bool {
+                const int st = u % NS, use = u / NS;
+                if (use > 0 && !wait_all(&bar[L::EMPTY + st], (use - 1) & 1)) return false;
+                uint64_t *b = &bar[(F8 ? L::RAW : L::FULL) + st];
+                land = smem_u32(b);
+                dst = base + L::kRing + st * L::UT;
+                if (go) mbar_arrive_expect_tx(b, F8 ? L::UT / 2 : L::UT);
+                __syncwarp();
+                ++u;
+                return true;
+            };
             for (int x = e0, hop = hop0; ok && x < e_end; x += hop, hop = turn - hop) {
                 Tile t;
                 if (!find_tile<G, MODE>(wk, a, x, rank, ranges, t, lane)) break;
                 if (t.n_steps == 0) continue;
                 if (*abort_flag) break;
-                // the V unit the sequence ends inside of: zero the rows behind the end (value heads h0 ..)
-                const int end = end_unit(t), end_row = (t.C / kBlockSize % kUnitBlocks) * kBlockSize;
-                auto clear = [&](uint32_t unit, int h0, int heads) {
-                    const int first = end_row + t.C % kBlockSize, rows = end_row + kBlockSize - first;
-                    for (int e = lane; e < rows * 8 * heads * NH; e += 32) {
-                        const int row = first + (e >> 3) % rows, ch = h0 * NH + (e >> 3) / rows;
-                        sts128(unit + ch * kVChunk + row * 128 + (e & 7) * 16, make_uint4(0, 0, 0, 0));
-                    }
-                };
-                if constexpr (!F8) {  // the MMA warp asks when the unit has landed
-                    if (end >= 0) {
-                        const int vs = end / 2, S = t.n_steps;
-                        const int v = u + 2 * S + 2 + 4 * vs + (end & 1) * (vs == S - 1 ? 1 : 3);
-                        if (!(ok = wait_all(&bar[L::END_ASK], ends & 1))) break;
-                        ++ends;
-                        clear(base + L::kRing + v % NS * L::UT, 0, 2);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar[L::END_CLEAR]);
-                    }
-                    u += 6 * t.n_steps;
-                } else {
-                    for (int i = 0; i < 6 * t.n_steps; ++i, ++u) {
-                        const int st = u % NS;
-                        if (D == 64 && (u & 1) != which >> 1) continue;
-                        if (!(ok = wait_all(&bar[L::RAW + st], (u / NS) & 1))) break;
-                        // second sweep: K, K of the first step, then of each step V, K, K, V (the next step's
-                        // keys; the last step has V, V)
-                        const int iv = i - 2 * t.n_steps - 2;
-                        const int vs = iv >> 2, vp = iv & 3;
-                        const bool tail = vs == t.n_steps - 1;
-                        const bool is_v = iv >= 0 && (tail || vp == 0 || vp == 3);
-                        const int vh = vp != 0;  // the V unit's half
-                        const uint32_t unit = base + L::kRing + st * L::UT;
-                        if constexpr (D == 128) {  // this warp's 32 rows
-                            if (is_v) {
-                                const int head = which >> 1, row0 = (which & 1) * 32;
-                                convert_f16<D, kVKeys>(unit + head * NH * kVChunk, lane, row0, 32);
-                                if (2 * vs + vh == end && end_row / 32 == (which & 1)) clear(unit, head, 1);
-                            } else {
-                                convert_f16<D, kKeys>(unit, lane, which * 32, 32);
-                            }
-                        } else {  // half of the keys, or a value head
-                            convert_f16<D, kVKeys>(unit + (which & 1) * kVChunk, lane, 0, kVKeys);
-                            if (is_v && 2 * vs + vh == end) clear(unit, which & 1, 1);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar[L::FULL + st]);
-                    }
-                }
-            }
-            if (!ok) set_abort();
-        }
-    } else if (warp == kScoreWarp || warp == Wp::kProduct) {
-        // ---------------------------------------------------------- S_m = Q_m K_m^T and O += W V
-        constexpr uint32_t idesc_qk = mma_idesc(kRows, kKeys, 0, F8), idesc_half = mma_idesc(kRows, 64, 0, F8);
-        constexpr uint32_t idesc_pv = mma_idesc(kRows, 2 * D, 1, F8);
-        const uint64_t qd = smem_desc(base + L::kQ, 16, 1024), kd = smem_desc(base + L::kRing, 16, 1024);
-        const uint64_t vd = smem_desc(base + L::kRing, kVChunk, 1024);
-        int slot = 0, n = 0;  // of the ring's next unit; tiles
-        uint32_t ph = 0;      // the parity of its phase
-        int reads = 0, steps = 0, ends = 0;  // first- and second-sweep steps, sequence ends
-        const uint32_t go = elect_one();
-        const uint32_t tm = __shfl_sync(kFull, tmem, 0);
-        auto skip = [&](int k) {
-            slot += k;
-            if (slot >= NS) {
-                slot -= NS;
-                ph ^= 1u;
-            }
-        };
-        // A slot's barrier has a phase per use.  The two warps wait each for its own units alone, and
-        // after what tells it that the slot's use before had been filled: the NS-th unit before is older than
-        // those that the weights (or the products) it has just waited for were made from.
-        auto unit = [&]() -> bool { return wait_all(&bar[L::FULL + slot], ph); };
-        // the unit in slot v has been used when this warp's MMAs so far have run
-        auto release = [&](int v) {
-            if constexpr (kPair) umma_commit_multicast_if(go, &bar[L::EMPTY + v], kBoth);
-            else umma_commit_if(go, &bar[L::EMPTY + v]);
-        };
-        // keys [64 half, 64 half + N) of the unit in slot v against map m's queries
-        auto scores = [&](int m, int v, int half, uint32_t idesc) {
-            tc_fence_after();
-            const uint64_t qm = qd + ((m * L::QT) >> 4), km = kd + ((v * L::UT + half * 64 * 128) >> 4);
+                if (n > 0 && !(ok = wait_all(&bar[L::Q_FREE], (n - 1) & 1))) break;
+                if (lane == 0) {
+                    uint64_t *qb = &bar[F8 ? L::Q_RAW : L::Q_FULL];
+                    mbar_arrive_expect_tx(qb, 2 * L::QT);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = ((kk >> 2) * kKHalf + (kk & 3) * 32) >> 4;
-                umma_if(go, tm + m * kKeys + half * 64, qm + off, km + off, idesc, kk > 0 ? 1u : 0u);
-            }
-        };
-        // all of map m's scores of a step
-        auto whole = [&](int m, uint64_t *full) -> bool {
-            if (!unit()) return false;
-            scores(m, slot, 0, idesc_qk);
-            umma_commit_if(go, full);
-            release(slot);
-            skip(1);
-            return true;
-        };
-        auto first_sweep = [&](int s, int m) -> bool {
-            // S_m is free: its last scores are in registers, and the weights over S_1 have been used
-            if (s > 0) {
-                if (!wait_all(&bar[L::ST_READ + m], (reads - 1) & 1)) return false;
-            } else if (n > 0) {
-                if (m == 0 && !(wait_all(&bar[L::PV_DONE], (steps - 1) & 1) && wait_all(&bar[L::PV_DONE + 1], (steps - 1) & 1)))
-                    return false;
-                if (m == 1 && !wait_all(&bar[L::S2_READ], (steps - 1) & 1)) return false;
-            }
-            return whole(m, &bar[L::ST_FULL + m]);
-        };
-        // map 1's scores of a half, in the second sweep
-        auto half_of = [&](int half) {
-            scores(0, slot, half, idesc_half);
-            umma_commit_if(go, &bar[L::S1_FULL + half]);
-            if (half == 1) release(slot);
-        };
-        auto product = [&](int s, int h, int end) -> bool {
-            // (before the unit's wait, see there)
-            if (!wait_all(&bar[L::P_FULL + h], steps & 1)) return false;
-            if (s == 0 && h == 0 && !wait_all(&bar[L::O_FREE], n & 1)) return false;
-            if (!unit()) return false;
-            if (!F8 && 2 * s + h == end) {
-                if (go) mbar_arrive(&bar[L::END_ASK]);
-                __syncwarp();
-                if (!wait_all(&bar[L::END_CLEAR], ends & 1)) return false;
-                ++ends;
-            }
-            tc_fence_after();
-            const uint64_t vm = vd + ((slot * L::UT) >> 4);
+                    for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int kk = 0; kk < kVKeys / 16; ++kk)
-                umma_ts_if(go, tm + kColO, tm + h * kVKeys + (kk >> 1) * 32 + (kk & 1) * 8, vm + ((kk * 2048) >> 4), idesc_pv,
-                           (s > 0 || h > 0 || kk > 0) ? 1u : 0u);
-            umma_commit_if(go, &bar[L::PV_DONE + h]);
-            release(slot);
-            skip(1);
-            return true;
-        };
-        auto walk = [&](auto on_scores) -> bool {
-            constexpr bool kScores = decltype(on_scores)::value;
-            for (int x = e0, hop = hop0; x < e_end; x += hop, hop = turn - hop) {
-                Tile t;
-                if (!find_tile<G, MODE>(wk, a, x, rank, ranges, t, lane)) break;
-                if (t.n_steps == 0) continue;
-                if (*abort_flag) break;
-                const int S = __shfl_sync(kFull, t.n_steps, 0);
-                if constexpr (kScores) {
-                    if (!wait_all(&bar[L::Q_FULL], n & 1)) return false;
-                    for (int s = 0; s < S; ++s, ++reads)
-                        if (!(first_sweep(s, 0) && first_sweep(s, 1))) return false;
-                    // second sweep: the first step's scores
-                    if (!(wait_all(&bar[L::ST_READ + 1], (reads - 1) & 1) && whole(1, &bar[L::S2_FULL]))) return false;
-                    if (!(wait_all(&bar[L::ST_READ], (reads - 1) & 1) && unit())) return false;
-                    half_of(0);
-                    half_of(1);
-                    skip(1);
-                    for (int s = 0; s + 1 < S; ++s, ++steps) {
-                        skip(1);  // V
-                        if (!(wait_all(&bar[L::S2_READ], steps & 1) && whole(1, &bar[L::S2_FULL]))) return false;
-                        if (!(wait_all(&bar[L::PV_DONE], steps & 1) && unit())) return false;
-                        half_of(0);
-                        if (!wait_all(&bar[L::PV_DONE + 1], steps & 1)) return false;
-                        half_of(1);
-                        skip(2);  // and V
-                    }
-                    umma_commit_if(go, &bar[L::Q_FREE]);
-                    ++steps;
-                    skip(2);  // V, V
-                } else {
-                    const int end = end_unit(t);
-                    const int at = (slot + (int)ph * NS + 2 * S + 2) % (2 * NS);  // the first sweep's keys, the first step's
-                    slot = at % NS;
-                    ph = at >= NS;
-                    for (int s = 0; s < S; ++s, ++steps) {
-                        if (!product(s, 0, end)) return false;
-                        if (s + 1 < S) skip(2);  // keys
-                        if (!product(s, 1, end)) return false;
-                    }
-                    umma_commit_if(go, &bar[L::O_FULL]);
+                        for (int h = 0; h < NH; ++h)
+                            tma_load_4d(sm + L::kQ + m * L::QT + h * kKHalf, &tm_q, 64 * h, m, t.p * G, t.row0 + t.rt0 / G,
+                                        qb, policy);
                 }
                 ++n;
+                const int32_t *trow = a.block_tables + (int64_t)t.b * a.W;
+                // lane k < 8: the entry rows of block k's pair of step s, or rows past the pool (zero filled)
+                auto rows_of = [&](int s, bool flag) -> int {
+                    const int nb = (t.s0 + s) * kStepBlocks + lane;
+                    const bool present = lane < kStepBlocks && nb < t.n_blocks;
+                    const int id = present ? trow[nb] : -1;
+                    const bool valid = id >= 0 && id < a.num_blocks;
+                    if (present && !valid && flag) atomicOr(a.err, PKV_DEVERR_BLOCK_RANGE);
+                    return valid ? (int)((id * (int64_t)a.n_kv + 2 * t.p) * 2 * kBlockSize) : a.oob_row;
+                };
+                auto copy_box = [&](uint32_t to, int c, int y, uint32_t land) {
+                    if constexpr (kPair) tma_load_2d_multicast_if(go, to, &tm_kv, c, y, land, kBoth, policy);
+                    else tma_load_2d_if(go, to, &tm_kv, c, y, land, policy);
+                };
+                constexpr int kTileRows = D == 128 ? kKeys : kVKeys;  // of a K unit's tiles, FP8 pools
+                constexpr int kShare = kPair ? 2 : 1;  // this CTA's blocks of a unit: every kShare-th
+                auto copy_k = [&](int y0, int m) -> bool {
+                    uint32_t land, dst;
+                    if (!open(land, dst)) return false;
+#pragma unroll
+                    for (int i = 0; i < kStepBlocks / kShare; ++i) {
+                        const int k = kShare * i + (kPair ? rank : 0);
+                        const int yk = __shfl_sync(kFull, y0, k);
+                        const int y = yk == a.oob_row ? yk : yk + m * 2 * kBlockSize;
+                        if constexpr (F8) {
+                            copy_box(dst + (k * kBlockSize / kTileRows) * (kTileRows * 2 * D) + kTileRows * D +
+                                         (k * kBlockSize % kTileRows) * D,
+                                     0, y, land);
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < NH; ++h)
+                                copy_box(dst + h * kKHalf + k * (kBlockSize * 128), 64 * h, y, land);
+                        }
+                    }
+                    return true;
+                };
+                auto copy_v = [&](int y0, int h) -> bool {
+                    uint32_t land, dst;
+                    if (!open(land, dst)) return false;
+#pragma unroll
+                    for (int i = 0; i < kUnitBlocks / kShare; ++i) {
+                        const int k = kShare * i + (kPair ? rank : 0);
+                        const int yk = __shfl_sync(kFull, y0, h * kUnitBlocks + k);
+#pragma unroll
+                        for (int head = 0; head < 2; ++head) {
+                            const int y = yk == a.oob_row ? yk : yk + head * 2 * kBlockSize + kBlockSize;
+                            const uint32_t to = dst + head * NH * kVChunk;
+                            if constexpr (F8) {
+                                copy_box(to + kVKeys * D + k * (kBlockSize * D), 0, y, land);
+                            } else {
+#pragma unroll
+                                for (int c = 0; c < NH; ++c)
+                                    copy_box(to + c * kVChunk + k * (kBlockSize * 128), 64 * c, y, land);
+                            }
+                        }
+                    }
+                    return true;
+                };
+                int nxt = rows_of(0, true);
+                for (int s = 0; s < t.n_steps && ok; ++s) {
+                    const int y0 = nxt;
+                    if (s + 1 < t.n_steps) nxt = rows_of(s + 1, true);
+                    ok = copy_k(y0, 0) && copy_k(y0, 1);
+                }
+                if (!ok) break;
+                int y0 = rows_of(0, false);
+                ok = copy_k(y0, 1) && copy_k(y0, 0);
+                for (int s = 0; s < t.n_steps && ok; ++s) {  // in the order of the MMAs
+                    if (s + 1 < t.n_steps) nxt = rows_of(s + 1, false);
+                    const bool more = s + 1 < t.n_steps;
+                    ok = copy_v(y0, 0) && (!more || (copy_k(nxt, 1) && copy_k(nxt, 0))) && copy_v(y0, 1);
+                    y0 = nxt;
+                }
             }
-            return true;
-        };
-        bool ok;
-        if (warp == kScoreWarp) ok = walk(std::true_type{});
-        else ok = walk(std::false_type{});
-        umma_commit_if(go, &bar[L::DRAIN]);
-        __syncwarp();
-        mbar_wait_bounded(&bar[L::DRAIN], 0);
-        if (!ok) set_abort();
-    }
+            // copies still in flight (after an abort) land before the CTA exits
+            for (int i = max(0, u - NS); i < u; ++i)
+                mbar_wait_bounded(&bar[(F8 ? L::RAW : L::FULL) + i % NS], (i / NS) & 1);
+            // and the other CTA's arrivals on this one's barriers (none comes after the last units')
+            for (int i = max(0, u - NS); i < u && ok && !*abort_flag; ++i)
+                ok = wait_all(&bar[L::EMPTY + i % NS], (i / NS) & 1);
+            if (n > 0) mbar_wait_bounded(&bar[F8 ? L::Q_RAW : L::Q_FULL], (n - 1) & 1);
+            if (!ok) set_abort();
+        } else if (warp >= kPrepWarp && warp < Wp::kProduct) {
+            // ---------------------------------------------------------- units made ready
+            const int which = warp - kPrepWarp;
+            {
+                int u = 0, ends = 0;
+                bool ok = true;
+                for (int x = e0, hop = hop0; ok && x < e_end; x += hop, hop = turn - hop) {
+                    Tile t;
+                    if (!find_tile<G, MODE>(wk, a, x, rank, ranges, t, lane)) break;
+                    if (t.n_steps == 0) continue;
+                    if (*abort_flag) break;
+                    // the V unit the sequence ends inside of: zero the rows behind the end (value heads h0 ..)
+                    const int end = end_unit(t), end_row = (t.C / kBlockSize % kUnitBlocks) * kBlockSize;
+                    auto clear = [&](uint32_t unit, int h0, int heads) {
+                        const int first = end_row + t.C % kBlockSize, rows = end_row + kBlockSize - first;
+                        for (int e = lane; e < rows * 8 * heads * NH; e += 32) {
+                            const int row = first + (e >> 3) % rows, ch = h0 * NH + (e >> 3) / rows;
+                            sts128(unit + ch * kVChunk + row * 128 + (e & 7) * 16, make_uint4(0, 0, 0, 0));
+                        }
+                    };
+                    if constexpr (!F8) {  // the MMA warp asks when the unit has landed
+                        if (end >= 0) {
+                            const int vs = end / 2, S = t.n_steps;
+                            const int v = u + 2 * S + 2 + 4 * vs + (end & 1) * (vs == S - 1 ? 1 : 3);
+                            if (!(ok = wait_all(&bar[L::END_ASK], ends & 1))) break;
+                            ++ends;
+                            clear(base + L::kRing + v % NS * L::UT, 0, 2);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bar[L::END_CLEAR]);
+                        }
+                        u += 6 * t.n_steps;
+                    } else {
+                        for (int i = 0; i < 6 * t.n_steps; ++i, ++u) {
+                            const int st = u % NS;
+                            if (D == 64 && (u & 1) != which >> 1) continue;
+                            if (!(ok = wait_all(&bar[L::RAW + st], (u / NS) & 1))) break;
+                            // second sweep: K, K of the first step, then of each step V, K, K, V (the next step's
+                            // keys; the last step has V, V)
+                            const int iv = i - 2 * t.n_steps - 2;
+                            const int vs = iv >> 2, vp = iv & 3;
+                            const bool tail = vs == t.n_steps - 1;
+                            const bool is_v = iv >= 0 && (tail || vp == 0 || vp == 3);
+                            const int vh = vp != 0;  // the V unit's half
+                            const uint32_t unit = base + L::kRing + st * L::UT;
+                            if constexpr (D == 128) {  // this warp's 32 rows
+                                if (is_v) {
+                                    const int head = which >> 1, row0 = (which & 1) * 32;
+                                    convert_f16<D, kVKeys>(unit + head * NH * kVChunk, lane, row0, 32);
+                                    if (2 * vs + vh == end && end_row / 32 == (which & 1)) clear(unit, head, 1);
+                                } else {
+                                    convert_f16<D, kKeys>(unit, lane, which * 32, 32);
+                                }
+                            } else {  // half of the keys, or a value head
+                                convert_f16<D, kVKeys>(unit + (which & 1) * kVChunk, lane, 0, kVKeys);
+                                if (is_v && 2 * vs + vh == end) clear(unit, which & 1, 1);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bar[L::FULL + st]);
+                        }
+                    }
+                }
+                if (!ok) set_abort();
+            }
+        } else if (warp == kScoreWarp || warp == Wp::kProduct) {
+            // ---------------------------------------------------------- S_m = Q_m K_m^T and O += W V
+            constexpr uint32_t idesc_qk = mma_idesc(kRows, kKeys, 0, F8), idesc_half = mma_idesc(kRows, 64, 0, F8);
+            constexpr uint32_t idesc_pv = mma_idesc(kRows, 2 * D, 1, F8);
+            const uint64_t qd = smem_desc(base + L::kQ, 16, 1024), kd = smem_desc(base + L::kRing, 16, 1024);
+            const uint64_t vd = smem_desc(base + L::kRing, kVChunk, 1024);
+            int slot = 0, n = 0;  // of the ring's next unit; tiles
+            uint32_t ph = 0;      // the parity of its phase
+            int reads = 0, steps = 0, ends = 0;  // first- and second-sweep steps, sequence ends
+            const uint32_t go = elect_one();
+            const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+            auto skip = [&](int k) {
+                slot += k;
+                if (slot >= NS) {
+                    slot -= NS;
+                    ph ^= 1u;
+                }
+            };
+            // A slot's barrier has a phase per use.  The two warps wait each for its own units alone, and
+            // after what tells it that the slot's use before had been filled: the NS-th unit before is older than
+            // those that the weights (or the products) it has just waited for were made from.
+            auto unit = [&]() -> bool { return wait_all(&bar[L::FULL + slot], ph); };
+            // the unit in slot v has been used when this warp's MMAs so far have run
+            auto release = [&](int v) {
+                if constexpr (kPair) umma_commit_multicast_if(go, &bar[L::EMPTY + v], kBoth);
+                else umma_commit_if(go, &bar[L::EMPTY + v]);
+            };
+            // keys [64 half, 64 half + N) of the unit in slot v against map m's queries
+            auto scores = [&](int m, int v, int half, uint32_t idesc) {
+                tc_fence_after();
+                const uint64_t qm = qd + ((m * L::QT) >> 4), km = kd + ((v * L::UT + half * 64 * 128) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = ((kk >> 2) * kKHalf + (kk & 3) * 32) >> 4;
+                    umma_if(go, tm + m * kKeys + half * 64, qm + off, km + off, idesc, kk > 0 ? 1u : 0u);
+                }
+            };
+            // all of map m's scores of a step
+            auto whole = [&](int m, uint64_t *full) -> bool {
+                if (!unit()) return false;
+                scores(m, slot, 0, idesc_qk);
+                umma_commit_if(go, full);
+                release(slot);
+                skip(1);
+                return true;
+            };
+            auto first_sweep = [&](int s, int m) -> bool {
+                // S_m is free: its last scores are in registers, and the weights over S_1 have been used
+                if (s > 0) {
+                    if (!wait_all(&bar[L::ST_READ + m], (reads - 1) & 1)) return false;
+                } else if (n > 0) {
+                    if (m == 0 && !(wait_all(&bar[L::PV_DONE], (steps - 1) & 1) && wait_all(&bar[L::PV_DONE + 1], (steps - 1) & 1)))
+                        return false;
+                    if (m == 1 && !wait_all(&bar[L::S2_READ], (steps - 1) & 1)) return false;
+                }
+                return whole(m, &bar[L::ST_FULL + m]);
+            };
+            // map 1's scores of a half, in the second sweep
+            auto half_of = [&](int half) {
+                scores(0, slot, half, idesc_half);
+                umma_commit_if(go, &bar[L::S1_FULL + half]);
+                if (half == 1) release(slot);
+            };
+            auto product = [&](int s, int h, int end) -> bool {
+                // (before the unit's wait, see there)
+                if (!wait_all(&bar[L::P_FULL + h], steps & 1)) return false;
+                if (s == 0 && h == 0 && !wait_all(&bar[L::O_FREE], n & 1)) return false;
+                if (!unit()) return false;
+                if (!F8 && 2 * s + h == end) {
+                    if (go) mbar_arrive(&bar[L::END_ASK]);
+                    __syncwarp();
+                    if (!wait_all(&bar[L::END_CLEAR], ends & 1)) return false;
+                    ++ends;
+                }
+                tc_fence_after();
+                const uint64_t vm = vd + ((slot * L::UT) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kVKeys / 16; ++kk)
+                    umma_ts_if(go, tm + kColO, tm + h * kVKeys + (kk >> 1) * 32 + (kk & 1) * 8, vm + ((kk * 2048) >> 4), idesc_pv,
+                               (s > 0 || h > 0 || kk > 0) ? 1u : 0u);
+                umma_commit_if(go, &bar[L::PV_DONE + h]);
+                release(slot);
+                skip(1);
+                return true;
+            };
+            auto walk = [&](auto on_scores) -> bool {
+                constexpr bool kScores = decltype(on_scores)::value;
+                for (int x = e0, hop = hop0; x < e_end; x += hop, hop = turn - hop) {
+                    Tile t;
+                    if (!find_tile<G, MODE>(wk, a, x, rank, ranges, t, lane)) break;
+                    if (t.n_steps == 0) continue;
+                    if (*abort_flag) break;
+                    const int S = __shfl_sync(kFull, t.n_steps, 0);
+                    if constexpr (kScores) {
+                        if (!wait_all(&bar[L::Q_FULL], n & 1)) return false;
+                        for (int s = 0; s < S; ++s, ++reads)
+                            if (!(first_sweep(s, 0) && first_sweep(s, 1))) return false;
+                        // second sweep: the first step's scores
+                        if (!(wait_all(&bar[L::ST_READ + 1], (reads - 1) & 1) && whole(1, &bar[L::S2_FULL]))) return false;
+                        if (!(wait_all(&bar[L::ST_READ], (reads - 1) & 1) && unit())) return false;
+                        half_of(0);
+                        half_of(1);
+                        skip(1);
+                        for (int s = 0; s + 1 < S; ++s, ++steps) {
+                            skip(1);  // V
+                            if (!(wait_all(&bar[L::S2_READ], steps & 1) && whole(1, &bar[L::S2_FULL]))) return false;
+                            if (!(wait_all(&bar[L::PV_DONE], steps & 1) && unit())) return false;
+                            half_of(0);
+                            if (!wait_all(&bar[L::PV_DONE + 1], steps & 1)) return false;
+                            half_of(1);
+                            skip(2);  // and V
+                        }
+                        umma_commit_if(go, &bar[L::Q_FREE]);
+                        ++steps;
+                        skip(2);  // V, V
+                    } else {
+                        const int end = end_unit(t);
+                        const int at = (slot + (int)ph * NS + 2 * S + 2) % (2 * NS);  // the first sweep's keys, the first step's
+                        slot = at % NS;
+                        ph = at >= NS;
+                        for (int s = 0; s < S; ++s, ++steps) {
+                            if (!product(s, 0, end)) return false;
+                            if (s + 1 < S) skip(2);  // keys
+                            if (!product(s, 1, end)) return false;
+                        }
+                        umma_commit_if(go, &bar[L::O_FULL]);
+                    }
+                    ++n;
+                }
+                return true;
+            };
+            bool ok;
+            if (warp == kScoreWarp) ok = walk(std::true_type{});
+            else ok = walk(std::false_type{});
+            umma_commit_if(go, &bar[L::DRAIN]);
+            __syncwarp();
+            mbar_wait_bounded(&bar[L::DRAIN], 0);
+            if (!ok) set_abort();
+        }
     } else {
         // ---------------------------------------------------------- statistics, weights, norm
         if constexpr (F8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Wp::kScoreRegs));
