@@ -9,7 +9,7 @@
 // makes per position matters: the host stores turn_i = frac(inv_freq[i] /
 // 2 pi) as a 64-bit fixed-point fraction, the kernel multiplies it by the
 // position modulo 2^64 (exact, whatever the position) and takes sine and
-// cosine of the top 32 bits with sincospif.  The angle is thus good to about
+// cosine of the top 32 bits (turn_of).  The angle is thus good to about
 // 2^-32 of a turn at every position, where a 32-bit product would be off by
 // 2^-24 * angle (0.004 radians at 65536), without 64-bit floating point.
 // The rotation runs in fp32 and is rounded once: to bf16 (queries, bf16
@@ -59,6 +59,34 @@ struct RopeArgs {
     const float *k_params;     // 4-bit: [2][n_kv][D]
     unsigned *err;
 };
+
+// Sine and cosine of u 2^-32 turns: the nearest quarter turn is taken off as an integer, and the rest t, within
+// pi / 4, goes into the Taylor series of both, with what its 24 bits cannot hold (lo) and with the rounding of the
+// cosine's second sum.  Off by 0.71 of a last place at most, 0.25 in the mean (which is that of rounding alone), as
+// fast as sincospif of the rounded angle, which is off by up to 2.
+__device__ __forceinline__ void turn_of(uint32_t u, float &sn, float &cs)
+{
+    constexpr float kPi = 3.14159274f, kPiRest = -8.74227766e-8f;  // pi and what its rounding leaves
+    const uint32_t quarter = (u + 0x20000000u) >> 30;
+    const int32_t rest = (int32_t)(u - (quarter << 30));  // within 2^29
+    const float n = (float)rest;
+    const float x = n * 4.656612873077393e-10f;  // 2^-31 half turns
+    const float t = x * kPi;
+    const float lo = fmaf(x, kPi, -t) + fmaf(x, kPiRest, (float)(rest - (int32_t)n) * (kPi * 4.656612873077393e-10f));
+    const float z = t * t, zl = fmaf(t, t, -z);
+    float p = fmaf(z, 1.0f / 362880, -1.0f / 5040);
+    p = fmaf(p, z, 1.0f / 120);
+    p = fmaf(p, z, -1.0f / 6);
+    const float s = t + fmaf(t * z, p, fmaf(-0.5f * z, lo, lo));
+    float q = fmaf(z, -1.0f / 3628800, 1.0f / 40320);
+    q = fmaf(q, z, -1.0f / 720);
+    q = fmaf(q, z, 1.0f / 24);
+    const float w = 1.0f - 0.5f * z, e = (1.0f - w) - 0.5f * z;  // (exact)
+    const float c = w + (e + fmaf(z * z, q, fmaf(-lo, t, -0.5f * zl)));
+    const float a = quarter & 1u ? c : s, b = quarter & 1u ? s : c;
+    sn = quarter & 2u ? -a : a;
+    cs = (quarter + 1u) & 2u ? -b : b;
+}
 
 // 4-bit code of x: clamp(rint((x - z) / s), 0, 15), each step correctly rounded in fp32, NaN to 0.  `r` is
 // 1 / s to a few units of its last place: the product with it is off by less than 2^-17 where the code is
@@ -181,8 +209,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_append_kernel(const __gr
                 const int pair = 8 * j + r * PPL + i;
                 const int64_t pos = a.positions[(int64_t)a.axis[pair] * a.n_tokens + t];
                 const uint64_t frac = a.turn[pair] * (uint64_t)pos;  // fraction of a turn, modulo 2^64
-                const int32_t top = (int32_t)(uint32_t)((frac + 0x80000000ull) >> 32);
-                sincospif((float)top * 4.656612873077393e-10f, &s[i], &c[i]);  // 2^-31 half turns
+                turn_of((uint32_t)((frac + 0x80000000ull) >> 32), s[i], c[i]);
             }
         }
 #pragma unroll
