@@ -176,6 +176,28 @@ def test_rope_append_at_position_zero_is_the_plain_append(kv):
 
 
 @pytest.mark.gpu
+def test_rope_append_rounds_every_bf16_value_to_the_e4m3_of_the_plain_append():
+    """All 2^16 bit patterns (zeros of both signs, subnormals, infinities and NaN among them) as values, divided by
+    scales from one end of fp32's range to the other: the same bytes as the append's correctly rounded division."""
+    scales = np.float32([1e-37, 2.0 ** -61, 1.1e-18, 0.0078, 0.3, 1.0, 448.0 / 3, 1.1e18, 2.0 ** 61, 3e38, 1.9999999, 0.1])
+    d, n_kv, T = 128, len(scales), 512
+    v = torch.arange(2 ** 16, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).view(T, 1, d).repeat(1, n_kv, 1).cuda()
+    q, k = torch.zeros(T, 2 * n_kv, d, dtype=torch.bfloat16, device="cuda"), torch.zeros_like(v)
+    slots, pos = torch.arange(T, device="cuda"), torch.zeros(1, T, dtype=torch.int32, device="cuda")
+    rope = pkv.Rope(np.ones(16))
+    got = []
+    for rotary in (False, True):
+        with pkv.kv_pool_create(T // BS, BS, n_kv, d, pkv.FP8_E4M3) as pool:
+            pool.set_fp8_scales(scales, scales)
+            if rotary:
+                pkv.paged_rope_append(pool, rope, q, k, v, pos, slots)
+            else:
+                pkv.paged_kv_append(pool, k, v, slots)
+            got.append(raw(pool)[1])
+    assert np.array_equal(*got)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kv", ["bf16", "int4"])
 def test_rope_append_from_a_fused_projection_in_place(kv):
     """q, k and v as slices of one [T, heads, d] array, q turned in place: the same bytes as from
