@@ -80,6 +80,7 @@ def test_diff_prefill_matches_the_64_bit_form(kv, case, pad):
     ("fp8", 4, 2, 64, [9000, 17, 3], [3, 17, 1]),
     ("bf16", 4, 1, 64, [1030], [1030]),
     ("fp8", 16, 4, 128, [129] * 24, [100] * 24),                    # whole: single tiles of their pairs
+    ("bf16", 64, 1, 64, [600, 520, 700, 513, 1, 640], [600, 520, 700, 513, 1, 640]),  # windows of four sequences
 ])
 def test_diff_prefill_shapes(kv, n_kv, G, d, lens, chunks):
     with Cache(kv, n_kv, d, lens, seed=8) as c:
