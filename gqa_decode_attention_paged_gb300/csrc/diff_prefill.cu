@@ -19,7 +19,7 @@
 //
 // Design (persistent clusters of two CTAs, one per SM, warp-specialised; the
 // times are of 16 prompts of 700..1024 tokens on contexts of up to 2048, bf16,
-// d_head 128, 32 query heads: 355 us in all, 200 for the MMAs alone):
+// d_head 128, 32 query heads: 346 us in all, 200 for the MMAs alone):
 //   * a tile is 128 query rows (token, head) of one (sequence, pair): both
 //     maps' queries.  A step is 128 keys.  The two CTAs of a cluster take
 //     neighbouring tiles of the same (sequence, pair) and walk the same keys:
@@ -45,7 +45,7 @@
 //     are zeroed, and FP8 units are widened to f16 in place, by four warps (two
 //     bound the kernel: 596 us against 504 at d_head 128).  Widening writes and
 //     reads shared memory once more than the MMAs alone, which keep it busy as
-//     it is: FP8 prompts at d_head 128 take 457 us.
+//     it is: FP8 prompts at d_head 128 take 452 us.
 //   * sixteen warps work on scores, four threads a row (a step's exponentials
 //     are many, and short dependent chains need several warps per scheduler to
 //     fill it: with eight warps a step took twice as long).  First sweep: each
@@ -1140,24 +1140,44 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                 ss = (__uint_as_float(y[0]) + __uint_as_float(y[1])) + (__uint_as_float(y[2]) + __uint_as_float(y[3]));
             }
             const float rn = a.w.out_scale * rsqrtf(ss * (1.0f / (2 * D)) + a.w.eps);
-            if (r < t.R) {
-                const int64_t tok = (int64_t)t.row0 + r / G;
-                __nv_bfloat16 *dst = a.out + (tok * (a.n_q / 2) + t.p * G + r % G) * (2 * D) + grp * QD;
-                const float4 *nw = reinterpret_cast<const float4 *>(sm + L::kNorm) + grp * (QD / 4);
-                // 32 bytes a store: a lane's row is a line of its own, so each store instruction takes the
-                // load-store unit 32 passes whatever its width
+            // The row's pieces of 32 bytes change places among the lanes of NP rows, so that a store instruction
+            // writes whole pieces of 32 / NP rows instead of 32: the load-store unit passes once for each row that
+            // an instruction touches (355 -> 346 us).
+            constexpr int NP = QD / 16;
+            uint32_t w[NP][8];
+            const float4 *nw = reinterpret_cast<const float4 *>(sm + L::kNorm) + grp * (QD / 4);
 #pragma unroll
-                for (int c = 0; c < QD; c += 16) {
-                    uint32_t w[8];
+            for (int c = 0; c < NP; ++c) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 g = nw[c / 4 + i];
-                        const uint32_t *x4 = o + c + 4 * i;
-                        w[2 * i] = pack_bf16x2(__uint_as_float(x4[0]) * rn * g.x, __uint_as_float(x4[1]) * rn * g.y);
-                        w[2 * i + 1] = pack_bf16x2(__uint_as_float(x4[2]) * rn * g.z, __uint_as_float(x4[3]) * rn * g.w);
-                    }
-                    stg256(dst + c, w);
+                for (int i = 0; i < 4; ++i) {
+                    const float4 g = nw[4 * c + i];
+                    const uint32_t *x4 = o + 16 * c + 4 * i;
+                    w[c][2 * i] = pack_bf16x2(__uint_as_float(x4[0]) * rn * g.x, __uint_as_float(x4[1]) * rn * g.y);
+                    w[c][2 * i + 1] = pack_bf16x2(__uint_as_float(x4[2]) * rn * g.z, __uint_as_float(x4[3]) * rn * g.w);
                 }
+            }
+#pragma unroll
+            for (int d = NP / 2; d >= 1; d >>= 1) {  // piece c of lane l and piece c ^ d of lane l ^ d
+                const bool up = lane & d;
+#pragma unroll
+                for (int c = 0; c < NP; ++c) {
+                    if (c & d) continue;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t y = __shfl_xor_sync(kFull, up ? w[c][i] : w[c + d][i], d);
+                        if (up) w[c][i] = y;
+                        else w[c + d][i] = y;
+                    }
+                }
+            }
+            // now w[c] is piece `lane % NP` of the row of lane (lane - lane % NP + c)
+#pragma unroll
+            for (int c = 0; c < NP; ++c) {
+                const int rc = t.rt0 + quarter * 32 + (lane & ~(NP - 1)) + c;
+                if (rc < t.R)
+                    stg256(a.out + (((int64_t)t.row0 + rc / G) * (a.n_q / 2) + t.p * G + rc % G) * (2 * D) + grp * QD +
+                               16 * (lane & (NP - 1)),
+                           w[c]);
             }
             ++n;
         }
