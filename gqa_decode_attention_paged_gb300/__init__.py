@@ -474,7 +474,7 @@ def paged_rope_append(pool: Pool, rope: Rope, q, k_new, v_new, positions, slot_m
         n_q = q.shape[1] if q.dim() == 3 else -1
         qp, qs = _rows_ptr(pool, q, "q", n_q, T)
         if q_out is None:
-            q_out = q.new_empty((T, n_q, pool.d_head))
+            q_out = torch.empty((T, n_q, pool.d_head), dtype=torch.bfloat16, device=q.device)
             op, os_ = q_out.data_ptr(), n_q * pool.d_head
         else:
             op, os_ = _rows_ptr(pool, q_out, "q_out", n_q, T)
@@ -511,13 +511,14 @@ def paged_kv_gather(pool: Pool, out_indptr, block_tables, starts=None, n_rows=No
         shape, dev = (n, pool.n_kv, pool.d_head), out_indptr.device
         k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
         v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        kp, vp = k_out.data_ptr(), v_out.data_ptr()
     else:
         n = int(k_out.shape[0])
         if n_rows is not None and n != int(n_rows):
             raise ValueError(f"k_out has {n} rows, n_rows is {n_rows}")
-    shape = (n, pool.n_kv, pool.d_head)
-    kp = _fast_ptr(pool, k_out, "k_out", torch.bfloat16, shape)
-    vp = _fast_ptr(pool, v_out, "v_out", torch.bfloat16, shape)
+        shape = (n, pool.n_kv, pool.d_head)
+        kp = _fast_ptr(pool, k_out, "k_out", torch.bfloat16, shape)
+        vp = _fast_ptr(pool, v_out, "v_out", torch.bfloat16, shape)
     _check(load().paged_kv_gather(pool.handle, ip, tp, W, st, B, n, kp, vp, _raw_stream(pool, stream)))
     return k_out, v_out
 
@@ -615,7 +616,7 @@ def _diff_args(pool, q, params, rows, out):
                          f"{pool.d_head} on cuda:{pool.device}")
     shape = (rows, n_q // 2, 2 * pool.d_head)
     if out is None:
-        out = q.new_empty(shape)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
         return qp, n_q, out, out.data_ptr()
     return qp, n_q, out, _fast_ptr(pool, out, "out", torch.bfloat16, shape)
 
