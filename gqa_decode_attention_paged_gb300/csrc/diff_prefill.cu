@@ -268,7 +268,7 @@ __device__ __forceinline__ int first_of_class(const Walker &w)
 {
     constexpr int q = 2 * kRows / G;  // tokens of a pair of tiles
     const int past = kKeys * (w.steps - 1) - (w.C - w.T);  // of the chunk's tokens, those that fewer steps cover
-    return past < 0 ? 0 : min(past / q, w.left);
+    return past < 0 ? 0 : past >= w.T ? w.left : min(past / q, w.left);
 }
 
 // The entries of the most steps among those left.
