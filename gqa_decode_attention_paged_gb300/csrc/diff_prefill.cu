@@ -19,14 +19,13 @@
 //
 // Design (persistent clusters of two CTAs, one per SM, warp-specialised; the
 // times are of 16 prompts of 700..1024 tokens on contexts of up to 2048, bf16,
-// d_head 128, 32 query heads: 346 us in all, 200 for the MMAs alone):
+// d_head 128, 32 query heads: 369 us in all, 200 for the MMAs alone; pairs of
+// times compare two forms at the state when the choice was made):
 //   * a tile is 128 query rows (token, head) of one (sequence, pair): both
 //     maps' queries.  A step is 128 keys.  The two CTAs of a cluster take
-//     neighbouring tiles of the same (sequence, pair) and walk the same keys:
-//     each copies half of every unit into both CTAs' shared memory (multicast).
-//     A step moves 6 units of 32 KiB into each SM for 3 of MMA work each;
-//     with each CTA copying for itself that bound the kernel (602 us against
-//     435 at that stage).
+//     neighbouring tiles of the same (sequence, pair) and walk the same keys at
+//     about the same time, each copying for itself (the second read of a unit
+//     comes from the L2).  A step moves 6 units of 32 KiB into each SM.
 //   * warp 16 streams Q and, through one ring, what the MMAs take in the order
 //     they take it: K_m units (128 keys of one map) and, in the second sweep, V
 //     units (64 keys x 2 d channels).  One ring for both: in the first sweep
@@ -445,7 +444,6 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
     const int warp = __shfl_sync(kFull, tid >> 5, 0);  // the same in all lanes, and known to be
     constexpr bool kPair = MODE == kWhole;
     const int rank = (int)cluster_rank(), ranges = kPair ? 2 : (int)cluster_size();
-    constexpr uint16_t kBoth = 3;
     // the cluster's entries of the list: there and back in turns (c, 2 N - 1 - c, 2 N + c, ..; kWhole), or one
     const int e0 = (int)(kPair ? blockIdx.x / 2 : blockIdx.x / ranges);
     const int turn = (int)gridDim.x, hop0 = turn - 1 - 2 * e0;  // (2 N)
@@ -466,7 +464,6 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
             if (i >= L::QUAD && i < L::QUAD + 4) n = 4;  // the four warps of a lane quarter
             if (i == L::Q_FULL && F8) n = kSoftmaxWarps;  // each widens its share of the queries
             if (i >= L::FULL && i < L::EMPTY) n = kSplit;
-            if (i >= L::EMPTY && i < L::EMPTY + NS && kPair) n = 2;  // both CTAs have used the slot
             if (i == L::STAT) n = 4 * ranges;              // of every CTA, the warps that hold a row's statistics
             if (i == L::PARTS) n = kSoftmaxWarps * ranges;
             if (i == L::DRAIN) n = 2;
@@ -555,17 +552,14 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                     return valid ? (int)((id * (int64_t)a.n_kv + 2 * t.p) * 2 * kBlockSize) : a.oob_row;
                 };
                 auto copy_box = [&](uint32_t to, int c, int y, uint32_t land) {
-                    if constexpr (kPair) tma_load_2d_multicast_if(go, to, &tm_kv, c, y, land, kBoth, policy);
-                    else tma_load_2d_if(go, to, &tm_kv, c, y, land, policy);
+                    tma_load_2d_if(go, to, &tm_kv, c, y, land, policy);
                 };
                 constexpr int kTileRows = D == 128 ? kKeys : kVKeys;  // of a K unit's tiles, FP8 pools
-                constexpr int kShare = kPair ? 2 : 1;  // this CTA's blocks of a unit: every kShare-th
                 auto copy_k = [&](int y0, int m) -> bool {
                     uint32_t land, dst;
                     if (!open(land, dst)) return false;
 #pragma unroll
-                    for (int i = 0; i < kStepBlocks / kShare; ++i) {
-                        const int k = kShare * i + (kPair ? rank : 0);
+                    for (int k = 0; k < kStepBlocks; ++k) {
                         const int yk = __shfl_sync(kFull, y0, k);
                         const int y = yk == a.oob_row ? yk : yk + m * 2 * kBlockSize;
                         if constexpr (F8) {
@@ -584,8 +578,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                     uint32_t land, dst;
                     if (!open(land, dst)) return false;
 #pragma unroll
-                    for (int i = 0; i < kUnitBlocks / kShare; ++i) {
-                        const int k = kShare * i + (kPair ? rank : 0);
+                    for (int k = 0; k < kUnitBlocks; ++k) {
                         const int yk = __shfl_sync(kFull, y0, h * kUnitBlocks + k);
 #pragma unroll
                         for (int head = 0; head < 2; ++head) {
@@ -621,9 +614,6 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
             // copies still in flight (after an abort) land before the CTA exits
             for (int i = max(0, u - NS); i < u; ++i)
                 mbar_wait_bounded(&bar[(F8 ? L::RAW : L::FULL) + i % NS], (i / NS) & 1);
-            // and the other CTA's arrivals on this one's barriers (none comes after the last units')
-            for (int i = max(0, u - NS); i < u && ok && !*abort_flag; ++i)
-                ok = wait_all(&bar[L::EMPTY + i % NS], (i / NS) & 1);
             if (n > 0) mbar_wait_bounded(&bar[F8 ? L::Q_RAW : L::Q_FULL], (n - 1) & 1);
             if (!ok) set_abort();
         } else if (warp >= kPrepWarp && warp < Wp::kProduct) {
@@ -714,10 +704,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
             // those that the weights (or the products) it has just waited for were made from.
             auto unit = [&]() -> bool { return wait_all(&bar[L::FULL + slot], ph); };
             // the unit in slot v has been used when this warp's MMAs so far have run
-            auto release = [&](int v) {
-                if constexpr (kPair) umma_commit_multicast_if(go, &bar[L::EMPTY + v], kBoth);
-                else umma_commit_if(go, &bar[L::EMPTY + v]);
-            };
+            auto release = [&](int v) { umma_commit_if(go, &bar[L::EMPTY + v]); };
             // keys [64 half, 64 half + N) of the unit in slot v against map m's queries
             auto scores = [&](int m, int v, int half, uint32_t idesc) {
                 tc_fence_after();

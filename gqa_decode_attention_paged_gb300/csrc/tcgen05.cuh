@@ -99,28 +99,6 @@ __device__ __forceinline__ void tma_load_2d_if(uint32_t go, uint32_t dst_smem, c
                  : "memory");
 }
 
-// The same into every CTA of the cluster named by `mask`, at the same place of its shared memory and
-// completing on its barrier there.
-__device__ __forceinline__ void tma_load_2d_multicast_if(uint32_t go, uint32_t dst_smem, const CUtensorMap *map, int x,
-                                                         int y, uint32_t bar, uint16_t mask, uint64_t policy)
-{
-    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %7, 0;\n\t"
-                 "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                 ".multicast::cluster.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5, %6;\n\t}"
-                 ::"r"(dst_smem), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "h"(mask), "l"(policy),
-                 "r"(go)
-                 : "memory");
-}
-
-// umma_commit_if on the barrier at the same place in every CTA of the cluster named by `mask`.
-__device__ __forceinline__ void umma_commit_multicast_if(uint32_t go, uint64_t *bar, uint16_t mask)
-{
-    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
-                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
-                 ::"r"(smem_u32(bar)), "h"(mask), "r"(go)
-                 : "memory");
-}
-
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
