@@ -669,12 +669,14 @@ struct Plan {
     size_t ml_bytes = 0, bytes = 0;
 };
 
+// `most_resident`: for any number of sequences up to `batch`.  Every part of the plan rises with the batch but the
+// resident CTAs, whose shared memory holds the batch's lists: the fewest sequences have the most of them.
 template <int D, int G, int KV>
-pkv_status plan_call(const pkv_pool *pool, int batch, int W, Plan *pl)
+pkv_status plan_call(const pkv_pool *pool, int batch, int W, Plan *pl, bool most_resident = false)
 {
     using C = DCfg<D, G, KV>;
     int occ = 0;
-    pkv_status st = resident<D, G, KV>(pool, batch, &occ);
+    pkv_status st = resident<D, G, KV>(pool, most_resident ? 1 : batch, &occ);
     if (st != PKV_OK) return st;
     const int slice_blocks = pool->partition_tokens / kBlockSize;
     const int64_t most = (int64_t)batch * (pool->n_kv / 2) * W;  // blocks of the largest possible batch
@@ -742,8 +744,11 @@ struct Launch {
 };
 
 template <int D, int G, int KV>
-struct PlanCall {
-    static pkv_status run(const pkv_pool *pool, int batch, int W, Plan *pl) { return plan_call<D, G, KV>(pool, batch, W, pl); }
+struct PlanMost {
+    static pkv_status run(const pkv_pool *pool, int batch, int W, Plan *pl)
+    {
+        return plan_call<D, G, KV>(pool, batch, W, pl, true);
+    }
 };
 
 }  // namespace
@@ -820,7 +825,11 @@ extern "C" pkv_status paged_diff_reserve_workspace(pkv_pool *pool, int32_t batch
     if (st == PKV_OK) st = check_diff_pool(pool, who);
     if (st != PKV_OK || batch == 0) return st;
     st = check_pool_device(pool, who);
-    Plan pl;
-    if (st == PKV_OK) st = for_config<PlanCall>(pool, n_q / pool->n_kv, pool, batch, max_blocks_per_seq, &pl);
-    return st == PKV_OK ? ensure_workspace(pool, pl.bytes) : st;
+    size_t bytes = 0;
+    for (int G = 1; st == PKV_OK && G <= n_q / pool->n_kv; G *= 2) {  // fewer query heads, too
+        Plan pl;
+        st = for_config<PlanMost>(pool, G, pool, batch, max_blocks_per_seq, &pl);
+        bytes = std::max(bytes, pl.bytes);
+    }
+    return st == PKV_OK ? ensure_workspace(pool, bytes) : st;
 }
