@@ -260,6 +260,16 @@ def kv_bytes_per_token(layers: int, n_kv: int, d_head: int, bytes_per_value: flo
     return float(load().kv_bytes_per_token(layers, n_kv, d_head, float(bytes_per_value)))
 
 
+class _PoolMemory:
+    """A pool's memory through the CUDA array interface.  A tensor made from it holds it, and so the pool
+    (which holds neither: the last view that goes lets the pool go at once)."""
+
+    def __init__(self, pool, ptr, n):
+        self.pool = pool
+        self.__cuda_array_interface__ = {"shape": (n,), "typestr": "|u1", "data": (ptr, False), "version": 3,
+                                         "strides": None}
+
+
 class Pool:
     """A K/V block pool owned by the library (one layer).  Use kv_pool_create().
     Its memory lives until close() (or the end of the ``with`` block), or until
@@ -375,12 +385,7 @@ class Pool:
     def _bytes_view(self, ptr, n):
         import torch
 
-        class _Holder:  # exposes the pool's memory through the CUDA array interface
-            __cuda_array_interface__ = {"shape": (n,), "typestr": "|u1", "data": (ptr, False),
-                                        "version": 3, "strides": None}
-            pool = self  # the tensor holds this object, so the memory outlives every view of it
-
-        return torch.as_tensor(_Holder(), device="cuda")
+        return torch.as_tensor(_PoolMemory(self, ptr, n), device="cuda")
 
     def _alloc_bytes_view(self, lay):
         """The pool's whole allocation (every (block, KV head) entry), as uint8."""
