@@ -210,6 +210,21 @@ def _raw_stream(pool, stream):
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
+def _output(shape, device, stream):
+    """A bf16 output, from the memory of the stream that the call goes to: memory of another stream may still
+    be in use by what that one has to do, and would be used again by it as soon as the output is dropped."""
+    import torch
+
+    if stream is not None:
+        handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+        if handle != torch._C._cuda_getCurrentRawStream(device.index):
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(handle, device=device)
+            with torch.cuda.stream(stream):
+                return torch.empty(shape, dtype=torch.bfloat16, device=device)
+    return torch.empty(shape, dtype=torch.bfloat16, device=device)
+
+
 def _fast_ptr(pool, t, name, dtype, shape):
     """Address of a contiguous tensor of this exact shape and type on the pool's device (cheap checks
     first: small calls are bound by the host; what fails them gets _pool_ptr's message)."""
@@ -479,7 +494,7 @@ def paged_rope_append(pool: Pool, rope: Rope, q, k_new, v_new, positions, slot_m
         n_q = q.shape[1] if q.dim() == 3 else -1
         qp, qs = _rows_ptr(pool, q, "q", n_q, T)
         if q_out is None:
-            q_out = torch.empty((T, n_q, pool.d_head), dtype=torch.bfloat16, device=q.device)
+            q_out = _output((T, n_q, pool.d_head), q.device, stream)
             op, os_ = q_out.data_ptr(), n_q * pool.d_head
         else:
             op, os_ = _rows_ptr(pool, q_out, "q_out", n_q, T)
@@ -514,8 +529,7 @@ def paged_kv_gather(pool: Pool, out_indptr, block_tables, starts=None, n_rows=No
             raise ValueError("give n_rows, or k_out and v_out")
         n = int(n_rows)
         shape, dev = (n, pool.n_kv, pool.d_head), out_indptr.device
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        k_out, v_out = _output(shape, dev, stream), _output(shape, dev, stream)
         kp, vp = k_out.data_ptr(), v_out.data_ptr()
     else:
         n = int(k_out.shape[0])
@@ -539,7 +553,7 @@ def paged_decode_attention(pool: Pool, q, block_tables, context_lens, scale: flo
     tp = _dev_ptr(block_tables, "block_tables", torch.int32, 2, (B, None))
     cp = _dev_ptr(context_lens, "context_lens", torch.int32, 1, (B,))
     if out is None:
-        out = torch.empty_like(q)
+        out = _output(q.shape, q.device, stream)
     op = _dev_ptr(out, "out", torch.bfloat16, 3, tuple(q.shape))
     _check(load().paged_decode_attention(pool.handle, qp, n_q, tp, int(block_tables.shape[1]), cp, B,
                                          float(scale), op, _stream_handle(stream)))
@@ -558,7 +572,7 @@ def paged_decode_attention_csr(pool: Pool, q, kv_indptr, kv_indices, context_len
     xp = _dev_ptr(kv_indices, "kv_indices", torch.int32, 1)
     cp = _dev_ptr(context_lens, "context_lens", torch.int32, 1, (B,))
     if out is None:
-        out = torch.empty_like(q)
+        out = _output(q.shape, q.device, stream)
     op = _dev_ptr(out, "out", torch.bfloat16, 3, tuple(q.shape))
     _check(load().paged_decode_attention_csr(pool.handle, qp, n_q, ip, xp, int(kv_indices.shape[0]), cp, B,
                                              float(scale), op, _stream_handle(stream)))
@@ -580,7 +594,7 @@ def paged_prefill_attention(pool: Pool, q, qo_indptr, block_tables, context_lens
     tp = _dev_ptr(block_tables, "block_tables", torch.int32, 2, (B, None))
     cp = _dev_ptr(context_lens, "context_lens", torch.int32, 1, (B,))
     if out is None:
-        out = torch.empty_like(q)
+        out = _output(q.shape, q.device, stream)
     op = _dev_ptr(out, "out", torch.bfloat16, 3, tuple(q.shape))
     _check(load().paged_prefill_attention(pool.handle, qp, rows, n_q, ip, tp, int(block_tables.shape[1]), cp, B,
                                           float(scale), op, _stream_handle(stream)))
@@ -606,7 +620,7 @@ class DiffParams:
         self._ref = ctypes.byref(self._c)
 
 
-def _diff_args(pool, q, params, rows, out):
+def _diff_args(pool, q, params, rows, out, stream):
     """Checks shared by the differential calls; (q pointer, n_q, out, out pointer)."""
     import torch
 
@@ -621,7 +635,7 @@ def _diff_args(pool, q, params, rows, out):
                          f"{pool.d_head} on cuda:{pool.device}")
     shape = (rows, n_q // 2, 2 * pool.d_head)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        out = _output(shape, q.device, stream)
         return qp, n_q, out, out.data_ptr()
     return qp, n_q, out, _fast_ptr(pool, out, "out", torch.bfloat16, shape)
 
@@ -635,7 +649,7 @@ def paged_diff_decode_attention(pool: Pool, q, block_tables, context_lens, scale
     import torch
 
     B, W = int(context_lens.shape[0]), int(block_tables.shape[-1])
-    qp, n_q, out, op = _diff_args(pool, q, params, B, out)
+    qp, n_q, out, op = _diff_args(pool, q, params, B, out, stream)
     cp = _fast_ptr(pool, context_lens, "context_lens", torch.int32, (B,))
     tp = _fast_ptr(pool, block_tables, "block_tables", torch.int32, (B, W))
     _check(load().paged_diff_decode_attention(pool.handle, qp, n_q, tp, W, cp, B, float(scale), params._ref, op,
@@ -654,7 +668,7 @@ def paged_diff_prefill_attention(pool: Pool, q, qo_indptr, block_tables, context
 
     B, W = int(context_lens.shape[0]), int(block_tables.shape[-1])
     rows = int(q.shape[0])
-    qp, n_q, out, op = _diff_args(pool, q, params, rows, out)
+    qp, n_q, out, op = _diff_args(pool, q, params, rows, out, stream)
     cp = _fast_ptr(pool, context_lens, "context_lens", torch.int32, (B,))
     ip = _fast_ptr(pool, qo_indptr, "qo_indptr", torch.int32, (B + 1,))
     tp = _fast_ptr(pool, block_tables, "block_tables", torch.int32, (B, W))
@@ -676,7 +690,7 @@ def paged_decode_attention_prefix(pool: Pool, q, prefix_blocks, block_tables, co
     tp = _dev_ptr(block_tables, "block_tables", torch.int32, 2, (B, None))
     cp = _dev_ptr(context_lens, "context_lens", torch.int32, 1, (B,))
     if out is None:
-        out = torch.empty_like(q)
+        out = _output(q.shape, q.device, stream)
     op = _dev_ptr(out, "out", torch.bfloat16, 3, tuple(q.shape))
     _check(load().paged_decode_attention_prefix(pool.handle, qp, n_q, pp, int(prefix_blocks.shape[0]), tp,
                                                 int(block_tables.shape[1]), cp, B, float(scale), op,
@@ -697,7 +711,7 @@ def paged_decode_step(pool: Pool, q, k_new, v_new, block_tables, context_lens, s
     tp = _dev_ptr(block_tables, "block_tables", torch.int32, 2, (B, None))
     cp = _dev_ptr(context_lens, "context_lens", torch.int32, 1, (B,))
     if out is None:
-        out = torch.empty_like(q)
+        out = _output(q.shape, q.device, stream)
     op = _dev_ptr(out, "out", torch.bfloat16, 3, tuple(q.shape))
     _check(load().paged_decode_step(pool.handle, qp, kp, vp, n_q, tp, int(block_tables.shape[1]), cp, B,
                                     float(scale), op, _stream_handle(stream)))
@@ -783,7 +797,7 @@ def paged_decode_attention_noalloc(pool: Pool, q, block_tables, context_lens, sc
     tp = _dev_ptr(block_tables, "block_tables", torch.int32, 2, (B, None))
     cp = _dev_ptr(context_lens, "context_lens", torch.int32, 1, (B,))
     if out is None:
-        out = torch.empty_like(q)
+        out = _output(q.shape, q.device, stream)
     op = _dev_ptr(out, "out", torch.bfloat16, 3, tuple(q.shape))
     _check(load().paged_decode_attention_noalloc(pool.handle, qp, n_q, tp, int(block_tables.shape[1]), cp, B,
                                                  float(scale), op, _stream_handle(stream)))
