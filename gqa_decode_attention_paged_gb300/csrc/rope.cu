@@ -7,11 +7,13 @@
 //   (a, b) -> (a cos - b sin, b cos + a sin).
 // Positions are whole numbers, so only the fraction of a turn that inv_freq
 // makes per position matters: the host stores turn_i = frac(inv_freq[i] /
-// 2 pi) as a 64-bit fixed-point fraction, the kernel multiplies it by the
-// position modulo 2^64 (exact, whatever the position) and takes sine and
-// cosine of the top 32 bits (turn_of).  The angle is thus good to about
-// 2^-32 of a turn at every position, where a 32-bit product would be off by
-// 2^-24 * angle (0.004 radians at 65536), without 64-bit floating point.
+// 2 pi) as a 64-bit fixed-point fraction (turn_fraction), the kernel multiplies
+// it by the position modulo 2^64 (exact, whatever the position) and takes sine
+// and cosine of the top 32 bits (turn_of).  The angle is thus off by at most
+// 2^-34 of a turn from the fraction's rounding, at the farthest position, and
+// 2^-33 from the top bits': below 2^-32 at every position, where a 32-bit
+// product would be off by 2^-24 * angle (0.004 radians at 65536), without
+// 64-bit floating point in the kernel.
 // The rotation runs in fp32 and is rounded once: to bf16 (queries, bf16
 // pools), to E4M3 or to the 4-bit code.
 //
@@ -25,6 +27,7 @@
 // copy rate; a decode step's 64 tokens: 6.2 us, the latency of a launch and of
 // two dependent loads.
 #include "pkv_internal.cuh"
+#include "turn.cuh"
 
 #include <math.h>
 
@@ -421,9 +424,7 @@ extern "C" pkv_status pkv_rope_create(int32_t rot_dim, int32_t interleaved, int3
     r->interleaved = interleaved;
     r->n_axes = n_axes;
     for (int i = 0; i < rot_dim / 2; ++i) {
-        const double f = inv_freq[i] * 0.15915494309189533577;  // turns per position
-        const double fixed = ldexp(f - floor(f), 64);            // in [0, 2^64]
-        r->turn[i] = fixed < 18446744073709551616.0 ? (uint64_t)fixed : 0;
+        r->turn[i] = turn_fraction(inv_freq[i]);
         r->axis[i] = (uint8_t)(pair_axis ? pair_axis[i] : 0);
     }
     *out = r;
