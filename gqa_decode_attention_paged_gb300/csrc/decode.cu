@@ -1284,7 +1284,7 @@ static pkv_status launch_decode(pkv_pool *pool, DecodeArgs a, cudaStream_t s)
     pkv_status st = decode_grid<D, G, KV>(pool, a.batch, a.W, &grid, &smem);
     if (st != PKV_OK) return st;
     const WsLayout L = ws_layout(a.n_q, a.n_kv, D, max_slots(pool, a.batch, a.n_kv, a.W, grid * C::NW));
-    st = ensure_workspace(pool, L.total);
+    st = ensure_workspace(pool, L.total, s, nullptr);
     if (st != PKV_OK) return st;
     bind_workspace(a, static_cast<uint8_t *>(pool->ws), L);
     LaunchScope ls(pool, kDecode, s);
@@ -1504,7 +1504,7 @@ static pkv_status launch_step(pkv_pool *pool, DecodeArgs a, cudaStream_t s)
     pkv_status st = decode_grid<D, G, KV, true>(pool, a.batch, a.W, &grid, &smem);
     if (st != PKV_OK) return st;
     const WsLayout L = ws_layout(a.n_q, a.n_kv, D, max_slots(pool, a.batch, a.n_kv, a.W, grid * C::NW));
-    st = ensure_workspace(pool, L.total);
+    st = ensure_workspace(pool, L.total, s, nullptr);
     if (st != PKV_OK) return st;
     bind_workspace(a, static_cast<uint8_t *>(pool->ws), L);
     LaunchScope ls(pool, kDecode, s);
@@ -1748,6 +1748,7 @@ extern "C" pkv_status paged_decode_step_host(pkv_pool *pool, const void *q_host,
             return PKV_OK;
         }
         cudaStream_t cs = pool->capture_stream;
+        const bool captured = pool->ws_captured;  // this graph is not replayed once the workspace is another
         cudaGraph_t graph = nullptr;
         bool ok = cudaStreamBeginCapture(cs, cudaStreamCaptureModeThreadLocal) == cudaSuccess;
         if (ok) {
@@ -1759,6 +1760,7 @@ extern "C" pkv_status paged_decode_step_host(pkv_pool *pool, const void *q_host,
             const bool ended = cudaStreamEndCapture(cs, &graph) == cudaSuccess;
             ok = ok && ended && graph;
         }
+        pool->ws_captured = captured;
         cudaGraphExec_t exec = nullptr;
         if (ok && cudaGraphInstantiate(&exec, graph, 0) == cudaSuccess) {
             if (pool->host_graph) cudaGraphExecDestroy(pool->host_graph);
@@ -1813,7 +1815,7 @@ static pkv_status launch_prefix_decode(pkv_pool *pool, DecodeArgs a, const int32
     prefix_stage_chunks(pool, a.batch, a.n_q, n_prefix_blocks, &chunk_blocks, &n_chunks);
     const int64_t tail_slots = max_slots(pool, a.batch, a.n_kv, a.W, grid * C::NW);
     const WsLayout L = ws_layout(a.n_q, a.n_kv, D, tail_slots + (int64_t)n_chunks * a.batch * a.n_kv);
-    st = ensure_workspace(pool, L.total);
+    st = ensure_workspace(pool, L.total, s, nullptr);
     if (st != PKV_OK) return st;
     bind_workspace(a, static_cast<uint8_t *>(pool->ws), L);
     a.skip_blocks = n_prefix_blocks;

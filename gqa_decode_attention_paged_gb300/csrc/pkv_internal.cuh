@@ -93,7 +93,8 @@ struct pkv_pool {
     unsigned *err = nullptr;          // device sticky error word
     void *ws = nullptr;               // split-KV workspace (grow-only)
     size_t ws_bytes = 0;
-    std::vector<void *> old_ws;       // workspaces replaced by larger ones (graphs may use them)
+    bool ws_captured = false;         // a captured graph may use it
+    std::vector<void *> old_ws;       // captured workspaces replaced by larger ones
     void *stage = nullptr;            // device staging for paged_decode_step_host (grow-only)
     size_t stage_bytes = 0;
     int partition_tokens = pkv::kDefaultPartitionTokens;
@@ -134,11 +135,12 @@ struct LaunchScope {
     void done();
 };
 
-// Grows the workspace to `bytes` at least.  The one it replaces is kept until
-// the pool is destroyed: a captured graph may still use it.
+// Grows the workspace to `bytes` at least.  One that a capture has seen is kept until
+// the pool is destroyed, as the graph may still use it; any other is freed first.
 pkv_status ensure_workspace(pkv_pool *pool, size_t bytes);
-// The same, refused (PKV_EINVAL) where it would have to allocate while `s` is captured.
-pkv_status ensure_workspace(pkv_pool *pool, size_t bytes, cudaStream_t s, const char *who);
+// The same for a launch on `s`.  `refuse`: the caller's name, where growing while `s` is
+// captured is refused (PKV_EINVAL); null: left to CUDA, which allows it in some capture modes.
+pkv_status ensure_workspace(pkv_pool *pool, size_t bytes, cudaStream_t s, const char *refuse);
 // The device address of paged_decode_attention_noalloc's scratch array on the
 // current device (cudaGetSymbolAddress; loads the decode code if it is not
 // loaded yet, which reserves the array's memory).

@@ -66,31 +66,61 @@ pkv_status check_pool_device(const pkv_pool *pool, const char *who)
     return PKV_OK;
 }
 
-pkv_status ensure_workspace(pkv_pool *pool, size_t bytes)
+static pkv_status grow_workspace(pkv_pool *pool, size_t bytes, bool capturing)
 {
-    if (bytes <= pool->ws_bytes) return PKV_OK;
-    // grow with headroom; at least doubling keeps all replaced workspaces together below the current one
-    size_t want = std::max(bytes + bytes / 4, 2 * pool->ws_bytes);
-    want = (want + (1u << 20) - 1) & ~size_t((1u << 20) - 1);
+    const size_t unit = size_t(1) << 20;
+    auto round_up = [&](size_t x) { return (x + unit - 1) & ~(unit - 1); };
+    size_t want = bytes + bytes / 4;  // grow with headroom
+    if (pool->ws && (pool->ws_captured || capturing)) {
+        // at least doubling keeps all workspaces that are kept together below the current one
+        want = std::max(want, 2 * pool->ws_bytes);
+        try {
+            pool->old_ws.reserve(pool->old_ws.size() + 1);
+        } catch (const std::bad_alloc &) {
+            return fail(PKV_ENOMEM, "workspace: host allocation failed");
+        }
+    } else if (pool->ws) {
+        cudaError_t e = cudaFree(pool->ws);  // synchronises: no kernel still uses it
+        pool->ws = nullptr;
+        pool->ws_bytes = 0;
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFree(workspace)");
+    }
+    want = round_up(want);
     void *fresh = nullptr;
     cudaError_t e = cudaMalloc(&fresh, want);
+    if (e == cudaErrorMemoryAllocation && round_up(bytes) < want) {  // no room for the headroom
+        cudaGetLastError();
+        want = round_up(bytes);
+        e = cudaMalloc(&fresh, want);
+    }
     if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(workspace)");
-    if (pool->ws) pool->old_ws.push_back(pool->ws);  // captured graphs may still use it
+    if (pool->ws) pool->old_ws.push_back(pool->ws);
     pool->ws = fresh;
     pool->ws_bytes = want;
+    pool->ws_captured = false;
     return PKV_OK;
 }
 
-pkv_status ensure_workspace(pkv_pool *pool, size_t bytes, cudaStream_t s, const char *who)
+pkv_status ensure_workspace(pkv_pool *pool, size_t bytes)
 {
-    if (bytes <= pool->ws_bytes) return PKV_OK;
+    return bytes <= pool->ws_bytes ? PKV_OK : grow_workspace(pool, bytes, false);
+}
+
+pkv_status ensure_workspace(pkv_pool *pool, size_t bytes, cudaStream_t s, const char *refuse)
+{
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    cudaError_t e = cudaStreamIsCapturing(s, &cap);
-    if (e != cudaSuccess) cudaGetLastError();
-    if (e != cudaSuccess || cap != cudaStreamCaptureStatusNone)
-        return fail(PKV_EINVAL, "%s: the workspace has to grow to %zu bytes while the stream is captured; reserve it "
-                    "first", who, bytes);
-    return ensure_workspace(pool, bytes);
+    const cudaError_t e = cudaStreamIsCapturing(s, &cap);
+    if (e != cudaSuccess) cudaGetLastError();  // the legacy stream while another one is captured
+    const bool capturing = e == cudaSuccess && cap != cudaStreamCaptureStatusNone;
+    if (bytes > pool->ws_bytes) {
+        if (refuse && (capturing || e != cudaSuccess))
+            return fail(PKV_EINVAL, "%s: the workspace has to grow to %zu bytes while the stream is captured; reserve it "
+                        "first", refuse, bytes);
+        pkv_status st = grow_workspace(pool, bytes, capturing);
+        if (st != PKV_OK) return st;
+    }
+    pool->ws_captured |= capturing;
+    return PKV_OK;
 }
 
 pkv_status ensure_staging(pkv_pool *pool, size_t bytes)
