@@ -71,34 +71,6 @@ struct RopeArgs {
     unsigned *err;
 };
 
-// Sine and cosine of u 2^-32 turns: the nearest quarter turn is taken off as an integer, and the rest t, within
-// pi / 4, goes into the Taylor series of both, with what its 24 bits cannot hold (lo) and with the rounding of the
-// cosine's second sum.  Off by 0.71 of a last place at most, 0.25 in the mean (which is that of rounding alone), as
-// fast as sincospif of the rounded angle, which is off by up to 2.
-__device__ __forceinline__ void turn_of(uint32_t u, float &sn, float &cs)
-{
-    constexpr float kPi = 3.14159274f, kPiRest = -8.74227766e-8f;  // pi and what its rounding leaves
-    const uint32_t quarter = (u + 0x20000000u) >> 30;
-    const int32_t rest = (int32_t)(u - (quarter << 30));  // within 2^29
-    const float n = (float)rest;
-    const float x = n * 4.656612873077393e-10f;  // 2^-31 half turns
-    const float t = x * kPi;
-    const float lo = fmaf(x, kPi, -t) + fmaf(x, kPiRest, (float)(rest - (int32_t)n) * (kPi * 4.656612873077393e-10f));
-    const float z = t * t, zl = fmaf(t, t, -z);
-    float p = fmaf(z, 1.0f / 362880, -1.0f / 5040);
-    p = fmaf(p, z, 1.0f / 120);
-    p = fmaf(p, z, -1.0f / 6);
-    const float s = t + fmaf(t * z, p, fmaf(-0.5f * z, lo, lo));
-    float q = fmaf(z, -1.0f / 3628800, 1.0f / 40320);
-    q = fmaf(q, z, -1.0f / 720);
-    q = fmaf(q, z, 1.0f / 24);
-    const float w = 1.0f - 0.5f * z, e = (1.0f - w) - 0.5f * z;  // (exact)
-    const float c = w + (e + fmaf(z * z, q, fmaf(-lo, t, -0.5f * zl)));
-    const float a = quarter & 1u ? c : s, b = quarter & 1u ? s : c;
-    sn = quarter & 2u ? -a : a;
-    cs = (quarter + 1u) & 2u ? -b : b;
-}
-
 // 4-bit code of x: clamp(rint((x - z) / s), 0, 15), each step correctly rounded in fp32, NaN to 0.  `r` is
 // 1 / s to a few units of its last place: the product with it is off by less than 2^-17 where the code is
 // not clamped, so the correctly rounded quotient is needed only next to a border between two codes (or
