@@ -72,7 +72,7 @@ struct RopeArgs {
 };
 
 // 4-bit code of x: clamp(rint((x - z) / s), 0, 15), each step correctly rounded in fp32, NaN to 0.  `r` is
-// 1 / s to a few units of its last place: the product with it is off by less than 2^-17 where the code is
+// 1 / s to a few units of its last place, or NaN: the product with it is off by less than 2^-17 where the code is
 // not clamped, so the correctly rounded quotient is needed only next to a border between two codes (or
 // where the product is not finite); everywhere else both round to the same code.
 __device__ __forceinline__ uint32_t code4(float x, float s, float z, float r)
@@ -99,7 +99,8 @@ __device__ __forceinline__ uint32_t key_codes(const float *x, const float *ks, c
     const float zv[8] = {z[0].x, z[0].y, z[0].z, z[0].w, z[1].x, z[1].y, z[1].z, z[1].w};
     uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w |= code4(x[i], sv[i], zv[i], rcp_approx(sv[i])) << (4 * i);
+    for (int i = 0; i < 8; ++i)  // (from 2^126 on 1 / s is below fp32's normal range, and NaN asks for the quotient)
+        w |= code4(x[i], sv[i], zv[i], sv[i] < 0x1p126f ? rcp_approx(sv[i]) : __int_as_float(0x7fffffff)) << (4 * i);
     return w;
 }
 

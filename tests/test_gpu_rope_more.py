@@ -39,3 +39,35 @@ def test_rope_append_turns_by_fast_frequencies_at_far_positions():
         ref = np.concatenate((a * c - b * s, b * c + a * s), -1)
         size = np.tile(np.abs(a) + np.abs(b), 2)
         assert (np.abs(y - ref) <= 2.0 ** -21 * size + 2.0 ** -8 * np.abs(ref)).all()
+
+
+@pytest.mark.gpu
+def test_rope_append_gives_every_bf16_key_the_4_bit_code_of_the_plain_append():
+    """All 2^16 bit patterns as keys at position 0, with scales from one end of fp32's range to the other and zero
+    points beside and far from them: the same bytes as the append's correctly rounded quotient."""
+    d, free = 128, 112  # channels that turn (the first 16) hold 0: one that is not finite spoils its pair's other one
+    scales = np.float32([1e-45, 1e-39, 2.0 ** -126, 1e-30, 0.01, 0.37, 1.0, 3.0, 1e30, 2.0 ** 125, 2.0 ** 126, 1.2e38, 3.4e38])
+    n_kv = len(scales)
+    ks = np.repeat(scales[:, None], d, 1)
+    kz = np.clip(ks.astype(np.float64) * np.repeat([-7.5, 0.0, 1.0, -1e38], d // 4), -3e38, 3e38).astype(np.float32)
+    # every pattern meets every zero point: rows of 112 patterns, four times, turned by 28 channels each time
+    T = 592
+    x = torch.arange(T * free, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).view(T, free)
+    k = torch.zeros(4 * T, n_kv, d, dtype=torch.bfloat16)
+    for i in range(4):
+        k[i * T:(i + 1) * T, :, 16:] = torch.roll(x, 28 * i, -1)[:, None]
+    k = k.cuda()
+    T *= 4
+    v = torch.zeros_like(k)
+    slots, pos = torch.arange(T, device="cuda"), torch.zeros(1, T, dtype=torch.int32, device="cuda")
+    got = []
+    for rotary in (False, True):
+        with pkv.kv_pool_create(T // BS, BS, n_kv, d, pkv.INT4) as pool:
+            pool.set_int4_key_params(ks, kz)
+            if rotary:
+                pkv.paged_rope_append(pool, pkv.Rope(np.ones(8)), None, k, v, pos, slots)
+            else:
+                pkv.paged_kv_append(pool, k, v, slots)
+            got.append(pool.k_view().cpu().numpy())
+    bad = [(float(scales[g]), int((got[0][:, g] != got[1][:, g]).sum())) for g in range(n_kv)]
+    assert all(n == 0 for _, n in bad), bad
