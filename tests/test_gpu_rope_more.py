@@ -71,3 +71,37 @@ def test_rope_append_gives_every_bf16_key_the_4_bit_code_of_the_plain_append():
             got.append(pool.k_view().cpu().numpy())
     bad = [(float(scales[g]), int((got[0][:, g] != got[1][:, g]).sum())) for g in range(n_kv)]
     assert all(n == 0 for _, n in bad), bad
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_rope_append_and_plain_append_store_4_bit_values_within_a_rounding_of_one_another(d):
+    """The rows' scales are (max - min) * fp32(1/15) here and (max - min) / 15 there: fp32(1/15) is off by at most 2^-24
+    of itself and each result by its rounding, 2^-24, so they differ by at most 3 * 2^-24 of the scale; the minimum
+    is the same.  (v - min) / scale then differs by at most 15 * 5 * 2^-24 (each quotient is rounded, too) < 2^-17, so
+    only a value that close to the border between two codes gets another one, the next, and both stand for it within
+    half a step and that."""
+    T, n_kv = 512, 3
+    g = torch.Generator().manual_seed(d)
+    v = torch.randn(T, n_kv, d, generator=g).to(torch.bfloat16)
+    v[0], v[1] = 0, 2.5
+    v[2] = torch.arange(d).to(torch.bfloat16)
+    slots, pos = torch.arange(T, device="cuda"), torch.zeros(1, T, dtype=torch.int32, device="cuda")
+    got = []
+    for rotary in (False, True):
+        with pkv.kv_pool_create(T // BS, BS, n_kv, d, pkv.INT4) as pool:
+            pool.set_int4_key_params(np.ones((n_kv, d)), np.zeros((n_kv, d)))
+            if rotary:
+                pkv.paged_rope_append(pool, pkv.Rope(np.ones(8)), None, v.cuda(), v.cuda(), pos, slots)
+            else:
+                pkv.paged_kv_append(pool, v.cuda(), v.cuda(), slots)
+            c = pool.v_view().cpu().transpose(1, 2).reshape(T, n_kv, d // 2)
+            p = pool.v_params_view().cpu().transpose(1, 2).reshape(T, n_kv, 2).double()
+            got.append((torch.stack((c & 15, c >> 4), -1).reshape(T, n_kv, d).double(), p[..., :1], p[..., 1:]))
+    (c0, s0, z0), (c1, s1, z1) = got
+    assert torch.equal(z0, z1)
+    assert ((s0 - s1).abs() <= 3 * 2.0 ** -24 * s0).all()
+    away = ((v.double() - z0) / s0 - (c0 + c1) / 2).abs()  # of the border between the two codes
+    assert ((c0 == c1) | (((c0 - c1).abs() == 1) & (away <= 2.0 ** -17))).all()
+    for c, s, z in got:
+        assert ((c * s + z - v.double()).abs() <= s * (0.5 + 2.0 ** -17)).all()
