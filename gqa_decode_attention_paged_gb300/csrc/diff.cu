@@ -29,6 +29,7 @@
 // one it ends inside of (2 * slice + 1), so the workspace grows with the
 // number of slices alone, not with batch * heads.
 #include <algorithm>
+#include <float.h>
 #include <math.h>
 #include <mutex>
 
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(DCfg<D, G, KV>::kThreads, 2)
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
             for (int t = 0; t < 2 * NT; ++t) o[nb][t][0] = o[nb][t][1] = o[nb][t][2] = o[nb][t][3] = 0.0f;
-            m0[nb] = m1[nb] = -INFINITY;
+            m0[nb] = m1[nb] = -FLT_MAX;  // (finite: a score of -inf is below it and weighs 0)
             l0[nb] = l1[nb] = 0.0f;
         }
 
