@@ -11,11 +11,15 @@
 // the two sums are), and adds w V; o = accumulator / (c1 l1).  The difference
 // is taken in fp32 before the rounding to the product's type, so what the two
 // maps share never enters it, and V is multiplied once instead of once per
-// map: with the second Q K^T the MMA work is that of separate products of both
-// maps (12 d per row and key), in half the accumulator -- two accumulators of
-// 2 d columns would take all of tensor memory at d_head 128 and leave none for
-// scores.  All statistics are final before the first weight is formed: no
-// accumulator is ever rescaled.
+// map.  That rounding is to bf16 (bf16 pools: V's range is not f16's), which
+// makes the result's 2-norm error 2.3e-3 where its own rounding alone is 1.7e-3
+// (a second bf16 for what is left, as in diff.cu, would be a third more MMA
+// work), or to f16 (FP8 pools: 1.7e-3).  With the second Q K^T the MMA work is
+// that of separate products of both maps (12 d per row and key), in half the
+// accumulator -- two accumulators of 2 d columns would take all of tensor memory
+// at d_head 128 and leave none for scores (at d_head 64 they would not; one
+// sweep there is not built).  All statistics are final before the first weight
+// is formed: no accumulator is ever rescaled.
 //
 // Design (persistent clusters of two CTAs, one per SM, warp-specialised; the
 // times are of 16 prompts of 700..1024 tokens on contexts of up to 2048, bf16,
@@ -25,7 +29,9 @@
 //     maps' queries.  A step is 128 keys.  The two CTAs of a cluster take
 //     neighbouring tiles of the same (sequence, pair) and walk the same keys at
 //     about the same time, each copying for itself (the second read of a unit
-//     comes from the L2).  A step moves 6 units of 32 KiB into each SM.
+//     comes from the L2).  A step moves 6 units of 32 KiB into each SM.  Both
+//     walk to the second tile's last key: where each stops at its own, they fall
+//     out of step and their reads no longer meet (478 us against 369).
 //   * warp 16 streams Q and, through one ring, what the MMAs take in the order
 //     they take it: K_m units (128 keys of one map) and, in the second sweep, V
 //     units (64 keys x 2 d channels).  One ring for both: in the first sweep
@@ -44,7 +50,7 @@
 //     are zeroed, and FP8 units are widened to f16 in place, by four warps (two
 //     bound the kernel: 596 us against 504 at d_head 128).  Widening writes and
 //     reads shared memory once more than the MMAs alone, which keep it busy as
-//     it is: FP8 prompts at d_head 128 take 452 us.
+//     it is: FP8 prompts at d_head 128 take 455 us.
 //   * sixteen warps work on scores, four threads a row (a step's exponentials
 //     are many, and short dependent chains need several warps per scheduler to
 //     fill it: with eight warps a step took twice as long).  First sweep: each
@@ -227,7 +233,7 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b)
 // ------------------------------------------------------------- tile walk
 
 struct Tile {
-    int b, p, rt0;  // sequence, pair, this CTA's first local row (past R: no rows, it helps to copy)
+    int b, p, rt0;  // sequence, pair, this CTA's first local row (past R: no rows, it walks along)
     int R;          // rows of (b, p): T * G
     int row0, T, C; // first query token row of b, chunk length, context length (clamped)
     int n_blocks, n_steps;  // blocks the tile sees; steps of this CTA's range
@@ -1129,7 +1135,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
             const float rn = a.w.out_scale * rsqrtf(ss * (1.0f / (2 * D)) + a.w.eps);
             // The row's pieces of 32 bytes change places among the lanes of NP rows, so that a store instruction
             // writes whole pieces of 32 / NP rows instead of 32: the load-store unit passes once for each row that
-            // an instruction touches (355 -> 346 us).
+            // an instruction touches (9 of 355 us).
             constexpr int NP = QD / 16;
             uint32_t w[NP][8];
             const float4 *nw = reinterpret_cast<const float4 *>(sm + L::kNorm) + grp * (QD / 4);

@@ -23,7 +23,7 @@
 // rotation needs no exchange between lanes; the 32 / (D / 16) lanes that hold
 // the same pairs of different heads compute 8 sines and cosines between them
 // and swap them by shuffles, once for all heads of the token.
-// 20322 image tokens (32 query, 8 KV heads of 128, E4M3): 82 us, 84 % of the
+// 20321 image tokens (32 query, 8 KV heads of 128, E4M3): 82 us, 84 % of the
 // copy rate; a decode step's 64 tokens: 6.2 us, the latency of a launch and of
 // two dependent loads.
 #include "pkv_internal.cuh"
@@ -45,8 +45,8 @@ namespace pkv {
 namespace {
 
 constexpr int kRopeWarps = 2;  // warps per CTA (2: 81 us, 4: 82, at the tokens below)
-// What was tried is quoted for 20322 image tokens to an E4M3 pool (459 MB: 69 us at the copy rate), and for 10350
-// tokens written to a 4-bit pool and read back (42 in all).
+// What was tried is quoted for 20321 image tokens to an E4M3 pool (459 MB: 69 us at the copy rate), and for 9625
+// tokens written to a 4-bit pool and read back (42 in all, 33 of them the write).
 // Head rows a lane has in flight: 1: 94 us, 2: 82, 3: 96; 4-bit pools 1: 43, 2: 45, 3: 45.
 constexpr int unroll_of(int kv) { return kv == PKV_INT4 ? 1 : 2; }
 // CTAs an SM has room for, which bounds the registers: 20 warps 82 us, 24: 88; 4-bit pools 47 and 45.
@@ -118,7 +118,7 @@ __device__ __forceinline__ uint4 pack_bf16(const float *x)
 // E4M3 codes of x / s, the quotient correctly rounded in fp32, from r = 1 / s to two units of its last place.  The
 // product with r is off by less than 8 units; in E4M3's normal range that leaves the code as it is unless the 20 bits
 // that the rounding drops are that close to a half.  Only there, and below that range or where r is not in fp32's, is
-// the quotient itself needed (dividing always took 90 us of 20322 image tokens, this 82).
+// the quotient itself needed (dividing always took 90 us of 20321 image tokens, this 82).
 __device__ __forceinline__ uint2 pack_e4m3(const float *x, float s, float r)
 {
     float y[8];

@@ -455,9 +455,14 @@ pkv_status paged_prefill_attention(pkv_pool *pool, const void *q, int64_t n_rows
  *           V = [V_2p | V_2p+1]
  *   out_h = (1 - lambda_init) * norm_weight * o_h / sqrt(mean(o_h^2) + eps)
  *   lambda = exp(lambdas[0] . lambdas[1]) - exp(lambdas[2] . lambdas[3]) + lambda_init
- * The softmax statistics, the sums, lambda and the norm are held in fp32;
- * the weights of a map enter the products with V as bf16 (bf16 pools) or f16
- * (FP8 pools), and out is rounded once, to bf16.
+ * The softmax statistics, the sums, lambda and the norm are held in fp32, and
+ * out is rounded once, to bf16.  The products with V take, for single tokens,
+ * each map's weights as the sum of two bf16 (bf16 pools) or as one f16 (FP8
+ * pools); for chunks, the difference of the two maps' weights, formed in fp32
+ * and rounded once, to bf16 or f16.  On FP8 pools queries and keys are
+ * multiplied as f16, so |q| must stay in f16's range (65504).
+ * A visible key whose score is -infinity weighs nothing.  A NaN reaches the
+ * rows that see it.
  * --------------------------------------------------------------------- */
 typedef struct {
     const float *lambdas;      /* device fp32 [4][d_head] */
@@ -472,8 +477,7 @@ typedef struct {
  *   out     device bf16 [batch][n_q / 2][2 d_head], 16-byte aligned.
  * block_tables, context_lens, scale, limits and range errors as
  * paged_decode_attention (a context of 0 gives a row of zeros, a block id
- * outside the pool counts as masked).  bf16 and FP8 pools; on FP8 pools the
- * products run in f16 (|q| must stay in f16's range).  Two launches, like
+ * outside the pool counts as masked).  bf16 and FP8 pools.  Two launches, like
  * paged_decode_attention; uses the same workspace (grown outside stream
  * captures: see paged_diff_reserve_workspace) and the pool's partition
  * setting.
@@ -501,7 +505,9 @@ pkv_status paged_diff_decode_attention(pkv_pool *pool, const void *q, int32_t n_
  *              of no sequence, or of one that is skipped, stay as they were.
  * A block id outside the pool counts as masked and sets
  * PKV_DEVERR_BLOCK_RANGE; a row that sees nothing is zero.  Cached rows
- * behind C_b are never used, whatever they hold.  bf16 and FP8 pools; one
+ * behind C_b are never used, whatever they hold; cached values that some of a
+ * chunk's rows do not see but later ones do have to be finite, as those rows
+ * multiply them by 0.  bf16 and FP8 pools; one
  * launch on the tcgen05 tensor cores, no workspace.  Where the call's rows
  * fill few tiles of 128 (short chunks, few sequences), several thread blocks
  * share a tile's keys; results of a call do not depend on timing, but may
@@ -516,9 +522,11 @@ pkv_status paged_diff_prefill_attention(pkv_pool *pool, const void *q, int64_t n
 /* Grow the pool's workspace now, so that later paged_diff_decode_attention
  * calls with at most `batch` sequences, `n_q` query heads and
  * `max_blocks_per_seq` table entries allocate nothing and may be captured.
- * Memory that captured graphs may use stays valid: a workspace that is
- * replaced by a larger one is kept until the pool is destroyed.  Graphs of
- * one pool share its workspace: replay them one after the other.
+ * (With the pool's partition setting of now: reserve again after changing it.)
+ * Memory that captured graphs may use stays valid: a workspace that a capture
+ * has seen is kept until the pool is destroyed, any other is freed when a
+ * larger one replaces it.  Graphs of one pool share its workspace: replay
+ * them one after the other.
  * Errors: EINVAL, EUNSUPPORTED, ENOMEM. */
 pkv_status paged_diff_reserve_workspace(pkv_pool *pool, int32_t batch, int32_t n_q, int32_t max_blocks_per_seq);
 
