@@ -218,8 +218,8 @@ def _output(shape, device, stream):
     if stream is not None:
         handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
         if handle != torch._C._cuda_getCurrentRawStream(device.index):
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(handle, device=device)
+            if not isinstance(stream, torch.cuda.Stream):  # (0 is the default stream, and no external one)
+                stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
             with torch.cuda.stream(stream):
                 return torch.empty(shape, dtype=torch.bfloat16, device=device)
     return torch.empty(shape, dtype=torch.bfloat16, device=device)

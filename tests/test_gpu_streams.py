@@ -60,5 +60,10 @@ def test_outputs_are_memory_of_the_given_stream(handle):
                 assert owner(y) == side.cuda_stream, name
             with torch.cuda.stream(side):  # the same stream by another name
                 assert all(owner(y) == side.cuda_stream for y in outs(call(stream=side.cuda_stream)))
+                here = torch.cuda.default_stream()
+                got = outs(call(stream=here.cuda_stream if handle else here))  # back on the default stream
+                assert all(owner(y) == here.cuda_stream for y in got)
             torch.cuda.synchronize()
+            for x, y in zip(want, got):
+                assert torch.equal(x, y), name
         assert pool.get_error() == 0
