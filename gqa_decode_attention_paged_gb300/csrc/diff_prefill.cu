@@ -620,6 +620,9 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
             // copies still in flight (after an abort) land before the CTA exits
             for (int i = max(0, u - NS); i < u; ++i)
                 mbar_wait_bounded(&bar[(F8 ? L::RAW : L::FULL) + i % NS], (i / NS) & 1);
+            // and so do the MMAs' arrivals for the last units
+            for (int i = max(0, u - NS); i < u && ok && !*abort_flag; ++i)
+                ok = wait_all(&bar[L::EMPTY + i % NS], (i / NS) & 1);
             if (n > 0) mbar_wait_bounded(&bar[F8 ? L::Q_RAW : L::Q_FULL], (n - 1) & 1);
             if (!ok) set_abort();
         } else if (warp >= kPrepWarp && warp < Wp::kProduct) {
