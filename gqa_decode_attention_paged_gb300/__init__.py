@@ -31,6 +31,7 @@ DEVERR_SLOT_RANGE = 0x1
 DEVERR_BLOCK_RANGE = 0x2
 DEVERR_CTX_RANGE = 0x4
 DEVERR_TIMEOUT = 0x8
+DEVERR_NAN = 0x10
 
 _lib = None
 _lock = threading.Lock()
@@ -117,6 +118,13 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.paged_diff_prefill_attention.argtypes = [P, P, c.c_int64, c.c_int32, P, P, c.c_int32, P, c.c_int32,
                                                      c.c_float, c.POINTER(_DiffParams), P, P]
         lib.paged_diff_reserve_workspace.argtypes = [P, c.c_int32, c.c_int32, c.c_int32]
+        lib.paged_tree_attention.argtypes = [P, P, c.c_int64, c.c_int32, P, P, c.c_int32, P, c.c_int32, P, c.c_int32,
+                                             c.c_float, P, P]
+        lib.paged_tree_commit.argtypes = [P, P, P, c.c_int32, P, P, c.c_int32, P, c.c_int32, P, P]
+        lib.paged_beam_select.argtypes = [P, P, c.c_int32, c.c_int64, P, c.c_int32, c.c_int32, c.c_int32, c.c_int32, P,
+                                          P, P, P]
+        lib.paged_beam_reserve_workspace.argtypes = [P, c.c_int32, c.c_int32, c.c_int32, c.c_int32]
+        lib.paged_beam_reorder.argtypes = [P, P, c.c_int32, c.c_int32, c.c_int32, P, c.c_int32, P, P, P, P, P]
         lib.paged_decode_step.argtypes = [P, P, P, P, c.c_int32, P, c.c_int32, P, c.c_int32, c.c_float, P, P]
         lib.paged_decode_step_host.argtypes = [P, P, P, P, c.c_int32, P, c.c_int32, P, c.c_int32, c.c_float,
                                                P, P]
@@ -152,7 +160,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                      "kv_pool_set_partition_tokens", "kv_pool_set_cascade_mode", "kv_pool_reserve_workspace",
                      "paged_kv_append", "pkv_rope_create", "pkv_rope_destroy", "paged_rope_append",
                      "paged_kv_gather", "paged_diff_decode_attention", "paged_diff_prefill_attention",
-                     "paged_diff_reserve_workspace",
+                     "paged_diff_reserve_workspace", "paged_tree_attention", "paged_tree_commit",
+                     "paged_beam_select", "paged_beam_reserve_workspace", "paged_beam_reorder",
                      "paged_decode_attention", "paged_decode_attention_noalloc", "paged_decode_step",
                      "paged_decode_attention_csr", "paged_prefill_attention",
                      "paged_decode_step_host", "paged_decode_attention_prefix", "pkv_get_error", "pkv_timing_enable", "pkv_timing_read",
@@ -210,19 +219,22 @@ def _raw_stream(pool, stream):
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _output(shape, device, stream):
-    """A bf16 output, from the memory of the stream that the call goes to: memory of another stream may still
-    be in use by what that one has to do, and would be used again by it as soon as the output is dropped."""
+def _output(shape, device, stream, dtype=None):
+    """An output (bf16 unless said otherwise), from the memory of the stream that the call goes to: memory of another
+    stream may still be in use by what that one has to do, and would be used again by it as soon as the output is
+    dropped."""
     import torch
 
+    if dtype is None:
+        dtype = torch.bfloat16
     if stream is not None:
         handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
         if handle != torch._C._cuda_getCurrentRawStream(device.index):
             if not isinstance(stream, torch.cuda.Stream):  # (0 is the default stream, and no external one)
                 stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
             with torch.cuda.stream(stream):
-                return torch.empty(shape, dtype=torch.bfloat16, device=device)
-    return torch.empty(shape, dtype=torch.bfloat16, device=device)
+                return torch.empty(shape, dtype=dtype, device=device)
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _fast_ptr(pool, t, name, dtype, shape):
@@ -371,6 +383,10 @@ class Pool:
     def reserve_diff_workspace(self, batch: int, n_q: int, max_blocks_per_seq: int):
         """Grow the workspace for paged_diff_decode_attention calls up to these sizes (before capturing one)."""
         _check(load().paged_diff_reserve_workspace(self.handle, batch, n_q, max_blocks_per_seq))
+
+    def reserve_beam_workspace(self, batch: int, beams: int, vocab: int, k: int):
+        """Grow the workspace for paged_beam_select calls up to these sizes (before capturing one)."""
+        _check(load().paged_beam_reserve_workspace(self.handle, batch, beams, vocab, k))
 
     def get_error(self, clear: bool = False) -> int:
         bits = ctypes.c_uint32(0)
@@ -677,6 +693,127 @@ def paged_diff_prefill_attention(pool: Pool, q, qo_indptr, block_tables, context
     return out
 
 
+def paged_tree_attention(pool: Pool, q, qo_indptr, tree_mask, block_tables, context_lens, scale: float, out=None,
+                         stream=None):
+    """Attention of each sequence's tree of drafted tokens over its cache.
+    q: bf16 [rows, n_q, d_head], the nodes sequence by sequence; qo_indptr:
+    int32 [B + 1]; tree_mask: int64 [rows, words], bit j % 64 of word j / 64 set
+    where the row sees its sequence's node j (all see the context before the
+    nodes); block_tables: int32 [B, W]; context_lens: int32 [B] (including the
+    nodes, which are the last entries of the cache).  Returns ``out`` (bf16
+    [rows, n_q, d_head], allocated if not given)."""
+    import torch
+
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise TypeError("q must be a torch tensor [rows, n_q, d_head]")
+    B, W = int(context_lens.shape[0]), int(block_tables.shape[-1])
+    rows, n_q, words = int(q.shape[0]), int(q.shape[1]), int(tree_mask.shape[-1])
+    shape = (rows, n_q, pool.d_head)
+    qp = _fast_ptr(pool, q, "q", torch.bfloat16, shape)
+    ip = _fast_ptr(pool, qo_indptr, "qo_indptr", torch.int32, (B + 1,))
+    mp = _fast_ptr(pool, tree_mask, "tree_mask", torch.int64, (rows, words))
+    tp = _fast_ptr(pool, block_tables, "block_tables", torch.int32, (B, W))
+    cp = _fast_ptr(pool, context_lens, "context_lens", torch.int32, (B,))
+    if out is None:
+        out = _output(shape, q.device, stream)
+        op = out.data_ptr()
+    else:
+        op = _fast_ptr(pool, out, "out", torch.bfloat16, shape)
+    _check(load().paged_tree_attention(pool.handle, qp, rows, n_q, ip, mp, words, tp, W, cp, B, float(scale), op,
+                                       _raw_stream(pool, stream)))
+    return out
+
+
+def paged_tree_commit(pool: Pool, qo_indptr, accepted, n_accepted, block_tables, context_lens, new_lens=None,
+                      stream=None):
+    """Move the cached rows of each tree's accepted path to the front of its
+    nodes.  qo_indptr: int32 [B + 1] (the nodes, as in paged_tree_attention);
+    accepted: int32 [B, most], ascending node numbers, of which n_accepted[b]
+    (int32 [B]) count; context_lens: int32 [B] (including the nodes).  Returns
+    ``new_lens`` (int32 [B], allocated if not given): the lengths after it."""
+    import torch
+
+    B, most, W = int(n_accepted.shape[0]), int(accepted.shape[-1]), int(block_tables.shape[-1])
+    ip = _fast_ptr(pool, qo_indptr, "qo_indptr", torch.int32, (B + 1,))
+    ap = _fast_ptr(pool, accepted, "accepted", torch.int32, (B, most))
+    np_ = _fast_ptr(pool, n_accepted, "n_accepted", torch.int32, (B,))
+    tp = _fast_ptr(pool, block_tables, "block_tables", torch.int32, (B, W))
+    cp = _fast_ptr(pool, context_lens, "context_lens", torch.int32, (B,))
+    if new_lens is None:
+        new_lens = _output((B,), n_accepted.device, stream, torch.int32)
+        lp = new_lens.data_ptr()
+    else:
+        lp = _fast_ptr(pool, new_lens, "new_lens", torch.int32, (B,))
+    _check(load().paged_tree_commit(pool.handle, ip, ap, most, np_, tp, W, cp, B, lp, _raw_stream(pool, stream)))
+    return new_lens
+
+
+def paged_beam_select(pool: Pool, logits, scores, k: int, stream=None):
+    """Beam search's selection: the k best of each search's beams x vocab
+    continuations by scores + log_softmax(logits), equal ones by the lower beam,
+    then token.  logits: bf16 or fp32 [B, beams, vocab] (rows may be slices of
+    wider ones); scores: fp32 [B, beams].  Returns (tokens int32, parents int32,
+    scores fp32), each [B, k]; -1, -1 and -inf where nothing is left."""
+    import torch
+
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 3:
+        raise TypeError("logits must be a torch tensor [searches, beams, vocab]")
+    if logits.dtype is torch.bfloat16:
+        kind = 0
+    elif logits.dtype is torch.float32:
+        kind = 1
+    else:
+        raise ValueError(f"logits must be torch.bfloat16 or torch.float32, got {logits.dtype}")
+    if logits.get_device() != pool.device:
+        raise ValueError(f"logits must be on the pool's device cuda:{pool.device}")
+    B, beams, vocab = logits.shape
+    sb, sj, st = logits.stride()
+    if beams == 1:  # (a stride of a dimension of one says nothing)
+        sj = sb if B > 1 else vocab
+    if vocab > 1 and st != 1 or B > 1 and sb != beams * sj:
+        raise ValueError(f"logits must hold rows of adjacent values at equal distances (strides {logits.stride()})")
+    k = int(k)
+    sp = _fast_ptr(pool, scores, "scores", torch.float32, (B, beams))
+    shape = (B, max(k, 0))
+    tokens, parents = (_output(shape, logits.device, stream, torch.int32) for _ in range(2))
+    best = _output(shape, logits.device, stream, torch.float32)
+    _check(load().paged_beam_select(pool.handle, logits.data_ptr(), kind, sj, sp, B, beams, vocab, k, tokens.data_ptr(),
+                                    parents.data_ptr(), best.data_ptr(), _raw_stream(pool, stream)))
+    return tokens, parents, best
+
+
+def paged_beam_reorder(pool: Pool, parents, block_tables, context_lens, spare_blocks, tables_out=None, lens_out=None,
+                       stream=None):
+    """Tables and lengths of the selected beams.  parents: int32 [B, k], the
+    beam that each new one goes on from (-1: none); block_tables: int32
+    [B * beams, W]; context_lens: int32 [B * beams]; spare_blocks: int32
+    [B * k].  A parent's first new beam keeps its unfilled block, the others get
+    their spare block, into which the filled rows are copied.  Returns
+    (tables_out int32 [B * k, W], lens_out int32 [B * k]), allocated if not
+    given."""
+    import torch
+
+    if not isinstance(parents, torch.Tensor) or parents.dim() != 2:
+        raise TypeError("parents must be a torch tensor [searches, beams]")
+    B, k = parents.shape
+    n, W = int(context_lens.shape[0]), int(block_tables.shape[-1])
+    if B and n % B:
+        raise ValueError(f"{n} tables for {B} searches")
+    pp = _fast_ptr(pool, parents, "parents", torch.int32, (B, k))
+    tp = _fast_ptr(pool, block_tables, "block_tables", torch.int32, (n, W))
+    cp = _fast_ptr(pool, context_lens, "context_lens", torch.int32, (n,))
+    sp = _fast_ptr(pool, spare_blocks, "spare_blocks", torch.int32, (B * k,))
+    if tables_out is None:
+        tables_out = _output((B * k, W), parents.device, stream, torch.int32)
+    if lens_out is None:
+        lens_out = _output((B * k,), parents.device, stream, torch.int32)
+    to = _fast_ptr(pool, tables_out, "tables_out", torch.int32, (B * k, W))
+    lo = _fast_ptr(pool, lens_out, "lens_out", torch.int32, (B * k,))
+    _check(load().paged_beam_reorder(pool.handle, pp, B, n // B if B else 1, k, tp, W, cp, sp, to, lo,
+                                     _raw_stream(pool, stream)))
+    return tables_out, lens_out
+
+
 def paged_decode_attention_prefix(pool: Pool, q, prefix_blocks, block_tables, context_lens, scale: float,
                                   out=None, stream=None):
     """Cascade decode: every sequence starts with the shared prefix whose
@@ -937,5 +1074,6 @@ __all__ = ["BF16", "FP8_E4M3", "INT4", "Pool", "PagedKVError", "kv_pool_create",
            "paged_decode_step_host", "paged_decode_attention_prefix", "paged_decode_attention_csr",
            "paged_prefill_attention", "Rope", "paged_rope_append", "paged_kv_gather",
            "DiffParams", "paged_diff_decode_attention", "paged_diff_prefill_attention",
+           "paged_tree_attention", "paged_tree_commit", "paged_beam_select", "paged_beam_reorder",
            "kv_bytes_per_token", "kv_block_bytes", "kv_swap_entry_bytes",
            "kv_block_copy", "kv_swap_out", "kv_swap_in", "BlockAllocator", "load", "library_path"]

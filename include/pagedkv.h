@@ -57,6 +57,7 @@ typedef enum {
 #define PKV_DEVERR_BLOCK_RANGE 0x2u  /* decode: block id outside [0, num_blocks) */
 #define PKV_DEVERR_CTX_RANGE   0x4u  /* decode: context_len < 0 or > W * block_size */
 #define PKV_DEVERR_TIMEOUT     0x8u  /* a bounded wait on the kernel's own copies ran out */
+#define PKV_DEVERR_NAN         0x10u /* beam selection: a beam whose logits have no log-softmax */
 
 typedef struct pkv_pool pkv_pool; /* opaque; owns its device memory */
 
@@ -529,6 +530,138 @@ pkv_status paged_diff_prefill_attention(pkv_pool *pool, const void *q, int64_t n
  * them one after the other.
  * Errors: EINVAL, EUNSUPPORTED, ENOMEM. */
 pkv_status paged_diff_reserve_workspace(pkv_pool *pool, int32_t batch, int32_t n_q, int32_t max_blocks_per_seq);
+
+/* ---------------------------------------------------------------------
+ * Several candidates per sequence: trees of drafted tokens, and beam search
+ * ("KV cache, PagedAttention and FlashAttention", Problem 4: beam branches
+ * share blocks, and a shared block is copied before it is written).
+ *
+ * A step with drafted tokens: append the tree's nodes behind the accepted
+ * context (paged_kv_append or paged_rope_append, positions by depth),
+ * paged_tree_attention in every layer, choose the accepted path, and
+ * paged_tree_commit in every layer.  A step of a beam search: decode, logits,
+ * paged_beam_select, and paged_beam_reorder in every layer.
+ * --------------------------------------------------------------------- */
+
+/* Attention of a tree of drafted tokens over the cache.  Sequence b's T_b =
+ * qo_indptr[b+1] - qo_indptr[b] nodes are the last entries of its cache
+ * (position C_b - T_b + i for node i, C_b = context_lens[b]).  Each node sees
+ * the whole context before them, positions 0 .. C_b - T_b - 1, and those of
+ * the T_b nodes whose bits are set in its mask: its ancestors and itself for a
+ * tree, but any mask is taken.
+ *   q          device bf16 [n_rows][n_q][d_head], 16-byte aligned.
+ *   qo_indptr  device int32 [batch + 1]: sequence b's nodes are rows
+ *              qo_indptr[b] .. qo_indptr[b+1].
+ *   tree_mask  device uint64 [n_rows][mask_words], 8-byte aligned: bit j % 64
+ *              of word j / 64 of a node's row is set where it sees node j.
+ *   mask_words 1 .. 16 (up to 1024 nodes).
+ *   out        device bf16 [n_rows][n_q][d_head], 32-byte aligned; rows of no
+ *              sequence, or of one that is skipped, stay as they were.
+ * A sequence whose rows run backwards or leave [0, n_rows), with more nodes
+ * than the masks have bits, more nodes than cached tokens, or a length past
+ * its table is skipped and sets PKV_DEVERR_CTX_RANGE.  A block id outside the
+ * pool counts as masked and sets PKV_DEVERR_BLOCK_RANGE.  A row that sees
+ * nothing is zero, and a visible key whose score is -infinity weighs nothing.
+ * Cached rows behind C_b are never used, whatever they hold; a node that some
+ * of the sequence's nodes see and others do not has to have finite values, as
+ * the others multiply them by 0.
+ * The softmax statistics and the sums are held in fp32; weights are rounded
+ * once, to bf16 (bf16 pools) or f16 (FP8 pools, whose queries are multiplied
+ * as f16: |q| must stay in f16's range), and out once, to bf16.
+ * bf16 and FP8 pools.  Other arguments, group sizes and limits as
+ * paged_prefill_attention.
+ * Errors: EINVAL, EUNSUPPORTED (4-bit pools, group size, mask_words, too many
+ * query rows), ENOMEM, ECUDA. */
+pkv_status paged_tree_attention(pkv_pool *pool, const void *q, int64_t n_rows, int32_t n_q, const int32_t *qo_indptr,
+                                const uint64_t *tree_mask, int32_t mask_words, const int32_t *block_tables,
+                                int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t batch, float scale,
+                                void *out, void *stream);
+
+/* Keep an accepted path of each tree: the cached row of node accepted[b][i]
+ * moves to position C_b - T_b + i, for i < n_accepted[b], every KV head, keys
+ * and values (and a 4-bit pool's value parameters), as they are stored.  The
+ * rows behind the path are left as they are.
+ *   qo_indptr     device int32 [batch + 1]: T_b as in paged_tree_attention.
+ *   accepted      device int32 [batch][max_accepted]: node numbers, ascending
+ *                 (a path from the root in a tree whose nodes follow their
+ *                 parents); those behind n_accepted[b] are not looked at.
+ *   n_accepted    device int32 [batch], 0 .. T_b.
+ *   context_lens  device int32 [batch]: C_b, the nodes included.
+ *   new_lens      device int32 [batch]: receives C_b - T_b + n_accepted[b].
+ *                 Must not overlap an input.
+ * Call it once for every layer's pool.  A sequence whose path is not
+ * ascending or leaves the tree, or whose lengths do not fit (more nodes than
+ * cached tokens, a length past the table, n_accepted beyond T_b or
+ * max_accepted) moves nothing, gets max(0, C_b - T_b) as its new length (C_b
+ * clamped to the table) and sets PKV_DEVERR_CTX_RANGE; a row from or to a block
+ * outside the pool is not moved and sets PKV_DEVERR_BLOCK_RANGE.  The blocks of
+ * a sequence's nodes must not be shared with another sequence (as for any
+ * append).  All pool types.  One launch, counted with the block launches.
+ * Errors: EINVAL, ECUDA. */
+pkv_status paged_tree_commit(pkv_pool *pool, const int32_t *qo_indptr, const int32_t *accepted, int32_t max_accepted,
+                             const int32_t *n_accepted, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                             const int32_t *context_lens, int32_t batch, int32_t *new_lens, void *stream);
+
+/* Types of paged_beam_select's logits. */
+#define PKV_LOGITS_BF16 0
+#define PKV_LOGITS_F32 1
+
+/* Beam search's selection: of every search's beams x vocab continuations,
+ * worth scores[b][j] + log_softmax(logits[b][j])[t], the k greatest in
+ * descending order; equal ones by the lower j * vocab + t.
+ *   logits      device, PKV_LOGITS_BF16 or PKV_LOGITS_F32, aligned to its
+ *               elements: row (b, j) at (b * beams + j) * row_stride elements,
+ *               row_stride >= vocab.  -infinity forbids a token.
+ *   scores      device fp32 [batch][beams]; -infinity: a beam that has ended
+ *               or not begun (its logits may be anything).
+ *   tokens, parents, out_scores  device int32, int32 and fp32 [batch][k]: the
+ *               token, the beam j it goes on from, and its worth.  Places for
+ *               which nothing above -infinity is left hold -1, -1 and
+ *               -infinity.  Must overlap neither each other nor an input.
+ * What decides between continuations is held in 64 bits, except for the
+ * exponentials themselves and the sums of a few hundred of them (32 bits);
+ * out_scores are rounded once.  A beam whose logits hold a NaN or +infinity,
+ * or whose score is one, has no continuations and sets PKV_DEVERR_NAN.
+ * batch <= 8192, beams and k in 1 .. 64, vocab <= 2^22.  Two launches, no
+ * cache is read: the pool gives its device, its workspace (grown outside
+ * stream captures: see paged_beam_reserve_workspace) and its error word.
+ * Errors: EINVAL, EUNSUPPORTED, ENOMEM, ECUDA. */
+pkv_status paged_beam_select(pkv_pool *pool, const void *logits, int32_t type, int64_t row_stride, const float *scores,
+                             int32_t batch, int32_t beams, int32_t vocab, int32_t k, int32_t *tokens, int32_t *parents,
+                             float *out_scores, void *stream);
+
+/* Grow the pool's workspace now, so that later paged_beam_select calls with at
+ * most `batch` searches and these beams, vocab and k allocate nothing and may be
+ * captured (see paged_diff_reserve_workspace for what a captured workspace
+ * means).  Errors: EINVAL, EUNSUPPORTED, ENOMEM. */
+pkv_status paged_beam_reserve_workspace(pkv_pool *pool, int32_t batch, int32_t beams, int32_t vocab, int32_t k);
+
+/* Go on from the selected beams: new beam i of search b takes the cache of
+ * beam parents[b][i].  With L that beam's length, entries 0 .. L / 16 - 1 of its
+ * table (full blocks) are shared.  Entry L / 16, the block that is written
+ * next, must be its own: the parent's first new beam keeps the parent's entry
+ * (filled or not yet given); every other one gets spare_blocks[b][i], into
+ * which the L % 16 filled rows are copied.  Entries behind it become -1.
+ *   parents       device int32 [batch][k]; -1: no beam (its table becomes -1,
+ *                 its length 0).
+ *   block_tables  device int32 [batch * beams][max_blocks_per_seq].
+ *   context_lens  device int32 [batch * beams].
+ *   spare_blocks  device int32 [batch * k]: free blocks, no id twice, none in a
+ *                 table (unchecked).  Which were taken follows from parents: a
+ *                 first new beam's, and a full table's (L / 16 =
+ *                 max_blocks_per_seq), stays free.
+ *   tables_out    device int32 [batch * k][max_blocks_per_seq], lens_out device
+ *                 int32 [batch * k]; must overlap neither each other nor an
+ *                 input.
+ * Call it once for every layer's pool, with the same arguments; the tables
+ * come out the same each time.  A parent outside -1 .. beams - 1 counts as -1
+ * and sets PKV_DEVERR_BLOCK_RANGE; a length outside the table is clamped and
+ * sets PKV_DEVERR_CTX_RANGE; a copy from or to a block outside the pool is left
+ * out and sets PKV_DEVERR_BLOCK_RANGE.  All pool types.  One launch, counted
+ * with the block launches.  Errors: EINVAL, EUNSUPPORTED, ECUDA. */
+pkv_status paged_beam_reorder(pkv_pool *pool, const int32_t *parents, int32_t batch, int32_t beams, int32_t k,
+                              const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
+                              const int32_t *spare_blocks, int32_t *tables_out, int32_t *lens_out, void *stream);
 
 /* paged_decode_attention without any allocation.  The pages have no
  * counterpart to this call; it exists for callers that cannot allocate
