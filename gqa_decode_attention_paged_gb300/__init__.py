@@ -120,6 +120,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.paged_diff_reserve_workspace.argtypes = [P, c.c_int32, c.c_int32, c.c_int32]
         lib.paged_tree_attention.argtypes = [P, P, c.c_int64, c.c_int32, P, P, c.c_int32, P, c.c_int32, P, c.c_int32,
                                              c.c_float, P, P]
+        lib.paged_tree_reserve_workspace.argtypes = [P, c.c_int64, c.c_int32]
         lib.paged_tree_commit.argtypes = [P, P, P, c.c_int32, P, P, c.c_int32, P, c.c_int32, P, P]
         lib.paged_beam_select.argtypes = [P, P, c.c_int32, c.c_int64, P, c.c_int32, c.c_int32, c.c_int32, c.c_int32, P,
                                           P, P, P]
@@ -160,8 +161,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                      "kv_pool_set_partition_tokens", "kv_pool_set_cascade_mode", "kv_pool_reserve_workspace",
                      "paged_kv_append", "pkv_rope_create", "pkv_rope_destroy", "paged_rope_append",
                      "paged_kv_gather", "paged_diff_decode_attention", "paged_diff_prefill_attention",
-                     "paged_diff_reserve_workspace", "paged_tree_attention", "paged_tree_commit",
-                     "paged_beam_select", "paged_beam_reserve_workspace", "paged_beam_reorder",
+                     "paged_diff_reserve_workspace", "paged_tree_attention", "paged_tree_reserve_workspace",
+                     "paged_tree_commit", "paged_beam_select", "paged_beam_reserve_workspace", "paged_beam_reorder",
                      "paged_decode_attention", "paged_decode_attention_noalloc", "paged_decode_step",
                      "paged_decode_attention_csr", "paged_prefill_attention",
                      "paged_decode_step_host", "paged_decode_attention_prefix", "pkv_get_error", "pkv_timing_enable", "pkv_timing_read",
@@ -383,6 +384,10 @@ class Pool:
     def reserve_diff_workspace(self, batch: int, n_q: int, max_blocks_per_seq: int):
         """Grow the workspace for paged_diff_decode_attention calls up to these sizes (before capturing one)."""
         _check(load().paged_diff_reserve_workspace(self.handle, batch, n_q, max_blocks_per_seq))
+
+    def reserve_tree_workspace(self, n_rows: int, n_q: int):
+        """Grow the workspace for paged_tree_attention calls up to these sizes (before capturing one)."""
+        _check(load().paged_tree_reserve_workspace(self.handle, n_rows, n_q))
 
     def reserve_beam_workspace(self, batch: int, beams: int, vocab: int, k: int):
         """Grow the workspace for paged_beam_select calls up to these sizes (before capturing one)."""

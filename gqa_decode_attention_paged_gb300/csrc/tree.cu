@@ -1,158 +1,917 @@
-// Attention of a tree of drafted tokens over the paged cache.
+// Attention of a tree of drafted tokens over the paged cache, on the tcgen05
+// tensor cores.
 //
-// Mathematics.  Node i of sequence b (row r = qo_indptr[b] + i) sits at cached
+// Mathematics.  Node i of sequence b (row qo_indptr[b] + i) sits at cached
 // position C - T + i; for query head h of KV head g
-//   out = sum_p softmax_p(s q_rh . K_pg) V_pg
+//   out = sum_p softmax_p(s q_ih . K_pg) V_pg
 // over the positions before the nodes and the nodes j whose bit is set in row
-// r's mask.  One pass over the keys with a running maximum and sum.
+// i's mask.  The rows of one KV head are (node i, head h of its group), row
+// i * G + h.  One pass over the keys with a running maximum and sum; a key
+// that a row does not see has score -infinity.
 //
-// A first form: one thread block per (row, KV head), its warps on every fourth
-// key, a lane on D / 32 channels.
-#include <float.h>
+// What bounds it: HBM, while a KV head's rows are few (the cache is read once,
+// 4 d rows operations for every 4 d bytes of a bf16 key and value), the tensor
+// cores and the exponentials from about 256 rows on.
+//
+// Design (one persistent CTA per SM, warp-specialised):
+//   * a unit is up to 256 rows (two tiles of 128) of one (sequence, KV head).
+//     The stream of all units' steps of 128 keys is cut into one equal slice
+//     per CTA, so that every SM has the same number of steps whatever the
+//     lengths are, and one long sequence keeps all of them busy.  A unit that a
+//     slice holds whole is finished by its CTA; of one that is cut each CTA
+//     leaves its part (reference maximum, sum, unnormalised O), which
+//     tree_merge_kernel joins.  A slice cuts at most two units, the one it
+//     starts inside of (partial slot 2 cta) and the one it ends inside of
+//     (2 cta + 1).
+//   * two streams of softmax, each with its own scores and accumulator in
+//     tensor memory and its own four warps (a thread per row, all 128 keys of a
+//     step): while one forms weights, the tensor cores work for the other.  A
+//     unit of two tiles gives each stream a tile, and both use every key and
+//     value tile; in a unit of one tile the streams take alternate steps, and
+//     join by log-sum-exp at its end.
+//   * warp 8 streams what the MMAs take through one ring of 32 KiB (d 128)
+//     tiles: keys of a step, its values, keys of the next.  Warps 9 and 10 issue
+//     one stream's MMAs each: S = Q K^T, and when the weights are written over
+//     S, O += P V.
+//   * the reference maximum is raised lazily (O is rescaled only when a row's
+//     maximum grows by more than 2^8).  Weights are rounded to bf16 (FP8 pools:
+//     f16) for the MMA, and the sum adds the rounded ones, so that the result is
+//     a convex combination of value rows.
+//   * FP8 pools: the E4M3 tiles are widened to f16 in place by four warps.
+//   * value rows behind the sequence's end are zeroed in shared memory before
+//     their product: a weight of 0 does not cancel what is not finite.
+// Every mbarrier wait is bounded; on a timeout the CTA records
+// PKV_DEVERR_TIMEOUT, every role stops, the MMA and copy pipes are drained
+// (bounded) and the tensor memory is released before the CTA exits.
+#include <algorithm>
+#include <climits>
+#include <mutex>
 
-#include "pkv_internal.cuh"
+#include "tcgen05.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kRows = 128;                 // query rows per tile (= TMEM lanes)
+constexpr int kUnitRows = 2 * kRows;
+constexpr int kKeys = 128;                 // keys per step
+constexpr int kStepBlocks = kKeys / kBlockSize;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kPrepWarp = 11;
+constexpr int kMaxWords = 16;
+constexpr int kMinShare = 2;               // steps of a slice at least
+template <bool F8>
+struct Warps {
+    static constexpr int kThreads = (F8 ? 16 : 12) * 32;
+    // FP8 pools: registers a thread at the launch, then of the softmax warps and of the others
+    static constexpr int kLaunchRegs = 128, kScoreRegs = 176, kWorkRegs = 80;
+    static_assert(8 * kScoreRegs + 8 * kWorkRegs <= 16 * kLaunchRegs, "more registers than the launch has");
+};
+// Tensor memory: S_x at 128 x (fp32 scores; the weights, packed in pairs, over its first 64 columns), O_x at 256 + D x.
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 256;
+constexpr uint32_t kHalf = 128 * 128;      // bytes of a 64-column range of a 128-row tile
+constexpr float kSlack = 8.0f;             // log2 of the largest weight before the reference maximum is raised
+
+// The unit that begins in a CTA's slice and goes on in the next ones, for the merge.  more < 0: none.
+struct Part {
+    int row0, r0, R, g, more;  // first token row, first local row, local rows, KV head, parts that follow
+};
 
 struct Args {
-    const uint8_t *pool;
-    int64_t num_blocks, n_rows;
-    int n_q, n_kv;
-    const __nv_bfloat16 *q;
-    const int32_t *qo_indptr;
-    const uint64_t *mask;
+    const int32_t *qo_indptr;  // [batch + 1]
+    const uint32_t *mask;      // [n_rows][2 words]
     int words;
     const int32_t *block_tables;
     int W;
     const int32_t *context_lens;
-    int batch;
+    int batch, n_q, n_kv;
+    int64_t num_blocks, n_rows;
+    int oob_row;          // a row index past the end of the pool's entry rows (zero-filled box)
     float qscale;         // scale * log2(e)
-    const float *scales;  // FP8 pools: [2 * n_kv]
-    __nv_bfloat16 *out;
+    const float *scales;  // FP8 pools: [2 * n_kv] fp32, K scales then V scales
+    int slot_rows;        // rows of a partial slot
+    Part *parts;          // [CTAs]
+    float2 *ws_ml;        // [2 CTAs][slot_rows] (reference maximum in log2 units, sum)
+    float *ws_o;          // [2 CTAs][slot_rows][D] unnormalised
+    __nv_bfloat16 *out;   // [n_rows][n_q][D]
     unsigned *err;
 };
 
-template <int D, int G, bool F8>
-__global__ void __launch_bounds__(kWarps * 32) tree_kernel(const __grid_constant__ Args a)
+template <int D>
+struct Layout {
+    static constexpr uint32_t QT = kRows * D * 2;  // a tile of queries
+    static constexpr uint32_t UT = kKeys * D * 2;  // a step's keys, or its values
+    static constexpr int kStages = D == 128 ? 5 : 10;
+    static constexpr uint32_t kQ = 0;
+    static constexpr uint32_t kRing = kQ + 2 * QT;
+    static constexpr uint32_t kStat = kRing + kStages * UT;  // a unit of one tile: stream 1's (m, l) per row
+    static constexpr uint32_t kBar = kStat + kRows * 8;
+    // RAW, Q_RAW: FP8 pools' copies complete there; FULL and Q_FULL follow when the rows are f16
+    enum { Q_RAW = 0, Q_FULL, Q_FREE, RAW, FULL = RAW + kStages, EMPTY = FULL + kStages,
+           S_FULL = EMPTY + kStages,  // per stream: scores of a step
+           P_FULL = S_FULL + 2,       // its weights are in tensor memory
+           PV_DONE = P_FULL + 2,      // their product has run
+           STAT = PV_DONE + 2,        // per lane quarter: stream 1's statistics and O are final
+           TAKEN = STAT + 4,          // they are read
+           DRAIN = TAKEN + 4, NBARS };
+    static constexpr uint32_t kTmemSlot = kBar + NBARS * 8;
+    static constexpr uint32_t kAbort = kTmemSlot + 4;
+    static constexpr uint32_t kEnd = kAbort + 4;
+    static constexpr size_t bytes = 1024 + kEnd;
+    static_assert(bytes <= 232448, "shared memory beyond the 227 KiB a CTA may use");
+};
+
+// A tile of R rows x D E4M3 -> f16, in place, by one warp: rows [row0, row0 + rows).
+// Before: rows of D bytes in the tile's upper half (the copies' swizzle: 16-byte
+// chunk c of row r at c ^ (r & 7) for 128-byte rows, c ^ ((r >> 1) & 3) for
+// 64-byte rows).  After: per 64 columns, f16 row r at r * 128 bytes, chunk j at
+// j ^ (r & 7).  For D = 128 row r's second 64 columns land exactly on its own
+// E4M3 row; for D = 64 f16 row r covers E4M3 rows 2 r - R and 2 r - R + 1, none
+// above r (so one warp takes all rows there, in order).  Rows are read before any
+// lane writes.
+template <int D, int R>
+__device__ __forceinline__ void widen(uint32_t tile, int lane, int row0, int rows)
 {
-    constexpr int PL = D / 32;  // channels of a lane
-    constexpr int KV = F8 ? PKV_FP8_E4M3 : PKV_BF16;
-    constexpr int ROWB = (int)kv_row_bytes(KV, D);
-    __shared__ float sm[kWarps][G], sl[kWarps][G], so[kWarps][G][D];
-    griddep_wait();
-    griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = blockIdx.x;
-    const int g = blockIdx.y;
-    if (row == 0 && g == 0)
-        for (int b = threadIdx.x; b < a.batch; b += kWarps * 32)
-            if (a.qo_indptr[b] < 0 || a.qo_indptr[b + 1] < a.qo_indptr[b]) atomicOr(a.err, PKV_DEVERR_CTX_RANGE);
-    int lo = 0, hi = a.batch;  // the last sequence that begins at or before the row
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.qo_indptr[mid] <= row) lo = mid; else hi = mid;
-    }
-    const int64_t first = a.qo_indptr[lo], end = a.qo_indptr[lo + 1];
-    if (first < 0 || row < first || row >= end) return;
-    const int64_t T = end - first;
-    const int C = a.context_lens[lo];
-    if (end > a.n_rows || T > 64 * a.words || C < T || C > a.W * kBlockSize) {
-        if (threadIdx.x == 0) atomicOr(a.err, PKV_DEVERR_CTX_RANGE);
-        return;
-    }
-    const int base = C - (int)T;
-    float q[G][PL], m[G], l[G], o[G][PL];
-    const float qs = a.qscale * (F8 ? a.scales[g] : 1.0f), vs = F8 ? a.scales[a.n_kv + g] : 1.0f;
+    constexpr int CPR = D / 16;      // 16-byte chunks of an E4M3 row
+    constexpr int RPI = 32 / CPR;    // rows per step of a warp
+    constexpr int U = 4;
+    const uint32_t in = tile + R * D;
+    const int c = lane % CPR;
+#pragma unroll 1
+    for (int i = row0; i < row0 + rows; i += U * RPI) {
+        uint4 x[U];
+        int r[U];
 #pragma unroll
-    for (int h = 0; h < G; ++h) {
-        m[h] = -FLT_MAX;  // (finite: a score of -inf is below it and weighs 0)
-        l[h] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < PL; ++i) {
-            q[h][i] = __bfloat162float(a.q[(row * a.n_q + g * G + h) * D + lane * PL + i]);
-            o[h][i] = 0.0f;
+        for (int u = 0; u < U; ++u) {
+            r[u] = i + u * RPI + lane / CPR;
+            const int sw = D == 128 ? r[u] & 7 : (r[u] >> 1) & 3;
+            x[u] = lds128(in + r[u] * D + ((c ^ sw) << 4));
         }
-    }
-    auto elem = [&](const uint8_t *p, int i) -> float {
-        if constexpr (F8) return (float)reinterpret_cast<const __nv_fp8_e4m3 *>(p)[i];
-        else return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[i]);
-    };
-    for (int pos = warp; pos < C; pos += kWarps) {
-        if (pos >= base) {
-            const int j = pos - base;
-            if (!((a.mask[row * a.words + j / 64] >> (j % 64)) & 1)) continue;
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            uint4 lo, hi;
+            e4m3x4_to_f16x4(x[u].x, lo.x, lo.y);
+            e4m3x4_to_f16x4(x[u].y, lo.z, lo.w);
+            e4m3x4_to_f16x4(x[u].z, hi.x, hi.y);
+            e4m3x4_to_f16x4(x[u].w, hi.z, hi.w);
+            const uint32_t row = tile + (c >> 2) * (R * 128) + r[u] * 128;
+            const int j = 2 * (c & 3);
+            sts128(row + ((j ^ (r[u] & 7)) << 4), lo);
+            sts128(row + (((j + 1) ^ (r[u] & 7)) << 4), hi);
         }
-        const int32_t blk = a.block_tables[(int64_t)lo * a.W + pos / kBlockSize];
-        if (blk < 0 || blk >= a.num_blocks) {
-            if (lane == 0) atomicOr(a.err, PKV_DEVERR_BLOCK_RANGE);
-            continue;
-        }
-        const uint8_t *k = a.pool + ((int64_t)blk * a.n_kv + g) * kv_entry_bytes(KV, D) + pos % kBlockSize * ROWB;
-        const uint8_t *v = k + kBlockSize * ROWB;
-        float kf[PL], vf[PL];
-#pragma unroll
-        for (int i = 0; i < PL; ++i) {
-            kf[i] = elem(k, lane * PL + i);
-            vf[i] = elem(v, lane * PL + i);
-        }
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-            float s = 0.0f;
-#pragma unroll
-            for (int i = 0; i < PL; ++i) s = fmaf(q[h][i], kf[i], s);
-#pragma unroll
-            for (int x = 16; x >= 1; x >>= 1) s += __shfl_xor_sync(kFull, s, x);
-            s *= qs;
-            const float mn = fmaxf(m[h], s), f = exp2f(m[h] - mn), w = exp2f(s - mn);
-            l[h] = l[h] * f + w;
-#pragma unroll
-            for (int i = 0; i < PL; ++i) o[h][i] = o[h][i] * f + w * vf[i];
-            m[h] = mn;
-        }
-    }
-#pragma unroll
-    for (int h = 0; h < G; ++h) {
-        sm[warp][h] = m[h];
-        sl[warp][h] = l[h];
-#pragma unroll
-        for (int i = 0; i < PL; ++i) so[warp][h][lane * PL + i] = o[h][i];
-    }
-    __syncthreads();
-    for (int h = warp; h < G; h += kWarps) {
-        float M = -FLT_MAX, L = 0.0f, acc[PL] = {};
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w][h]);
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = exp2f(sm[w][h] - M);
-            L += sl[w][h] * f;
-#pragma unroll
-            for (int i = 0; i < PL; ++i) acc[i] += so[w][h][lane * PL + i] * f;
-        }
-        const float inv = L == 0.0f ? 0.0f : vs / L;
-#pragma unroll
-        for (int i = 0; i < PL; ++i)
-            a.out[(row * a.n_q + g * G + h) * D + lane * PL + i] = __float2bfloat16(acc[i] * inv);
+        __syncwarp();
     }
 }
 
-template <int D, bool F8>
-cudaError_t launch(const Args &a, int G, cudaStream_t s)
+// ------------------------------------------------------------- the stream of steps
+
+// Steps [s0, s0 + n) of a unit: what a CTA does of it.
+struct Piece {
+    int b, g, r0;      // sequence, KV head, first local row
+    int row0, T, R, C; // first token row, nodes, local rows (nodes x heads), cache length
+    int S, s0, n;      // the unit's steps; this piece's
+    int n_blocks;
+    __device__ __forceinline__ bool two() const { return R - r0 > kRows; }
+    __device__ __forceinline__ bool whole() const { return n == S; }
+};
+
+// A window of 32 sequences, one per lane: each warp walks the stream itself, with the same arithmetic.
+struct Walker {
+    int wb = 0, wbase = 0, tot = 0;  // first sequence of the window, steps before it, its steps
+    int incl = 0;                    // steps up to and with this lane's sequence
+    int row0 = 0, T = 0, C = 0;      // this lane's sequence
+    int S = 0, pairs = 0;            // steps and units per KV head
+};
+
+__device__ __forceinline__ int inclusive_sum(int x, int lane)
 {
-    const dim3 grid((unsigned)a.n_rows, (unsigned)a.n_kv);
-    switch (G) {
-    case 1: return launch_pdl(tree_kernel<D, 1, F8>, grid, dim3(kWarps * 32), 0, s, a);
-    case 2: return launch_pdl(tree_kernel<D, 2, F8>, grid, dim3(kWarps * 32), 0, s, a);
-    case 4: return launch_pdl(tree_kernel<D, 4, F8>, grid, dim3(kWarps * 32), 0, s, a);
-    default: return launch_pdl(tree_kernel<D, 8, F8>, grid, dim3(kWarps * 32), 0, s, a);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, x, o);
+        if (lane >= o) x += y;
     }
+    return x;
+}
+
+// Sequence b's nodes, length, steps and units; no work where it does not fit.
+template <int G>
+__device__ __forceinline__ int sequence(const Args &a, int b, Walker &w, bool flag)
+{
+    w.row0 = w.T = w.C = w.S = w.pairs = 0;
+    if (b >= a.batch) return 0;
+    const int lo = a.qo_indptr[b], hi = a.qo_indptr[b + 1], C = a.context_lens[b];
+    if (lo < 0 || hi < lo || hi > a.n_rows || hi - lo > 64 * a.words || C < hi - lo || C > a.W * kBlockSize) {
+        if (flag) atomicOr(a.err, PKV_DEVERR_CTX_RANGE);
+        return 0;
+    }
+    w.row0 = lo;
+    w.T = hi - lo;
+    w.C = C;
+    if (w.T > 0) {
+        w.S = (C + kKeys - 1) / kKeys;
+        w.pairs = (w.T * G + kUnitRows - 1) / kUnitRows;
+    }
+    return w.S * w.pairs * a.n_kv;
+}
+
+template <int G>
+__device__ __forceinline__ void load_window(Walker &w, const Args &a, int lane)
+{
+    const int work = sequence<G>(a, w.wb + lane, w, false);
+    w.incl = inclusive_sum(work, lane);
+    w.tot = __shfl_sync(kFull, w.incl, 31);
+}
+
+// The piece that begins at step f of the stream, up to step `end`; false past it.  Warp-wide, uniform result.
+template <int G>
+__device__ __forceinline__ bool find_piece(Walker &w, const Args &a, int f, int end, Piece &p, int lane)
+{
+    if (f >= end) return false;
+    while (f >= w.wbase + w.tot) {
+        if (w.wb + 32 >= a.batch) return false;
+        w.wbase += w.tot;
+        w.wb += 32;
+        load_window<G>(w, a, lane);
+    }
+    const int at = f - w.wbase;
+    const int l = __ffs(__ballot_sync(kFull, w.incl > at)) - 1;
+    p.b = w.wb + l;
+    p.row0 = __shfl_sync(kFull, w.row0, l);
+    p.T = __shfl_sync(kFull, w.T, l);
+    p.C = __shfl_sync(kFull, w.C, l);
+    p.S = __shfl_sync(kFull, w.S, l);
+    const int pairs = __shfl_sync(kFull, w.pairs, l);
+    const int within = at - (__shfl_sync(kFull, w.incl, l) - p.S * pairs * a.n_kv);
+    const int unit = within / p.S;
+    p.s0 = within - unit * p.S;
+    p.g = unit / pairs;
+    p.r0 = (unit - p.g * pairs) * kUnitRows;
+    p.n = min(p.S - p.s0, end - f);
+    p.R = p.T * G;
+    p.n_blocks = (p.C + kBlockSize - 1) / kBlockSize;
+    return true;
+}
+
+// Bits [at, at + 32) of a row's view of its sequence's T nodes; the positions before the nodes are all seen.
+__device__ __forceinline__ uint32_t node_bits(const uint32_t *row, int words, int T, int at)
+{
+    if (at <= -32) return kFull;
+    if (at >= T) return 0;
+    auto word = [&](int i) -> uint32_t { return i >= 0 && i < words ? __ldg(row + i) : i < 0 ? kFull : 0u; };
+    const int i = at >> 5;  // (rounds down: -1 where the 32 begin before the nodes)
+    uint32_t bits = __funnelshift_r(word(i), word(i + 1), at & 31);
+    if (T - at < 32) bits &= (1u << (T - at)) - 1u;
+    return bits;
+}
+
+// ------------------------------------------------------------- the kernel
+
+template <int D, int G, bool F8>
+__global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
+                const __grid_constant__ Args a)
+{
+    using L = Layout<D>;
+    using Wp = Warps<F8>;
+    constexpr int NH = D / 64;  // 64-column ranges of a row
+    constexpr int NS = L::kStages;
+    constexpr int kWarps = Wp::kThreads / 32;
+    // FP8 pools: the preparing warps take a quarter of every tile at d_head 128, and half of every other tile at 64
+    // (NS is even there, so a warp sees every phase of its slots)
+    constexpr int kSplit = !F8 ? 1 : D == 128 ? 4 : 2;  // warps on a tile
+    static_assert(D == 128 || NS % 2 == 0, "a preparing warp would miss phases of its slots");
+    extern __shared__ __align__(1024) uint8_t tree_smem[];
+    uint8_t *sm = tree_smem + ((1024u - (smem_u32(tree_smem) & 1023u)) & 1023u);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::kBar);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::kAbort);
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(kFull, tid >> 5, 0);  // the same in all lanes, and known to be
+
+    if (warp == kCopyWarp && lane == 0) {
+        prefetch_tensormap(&tm_q);
+        prefetch_tensormap(&tm_kv);
+        *abort_flag = 0;
+    }
+    static_assert(L::NBARS <= 12 * 32, "a thread per barrier");
+    if (tid < L::NBARS) {
+        const int i = tid;
+        uint32_t n = 1;
+        if (i >= L::P_FULL && i < L::P_FULL + 2) n = 4;            // a stream's warps
+        if (i == L::Q_FREE || i == L::DRAIN) n = 2;                // both issuing warps
+        if (i >= L::EMPTY && i < L::EMPTY + NS) n = 2;
+        if (i == L::Q_FULL && F8) n = 8;                           // each softmax warp widens its share of the queries
+        if (i >= L::FULL && i < L::FULL + NS) n = kSplit;
+        mbar_init(&bar[i], n);
+        fence_mbarrier_init();
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(sm + L::kTmemSlot)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + L::kTmemSlot);
+    griddep_wait();
+    griddep_launch_dependents();
+
+    auto set_abort = [&]() {
+        if (lane == 0) {
+            atomicOr(a.err, PKV_DEVERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+    };
+
+    // ---- this CTA's slice of the stream, and the window in which it begins ----
+    Walker w0;
+    int f0, f1, share;
+    {
+        int *win = reinterpret_cast<int *>(sm + L::kRing);  // steps of each window of 32 sequences
+        const int windows = (a.batch + 31) / 32;
+        for (int i = warp; i < windows; i += kWarps) {
+            const int x = inclusive_sum(sequence<G>(a, 32 * i + lane, w0, blockIdx.x == 0), lane);
+            if (lane == 31) win[i] = x;
+        }
+        __syncthreads();
+        int total = 0;
+        for (int i = 0; i < windows; i += 32) total += __reduce_add_sync(kFull, i + lane < windows ? win[i + lane] : 0);
+        share = max(kMinShare, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+        f0 = min((int64_t)total, (int64_t)blockIdx.x * share);
+        f1 = min((int64_t)total, (int64_t)f0 + share);
+        int before = 0;
+        for (int i = 0; i < windows; i += 32) {
+            const int x = i + lane < windows ? win[i + lane] : 0;
+            const int incl = inclusive_sum(x, lane);
+            const unsigned on = __ballot_sync(kFull, i + lane < windows && before + incl - x <= f0);
+            if (on) {
+                const int l = 31 - __clz(on);
+                w0.wb = 32 * (i + l);
+                w0.wbase = before + __shfl_sync(kFull, incl - x, l);
+            }
+            before += __shfl_sync(kFull, incl, 31);
+        }
+        fence_proxy_async_smem();
+        __syncthreads();  // the ring is free for the copies
+    }
+    Walker wk;
+    wk.wb = w0.wb;
+    wk.wbase = w0.wbase;
+    load_window<G>(wk, a, lane);
+    const uint32_t base = smem_u32(sm);
+
+    if (warp >= kCopyWarp) {
+        if constexpr (F8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Wp::kWorkRegs));
+        if (warp == kCopyWarp) {
+            // ---------------------------------------------------------- copies
+            const uint64_t policy = l2_policy_evict_normal();
+            const uint32_t go = elect_one();  // one lane issues all copies, the warp running as one
+            int u = 0, n = 0;                 // tiles of the ring, pieces
+            bool ok = true;
+            Piece p;
+            Part begun = {0, 0, 0, 0, -1};
+            for (int f = f0; ok && find_piece<G>(wk, a, f, f1, p, lane); f += p.n) {
+                if (*abort_flag) break;
+                if (n > 0 && !(ok = wait_all(&bar[L::Q_FREE], (n - 1) & 1))) break;
+                if (lane == 0) {
+                    uint64_t *qb = &bar[F8 ? L::Q_RAW : L::Q_FULL];
+                    mbar_arrive_expect_tx(qb, p.two() ? 2 * L::QT : L::QT);
+                    for (int t = 0; t < (p.two() ? 2 : 1); ++t)
+#pragma unroll
+                        for (int h = 0; h < NH; ++h)
+                            tma_load_3d(sm + L::kQ + t * L::QT + h * kHalf, &tm_q, 64 * h, p.g * G,
+                                        p.row0 + (p.r0 + t * kRows) / G, qb, policy);
+                }
+                __syncwarp();
+                ++n;
+                if (p.s0 == 0 && !p.whole()) begun = {p.row0, p.r0, p.R, p.g, (p.S - p.n + share - 1) / share};
+                const int32_t *trow = a.block_tables + (int64_t)p.b * a.W;
+                // lane k < 8: the entry rows of block k of a step, or rows past the pool (zero filled)
+                auto rows_of = [&](int s) -> int {
+                    const int nb = (p.s0 + s) * kStepBlocks + lane;
+                    const bool present = lane < kStepBlocks && nb < p.n_blocks;
+                    const int id = present ? trow[nb] : -1;
+                    const bool valid = id >= 0 && id < a.num_blocks;
+                    if (present && !valid) atomicOr(a.err, PKV_DEVERR_BLOCK_RANGE);
+                    return valid ? (int)((id * (int64_t)a.n_kv + p.g) * 2 * kBlockSize) : a.oob_row;
+                };
+                int nxt = rows_of(0);
+                for (int s = 0; s < p.n && ok; ++s) {
+                    const int y0 = nxt;
+                    if (s + 1 < p.n) nxt = rows_of(s + 1);
+#pragma unroll
+                    for (int v = 0; v < 2; ++v, ++u) {  // keys, then values
+                        const int st = u % NS, use = u / NS;
+                        if (use > 0 && !(ok = wait_all(&bar[L::EMPTY + st], (use - 1) & 1))) break;
+                        uint64_t *b = &bar[(F8 ? L::RAW : L::FULL) + st];
+                        const uint32_t land = smem_u32(b), dst = base + L::kRing + st * L::UT;
+                        if (go) mbar_arrive_expect_tx(b, F8 ? L::UT / 2 : L::UT);
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < kStepBlocks; ++k) {
+                            const int yk = __shfl_sync(kFull, y0, k);
+                            const int y = yk == a.oob_row ? yk : yk + v * kBlockSize;
+                            if constexpr (F8) {
+                                constexpr int kTileRows = D == 128 ? 128 : 64;  // (see widen)
+                                tma_load_2d_if(go, dst + (k * kBlockSize / kTileRows) * (kTileRows * 2 * D) + kTileRows * D +
+                                                       (k * kBlockSize % kTileRows) * D,
+                                               &tm_kv, 0, y, land, policy);
+                            } else {
+#pragma unroll
+                                for (int h = 0; h < NH; ++h)
+                                    tma_load_2d_if(go, dst + h * kHalf + k * (kBlockSize * 128), &tm_kv, 64 * h, y, land, policy);
+                            }
+                        }
+                    }
+                }
+            }
+            if (lane == 0) a.parts[blockIdx.x] = begun;
+            // copies still in flight (after an abort) land before the CTA exits
+            for (int i = max(0, u - NS); i < u; ++i)
+                mbar_wait_bounded(&bar[(F8 ? L::RAW : L::FULL) + i % NS], (i / NS) & 1);
+            // and so do the MMAs' arrivals for the last tiles
+            for (int i = max(0, u - NS); i < u && ok && !*abort_flag; ++i)
+                ok = wait_all(&bar[L::EMPTY + i % NS], (i / NS) & 1);
+            if (n > 0) mbar_wait_bounded(&bar[F8 ? L::Q_RAW : L::Q_FULL], (n - 1) & 1);
+            if (!ok) set_abort();
+        } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+            // ---------------------------------------------------------- S = Q K^T and O += P V of one stream
+            const int x = warp - kMmaWarp;
+            constexpr uint32_t idesc_qk = mma_idesc(kRows, kKeys, 0, F8), idesc_pv = mma_idesc(kRows, D, 1, F8);
+            const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+            const uint32_t go = elect_one();
+            const uint64_t kd = smem_desc(base + L::kRing, 16, 1024), vd = smem_desc(base + L::kRing, kHalf, 1024);
+            int u = 0, n = 0, turns = 0;  // tiles of the ring, pieces, this stream's steps
+            bool ok = true;
+            Piece p;
+            auto full = [&](int i) -> bool { return wait_all(&bar[L::FULL + i % NS], (i / NS) & 1); };
+            for (int f = f0; ok && find_piece<G>(wk, a, f, f1, p, lane); f += p.n) {
+                if (*abort_flag) break;
+                if (!(ok = wait_all(&bar[L::Q_FULL], n & 1))) break;
+                const bool two = p.two();
+                const uint64_t qd = smem_desc(base + L::kQ + (two ? x * L::QT : 0), 16, 1024);
+                bool q_held = true;
+                for (int s = 0; s < p.n; ++s, u += 2) {
+                    const int ks = u % NS, vs = (u + 1) % NS;
+                    if (!two && (s & 1) != x) {  // the other stream's: only say that it is not needed here (any more)
+                        if (!(ok = full(u) && full(u + 1))) break;
+                        if (go) {
+                            mbar_arrive(&bar[L::EMPTY + ks]);
+                            mbar_arrive(&bar[L::EMPTY + vs]);
+                        }
+                        __syncwarp();
+                        continue;
+                    }
+                    const bool first = two ? s == 0 : s == x;
+                    // the scores' place is free: the weights over the last ones have been used
+                    if (!(ok = full(u))) break;
+                    if (turns > 0 && !(ok = wait_all(&bar[L::PV_DONE + x], (turns - 1) & 1))) break;
+                    tc_fence_after();
+                    const uint64_t km = kd + ((ks * L::UT) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+                        umma_if(go, tm + x * kKeys, qd + off, km + off, idesc_qk, kk > 0 ? 1u : 0u);
+                    }
+                    umma_commit_if(go, &bar[L::S_FULL + x]);
+                    umma_commit_if(go, &bar[L::EMPTY + ks]);
+                    if (s + (two ? 1 : 2) >= p.n) {  // the piece's last scores
+                        umma_commit_if(go, &bar[L::Q_FREE]);
+                        q_held = false;
+                    }
+                    if (!(ok = full(u + 1))) break;
+                    if (!F8 && p.s0 + s == p.S - 1 && p.C % kBlockSize) {
+                        // the sequence ends inside a block: zero the value rows behind its end (both streams of
+                        // two tiles do, each before its own product; the second writes zeros over zeros)
+                        const int r0 = p.C % kKeys, rows = kBlockSize - p.C % kBlockSize;
+                        for (int e = lane; e < rows * 8 * NH; e += 32) {
+                            const int row = r0 + (e >> 3) % rows, h = (e >> 3) / rows;
+                            sts128(base + L::kRing + vs * L::UT + h * kHalf + row * 128 + (e & 7) * 16, make_uint4(0, 0, 0, 0));
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (!(ok = wait_all(&bar[L::P_FULL + x], turns & 1))) break;
+                    tc_fence_after();
+                    const uint64_t vm = vd + ((vs * L::UT) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < kKeys / 16; ++kk)
+                        umma_ts_if(go, tm + kColO + x * D, tm + x * kKeys + kk * 8, vm + ((kk * 2048) >> 4), idesc_pv,
+                                   !first || kk > 0 ? 1u : 0u);
+                    umma_commit_if(go, &bar[L::PV_DONE + x]);
+                    umma_commit_if(go, &bar[L::EMPTY + vs]);
+                    ++turns;
+                }
+                if (!ok) break;
+                if (q_held) umma_commit_if(go, &bar[L::Q_FREE]);  // (a piece of one step has none for stream 1)
+                ++n;
+            }
+            umma_commit_if(go, &bar[L::DRAIN]);
+            __syncwarp();
+            mbar_wait_bounded(&bar[L::DRAIN], 0);
+            if (!ok) set_abort();
+        } else if (F8 && warp >= kPrepWarp && warp < kPrepWarp + 4) {
+            // ---------------------------------------------------------- E4M3 tiles widened
+            const int which = warp - kPrepWarp;
+            int u = 0;
+            bool ok = true;
+            Piece p;
+            for (int f = f0; ok && find_piece<G>(wk, a, f, f1, p, lane); f += p.n) {
+                if (*abort_flag) break;
+                for (int i = 0; i < 2 * p.n; ++i, ++u) {
+                    if (D == 64 && (u & 1) != which >> 1) continue;
+                    const int st = u % NS;
+                    if (!(ok = wait_all(&bar[L::RAW + st], (u / NS) & 1))) break;
+                    const uint32_t tile = base + L::kRing + st * L::UT;
+                    constexpr int kOwn = D == 128 ? 32 : 64;  // rows of this warp
+                    const int own0 = D == 128 ? which * 32 : (which & 1) * 64;
+                    if constexpr (D == 128) widen<D, 128>(tile, lane, own0, 32);
+                    else widen<D, 64>(tile + own0 * 128, lane, 0, 64);
+                    if ((i & 1) && p.s0 + (i >> 1) == p.S - 1 && p.C % kBlockSize) {  // value rows behind the end
+                        const int r0 = p.C % kKeys, rows = kBlockSize - p.C % kBlockSize;
+                        if (r0 / kOwn * kOwn == own0) {
+                            for (int e = lane; e < rows * 8 * NH; e += 32) {
+                                const int row = r0 + (e >> 3) % rows, h = (e >> 3) / rows;
+                                sts128(tile + h * kHalf + row * 128 + (e & 7) * 16, make_uint4(0, 0, 0, 0));
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[L::FULL + st]);
+                }
+            }
+            if (!ok) set_abort();
+        }
+    } else {
+        // ---------------------------------------------------------- softmax
+        if constexpr (F8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Wp::kScoreRegs));
+        const int x = warp >> 2, quarter = warp & 3;  // stream; TMEM lanes 32 quarter ..
+        const int row = quarter * 32 + lane;
+        const uint32_t ts = tmem + ((uint32_t)(quarter * 32) << 16);
+        float2 *stat = reinterpret_cast<float2 *>(sm + L::kStat);
+        const bool rising = a.qscale >= 0.0f;  // else scores are negated as they are read
+        int turns = 0, n = 0, joins = 0;       // this stream's steps, pieces, units of one tile
+        bool ok = true;
+        Piece p;
+        for (int f = f0; ok && find_piece<G>(wk, a, f, f1, p, lane); f += p.n) {
+            if (*abort_flag) break;
+            const bool two = p.two();
+            if constexpr (F8) {  // the queries to f16 in place, element by element: this warp's share
+                if (!(ok = wait_all(&bar[L::Q_RAW], n & 1))) break;
+                const uint32_t part = (two ? 2 : 1) * L::QT / 8;
+#pragma unroll 4
+                for (uint32_t off = warp * part + 16u * lane; off < (warp + 1) * part; off += 16u * 32) {
+                    uint4 v = lds128(base + off);
+                    uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 q = bf16x2_to_f32x2(w[k]);
+                        w[k] = pack_f16x2(q.x, q.y);
+                    }
+                    sts128(base + off, v);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[L::Q_FULL]);
+            }
+            ++n;
+            const int t0 = p.r0 + (two ? x * kRows : 0);  // the tile's first local row
+            const int r = t0 + row;
+            const bool live = t0 + quarter * 32 < p.R;    // some row of this warp is
+            const int node = min(r, p.R - 1) / G;
+            const uint32_t *mrow = a.mask + ((int64_t)p.row0 + node) * 2 * a.words;
+            const int before = p.C - p.T;                 // positions before the nodes
+            const float qs = fabsf(a.qscale) * (F8 ? a.scales[p.g] : 1.0f);
+            const int32_t *trow = a.block_tables + (int64_t)p.b * a.W;
+            const int hop = two ? 1 : 2, s1 = two ? 0 : x;
+            auto ids_of = [&](int s) -> int {
+                const int nb = (p.s0 + s) * kStepBlocks + lane;
+                return lane < kStepBlocks && s < p.n && nb < p.n_blocks ? trow[nb] : -1;
+            };
+            float mref = -INFINITY, l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            int nxt = ids_of(s1);
+            for (int s = s1; s < p.n; s += hop, ++turns) {
+                // blocks that are there, as the copies decided
+                const uint32_t valid = __ballot_sync(kFull, lane < kStepBlocks && nxt >= 0 && nxt < a.num_blocks);
+                nxt = ids_of(s + hop);
+                if (!(ok = wait_all(&bar[L::S_FULL + x], turns & 1))) break;
+                if (live) {
+                    tc_fence_after();
+                    uint32_t sr[kKeys];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(ts + x * kKeys + 32 * c, sr + 32 * c);
+                    tmem_wait_ld();
+                    if (!rising) {
+#pragma unroll
+                        for (int i = 0; i < kKeys; ++i) sr[i] ^= 0x80000000u;
+                    }
+                    const int key0 = (p.s0 + s) * kKeys;
+                    if (key0 + kKeys > before || valid != (1u << kStepBlocks) - 1) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t bits = node_bits(mrow, 2 * a.words, p.T, key0 + 32 * c - before);
+                            if (!((valid >> (2 * c)) & 1u)) bits &= 0xffff0000u;
+                            if (!((valid >> (2 * c)) & 2u)) bits &= 0xffffu;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (!((bits >> k) & 1u)) sr[32 * c + k] = 0xff800000u;
+                        }
+                    }
+                    auto e = [&](int i) { return __uint_as_float(sr[i]); };
+                    float mx[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        mx[j] = fmax3(e(j), e(j + 8), e(j + 16));
+#pragma unroll
+                        for (int i = 3; i < 15; i += 2) mx[j] = fmax3(mx[j], e(j + 8 * i), e(j + 8 * i + 8));
+                        mx[j] = fmaxf(mx[j], e(j + 120));
+                    }
+                    const float top = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * qs;
+                    const bool raise = top > mref + kSlack;
+                    float alpha = 1.0f;
+                    if (raise) {
+                        alpha = ex2(mref - top);  // 0 when mref is -inf
+                        mref = top;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) l4[i] *= alpha;
+                    }
+                    const float nm = mref == -INFINITY ? 0.0f : -mref;
+                    uint32_t pk[kKeys / 2];
+#pragma unroll
+                    for (int i = 0; i < kKeys / 2; ++i) {
+                        const float2 d = ffma2(make_float2(e(2 * i), e(2 * i + 1)), make_float2(qs, qs), make_float2(nm, nm));
+                        if constexpr (F8) {
+                            pk[i] = pack_f16x2(ex2(d.x), ex2(d.y));
+                            add_f16x2_to(l4[i & 3], pk[i]);
+                        } else {
+                            pk[i] = pack_bf16x2(ex2(d.x), ex2(d.y));
+                            add_bf16x2_to(l4[i & 3], pk[i]);
+                        }
+                    }
+                    // (the scores were issued after the last product had run, so O is final)
+                    if (s != s1 && __any_sync(kFull, raise)) {
+#pragma unroll
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(ts + kColO + x * D + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            tmem_st32(ts + kColO + x * D + c, o);
+                        }
+                    }
+                    // the weights over the scores, which are read
+                    tmem_st32(ts + x * kKeys, pk);
+                    tmem_st32(ts + x * kKeys + 32, pk + 32);
+                    tmem_wait_st();
+                }
+                // stream 1: its O of the last unit of one tile is read
+                if (x == 1 && s == s1 && joins > 0 && !(ok = wait_all(&bar[L::TAKEN + quarter], (joins - 1) & 1))) break;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[L::P_FULL + x]);
+            }
+            if (!ok) break;
+            // ---- the end of the piece ----
+            const bool any = s1 < p.n;  // this stream had steps
+            if (any && !(ok = wait_all(&bar[L::PV_DONE + x], (turns - 1) & 1))) break;
+            tc_fence_after();
+            float l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
+            float fa = 1.0f, fb = 0.0f;  // O = fa O_x + fb O_1
+            if (!two) {
+                if (x == 1) {
+                    if (joins > 0 && !any && !(ok = wait_all(&bar[L::TAKEN + quarter], (joins - 1) & 1))) break;
+                    stat[row] = make_float2(mref, l);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[L::STAT + quarter]);
+                    ++joins;
+                    continue;
+                }
+                if (!(ok = wait_all(&bar[L::STAT + quarter], joins & 1))) break;
+                ++joins;
+                tc_fence_after();
+                const float2 y = stat[row];
+                const float top = fmaxf(mref, y.x);
+                fa = mref == -INFINITY ? 0.0f : ex2(mref - top);
+                fb = y.x == -INFINITY ? 0.0f : ex2(y.x - top);
+                l = l * fa + y.y * fb;
+                mref = top;
+            }
+            const float vs = F8 ? a.scales[a.n_kv + p.g] : 1.0f;
+            const bool join = !two && p.n > 1;
+            const float norm = p.whole() ? (l > 0.0f ? vs / l : l == 0.0f ? 0.0f : l) : vs;
+            fa *= norm;
+            fb *= norm;
+            const int slot = 2 * (int)blockIdx.x + (p.s0 == 0 ? 1 : 0);
+            const int64_t at = (int64_t)slot * a.slot_rows + (r - p.r0);
+            __nv_bfloat16 *dst = a.out + (((int64_t)p.row0 + node) * a.n_q + p.g * G + min(r, p.R - 1) % G) * D;
+            if (live) {
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(ts + kColO + x * D + c, o);
+                    if (join) {
+                        uint32_t o1[32];
+                        tmem_ld32(ts + kColO + D + c, o1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = __float_as_uint(fa == 0.0f && fb == 0.0f ? 0.0f : fmaf(fb, __uint_as_float(o1[i]), fa * __uint_as_float(o[i])));
+                    } else {
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fa);
+                    }
+                    if (r < p.R) {
+                        if (p.whole()) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t w[8];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    w[i] = pack_bf16x2(__uint_as_float(o[16 * h + 2 * i]), __uint_as_float(o[16 * h + 2 * i + 1]));
+                                stg256(dst + c + 16 * h, w);
+                            }
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) stg256(a.ws_o + at * D + c + 8 * h, o + 8 * h);
+                        }
+                    }
+                }
+                if (!p.whole() && r < p.R) a.ws_ml[at] = make_float2(mref, l);
+            }
+            if (!two) {  // stream 1 may go on
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[L::TAKEN + quarter]);
+            }
+        }
+        if (!ok) set_abort();
+    }
+
+    tc_fence_before();
+    __syncthreads();  // every role is done with the tensor memory
+    tc_fence_after();
+    if (warp == kMmaWarp)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+// ------------------------------------------------------------- the parts of cut units
+
+struct MergeArgs {
+    const Part *parts;
+    const float2 *ws_ml;
+    const float *ws_o;
+    int slot_rows, n_q;
+    __nv_bfloat16 *out;
+};
+
+constexpr int kMergeWarps = 8;
+
+// Block (c, y): rows 8 y .. of the unit that begins in slice c and goes on in the next ones; a warp a row.
+template <int D, int G>
+__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ MergeArgs a)
+{
+    constexpr int PL = D / 32;  // channels of a lane
+    griddep_wait();
+    griddep_launch_dependents();
+    const int c = blockIdx.x, lane = threadIdx.x & 31;
+    const Part p = a.parts[c];
+    const int i = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);  // row of the unit
+    const int r = p.r0 + i;
+    if (p.more < 0 || i >= kUnitRows || r >= p.R) return;
+    auto at = [&](int k) -> int64_t { return (int64_t)(k == 0 ? 2 * c + 1 : 2 * (c + k)) * a.slot_rows + i; };
+    float M = -INFINITY;
+    for (int k = lane; k <= p.more; k += 32) M = fmaxf(M, a.ws_ml[at(k)].x);
+#pragma unroll
+    for (int s = 16; s >= 1; s >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, s));
+    float o[PL] = {}, l = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k <= p.more; ++k) {
+        const float2 y = a.ws_ml[at(k)];
+        const float f = y.x == -INFINITY ? 0.0f : exp2f(y.x - M);
+        l = fmaf(y.y, f, l);
+        const float *src = a.ws_o + at(k) * D + lane * PL;
+        float z[PL];
+        if constexpr (PL == 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(src);
+            z[0] = v.x; z[1] = v.y; z[2] = v.z; z[3] = v.w;
+        } else {
+            const float2 v = *reinterpret_cast<const float2 *>(src);
+            z[0] = v.x; z[1] = v.y;
+        }
+#pragma unroll
+        for (int d = 0; d < PL; ++d) o[d] = fmaf(z[d], f, o[d]);
+    }
+    const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+    __nv_bfloat16 *dst = a.out + (((int64_t)p.row0 + r / G) * a.n_q + p.g * G + r % G) * D + lane * PL;
+    if constexpr (PL == 4)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    else
+        *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(o[0] * inv, o[1] * inv);
+}
+
+// ------------------------------------------------------------- launch
+
+// The workspace of a call: parts, (m, l) and O of every slot.
+struct Space {
+    int slot_rows;
+    size_t ml, o, bytes;
+};
+Space space_of(const pkv_pool *pool, int64_t n_rows, int G, int ctas)
+{
+    Space s;
+    s.slot_rows = (int)std::min<int64_t>(kUnitRows, n_rows * G);
+    const size_t slots = 2 * (size_t)ctas;
+    s.ml = (ctas * sizeof(Part) + 255) / 256 * 256;
+    s.o = s.ml + (slots * s.slot_rows * sizeof(float2) + 255) / 256 * 256;
+    s.bytes = s.o + slots * s.slot_rows * (size_t)pool->d_head * sizeof(float);
+    return s;
+}
+
+// The kernel's attributes are set, once per device.
+template <int D, int G, bool F8>
+pkv_status prepare(const pkv_pool *pool)
+{
+    static std::mutex mu;
+    static bool ready[64];
+    std::lock_guard<std::mutex> lock(mu);
+    if (pool->device < 64 && ready[pool->device]) return PKV_OK;
+    auto kern = tree_kernel<D, G, F8>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::bytes);
+    cudaFuncAttributes fa;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return cuda_fail(e, "paged_tree_attention: kernel attributes");
+    // (with fewer registers at the launch, the softmax warps would wait for theirs)
+    if (F8 && fa.numRegs < Warps<F8>::kLaunchRegs)
+        return fail(PKV_EUNSUPPORTED, "paged_tree_attention: built with %d registers a thread", fa.numRegs);
+    if (pool->device < 64) ready[pool->device] = true;
+    return PKV_OK;
+}
+
+template <int D, int G, bool F8>
+pkv_status launch(pkv_pool *pool, const void *q, Args a, int ctas, cudaStream_t s)
+{
+    pkv_status st = prepare<D, G, F8>(pool);
+    if (st != PKV_OK) return st;
+    CUtensorMap tm_q;
+    st = make_q_map(&tm_q, q, a.n_rows, a.n_q, D, G, kRows / G);
+    if (st != PKV_OK) return st;
+    {
+        LaunchScope ls(pool, kDecode, s);
+        cudaError_t e = launch_pdl(tree_kernel<D, G, F8>, dim3(ctas), dim3(Warps<F8>::kThreads), Layout<D>::bytes, s, tm_q,
+                                   pool->tm_block, a);
+        ls.done();
+        if (e != cudaSuccess) return cuda_fail(e, "paged_tree_attention launch");
+    }
+    MergeArgs m;
+    m.parts = a.parts;
+    m.ws_ml = a.ws_ml;
+    m.ws_o = a.ws_o;
+    m.slot_rows = a.slot_rows;
+    m.n_q = a.n_q;
+    m.out = a.out;
+    LaunchScope ls(pool, kMerge, s);
+    cudaError_t e = launch_pdl(tree_merge_kernel<D, G>, dim3(ctas, (a.slot_rows + kMergeWarps - 1) / kMergeWarps),
+                               dim3(kMergeWarps * 32), 0, s, m);
+    ls.done();
+    if (e != cudaSuccess) return cuda_fail(e, "paged_tree_attention merge launch");
+    return PKV_OK;
+}
+
+template <int D, bool F8>
+pkv_status dispatch_g(pkv_pool *pool, const void *q, int G, const Args &a, int ctas, cudaStream_t s)
+{
+    switch (G) {
+    case 1: return launch<D, 1, F8>(pool, q, a, ctas, s);
+    case 2: return launch<D, 2, F8>(pool, q, a, ctas, s);
+    case 4: return launch<D, 4, F8>(pool, q, a, ctas, s);
+    case 8: return launch<D, 8, F8>(pool, q, a, ctas, s);
+    }
+    return fail(PKV_EUNSUPPORTED, "paged_tree_attention: group size %d unsupported (1, 2, 4 or 8)", G);
 }
 
 }  // namespace
 }  // namespace pkv
 
 using namespace pkv;
+
+extern "C" pkv_status paged_tree_reserve_workspace(pkv_pool *pool, int64_t n_rows, int32_t n_q)
+{
+    const char *who = "paged_tree_reserve_workspace";
+    pkv_status st = check_step_args(pool, who, n_q, 1, 0, 1.0f);
+    if (st != PKV_OK) return st;
+    if (pool->dtype == PKV_INT4) return fail(PKV_EUNSUPPORTED, "%s: bf16 and FP8 pools only (not 4-bit)", who);
+    if (n_rows < 0) return fail(PKV_EINVAL, "%s: n_rows < 0", who);
+    st = check_pool_device(pool, who);
+    if (st != PKV_OK) return st;
+    return ensure_workspace(pool, space_of(pool, std::min<int64_t>(n_rows, kUnitRows), n_q / pool->n_kv, pool->num_sms).bytes);
+}
 
 extern "C" pkv_status paged_tree_attention(pkv_pool *pool, const void *q, int64_t n_rows, int32_t n_q,
                                            const int32_t *qo_indptr, const uint64_t *tree_mask, int32_t mask_words,
@@ -166,7 +925,7 @@ extern "C" pkv_status paged_tree_attention(pkv_pool *pool, const void *q, int64_
     if (pool->dtype == PKV_INT4) return fail(PKV_EUNSUPPORTED, "%s: bf16 and FP8 pools only (not 4-bit)", who);
     if (n_rows < 0) return fail(PKV_EINVAL, "%s: n_rows < 0", who);
     if (mask_words < 1) return fail(PKV_EINVAL, "%s: mask_words %d", who, mask_words);
-    if (mask_words > 16) return fail(PKV_EUNSUPPORTED, "%s: mask_words %d > 16", who, mask_words);
+    if (mask_words > kMaxWords) return fail(PKV_EUNSUPPORTED, "%s: mask_words %d > %d", who, mask_words, kMaxWords);
     if (batch == 0 || n_rows == 0) return PKV_OK;
     const int G = n_q / pool->n_kv;
     if (n_rows > INT32_MAX / G) return fail(PKV_EUNSUPPORTED, "%s: more than 2^31 query rows x group size", who);
@@ -178,30 +937,41 @@ extern "C" pkv_status paged_tree_attention(pkv_pool *pool, const void *q, int64_
         return fail(PKV_EINVAL, "%s: indptr, tables and lengths must be 4-byte, masks 8-byte aligned", who);
     st = check_pool_device(pool, who);
     if (st != PKV_OK) return st;
+    // the most units and steps that the call can have: sequences may share rows (their indptr is not checked here)
+    const int64_t most = std::min<int64_t>((int64_t)64 * mask_words, n_rows) * G;  // rows of a sequence and KV head
+    const int64_t units = (int64_t)batch * pool->n_kv * ((most + kUnitRows - 1) / kUnitRows);
+    const int64_t steps = (max_blocks_per_seq + kStepBlocks - 1) / kStepBlocks;
+    if (units > (INT32_MAX / 2) / steps) return fail(PKV_EUNSUPPORTED, "%s: too many rows x table entries", who);
+    const int ctas = (int)std::min<int64_t>(pool->num_sms, units * steps);
+    const Space sp = space_of(pool, n_rows, G, ctas);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    st = ensure_workspace(pool, sp.bytes, s, who);
+    if (st != PKV_OK) return st;
     Args a;
-    a.pool = static_cast<const uint8_t *>(pool->k);
-    a.num_blocks = pool->num_blocks;
-    a.n_rows = n_rows;
-    a.n_q = n_q;
-    a.n_kv = pool->n_kv;
-    a.q = static_cast<const __nv_bfloat16 *>(q);
     a.qo_indptr = qo_indptr;
-    a.mask = tree_mask;
+    a.mask = reinterpret_cast<const uint32_t *>(tree_mask);
     a.words = mask_words;
     a.block_tables = block_tables;
     a.W = max_blocks_per_seq;
     a.context_lens = context_lens;
     a.batch = batch;
-    a.qscale = scale * kLog2e;
+    a.n_q = n_q;
+    a.n_kv = pool->n_kv;
+    a.num_blocks = pool->num_blocks;
+    a.n_rows = n_rows;
+    a.oob_row = (int)(pool->num_blocks * pool->n_kv * 2 * kBlockSize);
+    // (0 as 1e-30: the same scores to fp32, but -inf for hidden ones stays -inf)
+    a.qscale = scale == 0.0f ? 1e-30f : scale * kLog2e;
     a.scales = pool->scales;
+    a.slot_rows = sp.slot_rows;
+    uint8_t *ws = static_cast<uint8_t *>(pool->ws);
+    a.parts = reinterpret_cast<Part *>(ws);
+    a.ws_ml = reinterpret_cast<float2 *>(ws + sp.ml);
+    a.ws_o = reinterpret_cast<float *>(ws + sp.o);
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.err = pool->err;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool f8 = pool->dtype == PKV_FP8_E4M3;
-    LaunchScope ls(pool, kDecode, s);
-    cudaError_t e = pool->d_head == 128 ? (f8 ? launch<128, true>(a, G, s) : launch<128, false>(a, G, s))
-                                        : (f8 ? launch<64, true>(a, G, s) : launch<64, false>(a, G, s));
-    ls.done();
-    if (e != cudaSuccess) return cuda_fail(e, "paged_tree_attention launch");
-    return PKV_OK;
+    if (pool->d_head == 128)
+        return f8 ? dispatch_g<128, true>(pool, q, G, a, ctas, s) : dispatch_g<128, false>(pool, q, G, a, ctas, s);
+    return f8 ? dispatch_g<64, true>(pool, q, G, a, ctas, s) : dispatch_g<64, false>(pool, q, G, a, ctas, s);
 }

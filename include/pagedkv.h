@@ -568,14 +568,24 @@ pkv_status paged_diff_reserve_workspace(pkv_pool *pool, int32_t batch, int32_t n
  * The softmax statistics and the sums are held in fp32; weights are rounded
  * once, to bf16 (bf16 pools) or f16 (FP8 pools, whose queries are multiplied
  * as f16: |q| must stay in f16's range), and out once, to bf16.
- * bf16 and FP8 pools.  Other arguments, group sizes and limits as
- * paged_prefill_attention.
- * Errors: EINVAL, EUNSUPPORTED (4-bit pools, group size, mask_words, too many
- * query rows), ENOMEM, ECUDA. */
+ * bf16 and FP8 pools.  Two launches on the pool's workspace: equal slices of
+ * the (sequence, KV head, step of 128 keys) stream on the tcgen05 tensor cores,
+ * then a join of what was cut.  Results of a call do not depend on timing, but
+ * may differ in rounding between calls of different batches.  Other arguments,
+ * group sizes and limits as paged_prefill_attention.
+ * Errors: EINVAL (also a workspace that would have to grow while `stream` is
+ * captured), EUNSUPPORTED (4-bit pools, group size, mask_words, too many query
+ * rows), ENOMEM, ECUDA. */
 pkv_status paged_tree_attention(pkv_pool *pool, const void *q, int64_t n_rows, int32_t n_q, const int32_t *qo_indptr,
                                 const uint64_t *tree_mask, int32_t mask_words, const int32_t *block_tables,
                                 int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t batch, float scale,
                                 void *out, void *stream);
+
+/* Grow the pool's workspace now, so that later paged_tree_attention calls of at
+ * most n_rows rows and n_q query heads allocate nothing and may be captured (see
+ * paged_diff_reserve_workspace for what a captured workspace means).
+ * Errors: EINVAL, EUNSUPPORTED, ENOMEM. */
+pkv_status paged_tree_reserve_workspace(pkv_pool *pool, int64_t n_rows, int32_t n_q);
 
 /* Keep an accepted path of each tree: the cached row of node accepted[b][i]
  * moves to position C_b - T_b + i, for i < n_accepted[b], every KV head, keys
