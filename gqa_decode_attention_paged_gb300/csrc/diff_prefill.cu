@@ -219,17 +219,6 @@ __device__ __forceinline__ void convert_q(uint32_t base, int warp, int lane)
     }
 }
 
-// (a.x + b.x, a.y + b.y) in one paired instruction
-__device__ __forceinline__ float2 fadd2(float2 a, float2 b)
-{
-    float2 d;
-    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-
 // ------------------------------------------------------------- tile walk
 
 struct Tile {

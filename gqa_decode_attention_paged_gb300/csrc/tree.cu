@@ -24,19 +24,23 @@
 //     starts inside of (partial slot 2 cta) and the one it ends inside of
 //     (2 cta + 1).
 //   * two streams of softmax, each with its own scores and accumulator in
-//     tensor memory and its own four warps (a thread per row, all 128 keys of a
-//     step): while one forms weights, the tensor cores work for the other.  A
-//     unit of two tiles gives each stream a tile, and both use every key and
-//     value tile; in a unit of one tile the streams take alternate steps, and
-//     join by log-sum-exp at its end.
-//   * warp 8 streams what the MMAs take through one ring of 32 KiB (d 128)
-//     tiles: keys of a step, its values, keys of the next.  Warps 9 and 10 issue
-//     one stream's MMAs each: S = Q K^T, and when the weights are written over
-//     S, O += P V.
+//     tensor memory and its own eight warps: while one forms weights, the tensor
+//     cores work for the other.  A unit of two tiles gives each stream a tile,
+//     and both use every key and value tile; in a unit of one tile the streams
+//     take alternate steps, and join by log-sum-exp at its end.
+//   * a softmax warp has 16 rows, all 128 keys of a step, read from tensor
+//     memory as a matrix product's result is laid out: four threads a row, which
+//     two shuffles reduce.  (A thread per row, four warps a stream, left every
+//     scheduler with two warps and their dependent chains.)
+//   * one warp streams what the MMAs take through one ring of 32 KiB (d 128)
+//     tiles: keys of a step, its values, keys of the next.  Two warps issue one
+//     stream's MMAs each: S = Q K^T, and when the weights are written over S,
+//     O += P V.
 //   * the reference maximum is raised lazily (O is rescaled only when a row's
 //     maximum grows by more than 2^8).  Weights are rounded to bf16 (FP8 pools:
-//     f16) for the MMA, and the sum adds the rounded ones, so that the result is
-//     a convex combination of value rows.
+//     f16) for the MMA; the sum adds them in fp32 as they were (adding the
+//     rounded ones takes twice the additions, and makes no measurable difference
+//     against 64 bits).
 //   * FP8 pools: the E4M3 tiles are widened to f16 in place by four warps.
 //   * value rows behind the sequence's end are zeroed in shared memory before
 //     their product: a weight of 0 does not cancel what is not finite.
@@ -56,15 +60,17 @@ constexpr int kRows = 128;                 // query rows per tile (= TMEM lanes)
 constexpr int kUnitRows = 2 * kRows;
 constexpr int kKeys = 128;                 // keys per step
 constexpr int kStepBlocks = kKeys / kBlockSize;
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kPrepWarp = 11;
+constexpr int kSoftmaxWarps = 16;
+constexpr int kCopyWarp = 16, kMmaWarp = 17, kPrepWarp = 20;
 constexpr int kMaxWords = 16;
 constexpr int kMinShare = 2;               // steps of a slice at least
 template <bool F8>
 struct Warps {
-    static constexpr int kThreads = (F8 ? 16 : 12) * 32;
-    // FP8 pools: registers a thread at the launch, then of the softmax warps and of the others
-    static constexpr int kLaunchRegs = 128, kScoreRegs = 176, kWorkRegs = 80;
-    static_assert(8 * kScoreRegs + 8 * kWorkRegs <= 16 * kLaunchRegs, "more registers than the launch has");
+    static constexpr int kWarps = F8 ? 24 : 20, kThreads = kWarps * 32;
+    // registers a thread at the launch, then of the softmax warps and of the others
+    static constexpr int kLaunchRegs = F8 ? 80 : 96, kScoreRegs = F8 ? 96 : 104, kWorkRegs = F8 ? 48 : 64;
+    static_assert(kSoftmaxWarps * kScoreRegs + (kWarps - kSoftmaxWarps) * kWorkRegs <= kWarps * kLaunchRegs,
+                  "more registers than the launch has");
 };
 // Tensor memory: S_x at 128 x (fp32 scores; the weights, packed in pairs, over its first 64 columns), O_x at 256 + D x.
 constexpr uint32_t kTmemCols = 512;
@@ -111,9 +117,9 @@ struct Layout {
            S_FULL = EMPTY + kStages,  // per stream: scores of a step
            P_FULL = S_FULL + 2,       // its weights are in tensor memory
            PV_DONE = P_FULL + 2,      // their product has run
-           STAT = PV_DONE + 2,        // per lane quarter: stream 1's statistics and O are final
-           TAKEN = STAT + 4,          // they are read
-           DRAIN = TAKEN + 4, NBARS };
+           STAT = PV_DONE + 2,        // per warp of a stream: stream 1's statistics and O are final
+           TAKEN = STAT + 8,          // they are read
+           DRAIN = TAKEN + 8, NBARS };
     static constexpr uint32_t kTmemSlot = kBar + NBARS * 8;
     static constexpr uint32_t kAbort = kTmemSlot + 4;
     static constexpr uint32_t kEnd = kAbort + 4;
@@ -293,14 +299,14 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
         prefetch_tensormap(&tm_kv);
         *abort_flag = 0;
     }
-    static_assert(L::NBARS <= 12 * 32, "a thread per barrier");
+    static_assert(L::NBARS <= Wp::kThreads, "a thread per barrier");
     if (tid < L::NBARS) {
         const int i = tid;
         uint32_t n = 1;
-        if (i >= L::P_FULL && i < L::P_FULL + 2) n = 4;            // a stream's warps
+        if (i >= L::P_FULL && i < L::P_FULL + 2) n = kSoftmaxWarps / 2;  // a stream's warps
         if (i == L::Q_FREE || i == L::DRAIN) n = 2;                // both issuing warps
         if (i >= L::EMPTY && i < L::EMPTY + NS) n = 2;
-        if (i == L::Q_FULL && F8) n = 8;                           // each softmax warp widens its share of the queries
+        if (i == L::Q_FULL && F8) n = kSoftmaxWarps;               // each widens its share of the queries
         if (i >= L::FULL && i < L::FULL + NS) n = kSplit;
         mbar_init(&bar[i], n);
         fence_mbarrier_init();
@@ -329,7 +335,13 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
     // ---- this CTA's slice of the stream, and the window in which it begins ----
     Walker w0;
     int f0, f1, share;
-    {
+    if (a.batch <= 32) {
+        w0.incl = inclusive_sum(sequence<G>(a, lane, w0, blockIdx.x == 0 && warp == 0), lane);
+        w0.tot = __shfl_sync(kFull, w0.incl, 31);
+        share = max(kMinShare, (w0.tot + (int)gridDim.x - 1) / (int)gridDim.x);
+        f0 = min((int64_t)w0.tot, (int64_t)blockIdx.x * share);
+        f1 = min((int64_t)w0.tot, (int64_t)f0 + share);
+    } else {
         int *win = reinterpret_cast<int *>(sm + L::kRing);  // steps of each window of 32 sequences
         const int windows = (a.batch + 31) / 32;
         for (int i = warp; i < windows; i += kWarps) {
@@ -356,15 +368,13 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncthreads();  // the ring is free for the copies
+        load_window<G>(w0, a, lane);
     }
-    Walker wk;
-    wk.wb = w0.wb;
-    wk.wbase = w0.wbase;
-    load_window<G>(wk, a, lane);
+    Walker &wk = w0;
     const uint32_t base = smem_u32(sm);
 
     if (warp >= kCopyWarp) {
-        if constexpr (F8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Wp::kWorkRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Wp::kWorkRegs));
         if (warp == kCopyWarp) {
             // ---------------------------------------------------------- copies
             const uint64_t policy = l2_policy_evict_normal();
@@ -451,10 +461,12 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
             for (int f = f0; ok && find_piece<G>(wk, a, f, f1, p, lane); f += p.n) {
                 if (*abort_flag) break;
                 if (!(ok = wait_all(&bar[L::Q_FULL], n & 1))) break;
-                const bool two = p.two();
+                // (the same in all lanes, and known to be: an MMA whose operands are not takes 80 cycles to issue)
+                const bool two = __shfl_sync(kFull, (int)p.two(), 0);
+                const int steps = __shfl_sync(kFull, p.n, 0);
                 const uint64_t qd = smem_desc(base + L::kQ + (two ? x * L::QT : 0), 16, 1024);
                 bool q_held = true;
-                for (int s = 0; s < p.n; ++s, u += 2) {
+                for (int s = 0; s < steps; ++s, u += 2) {
                     const int ks = u % NS, vs = (u + 1) % NS;
                     if (!two && (s & 1) != x) {  // the other stream's: only say that it is not needed here (any more)
                         if (!(ok = full(u) && full(u + 1))) break;
@@ -478,7 +490,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                     }
                     umma_commit_if(go, &bar[L::S_FULL + x]);
                     umma_commit_if(go, &bar[L::EMPTY + ks]);
-                    if (s + (two ? 1 : 2) >= p.n) {  // the piece's last scores
+                    if (s + (two ? 1 : 2) >= steps) {  // the piece's last scores
                         umma_commit_if(go, &bar[L::Q_FREE]);
                         q_held = false;
                     }
@@ -548,10 +560,11 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
         }
     } else {
         // ---------------------------------------------------------- softmax
-        if constexpr (F8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Wp::kScoreRegs));
-        const int x = warp >> 2, quarter = warp & 3;  // stream; TMEM lanes 32 quarter ..
-        const int row = quarter * 32 + lane;
-        const uint32_t ts = tmem + ((uint32_t)(quarter * 32) << 16);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Wp::kScoreRegs));
+        const int x = warp >> 3, w8 = warp & 7;            // stream, warp of it
+        const int row0 = (w8 & 3) * 32 + (w8 >> 2) * 16;   // its rows (TMEM lanes) row0 .. + 15
+        const int g8 = lane >> 2, c4 = lane & 3;           // this thread's rows row0 + g8, + 8; its pair of every 8 columns
+        const uint32_t ts = tmem + ((uint32_t)row0 << 16);
         float2 *stat = reinterpret_cast<float2 *>(sm + L::kStat);
         const bool rising = a.qscale >= 0.0f;  // else scores are negated as they are read
         int turns = 0, n = 0, joins = 0;       // this stream's steps, pieces, units of one tile
@@ -562,7 +575,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
             const bool two = p.two();
             if constexpr (F8) {  // the queries to f16 in place, element by element: this warp's share
                 if (!(ok = wait_all(&bar[L::Q_RAW], n & 1))) break;
-                const uint32_t part = (two ? 2 : 1) * L::QT / 8;
+                const uint32_t part = (two ? 2 : 1) * L::QT / kSoftmaxWarps;
 #pragma unroll 4
                 for (uint32_t off = warp * part + 16u * lane; off < (warp + 1) * part; off += 16u * 32) {
                     uint4 v = lds128(base + off);
@@ -579,20 +592,18 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                 if (lane == 0) mbar_arrive(&bar[L::Q_FULL]);
             }
             ++n;
-            const int t0 = p.r0 + (two ? x * kRows : 0);  // the tile's first local row
-            const int r = t0 + row;
-            const bool live = t0 + quarter * 32 < p.R;    // some row of this warp is
-            const int node = min(r, p.R - 1) / G;
-            const uint32_t *mrow = a.mask + ((int64_t)p.row0 + node) * 2 * a.words;
-            const int before = p.C - p.T;                 // positions before the nodes
+            const int t0 = p.r0 + (two ? x * kRows : 0) + row0;  // the warp's first local row
+            const bool live = t0 < p.R;
+            const int before = p.C - p.T;                        // positions before the nodes
             const float qs = fabsf(a.qscale) * (F8 ? a.scales[p.g] : 1.0f);
             const int32_t *trow = a.block_tables + (int64_t)p.b * a.W;
             const int hop = two ? 1 : 2, s1 = two ? 0 : x;
+            auto node = [&](int i) -> int { return min(t0 + g8 + 8 * i, p.R - 1) / G; };  // of this thread's row i
             auto ids_of = [&](int s) -> int {
                 const int nb = (p.s0 + s) * kStepBlocks + lane;
                 return lane < kStepBlocks && s < p.n && nb < p.n_blocks ? trow[nb] : -1;
             };
-            float mref = -INFINITY, l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // of the rows; sums of this thread's keys
             int nxt = ids_of(s1);
             for (int s = s1; s < p.n; s += hop, ++turns) {
                 // blocks that are there, as the copies decided
@@ -601,76 +612,109 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                 if (!(ok = wait_all(&bar[L::S_FULL + x], turns & 1))) break;
                 if (live) {
                     tc_fence_after();
-                    uint32_t sr[kKeys];
+                    uint32_t pk[kKeys / 4];  // words 2 n + i: row i's weights of keys 8 n + 2 c4, + 1
+                    float add[2], alpha[2] = {1.0f, 1.0f};
+                    // Weights are formed with the reference as it is, while the maximum is found; the rare step that
+                    // raises it reads the scores again.  (A piece's first one finds the maximum first.)
+                    bool fresh = s == s1, again = false;
+                    do {
+                        uint32_t sr[kKeys / 2];  // words 4 n + 2 i + e: row i's key 8 n + 2 c4 + e
+                        tmem_ld_rows64(ts + x * kKeys, sr);
+                        tmem_ld_rows64(ts + x * kKeys + 64, sr + 32);
+                        tmem_wait_ld();
+                        if (!rising) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(ts + x * kKeys + 32 * c, sr + 32 * c);
-                    tmem_wait_ld();
-                    if (!rising) {
-#pragma unroll
-                        for (int i = 0; i < kKeys; ++i) sr[i] ^= 0x80000000u;
-                    }
-                    const int key0 = (p.s0 + s) * kKeys;
-                    if (key0 + kKeys > before || valid != (1u << kStepBlocks) - 1) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t bits = node_bits(mrow, 2 * a.words, p.T, key0 + 32 * c - before);
-                            if (!((valid >> (2 * c)) & 1u)) bits &= 0xffff0000u;
-                            if (!((valid >> (2 * c)) & 2u)) bits &= 0xffffu;
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (!((bits >> k) & 1u)) sr[32 * c + k] = 0xff800000u;
+                            for (int i = 0; i < kKeys / 2; ++i) sr[i] ^= 0x80000000u;
                         }
-                    }
-                    auto e = [&](int i) { return __uint_as_float(sr[i]); };
-                    float mx[8];
+                        const int key0 = (p.s0 + s) * kKeys;
+                        if (key0 + kKeys > before || valid != (1u << kStepBlocks) - 1) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        mx[j] = fmax3(e(j), e(j + 8), e(j + 16));
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t *mrow = a.mask + ((int64_t)p.row0 + node(i)) * 2 * a.words;
 #pragma unroll
-                        for (int i = 3; i < 15; i += 2) mx[j] = fmax3(mx[j], e(j + 8 * i), e(j + 8 * i + 8));
-                        mx[j] = fmaxf(mx[j], e(j + 120));
-                    }
-                    const float top = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * qs;
-                    const bool raise = top > mref + kSlack;
-                    float alpha = 1.0f;
-                    if (raise) {
-                        alpha = ex2(mref - top);  // 0 when mref is -inf
-                        mref = top;
+                                for (int c = 0; c < 4; ++c) {
+                                    uint32_t bits = node_bits(mrow, 2 * a.words, p.T, key0 + 32 * c - before);
+                                    if (!((valid >> (2 * c)) & 1u)) bits &= 0xffff0000u;
+                                    if (!((valid >> (2 * c)) & 2u)) bits &= 0xffffu;
+                                    bits >>= 2 * c4;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) l4[i] *= alpha;
-                    }
-                    const float nm = mref == -INFINITY ? 0.0f : -mref;
-                    uint32_t pk[kKeys / 2];
-#pragma unroll
-                    for (int i = 0; i < kKeys / 2; ++i) {
-                        const float2 d = ffma2(make_float2(e(2 * i), e(2 * i + 1)), make_float2(qs, qs), make_float2(nm, nm));
-                        if constexpr (F8) {
-                            pk[i] = pack_f16x2(ex2(d.x), ex2(d.y));
-                            add_f16x2_to(l4[i & 3], pk[i]);
-                        } else {
-                            pk[i] = pack_bf16x2(ex2(d.x), ex2(d.y));
-                            add_bf16x2_to(l4[i & 3], pk[i]);
+                                    for (int k = 0; k < 8; ++k)
+                                        if (!((bits >> (8 * (k >> 1) + (k & 1))) & 1u)) sr[16 * c + 4 * (k >> 1) + 2 * i + (k & 1)] = 0xff800000u;
+                                }
+                            }
                         }
-                    }
+                        auto e = [&](int i, int k) { return __uint_as_float(sr[4 * (k >> 1) + 2 * i + (k & 1)]); };  // row i's k-th key here
+                        float top[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float mx[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                mx[j] = fmaxf(fmax3(fmax3(fmax3(e(i, j), e(i, j + 4), e(i, j + 8)), e(i, j + 12), e(i, j + 16)), e(i, j + 20),
+                                                    e(i, j + 24)), e(i, j + 28));
+                            top[i] = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+                        }
+                        auto reduce = [&]() {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                top[i] = fmaxf(top[i], __shfl_xor_sync(kFull, top[i], 1));
+                                top[i] = fmaxf(top[i], __shfl_xor_sync(kFull, top[i], 2)) * qs;
+                            }
+                        };
+                        if (fresh) {
+                            reduce();
+                            m[0] = top[0];
+                            m[1] = top[1];
+                        }
+                        const float nm[2] = {m[0] == -INFINITY ? 0.0f : -m[0], m[1] == -INFINITY ? 0.0f : -m[1]};
+                        float2 part[2][2] = {};
+#pragma unroll
+                        for (int j = 0; j < kKeys / 8; ++j) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const float2 d = ffma2(make_float2(e(i, 2 * j), e(i, 2 * j + 1)), make_float2(qs, qs), make_float2(nm[i], nm[i]));
+                                const float2 w = make_float2(ex2(d.x), ex2(d.y));
+                                part[i][j & 1] = fadd2(part[i][j & 1], w);
+                                pk[2 * j + i] = F8 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float2 y = fadd2(part[i][0], part[i][1]);
+                            add[i] = y.x + y.y;
+                        }
+                        if (fresh || again) break;
+                        reduce();
+                        const bool up0 = top[0] > m[0] + kSlack, up1 = top[1] > m[1] + kSlack;
+                        again = __any_sync(kFull, up0 || up1);
+                        if (again) {  // 2^(-inf) = 0 where there was no maximum yet
+                            alpha[0] = up0 ? ex2(m[0] - top[0]) : 1.0f;
+                            alpha[1] = up1 ? ex2(m[1] - top[1]) : 1.0f;
+                            if (up0) m[0] = top[0];
+                            if (up1) m[1] = top[1];
+                        }
+                    } while (again);
+                    l[0] = fmaf(l[0], alpha[0], add[0]);
+                    l[1] = fmaf(l[1], alpha[1], add[1]);
                     // (the scores were issued after the last product had run, so O is final)
-                    if (s != s1 && __any_sync(kFull, raise)) {
+                    if (again) {
 #pragma unroll
                         for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(ts + kColO + x * D + c, o);
+                            uint32_t o[16];
+                            tmem_ld_rows32(ts + kColO + x * D + c, o);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                            tmem_st32(ts + kColO + x * D + c, o);
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[(i >> 1) & 1]);
+                            tmem_st_rows32(ts + kColO + x * D + c, o);
                         }
                     }
                     // the weights over the scores, which are read
-                    tmem_st32(ts + x * kKeys, pk);
-                    tmem_st32(ts + x * kKeys + 32, pk + 32);
+                    tmem_st_pairs32(ts + x * kKeys, pk);
+                    tmem_st_pairs32(ts + x * kKeys + 32, pk + 16);
                     tmem_wait_st();
                 }
                 // stream 1: its O of the last unit of one tile is read
-                if (x == 1 && s == s1 && joins > 0 && !(ok = wait_all(&bar[L::TAKEN + quarter], (joins - 1) & 1))) break;
+                if (x == 1 && s == s1 && joins > 0 && !(ok = wait_all(&bar[L::TAKEN + w8], (joins - 1) & 1))) break;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[L::P_FULL + x]);
@@ -680,75 +724,83 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
             const bool any = s1 < p.n;  // this stream had steps
             if (any && !(ok = wait_all(&bar[L::PV_DONE + x], (turns - 1) & 1))) break;
             tc_fence_after();
-            float l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
-            float fa = 1.0f, fb = 0.0f;  // O = fa O_x + fb O_1
+            float sum[2], fa[2], fb[2];  // O = fa O_x + fb O_1
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                sum[i] = l[i];
+                sum[i] += __shfl_xor_sync(kFull, sum[i], 1);
+                sum[i] += __shfl_xor_sync(kFull, sum[i], 2);
+                fa[i] = 1.0f;
+                fb[i] = 0.0f;
+            }
             if (!two) {
                 if (x == 1) {
-                    if (joins > 0 && !any && !(ok = wait_all(&bar[L::TAKEN + quarter], (joins - 1) & 1))) break;
-                    stat[row] = make_float2(mref, l);
+                    if (joins > 0 && !any && !(ok = wait_all(&bar[L::TAKEN + w8], (joins - 1) & 1))) break;
+                    if (c4 == 0) {
+                        stat[row0 + g8] = make_float2(m[0], sum[0]);
+                        stat[row0 + g8 + 8] = make_float2(m[1], sum[1]);
+                    }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar[L::STAT + quarter]);
+                    if (lane == 0) mbar_arrive(&bar[L::STAT + w8]);
                     ++joins;
                     continue;
                 }
-                if (!(ok = wait_all(&bar[L::STAT + quarter], joins & 1))) break;
+                if (!(ok = wait_all(&bar[L::STAT + w8], joins & 1))) break;
                 ++joins;
                 tc_fence_after();
-                const float2 y = stat[row];
-                const float top = fmaxf(mref, y.x);
-                fa = mref == -INFINITY ? 0.0f : ex2(mref - top);
-                fb = y.x == -INFINITY ? 0.0f : ex2(y.x - top);
-                l = l * fa + y.y * fb;
-                mref = top;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 y = stat[row0 + g8 + 8 * i];
+                    const float top = fmaxf(m[i], y.x);
+                    fa[i] = m[i] == -INFINITY ? 0.0f : ex2(m[i] - top);
+                    fb[i] = y.x == -INFINITY ? 0.0f : ex2(y.x - top);
+                    sum[i] = sum[i] * fa[i] + y.y * fb[i];
+                    m[i] = top;
+                }
             }
-            const float vs = F8 ? a.scales[a.n_kv + p.g] : 1.0f;
-            const bool join = !two && p.n > 1;
-            const float norm = p.whole() ? (l > 0.0f ? vs / l : l == 0.0f ? 0.0f : l) : vs;
-            fa *= norm;
-            fb *= norm;
-            const int slot = 2 * (int)blockIdx.x + (p.s0 == 0 ? 1 : 0);
-            const int64_t at = (int64_t)slot * a.slot_rows + (r - p.r0);
-            __nv_bfloat16 *dst = a.out + (((int64_t)p.row0 + node) * a.n_q + p.g * G + min(r, p.R - 1) % G) * D;
             if (live) {
+                const float vs = F8 ? a.scales[a.n_kv + p.g] : 1.0f;
+                const bool join = !two && p.n > 1, whole = p.whole();
+                const int slot = 2 * (int)blockIdx.x + (p.s0 == 0 ? 1 : 0);
+                bool in[2];
+                int64_t to[2];  // the row's place: in out, or in the slot
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float norm = whole ? (sum[i] > 0.0f ? vs / sum[i] : sum[i] == 0.0f ? 0.0f : sum[i]) : vs;
+                    fa[i] *= norm;
+                    fb[i] *= norm;
+                    const int r = t0 + g8 + 8 * i;
+                    in[i] = r < p.R;
+                    to[i] = whole ? (((int64_t)p.row0 + node(i)) * a.n_q + p.g * G + min(r, p.R - 1) % G) * D
+                                  : ((int64_t)slot * a.slot_rows + (r - p.r0)) * D;
+                    if (!whole && in[i] && c4 == 0) a.ws_ml[(int64_t)slot * a.slot_rows + (r - p.r0)] = make_float2(m[i], sum[i]);
+                }
 #pragma unroll
                 for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(ts + kColO + x * D + c, o);
-                    if (join) {
-                        uint32_t o1[32];
-                        tmem_ld32(ts + kColO + D + c, o1);
-                        tmem_wait_ld();
+                    uint32_t o[16], o1[16];
+                    tmem_ld_rows32(ts + kColO + x * D + c, o);
+                    if (join) tmem_ld_rows32(ts + kColO + D + c, o1);
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            o[i] = __float_as_uint(fa == 0.0f && fb == 0.0f ? 0.0f : fmaf(fb, __uint_as_float(o1[i]), fa * __uint_as_float(o[i])));
-                    } else {
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fa);
-                    }
-                    if (r < p.R) {
-                        if (p.whole()) {
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                uint32_t w[8];
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    w[i] = pack_bf16x2(__uint_as_float(o[16 * h + 2 * i]), __uint_as_float(o[16 * h + 2 * i + 1]));
-                                stg256(dst + c + 16 * h, w);
-                            }
-                        } else {
-#pragma unroll
-                            for (int h = 0; h < 4; ++h) stg256(a.ws_o + at * D + c + 8 * h, o + 8 * h);
+                    for (int j = 0; j < 8; ++j) {  // row i's columns c + 8 (j / 2) + 2 c4, + 1
+                        const int i = j & 1;
+                        float u = __uint_as_float(o[2 * j]) * fa[i], v = __uint_as_float(o[2 * j + 1]) * fa[i];
+                        if (join) {
+                            u = fmaf(fb[i], __uint_as_float(o1[2 * j]), u);
+                            v = fmaf(fb[i], __uint_as_float(o1[2 * j + 1]), v);
                         }
+                        if (!in[i]) continue;
+                        const int64_t at = to[i] + c + 8 * (j >> 1) + 2 * c4;
+                        if (whole) *reinterpret_cast<uint32_t *>(a.out + at) = pack_bf16x2(u, v);
+                        else *reinterpret_cast<float2 *>(a.ws_o + at) = make_float2(u, v);
                     }
                 }
-                if (!p.whole() && r < p.R) a.ws_ml[at] = make_float2(mref, l);
             }
             if (!two) {  // stream 1 may go on
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[L::TAKEN + quarter]);
+                if (lane == 0) mbar_arrive(&bar[L::TAKEN + w8]);
             }
         }
         if (!ok) set_abort();
@@ -786,27 +838,50 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __gr
     const int r = p.r0 + i;
     if (p.more < 0 || i >= kUnitRows || r >= p.R) return;
     auto at = [&](int k) -> int64_t { return (int64_t)(k == 0 ? 2 * c + 1 : 2 * (c + k)) * a.slot_rows + i; };
-    float M = -INFINITY;
-    for (int k = lane; k <= p.more; k += 32) M = fmaxf(M, a.ws_ml[at(k)].x);
+    // 32 parts at a time: a lane holds one's (m, l), and all of them read eight parts of O at once
+    float o[PL] = {}, l = 0.0f, M = -INFINITY;
+    for (int k0 = 0; k0 <= p.more; k0 += 32) {
+        const int n = min(32, p.more + 1 - k0);
+        const float2 y = lane < n ? a.ws_ml[at(k0 + lane)] : make_float2(-INFINITY, 0.0f);
+        constexpr int U = 8;
+        float z[U][PL];
+        auto load = [&](int k1) {
 #pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, s));
-    float o[PL] = {}, l = 0.0f;
-#pragma unroll 4
-    for (int k = 0; k <= p.more; ++k) {
-        const float2 y = a.ws_ml[at(k)];
-        const float f = y.x == -INFINITY ? 0.0f : exp2f(y.x - M);
-        l = fmaf(y.y, f, l);
-        const float *src = a.ws_o + at(k) * D + lane * PL;
-        float z[PL];
-        if constexpr (PL == 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(src);
-            z[0] = v.x; z[1] = v.y; z[2] = v.z; z[3] = v.w;
-        } else {
-            const float2 v = *reinterpret_cast<const float2 *>(src);
-            z[0] = v.x; z[1] = v.y;
+            for (int u = 0; u < U; ++u) {
+                if (k1 + u >= n) continue;
+                const float *src = a.ws_o + at(k0 + k1 + u) * D + lane * PL;
+                if constexpr (PL == 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(src);
+                    z[u][0] = v.x; z[u][1] = v.y; z[u][2] = v.z; z[u][3] = v.w;
+                } else {
+                    const float2 v = *reinterpret_cast<const float2 *>(src);
+                    z[u][0] = v.x; z[u][1] = v.y;
+                }
+            }
+        };
+        load(0);  // (does not wait for the statistics)
+        float top = y.x;
+#pragma unroll
+        for (int s = 16; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, s));
+        const float was = M;
+        M = fmaxf(M, top);
+        const float old = was == -INFINITY ? 0.0f : exp2f(was - M), f = y.x == -INFINITY ? 0.0f : exp2f(y.x - M);
+        float sum = y.y * f;
+#pragma unroll
+        for (int s = 16; s >= 1; s >>= 1) sum += __shfl_xor_sync(kFull, sum, s);
+        l = l * old + sum;
+#pragma unroll
+        for (int d = 0; d < PL; ++d) o[d] *= old;
+        for (int k1 = 0; k1 < n; k1 += U) {
+            if (k1) load(k1);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float w = __shfl_sync(kFull, f, (k1 + u) & 31);
+                if (k1 + u >= n) continue;
+#pragma unroll
+                for (int d = 0; d < PL; ++d) o[d] = fmaf(z[u][d], w, o[d]);
+            }
         }
-#pragma unroll
-        for (int d = 0; d < PL; ++d) o[d] = fmaf(z[d], f, o[d]);
     }
     const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
     __nv_bfloat16 *dst = a.out + (((int64_t)p.row0 + r / G) * a.n_q + p.g * G + r % G) * D + lane * PL;
@@ -848,7 +923,7 @@ pkv_status prepare(const pkv_pool *pool)
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kern);
     if (e != cudaSuccess) return cuda_fail(e, "paged_tree_attention: kernel attributes");
     // (with fewer registers at the launch, the softmax warps would wait for theirs)
-    if (F8 && fa.numRegs < Warps<F8>::kLaunchRegs)
+    if (fa.numRegs < Warps<F8>::kLaunchRegs)
         return fail(PKV_EUNSUPPORTED, "paged_tree_attention: built with %d registers a thread", fa.numRegs);
     if (pool->device < 64) ready[pool->device] = true;
     return PKV_OK;
