@@ -11,14 +11,16 @@
 // into slices so that every SM has work, leaves each slice's maximum, sum of
 // exponentials and k greatest logits; a merge of each search's lists.
 //
-// Selecting while scanning.  A slice is read in chunks of 1984 vectors of 16
-// bytes.  In its first chunk the threads' greatest logits, reduced to 4 k
-// groups or more, give a bar: the k-th greatest group maximum, at or above
-// which at least k logits are.  The logits that reach the bar belong to k
-// groups, so they fit the buffer whatever the data.  Later chunks seldom have
-// any: one barrier a chunk finds that out.  What would not fit raises the bar
-// first.  Keys (logit as an ordered integer, then the lower index) are unique,
-// so ties need no care and results do not depend on the order of arrival.
+// Selecting while scanning.  From a slice's first part (kVecs vectors of 16
+// bytes per thread) the threads' greatest logits, reduced to 4 k groups or more,
+// give a bar: the k-th greatest group maximum, which at least k logits reach.
+// Those that do belong to k groups, so they fit the buffer whatever the data.
+// The warps then read the rest each for itself, without barriers, and add what
+// is above the bar: k (n / n_1 - 1) logits where they come in any order.  Only
+// where they rise along the row can the buffer run over; the slice is then read
+// again in parts, each of which raises the bar first.  Keys (logit as an ordered
+// integer, then the lower index) are unique, so ties need no care and results do
+// not depend on the order of arrival.
 //
 // A row may begin anywhere.  Which thread adds which logits must not depend on
 // that, or two beams with equal logits would get sums that differ in the last
@@ -36,17 +38,18 @@
 #include <climits>
 #include <math.h>
 
-#include "pkv_internal.cuh"
+#include "tcgen05.cuh"
 
 namespace pkv {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kVecs = 4;                         // 16-byte vectors of a thread and chunk
+constexpr int kWarps = kThreads / 32;
+constexpr int kVecs = 4;                         // 16-byte vectors of a thread in a part
 constexpr int kLanes = 31;                       // lanes of a warp that have logits
-constexpr int kChunkVecs = kThreads / 32 * kLanes * kVecs;
+constexpr int kRunVecs = kWarps * kLanes;        // a vector each: the unit in which rows are cut
 constexpr int kMaxK = 64, kMaxBeams = 64;
-constexpr int kCap = 5120;                       // keys the buffer holds: a chunk's 4096 at most, k kept ones, some more
+constexpr int kCap = 5120;                       // keys the buffer holds: a part's 4096 at most, k kept ones, some more
 constexpr int kMaxLists = 1024;                  // (beam, slice) lists of a search
 constexpr int kMergeThreads = 256;
 constexpr int kMergeKeys = 4096;                 // keys of a search that the merge holds in shared memory
@@ -104,20 +107,13 @@ struct Elems<float> {
     }
 };
 
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 struct Shared {
     uint64_t buf[kCap];
     uint64_t group[256];
     uint64_t bar;      // keys below it are not among the k greatest
-    uint64_t sums[kThreads / 32];
-    float tops[kThreads / 32];
-    int n;             // keys in buf
+    uint64_t sums[kWarps];
+    float tops[kWarps];
+    int n;             // keys in buf (those past kCap are not there)
 };
 
 __device__ __forceinline__ uint64_t max64(uint64_t a, uint64_t b) { return a > b ? a : b; }
@@ -132,7 +128,7 @@ __device__ __forceinline__ void raise_bar(Shared &sh, uint64_t mine, int k, int 
     for (int o = size / 2; o >= 1; o >>= 1) mine = max64(mine, __shfl_xor_sync(kFull, mine, o));
     if (lane % size == 0) sh.group[warp * p + lane / size] = mine;
     __syncthreads();
-    const int groups = (kThreads / 32) * p;
+    const int groups = kWarps * p;
     if (tid < groups) {
         const uint64_t x = sh.group[tid];
         int rank = 0;
@@ -170,173 +166,234 @@ __device__ __forceinline__ int thin_out(Shared &sh, int n, int k, int p, int mos
     return n;
 }
 
+// A row of logits, as one warp reads it: run r is kLanes vectors of every warp, a vector a lane.
+template <typename T>
+struct Row {
+    using El = Elems<T>;
+    static constexpr int N = El::N;
+    const T *x;
+    int vocab, lead;  // elements before the row in its first aligned vector
+    int lane, warp;
+
+    // index of this lane's first element of run r
+    __device__ __forceinline__ int first(int r) const { return ((r * kWarps + warp) * kLanes + lane) * N; }
+    // the aligned vector in which it is
+    __device__ __forceinline__ uint4 load(int r) const
+    {
+        const int i = first(r) - lead;
+        if (i >= 0 && i <= vocab - N) return ldg_nc_v4(x + i);
+        uint32_t w[4] = {El::kLow, El::kLow, El::kLow, El::kLow};  // the row's ends
+        if (i > -N && i < vocab) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                if (i + e < 0 || i + e >= vocab) continue;
+                if constexpr (N == 4) {
+                    w[e] = __float_as_uint(x[i + e]);
+                } else {
+                    const uint32_t h = __bfloat16_as_ushort(x[i + e]);
+                    w[e / 2] = e % 2 ? (w[e / 2] & 0xffffu) | (h << 16) : (w[e / 2] & 0xffff0000u) | h;
+                }
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // this lane's elements, from its vector and the next lane's
+    __device__ __forceinline__ uint4 line_up(const uint4 &r) const
+    {
+        uint32_t w[8] = {r.x, r.y, r.z, r.w};
+        if (lead) {
+            const int words = lead * (int)sizeof(T) / 4;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[4 + i] = __shfl_down_sync(kFull, w[i], 1);
+            if (words & 2) {
+#pragma unroll
+                for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+            }
+            if (words & 1) {
+#pragma unroll
+                for (int i = 0; i < 7; ++i) w[i] = w[i + 1];
+            }
+            if (N == 8 && (lead & 1)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+            }
+        }
+        const bool on = lane < kLanes;
+        return make_uint4(on ? w[0] : El::kLow, on ? w[1] : El::kLow, on ? w[2] : El::kLow, on ? w[3] : El::kLow);
+    }
+};
+
+// The greatest of a vector's logits; a NaN is passed over.
+template <typename T>
+__device__ __forceinline__ float greatest_of(const uint4 &v)
+{
+    if constexpr (sizeof(T) == 2) {
+        auto h = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); };
+        const __nv_bfloat162 m = __hmax2(__hmax2(h(v.x), h(v.y)), __hmax2(h(v.z), h(v.w)));
+        return fmaxf(__low2float(m), __high2float(m));
+    } else {
+        return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+    }
+}
+
+// A thread's greatest logit so far and the sum of exp(x - m).
+struct Sum {
+    float m = -INFINITY, s = 0.0f;
+    // kVecs vectors with the greatest logit top
+    template <typename T>
+    __device__ __forceinline__ void add(const uint4 (&v)[kVecs], float top)
+    {
+        constexpr int N = Elems<T>::N;
+        if (top > m) {
+            s = m == -INFINITY ? s : s * ex2((m - top) * kLog2e);
+            m = top;
+        }
+        // (of x - m, not of x log2(e) - m log2(e), whose second product's rounding would be in every term alike)
+        const float neg = m == -INFINITY ? 0.0f : -m;
+        float2 part = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            float x[N];
+            Elems<T>::widen(v[i], x);
+#pragma unroll
+            for (int e = 0; e < N; e += 2) {
+                const float2 d = fmul2(fadd2(make_float2(x[e], x[e + 1]), make_float2(neg, neg)), make_float2(kLog2e, kLog2e));
+                part = fadd2(part, make_float2(ex2(d.x), ex2(d.y)));
+            }
+        }
+        s += part.x + part.y;
+    }
+};
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) beam_scan_kernel(const __grid_constant__ ScanArgs a)
 {
     using El = Elems<T>;
-    constexpr int N = El::N, kChunk = kChunkVecs * N;
+    constexpr int N = El::N;
     __shared__ Shared sh;
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int slice = blockIdx.x;
     const int64_t row = (int64_t)blockIdx.y * gridDim.z + blockIdx.z;  // (search, beam)
-    const T *x0 = static_cast<const T *>(a.logits) + row * a.stride;
-    const int lead = (int)(((uintptr_t)x0 & 15u) / sizeof(T));  // elements before the row in its first vector
-    const int chunks = (a.vocab + kChunk - 1) / kChunk;
-    const int c0 = (int)((int64_t)chunks * slice / a.slices), c1 = (int)((int64_t)chunks * (slice + 1) / a.slices);
+    Row<T> rw;
+    rw.x = static_cast<const T *>(a.logits) + row * a.stride;
+    rw.vocab = a.vocab;
+    rw.lead = (int)(((uintptr_t)rw.x & 15u) / sizeof(T));
+    rw.lane = lane;
+    rw.warp = warp;
+    const int runs = (a.vocab + kRunVecs * N - 1) / (kRunVecs * N);
+    const int r0 = (int)((int64_t)runs * slice / a.slices), r1 = (int)((int64_t)runs * (slice + 1) / a.slices);
     const int k = a.k;
     const int p = k <= 4 ? 1 : k <= 8 ? 2 : k <= 16 ? 4 : k <= 32 ? 8 : 16;  // groups of a warp
     if (tid == 0) {
         sh.n = 0;
         sh.bar = 0;
     }
-    // index in the row of this lane's first element of vector v of chunk c
-    auto first = [&](int c, int v) -> int { return (((c * kVecs + v) * (kThreads / 32) + warp) * kLanes + lane) * N; };
-    auto load = [&](int c, uint4 (&r)[kVecs]) {  // the aligned vectors in which they are
+    const uint4 none = make_uint4(El::kLow, El::kLow, El::kLow, El::kLow);
+    auto load = [&](int r, uint4 (&v)[kVecs]) {
 #pragma unroll
-        for (int v = 0; v < kVecs; ++v) {
-            const int i = first(c, v) - lead;
-            if (i >= 0 && i <= a.vocab - N) {
-                r[v] = ldg_nc_v4(x0 + i);
-            } else {  // the row's ends
-                uint32_t w[4] = {El::kLow, El::kLow, El::kLow, El::kLow};
-                if (i > -N && i < a.vocab) {
+        for (int i = 0; i < kVecs; ++i) v[i] = r + i < r1 ? rw.load(r + i) : none;
+    };
+    auto line_up = [&](uint4 (&v)[kVecs]) {
 #pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        if (i + e < 0 || i + e >= a.vocab) continue;
-                        if constexpr (N == 4) {
-                            w[e] = __float_as_uint(x0[i + e]);
-                        } else {
-                            const uint32_t h = __bfloat16_as_ushort(x0[i + e]);
-                            w[e / 2] = e % 2 ? (w[e / 2] & 0xffffu) | (h << 16) : (w[e / 2] & 0xffff0000u) | h;
-                        }
-                    }
-                }
-                r[v] = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < kVecs; ++i) v[i] = rw.line_up(v[i]);
+    };
+    auto greatest = [&](const uint4 (&v)[kVecs]) -> float {
+        static_assert(kVecs == 4, "");
+        return fmaxf(fmaxf(greatest_of<T>(v[0]), greatest_of<T>(v[1])), fmaxf(greatest_of<T>(v[2]), greatest_of<T>(v[3])));
+    };
+    // the key of a thread's greatest logit: of equal ones the first
+    auto key_at = [&](const uint4 (&v)[kVecs], int r, float top) -> uint64_t {
+        if (!(top > -INFINITY)) return 0;
+        int at = 0;
+#pragma unroll
+        for (int i = kVecs - 1; i >= 0; --i) {
+            float x[N];
+            El::widen(v[i], x);
+#pragma unroll
+            for (int e = N - 1; e >= 0; --e) at = x[e] == top ? i * (kRunVecs * N) + e : at;
+        }
+        return key_of(top, rw.first(r) + at);
+    };
+    // adds this thread's logits that reach the bar to the buffer
+    auto add_keys = [&](const uint4 (&v)[kVecs], int r, uint64_t bar) {
+#pragma unroll 1
+        for (int i = 0; i < kVecs; ++i) {
+            const uint4 w = i == 0 ? v[0] : i == 1 ? v[1] : i == 2 ? v[2] : v[3];
+            const float top = greatest_of<T>(w);
+            if (!(top > -INFINITY) || (bar && top < logit_of(bar))) continue;
+            float x[N];
+            El::widen(w, x);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                if (!(x[e] > -INFINITY)) continue;
+                const uint64_t key = key_of(x[e], rw.first(r + i) + e);
+                if (key < bar) continue;
+                const int at = atomicAdd(&sh.n, 1);
+                if (at < kCap) sh.buf[at] = key;
             }
         }
     };
-    // this lane's elements, from its vector and the next lane's
-    auto line_up = [&](uint4 (&r)[kVecs]) {
-        if (lead) {
-            const int words = lead * (int)sizeof(T) / 4;
-#pragma unroll
-            for (int v = 0; v < kVecs; ++v) {
-                uint32_t w[8] = {r[v].x, r[v].y, r[v].z, r[v].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[4 + i] = __shfl_down_sync(kFull, w[i], 1);
-                if (words & 2) {
-#pragma unroll
-                    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-                }
-                if (words & 1) {
-#pragma unroll
-                    for (int i = 0; i < 7; ++i) w[i] = w[i + 1];
-                }
-                if (N == 8 && (lead & 1)) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-                }
-                r[v] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
-        if (lane == kLanes) {
-#pragma unroll
-            for (int v = 0; v < kVecs; ++v) r[v] = make_uint4(El::kLow, El::kLow, El::kLow, El::kLow);
-        }
-    };
-    float m = -INFINITY, s = 0.0f;
+    Sum sum;
     uint4 cur[kVecs], nxt[kVecs];
-    if (c0 < c1) load(c0, cur);
-    __syncthreads();
-    for (int c = c0; c < c1; ++c) {
-        if (c + 1 < c1) load(c + 1, nxt);
+    load(r0, cur);
+    load(r0 + kVecs, nxt);
+    line_up(cur);
+    float top = greatest(cur);
+    __syncthreads();  // (the bar and the count are set)
+    raise_bar(sh, key_at(cur, r0, top), k, p);
+    uint64_t bar = sh.bar;
+    add_keys(cur, r0, bar);
+    sum.add<T>(cur, top);
+    // ---- the rest of the slice, every warp for itself ----
+    const float high = bar ? logit_of(bar) : -INFINITY;
+    for (int r = r0 + kVecs; r < r1; r += kVecs) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) cur[i] = nxt[i];
+        load(r + kVecs, nxt);
         line_up(cur);
-        float mv[kVecs];  // the vectors' greatest logits
-#pragma unroll
-        for (int v = 0; v < kVecs; ++v) {
-            float x[N];
-            El::widen(cur[v], x);
-            mv[v] = x[0];
-#pragma unroll
-            for (int e = 1; e < N; ++e) mv[v] = fmaxf(mv[v], x[e]);
-        }
-        const float mc = fmaxf(fmaxf(mv[0], mv[1]), fmaxf(mv[2], mv[3]));
-        if (mc > m) {
-            s = m == -INFINITY ? s : s * ex2((m - mc) * kLog2e);
-            m = mc;
-        }
-        const float ref = m == -INFINITY ? 0.0f : m;
-        float part[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int v = 0; v < kVecs; ++v) {
-            float x[N];
-            El::widen(cur[v], x);
-#pragma unroll
-            for (int e = 0; e < N; ++e) part[e & 1] += ex2((x[e] - ref) * kLog2e);
-        }
-        s += part[0] + part[1];
-        // ---- candidates ----
-        // the k-th greatest key of this chunk's groups, where no bar is known yet or too many reach it
-        auto greatest = [&]() -> uint64_t {
-            uint64_t best = 0;
-#pragma unroll
-            for (int v = 0; v < kVecs; ++v) {
-                float x[N];
-                El::widen(cur[v], x);
-#pragma unroll
-                for (int e = 0; e < N; ++e)
-                    if (x[e] > -INFINITY) best = max64(best, key_of(x[e], first(c, v) + e));
-            }
-            return best;
-        };
-        const uint64_t old = sh.bar;
-        const int have = sh.n;
-        const bool reach = mc > -INFINITY && (old == 0 || mc >= logit_of(old));
-        const int hits = __syncthreads_count(reach);
-        if (hits) {
-            const bool many = hits * kVecs * N > kCap - kMaxK;
-            if (many) raise_bar(sh, greatest(), k, p);
-            if (have + (many ? 4096 : hits * kVecs * N) > kCap) thin_out(sh, have, k, p, kMaxK);
-            const uint64_t bar = sh.bar;
-            if (reach && (bar == 0 || mc >= logit_of(bar))) {
-#pragma unroll
-                for (int v = 0; v < kVecs; ++v) {
-                    if (!(mv[v] > -INFINITY) || (bar && mv[v] < logit_of(bar))) continue;
-                    float x[N];
-                    El::widen(cur[v], x);
-#pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        if (!(x[e] > -INFINITY)) continue;
-                        const uint64_t key = key_of(x[e], first(c, v) + e);
-                        if (key >= bar) sh.buf[atomicAdd(&sh.n, 1)] = key;
-                    }
-                }
-            }
-            __syncthreads();
-        }
-#pragma unroll
-        for (int v = 0; v < kVecs; ++v) cur[v] = nxt[v];
+        top = greatest(cur);
+        if (top > high) add_keys(cur, r, bar);  // (an equal one has a greater index than the bar's)
+        sum.add<T>(cur, top);
     }
     // ---- the slice's maximum and sum ----
-    float M = m;
+    float M = sum.m;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
     if (lane == 0) sh.tops[warp] = M;
-    const bool bad = __syncthreads_or(!(s < INFINITY));  // (the sum of a NaN or an infinite logit is NaN)
+    const bool bad = __syncthreads_or(!(sum.s < INFINITY));  // (the sum of a NaN or an infinite logit is NaN)
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) M = fmaxf(M, sh.tops[w]);
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sh.tops[w]);
     uint64_t f = 0;  // this thread's sum in units of 2^-40
-    if (!bad && m > -INFINITY) f = __float2ull_rn(s * ex2((m - M) * kLog2e) * 0x1p40f);
+    if (!bad && sum.m > -INFINITY) f = __float2ull_rn(sum.s * ex2((sum.m - M) * kLog2e) * 0x1p40f);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) f += __shfl_xor_sync(kFull, f, o);
     if (lane == 0) sh.sums[warp] = f;
-    const int n = thin_out(sh, sh.n, k, p, 256);  // (no keys are added any more)
+    int n = sh.n;  // (no keys are added any more)
     __syncthreads();
+    if (n > kCap) {  // the buffer ran over: the slice again, part by part
+        if (tid == 0) {
+            sh.n = 0;
+            sh.bar = 0;
+        }
+        __syncthreads();
+        for (int r = r0; r < r1; r += kVecs) {
+            const int have = sh.n;
+            load(r, cur);
+            line_up(cur);
+            raise_bar(sh, key_at(cur, r, greatest(cur)), k, p);
+            if (have + 4096 > kCap) thin_out(sh, have, k, p, kMaxK);
+            add_keys(cur, r, sh.bar);
+            __syncthreads();
+        }
+        n = sh.n;
+        __syncthreads();
+    }
+    n = thin_out(sh, n, k, p, 256);
     const int64_t list = row * a.slices + slice;
     if (tid == 0) {
-        for (int w = 1; w < kThreads / 32; ++w) f += sh.sums[w];
+        for (int w = 1; w < kWarps; ++w) f += sh.sums[w];
         a.top[list] = M;
         a.sum[list] = bad ? (double)NAN : (double)f * 0x1p-40;
     }
@@ -413,21 +470,26 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
     if (hold)
         for (int i = tid; i < total; i += kMergeThreads) held[i] = keys[i];
     for (int i = tid; i < lists; i += kMergeThreads) at[i] = 0;
-    if (tid < a.beams) {
-        const int64_t l0 = (item * a.beams + tid) * a.slices;
+    for (int j = warp; j < a.beams; j += kMergeThreads / 32) {  // a warp a beam, a lane a slice
+        const int64_t l0 = (item * a.beams + j) * a.slices;
         float M = -INFINITY;
-        for (int i = 0; i < a.slices; ++i) M = fmaxf(M, a.top[l0 + i]);
+        for (int i = lane; i < a.slices; i += 32) M = fmaxf(M, a.top[l0 + i]);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
         double s = 0.0;
-        for (int i = 0; i < a.slices; ++i) {
+        for (int i = lane; i < a.slices; i += 32) {
             const float t = a.top[l0 + i];
             const double x = a.sum[l0 + i];  // (of an infinite maximum NaN)
             s += t == M || x != x ? x : t == -INFINITY ? 0.0 : x * exp((double)t - (double)M);
         }
-        const float sc = a.scores[item * a.beams + tid];
+        for (int o = 16; o >= 1; o >>= 1)
+            if (o < a.slices) s += __shfl_xor_sync(kFull, s, o);  // (lanes past the slices hold 0)
+        if (lane) continue;
+        const float sc = a.scores[item * a.beams + j];
         const bool odd = sc != -INFINITY && (s != s || sc != sc || sc == INFINITY);
         if (odd) atomicOr(a.err, PKV_DEVERR_NAN);
-        shift[tid] = odd || sc == -INFINITY || M == -INFINITY ? (double)NAN : (double)sc - log(s);
-        highest[tid] = M;
+        shift[j] = odd || sc == -INFINITY || M == -INFINITY ? (double)NAN : (double)sc - log(s);
+        highest[j] = M;
     }
     __syncthreads();
     constexpr Best kNone = {0, 0, INT_MAX};
@@ -479,13 +541,13 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
     }
 }
 
-// Slices of a row: enough for two blocks on every SM, no more than the row has chunks, nor than the merge takes.
+// Slices of a row: enough for two blocks on every SM, no more than the row has parts, nor than the merge takes.
 int slices_of(const pkv_pool *pool, int64_t rows, int beams, int vocab, int elem)
 {
-    const int64_t chunk = (int64_t)kChunkVecs * (16 / elem);
-    const int64_t chunks = (vocab + chunk - 1) / chunk;
+    const int64_t part = (int64_t)kRunVecs * kVecs * (16 / elem);
+    const int64_t parts = (vocab + part - 1) / part;
     const int64_t want = std::max<int64_t>(1, 2 * (int64_t)pool->num_sms / std::max<int64_t>(1, rows));
-    return (int)std::max<int64_t>(1, std::min({want, chunks, (int64_t)(kMaxLists / beams)}));
+    return (int)std::max<int64_t>(1, std::min({want, parts, (int64_t)(kMaxLists / beams)}));
 }
 
 size_t beam_bytes(int64_t rows, int slices, int k) { return (size_t)rows * slices * (8 * (size_t)k + 16); }
