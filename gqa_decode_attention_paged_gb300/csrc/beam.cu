@@ -11,23 +11,23 @@
 // into slices so that every SM has work, leaves each slice's maximum, sum of
 // exponentials and k greatest logits; a merge of each search's lists.
 //
-// Selecting while scanning.  From a slice's first part (kVecs vectors of 16
-// bytes per thread) the threads' greatest logits, reduced to 4 k groups or more,
-// give a bar: the k-th greatest group maximum, which at least k logits reach.
-// Those that do belong to k groups, so they fit the buffer whatever the data.
-// The warps then read the rest each for itself, without barriers, and add what
-// is above the bar: k (n / n_1 - 1) logits where they come in any order.  Only
-// where they rise along the row can the buffer run over; the slice is then read
-// again in parts, each of which raises the bar first.  Keys (logit as an ordered
-// integer, then the lower index) are unique, so ties need no care and results do
-// not depend on the order of arrival.
+// Reading.  A slice's rows stream through a ring of four parts of 16 KiB in
+// shared memory (bulk copies; 128 KiB of them in flight on an SM, where a vector
+// a thread ahead had 64 and waited for memory: 35 us against XX).  A row may begin
+// anywhere.  Which thread adds which logits must not depend on that, or two beams
+// with equal logits would get sums that differ in the last place, and equal
+// continuations would not go to the lower beam.  So a thread takes the N elements
+// from a multiple of N of the row on, out of two aligned vectors.
 //
-// A row may begin anywhere.  Which thread adds which logits must not depend on
-// that, or two beams with equal logits would get sums that differ in the last
-// place, and equal continuations would not go to the lower beam.  So a lane
-// takes the N elements from a multiple of N of the row on, out of two aligned
-// vectors: its own and the next lane's.  The last lane of a warp only passes
-// its vector on.
+// Selecting while scanning.  From a slice's first two parts the threads' greatest
+// logits, reduced to 4 k groups or more, give a bar: the k-th greatest group
+// maximum, which at least k logits reach.  Those that do belong to k groups, so
+// they fit the buffer whatever the data.  The warps then go through the rest each
+// for itself and add what is above the bar: k (n / n_1 - 1) logits where they come
+// in any order.  Only where they rise along the row can the buffer run over; the
+// slice is then read again in pieces, each of which raises the bar first.  Keys
+// (logit as an ordered integer, then the lower index) are unique, so ties need no
+// care and results do not depend on the order of arrival.
 //
 // Accuracy.  Candidates of different beams may lie arbitrarily close, so what
 // decides between them is held in more than 32 bits: the exponentials are
@@ -37,6 +37,7 @@
 #include <algorithm>
 #include <climits>
 #include <math.h>
+#include <mutex>
 
 #include "tcgen05.cuh"
 
@@ -45,14 +46,13 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kVecs = 4;                         // 16-byte vectors of a thread in a part
-constexpr int kLanes = 31;                       // lanes of a warp that have logits
-constexpr int kRunVecs = kWarps * kLanes;        // a vector each: the unit in which rows are cut
+constexpr int kPartVecs = 2 * kThreads;          // 16-byte vectors of a part: two a thread
+constexpr int kStages = 4;
+constexpr int kStageBytes = kPartVecs * 16 + 128; // with the vector behind it
 constexpr int kMaxK = 64, kMaxBeams = 64;
-constexpr int kCap = 5120;                       // keys the buffer holds: a part's 4096 at most, k kept ones, some more
+constexpr int kCap = 5120;                       // keys the buffer holds: 4096 of two parts at most, k kept ones, some more
 constexpr int kMaxLists = 1024;                  // (beam, slice) lists of a search
 constexpr int kMergeThreads = 256;
-constexpr int kMergeKeys = 4096;                 // keys of a search that the merge holds in shared memory
 
 struct ScanArgs {
     const void *logits;
@@ -61,6 +61,7 @@ struct ScanArgs {
     uint64_t *keys;  // [rows][slices][k], greatest first, 0: none
     float *top;      // [rows][slices] maximum
     double *sum;     // [rows][slices] sum of exp(x - maximum); NaN where the slice holds a NaN or +infinity
+    unsigned *err;
 };
 
 // The order of keys is that of the logits, then of the lower index; 0 is below all of them.
@@ -108,6 +109,8 @@ struct Elems<float> {
 };
 
 struct Shared {
+    alignas(128) uint8_t ring[kStages][kStageBytes];
+    uint64_t full[kStages], empty[kStages];
     uint64_t buf[kCap];
     uint64_t group[256];
     uint64_t bar;      // keys below it are not among the k greatest
@@ -166,60 +169,61 @@ __device__ __forceinline__ int thin_out(Shared &sh, int n, int k, int p, int mos
     return n;
 }
 
-// A row of logits, as one warp reads it: run r is kLanes vectors of every warp, a vector a lane.
+// A row of logits as 16-byte aligned vectors u, elements u N - lead .. + N - 1.
 template <typename T>
 struct Row {
     using El = Elems<T>;
     static constexpr int N = El::N;
     const T *x;
     int vocab, lead;  // elements before the row in its first aligned vector
-    int lane, warp;
 
-    // index of this lane's first element of run r
-    __device__ __forceinline__ int first(int r) const { return ((r * kWarps + warp) * kLanes + lane) * N; }
-    // the aligned vector in which it is
-    __device__ __forceinline__ uint4 load(int r) const
+    // vectors [inner0(), inner1()) are inside the row
+    __device__ __forceinline__ int inner0() const { return lead ? 1 : 0; }
+    __device__ __forceinline__ int inner1() const { return (int)(((int64_t)vocab + lead) / N); }
+    __device__ __forceinline__ bool inside(int u) const { return u >= inner0() && u < inner1(); }
+    __device__ __forceinline__ const T *at(int u) const { return x + ((int64_t)u * N - lead); }
+    // a vector that the row begins or ends in, or one behind it
+    __device__ uint4 edge(int u) const
     {
-        const int i = first(r) - lead;
-        if (i >= 0 && i <= vocab - N) return ldg_nc_v4(x + i);
-        uint32_t w[4] = {El::kLow, El::kLow, El::kLow, El::kLow};  // the row's ends
-        if (i > -N && i < vocab) {
+        const int i = u * N - lead;
+        uint32_t w[4] = {El::kLow, El::kLow, El::kLow, El::kLow};
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                if (i + e < 0 || i + e >= vocab) continue;
-                if constexpr (N == 4) {
-                    w[e] = __float_as_uint(x[i + e]);
-                } else {
-                    const uint32_t h = __bfloat16_as_ushort(x[i + e]);
-                    w[e / 2] = e % 2 ? (w[e / 2] & 0xffffu) | (h << 16) : (w[e / 2] & 0xffff0000u) | h;
-                }
+        for (int e = 0; e < N; ++e) {
+            if (i + e < 0 || i + e >= vocab) continue;
+            if constexpr (N == 4) {
+                w[e] = __float_as_uint(x[i + e]);
+            } else {
+                const uint32_t h = __bfloat16_as_ushort(x[i + e]);
+                w[e / 2] = e % 2 ? (w[e / 2] & 0xffffu) | (h << 16) : (w[e / 2] & 0xffff0000u) | h;
             }
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    // this lane's elements, from its vector and the next lane's
-    __device__ __forceinline__ uint4 line_up(const uint4 &r) const
+    // elements u N .. + N - 1, out of vectors u and u + 1
+    __device__ __forceinline__ uint4 line_up(const uint4 &r, const uint4 &next) const
     {
-        uint32_t w[8] = {r.x, r.y, r.z, r.w};
-        if (lead) {
-            const int words = lead * (int)sizeof(T) / 4;
+        uint32_t w[8] = {r.x, r.y, r.z, r.w, next.x, next.y, next.z, next.w};
+        const int words = lead * (int)sizeof(T) / 4;
+        if (words & 2) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[4 + i] = __shfl_down_sync(kFull, w[i], 1);
-            if (words & 2) {
-#pragma unroll
-                for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-            }
-            if (words & 1) {
-#pragma unroll
-                for (int i = 0; i < 7; ++i) w[i] = w[i + 1];
-            }
-            if (N == 8 && (lead & 1)) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-            }
+            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
         }
-        const bool on = lane < kLanes;
-        return make_uint4(on ? w[0] : El::kLow, on ? w[1] : El::kLow, on ? w[2] : El::kLow, on ? w[3] : El::kLow);
+        if (words & 1) {
+#pragma unroll
+            for (int i = 0; i < 7; ++i) w[i] = w[i + 1];
+        }
+        if (N == 8 && (lead & 1)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    template <typename Get>
+    __device__ __forceinline__ uint4 elements(int u, Get &&get) const
+    {
+        const uint4 r = inside(u) ? get(u) : edge(u);
+        if (!lead) return r;
+        return line_up(r, inside(u + 1) ? get(u + 1) : edge(u + 1));
     }
 };
 
@@ -239,9 +243,9 @@ __device__ __forceinline__ float greatest_of(const uint4 &v)
 // A thread's greatest logit so far and the sum of exp(x - m).
 struct Sum {
     float m = -INFINITY, s = 0.0f;
-    // kVecs vectors with the greatest logit top
-    template <typename T>
-    __device__ __forceinline__ void add(const uint4 (&v)[kVecs], float top)
+    // V vectors with the greatest logit top
+    template <typename T, int V>
+    __device__ __forceinline__ void add(const uint4 (&v)[V], float top)
     {
         constexpr int N = Elems<T>::N;
         if (top > m) {
@@ -252,7 +256,7 @@ struct Sum {
         const float neg = m == -INFINITY ? 0.0f : -m;
         float2 part = {0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
+        for (int i = 0; i < V; ++i) {
             float x[N];
             Elems<T>::widen(v[i], x);
 #pragma unroll
@@ -270,92 +274,133 @@ __global__ void __launch_bounds__(kThreads, 2) beam_scan_kernel(const __grid_con
 {
     using El = Elems<T>;
     constexpr int N = El::N;
-    __shared__ Shared sh;
+    extern __shared__ __align__(128) uint8_t beam_smem[];
+    Shared &sh = *reinterpret_cast<Shared *>(beam_smem);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        sh.n = 0;
+        sh.bar = 0;
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], kWarps);
+        }
+        fence_mbarrier_init();
+    }
     griddep_wait();
     griddep_launch_dependents();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int slice = blockIdx.x;
     const int64_t row = (int64_t)blockIdx.y * gridDim.z + blockIdx.z;  // (search, beam)
     Row<T> rw;
     rw.x = static_cast<const T *>(a.logits) + row * a.stride;
     rw.vocab = a.vocab;
     rw.lead = (int)(((uintptr_t)rw.x & 15u) / sizeof(T));
-    rw.lane = lane;
-    rw.warp = warp;
-    const int runs = (a.vocab + kRunVecs * N - 1) / (kRunVecs * N);
-    const int r0 = (int)((int64_t)runs * slice / a.slices), r1 = (int)((int64_t)runs * (slice + 1) / a.slices);
+    const int parts = (a.vocab + kPartVecs * N - 1) / (kPartVecs * N);
+    const int r0 = (int)((int64_t)parts * slice / a.slices), r1 = (int)((int64_t)parts * (slice + 1) / a.slices);
     const int k = a.k;
     const int p = k <= 4 ? 1 : k <= 8 ? 2 : k <= 16 ? 4 : k <= 32 ? 8 : 16;  // groups of a warp
-    if (tid == 0) {
-        sh.n = 0;
-        sh.bar = 0;
-    }
-    const uint4 none = make_uint4(El::kLow, El::kLow, El::kLow, El::kLow);
-    auto load = [&](int r, uint4 (&v)[kVecs]) {
+    const uint64_t policy = l2_policy_evict_first();
+    // part r into its stage: the vectors that are inside the row, and the one behind the part's last
+    auto issue = [&](int r) {
+        const int u0 = max(r * kPartVecs, rw.inner0()), u1 = min((r + 1) * kPartVecs + (rw.lead ? 1 : 0), rw.inner1());
+        const int st = (r - r0) % kStages;
+        const uint32_t bytes = u1 > u0 ? 16u * (uint32_t)(u1 - u0) : 0u;
+        mbar_arrive_expect_tx(&sh.full[st], bytes);
+        if (bytes) bulk_g2s(sh.ring[st] + (u0 - r * kPartVecs) * 16, rw.at(u0), bytes, &sh.full[st], policy);
+    };
+    if (tid == 0)
+        for (int r = r0; r < min(r1, r0 + kStages); ++r) issue(r);
+    __syncthreads();
+    bool ok = true;
+    // this thread's two vectors of part r (none past the slice)
+    auto fetch = [&](int r, uint4 *v) {
+        v[0] = v[1] = make_uint4(El::kLow, El::kLow, El::kLow, El::kLow);
+        if (r >= r1) return;
+        const int st = (r - r0) % kStages;
+        ok = ok && __all_sync(kFull, mbar_wait_bounded(&sh.full[st], ((r - r0) / kStages) & 1));
+        const uint32_t ring = smem_u32(sh.ring[st]);
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) v[i] = r + i < r1 ? rw.load(r + i) : none;
+        for (int i = 0; i < 2; ++i)
+            v[i] = rw.elements(r * kPartVecs + i * kThreads + tid, [&](int u) { return lds128(ring + (u - r * kPartVecs) * 16); });
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[st]);
     };
-    auto line_up = [&](uint4 (&v)[kVecs]) {
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) v[i] = rw.line_up(v[i]);
+    // part r's stage to the part kStages further on, when all warps have read it
+    auto refill = [&](int r) {
+        if (warp != 0 || r < r0 || r + kStages >= r1) return;
+        const int st = (r - r0) % kStages;
+        ok = ok && __all_sync(kFull, mbar_wait_bounded(&sh.empty[st], ((r - r0) / kStages) & 1));
+        if (lane == 0) {
+            fence_proxy_async_smem();
+            issue(r + kStages);
+        }
+        __syncwarp();
     };
-    auto greatest = [&](const uint4 (&v)[kVecs]) -> float {
-        static_assert(kVecs == 4, "");
-        return fmaxf(fmaxf(greatest_of<T>(v[0]), greatest_of<T>(v[1])), fmaxf(greatest_of<T>(v[2]), greatest_of<T>(v[3])));
+    auto greatest = [&](const uint4 *v, int n) -> float {
+        float top = greatest_of<T>(v[0]);
+        for (int i = 1; i < n; ++i) top = fmaxf(top, greatest_of<T>(v[i]));
+        return top;
     };
+    // index in the row of vector i's first element, for the vectors of parts r, r + 1
+    auto first = [&](int r, int i) -> int { return (r * kPartVecs + i * kThreads + tid) * N; };
     // the key of a thread's greatest logit: of equal ones the first
-    auto key_at = [&](const uint4 (&v)[kVecs], int r, float top) -> uint64_t {
+    auto key_at = [&](const uint4 (&v)[4], int r, float top) -> uint64_t {
         if (!(top > -INFINITY)) return 0;
         int at = 0;
 #pragma unroll
-        for (int i = kVecs - 1; i >= 0; --i) {
+        for (int i = 3; i >= 0; --i) {
             float x[N];
             El::widen(v[i], x);
 #pragma unroll
-            for (int e = N - 1; e >= 0; --e) at = x[e] == top ? i * (kRunVecs * N) + e : at;
+            for (int e = N - 1; e >= 0; --e) at = x[e] == top ? i * (kThreads * N) + e : at;
         }
-        return key_of(top, rw.first(r) + at);
+        return key_of(top, first(r, 0) + at);
     };
-    // adds this thread's logits that reach the bar to the buffer
-    auto add_keys = [&](const uint4 (&v)[kVecs], int r, uint64_t bar) {
-#pragma unroll 1
-        for (int i = 0; i < kVecs; ++i) {
-            const uint4 w = i == 0 ? v[0] : i == 1 ? v[1] : i == 2 ? v[2] : v[3];
-            const float top = greatest_of<T>(w);
-            if (!(top > -INFINITY) || (bar && top < logit_of(bar))) continue;
-            float x[N];
-            El::widen(w, x);
+    // adds a vector's logits that reach the bar to the buffer
+    auto add_keys = [&](const uint4 &w, int at0, uint64_t bar) {
+        const float top = greatest_of<T>(w);
+        if (!(top > -INFINITY) || (bar && top < logit_of(bar))) return;
+        float x[N];
+        El::widen(w, x);
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                if (!(x[e] > -INFINITY)) continue;
-                const uint64_t key = key_of(x[e], rw.first(r + i) + e);
-                if (key < bar) continue;
-                const int at = atomicAdd(&sh.n, 1);
-                if (at < kCap) sh.buf[at] = key;
-            }
+        for (int e = 0; e < N; ++e) {
+            if (!(x[e] > -INFINITY)) continue;
+            const uint64_t key = key_of(x[e], at0 + e);
+            if (key < bar) continue;
+            const int at = atomicAdd(&sh.n, 1);
+            if (at < kCap) sh.buf[at] = key;
         }
     };
     Sum sum;
-    uint4 cur[kVecs], nxt[kVecs];
-    load(r0, cur);
-    load(r0 + kVecs, nxt);
-    line_up(cur);
-    float top = greatest(cur);
-    __syncthreads();  // (the bar and the count are set)
-    raise_bar(sh, key_at(cur, r0, top), k, p);
-    uint64_t bar = sh.bar;
-    add_keys(cur, r0, bar);
-    sum.add<T>(cur, top);
+    {
+        uint4 v[4];
+        fetch(r0, v);
+        fetch(r0 + 1, v + 2);
+        const float top = greatest(v, 4);
+        raise_bar(sh, key_at(v, r0, top), k, p);
+        const uint64_t bar = sh.bar;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) add_keys(v[i], first(r0, i), bar);
+        sum.add<T, 4>(v, top);
+        refill(r0);
+    }
+    const uint64_t bar = sh.bar;
     // ---- the rest of the slice, every warp for itself ----
     const float high = bar ? logit_of(bar) : -INFINITY;
-    for (int r = r0 + kVecs; r < r1; r += kVecs) {
+    for (int r = r0 + 2; r < r1; ++r) {
+        uint4 v[2];
+        fetch(r, v);
+        refill(r - 1);
+        const float top = greatest(v, 2);
+        if (top > high) {  // (an equal one has a greater index than the bar's)
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) cur[i] = nxt[i];
-        load(r + kVecs, nxt);
-        line_up(cur);
-        top = greatest(cur);
-        if (top > high) add_keys(cur, r, bar);  // (an equal one has a greater index than the bar's)
-        sum.add<T>(cur, top);
+            for (int i = 0; i < 2; ++i) add_keys(v[i], first(r, i), bar);
+        }
+        sum.add<T, 2>(v, top);
+    }
+    if (!ok) {
+        if (lane == 0) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
+        if (warp == 0)  // copies in flight land before the block exits
+            for (int r = max(r0, r1 - kStages); r < r1; ++r) mbar_wait_bounded(&sh.full[(r - r0) % kStages], ((r - r0) / kStages) & 1);
     }
     // ---- the slice's maximum and sum ----
     float M = sum.m;
@@ -378,13 +423,18 @@ __global__ void __launch_bounds__(kThreads, 2) beam_scan_kernel(const __grid_con
             sh.bar = 0;
         }
         __syncthreads();
-        for (int r = r0; r < r1; r += kVecs) {
+        for (int r = r0; r < r1; r += 2) {
             const int have = sh.n;
-            load(r, cur);
-            line_up(cur);
-            raise_bar(sh, key_at(cur, r, greatest(cur)), k, p);
+            uint4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = r + i / 2 < r1 ? rw.elements(first(r, i) / N, [&](int u) { return ldg_nc_v4(rw.at(u)); })
+                                      : make_uint4(El::kLow, El::kLow, El::kLow, El::kLow);
+            raise_bar(sh, key_at(v, r, greatest(v, 4)), k, p);
             if (have + 4096 > kCap) thin_out(sh, have, k, p, kMaxK);
-            add_keys(cur, r, sh.bar);
+            const uint64_t now = sh.bar;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) add_keys(v[i], first(r, i), now);
             __syncthreads();
         }
         n = sh.n;
@@ -419,58 +469,71 @@ struct MergeArgs {
     unsigned *err;
 };
 
-// A continuation: its worth as an ordered integer (0: none), its beam and its key.  Equal worths go to the lower
-// beam, then to the greater key (doubles may round a beam's different logits to one worth).
-struct Best {
-    uint64_t value, key;
-    int beam;
-    __device__ __forceinline__ bool before(const Best &y) const
-    {
-        return value != y.value ? value > y.value : beam != y.beam ? beam < y.beam : key > y.key;
-    }
+// A continuation: its worth as an ordered integer (0: none), then what settles equal worths: the lower beam, then the
+// greater logit (a beam's different logits may have one worth in 64 bits), then the lower token.
+struct Cand {
+    uint64_t value, tie;
+    __device__ __forceinline__ bool above(const Cand &y) const { return value != y.value ? value > y.value : tie > y.tie; }
+};
+constexpr int kTokenBits = 22;
+__device__ __forceinline__ Cand shfl_xor(const Cand &x, int o)
+{
+    return {__shfl_xor_sync(kFull, x.value, o), __shfl_xor_sync(kFull, x.tie, o)};
+}
+
+constexpr int kMergeWarps = kMergeThreads / 32;
+constexpr int kHold = 16;                        // continuations of a thread, at a time
+constexpr int kMergeCap = 3072;                  // that the merge holds in shared memory
+
+struct MergeShared {
+    Cand buf[kMergeCap];
+    Cand group[kMergeThreads];
+    Cand bar;
+    int n;
+    double shift[kMaxBeams];   // score - log of the sum of exp(x - m); NaN: no continuations
+    float highest[kMaxBeams];  // m: v = (x - m) + shift, in which large logits cost nothing
 };
 
-__device__ __forceinline__ uint64_t warp_max(uint64_t x, bool on)
+// The k-th greatest of the groups' greatest continuations, if as many groups have one: as raise_bar, 8 p groups.
+__device__ __forceinline__ void raise_bar(MergeShared &sh, Cand mine, int k, int p)
 {
-    const uint32_t hi = __reduce_max_sync(kFull, on ? (uint32_t)(x >> 32) : 0u);
-    const uint32_t lo = __reduce_max_sync(kFull, on && (uint32_t)(x >> 32) == hi ? (uint32_t)x : 0u);
-    return ((uint64_t)hi << 32) | lo;
-}
-
-// The first of a warp's.
-__device__ __forceinline__ Best warp_best(const Best &x)
-{
-    const uint64_t value = warp_max(x.value, true);
-    unsigned on = __ballot_sync(kFull, x.value == value);
-    if (on & (on - 1)) {  // the same for all lanes
-        const int beam = __reduce_min_sync(kFull, x.value == value ? x.beam : INT_MAX);
-        const bool mine = x.value == value && x.beam == beam;
-        const uint64_t key = warp_max(x.key, mine);
-        on = __ballot_sync(kFull, mine && x.key == key);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, size = 32 / p;
+    for (int o = size / 2; o >= 1; o >>= 1) {
+        const Cand y = shfl_xor(mine, o);
+        if (y.above(mine)) mine = y;
     }
-    const int l = __ffs(on) - 1;
-    return {value, __shfl_sync(kFull, x.key, l), __shfl_sync(kFull, x.beam, l)};
+    if (lane % size == 0) sh.group[warp * p + lane / size] = mine;
+    __syncthreads();
+    const int groups = kMergeWarps * p;
+    if (tid < groups) {
+        const Cand x = sh.group[tid];
+        int rank = 0;
+        for (int i = 0; i < groups; ++i) rank += sh.group[i].above(x);
+        if (x.value && rank == k - 1 && x.above(sh.bar)) sh.bar = x;  // (one thread: continuations are unique)
+    }
+    __syncthreads();
 }
 
-// One search: its beams' log-sums, then k times the best of the lists' heads.
+// One search: its beams' log-sums, the worth of its lists' continuations, and the k greatest of them, found as the
+// scan finds a row's (k rounds over the lists' heads took 0.65 us each).
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_constant__ MergeArgs a)
 {
-    __shared__ double shift[kMaxBeams];  // score - log of the sum of exp(x - m); NaN: no candidates
-    __shared__ float highest[kMaxBeams]; // m: v = (x - m) + shift, in which large logits cost nothing
-    __shared__ uint64_t held[kMergeKeys];
-    __shared__ uint8_t at[kMaxLists];    // keys of a list that are taken
-    __shared__ Best bests[2][kMergeThreads / 32];
+    extern __shared__ __align__(16) uint8_t merge_smem[];
+    MergeShared &sh = *reinterpret_cast<MergeShared *>(merge_smem);
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t item = blockIdx.x;
-    const int lists = a.beams * a.slices, total = lists * a.k;
+    const int per_beam = a.slices * a.k, total = a.beams * per_beam;
     const uint64_t *keys = a.keys + item * total;
-    const bool hold = total <= kMergeKeys;
-    if (hold)
-        for (int i = tid; i < total; i += kMergeThreads) held[i] = keys[i];
-    for (int i = tid; i < lists; i += kMergeThreads) at[i] = 0;
-    for (int j = warp; j < a.beams; j += kMergeThreads / 32) {  // a warp a beam, a lane a slice
+    if (tid == 0) {
+        sh.bar = {0, 0};
+        sh.n = 0;
+    }
+    uint64_t held[kHold];  // the first keys, read while the log-sums are formed
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) held[i] = i * kMergeThreads + tid < total ? keys[i * kMergeThreads + tid] : 0;
+    for (int j = warp; j < a.beams; j += kMergeWarps) {  // a warp a beam, a lane a slice
         const int64_t l0 = (item * a.beams + j) * a.slices;
         float M = -INFINITY;
         for (int i = lane; i < a.slices; i += 32) M = fmaxf(M, a.top[l0 + i]);
@@ -488,66 +551,104 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
         const float sc = a.scores[item * a.beams + j];
         const bool odd = sc != -INFINITY && (s != s || sc != sc || sc == INFINITY);
         if (odd) atomicOr(a.err, PKV_DEVERR_NAN);
-        shift[j] = odd || sc == -INFINITY || M == -INFINITY ? (double)NAN : (double)sc - log(s);
-        highest[j] = M;
+        sh.shift[j] = odd || sc == -INFINITY || M == -INFINITY ? (double)NAN : (double)sc - log(s);
+        sh.highest[j] = M;
     }
     __syncthreads();
-    constexpr Best kNone = {0, 0, INT_MAX};
-    auto head = [&](int l) -> Best {  // of a list
-        const int n = at[l], j = l / a.slices;
-        if (n >= a.k) return kNone;
-        const uint64_t key = hold ? held[l * a.k + n] : keys[(int64_t)l * a.k + n];
-        const double v = ((double)logit_of(key) - (double)highest[j]) + shift[j];
-        if (!key || v != v) return kNone;
+    auto worth = [&](uint64_t key, int i) -> Cand {
+        if (!key) return {0, 0};
+        const int j = i / per_beam;
+        const double v = ((double)logit_of(key) - (double)sh.highest[j]) + sh.shift[j];
+        if (v != v) return {0, 0};
         const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
-        return {u ^ ((u >> 63) ? ~0ull : 1ull << 63), key, j};
+        return {u ^ ((u >> 63) ? ~0ull : 1ull << 63),
+                ((uint64_t)(kMaxBeams - 1 - j) << (32 + kTokenBits)) | ((key >> 32) << kTokenBits) |
+                    (uint64_t)((1 << kTokenBits) - 1 - index_of(key))};
     };
-    const bool alone = lists <= 32;  // one warp has all lists
-    if (alone && warp) return;
-    Best mine;
-    int from = 0;
-    auto look = [&]() {
-        mine = kNone;
-        for (int l = tid; l < lists; l += kMergeThreads) {
-            const Best x = head(l);
-            if (x.before(mine)) {
-                mine = x;
-                from = l;
-            }
+    // kHold keys a thread at a time: at least k of them reach the bar, and those that do are of k groups
+    const int p = a.k <= 4 ? 2 : a.k <= 8 ? 4 : a.k <= 16 ? 8 : a.k <= 32 ? 16 : 32;  // groups of a warp
+    auto greatest = [&](const Cand (&c)[kHold]) -> Cand {
+        Cand top = c[0];
+#pragma unroll
+        for (int i = 1; i < kHold; ++i)
+            if (c[i].above(top)) top = c[i];
+        return top;
+    };
+    // keeps those of c that reach the bar: 32 / p threads' kHold of k groups, 1024 at most
+    auto keep = [&](const Cand (&c)[kHold]) {
+        const Cand bar = sh.bar;
+#pragma unroll
+        for (int i = 0; i < kHold; ++i)
+            if (c[i].value && !bar.above(c[i])) sh.buf[atomicAdd(&sh.n, 1)] = c[i];
+        __syncthreads();
+    };
+    static_assert(kMergeCap >= 2048 + kHold * kMergeThreads / 4, "");
+    for (int base = 0; base < total; base += kHold * kMergeThreads) {
+        Cand c[kHold];
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+            const int at = base + i * kMergeThreads + tid;
+            c[i] = worth(base == 0 ? held[i] : at < total ? keys[at] : 0, at);
         }
-    };
-    look();
-    for (int i = 0; i < a.k; ++i) {
-        Best w = warp_best(mine);
-        if (!alone) {
-            if (lane == 0) bests[i & 1][warp] = w;
+        raise_bar(sh, greatest(c), a.k, p);
+        keep(c);
+        // fewer again, before the next ones or the end
+        for (int n = sh.n; n > (base + kHold * kMergeThreads < total ? 2048 : kMergeThreads);) {
+            __syncthreads();  // (n is read)
+#pragma unroll
+            for (int i = 0; i < kHold; ++i) c[i] = i * kMergeThreads + tid < n ? sh.buf[i * kMergeThreads + tid] : Cand{0, 0};
+            raise_bar(sh, greatest(c), a.k, p);
+            if (tid == 0) sh.n = 0;
             __syncthreads();
-            w = warp_best(lane < kMergeThreads / 32 ? bests[i & 1][lane] : kNone);
+            keep(c);
+            n = sh.n;
         }
-        const int64_t o = item * a.k + i;
-        if (w.value == 0) {  // no candidate is left
-            if (tid == 0) {
-                a.tokens[o] = a.parents[o] = -1;
-                a.out[o] = -INFINITY;
-            }
-        } else if (mine.beam == w.beam && mine.key == w.key) {
-            const uint64_t u = w.value ^ ((w.value >> 63) ? 1ull << 63 : ~0ull);
-            a.tokens[o] = index_of(w.key);
-            a.parents[o] = w.beam;
+        __syncthreads();
+    }
+    // ---- in order ----
+    const int n = sh.n;
+    if (tid < n) {
+        const Cand x = sh.buf[tid];
+        int rank = 0;
+        for (int i = 0; i < n; ++i) rank += sh.buf[i].above(x);
+        if (rank < a.k) {
+            const int64_t o = item * a.k + rank;
+            const uint64_t u = x.value ^ ((x.value >> 63) ? 1ull << 63 : ~0ull);
+            a.tokens[o] = (1 << kTokenBits) - 1 - (int)(x.tie & ((1 << kTokenBits) - 1));
+            a.parents[o] = kMaxBeams - 1 - (int)(x.tie >> (32 + kTokenBits));
             a.out[o] = (float)__longlong_as_double((long long)u);
-            ++at[from];
-            look();
         }
+    } else if (tid < a.k) {  // no continuation is left for this place
+        const int64_t o = item * a.k + tid;
+        a.tokens[o] = a.parents[o] = -1;
+        a.out[o] = -INFINITY;
     }
 }
 
-// Slices of a row: enough for two blocks on every SM, no more than the row has parts, nor than the merge takes.
+// Slices of a row: enough for two blocks on every SM, but two parts each at least, and no more than the merge takes.
 int slices_of(const pkv_pool *pool, int64_t rows, int beams, int vocab, int elem)
 {
-    const int64_t part = (int64_t)kRunVecs * kVecs * (16 / elem);
+    const int64_t part = (int64_t)kPartVecs * (16 / elem);
     const int64_t parts = (vocab + part - 1) / part;
     const int64_t want = std::max<int64_t>(1, 2 * (int64_t)pool->num_sms / std::max<int64_t>(1, rows));
-    return (int)std::max<int64_t>(1, std::min({want, parts, (int64_t)(kMaxLists / beams)}));
+    return (int)std::max<int64_t>(1, std::min({want, (parts + 1) / 2, (int64_t)(kMaxLists / beams)}));
+}
+
+// The kernels' shared memory is allowed, once per device.
+pkv_status prepare_scan(const pkv_pool *pool)
+{
+    static std::mutex mu;
+    static bool ready[64];
+    std::lock_guard<std::mutex> lock(mu);
+    if (pool->device < 64 && ready[pool->device]) return PKV_OK;
+    cudaError_t e = cudaFuncSetAttribute(beam_scan_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(beam_scan_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(MergeShared));
+    if (e != cudaSuccess) return cuda_fail(e, "paged_beam_select: kernel attributes");
+    if (pool->device < 64) ready[pool->device] = true;
+    return PKV_OK;
 }
 
 size_t beam_bytes(int64_t rows, int slices, int k) { return (size_t)rows * slices * (8 * (size_t)k + 16); }
@@ -618,8 +719,11 @@ extern "C" pkv_status paged_beam_select(pkv_pool *pool, const void *logits, int3
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     st = ensure_workspace(pool, beam_bytes(rows, slices, k), s, who);
     if (st != PKV_OK) return st;
+    st = prepare_scan(pool);
+    if (st != PKV_OK) return st;
     const size_t lists = (size_t)rows * slices;
     ScanArgs a;
+    a.err = pool->err;
     a.logits = logits;
     a.stride = row_stride;
     a.vocab = vocab;
@@ -631,8 +735,8 @@ extern "C" pkv_status paged_beam_select(pkv_pool *pool, const void *logits, int3
     {
         LaunchScope ls(pool, kDecode, s);
         const dim3 grid((unsigned)slices, (unsigned)batch, (unsigned)beams);
-        cudaError_t e = elem == 4 ? launch_pdl(beam_scan_kernel<float>, grid, dim3(kThreads), 0, s, a)
-                                  : launch_pdl(beam_scan_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, s, a);
+        cudaError_t e = elem == 4 ? launch_pdl(beam_scan_kernel<float>, grid, dim3(kThreads), sizeof(Shared), s, a)
+                                  : launch_pdl(beam_scan_kernel<__nv_bfloat16>, grid, dim3(kThreads), sizeof(Shared), s, a);
         ls.done();
         if (e != cudaSuccess) return cuda_fail(e, "paged_beam_select scan launch");
     }
@@ -649,7 +753,7 @@ extern "C" pkv_status paged_beam_select(pkv_pool *pool, const void *logits, int3
     m.out = out_scores;
     m.err = pool->err;
     LaunchScope ls(pool, kMerge, s);
-    cudaError_t e = launch_pdl(beam_merge_kernel, dim3((unsigned)batch), dim3(kMergeThreads), 0, s, m);
+    cudaError_t e = launch_pdl(beam_merge_kernel, dim3((unsigned)batch), dim3(kMergeThreads), sizeof(MergeShared), s, m);
     ls.done();
     if (e != cudaSuccess) return cuda_fail(e, "paged_beam_select merge launch");
     return PKV_OK;
