@@ -6,28 +6,32 @@
 // a row v grows with x, so a row's candidates are its k greatest logits, and
 // only those need v.
 //
-// What bounds it: HBM, the logits read once; close behind it the exponentials
-// (one per logit, 16 an SM and cycle).  Two launches: a scan of the rows, cut
-// into slices so that every SM has work, leaves each slice's maximum, sum of
-// exponentials and k greatest logits; a merge of each search's lists.
+// What bounds it: HBM, the logits read once; close behind it the instructions
+// (about five per logit).  Two launches: a scan of the rows, cut into pieces so
+// that every SM has three blocks where the rows are few, leaves each piece's
+// maximum, sum of exponentials and k greatest logits; a merge takes each
+// search's pieces.
 //
-// Reading.  A slice's rows stream through a ring of four parts of 16 KiB in
-// shared memory (bulk copies; 128 KiB of them in flight on an SM, where a vector
-// a thread ahead had 64 and waited for memory: 35 us against XX).  A row may begin
-// anywhere.  Which thread adds which logits must not depend on that, or two beams
-// with equal logits would get sums that differ in the last place, and equal
-// continuations would not go to the lower beam.  So a thread takes the N elements
-// from a multiple of N of the row on, out of two aligned vectors.
+// Reading.  A piece streams through a ring of three parts of 16 KiB in shared
+// memory (bulk copies: a vector a thread ahead kept 64 KiB in flight on an SM and
+// waited for memory).  A row may begin anywhere.  Which thread adds which logits
+// must depend neither on that nor on the row's number, or two beams with equal
+// logits would get sums that differ in the last place, and equal continuations
+// would not go to the lower beam.  So a thread takes the N elements from a
+// multiple of N of the row on, out of two aligned vectors, and all rows are cut
+// at the same places.
 //
-// Selecting while scanning.  From a slice's first two parts the threads' greatest
+// Selecting while scanning.  From a piece's first part the threads' greatest
 // logits, reduced to 4 k groups or more, give a bar: the k-th greatest group
-// maximum, which at least k logits reach.  Those that do belong to k groups, so
-// they fit the buffer whatever the data.  The warps then go through the rest each
-// for itself and add what is above the bar: k (n / n_1 - 1) logits where they come
-// in any order.  Only where they rise along the row can the buffer run over; the
-// slice is then read again in pieces, each of which raises the bar first.  Keys
-// (logit as an ordered integer, then the lower index) are unique, so ties need no
-// care and results do not depend on the order of arrival.
+// maximum, which at least k logits reach.  The warps then go through the rest
+// each for itself, and note the vectors that have a logit above the bar: about
+// k (n / n_1 - 1) where the logits come in any order.  At the end the logits of
+// the noted vectors are taken out of them.  Where they rise along the row, or
+// many equal the bar, the notes or what is in them can be too many; the piece is
+// then read again, and every part raises the bar first: what reaches it belongs
+// to k groups, so it fits whatever the data.  Keys (logit as an ordered integer,
+// then the lower index) are unique, so ties need no care and results do not
+// depend on the order of arrival.
 //
 // Accuracy.  Candidates of different beams may lie arbitrarily close, so what
 // decides between them is held in more than 32 bits: the exponentials are
@@ -44,23 +48,33 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kPartVecs = 2 * kThreads;          // 16-byte vectors of a part: two a thread
-constexpr int kStages = 4;
+constexpr int kVecs = 4;                         // 16-byte vectors of a thread and part
+constexpr int kPartVecs = kVecs * kThreads;
+constexpr int kStages = 3;
+constexpr int kBlocksPerSm = 3;
 constexpr int kStageBytes = kPartVecs * 16 + 128; // with the vector behind it
 constexpr int kMaxK = 64, kMaxBeams = 64;
-constexpr int kCap = 5120;                       // keys the buffer holds: 4096 of two parts at most, k kept ones, some more
-constexpr int kMaxLists = 1024;                  // (beam, slice) lists of a search
+constexpr int kPartKeys = 2048;                  // of a part, that reach its bar, at most
+constexpr int kCap = 2304;                       // keys the buffer holds: those, k kept ones, some more
+constexpr int kNotes = 1280;                     // vectors that can be noted
 constexpr int kMergeThreads = 256;
+
+// How rows are cut: piece i of a row has parts [first(i), first(i + 1)).
+struct Cut {
+    int parts, pieces;
+    __host__ __device__ int first(int i) const { return (int)((int64_t)parts * i / pieces); }
+};
 
 struct ScanArgs {
     const void *logits;
     int64_t stride;  // elements between rows
-    int vocab, k, slices;
-    uint64_t *keys;  // [rows][slices][k], greatest first, 0: none
-    float *top;      // [rows][slices] maximum
-    double *sum;     // [rows][slices] sum of exp(x - maximum); NaN where the slice holds a NaN or +infinity
+    int vocab, k;
+    Cut cut;
+    uint64_t *keys;  // [rows][cut.pieces][k], greatest first, 0: none
+    float *top;      // [rows][cut.pieces] maximum
+    double *sum;     // [rows][cut.pieces] sum of exp(x - maximum); NaN where the piece holds a NaN or +infinity
     unsigned *err;
 };
 
@@ -110,9 +124,12 @@ struct Elems<float> {
 
 struct Shared {
     alignas(128) uint8_t ring[kStages][kStageBytes];
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[kStages];
+    int readers[kStages];  // warps that have read a stage's part
     uint64_t buf[kCap];
-    uint64_t group[256];
+    uint64_t group[kThreads];
+    int note[kNotes];
+    int notes;         // (those past kNotes are not there)
     uint64_t bar;      // keys below it are not among the k greatest
     uint64_t sums[kWarps];
     float tops[kWarps];
@@ -243,9 +260,9 @@ __device__ __forceinline__ float greatest_of(const uint4 &v)
 // A thread's greatest logit so far and the sum of exp(x - m).
 struct Sum {
     float m = -INFINITY, s = 0.0f;
-    // V vectors with the greatest logit top
-    template <typename T, int V>
-    __device__ __forceinline__ void add(const uint4 (&v)[V], float top)
+    // a part's vectors, with the greatest logit top
+    template <typename T>
+    __device__ __forceinline__ void add(const uint4 (&v)[kVecs], float top)
     {
         constexpr int N = Elems<T>::N;
         if (top > m) {
@@ -256,7 +273,7 @@ struct Sum {
         const float neg = m == -INFINITY ? 0.0f : -m;
         float2 part = {0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < kVecs; ++i) {
             float x[N];
             Elems<T>::widen(v[i], x);
 #pragma unroll
@@ -270,7 +287,7 @@ struct Sum {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) beam_scan_kernel(const __grid_constant__ ScanArgs a)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) beam_scan_kernel(const __grid_constant__ ScanArgs a)
 {
     using El = Elems<T>;
     constexpr int N = El::N;
@@ -278,87 +295,91 @@ __global__ void __launch_bounds__(kThreads, 2) beam_scan_kernel(const __grid_con
     Shared &sh = *reinterpret_cast<Shared *>(beam_smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
-        sh.n = 0;
+        sh.n = sh.notes = 0;
         sh.bar = 0;
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], kWarps);
+            sh.readers[i] = 0;
         }
         fence_mbarrier_init();
     }
     griddep_wait();
     griddep_launch_dependents();
-    const int slice = blockIdx.x;
+    const int k = a.k;
+    // groups of a warp: 4 k in all, and k of them have k (32 / p) threads' 32 logits, kPartKeys at most
+    const int p = k <= 4 ? 2 : k <= 8 ? 4 : k <= 16 ? 8 : k <= 32 ? 16 : 32;
+    const uint64_t policy = l2_policy_evict_first();
+    const int piece = blockIdx.x, r0 = a.cut.first(piece), parts = a.cut.first(piece + 1) - r0;
     const int64_t row = (int64_t)blockIdx.y * gridDim.z + blockIdx.z;  // (search, beam)
     Row<T> rw;
     rw.x = static_cast<const T *>(a.logits) + row * a.stride;
     rw.vocab = a.vocab;
     rw.lead = (int)(((uintptr_t)rw.x & 15u) / sizeof(T));
-    const int parts = (a.vocab + kPartVecs * N - 1) / (kPartVecs * N);
-    const int r0 = (int)((int64_t)parts * slice / a.slices), r1 = (int)((int64_t)parts * (slice + 1) / a.slices);
-    const int k = a.k;
-    const int p = k <= 4 ? 1 : k <= 8 ? 2 : k <= 16 ? 4 : k <= 32 ? 8 : 16;  // groups of a warp
-    const uint64_t policy = l2_policy_evict_first();
-    // part r into its stage: the vectors that are inside the row, and the one behind the part's last
-    auto issue = [&](int r) {
-        const int u0 = max(r * kPartVecs, rw.inner0()), u1 = min((r + 1) * kPartVecs + (rw.lead ? 1 : 0), rw.inner1());
-        const int st = (r - r0) % kStages;
+    // part q into its stage: the vectors that are inside the row, and the one behind the part's last
+    auto issue = [&](int q) {
+        const int v0 = (r0 + q) * kPartVecs, st = q % kStages;
+        const int u0 = max(v0, rw.inner0()), u1 = min(v0 + kPartVecs + (rw.lead ? 1 : 0), rw.inner1());
         const uint32_t bytes = u1 > u0 ? 16u * (uint32_t)(u1 - u0) : 0u;
         mbar_arrive_expect_tx(&sh.full[st], bytes);
-        if (bytes) bulk_g2s(sh.ring[st] + (u0 - r * kPartVecs) * 16, rw.at(u0), bytes, &sh.full[st], policy);
+        if (bytes) bulk_g2s(sh.ring[st] + (u0 - v0) * 16, rw.at(u0), bytes, &sh.full[st], policy);
     };
     if (tid == 0)
-        for (int r = r0; r < min(r1, r0 + kStages); ++r) issue(r);
+        for (int q = 0; q < min(parts, kStages); ++q) issue(q);
     __syncthreads();
     bool ok = true;
-    // this thread's two vectors of part r (none past the slice)
-    auto fetch = [&](int r, uint4 *v) {
-        v[0] = v[1] = make_uint4(El::kLow, El::kLow, El::kLow, El::kLow);
-        if (r >= r1) return;
-        const int st = (r - r0) % kStages;
-        ok = ok && __all_sync(kFull, mbar_wait_bounded(&sh.full[st], ((r - r0) / kStages) & 1));
+    // this thread's vectors of part q
+    auto fetch = [&](int q, uint4 (&v)[kVecs]) {
+        const int st = q % kStages, v0 = (r0 + q) * kPartVecs;
+        ok = ok && __all_sync(kFull, mbar_wait_bounded(&sh.full[st], (q / kStages) & 1));
         const uint32_t ring = smem_u32(sh.ring[st]);
+        const bool inner = v0 >= rw.inner0() && v0 + kPartVecs < rw.inner1();
+        if (inner) {  // (and the vector behind the part is)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            v[i] = rw.elements(r * kPartVecs + i * kThreads + tid, [&](int u) { return lds128(ring + (u - r * kPartVecs) * 16); });
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.empty[st]);
-    };
-    // part r's stage to the part kStages further on, when all warps have read it
-    auto refill = [&](int r) {
-        if (warp != 0 || r < r0 || r + kStages >= r1) return;
-        const int st = (r - r0) % kStages;
-        ok = ok && __all_sync(kFull, mbar_wait_bounded(&sh.empty[st], ((r - r0) / kStages) & 1));
-        if (lane == 0) {
-            fence_proxy_async_smem();
-            issue(r + kStages);
+            for (int i = 0; i < kVecs; ++i) v[i] = lds128(ring + (i * kThreads + tid) * 16);
+            if (rw.lead) {
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i) v[i] = rw.line_up(v[i], lds128(ring + (i * kThreads + tid + 1) * 16));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i)
+                v[i] = rw.elements(v0 + i * kThreads + tid, [&](int u) { return lds128(ring + (u - v0) * 16); });
         }
+        // the last warp to have read a part has its stage filled again: none waits for another
+        __threadfence_block();
         __syncwarp();
+        if (lane == 0 && atomicAdd(&sh.readers[st], 1) == kWarps - 1) {
+            sh.readers[st] = 0;
+            if (q + kStages < parts) {
+                __threadfence_block();
+                fence_proxy_async_smem();
+                issue(q + kStages);
+            }
+        }
     };
-    auto greatest = [&](const uint4 *v, int n) -> float {
-        float top = greatest_of<T>(v[0]);
-        for (int i = 1; i < n; ++i) top = fmaxf(top, greatest_of<T>(v[i]));
-        return top;
+    static_assert(kVecs == 4, "");
+    auto greatest = [&](const uint4 (&v)[kVecs], float (&tops)[kVecs]) -> float {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) tops[i] = greatest_of<T>(v[i]);
+        return fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
     };
-    // index in the row of vector i's first element, for the vectors of parts r, r + 1
-    auto first = [&](int r, int i) -> int { return (r * kPartVecs + i * kThreads + tid) * N; };
+    // index in the row of the first element of this thread's vector i of part q
+    auto first = [&](int q, int i) -> int { return ((r0 + q) * kPartVecs + i * kThreads + tid) * N; };
     // the key of a thread's greatest logit: of equal ones the first
-    auto key_at = [&](const uint4 (&v)[4], int r, float top) -> uint64_t {
+    auto key_at = [&](const uint4 (&v)[kVecs], int q, float top) -> uint64_t {
         if (!(top > -INFINITY)) return 0;
         int at = 0;
 #pragma unroll
-        for (int i = 3; i >= 0; --i) {
+        for (int i = kVecs - 1; i >= 0; --i) {
             float x[N];
             El::widen(v[i], x);
 #pragma unroll
             for (int e = N - 1; e >= 0; --e) at = x[e] == top ? i * (kThreads * N) + e : at;
         }
-        return key_of(top, first(r, 0) + at);
+        return key_of(top, first(q, 0) + at);
     };
     // adds a vector's logits that reach the bar to the buffer
     auto add_keys = [&](const uint4 &w, int at0, uint64_t bar) {
-        const float top = greatest_of<T>(w);
-        if (!(top > -INFINITY) || (bar && top < logit_of(bar))) return;
         float x[N];
         El::widen(w, x);
 #pragma unroll
@@ -370,39 +391,34 @@ __global__ void __launch_bounds__(kThreads, 2) beam_scan_kernel(const __grid_con
             if (at < kCap) sh.buf[at] = key;
         }
     };
+    auto note = [&](int q, int i) {
+        const int at = atomicAdd(&sh.notes, 1);
+        if (at < kNotes) sh.note[at] = first(q, i);
+    };
     Sum sum;
-    {
-        uint4 v[4];
-        fetch(r0, v);
-        fetch(r0 + 1, v + 2);
-        const float top = greatest(v, 4);
-        raise_bar(sh, key_at(v, r0, top), k, p);
-        const uint64_t bar = sh.bar;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) add_keys(v[i], first(r0, i), bar);
-        sum.add<T, 4>(v, top);
-        refill(r0);
-    }
+    uint4 v[kVecs];
+    float tops[kVecs];
+    fetch(0, v);
+    float top = greatest(v, tops);
+    raise_bar(sh, key_at(v, 0, top), k, p);
     const uint64_t bar = sh.bar;
-    // ---- the rest of the slice, every warp for itself ----
     const float high = bar ? logit_of(bar) : -INFINITY;
-    for (int r = r0 + 2; r < r1; ++r) {
-        uint4 v[2];
-        fetch(r, v);
-        refill(r - 1);
-        const float top = greatest(v, 2);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+        if (tops[i] > -INFINITY && tops[i] >= high) note(0, i);
+    sum.add<T>(v, top);
+    // ---- the rest of the piece, every warp for itself ----
+    for (int q = 1; q < parts; ++q) {
+        fetch(q, v);
+        top = greatest(v, tops);
         if (top > high) {  // (an equal one has a greater index than the bar's)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) add_keys(v[i], first(r, i), bar);
+            for (int i = 0; i < kVecs; ++i)
+                if (tops[i] > high) note(q, i);
         }
-        sum.add<T, 2>(v, top);
+        sum.add<T>(v, top);
     }
-    if (!ok) {
-        if (lane == 0) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
-        if (warp == 0)  // copies in flight land before the block exits
-            for (int r = max(r0, r1 - kStages); r < r1; ++r) mbar_wait_bounded(&sh.full[(r - r0) % kStages], ((r - r0) / kStages) & 1);
-    }
-    // ---- the slice's maximum and sum ----
+    // ---- the piece's maximum and sum ----
     float M = sum.m;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
@@ -415,33 +431,35 @@ __global__ void __launch_bounds__(kThreads, 2) beam_scan_kernel(const __grid_con
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) f += __shfl_xor_sync(kFull, f, o);
     if (lane == 0) sh.sums[warp] = f;
-    int n = sh.n;  // (no keys are added any more)
+    const int notes = sh.notes;
+    auto read = [&](int i0) -> uint4 { return rw.elements(i0 / N, [&](int u) { return ldg_nc_v4(rw.at(u)); }); };
+    if (notes <= kNotes)
+        for (int i = tid; i < notes; i += kThreads) add_keys(read(sh.note[i]), sh.note[i], bar);
     __syncthreads();
-    if (n > kCap) {  // the buffer ran over: the slice again, part by part
+    int n = sh.n;
+    __syncthreads();
+    if (notes > kNotes || n > kCap) {  // too many: the piece again, part by part
         if (tid == 0) {
             sh.n = 0;
             sh.bar = 0;
         }
         __syncthreads();
-        for (int r = r0; r < r1; r += 2) {
+        for (int q = 0; q < parts; ++q) {
             const int have = sh.n;
-            uint4 v[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] = r + i / 2 < r1 ? rw.elements(first(r, i) / N, [&](int u) { return ldg_nc_v4(rw.at(u)); })
-                                      : make_uint4(El::kLow, El::kLow, El::kLow, El::kLow);
-            raise_bar(sh, key_at(v, r, greatest(v, 4)), k, p);
-            if (have + 4096 > kCap) thin_out(sh, have, k, p, kMaxK);
+            for (int i = 0; i < kVecs; ++i) v[i] = read(first(q, i));
+            raise_bar(sh, key_at(v, q, greatest(v, tops)), k, p);
+            if (have + kPartKeys > kCap) thin_out(sh, have, k, p, kMaxK);
             const uint64_t now = sh.bar;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) add_keys(v[i], first(r, i), now);
+#pragma unroll 1
+            for (int i = 0; i < kVecs; ++i) add_keys(i == 0 ? v[0] : i == 1 ? v[1] : i == 2 ? v[2] : v[3], first(q, i), now);
             __syncthreads();
         }
         n = sh.n;
         __syncthreads();
     }
-    n = thin_out(sh, n, k, p, 256);
-    const int64_t list = row * a.slices + slice;
+    n = thin_out(sh, n, k, p, kThreads);
+    const int64_t list = row * a.cut.pieces + piece;
     if (tid == 0) {
         for (int w = 1; w < kWarps; ++w) f += sh.sums[w];
         a.top[list] = M;
@@ -456,14 +474,21 @@ __global__ void __launch_bounds__(kThreads, 2) beam_scan_kernel(const __grid_con
     } else if (tid < k) {
         a.keys[list * k + tid] = 0;
     }
+    if (!ok) {
+        if (lane == 0) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
+        if (warp == 0)  // copies in flight land before the block exits
+            for (int q = max(0, parts - kStages); q < parts; ++q) mbar_wait_bounded(&sh.full[q % kStages], (q / kStages) & 1);
+    }
 }
+
+static_assert(kBlocksPerSm * (sizeof(Shared) + 1024) <= 232448, "fewer blocks would fit on an SM");
 
 struct MergeArgs {
     const uint64_t *keys;
     const float *top;
     const double *sum;
     const float *scores;  // [batch][beams]
-    int beams, slices, k;
+    int beams, pieces, k;
     int32_t *tokens, *parents;  // [batch][k]
     float *out;                 // [batch][k]
     unsigned *err;
@@ -484,6 +509,7 @@ __device__ __forceinline__ Cand shfl_xor(const Cand &x, int o)
 constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kHold = 16;                        // continuations of a thread, at a time
 constexpr int kMergeCap = 3072;                  // that the merge holds in shared memory
+constexpr int kFewLists = 16;                    // bisected by every continuation: 16 lists of 8 take 0.5 us, the bar 3 us
 
 struct MergeShared {
     Cand buf[kMergeCap];
@@ -524,31 +550,33 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t item = blockIdx.x;
-    const int per_beam = a.slices * a.k, total = a.beams * per_beam;
+    const int per_beam = a.pieces * a.k, total = a.beams * per_beam;
     const uint64_t *keys = a.keys + item * total;
     if (tid == 0) {
         sh.bar = {0, 0};
         sh.n = 0;
     }
-    uint64_t held[kHold];  // the first keys, read while the log-sums are formed
-#pragma unroll
-    for (int i = 0; i < kHold; ++i) held[i] = i * kMergeThreads + tid < total ? keys[i * kMergeThreads + tid] : 0;
-    for (int j = warp; j < a.beams; j += kMergeWarps) {  // a warp a beam, a lane a slice
-        const int64_t l0 = (item * a.beams + j) * a.slices;
-        float M = -INFINITY;
-        for (int i = lane; i < a.slices; i += 32) M = fmaxf(M, a.top[l0 + i]);
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-        double s = 0.0;
-        for (int i = lane; i < a.slices; i += 32) {
-            const float t = a.top[l0 + i];
-            const double x = a.sum[l0 + i];  // (of an infinite maximum NaN)
-            s += t == M || x != x ? x : t == -INFINITY ? 0.0 : x * exp((double)t - (double)M);
-        }
-        for (int o = 16; o >= 1; o >>= 1)
-            if (o < a.slices) s += __shfl_xor_sync(kFull, s, o);  // (lanes past the slices hold 0)
-        if (lane) continue;
-        const float sc = a.scores[item * a.beams + j];
+    auto key_at = [&](int i) -> uint64_t { return i < total ? keys[i] : 0; };
+    uint64_t held = key_at(tid);  // (read while the log-sums are formed)
+    // a lane a piece, as many beams a warp as its lanes have room for
+    int group = 1;
+    while (group < a.pieces && group < 32) group *= 2;
+    for (int j0 = warp * (32 / group); j0 < a.beams; j0 += kMergeWarps * (32 / group)) {
+        const int j = j0 + lane / group, first = lane % group;
+        const bool there = j < a.beams;
+        const int64_t row = item * a.beams + j, l0 = row * a.pieces;
+        const float sc = there ? a.scores[row] : -INFINITY;
+        const float t0 = there && first < a.pieces ? a.top[l0 + first] : -INFINITY;
+        const double x0 = there && first < a.pieces ? a.sum[l0 + first] : 0.0;
+        float M = t0;
+        for (int i = first + 32; there && i < a.pieces; i += 32) M = fmaxf(M, a.top[l0 + i]);
+        for (int o = group / 2; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+        // (of an infinite maximum the sum is NaN)
+        auto scaled = [&](float t, double x) { return t == M || x != x ? x : t == -INFINITY ? 0.0 : x * exp((double)t - (double)M); };
+        double s = scaled(t0, x0);
+        for (int i = first + 32; there && i < a.pieces; i += 32) s += scaled(a.top[l0 + i], a.sum[l0 + i]);
+        for (int o = group / 2; o >= 1; o >>= 1) s += __shfl_xor_sync(kFull, s, o);  // (lanes past the pieces hold 0)
+        if (!there || first) continue;
         const bool odd = sc != -INFINITY && (s != s || sc != sc || sc == INFINITY);
         if (odd) atomicOr(a.err, PKV_DEVERR_NAN);
         sh.shift[j] = odd || sc == -INFINITY || M == -INFINITY ? (double)NAN : (double)sc - log(s);
@@ -565,6 +593,44 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
                 ((uint64_t)(kMaxBeams - 1 - j) << (32 + kTokenBits)) | ((key >> 32) << kTokenBits) |
                     (uint64_t)((1 << kTokenBits) - 1 - index_of(key))};
     };
+    auto put = [&](int rank, const Cand &x) {
+        const int64_t o = item * a.k + rank;
+        const uint64_t u = x.value ^ ((x.value >> 63) ? 1ull << 63 : ~0ull);
+        a.tokens[o] = (1 << kTokenBits) - 1 - (int)(x.tie & ((1 << kTokenBits) - 1));
+        a.parents[o] = kMaxBeams - 1 - (int)(x.tie >> (32 + kTokenBits));
+        a.out[o] = (float)__longlong_as_double((long long)u);
+    };
+    auto put_none = [&](int rank) {  // no continuation is left for this place
+        const int64_t o = item * a.k + rank;
+        a.tokens[o] = a.parents[o] = -1;
+        a.out[o] = -INFINITY;
+    };
+    const int lists = a.beams * a.pieces;
+    if (lists <= kFewLists && total <= kMergeThreads) {
+        // a thread a continuation: its rank is its place in its list and, by bisection, in every other one
+        const Cand x = worth(held, tid);
+        sh.buf[tid] = x;
+        const int live = __syncthreads_count(x.value != 0);
+        if (tid >= live && tid < a.k) put_none(tid);
+        if (!x.value) return;
+        const int own = tid / a.k;
+        int rank = tid - own * a.k;
+        // (not unrolled: code that runs once waits for its instructions)
+#pragma unroll 1
+        for (int l = 0; l < lists; ++l) {
+            if (l == own) continue;
+            int lo = 0, hi = a.k;  // elements [0, lo) are above x, [hi, k) are not
+#pragma unroll 1
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (sh.buf[l * a.k + mid].above(x)) lo = mid + 1;
+                else hi = mid;
+            }
+            rank += lo;
+        }
+        if (rank < a.k) put(rank, x);
+        return;
+    }
     // kHold keys a thread at a time: at least k of them reach the bar, and those that do are of k groups
     const int p = a.k <= 4 ? 2 : a.k <= 8 ? 4 : a.k <= 16 ? 8 : a.k <= 32 ? 16 : 32;  // groups of a warp
     auto greatest = [&](const Cand (&c)[kHold]) -> Cand {
@@ -574,7 +640,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
             if (c[i].above(top)) top = c[i];
         return top;
     };
-    // keeps those of c that reach the bar: 32 / p threads' kHold of k groups, 1024 at most
+    // keeps those of c that reach the bar: of k groups of 32 / p threads with kHold each, 1024 at most
     auto keep = [&](const Cand (&c)[kHold]) {
         const Cand bar = sh.bar;
 #pragma unroll
@@ -588,7 +654,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
 #pragma unroll
         for (int i = 0; i < kHold; ++i) {
             const int at = base + i * kMergeThreads + tid;
-            c[i] = worth(base == 0 ? held[i] : at < total ? keys[at] : 0, at);
+            c[i] = worth(base == 0 && i == 0 ? held : key_at(at), at);
         }
         raise_bar(sh, greatest(c), a.k, p);
         keep(c);
@@ -611,27 +677,22 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
         const Cand x = sh.buf[tid];
         int rank = 0;
         for (int i = 0; i < n; ++i) rank += sh.buf[i].above(x);
-        if (rank < a.k) {
-            const int64_t o = item * a.k + rank;
-            const uint64_t u = x.value ^ ((x.value >> 63) ? 1ull << 63 : ~0ull);
-            a.tokens[o] = (1 << kTokenBits) - 1 - (int)(x.tie & ((1 << kTokenBits) - 1));
-            a.parents[o] = kMaxBeams - 1 - (int)(x.tie >> (32 + kTokenBits));
-            a.out[o] = (float)__longlong_as_double((long long)u);
-        }
-    } else if (tid < a.k) {  // no continuation is left for this place
-        const int64_t o = item * a.k + tid;
-        a.tokens[o] = a.parents[o] = -1;
-        a.out[o] = -INFINITY;
+        if (rank < a.k) put(rank, x);
+    } else if (tid < a.k) {
+        put_none(tid);
     }
 }
 
-// Slices of a row: enough for two blocks on every SM, but two parts each at least, and no more than the merge takes.
-int slices_of(const pkv_pool *pool, int64_t rows, int beams, int vocab, int elem)
+// Pieces of a row: as many as all blocks that run at once have room for, of two parts each at least (the bar comes
+// from the first).
+Cut cut_of(const pkv_pool *pool, int64_t rows, int vocab, int elem)
 {
-    const int64_t part = (int64_t)kPartVecs * (16 / elem);
-    const int64_t parts = (vocab + part - 1) / part;
-    const int64_t want = std::max<int64_t>(1, 2 * (int64_t)pool->num_sms / std::max<int64_t>(1, rows));
-    return (int)std::max<int64_t>(1, std::min({want, (parts + 1) / 2, (int64_t)(kMaxLists / beams)}));
+    const int part = kPartVecs * (16 / elem);
+    Cut c;
+    c.parts = (vocab + part - 1) / part;
+    const int64_t room = (int64_t)kBlocksPerSm * pool->num_sms / std::max<int64_t>(1, rows);
+    c.pieces = (int)std::max<int64_t>(1, std::min<int64_t>(room, c.parts / 2));
+    return c;
 }
 
 // The kernels' shared memory is allowed, once per device.
@@ -651,7 +712,7 @@ pkv_status prepare_scan(const pkv_pool *pool)
     return PKV_OK;
 }
 
-size_t beam_bytes(int64_t rows, int slices, int k) { return (size_t)rows * slices * (8 * (size_t)k + 16); }
+size_t beam_bytes(int64_t rows, const Cut &c, int k) { return (size_t)rows * c.pieces * (8 * (size_t)k + 16); }
 
 pkv_status check_beam(const pkv_pool *pool, const char *who, int batch, int beams, int vocab, int k, int type)
 {
@@ -682,10 +743,10 @@ extern "C" pkv_status paged_beam_reserve_workspace(pkv_pool *pool, int32_t batch
     if (st == PKV_OK) st = check_pool_device(pool, who);
     if (st != PKV_OK) return st;
     size_t most = 0;
-    for (int b = 1; b <= batch; ++b)  // (calls of fewer rows have more slices)
+    for (int b = 1; b <= batch; ++b)  // (rows of smaller calls have more pieces)
         for (int elem : {2, 4}) {
             const int64_t rows = (int64_t)b * beams;
-            most = std::max(most, beam_bytes(rows, slices_of(pool, rows, beams, vocab, elem), k));
+            most = std::max(most, beam_bytes(rows, cut_of(pool, rows, vocab, elem), k));
         }
     return ensure_workspace(pool, most);
 }
@@ -715,26 +776,26 @@ extern "C" pkv_status paged_beam_select(pkv_pool *pool, const void *logits, int3
     }
     st = check_pool_device(pool, who);
     if (st != PKV_OK) return st;
-    const int slices = slices_of(pool, rows, beams, vocab, elem);
+    const Cut cut = cut_of(pool, rows, vocab, elem);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    st = ensure_workspace(pool, beam_bytes(rows, slices, k), s, who);
+    st = ensure_workspace(pool, beam_bytes(rows, cut, k), s, who);
     if (st != PKV_OK) return st;
     st = prepare_scan(pool);
     if (st != PKV_OK) return st;
-    const size_t lists = (size_t)rows * slices;
+    const size_t lists = (size_t)rows * cut.pieces;
     ScanArgs a;
     a.err = pool->err;
     a.logits = logits;
     a.stride = row_stride;
     a.vocab = vocab;
     a.k = k;
-    a.slices = slices;
+    a.cut = cut;
     a.keys = static_cast<uint64_t *>(pool->ws);
     a.sum = reinterpret_cast<double *>(a.keys + lists * k);
     a.top = reinterpret_cast<float *>(a.sum + lists);
     {
         LaunchScope ls(pool, kDecode, s);
-        const dim3 grid((unsigned)slices, (unsigned)batch, (unsigned)beams);
+        const dim3 grid((unsigned)cut.pieces, (unsigned)batch, (unsigned)beams);
         cudaError_t e = elem == 4 ? launch_pdl(beam_scan_kernel<float>, grid, dim3(kThreads), sizeof(Shared), s, a)
                                   : launch_pdl(beam_scan_kernel<__nv_bfloat16>, grid, dim3(kThreads), sizeof(Shared), s, a);
         ls.done();
@@ -746,7 +807,7 @@ extern "C" pkv_status paged_beam_select(pkv_pool *pool, const void *logits, int3
     m.sum = a.sum;
     m.scores = scores;
     m.beams = beams;
-    m.slices = slices;
+    m.pieces = cut.pieces;
     m.k = k;
     m.tokens = tokens;
     m.parents = parents;
