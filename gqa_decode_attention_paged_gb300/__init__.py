@@ -779,9 +779,9 @@ def paged_beam_select(pool: Pool, logits, scores, k: int, stream=None):
         raise ValueError(f"logits must hold rows of adjacent values at equal distances (strides {logits.stride()})")
     k = int(k)
     sp = _fast_ptr(pool, scores, "scores", torch.float32, (B, beams))
-    shape = (B, max(k, 0))
-    tokens, parents = (_output(shape, logits.device, stream, torch.int32) for _ in range(2))
-    best = _output(shape, logits.device, stream, torch.float32)
+    shape, dev = (B, max(k, 0)), logits.device
+    tokens, parents = _output(shape, dev, stream, torch.int32), _output(shape, dev, stream, torch.int32)
+    best = _output(shape, dev, stream, torch.float32)
     _check(load().paged_beam_select(pool.handle, logits.data_ptr(), kind, sj, sp, B, beams, vocab, k, tokens.data_ptr(),
                                     parents.data_ptr(), best.data_ptr(), _raw_stream(pool, stream)))
     return tokens, parents, best
@@ -807,13 +807,18 @@ def paged_beam_reorder(pool: Pool, parents, block_tables, context_lens, spare_bl
     pp = _fast_ptr(pool, parents, "parents", torch.int32, (B, k))
     tp = _fast_ptr(pool, block_tables, "block_tables", torch.int32, (n, W))
     cp = _fast_ptr(pool, context_lens, "context_lens", torch.int32, (n,))
-    sp = _fast_ptr(pool, spare_blocks, "spare_blocks", torch.int32, (B * k,))
+    rows = B * k
+    sp = _fast_ptr(pool, spare_blocks, "spare_blocks", torch.int32, (rows,))
     if tables_out is None:
-        tables_out = _output((B * k, W), parents.device, stream, torch.int32)
+        tables_out = _output((rows, W), parents.device, stream, torch.int32)
+        to = tables_out.data_ptr()
+    else:
+        to = _fast_ptr(pool, tables_out, "tables_out", torch.int32, (rows, W))
     if lens_out is None:
-        lens_out = _output((B * k,), parents.device, stream, torch.int32)
-    to = _fast_ptr(pool, tables_out, "tables_out", torch.int32, (B * k, W))
-    lo = _fast_ptr(pool, lens_out, "lens_out", torch.int32, (B * k,))
+        lens_out = _output((rows,), parents.device, stream, torch.int32)
+        lo = lens_out.data_ptr()
+    else:
+        lo = _fast_ptr(pool, lens_out, "lens_out", torch.int32, (rows,))
     _check(load().paged_beam_reorder(pool.handle, pp, B, n // B if B else 1, k, tp, W, cp, sp, to, lo,
                                      _raw_stream(pool, stream)))
     return tables_out, lens_out

@@ -7,10 +7,10 @@
 // only those need v.
 //
 // What bounds it: HBM, the logits read once; close behind it the instructions
-// (about five per logit).  Two launches: a scan of the rows, cut into pieces so
-// that every SM has three blocks where the rows are few, leaves each piece's
-// maximum, sum of exponentials and k greatest logits; a merge takes each
-// search's pieces.
+// (about five per logit).  One launch: a scan of the rows, cut into pieces so that
+// every SM has three blocks where the rows are few, leaves each piece's maximum,
+// sum of exponentials and k greatest logits; the block that is the last of a
+// search to get there merges them (a launch of its own took 4 us more).
 //
 // Reading.  A piece streams through a ring of three parts of 16 KiB in shared
 // memory (bulk copies: a vector a thread ahead kept 64 KiB in flight on an SM and
@@ -59,7 +59,6 @@ constexpr int kMaxK = 64, kMaxBeams = 64;
 constexpr int kPartKeys = 2048;                  // of a part, that reach its bar, at most
 constexpr int kCap = 2304;                       // keys the buffer holds: those, k kept ones, some more
 constexpr int kNotes = 1280;                     // vectors that can be noted
-constexpr int kMergeThreads = 256;
 
 // How rows are cut: piece i of a row has parts [first(i), first(i + 1)).
 struct Cut {
@@ -67,14 +66,18 @@ struct Cut {
     __host__ __device__ int first(int i) const { return (int)((int64_t)parts * i / pieces); }
 };
 
-struct ScanArgs {
+struct Args {
     const void *logits;
-    int64_t stride;  // elements between rows
+    int64_t stride;       // elements between rows
     int vocab, k;
     Cut cut;
-    uint64_t *keys;  // [rows][cut.pieces][k], greatest first, 0: none
-    float *top;      // [rows][cut.pieces] maximum
-    double *sum;     // [rows][cut.pieces] sum of exp(x - maximum); NaN where the piece holds a NaN or +infinity
+    const float *scores;  // [batch][beams]
+    uint64_t *keys;       // [rows][cut.pieces][k], greatest first, 0: none
+    float *top;           // [rows][cut.pieces] maximum
+    double *sum;          // [rows][cut.pieces] sum of exp(x - maximum); NaN where the piece holds a NaN or +infinity
+    unsigned *tickets;    // [batch] blocks of a search that have left their lists; 0 before and after a call
+    int32_t *tokens, *parents;  // [batch][k]
+    float *out;                 // [batch][k]
     unsigned *err;
 };
 
@@ -134,6 +137,7 @@ struct Shared {
     uint64_t sums[kWarps];
     float tops[kWarps];
     int n;             // keys in buf (those past kCap are not there)
+    bool last;         // the block merges
 };
 
 __device__ __forceinline__ uint64_t max64(uint64_t a, uint64_t b) { return a > b ? a : b; }
@@ -184,6 +188,189 @@ __device__ __forceinline__ int thin_out(Shared &sh, int n, int k, int p, int mos
         __syncthreads();  // (read by all before anyone adds to it)
     }
     return n;
+}
+
+// A continuation: its worth as an ordered integer (0: none), then what settles equal worths: the lower beam, then the
+// greater logit (a beam's different logits may have one worth in 64 bits), then the lower token.
+struct Cand {
+    uint64_t value, tie;
+    __device__ __forceinline__ bool above(const Cand &y) const { return value != y.value ? value > y.value : tie > y.tie; }
+};
+constexpr int kTokenBits = 22;
+__device__ __forceinline__ Cand shfl_xor(const Cand &x, int o)
+{
+    return {__shfl_xor_sync(kFull, x.value, o), __shfl_xor_sync(kFull, x.tie, o)};
+}
+
+constexpr int kHold = 8;                         // continuations of a thread, at a time
+constexpr int kMergeKeep = 1024;                 // kept between rounds
+constexpr int kMergeCap = kMergeKeep + kHold * kThreads / 4;
+constexpr int kFewLists = 16;                    // bisected by every continuation: 16 lists of 8 take 0.5 us, the bar 3 us
+
+struct MergeShared {
+    Cand buf[kMergeCap];
+    Cand group[kThreads];
+    Cand bar;
+    int n;
+    double shift[kMaxBeams];   // score - log of the sum of exp(x - m); NaN: no continuations
+    float highest[kMaxBeams];  // m: v = (x - m) + shift, in which large logits cost nothing
+};
+
+// The k-th greatest of the groups' greatest continuations, if as many groups have one: as raise_bar, 8 p groups.
+__device__ __forceinline__ void raise_bar(MergeShared &sh, Cand mine, int k, int p)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, size = 32 / p;
+    for (int o = size / 2; o >= 1; o >>= 1) {
+        const Cand y = shfl_xor(mine, o);
+        if (y.above(mine)) mine = y;
+    }
+    if (lane % size == 0) sh.group[warp * p + lane / size] = mine;
+    __syncthreads();
+    const int groups = kWarps * p;
+    if (tid < groups) {
+        const Cand x = sh.group[tid];
+        int rank = 0;
+        for (int i = 0; i < groups; ++i) rank += sh.group[i].above(x);
+        if (x.value && rank == k - 1 && x.above(sh.bar)) sh.bar = x;  // (one thread: continuations are unique)
+    }
+    __syncthreads();
+}
+
+// One search: its beams' log-sums, the worth of its lists' continuations, and the k greatest of them, found as the
+// scan finds a row's (k rounds over the lists' heads took 0.65 us each).
+__device__ __noinline__ void merge(MergeShared &sh, const Args &a, int beams, int64_t item)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int pieces = a.cut.pieces, per_beam = pieces * a.k, total = beams * per_beam;
+    const uint64_t *keys = a.keys + item * total;
+    if (tid == 0) {
+        sh.bar = {0, 0};
+        sh.n = 0;
+    }
+    auto key_at = [&](int i) -> uint64_t { return i < total ? __ldcg(keys + i) : 0; };  // (from the L2: other blocks wrote them)
+    uint64_t held = key_at(tid);  // (read while the log-sums are formed)
+    // a lane a piece, as many beams a warp as its lanes have room for
+    int group = 1;
+    while (group < pieces && group < 32) group *= 2;
+    for (int j0 = warp * (32 / group); j0 < beams; j0 += kWarps * (32 / group)) {
+        const int j = j0 + lane / group, first = lane % group;
+        const bool there = j < beams;
+        const int64_t row = item * beams + j, l0 = row * pieces;
+        const float sc = there ? a.scores[row] : -INFINITY;
+        const float t0 = there && first < pieces ? __ldcg(a.top + l0 + first) : -INFINITY;
+        const double x0 = there && first < pieces ? __ldcg(a.sum + l0 + first) : 0.0;
+        float M = t0;
+        for (int i = first + 32; there && i < pieces; i += 32) M = fmaxf(M, __ldcg(a.top + l0 + i));
+        for (int o = group / 2; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+        // (of an infinite maximum the sum is NaN)
+        auto scaled = [&](float t, double x) { return t == M || x != x ? x : t == -INFINITY ? 0.0 : x * exp((double)t - (double)M); };
+        double s = scaled(t0, x0);
+        for (int i = first + 32; there && i < pieces; i += 32) s += scaled(__ldcg(a.top + l0 + i), __ldcg(a.sum + l0 + i));
+        for (int o = group / 2; o >= 1; o >>= 1) s += __shfl_xor_sync(kFull, s, o);  // (lanes past the pieces hold 0)
+        if (!there || first) continue;
+        const bool odd = sc != -INFINITY && (s != s || sc != sc || sc == INFINITY);
+        if (odd) atomicOr(a.err, PKV_DEVERR_NAN);
+        sh.shift[j] = odd || sc == -INFINITY || M == -INFINITY ? (double)NAN : (double)sc - log(s);
+        sh.highest[j] = M;
+    }
+    __syncthreads();
+    auto worth = [&](uint64_t key, int i) -> Cand {
+        if (!key) return {0, 0};
+        const int j = i / per_beam;
+        const double v = ((double)logit_of(key) - (double)sh.highest[j]) + sh.shift[j];
+        if (v != v) return {0, 0};
+        const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
+        return {u ^ ((u >> 63) ? ~0ull : 1ull << 63),
+                ((uint64_t)(kMaxBeams - 1 - j) << (32 + kTokenBits)) | ((key >> 32) << kTokenBits) |
+                    (uint64_t)((1 << kTokenBits) - 1 - index_of(key))};
+    };
+    auto put = [&](int rank, const Cand &x) {
+        const int64_t o = item * a.k + rank;
+        const uint64_t u = x.value ^ ((x.value >> 63) ? 1ull << 63 : ~0ull);
+        a.tokens[o] = (1 << kTokenBits) - 1 - (int)(x.tie & ((1 << kTokenBits) - 1));
+        a.parents[o] = kMaxBeams - 1 - (int)(x.tie >> (32 + kTokenBits));
+        a.out[o] = (float)__longlong_as_double((long long)u);
+    };
+    auto put_none = [&](int rank) {  // no continuation is left for this place
+        const int64_t o = item * a.k + rank;
+        a.tokens[o] = a.parents[o] = -1;
+        a.out[o] = -INFINITY;
+    };
+    const int lists = beams * pieces;
+    if (lists <= kFewLists && total <= kThreads) {
+        // a thread a continuation: its rank is its place in its list and, by bisection, in every other one
+        const Cand x = worth(held, tid);
+        sh.buf[tid] = x;
+        const int live = __syncthreads_count(x.value != 0);
+        if (tid >= live && tid < a.k) put_none(tid);
+        if (!x.value) return;
+        const int own = tid / a.k;
+        int rank = tid - own * a.k;
+        // (not unrolled: code that runs once waits for its instructions)
+#pragma unroll 1
+        for (int l = 0; l < lists; ++l) {
+            if (l == own) continue;
+            int lo = 0, hi = a.k;  // elements [0, lo) are above x, [hi, k) are not
+#pragma unroll 1
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (sh.buf[l * a.k + mid].above(x)) lo = mid + 1;
+                else hi = mid;
+            }
+            rank += lo;
+        }
+        if (rank < a.k) put(rank, x);
+        return;
+    }
+    // kHold keys a thread at a time: at least k of them reach the bar, and those that do are of k groups
+    const int p = a.k <= 4 ? 2 : a.k <= 8 ? 4 : a.k <= 16 ? 8 : a.k <= 32 ? 16 : 32;  // groups of a warp
+    auto greatest = [&](const Cand (&c)[kHold]) -> Cand {
+        Cand top = c[0];
+#pragma unroll
+        for (int i = 1; i < kHold; ++i)
+            if (c[i].above(top)) top = c[i];
+        return top;
+    };
+    // keeps those of c that reach the bar: of k groups of 32 / p threads with kHold each, 512 at most
+    auto keep = [&](const Cand (&c)[kHold]) {
+        const Cand bar = sh.bar;
+#pragma unroll
+        for (int i = 0; i < kHold; ++i)
+            if (c[i].value && !bar.above(c[i])) sh.buf[atomicAdd(&sh.n, 1)] = c[i];
+        __syncthreads();
+    };
+    for (int base = 0; base < total; base += kHold * kThreads) {
+        Cand c[kHold];
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+            const int at = base + i * kThreads + tid;
+            c[i] = worth(base == 0 && i == 0 ? held : key_at(at), at);
+        }
+        raise_bar(sh, greatest(c), a.k, p);
+        keep(c);
+        // fewer again, before the next ones or the end
+        for (int n = sh.n; n > (base + kHold * kThreads < total ? kMergeKeep : kThreads);) {
+            __syncthreads();  // (n is read)
+#pragma unroll
+            for (int i = 0; i < kHold; ++i) c[i] = i * kThreads + tid < n ? sh.buf[i * kThreads + tid] : Cand{0, 0};
+            raise_bar(sh, greatest(c), a.k, p);
+            if (tid == 0) sh.n = 0;
+            __syncthreads();
+            keep(c);
+            n = sh.n;
+        }
+        __syncthreads();
+    }
+    // ---- in order ----
+    const int n = sh.n;
+    if (tid < n) {
+        const Cand x = sh.buf[tid];
+        int rank = 0;
+        for (int i = 0; i < n; ++i) rank += sh.buf[i].above(x);
+        if (rank < a.k) put(rank, x);
+    } else if (tid < a.k) {
+        put_none(tid);
+    }
 }
 
 // A row of logits as 16-byte aligned vectors u, elements u N - lead .. + N - 1.
@@ -287,7 +474,7 @@ struct Sum {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) beam_scan_kernel(const __grid_constant__ ScanArgs a)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) beam_select_kernel(const __grid_constant__ Args a)
 {
     using El = Elems<T>;
     constexpr int N = El::N;
@@ -474,214 +661,30 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) beam_scan_kernel(const
     } else if (tid < k) {
         a.keys[list * k + tid] = 0;
     }
+    // ---- the last block of the search takes all its lists ----
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+        unsigned *ticket = a.tickets + blockIdx.y;
+        const unsigned blocks = gridDim.x * gridDim.z;
+        sh.last = atomicAdd(ticket, 1u) == blocks - 1;
+        if (sh.last) *ticket = 0;  // (nobody else comes)
+        __threadfence();
+    }
+    __syncthreads();
     if (!ok) {
         if (lane == 0) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
         if (warp == 0)  // copies in flight land before the block exits
             for (int q = max(0, parts - kStages); q < parts; ++q) mbar_wait_bounded(&sh.full[q % kStages], (q / kStages) & 1);
     }
+    if (sh.last) {
+        __syncthreads();  // (read by all: the merge has the same memory)
+        merge(*reinterpret_cast<MergeShared *>(beam_smem), a, (int)gridDim.z, blockIdx.y);
+    }
 }
 
 static_assert(kBlocksPerSm * (sizeof(Shared) + 1024) <= 232448, "fewer blocks would fit on an SM");
-
-struct MergeArgs {
-    const uint64_t *keys;
-    const float *top;
-    const double *sum;
-    const float *scores;  // [batch][beams]
-    int beams, pieces, k;
-    int32_t *tokens, *parents;  // [batch][k]
-    float *out;                 // [batch][k]
-    unsigned *err;
-};
-
-// A continuation: its worth as an ordered integer (0: none), then what settles equal worths: the lower beam, then the
-// greater logit (a beam's different logits may have one worth in 64 bits), then the lower token.
-struct Cand {
-    uint64_t value, tie;
-    __device__ __forceinline__ bool above(const Cand &y) const { return value != y.value ? value > y.value : tie > y.tie; }
-};
-constexpr int kTokenBits = 22;
-__device__ __forceinline__ Cand shfl_xor(const Cand &x, int o)
-{
-    return {__shfl_xor_sync(kFull, x.value, o), __shfl_xor_sync(kFull, x.tie, o)};
-}
-
-constexpr int kMergeWarps = kMergeThreads / 32;
-constexpr int kHold = 16;                        // continuations of a thread, at a time
-constexpr int kMergeCap = 3072;                  // that the merge holds in shared memory
-constexpr int kFewLists = 16;                    // bisected by every continuation: 16 lists of 8 take 0.5 us, the bar 3 us
-
-struct MergeShared {
-    Cand buf[kMergeCap];
-    Cand group[kMergeThreads];
-    Cand bar;
-    int n;
-    double shift[kMaxBeams];   // score - log of the sum of exp(x - m); NaN: no continuations
-    float highest[kMaxBeams];  // m: v = (x - m) + shift, in which large logits cost nothing
-};
-
-// The k-th greatest of the groups' greatest continuations, if as many groups have one: as raise_bar, 8 p groups.
-__device__ __forceinline__ void raise_bar(MergeShared &sh, Cand mine, int k, int p)
-{
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, size = 32 / p;
-    for (int o = size / 2; o >= 1; o >>= 1) {
-        const Cand y = shfl_xor(mine, o);
-        if (y.above(mine)) mine = y;
-    }
-    if (lane % size == 0) sh.group[warp * p + lane / size] = mine;
-    __syncthreads();
-    const int groups = kMergeWarps * p;
-    if (tid < groups) {
-        const Cand x = sh.group[tid];
-        int rank = 0;
-        for (int i = 0; i < groups; ++i) rank += sh.group[i].above(x);
-        if (x.value && rank == k - 1 && x.above(sh.bar)) sh.bar = x;  // (one thread: continuations are unique)
-    }
-    __syncthreads();
-}
-
-// One search: its beams' log-sums, the worth of its lists' continuations, and the k greatest of them, found as the
-// scan finds a row's (k rounds over the lists' heads took 0.65 us each).
-__global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_constant__ MergeArgs a)
-{
-    extern __shared__ __align__(16) uint8_t merge_smem[];
-    MergeShared &sh = *reinterpret_cast<MergeShared *>(merge_smem);
-    griddep_wait();
-    griddep_launch_dependents();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t item = blockIdx.x;
-    const int per_beam = a.pieces * a.k, total = a.beams * per_beam;
-    const uint64_t *keys = a.keys + item * total;
-    if (tid == 0) {
-        sh.bar = {0, 0};
-        sh.n = 0;
-    }
-    auto key_at = [&](int i) -> uint64_t { return i < total ? keys[i] : 0; };
-    uint64_t held = key_at(tid);  // (read while the log-sums are formed)
-    // a lane a piece, as many beams a warp as its lanes have room for
-    int group = 1;
-    while (group < a.pieces && group < 32) group *= 2;
-    for (int j0 = warp * (32 / group); j0 < a.beams; j0 += kMergeWarps * (32 / group)) {
-        const int j = j0 + lane / group, first = lane % group;
-        const bool there = j < a.beams;
-        const int64_t row = item * a.beams + j, l0 = row * a.pieces;
-        const float sc = there ? a.scores[row] : -INFINITY;
-        const float t0 = there && first < a.pieces ? a.top[l0 + first] : -INFINITY;
-        const double x0 = there && first < a.pieces ? a.sum[l0 + first] : 0.0;
-        float M = t0;
-        for (int i = first + 32; there && i < a.pieces; i += 32) M = fmaxf(M, a.top[l0 + i]);
-        for (int o = group / 2; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-        // (of an infinite maximum the sum is NaN)
-        auto scaled = [&](float t, double x) { return t == M || x != x ? x : t == -INFINITY ? 0.0 : x * exp((double)t - (double)M); };
-        double s = scaled(t0, x0);
-        for (int i = first + 32; there && i < a.pieces; i += 32) s += scaled(a.top[l0 + i], a.sum[l0 + i]);
-        for (int o = group / 2; o >= 1; o >>= 1) s += __shfl_xor_sync(kFull, s, o);  // (lanes past the pieces hold 0)
-        if (!there || first) continue;
-        const bool odd = sc != -INFINITY && (s != s || sc != sc || sc == INFINITY);
-        if (odd) atomicOr(a.err, PKV_DEVERR_NAN);
-        sh.shift[j] = odd || sc == -INFINITY || M == -INFINITY ? (double)NAN : (double)sc - log(s);
-        sh.highest[j] = M;
-    }
-    __syncthreads();
-    auto worth = [&](uint64_t key, int i) -> Cand {
-        if (!key) return {0, 0};
-        const int j = i / per_beam;
-        const double v = ((double)logit_of(key) - (double)sh.highest[j]) + sh.shift[j];
-        if (v != v) return {0, 0};
-        const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
-        return {u ^ ((u >> 63) ? ~0ull : 1ull << 63),
-                ((uint64_t)(kMaxBeams - 1 - j) << (32 + kTokenBits)) | ((key >> 32) << kTokenBits) |
-                    (uint64_t)((1 << kTokenBits) - 1 - index_of(key))};
-    };
-    auto put = [&](int rank, const Cand &x) {
-        const int64_t o = item * a.k + rank;
-        const uint64_t u = x.value ^ ((x.value >> 63) ? 1ull << 63 : ~0ull);
-        a.tokens[o] = (1 << kTokenBits) - 1 - (int)(x.tie & ((1 << kTokenBits) - 1));
-        a.parents[o] = kMaxBeams - 1 - (int)(x.tie >> (32 + kTokenBits));
-        a.out[o] = (float)__longlong_as_double((long long)u);
-    };
-    auto put_none = [&](int rank) {  // no continuation is left for this place
-        const int64_t o = item * a.k + rank;
-        a.tokens[o] = a.parents[o] = -1;
-        a.out[o] = -INFINITY;
-    };
-    const int lists = a.beams * a.pieces;
-    if (lists <= kFewLists && total <= kMergeThreads) {
-        // a thread a continuation: its rank is its place in its list and, by bisection, in every other one
-        const Cand x = worth(held, tid);
-        sh.buf[tid] = x;
-        const int live = __syncthreads_count(x.value != 0);
-        if (tid >= live && tid < a.k) put_none(tid);
-        if (!x.value) return;
-        const int own = tid / a.k;
-        int rank = tid - own * a.k;
-        // (not unrolled: code that runs once waits for its instructions)
-#pragma unroll 1
-        for (int l = 0; l < lists; ++l) {
-            if (l == own) continue;
-            int lo = 0, hi = a.k;  // elements [0, lo) are above x, [hi, k) are not
-#pragma unroll 1
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (sh.buf[l * a.k + mid].above(x)) lo = mid + 1;
-                else hi = mid;
-            }
-            rank += lo;
-        }
-        if (rank < a.k) put(rank, x);
-        return;
-    }
-    // kHold keys a thread at a time: at least k of them reach the bar, and those that do are of k groups
-    const int p = a.k <= 4 ? 2 : a.k <= 8 ? 4 : a.k <= 16 ? 8 : a.k <= 32 ? 16 : 32;  // groups of a warp
-    auto greatest = [&](const Cand (&c)[kHold]) -> Cand {
-        Cand top = c[0];
-#pragma unroll
-        for (int i = 1; i < kHold; ++i)
-            if (c[i].above(top)) top = c[i];
-        return top;
-    };
-    // keeps those of c that reach the bar: of k groups of 32 / p threads with kHold each, 1024 at most
-    auto keep = [&](const Cand (&c)[kHold]) {
-        const Cand bar = sh.bar;
-#pragma unroll
-        for (int i = 0; i < kHold; ++i)
-            if (c[i].value && !bar.above(c[i])) sh.buf[atomicAdd(&sh.n, 1)] = c[i];
-        __syncthreads();
-    };
-    static_assert(kMergeCap >= 2048 + kHold * kMergeThreads / 4, "");
-    for (int base = 0; base < total; base += kHold * kMergeThreads) {
-        Cand c[kHold];
-#pragma unroll
-        for (int i = 0; i < kHold; ++i) {
-            const int at = base + i * kMergeThreads + tid;
-            c[i] = worth(base == 0 && i == 0 ? held : key_at(at), at);
-        }
-        raise_bar(sh, greatest(c), a.k, p);
-        keep(c);
-        // fewer again, before the next ones or the end
-        for (int n = sh.n; n > (base + kHold * kMergeThreads < total ? 2048 : kMergeThreads);) {
-            __syncthreads();  // (n is read)
-#pragma unroll
-            for (int i = 0; i < kHold; ++i) c[i] = i * kMergeThreads + tid < n ? sh.buf[i * kMergeThreads + tid] : Cand{0, 0};
-            raise_bar(sh, greatest(c), a.k, p);
-            if (tid == 0) sh.n = 0;
-            __syncthreads();
-            keep(c);
-            n = sh.n;
-        }
-        __syncthreads();
-    }
-    // ---- in order ----
-    const int n = sh.n;
-    if (tid < n) {
-        const Cand x = sh.buf[tid];
-        int rank = 0;
-        for (int i = 0; i < n; ++i) rank += sh.buf[i].above(x);
-        if (rank < a.k) put(rank, x);
-    } else if (tid < a.k) {
-        put_none(tid);
-    }
-}
+static_assert(sizeof(MergeShared) <= sizeof(Shared), "");
 
 // Pieces of a row: as many as all blocks that run at once have room for, of two parts each at least (the bar comes
 // from the first).
@@ -695,18 +698,16 @@ Cut cut_of(const pkv_pool *pool, int64_t rows, int vocab, int elem)
     return c;
 }
 
-// The kernels' shared memory is allowed, once per device.
+// The kernel's shared memory is allowed, once per device.
 pkv_status prepare_scan(const pkv_pool *pool)
 {
     static std::mutex mu;
     static bool ready[64];
     std::lock_guard<std::mutex> lock(mu);
     if (pool->device < 64 && ready[pool->device]) return PKV_OK;
-    cudaError_t e = cudaFuncSetAttribute(beam_scan_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
+    cudaError_t e = cudaFuncSetAttribute(beam_select_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(beam_scan_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(MergeShared));
+        e = cudaFuncSetAttribute(beam_select_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
     if (e != cudaSuccess) return cuda_fail(e, "paged_beam_select: kernel attributes");
     if (pool->device < 64) ready[pool->device] = true;
     return PKV_OK;
@@ -783,7 +784,7 @@ extern "C" pkv_status paged_beam_select(pkv_pool *pool, const void *logits, int3
     st = prepare_scan(pool);
     if (st != PKV_OK) return st;
     const size_t lists = (size_t)rows * cut.pieces;
-    ScanArgs a;
+    Args a;
     a.err = pool->err;
     a.logits = logits;
     a.stride = row_stride;
@@ -793,29 +794,16 @@ extern "C" pkv_status paged_beam_select(pkv_pool *pool, const void *logits, int3
     a.keys = static_cast<uint64_t *>(pool->ws);
     a.sum = reinterpret_cast<double *>(a.keys + lists * k);
     a.top = reinterpret_cast<float *>(a.sum + lists);
-    {
-        LaunchScope ls(pool, kDecode, s);
-        const dim3 grid((unsigned)cut.pieces, (unsigned)batch, (unsigned)beams);
-        cudaError_t e = elem == 4 ? launch_pdl(beam_scan_kernel<float>, grid, dim3(kThreads), sizeof(Shared), s, a)
-                                  : launch_pdl(beam_scan_kernel<__nv_bfloat16>, grid, dim3(kThreads), sizeof(Shared), s, a);
-        ls.done();
-        if (e != cudaSuccess) return cuda_fail(e, "paged_beam_select scan launch");
-    }
-    MergeArgs m;
-    m.keys = a.keys;
-    m.top = a.top;
-    m.sum = a.sum;
-    m.scores = scores;
-    m.beams = beams;
-    m.pieces = cut.pieces;
-    m.k = k;
-    m.tokens = tokens;
-    m.parents = parents;
-    m.out = out_scores;
-    m.err = pool->err;
-    LaunchScope ls(pool, kMerge, s);
-    cudaError_t e = launch_pdl(beam_merge_kernel, dim3((unsigned)batch), dim3(kMergeThreads), sizeof(MergeShared), s, m);
+    a.scores = scores;
+    a.tickets = pool->tickets;
+    a.tokens = tokens;
+    a.parents = parents;
+    a.out = out_scores;
+    LaunchScope ls(pool, kDecode, s);
+    const dim3 grid((unsigned)cut.pieces, (unsigned)batch, (unsigned)beams);
+    cudaError_t e = elem == 4 ? launch_pdl(beam_select_kernel<float>, grid, dim3(kThreads), sizeof(Shared), s, a)
+                              : launch_pdl(beam_select_kernel<__nv_bfloat16>, grid, dim3(kThreads), sizeof(Shared), s, a);
     ls.done();
-    if (e != cudaSuccess) return cuda_fail(e, "paged_beam_select merge launch");
+    if (e != cudaSuccess) return cuda_fail(e, "paged_beam_select launch");
     return PKV_OK;
 }

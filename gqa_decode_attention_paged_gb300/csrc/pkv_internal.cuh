@@ -91,6 +91,7 @@ struct pkv_pool {
     CUtensorMap tm_block, tm_entry;
     bool scales_set = false;
     unsigned *err = nullptr;          // device sticky error word
+    unsigned *tickets = nullptr;      // [kMaxBatch] behind it: paged_beam_select's, 0 between calls
     void *ws = nullptr;               // split-KV workspace (grow-only)
     size_t ws_bytes = 0;
     bool ws_captured = false;         // a captured graph may use it

@@ -337,7 +337,7 @@ pkv_status kv_pool_create(int64_t num_blocks, int32_t block_size, int32_t n_kv, 
             p->v_params = reinterpret_cast<float *>(static_cast<uint8_t *>(p->k) + i4_params_offset(d_head));
     }
     if (e == cudaSuccess) { what = "cudaMalloc(scales)"; e = cudaMalloc(&p->scales, sizeof(float) * 2 * n_kv); }
-    if (e == cudaSuccess) { what = "cudaMalloc(error word)"; e = cudaMalloc(&p->err, sizeof(unsigned)); }
+    if (e == cudaSuccess) { what = "cudaMalloc(error word)"; e = cudaMalloc(&p->err, sizeof(unsigned) * (1 + kMaxBatch)); }
     if (e == cudaSuccess && dtype == PKV_INT4) {
         what = "cudaMalloc(key params)";
         e = cudaMalloc(&p->k_params, sizeof(float) * 2 * n_kv * d_head);
@@ -345,7 +345,8 @@ pkv_status kv_pool_create(int64_t num_blocks, int32_t block_size, int32_t n_kv, 
     }
     if (e == cudaSuccess) { what = "cudaMemset"; e = cudaMemset(p->k, 0, p->alloc_bytes); }
     if (e == cudaSuccess) e = cudaMemset(p->scales, 0, sizeof(float) * 2 * n_kv);
-    if (e == cudaSuccess) e = cudaMemset(p->err, 0, sizeof(unsigned));
+    if (e == cudaSuccess) e = cudaMemset(p->err, 0, sizeof(unsigned) * (1 + kMaxBatch));
+    p->tickets = p->err + 1;
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
         pkv_status s = cuda_fail(e, what);

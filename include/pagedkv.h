@@ -632,7 +632,7 @@ pkv_status paged_tree_commit(pkv_pool *pool, const int32_t *qo_indptr, const int
  * exponentials themselves and the sums of a few hundred of them (32 bits);
  * out_scores are rounded once.  A beam whose logits hold a NaN or +infinity,
  * or whose score is one, has no continuations and sets PKV_DEVERR_NAN.
- * batch <= 8192, beams and k in 1 .. 64, vocab <= 2^22.  Two launches, no
+ * batch <= 8192, beams and k in 1 .. 64, vocab <= 2^22.  One launch, no
  * cache is read: the pool gives its device, its workspace (grown outside
  * stream captures: see paged_beam_reserve_workspace) and its error word.
  * Errors: EINVAL, EUNSUPPORTED, ENOMEM, ECUDA. */
