@@ -15,9 +15,11 @@
 //
 // Design (one persistent CTA per SM, warp-specialised):
 //   * a unit is up to 256 rows (two tiles of 128) of one (sequence, KV head).
-//     The stream of all units' steps of 128 keys is cut into one equal slice
-//     per CTA, so that every SM has the same number of steps whatever the
-//     lengths are, and one long sequence keeps all of them busy.  A unit that a
+//     The stream of all units' steps of 128 keys, weighed by what they cost, is
+//     cut into one equal slice per CTA, so that every SM has the same work
+//     whatever the lengths are, and one long sequence keeps all of them busy (64
+//     trees of 1..60 nodes on an E4M3 cache: 201 us with steps of one and of two
+//     tiles weighed alike, XX so).  A unit that a
 //     slice holds whole is finished by its CTA; of one that is cut each CTA
 //     leaves its part (reference maximum, sum, unnormalised O), which
 //     tree_merge_kernel joins.  A slice cuts at most two units, the one it
@@ -32,10 +34,12 @@
 //     memory as a matrix product's result is laid out: four threads a row, which
 //     two shuffles reduce.  (A thread per row, four warps a stream, left every
 //     scheduler with two warps and their dependent chains.)
-//   * one warp streams what the MMAs take through one ring of 32 KiB (d 128)
-//     tiles: keys of a step, its values, keys of the next.  Two warps issue one
-//     stream's MMAs each: S = Q K^T, and when the weights are written over S,
-//     O += P V.
+//   * one warp walks the slice, says what the next piece of work is (a queue of
+//     four in shared memory: where every warp walked for itself, the walk's
+//     registers were missing in the softmax, 1111 against XX us), and streams
+//     what the MMAs take through one ring of 32 KiB (d 128) tiles: keys of a
+//     step, its values, keys of the next.  Two warps issue one stream's MMAs
+//     each: S = Q K^T, and when the weights are written over S, O += P V.
 //   * the reference maximum is raised lazily (O is rescaled only when a row's
 //     maximum grows by more than 2^8).  Weights are rounded to bf16 (FP8 pools:
 //     f16) for the MMA; the sum adds them in fp32 as they were (adding the
@@ -63,7 +67,16 @@ constexpr int kStepBlocks = kKeys / kBlockSize;
 constexpr int kSoftmaxWarps = 16;
 constexpr int kCopyWarp = 16, kMmaWarp = 17, kPrepWarp = 20;
 constexpr int kMaxWords = 16;
-constexpr int kMinShare = 2;               // steps of a slice at least
+constexpr int kMany = 4;                   // windows of 32 sequences whose lengths are read at a time
+static_assert(sizeof(int) * 14 <= 64, "");
+// What a step costs in a unit of one tile (bound by HBM, or by the widening of its keys) and of two (by the products
+// and exponentials): bf16 1.4 and 2.1 us, E4M3 1.3 and 2.6 us.
+template <bool F8>
+struct Cost {
+    static constexpr int kOne = F8 ? 1 : 2, kTwo = F8 ? 2 : 3;
+    static constexpr int kMinShare = 2 * kOne;  // of a slice; a step at least, whatever its kind
+    static_assert(kMinShare >= kTwo, "a slice without a step inside a unit");
+};
 template <bool F8>
 struct Warps {
     static constexpr int kWarps = F8 ? 24 : 20, kThreads = kWarps * 32;
@@ -111,7 +124,9 @@ struct Layout {
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kRing = kQ + 2 * QT;
     static constexpr uint32_t kStat = kRing + kStages * UT;  // a unit of one tile: stream 1's (m, l) per row
-    static constexpr uint32_t kBar = kStat + kRows * 8;
+    static constexpr int kQueue = 4;
+    static constexpr uint32_t kPieces = kStat + kRows * 8;   // what to do next, 64 bytes each
+    static constexpr uint32_t kBar = kPieces + kQueue * 64;
     // RAW, Q_RAW: FP8 pools' copies complete there; FULL and Q_FULL follow when the rows are f16
     enum { Q_RAW = 0, Q_FULL, Q_FREE, RAW, FULL = RAW + kStages, EMPTY = FULL + kStages,
            S_FULL = EMPTY + kStages,  // per stream: scores of a step
@@ -119,7 +134,9 @@ struct Layout {
            PV_DONE = P_FULL + 2,      // their product has run
            STAT = PV_DONE + 2,        // per warp of a stream: stream 1's statistics and O are final
            TAKEN = STAT + 8,          // they are read
-           DRAIN = TAKEN + 8, NBARS };
+           NEXT = TAKEN + 8,          // a piece of the queue is there
+           DONE = NEXT + kQueue,      // every warp is done with it
+           DRAIN = DONE + kQueue, NBARS };
     static constexpr uint32_t kTmemSlot = kBar + NBARS * 8;
     static constexpr uint32_t kAbort = kTmemSlot + 4;
     static constexpr uint32_t kEnd = kAbort + 4;
@@ -177,17 +194,18 @@ struct Piece {
     int b, g, r0;      // sequence, KV head, first local row
     int row0, T, R, C; // first token row, nodes, local rows (nodes x heads), cache length
     int S, s0, n;      // the unit's steps; this piece's
-    int n_blocks;
+    int more;          // pieces of the unit in the slices that follow
+    int next;          // where the stream goes on
+    int blocks;        // of the sequence
     __device__ __forceinline__ bool two() const { return R - r0 > kRows; }
     __device__ __forceinline__ bool whole() const { return n == S; }
 };
 
-// A window of 32 sequences, one per lane: each warp walks the stream itself, with the same arithmetic.
+// A window of 32 sequences, one per lane.
 struct Walker {
-    int wb = 0, wbase = 0, tot = 0;  // first sequence of the window, steps before it, its steps
-    int incl = 0;                    // steps up to and with this lane's sequence
+    int wb = 0, wbase = 0, tot = 0;  // first sequence of the window, costs before it, its costs
+    int incl = 0;                    // costs up to and with this lane's sequence
     int row0 = 0, T = 0, C = 0;      // this lane's sequence
-    int S = 0, pairs = 0;            // steps and units per KV head
 };
 
 __device__ __forceinline__ int inclusive_sum(int x, int lane)
@@ -200,63 +218,88 @@ __device__ __forceinline__ int inclusive_sum(int x, int lane)
     return x;
 }
 
-// Sequence b's nodes, length, steps and units; no work where it does not fit.
-template <int G>
+// The units of a sequence and KV head with R rows: all but the last have two tiles.
+template <bool F8>
+struct Units {
+    int before, last;  // cost of a step in all units but the last together; in the last
+    __device__ __forceinline__ explicit Units(int R)
+    {
+        const int n = (R + kUnitRows - 1) / kUnitRows;
+        before = (n - 1) * Cost<F8>::kTwo;
+        last = R - (n - 1) * kUnitRows > kRows ? Cost<F8>::kTwo : Cost<F8>::kOne;
+    }
+};
+
+// Sequence b's nodes and length; its cost, none where it does not fit.
+template <int G, bool F8>
 __device__ __forceinline__ int sequence(const Args &a, int b, Walker &w, bool flag)
 {
-    w.row0 = w.T = w.C = w.S = w.pairs = 0;
+    w.row0 = w.T = w.C = 0;
     if (b >= a.batch) return 0;
     const int lo = a.qo_indptr[b], hi = a.qo_indptr[b + 1], C = a.context_lens[b];
     if (lo < 0 || hi < lo || hi > a.n_rows || hi - lo > 64 * a.words || C < hi - lo || C > a.W * kBlockSize) {
         if (flag) atomicOr(a.err, PKV_DEVERR_CTX_RANGE);
         return 0;
     }
+    if (hi == lo) return 0;
     w.row0 = lo;
     w.T = hi - lo;
     w.C = C;
-    if (w.T > 0) {
-        w.S = (C + kKeys - 1) / kKeys;
-        w.pairs = (w.T * G + kUnitRows - 1) / kUnitRows;
-    }
-    return w.S * w.pairs * a.n_kv;
+    const Units<F8> u(w.T * G);
+    return (C + kKeys - 1) / kKeys * (u.before + u.last) * a.n_kv;
 }
 
-template <int G>
-__device__ __forceinline__ void load_window(Walker &w, const Args &a, int lane)
+template <int G, bool F8>
+__device__ __forceinline__ void load_window(Walker &w, const Args &a, int lane, bool flag)
 {
-    const int work = sequence<G>(a, w.wb + lane, w, false);
+    const int work = sequence<G, F8>(a, w.wb + lane, w, flag);
     w.incl = inclusive_sum(work, lane);
     w.tot = __shfl_sync(kFull, w.incl, 31);
 }
 
-// The piece that begins at step f of the stream, up to step `end`; false past it.  Warp-wide, uniform result.
-template <int G>
-__device__ __forceinline__ bool find_piece(Walker &w, const Args &a, int f, int end, Piece &p, int lane)
+// The piece that begins at f in the stream, up to `end`; false past it.  A step belongs to the slice in which it
+// begins.  Warp-wide, uniform result.
+template <int G, bool F8>
+__device__ __forceinline__ bool find_piece(Walker &w, const Args &a, int f, int end, int share, Piece &p, int lane)
 {
-    if (f >= end) return false;
-    while (f >= w.wbase + w.tot) {
-        if (w.wb + 32 >= a.batch) return false;
-        w.wbase += w.tot;
-        w.wb += 32;
-        load_window<G>(w, a, lane);
+    for (;;) {
+        if (f >= end) return false;
+        while (f >= w.wbase + w.tot) {
+            if (w.wb + 32 >= a.batch) return false;
+            w.wbase += w.tot;
+            w.wb += 32;
+            load_window<G, F8>(w, a, lane, false);
+        }
+        const int at = f - w.wbase;
+        const int l = __ffs(__ballot_sync(kFull, w.incl > at)) - 1;
+        p.b = w.wb + l;
+        p.row0 = __shfl_sync(kFull, w.row0, l);
+        p.T = __shfl_sync(kFull, w.T, l);
+        p.C = __shfl_sync(kFull, w.C, l);
+        p.S = (p.C + kKeys - 1) / kKeys;
+        p.R = p.T * G;
+        const Units<F8> u(p.R);
+        const int head = p.S * (u.before + u.last);
+        const int within = at - (__shfl_sync(kFull, w.incl, l) - head * a.n_kv);
+        p.g = within / head;
+        int x = within - p.g * head;  // in the KV head, then in the unit
+        int cost = u.last, unit = u.before / Cost<F8>::kTwo;
+        if (x < p.S * u.before) {
+            cost = Cost<F8>::kTwo;
+            unit = x / (p.S * cost);
+        }
+        x -= unit * p.S * Cost<F8>::kTwo;
+        p.r0 = unit * kUnitRows;
+        const int e = min(p.S * cost, x + (end - f));
+        p.s0 = (x + cost - 1) / cost;
+        p.n = (e + cost - 1) / cost - p.s0;
+        p.next = f + (e - x);
+        const int left = cost * (p.S - 1) - e;  // the last step's beginning, behind this slice
+        p.more = left < 0 ? 0 : left / share + 1;
+        p.blocks = (p.C + kBlockSize - 1) / kBlockSize;
+        if (p.n > 0) return true;
+        f = p.next;
     }
-    const int at = f - w.wbase;
-    const int l = __ffs(__ballot_sync(kFull, w.incl > at)) - 1;
-    p.b = w.wb + l;
-    p.row0 = __shfl_sync(kFull, w.row0, l);
-    p.T = __shfl_sync(kFull, w.T, l);
-    p.C = __shfl_sync(kFull, w.C, l);
-    p.S = __shfl_sync(kFull, w.S, l);
-    const int pairs = __shfl_sync(kFull, w.pairs, l);
-    const int within = at - (__shfl_sync(kFull, w.incl, l) - p.S * pairs * a.n_kv);
-    const int unit = within / p.S;
-    p.s0 = within - unit * p.S;
-    p.g = unit / pairs;
-    p.r0 = (unit - p.g * pairs) * kUnitRows;
-    p.n = min(p.S - p.s0, end - f);
-    p.R = p.T * G;
-    p.n_blocks = (p.C + kBlockSize - 1) / kBlockSize;
-    return true;
 }
 
 // Bits [at, at + 32) of a row's view of its sequence's T nodes; the positions before the nodes are all seen.
@@ -306,7 +349,8 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
         if (i >= L::P_FULL && i < L::P_FULL + 2) n = kSoftmaxWarps / 2;  // a stream's warps
         if (i == L::Q_FREE || i == L::DRAIN) n = 2;                // both issuing warps
         if (i >= L::EMPTY && i < L::EMPTY + NS) n = 2;
-        if (i == L::Q_FULL && F8) n = kSoftmaxWarps;               // each widens its share of the queries
+        if (i >= L::DONE && i < L::DONE + L::kQueue) n = kSoftmaxWarps + 2 + (F8 ? 4 : 0);
+        if (i == L::Q_FULL && F8) n = 4;                           // the preparing warps widen the queries
         if (i >= L::FULL && i < L::FULL + NS) n = kSplit;
         mbar_init(&bar[i], n);
         fence_mbarrier_init();
@@ -332,77 +376,94 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
         }
     };
 
-    // ---- this CTA's slice of the stream, and the window in which it begins ----
-    Walker w0;
-    int f0, f1, share;
-    if (a.batch <= 32) {
-        w0.incl = inclusive_sum(sequence<G>(a, lane, w0, blockIdx.x == 0 && warp == 0), lane);
-        w0.tot = __shfl_sync(kFull, w0.incl, 31);
-        share = max(kMinShare, (w0.tot + (int)gridDim.x - 1) / (int)gridDim.x);
-        f0 = min((int64_t)w0.tot, (int64_t)blockIdx.x * share);
-        f1 = min((int64_t)w0.tot, (int64_t)f0 + share);
-    } else {
-        int *win = reinterpret_cast<int *>(sm + L::kRing);  // steps of each window of 32 sequences
-        const int windows = (a.batch + 31) / 32;
-        for (int i = warp; i < windows; i += kWarps) {
-            const int x = inclusive_sum(sequence<G>(a, 32 * i + lane, w0, blockIdx.x == 0), lane);
-            if (lane == 31) win[i] = x;
-        }
-        __syncthreads();
-        int total = 0;
-        for (int i = 0; i < windows; i += 32) total += __reduce_add_sync(kFull, i + lane < windows ? win[i + lane] : 0);
-        share = max(kMinShare, (total + (int)gridDim.x - 1) / (int)gridDim.x);
-        f0 = min((int64_t)total, (int64_t)blockIdx.x * share);
-        f1 = min((int64_t)total, (int64_t)f0 + share);
-        int before = 0;
-        for (int i = 0; i < windows; i += 32) {
-            const int x = i + lane < windows ? win[i + lane] : 0;
-            const int incl = inclusive_sum(x, lane);
-            const unsigned on = __ballot_sync(kFull, i + lane < windows && before + incl - x <= f0);
-            if (on) {
-                const int l = 31 - __clz(on);
-                w0.wb = 32 * (i + l);
-                w0.wbase = before + __shfl_sync(kFull, incl - x, l);
-            }
-            before += __shfl_sync(kFull, incl, 31);
-        }
-        fence_proxy_async_smem();
-        __syncthreads();  // the ring is free for the copies
-        load_window<G>(w0, a, lane);
-    }
-    Walker &wk = w0;
     const uint32_t base = smem_u32(sm);
+    // The queue's piece i, when it is there (n == 0: no more; null: time ran out); and the warp is done with it.
+    auto next_piece = [&](int i) -> const Piece * {
+        if (*abort_flag || !wait_all(&bar[L::NEXT + i % L::kQueue], (i / L::kQueue) & 1)) return nullptr;
+        return reinterpret_cast<const Piece *>(sm + L::kPieces + i % L::kQueue * 64);
+    };
+    auto done_with = [&](int i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[L::DONE + i % L::kQueue]);
+    };
 
     if (warp >= kCopyWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Wp::kWorkRegs));
         if (warp == kCopyWarp) {
             // ---------------------------------------------------------- copies
+            // ---- this CTA's slice of the stream, and the window in which it begins ----
+            Walker wk;
+            int total = 0, many0 = 0, many1 = 0, f0, f1, share;
+            static_assert(kMaxBatch <= 64 * 32 * kMany, "");
+            if (a.batch <= 32) {
+                load_window<G, F8>(wk, a, lane, blockIdx.x == 0);
+                total = wk.tot;
+            } else {
+                for (int b = 0; b < a.batch; b += 32 * kMany) {
+                    int x = 0;
+#pragma unroll
+                    for (int i = 0; i < kMany; ++i) x += sequence<G, F8>(a, b + 32 * i + lane, wk, blockIdx.x == 0);
+                    x = __reduce_add_sync(kFull, x);
+                    total += x;
+                    const int i = b / (32 * kMany);  // lane i % 32 keeps it
+                    if (lane == i % 32) (i < 32 ? many0 : many1) = x;
+                }
+            }
+            share = max(Cost<F8>::kMinShare, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+            f0 = min((int64_t)total, (int64_t)blockIdx.x * share);
+            f1 = min((int64_t)total, (int64_t)f0 + share);
+            if (a.batch > 32) {
+                const int incl0 = inclusive_sum(many0, lane), all0 = __shfl_sync(kFull, incl0, 31), incl1 = all0 + inclusive_sum(many1, lane);
+                const unsigned on0 = __ballot_sync(kFull, incl0 - many0 <= f0), on1 = __ballot_sync(kFull, incl1 - many1 <= f0);
+                // the last that begins at or before f0 (those behind the batch begin at its end)
+                const int i = on1 ? 63 - __clz(on1) : 31 - __clz(on0);
+                wk.wb = min(i * 32 * kMany, a.batch - 1) / (32 * kMany) * (32 * kMany);
+                const int j = wk.wb / (32 * kMany);
+                wk.wbase = __shfl_sync(kFull, j < 32 ? incl0 - many0 : incl1 - many1, j % 32);
+                load_window<G, F8>(wk, a, lane, false);
+            }
             const uint64_t policy = l2_policy_evict_normal();
             const uint32_t go = elect_one();  // one lane issues all copies, the warp running as one
             int u = 0, n = 0;                 // tiles of the ring, pieces
             bool ok = true;
-            Piece p;
             Part begun = {0, 0, 0, 0, -1};
-            for (int f = f0; ok && find_piece<G>(wk, a, f, f1, p, lane); f += p.n) {
+            for (int f = f0;;) {
                 if (*abort_flag) break;
-                if (n > 0 && !(ok = wait_all(&bar[L::Q_FREE], (n - 1) & 1))) break;
+                Piece p;
+                const bool some = find_piece<G, F8>(wk, a, f, f1, share, p, lane);
+                if (!some) p.n = 0;
+                const int slot = n % L::kQueue;
+                if (n >= L::kQueue && !(ok = wait_all(&bar[L::DONE + slot], (n / L::kQueue - 1) & 1))) break;
                 if (lane == 0) {
-                    uint64_t *qb = &bar[F8 ? L::Q_RAW : L::Q_FULL];
-                    mbar_arrive_expect_tx(qb, p.two() ? 2 * L::QT : L::QT);
-                    for (int t = 0; t < (p.two() ? 2 : 1); ++t)
-#pragma unroll
-                        for (int h = 0; h < NH; ++h)
-                            tma_load_3d(sm + L::kQ + t * L::QT + h * kHalf, &tm_q, 64 * h, p.g * G,
-                                        p.row0 + (p.r0 + t * kRows) / G, qb, policy);
+                    *reinterpret_cast<Piece *>(sm + L::kPieces + slot * 64) = p;
+                    mbar_arrive(&bar[L::NEXT + slot]);
                 }
                 __syncwarp();
-                ++n;
-                if (p.s0 == 0 && !p.whole()) begun = {p.row0, p.r0, p.R, p.g, (p.S - p.n + share - 1) / share};
+                if (!some) break;
+                f = p.next;
+                // The queries go out behind the first step's tiles: those need no more than what the piece before
+                // leaves of the ring, the queries that it has issued its last scores.
+                auto copy_q = [&]() -> bool {
+                    if (n > 0 && !wait_all(&bar[L::Q_FREE], (n - 1) & 1)) return false;
+                    if (lane == 0) {
+                        uint64_t *qb = &bar[F8 ? L::Q_RAW : L::Q_FULL];
+                        mbar_arrive_expect_tx(qb, p.two() ? 2 * L::QT : L::QT);
+                        for (int t = 0; t < (p.two() ? 2 : 1); ++t)
+#pragma unroll
+                            for (int h = 0; h < NH; ++h)
+                                tma_load_3d(sm + L::kQ + t * L::QT + h * kHalf, &tm_q, 64 * h, p.g * G,
+                                            p.row0 + (p.r0 + t * kRows) / G, qb, policy);
+                    }
+                    __syncwarp();
+                    return true;
+                };
+                static_assert(NS >= 2, "");
+                if (p.s0 == 0 && !p.whole()) begun = {p.row0, p.r0, p.R, p.g, p.more};
                 const int32_t *trow = a.block_tables + (int64_t)p.b * a.W;
                 // lane k < 8: the entry rows of block k of a step, or rows past the pool (zero filled)
                 auto rows_of = [&](int s) -> int {
                     const int nb = (p.s0 + s) * kStepBlocks + lane;
-                    const bool present = lane < kStepBlocks && nb < p.n_blocks;
+                    const bool present = lane < kStepBlocks && nb < p.blocks;
                     const int id = present ? trow[nb] : -1;
                     const bool valid = id >= 0 && id < a.num_blocks;
                     if (present && !valid) atomicOr(a.err, PKV_DEVERR_BLOCK_RANGE);
@@ -436,7 +497,10 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                             }
                         }
                     }
+                    if (ok && s == 0) ok = copy_q();
                 }
+                if (!ok) break;
+                ++n;
             }
             if (lane == 0) a.parts[blockIdx.x] = begun;
             // copies still in flight (after an abort) land before the CTA exits
@@ -445,7 +509,8 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
             // and so do the MMAs' arrivals for the last tiles
             for (int i = max(0, u - NS); i < u && ok && !*abort_flag; ++i)
                 ok = wait_all(&bar[L::EMPTY + i % NS], (i / NS) & 1);
-            if (n > 0) mbar_wait_bounded(&bar[F8 ? L::Q_RAW : L::Q_FULL], (n - 1) & 1);
+            for (int i = max(0, n - 1); i <= n && !ok; ++i) mbar_wait_bounded(&bar[F8 ? L::Q_RAW : L::Q_FULL], i & 1, kWaitLimitNs / 4);
+            if (n > 0 && ok) ok = wait_all(&bar[F8 ? L::Q_RAW : L::Q_FULL], (n - 1) & 1);
             if (!ok) set_abort();
         } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
             // ---------------------------------------------------------- S = Q K^T and O += P V of one stream
@@ -456,10 +521,12 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
             const uint64_t kd = smem_desc(base + L::kRing, 16, 1024), vd = smem_desc(base + L::kRing, kHalf, 1024);
             int u = 0, n = 0, turns = 0;  // tiles of the ring, pieces, this stream's steps
             bool ok = true;
-            Piece p;
             auto full = [&](int i) -> bool { return wait_all(&bar[L::FULL + i % NS], (i / NS) & 1); };
-            for (int f = f0; ok && find_piece<G>(wk, a, f, f1, p, lane); f += p.n) {
-                if (*abort_flag) break;
+            for (;;) {
+                const Piece *pp = next_piece(n);
+                if (!(ok = pp != nullptr)) break;
+                const Piece &p = *pp;
+                if (p.n == 0) break;
                 if (!(ok = wait_all(&bar[L::Q_FULL], n & 1))) break;
                 // (the same in all lanes, and known to be: an MMA whose operands are not takes 80 cycles to issue)
                 const bool two = __shfl_sync(kFull, (int)p.two(), 0);
@@ -519,6 +586,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                 }
                 if (!ok) break;
                 if (q_held) umma_commit_if(go, &bar[L::Q_FREE]);  // (a piece of one step has none for stream 1)
+                done_with(n);
                 ++n;
             }
             umma_commit_if(go, &bar[L::DRAIN]);
@@ -528,12 +596,36 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
         } else if (F8 && warp >= kPrepWarp && warp < kPrepWarp + 4) {
             // ---------------------------------------------------------- E4M3 tiles widened
             const int which = warp - kPrepWarp;
-            int u = 0;
+            int u = 0;  // tiles of the ring
             bool ok = true;
-            Piece p;
-            for (int f = f0; ok && find_piece<G>(wk, a, f, f1, p, lane); f += p.n) {
-                if (*abort_flag) break;
+            // the queries to f16 in place, element by element: this warp's quarter
+            auto widen_q = [&](int n, bool two) -> bool {
+                if (!wait_all(&bar[L::Q_RAW], n & 1)) return false;
+                const uint32_t part = (two ? 2 : 1) * L::QT / 4;
+#pragma unroll 4
+                for (uint32_t off = which * part + 16u * lane; off < (which + 1) * part; off += 16u * 32) {
+                    uint4 v = lds128(base + off);
+                    uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 q = bf16x2_to_f32x2(w[k]);
+                        w[k] = pack_f16x2(q.x, q.y);
+                    }
+                    sts128(base + off, v);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[L::Q_FULL]);
+                return true;
+            };
+            for (int n = 0;; ++n) {  // pieces
+                const Piece *pp = next_piece(n);
+                if (!(ok = pp != nullptr)) break;
+                const Piece &p = *pp;
+                if (p.n == 0) break;
                 for (int i = 0; i < 2 * p.n; ++i, ++u) {
+                    // (the first keys are widened before the queries, which come when the piece before is done with its own)
+                    if (i == 1 && !(ok = widen_q(n, p.two()))) break;
                     if (D == 64 && (u & 1) != which >> 1) continue;
                     const int st = u % NS;
                     if (!(ok = wait_all(&bar[L::RAW + st], (u / NS) & 1))) break;
@@ -555,6 +647,8 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar[L::FULL + st]);
                 }
+                if (!ok) break;
+                done_with(n);
             }
             if (!ok) set_abort();
         }
@@ -567,45 +661,29 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
         const uint32_t ts = tmem + ((uint32_t)row0 << 16);
         float2 *stat = reinterpret_cast<float2 *>(sm + L::kStat);
         const bool rising = a.qscale >= 0.0f;  // else scores are negated as they are read
-        int turns = 0, n = 0, joins = 0;       // this stream's steps, pieces, units of one tile
+        int turns = 0, joins = 0;              // this stream's steps, units of one tile
         bool ok = true;
-        Piece p;
-        for (int f = f0; ok && find_piece<G>(wk, a, f, f1, p, lane); f += p.n) {
-            if (*abort_flag) break;
+        for (int i = 0; ok; ++i) {  // pieces
+            const Piece *pp = next_piece(i);
+            if (!(ok = pp != nullptr)) break;
+            const Piece &p = *pp;
+            const int n = p.n;
+            if (n == 0) break;
             const bool two = p.two();
-            if constexpr (F8) {  // the queries to f16 in place, element by element: this warp's share
-                if (!(ok = wait_all(&bar[L::Q_RAW], n & 1))) break;
-                const uint32_t part = (two ? 2 : 1) * L::QT / kSoftmaxWarps;
-#pragma unroll 4
-                for (uint32_t off = warp * part + 16u * lane; off < (warp + 1) * part; off += 16u * 32) {
-                    uint4 v = lds128(base + off);
-                    uint32_t *w = reinterpret_cast<uint32_t *>(&v);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 q = bf16x2_to_f32x2(w[k]);
-                        w[k] = pack_f16x2(q.x, q.y);
-                    }
-                    sts128(base + off, v);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[L::Q_FULL]);
-            }
-            ++n;
             const int t0 = p.r0 + (two ? x * kRows : 0) + row0;  // the warp's first local row
             const bool live = t0 < p.R;
-            const int before = p.C - p.T;                        // positions before the nodes
-            const float qs = fabsf(a.qscale) * (F8 ? a.scales[p.g] : 1.0f);
-            const int32_t *trow = a.block_tables + (int64_t)p.b * a.W;
+            const int rel0 = p.s0 * kKeys - (p.C - p.T);         // the first step's first key, against the first node
+            const float qs = fabsf(a.qscale) * (F8 ? a.scales[p.g] : 1.0f), vs = F8 ? a.scales[a.n_kv + p.g] : 1.0f;
+            const int32_t *trow = a.block_tables + (int64_t)p.b * a.W + p.s0 * kStepBlocks;
+            const int blocks = p.blocks - p.s0 * kStepBlocks;
             const int hop = two ? 1 : 2, s1 = two ? 0 : x;
             auto node = [&](int i) -> int { return min(t0 + g8 + 8 * i, p.R - 1) / G; };  // of this thread's row i
             auto ids_of = [&](int s) -> int {
-                const int nb = (p.s0 + s) * kStepBlocks + lane;
-                return lane < kStepBlocks && s < p.n && nb < p.n_blocks ? trow[nb] : -1;
+                return lane < kStepBlocks && s < n && s * kStepBlocks + lane < blocks ? trow[s * kStepBlocks + lane] : -1;
             };
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // of the rows; sums of this thread's keys
             int nxt = ids_of(s1);
-            for (int s = s1; s < p.n; s += hop, ++turns) {
+            for (int s = s1; s < n; s += hop, ++turns) {
                 // blocks that are there, as the copies decided
                 const uint32_t valid = __ballot_sync(kFull, lane < kStepBlocks && nxt >= 0 && nxt < a.num_blocks);
                 nxt = ids_of(s + hop);
@@ -626,14 +704,14 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
 #pragma unroll
                             for (int i = 0; i < kKeys / 2; ++i) sr[i] ^= 0x80000000u;
                         }
-                        const int key0 = (p.s0 + s) * kKeys;
-                        if (key0 + kKeys > before || valid != (1u << kStepBlocks) - 1) {
+                        const int rel = rel0 + s * kKeys;
+                        if (rel + kKeys > 0 || valid != (1u << kStepBlocks) - 1) {
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 const uint32_t *mrow = a.mask + ((int64_t)p.row0 + node(i)) * 2 * a.words;
 #pragma unroll
                                 for (int c = 0; c < 4; ++c) {
-                                    uint32_t bits = node_bits(mrow, 2 * a.words, p.T, key0 + 32 * c - before);
+                                    uint32_t bits = node_bits(mrow, 2 * a.words, p.T, rel + 32 * c);
                                     if (!((valid >> (2 * c)) & 1u)) bits &= 0xffff0000u;
                                     if (!((valid >> (2 * c)) & 2u)) bits &= 0xffffu;
                                     bits >>= 2 * c4;
@@ -721,7 +799,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
             }
             if (!ok) break;
             // ---- the end of the piece ----
-            const bool any = s1 < p.n;  // this stream had steps
+            const bool any = s1 < n;  // this stream had steps
             if (any && !(ok = wait_all(&bar[L::PV_DONE + x], (turns - 1) & 1))) break;
             tc_fence_after();
             float sum[2], fa[2], fb[2];  // O = fa O_x + fb O_1
@@ -744,6 +822,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar[L::STAT + w8]);
                     ++joins;
+                    done_with(i);
                     continue;
                 }
                 if (!(ok = wait_all(&bar[L::STAT + w8], joins & 1))) break;
@@ -760,8 +839,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                 }
             }
             if (live) {
-                const float vs = F8 ? a.scales[a.n_kv + p.g] : 1.0f;
-                const bool join = !two && p.n > 1, whole = p.whole();
+                const bool join = !two && n > 1, whole = p.whole();
                 const int slot = 2 * (int)blockIdx.x + (p.s0 == 0 ? 1 : 0);
                 bool in[2];
                 int64_t to[2];  // the row's place: in out, or in the slot
@@ -776,7 +854,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                                   : ((int64_t)slot * a.slot_rows + (r - p.r0)) * D;
                     if (!whole && in[i] && c4 == 0) a.ws_ml[(int64_t)slot * a.slot_rows + (r - p.r0)] = make_float2(m[i], sum[i]);
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[16], o1[16];
                     tmem_ld_rows32(ts + kColO + x * D + c, o);
@@ -802,6 +880,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[L::TAKEN + w8]);
             }
+            done_with(i);
         }
         if (!ok) set_abort();
     }
