@@ -70,12 +70,13 @@ constexpr int kMaxWords = 16;
 constexpr int kMany = 4;                   // windows of 32 sequences whose lengths are read at a time
 static_assert(sizeof(int) * 14 <= 64, "");
 // What a step costs in a unit of one tile (bound by HBM, or by the widening of its keys) and of two (by the products
-// and exponentials): bf16 1.4 and 2.1 us, E4M3 1.3 and 2.6 us.
+// and exponentials), and a unit besides its steps: bf16 1.4, 2.1 and 3 us, E4M3 1.3, 2.6 and 3 us.
 template <bool F8>
 struct Cost {
-    static constexpr int kOne = F8 ? 1 : 2, kTwo = F8 ? 2 : 3;
-    static constexpr int kMinShare = 2 * kOne;  // of a slice; a step at least, whatever its kind
-    static_assert(kMinShare >= kTwo, "a slice without a step inside a unit");
+    static constexpr int kOne = F8 ? 1 : 2, kTwo = F8 ? 2 : 3, kUnit = F8 ? 2 : 4;
+    static constexpr int kMinShare = kUnit + 2 * kOne;  // of a slice
+    // (between two steps' beginnings: no slice inside a unit is without one)
+    static_assert(kMinShare >= kUnit + kTwo, "");
 };
 template <bool F8>
 struct Warps {
@@ -218,15 +219,24 @@ __device__ __forceinline__ int inclusive_sum(int x, int lane)
     return x;
 }
 
-// The units of a sequence and KV head with R rows: all but the last have two tiles.
+// The units of a sequence and KV head with R rows and S steps: all but the last have two tiles.  In a unit of step cost
+// w, step 0 begins at 0 and step s at kUnit + w s.
 template <bool F8>
 struct Units {
-    int before, last;  // cost of a step in all units but the last together; in the last
-    __device__ __forceinline__ explicit Units(int R)
+    int n, full, last;  // units, cost of all but the last, step cost of the last
+    int all;            // cost of the whole
+    __device__ __forceinline__ Units(int R, int S)
     {
-        const int n = (R + kUnitRows - 1) / kUnitRows;
-        before = (n - 1) * Cost<F8>::kTwo;
-        last = R - (n - 1) * kUnitRows > kRows ? Cost<F8>::kTwo : Cost<F8>::kOne;
+        using C = Cost<F8>;
+        n = (R + kUnitRows - 1) / kUnitRows;
+        full = S * C::kTwo + C::kUnit;
+        last = R - (n - 1) * kUnitRows > kRows ? C::kTwo : C::kOne;
+        all = (n - 1) * full + S * last + C::kUnit;
+    }
+    // steps that begin before x
+    static __device__ __forceinline__ int begun(int x, int w)
+    {
+        return x <= 0 ? 0 : max(1, (x - Cost<F8>::kUnit + w - 1) / w);
     }
 };
 
@@ -245,8 +255,7 @@ __device__ __forceinline__ int sequence(const Args &a, int b, Walker &w, bool fl
     w.row0 = lo;
     w.T = hi - lo;
     w.C = C;
-    const Units<F8> u(w.T * G);
-    return (C + kKeys - 1) / kKeys * (u.before + u.last) * a.n_kv;
+    return Units<F8>(w.T * G, (C + kKeys - 1) / kKeys).all * a.n_kv;
 }
 
 template <int G, bool F8>
@@ -278,23 +287,19 @@ __device__ __forceinline__ bool find_piece(Walker &w, const Args &a, int f, int 
         p.C = __shfl_sync(kFull, w.C, l);
         p.S = (p.C + kKeys - 1) / kKeys;
         p.R = p.T * G;
-        const Units<F8> u(p.R);
-        const int head = p.S * (u.before + u.last);
-        const int within = at - (__shfl_sync(kFull, w.incl, l) - head * a.n_kv);
-        p.g = within / head;
-        int x = within - p.g * head;  // in the KV head, then in the unit
-        int cost = u.last, unit = u.before / Cost<F8>::kTwo;
-        if (x < p.S * u.before) {
-            cost = Cost<F8>::kTwo;
-            unit = x / (p.S * cost);
-        }
-        x -= unit * p.S * Cost<F8>::kTwo;
+        const Units<F8> u(p.R, p.S);
+        const int within = at - (__shfl_sync(kFull, w.incl, l) - u.all * a.n_kv);
+        p.g = within / u.all;
+        int x = within - p.g * u.all;  // in the KV head, then in the unit
+        const int unit = min(x / u.full, u.n - 1), cost = unit == u.n - 1 ? u.last : Cost<F8>::kTwo;
+        x -= unit * u.full;
         p.r0 = unit * kUnitRows;
-        const int e = min(p.S * cost, x + (end - f));
-        p.s0 = (x + cost - 1) / cost;
-        p.n = (e + cost - 1) / cost - p.s0;
+        const int size = p.S * cost + Cost<F8>::kUnit, e = min(size, x + (end - f));
+        p.s0 = Units<F8>::begun(x, cost);
+        p.n = (e == size ? p.S : Units<F8>::begun(e, cost)) - p.s0;
         p.next = f + (e - x);
-        const int left = cost * (p.S - 1) - e;  // the last step's beginning, behind this slice
+        // the last step's beginning, behind this slice's end
+        const int left = (p.S == 1 ? 0 : Cost<F8>::kUnit + cost * (p.S - 1)) - e;
         p.more = left < 0 ? 0 : left / share + 1;
         p.blocks = (p.C + kBlockSize - 1) / kBlockSize;
         if (p.n > 0) return true;
@@ -1095,7 +1100,7 @@ extern "C" pkv_status paged_tree_attention(pkv_pool *pool, const void *q, int64_
     const int64_t most = std::min<int64_t>((int64_t)64 * mask_words, n_rows) * G;  // rows of a sequence and KV head
     const int64_t units = (int64_t)batch * pool->n_kv * ((most + kUnitRows - 1) / kUnitRows);
     const int64_t steps = (max_blocks_per_seq + kStepBlocks - 1) / kStepBlocks;
-    if (units > (INT32_MAX / 2) / steps) return fail(PKV_EUNSUPPORTED, "%s: too many rows x table entries", who);
+    if (units > INT32_MAX / (3 * steps + 4)) return fail(PKV_EUNSUPPORTED, "%s: too many rows x table entries", who);
     const int ctas = (int)std::min<int64_t>(pool->num_sms, units * steps);
     const Space sp = space_of(pool, n_rows, G, ctas);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
