@@ -29,7 +29,8 @@
 //     tensor memory and its own eight warps: while one forms weights, the tensor
 //     cores work for the other.  A unit of two tiles gives each stream a tile,
 //     and both use every key and value tile; in a unit of one tile the streams
-//     take alternate steps, and join by log-sum-exp at its end.
+//     take alternate steps (the second one the first, as it is the first that
+//     joins the two by log-sum-exp at the end).
 //   * a softmax warp has 16 rows, all 128 keys of a step, read from tensor
 //     memory as a matrix product's result is laid out: four threads a row, which
 //     two shuffles reduce.  (A thread per row, four warps a stream, left every
@@ -64,6 +65,8 @@ constexpr int kRows = 128;                 // query rows per tile (= TMEM lanes)
 constexpr int kUnitRows = 2 * kRows;
 constexpr int kKeys = 128;                 // keys per step
 constexpr int kStepBlocks = kKeys / kBlockSize;
+constexpr int kTurn = 64;                  // keys that a softmax warp takes at a time
+constexpr int kTurnBlocks = kTurn / kBlockSize;
 constexpr int kSoftmaxWarps = 16;
 constexpr int kCopyWarp = 16, kMmaWarp = 17, kPrepWarp = 20;
 constexpr int kMaxWords = 16;
@@ -73,7 +76,7 @@ static_assert(sizeof(int) * 14 <= 64, "");
 // and exponentials), and a unit besides its steps: bf16 1.4, 2.1 and 3 us, E4M3 1.3, 2.6 and 3 us.
 template <bool F8>
 struct Cost {
-    static constexpr int kOne = F8 ? 1 : 2, kTwo = F8 ? 2 : 3, kUnit = F8 ? 2 : 4;
+    static constexpr int kOne = F8 ? 1 : 2, kTwo = F8 ? 2 : 3, kUnit = F8 ? 3 : 6;
     static constexpr int kMinShare = kUnit + 2 * kOne;  // of a slice
     // (between two steps' beginnings: no slice inside a unit is without one)
     static_assert(kMinShare >= kUnit + kTwo, "");
@@ -86,7 +89,8 @@ struct Warps {
     static_assert(kSoftmaxWarps * kScoreRegs + (kWarps - kSoftmaxWarps) * kWorkRegs <= kWarps * kLaunchRegs,
                   "more registers than the launch has");
 };
-// Tensor memory: S_x at 128 x (fp32 scores; the weights, packed in pairs, over its first 64 columns), O_x at 256 + D x.
+// Tensor memory: S_x at 128 x, two places of 64 columns (fp32 scores of a turn; its weights, packed in pairs, over the
+// first 32), O_x at 256 + D x.
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;
 constexpr uint32_t kHalf = 128 * 128;      // bytes of a 64-column range of a 128-row tile
@@ -130,10 +134,10 @@ struct Layout {
     static constexpr uint32_t kBar = kPieces + kQueue * 64;
     // RAW, Q_RAW: FP8 pools' copies complete there; FULL and Q_FULL follow when the rows are f16
     enum { Q_RAW = 0, Q_FULL, Q_FREE, RAW, FULL = RAW + kStages, EMPTY = FULL + kStages,
-           S_FULL = EMPTY + kStages,  // per stream: scores of a step
-           P_FULL = S_FULL + 2,       // its weights are in tensor memory
-           PV_DONE = P_FULL + 2,      // their product has run
-           STAT = PV_DONE + 2,        // per warp of a stream: stream 1's statistics and O are final
+           S_FULL = EMPTY + kStages,  // per stream and place: scores of a turn
+           P_FULL = S_FULL + 4,       // its weights are in tensor memory
+           PV_DONE = P_FULL + 4,      // their product has run
+           STAT = PV_DONE + 4,        // per warp of a stream: stream 1's statistics and O are final
            TAKEN = STAT + 8,          // they are read
            NEXT = TAKEN + 8,          // a piece of the queue is there
            DONE = NEXT + kQueue,      // every warp is done with it
@@ -351,7 +355,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
     if (tid < L::NBARS) {
         const int i = tid;
         uint32_t n = 1;
-        if (i >= L::P_FULL && i < L::P_FULL + 2) n = kSoftmaxWarps / 2;  // a stream's warps
+        if (i >= L::P_FULL && i < L::P_FULL + 4) n = kSoftmaxWarps / 2;  // a stream's warps
         if (i == L::Q_FREE || i == L::DRAIN) n = 2;                // both issuing warps
         if (i >= L::EMPTY && i < L::EMPTY + NS) n = 2;
         if (i >= L::DONE && i < L::DONE + L::kQueue) n = kSoftmaxWarps + 2 + (F8 ? 4 : 0);
@@ -519,78 +523,104 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
             if (!ok) set_abort();
         } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
             // ---------------------------------------------------------- S = Q K^T and O += P V of one stream
+            // A turn is 64 keys.  A stream's scores have two places, so that the next turn's are there when the
+            // softmax has written this one's weights.
             const int x = warp - kMmaWarp;
-            constexpr uint32_t idesc_qk = mma_idesc(kRows, kKeys, 0, F8), idesc_pv = mma_idesc(kRows, D, 1, F8);
+            constexpr uint32_t idesc_qk = mma_idesc(kRows, kTurn, 0, F8), idesc_pv = mma_idesc(kRows, D, 1, F8);
             const uint32_t tm = __shfl_sync(kFull, tmem, 0);
             const uint32_t go = elect_one();
             const uint64_t kd = smem_desc(base + L::kRing, 16, 1024), vd = smem_desc(base + L::kRing, kHalf, 1024);
-            int u = 0, n = 0, turns = 0;  // tiles of the ring, pieces, this stream's steps
+            int u0 = 0, n = 0, turns = 0;  // tiles of the ring and turns of this stream before the piece; pieces
             bool ok = true;
             auto full = [&](int i) -> bool { return wait_all(&bar[L::FULL + i % NS], (i / NS) & 1); };
+            auto landed = [&](int i) -> bool { return __all_sync(kFull, mbar_test(&bar[L::FULL + i % NS], (i / NS) & 1)); };
             for (;;) {
                 const Piece *pp = next_piece(n);
                 if (!(ok = pp != nullptr)) break;
                 const Piece &p = *pp;
                 if (p.n == 0) break;
-                if (!(ok = wait_all(&bar[L::Q_FULL], n & 1))) break;
                 // (the same in all lanes, and known to be: an MMA whose operands are not takes 80 cycles to issue)
                 const bool two = __shfl_sync(kFull, (int)p.two(), 0);
                 const int steps = __shfl_sync(kFull, p.n, 0);
+                const bool tail = !F8 && p.s0 + steps == p.S && p.C % kBlockSize;
+                const int hop = two ? 1 : 2, s1 = two ? 0 : 1 - x;        // this stream's steps: s1, s1 + hop, ..
+                const int last = 2 * ((steps - s1 + hop - 1) / hop);      // its turns
                 const uint64_t qd = smem_desc(base + L::kQ + (two ? x * L::QT : 0), 16, 1024);
-                bool q_held = true;
-                for (int s = 0; s < steps; ++s, u += 2) {
-                    const int ks = u % NS, vs = (u + 1) % NS;
-                    if (!two && (s & 1) != x) {  // the other stream's: only say that it is not needed here (any more)
-                        if (!(ok = full(u) && full(u + 1))) break;
+                if (!(ok = wait_all(&bar[L::Q_FULL], n & 1))) break;
+                int passed = two ? steps : 0;  // the other stream's steps before it have been passed
+                // of the other stream's steps before s: only say that their tiles are not needed here (any more)
+                auto pass = [&](int s) -> bool {
+                    for (; passed < s; ++passed) {
+                        if ((passed & 1) != x) continue;
+                        const int u = u0 + 2 * passed;
+                        if (!full(u) || !full(u + 1)) return false;
                         if (go) {
-                            mbar_arrive(&bar[L::EMPTY + ks]);
-                            mbar_arrive(&bar[L::EMPTY + vs]);
+                            mbar_arrive(&bar[L::EMPTY + u % NS]);
+                            mbar_arrive(&bar[L::EMPTY + (u + 1) % NS]);
                         }
                         __syncwarp();
-                        continue;
                     }
-                    const bool first = two ? s == 0 : s == x;
-                    // the scores' place is free: the weights over the last ones have been used
-                    if (!(ok = full(u))) break;
-                    if (turns > 0 && !(ok = wait_all(&bar[L::PV_DONE + x], (turns - 1) & 1))) break;
+                    return true;
+                };
+                auto scores = [&](int t) -> bool {
+                    const int s = s1 + (t >> 1) * hop, half = t & 1, u = u0 + 2 * s, st = u % NS, at = (turns + t) & 1;
+                    if (half == 0 && !(pass(s) && full(u))) return false;
+                    // the place is free: the weights over its last scores, two turns ago, have been used
+                    if (turns + t >= 2 && !wait_all(&bar[L::PV_DONE + 2 * x + at], ((turns + t - 2) >> 1) & 1)) return false;
                     tc_fence_after();
-                    const uint64_t km = kd + ((ks * L::UT) >> 4);
+                    const uint64_t km = kd + ((st * L::UT + half * kTurn * 128) >> 4);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-                        umma_if(go, tm + x * kKeys, qd + off, km + off, idesc_qk, kk > 0 ? 1u : 0u);
+                        umma_if(go, tm + x * kKeys + at * kTurn, qd + off, km + off, idesc_qk, kk > 0 ? 1u : 0u);
                     }
-                    umma_commit_if(go, &bar[L::S_FULL + x]);
-                    umma_commit_if(go, &bar[L::EMPTY + ks]);
-                    if (s + (two ? 1 : 2) >= steps) {  // the piece's last scores
-                        umma_commit_if(go, &bar[L::Q_FREE]);
-                        q_held = false;
-                    }
-                    if (!(ok = full(u + 1))) break;
-                    if (!F8 && p.s0 + s == p.S - 1 && p.C % kBlockSize) {
-                        // the sequence ends inside a block: zero the value rows behind its end (both streams of
-                        // two tiles do, each before its own product; the second writes zeros over zeros)
-                        const int r0 = p.C % kKeys, rows = kBlockSize - p.C % kBlockSize;
-                        for (int e = lane; e < rows * 8 * NH; e += 32) {
-                            const int row = r0 + (e >> 3) % rows, h = (e >> 3) / rows;
-                            sts128(base + L::kRing + vs * L::UT + h * kHalf + row * 128 + (e & 7) * 16, make_uint4(0, 0, 0, 0));
+                    umma_commit_if(go, &bar[L::S_FULL + 2 * x + at]);
+                    if (half) umma_commit_if(go, &bar[L::EMPTY + st]);
+                    if (t == last - 1) umma_commit_if(go, &bar[L::Q_FREE]);
+                    return true;
+                };
+                auto product = [&](int t) -> bool {
+                    const int s = s1 + (t >> 1) * hop, half = t & 1, u = u0 + 2 * s + 1, st = u % NS, at = (turns + t) & 1;
+                    if (half == 0) {
+                        if (!full(u)) return false;
+                        if (tail && s == steps - 1) {
+                            // the sequence ends inside a block: zero the value rows behind its end (both streams of
+                            // two tiles do, each before its own product; the second writes zeros over zeros)
+                            const int r0 = p.C % kKeys, rows = kBlockSize - p.C % kBlockSize;
+                            for (int e = lane; e < rows * 8 * NH; e += 32) {
+                                const int row = r0 + (e >> 3) % rows, h = (e >> 3) / rows;
+                                sts128(base + L::kRing + st * L::UT + h * kHalf + row * 128 + (e & 7) * 16, make_uint4(0, 0, 0, 0));
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
                         }
-                        fence_proxy_async_smem();
-                        __syncwarp();
                     }
-                    if (!(ok = wait_all(&bar[L::P_FULL + x], turns & 1))) break;
+                    if (!wait_all(&bar[L::P_FULL + 2 * x + at], ((turns + t) >> 1) & 1)) return false;
                     tc_fence_after();
-                    const uint64_t vm = vd + ((vs * L::UT) >> 4);
+                    const uint64_t vm = vd + ((st * L::UT + half * kTurn * 128) >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; ++kk)
-                        umma_ts_if(go, tm + kColO + x * D, tm + x * kKeys + kk * 8, vm + ((kk * 2048) >> 4), idesc_pv,
-                                   !first || kk > 0 ? 1u : 0u);
-                    umma_commit_if(go, &bar[L::PV_DONE + x]);
-                    umma_commit_if(go, &bar[L::EMPTY + vs]);
-                    ++turns;
+                    for (int kk = 0; kk < kTurn / 16; ++kk)
+                        umma_ts_if(go, tm + kColO + x * D, tm + x * kKeys + at * kTurn + kk * 8, vm + ((kk * 2048) >> 4), idesc_pv,
+                                   t > 0 || kk > 0 ? 1u : 0u);
+                    umma_commit_if(go, &bar[L::PV_DONE + 2 * x + at]);
+                    if (half) umma_commit_if(go, &bar[L::EMPTY + st]);
+                    return true;
+                };
+                if (last == 0) umma_commit_if(go, &bar[L::Q_FREE]);  // (a piece of one step has none for stream 0)
+                else ok = scores(0);
+                for (int t = 0; t < last && ok; ++t) {
+                    // the next turn's scores first, unless their keys have not come yet: values wait for nothing then
+                    const int u = u0 + 2 * (s1 + ((t + 1) >> 1) * hop);
+                    const bool more = t + 1 < last;
+                    const bool early = more && ((t + 1) & 1 || (landed(u) && (two || (landed(u - 1) && landed(u - 2)))));
+                    if (early && !(ok = scores(t + 1))) break;
+                    if (!(ok = product(t))) break;
+                    if (more && !early) ok = scores(t + 1);
                 }
+                if (ok) ok = pass(steps);
                 if (!ok) break;
-                if (q_held) umma_commit_if(go, &bar[L::Q_FREE]);  // (a piece of one step has none for stream 1)
+                u0 += 2 * steps;
+                turns += last;
                 done_with(n);
                 ++n;
             }
@@ -666,7 +696,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
         const uint32_t ts = tmem + ((uint32_t)row0 << 16);
         float2 *stat = reinterpret_cast<float2 *>(sm + L::kStat);
         const bool rising = a.qscale >= 0.0f;  // else scores are negated as they are read
-        int turns = 0, joins = 0;              // this stream's steps, units of one tile
+        int turns = 0, joins = 0;              // this stream's turns, units of one tile
         bool ok = true;
         for (int i = 0; ok; ++i) {  // pieces
             const Piece *pp = next_piece(i);
@@ -681,44 +711,48 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
             const float qs = fabsf(a.qscale) * (F8 ? a.scales[p.g] : 1.0f), vs = F8 ? a.scales[a.n_kv + p.g] : 1.0f;
             const int32_t *trow = a.block_tables + (int64_t)p.b * a.W + p.s0 * kStepBlocks;
             const int blocks = p.blocks - p.s0 * kStepBlocks;
-            const int hop = two ? 1 : 2, s1 = two ? 0 : x;
+            const int hop = two ? 1 : 2, s1 = two ? 0 : 1 - x;
             auto node = [&](int i) -> int { return min(t0 + g8 + 8 * i, p.R - 1) / G; };  // of this thread's row i
             auto ids_of = [&](int s) -> int {
                 return lane < kStepBlocks && s < n && s * kStepBlocks + lane < blocks ? trow[s * kStepBlocks + lane] : -1;
             };
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // of the rows; sums of this thread's keys
             int nxt = ids_of(s1);
-            for (int s = s1; s < n; s += hop, ++turns) {
-                // blocks that are there, as the copies decided
-                const uint32_t valid = __ballot_sync(kFull, lane < kStepBlocks && nxt >= 0 && nxt < a.num_blocks);
-                nxt = ids_of(s + hop);
-                if (!(ok = wait_all(&bar[L::S_FULL + x], turns & 1))) break;
+            uint32_t valid = 0;
+            for (int s = s1, t = 0; s < n; s += hop * (t & 1), ++t, ++turns) {  // (two turns a step)
+                const int half = t & 1;
+                if (half == 0) {  // blocks that are there, as the copies decided
+                    valid = __ballot_sync(kFull, lane < kStepBlocks && nxt >= 0 && nxt < a.num_blocks);
+                    nxt = ids_of(s + hop);
+                }
+                const uint32_t place = ts + x * kKeys + (turns & 1) * kTurn;
+                if (!(ok = wait_all(&bar[L::S_FULL + 2 * x + (turns & 1)], (turns >> 1) & 1))) break;
                 if (live) {
                     tc_fence_after();
-                    uint32_t pk[kKeys / 4];  // words 2 n + i: row i's weights of keys 8 n + 2 c4, + 1
+                    uint32_t pk[kTurn / 4];  // words 2 n + i: row i's weights of keys 8 n + 2 c4, + 1
                     float add[2], alpha[2] = {1.0f, 1.0f};
-                    // Weights are formed with the reference as it is, while the maximum is found; the rare step that
+                    // Weights are formed with the reference as it is, while the maximum is found; the rare turn that
                     // raises it reads the scores again.  (A piece's first one finds the maximum first.)
-                    bool fresh = s == s1, again = false;
+                    bool fresh = t == 0, again = false;
                     do {
-                        uint32_t sr[kKeys / 2];  // words 4 n + 2 i + e: row i's key 8 n + 2 c4 + e
-                        tmem_ld_rows64(ts + x * kKeys, sr);
-                        tmem_ld_rows64(ts + x * kKeys + 64, sr + 32);
+                        uint32_t sr[kTurn / 2];  // words 4 n + 2 i + e: row i's key 8 n + 2 c4 + e
+                        tmem_ld_rows64(place, sr);
                         tmem_wait_ld();
                         if (!rising) {
 #pragma unroll
-                            for (int i = 0; i < kKeys / 2; ++i) sr[i] ^= 0x80000000u;
+                            for (int i = 0; i < kTurn / 2; ++i) sr[i] ^= 0x80000000u;
                         }
-                        const int rel = rel0 + s * kKeys;
-                        if (rel + kKeys > 0 || valid != (1u << kStepBlocks) - 1) {
+                        const int rel = rel0 + s * kKeys + half * kTurn;
+                        const uint32_t there = (valid >> (half * kTurnBlocks)) & ((1u << kTurnBlocks) - 1);
+                        if (rel + kTurn > 0 || there != (1u << kTurnBlocks) - 1) {
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 const uint32_t *mrow = a.mask + ((int64_t)p.row0 + node(i)) * 2 * a.words;
 #pragma unroll
-                                for (int c = 0; c < 4; ++c) {
+                                for (int c = 0; c < kTurn / 32; ++c) {
                                     uint32_t bits = node_bits(mrow, 2 * a.words, p.T, rel + 32 * c);
-                                    if (!((valid >> (2 * c)) & 1u)) bits &= 0xffff0000u;
-                                    if (!((valid >> (2 * c)) & 2u)) bits &= 0xffffu;
+                                    if (!((there >> (2 * c)) & 1u)) bits &= 0xffff0000u;
+                                    if (!((there >> (2 * c)) & 2u)) bits &= 0xffffu;
                                     bits >>= 2 * c4;
 #pragma unroll
                                     for (int k = 0; k < 8; ++k)
@@ -732,9 +766,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                         for (int i = 0; i < 2; ++i) {
                             float mx[4];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                mx[j] = fmaxf(fmax3(fmax3(fmax3(e(i, j), e(i, j + 4), e(i, j + 8)), e(i, j + 12), e(i, j + 16)), e(i, j + 20),
-                                                    e(i, j + 24)), e(i, j + 28));
+                            for (int j = 0; j < 4; ++j) mx[j] = fmaxf(fmax3(e(i, j), e(i, j + 4), e(i, j + 8)), e(i, j + 12));
                             top[i] = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
                         }
                         auto reduce = [&]() {
@@ -752,7 +784,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                         const float nm[2] = {m[0] == -INFINITY ? 0.0f : -m[0], m[1] == -INFINITY ? 0.0f : -m[1]};
                         float2 part[2][2] = {};
 #pragma unroll
-                        for (int j = 0; j < kKeys / 8; ++j) {
+                        for (int j = 0; j < kTurn / 8; ++j) {
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 const float2 d = ffma2(make_float2(e(i, 2 * j), e(i, 2 * j + 1)), make_float2(qs, qs), make_float2(nm[i], nm[i]));
@@ -779,9 +811,11 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                     } while (again);
                     l[0] = fmaf(l[0], alpha[0], add[0]);
                     l[1] = fmaf(l[1], alpha[1], add[1]);
-                    // (the scores were issued after the last product had run, so O is final)
                     if (again) {
-#pragma unroll
+                        // the last turn's product has run
+                        if (!(ok = wait_all(&bar[L::PV_DONE + 2 * x + ((turns - 1) & 1)], ((turns - 1) >> 1) & 1))) break;
+                        tc_fence_after();
+#pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
                             uint32_t o[16];
                             tmem_ld_rows32(ts + kColO + x * D + c, o);
@@ -792,20 +826,19 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                         }
                     }
                     // the weights over the scores, which are read
-                    tmem_st_pairs32(ts + x * kKeys, pk);
-                    tmem_st_pairs32(ts + x * kKeys + 32, pk + 16);
+                    tmem_st_pairs32(place, pk);
                     tmem_wait_st();
                 }
                 // stream 1: its O of the last unit of one tile is read
-                if (x == 1 && s == s1 && joins > 0 && !(ok = wait_all(&bar[L::TAKEN + w8], (joins - 1) & 1))) break;
+                if (x == 1 && t == 0 && joins > 0 && !(ok = wait_all(&bar[L::TAKEN + w8], (joins - 1) & 1))) break;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[L::P_FULL + x]);
+                if (lane == 0) mbar_arrive(&bar[L::P_FULL + 2 * x + (turns & 1)]);
             }
             if (!ok) break;
             // ---- the end of the piece ----
             const bool any = s1 < n;  // this stream had steps
-            if (any && !(ok = wait_all(&bar[L::PV_DONE + x], (turns - 1) & 1))) break;
+            if (any && !(ok = wait_all(&bar[L::PV_DONE + 2 * x + ((turns - 1) & 1)], ((turns - 1) >> 1) & 1))) break;
             tc_fence_after();
             float sum[2], fa[2], fb[2];  // O = fa O_x + fb O_1
 #pragma unroll
@@ -818,7 +851,6 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
             }
             if (!two) {
                 if (x == 1) {
-                    if (joins > 0 && !any && !(ok = wait_all(&bar[L::TAKEN + w8], (joins - 1) & 1))) break;
                     if (c4 == 0) {
                         stat[row0 + g8] = make_float2(m[0], sum[0]);
                         stat[row0 + g8 + 8] = make_float2(m[1], sum[1]);
@@ -845,13 +877,14 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
             }
             if (live) {
                 const bool join = !two && n > 1, whole = p.whole();
+                const int from = two ? x : n > 1 ? 0 : 1;  // a piece of one step is stream 1's alone
                 const int slot = 2 * (int)blockIdx.x + (p.s0 == 0 ? 1 : 0);
                 bool in[2];
                 int64_t to[2];  // the row's place: in out, or in the slot
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const float norm = whole ? (sum[i] > 0.0f ? vs / sum[i] : sum[i] == 0.0f ? 0.0f : sum[i]) : vs;
-                    fa[i] *= norm;
+                    fa[i] = (from == x ? fa[i] : fb[i]) * norm;
                     fb[i] *= norm;
                     const int r = t0 + g8 + 8 * i;
                     in[i] = r < p.R;
@@ -862,7 +895,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[16], o1[16];
-                    tmem_ld_rows32(ts + kColO + x * D + c, o);
+                    tmem_ld_rows32(ts + kColO + from * D + c, o);
                     if (join) tmem_ld_rows32(ts + kColO + D + c, o1);
                     tmem_wait_ld();
 #pragma unroll
