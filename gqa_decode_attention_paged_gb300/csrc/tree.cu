@@ -18,10 +18,9 @@
 //     The stream of all units' steps of 128 keys, weighed by what they cost, is
 //     cut into one equal slice per CTA, so that every SM has the same work
 //     whatever the lengths are, and one long sequence keeps all of them busy (64
-//     trees of 1..60 nodes on an E4M3 cache: 201 us with steps of one and of two
-//     tiles weighed alike, XX so).  A unit that a
-//     slice holds whole is finished by its CTA; of one that is cut each CTA
-//     leaves its part (reference maximum, sum, unnormalised O), which
+//     trees of 1..60 nodes on an E4M3 cache: 201 us with all steps weighed
+//     alike, 149 so).  A unit that a slice holds whole is finished by its CTA; of
+//     one that is cut each CTA leaves its part (reference maximum, sum, unnormalised O), which
 //     tree_merge_kernel joins.  A slice cuts at most two units, the one it
 //     starts inside of (partial slot 2 cta) and the one it ends inside of
 //     (2 cta + 1).
@@ -36,10 +35,9 @@
 //     two shuffles reduce.  (A thread per row, four warps a stream, left every
 //     scheduler with two warps and their dependent chains.)
 //   * one warp walks the slice, says what the next piece of work is (a queue of
-//     four in shared memory: where every warp walked for itself, the walk's
-//     registers were missing in the softmax, 1111 against XX us), and streams
-//     what the MMAs take through one ring of 32 KiB (d 128) tiles: keys of a
-//     step, its values, keys of the next.  Two warps issue one stream's MMAs
+//     four in shared memory: where every warp walked for itself, the softmax
+//     warps spilled), and streams what the MMAs take through one ring of 32 KiB
+//     (d 128) tiles: keys of a step, its values, keys of the next.  Two warps issue one stream's MMAs
 //     each: S = Q K^T, and when the weights are written over S, O += P V.
 //   * the reference maximum is raised lazily (O is rescaled only when a row's
 //     maximum grows by more than 2^8).  Weights are rounded to bf16 (FP8 pools:
@@ -71,16 +69,13 @@ constexpr int kSoftmaxWarps = 16;
 constexpr int kCopyWarp = 16, kMmaWarp = 17, kPrepWarp = 20;
 constexpr int kMaxWords = 16;
 constexpr int kMany = 4;                   // windows of 32 sequences whose lengths are read at a time
-static_assert(sizeof(int) * 14 <= 64, "");
 // What a step costs in a unit of one tile (bound by HBM, or by the widening of its keys) and of two (by the products
-// and exponentials), and a unit besides its steps: bf16 1.4, 2.1 and 3 us, E4M3 1.3, 2.6 and 3 us.
-template <bool F8>
-struct Cost {
-    static constexpr int kOne = F8 ? 1 : 2, kTwo = F8 ? 2 : 3, kUnit = F8 ? 3 : 6;
-    static constexpr int kMinShare = kUnit + 2 * kOne;  // of a slice
-    // (between two steps' beginnings: no slice inside a unit is without one)
-    static_assert(kMinShare >= kUnit + kTwo, "");
-};
+// and exponentials), and a unit besides its steps: about 1.4, 2 and 4 us.  (16 trees of 26 nodes on 1024..2048 tokens
+// and 64 of 1..60 on E4M3: 38.1 and 131 us so, 38.8 and 140 with 3, 4 and 6, 38.9 and 128..135 with units at half more.)
+constexpr int kCostOne = 2, kCostTwo = 3, kCostUnit = 6;
+constexpr int kMinShare = kCostUnit + 2 * kCostOne;  // of a slice
+// (between two steps' beginnings: no slice inside a unit is without one)
+static_assert(kMinShare >= kCostUnit + kCostTwo, "");
 template <bool F8>
 struct Warps {
     static constexpr int kWarps = F8 ? 24 : 20, kThreads = kWarps * 32;
@@ -224,28 +219,26 @@ __device__ __forceinline__ int inclusive_sum(int x, int lane)
 }
 
 // The units of a sequence and KV head with R rows and S steps: all but the last have two tiles.  In a unit of step cost
-// w, step 0 begins at 0 and step s at kUnit + w s.
-template <bool F8>
+// w, step 0 begins at 0 and step s at kCostUnit + w s.
 struct Units {
     int n, full, last;  // units, cost of all but the last, step cost of the last
     int all;            // cost of the whole
     __device__ __forceinline__ Units(int R, int S)
     {
-        using C = Cost<F8>;
         n = (R + kUnitRows - 1) / kUnitRows;
-        full = S * C::kTwo + C::kUnit;
-        last = R - (n - 1) * kUnitRows > kRows ? C::kTwo : C::kOne;
-        all = (n - 1) * full + S * last + C::kUnit;
+        full = S * kCostTwo + kCostUnit;
+        last = R - (n - 1) * kUnitRows > kRows ? kCostTwo : kCostOne;
+        all = (n - 1) * full + S * last + kCostUnit;
     }
     // steps that begin before x
     static __device__ __forceinline__ int begun(int x, int w)
     {
-        return x <= 0 ? 0 : max(1, (x - Cost<F8>::kUnit + w - 1) / w);
+        return x <= 0 ? 0 : max(1, (x - kCostUnit + w - 1) / w);
     }
 };
 
 // Sequence b's nodes and length; its cost, none where it does not fit.
-template <int G, bool F8>
+template <int G>
 __device__ __forceinline__ int sequence(const Args &a, int b, Walker &w, bool flag)
 {
     w.row0 = w.T = w.C = 0;
@@ -259,20 +252,20 @@ __device__ __forceinline__ int sequence(const Args &a, int b, Walker &w, bool fl
     w.row0 = lo;
     w.T = hi - lo;
     w.C = C;
-    return Units<F8>(w.T * G, (C + kKeys - 1) / kKeys).all * a.n_kv;
+    return Units(w.T * G, (C + kKeys - 1) / kKeys).all * a.n_kv;
 }
 
-template <int G, bool F8>
+template <int G>
 __device__ __forceinline__ void load_window(Walker &w, const Args &a, int lane, bool flag)
 {
-    const int work = sequence<G, F8>(a, w.wb + lane, w, flag);
+    const int work = sequence<G>(a, w.wb + lane, w, flag);
     w.incl = inclusive_sum(work, lane);
     w.tot = __shfl_sync(kFull, w.incl, 31);
 }
 
 // The piece that begins at f in the stream, up to `end`; false past it.  A step belongs to the slice in which it
 // begins.  Warp-wide, uniform result.
-template <int G, bool F8>
+template <int G>
 __device__ __forceinline__ bool find_piece(Walker &w, const Args &a, int f, int end, int share, Piece &p, int lane)
 {
     for (;;) {
@@ -281,7 +274,7 @@ __device__ __forceinline__ bool find_piece(Walker &w, const Args &a, int f, int 
             if (w.wb + 32 >= a.batch) return false;
             w.wbase += w.tot;
             w.wb += 32;
-            load_window<G, F8>(w, a, lane, false);
+            load_window<G>(w, a, lane, false);
         }
         const int at = f - w.wbase;
         const int l = __ffs(__ballot_sync(kFull, w.incl > at)) - 1;
@@ -291,19 +284,19 @@ __device__ __forceinline__ bool find_piece(Walker &w, const Args &a, int f, int 
         p.C = __shfl_sync(kFull, w.C, l);
         p.S = (p.C + kKeys - 1) / kKeys;
         p.R = p.T * G;
-        const Units<F8> u(p.R, p.S);
+        const Units u(p.R, p.S);
         const int within = at - (__shfl_sync(kFull, w.incl, l) - u.all * a.n_kv);
         p.g = within / u.all;
         int x = within - p.g * u.all;  // in the KV head, then in the unit
-        const int unit = min(x / u.full, u.n - 1), cost = unit == u.n - 1 ? u.last : Cost<F8>::kTwo;
+        const int unit = min(x / u.full, u.n - 1), cost = unit == u.n - 1 ? u.last : kCostTwo;
         x -= unit * u.full;
         p.r0 = unit * kUnitRows;
-        const int size = p.S * cost + Cost<F8>::kUnit, e = min(size, x + (end - f));
-        p.s0 = Units<F8>::begun(x, cost);
-        p.n = (e == size ? p.S : Units<F8>::begun(e, cost)) - p.s0;
+        const int size = p.S * cost + kCostUnit, e = min(size, x + (end - f));
+        p.s0 = Units::begun(x, cost);
+        p.n = (e == size ? p.S : Units::begun(e, cost)) - p.s0;
         p.next = f + (e - x);
         // the last step's beginning, behind this slice's end
-        const int left = (p.S == 1 ? 0 : Cost<F8>::kUnit + cost * (p.S - 1)) - e;
+        const int left = (p.S == 1 ? 0 : kCostUnit + cost * (p.S - 1)) - e;
         p.more = left < 0 ? 0 : left / share + 1;
         p.blocks = (p.C + kBlockSize - 1) / kBlockSize;
         if (p.n > 0) return true;
@@ -405,20 +398,20 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
             int total = 0, many0 = 0, many1 = 0, f0, f1, share;
             static_assert(kMaxBatch <= 64 * 32 * kMany, "");
             if (a.batch <= 32) {
-                load_window<G, F8>(wk, a, lane, blockIdx.x == 0);
+                load_window<G>(wk, a, lane, blockIdx.x == 0);
                 total = wk.tot;
             } else {
                 for (int b = 0; b < a.batch; b += 32 * kMany) {
                     int x = 0;
 #pragma unroll
-                    for (int i = 0; i < kMany; ++i) x += sequence<G, F8>(a, b + 32 * i + lane, wk, blockIdx.x == 0);
+                    for (int i = 0; i < kMany; ++i) x += sequence<G>(a, b + 32 * i + lane, wk, blockIdx.x == 0);
                     x = __reduce_add_sync(kFull, x);
                     total += x;
                     const int i = b / (32 * kMany);  // lane i % 32 keeps it
                     if (lane == i % 32) (i < 32 ? many0 : many1) = x;
                 }
             }
-            share = max(Cost<F8>::kMinShare, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+            share = max(kMinShare, (total + (int)gridDim.x - 1) / (int)gridDim.x);
             f0 = min((int64_t)total, (int64_t)blockIdx.x * share);
             f1 = min((int64_t)total, (int64_t)f0 + share);
             if (a.batch > 32) {
@@ -429,7 +422,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                 wk.wb = min(i * 32 * kMany, a.batch - 1) / (32 * kMany) * (32 * kMany);
                 const int j = wk.wb / (32 * kMany);
                 wk.wbase = __shfl_sync(kFull, j < 32 ? incl0 - many0 : incl1 - many1, j % 32);
-                load_window<G, F8>(wk, a, lane, false);
+                load_window<G>(wk, a, lane, false);
             }
             const uint64_t policy = l2_policy_evict_normal();
             const uint32_t go = elect_one();  // one lane issues all copies, the warp running as one
@@ -439,7 +432,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
             for (int f = f0;;) {
                 if (*abort_flag) break;
                 Piece p;
-                const bool some = find_piece<G, F8>(wk, a, f, f1, share, p, lane);
+                const bool some = find_piece<G>(wk, a, f, f1, share, p, lane);
                 if (!some) p.n = 0;
                 const int slot = n % L::kQueue;
                 if (n >= L::kQueue && !(ok = wait_all(&bar[L::DONE + slot], (n / L::kQueue - 1) & 1))) break;
@@ -1133,7 +1126,7 @@ extern "C" pkv_status paged_tree_attention(pkv_pool *pool, const void *q, int64_
     const int64_t most = std::min<int64_t>((int64_t)64 * mask_words, n_rows) * G;  // rows of a sequence and KV head
     const int64_t units = (int64_t)batch * pool->n_kv * ((most + kUnitRows - 1) / kUnitRows);
     const int64_t steps = (max_blocks_per_seq + kStepBlocks - 1) / kStepBlocks;
-    if (units > INT32_MAX / (3 * steps + 4)) return fail(PKV_EUNSUPPORTED, "%s: too many rows x table entries", who);
+    if (units > INT32_MAX / (kCostTwo * steps + kCostUnit)) return fail(PKV_EUNSUPPORTED, "%s: too many rows x table entries", who);
     const int ctas = (int)std::min<int64_t>(pool->num_sms, units * steps);
     const Space sp = space_of(pool, n_rows, G, ctas);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
