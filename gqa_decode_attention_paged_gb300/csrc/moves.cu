@@ -6,8 +6,11 @@
 // (scale, zero point) pair is 8), whatever the pool's type.  What bounds them
 // is latency: a few rows of 4 KiB per sequence move, behind a chain of
 // dependent reads (lengths and choices, then table entries, then rows).  So
-// every thread block handles one (sequence, KV head) or a few heads of one
-// beam, all of a step's reads are issued at once, and nothing is staged.
+// every thread block handles one (sequence or beam, KV head), all of a step's
+// reads are issued at once, and nothing is staged.  In a graph, 8 KV heads of
+// 128: 64 sequences that keep up to 7 of 26 nodes take 2.4 us, 200 on 4-bit rows
+// 2.8 us; 16 new beams 2.3 us, 640 with tables of 128 blocks 5.3 us (13.6 MB: 2.6
+// TB/s).
 #include <algorithm>
 
 #include "pkv_internal.cuh"
@@ -110,7 +113,7 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const __grid_cons
 struct ReorderArgs {
     uint8_t *pool;
     int64_t num_blocks;
-    int n_kv, heads;          // heads of a thread block
+    int n_kv;
     const int32_t *parents;   // [batch * k]
     int beams, k;
     const int32_t *tables;    // [batch * beams][W]
@@ -122,8 +125,8 @@ struct ReorderArgs {
     unsigned *err;
 };
 
-// One new beam and `heads` KV heads (the first heads' block writes the table
-// row).  The beam's entries before the block that it writes next are its
+// One new beam and KV head (the first head's block writes the table row).  The
+// beam's entries before the block that it writes next are its
 // parent's; that block is the parent's for the parent's first child, and for
 // every other child a spare one into which the filled rows are copied.
 template <int D, int KV>
@@ -173,33 +176,26 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const __grid_con
         if (lead && tid == 0) atomicOr(a.err, PKV_DEVERR_BLOCK_RANGE);
         return;
     }
-    // the filled rows of every head: `pieces` 16-byte pieces of keys, as many of values (and the rows' parameters)
+    // the head's filled rows: `pieces` 16-byte pieces of keys, as many of values (and the rows' parameters)
     const int pieces = rows * ROWB / 16;
-    const int h0 = blockIdx.y * a.heads, hn = min(a.heads, a.n_kv - h0);
-    const uint8_t *src = a.pool + ((int64_t)from * a.n_kv + h0) * ENTRY;
-    uint8_t *dst = a.pool + ((int64_t)fresh * a.n_kv + h0) * ENTRY;
-    constexpr int U = 4;
-    const int total = hn * 2 * pieces;
-    for (int i0 = tid; i0 < total; i0 += U * kThreads) {
-        uint4 x[U];
-        int64_t at[U];
+    const uint8_t *src = a.pool + ((int64_t)from * a.n_kv + blockIdx.y) * ENTRY;
+    uint8_t *dst = a.pool + ((int64_t)fresh * a.n_kv + blockIdx.y) * ENTRY;
+    constexpr int U = (2 * kBlockSize * ROWB / 16 + kThreads - 1) / kThreads;
+    uint4 x[U];
+    int at[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * kThreads;
-            if (i >= total) continue;
-            const int h = i / (2 * pieces), r = i - h * 2 * pieces;
-            const bool value = r >= pieces;
-            at[u] = h * ENTRY + (value ? kBlockSize * ROWB + (r - pieces) * 16 : r * 16);
-            x[u] = ldg_nc_v4(src + at[u]);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (i0 + u * kThreads < total) *reinterpret_cast<uint4 *>(dst + at[u]) = x[u];
+    for (int u = 0; u < U; ++u) {
+        const int i = u * kThreads + tid;
+        at[u] = i < 2 * pieces ? (i >= pieces ? kBlockSize * ROWB + (i - pieces) * 16 : i * 16) : -1;
+        if (at[u] >= 0) x[u] = ldg_nc_v4(src + at[u]);
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (at[u] >= 0) *reinterpret_cast<uint4 *>(dst + at[u]) = x[u];
     if constexpr (KV == PKV_INT4) {
-        for (int i = tid; i < hn * rows; i += kThreads) {
-            const int64_t at = (i / rows) * ENTRY + i4_params_offset(D) + 8 * (i % rows);
-            *reinterpret_cast<float2 *>(dst + at) = __ldg(reinterpret_cast<const float2 *>(src + at));
+        if (tid < rows) {
+            const int p_at = i4_params_offset(D) + 8 * tid;
+            *reinterpret_cast<float2 *>(dst + p_at) = __ldg(reinterpret_cast<const float2 *>(src + p_at));
         }
     }
 }
@@ -301,7 +297,6 @@ extern "C" pkv_status paged_beam_reorder(pkv_pool *pool, const int32_t *parents,
     a.pool = static_cast<uint8_t *>(pool->k);
     a.num_blocks = pool->num_blocks;
     a.n_kv = pool->n_kv;
-    a.heads = 1;
     a.parents = parents;
     a.beams = beams;
     a.k = k;
@@ -313,7 +308,7 @@ extern "C" pkv_status paged_beam_reorder(pkv_pool *pool, const int32_t *parents,
     a.lens_out = lens_out;
     a.err = pool->err;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const dim3 grid((unsigned)((int64_t)batch * k), (unsigned)((pool->n_kv + a.heads - 1) / a.heads));
+    const dim3 grid((unsigned)((int64_t)batch * k), (unsigned)pool->n_kv);
     LaunchScope ls(pool, kBlocks, s);
     cudaError_t e = PKV_LAUNCH_BY_POOL(beam_reorder_kernel, grid, s, a);
     ls.done();
