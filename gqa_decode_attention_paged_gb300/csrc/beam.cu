@@ -10,7 +10,8 @@
 // (about five per logit).  One launch: a scan of the rows, cut into pieces so that
 // every SM has three blocks where the rows are few, leaves each piece's maximum,
 // sum of exponentials and k greatest logits; the block that is the last of a
-// search to get there merges them (a launch of its own took 4 us more).
+// search to get there merges them (as a second launch that took the GPU as long,
+// and the host 20 us a call instead of 15).
 //
 // Reading.  A piece streams through a ring of three parts of 16 KiB in shared
 // memory (bulk copies: a vector a thread ahead kept 64 KiB in flight on an SM and
@@ -35,8 +36,9 @@
 //
 // Accuracy.  Candidates of different beams may lie arbitrarily close, so what
 // decides between them is held in more than 32 bits: the exponentials are
-// 32-bit (of x - m, exact near the maximum, where they count), a thread's sum
-// too, all further sums are 64-bit integers (2^-40 of the largest term), and
+// 32-bit (of x - m, exact near the maximum, where they count), a thread adds 16
+// or 32 of them in 32 bits and those sums with what their additions lose, all
+// further sums are 64-bit integers (2^-40 of the largest term), and
 // the logarithm and v are doubles.
 #include <algorithm>
 #include <climits>
@@ -444,16 +446,19 @@ __device__ __forceinline__ float greatest_of(const uint4 &v)
     }
 }
 
-// A thread's greatest logit so far and the sum of exp(x - m).
+// A thread's greatest logit so far and the sum of exp(x - m), as s + lost: a row of 2^22 logits in one piece is 1024
+// parts, which plain 32-bit additions would round as often.
 struct Sum {
-    float m = -INFINITY, s = 0.0f;
+    float m = -INFINITY, s = 0.0f, lost = 0.0f;
     // a part's vectors, with the greatest logit top
     template <typename T>
     __device__ __forceinline__ void add(const uint4 (&v)[kVecs], float top)
     {
         constexpr int N = Elems<T>::N;
         if (top > m) {
-            s = m == -INFINITY ? s : s * ex2((m - top) * kLog2e);
+            const float less = m == -INFINITY ? 1.0f : ex2((m - top) * kLog2e);
+            s *= less;
+            lost *= less;
             m = top;
         }
         // (of x - m, not of x log2(e) - m log2(e), whose second product's rounding would be in every term alike)
@@ -469,7 +474,10 @@ struct Sum {
                 part = fadd2(part, make_float2(ex2(d.x), ex2(d.y)));
             }
         }
-        s += part.x + part.y;
+        // (the greater of the two is not known: the two-sided form of the error of an addition)
+        const float add = part.x + part.y, t = __fadd_rn(s, add), b = __fsub_rn(t, s);
+        lost = __fadd_rn(lost, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(add, b)));
+        s = t;
     }
 };
 
@@ -614,7 +622,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) beam_select_kernel(con
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sh.tops[w]);
     uint64_t f = 0;  // this thread's sum in units of 2^-40
-    if (!bad && sum.m > -INFINITY) f = __float2ull_rn(sum.s * ex2((sum.m - M) * kLog2e) * 0x1p40f);
+    if (!bad && sum.m > -INFINITY) {
+        const float unit = ex2((sum.m - M) * kLog2e) * 0x1p40f;
+        f = (uint64_t)(__float2ll_rn(sum.s * unit) + __float2ll_rn(sum.lost * unit));
+    }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) f += __shfl_xor_sync(kFull, f, o);
     if (lane == 0) sh.sums[warp] = f;

@@ -629,7 +629,7 @@ pkv_status paged_tree_commit(pkv_pool *pool, const int32_t *qo_indptr, const int
  *               which nothing above -infinity is left hold -1, -1 and
  *               -infinity.  Must overlap neither each other nor an input.
  * What decides between continuations is held in 64 bits, except for the
- * exponentials themselves and the sums of a few hundred of them (32 bits);
+ * exponentials themselves and the sums of up to 32 of them (32 bits);
  * out_scores are rounded once.  A beam whose logits hold a NaN or +infinity,
  * or whose score is one, has no continuations and sets PKV_DEVERR_NAN.
  * batch <= 8192, beams and k in 1 .. 64, vocab <= 2^22.  One launch, no
