@@ -46,7 +46,11 @@
 //     against 64 bits).
 //   * FP8 pools: the E4M3 tiles are widened to f16 in place by four warps.
 //   * value rows behind the sequence's end are zeroed in shared memory before
-//     their product: a weight of 0 does not cancel what is not finite.
+//     their product: a weight of 0 does not cancel what is not finite.  Nodes that
+//     a row does not see may hold anything, too: what is not finite in the nodes'
+//     value rows becomes 0 there, and is added to the results of the rows that see
+//     it, when the slice is done (16 trees of 26 nodes on 1024..2048 tokens: 38 us
+//     without the look at the nodes' rows, 39 with it).
 // Every mbarrier wait is bounded; on a timeout the CTA records
 // PKV_DEVERR_TIMEOUT, every role stops, the MMA and copy pipes are drained
 // (bounded) and the tensor memory is released before the CTA exits.
@@ -104,6 +108,7 @@ struct Args {
     int W;
     const int32_t *context_lens;
     int batch, n_q, n_kv;
+    const uint8_t *pool;
     int64_t num_blocks, n_rows;
     int oob_row;          // a row index past the end of the pool's entry rows (zero-filled box)
     float qscale;         // scale * log2(e)
@@ -139,7 +144,9 @@ struct Layout {
            DRAIN = DONE + kQueue, NBARS };
     static constexpr uint32_t kTmemSlot = kBar + NBARS * 8;
     static constexpr uint32_t kAbort = kTmemSlot + 4;
-    static constexpr uint32_t kEnd = kAbort + 4;
+    static constexpr uint32_t kOdd = kAbort + 4;    // a value of a node was not finite
+    static constexpr uint32_t kSlice = kOdd + 4;    // where the CTA's slice begins
+    static constexpr uint32_t kEnd = kSlice + 20;
     static constexpr size_t bytes = 1024 + kEnd;
     static_assert(bytes <= 232448, "shared memory beyond the 227 KiB a CTA may use");
 };
@@ -187,6 +194,28 @@ __device__ __forceinline__ void widen(uint32_t tile, int lane, int row0, int row
     }
 }
 
+// What is not finite in rows [r0, r1) of a tile becomes 0, and *odd 1 before that (a second warp that does the same
+// and finds the 0 finds the 1, too).
+template <int D, bool F8>
+__device__ __forceinline__ void zero_odd(uint32_t tile, int lane, int r0, int r1, volatile int *odd)
+{
+    constexpr int NH = D / 64;
+    constexpr uint32_t kExp = F8 ? 0x7c007c00u : 0x7f807f80u, kUp = F8 ? 0x04000400u : 0x00800080u;
+#pragma unroll 4
+    for (int e = r0 * 8 * NH + lane; e < r1 * 8 * NH; e += 32) {
+        const uint32_t at = tile + (e >> 3) % NH * kHalf + (e >> 3) / NH * 128 + (e & 7) * 16;
+        uint4 v = lds128(at);
+        // an exponent of ones carries into the sign's place
+        auto bad = [&](uint32_t w) { return ((w & kExp) + kUp) & 0x80008000u; };
+        if (bad(v.x) | bad(v.y) | bad(v.z) | bad(v.w)) {
+            *odd = 1;
+            __threadfence_block();
+            auto clear = [&](uint32_t w) { return w & ~((bad(w) >> 15) * 0xffffu); };
+            sts128(at, make_uint4(clear(v.x), clear(v.y), clear(v.z), clear(v.w)));
+        }
+    }
+}
+
 // ------------------------------------------------------------- the stream of steps
 
 // Steps [s0, s0 + n) of a unit: what a CTA does of it.
@@ -197,6 +226,10 @@ struct Piece {
     int more;          // pieces of the unit in the slices that follow
     int next;          // where the stream goes on
     int blocks;        // of the sequence
+    // the first of the piece's steps that has nodes, and the rows of a step's tile that are nodes
+    __device__ __forceinline__ int node_step() const { return (C - T) / kKeys - s0; }
+    __device__ __forceinline__ int node0(int s) const { return max(0, C - T - (s0 + s) * kKeys); }
+    __device__ __forceinline__ int node1(int s) const { return min(kKeys, C - (s0 + s) * kKeys); }
     __device__ __forceinline__ bool two() const { return R - r0 > kRows; }
     __device__ __forceinline__ bool whole() const { return n == S; }
 };
@@ -316,6 +349,68 @@ __device__ __forceinline__ uint32_t node_bits(const uint32_t *row, int words, in
     return bits;
 }
 
+// Adds what zero_odd took out of a piece's nodes to the rows [t0, t0 + 16) that see it, as this warp has stored them:
+// in out, or unnormalised at `part`.
+template <int D, int G, bool F8>
+__device__ __forceinline__ void add_odd(const Args &a, const Piece &p, int t0, float *part, int lane)
+{
+    constexpr int PL = D / 32;  // channels of a lane
+    constexpr int KV = F8 ? PKV_FP8_E4M3 : PKV_BF16;
+    constexpr int64_t ROWB = kv_row_bytes(KV, D), ENTRY = kv_entry_bytes(KV, D);
+    const int at0 = p.C - p.T, j1 = min(p.T, (p.s0 + p.n) * kKeys - at0);
+#pragma unroll 1
+    for (int j = max(0, p.s0 * kKeys - at0); j < j1; ++j) {
+        const int pos = at0 + j, id = a.block_tables[(int64_t)p.b * a.W + pos / kBlockSize];
+        if (id < 0 || id >= a.num_blocks) continue;
+        const uint8_t *v = a.pool + ((int64_t)id * a.n_kv + p.g) * ENTRY + kv_v_offset(KV, D) + pos % kBlockSize * ROWB;
+        float x[PL];
+        bool odd = false;
+#pragma unroll
+        for (int d = 0; d < PL; ++d) {
+            const int c = lane * PL + d;
+            if constexpr (F8) x[d] = (v[c] & 0x7f) == 0x7f ? NAN : 0.0f;
+            else x[d] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(v)[c]);
+            if (x[d] - x[d] == 0.0f) x[d] = 0.0f;  // (finite)
+            else odd = true;
+        }
+        if (!__any_sync(kFull, odd)) continue;
+#pragma unroll 1
+        for (int r = t0; r < min(t0 + 16, p.R); ++r) {
+            const int64_t row = (int64_t)p.row0 + r / G;
+            if (!((a.mask[row * 2 * a.words + (j >> 5)] >> (j & 31)) & 1u)) continue;
+            __nv_bfloat16 *dst = a.out + (row * a.n_q + p.g * G + r % G) * D;
+#pragma unroll
+            for (int d = 0; d < PL; ++d) {
+                const int c = lane * PL + d;
+                if (x[d] == 0.0f) continue;
+                if (part) part[(int64_t)(r - p.r0) * D + c] += x[d];
+                else dst[c] = __float2bfloat16(__bfloat162float(dst[c]) + x[d]);
+            }
+        }
+    }
+}
+
+// Where a CTA's slice begins and ends, and in which window of 32 sequences.
+struct Slice {
+    int f0, f1, share, wb, wbase;
+};
+
+// The same for all rows that a softmax warp (w8 of stream x) has stored.
+template <int D, int G, bool F8>
+__device__ __noinline__ void add_odd_rows(const Args &a, const Slice &from, int x, int t0, int lane)
+{
+    Walker wk;
+    wk.wb = from.wb;
+    wk.wbase = from.wbase;
+    load_window<G>(wk, a, lane, false);
+    Piece p;
+    for (int f = from.f0; find_piece<G>(wk, a, f, from.f1, from.share, p, lane); f = p.next) {
+        if (!p.two() && x == 1) continue;
+        float *part = p.whole() ? nullptr : a.ws_o + (2 * (int64_t)blockIdx.x + (p.s0 == 0 ? 1 : 0)) * a.slot_rows * D;
+        add_odd<D, G, F8>(a, p, p.r0 + (p.two() ? x * kRows : 0) + t0, part, lane);
+    }
+}
+
 // ------------------------------------------------------------- the kernel
 
 template <int D, int G, bool F8>
@@ -336,13 +431,14 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
     uint8_t *sm = tree_smem + ((1024u - (smem_u32(tree_smem) & 1023u)) & 1023u);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + L::kBar);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::kAbort);
+    volatile int *odd_flag = reinterpret_cast<volatile int *>(sm + L::kOdd);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(kFull, tid >> 5, 0);  // the same in all lanes, and known to be
 
     if (warp == kCopyWarp && lane == 0) {
         prefetch_tensormap(&tm_q);
         prefetch_tensormap(&tm_kv);
-        *abort_flag = 0;
+        *abort_flag = *odd_flag = 0;
     }
     static_assert(L::NBARS <= Wp::kThreads, "a thread per barrier");
     if (tid < L::NBARS) {
@@ -424,6 +520,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                 wk.wbase = __shfl_sync(kFull, j < 32 ? incl0 - many0 : incl1 - many1, j % 32);
                 load_window<G>(wk, a, lane, false);
             }
+            if (lane == 0) *reinterpret_cast<Slice *>(sm + L::kSlice) = {f0, f1, share, wk.wb, wk.wbase};
             const uint64_t policy = l2_policy_evict_normal();
             const uint32_t go = elect_one();  // one lane issues all copies, the warp running as one
             int u = 0, n = 0;                 // tiles of the ring, pieces
@@ -534,7 +631,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                 if (p.n == 0) break;
                 // (the same in all lanes, and known to be: an MMA whose operands are not takes 80 cycles to issue)
                 const bool two = __shfl_sync(kFull, (int)p.two(), 0);
-                const int steps = __shfl_sync(kFull, p.n, 0);
+                const int steps = __shfl_sync(kFull, p.n, 0), nodes = __shfl_sync(kFull, p.node_step(), 0);
                 const bool tail = !F8 && p.s0 + steps == p.S && p.C % kBlockSize;
                 const int hop = two ? 1 : 2, s1 = two ? 0 : 1 - x;        // this stream's steps: s1, s1 + hop, ..
                 const int last = 2 * ((steps - s1 + hop - 1) / hop);      // its turns
@@ -584,6 +681,9 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                                 const int row = r0 + (e >> 3) % rows, h = (e >> 3) / rows;
                                 sts128(base + L::kRing + st * L::UT + h * kHalf + row * 128 + (e & 7) * 16, make_uint4(0, 0, 0, 0));
                             }
+                        }
+                        if (!F8 && s >= nodes) zero_odd<D, F8>(base + L::kRing + st * L::UT, lane, p.node0(s), p.node1(s), odd_flag);
+                        if (!F8 && (s >= nodes || (tail && s == steps - 1))) {
                             fence_proxy_async_smem();
                             __syncwarp();
                         }
@@ -651,6 +751,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                 if (!(ok = pp != nullptr)) break;
                 const Piece &p = *pp;
                 if (p.n == 0) break;
+                const int nodes = p.node_step();
                 for (int i = 0; i < 2 * p.n; ++i, ++u) {
                     // (the first keys are widened before the queries, which come when the piece before is done with its own)
                     if (i == 1 && !(ok = widen_q(n, p.two()))) break;
@@ -671,6 +772,8 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                             }
                         }
                     }
+                    if ((i & 1) && (i >> 1) >= nodes)  // (the rows are written: widen ends with a warp's barrier)
+                        zero_odd<D, F8>(tile, lane, max(p.node0(i >> 1), own0), min(p.node1(i >> 1), own0 + kOwn), odd_flag);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar[L::FULL + st]);
@@ -914,6 +1017,10 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
             done_with(i);
         }
         if (!ok) set_abort();
+        else if (*odd_flag) {
+            __syncwarp();
+            add_odd_rows<D, G, F8>(a, *reinterpret_cast<const Slice *>(sm + L::kSlice), x, row0, lane);
+        }
     }
 
     tc_fence_before();
@@ -1142,6 +1249,7 @@ extern "C" pkv_status paged_tree_attention(pkv_pool *pool, const void *q, int64_
     a.batch = batch;
     a.n_q = n_q;
     a.n_kv = pool->n_kv;
+    a.pool = static_cast<const uint8_t *>(pool->k);
     a.num_blocks = pool->num_blocks;
     a.n_rows = n_rows;
     a.oob_row = (int)(pool->num_blocks * pool->n_kv * 2 * kBlockSize);

@@ -562,9 +562,9 @@ pkv_status paged_diff_reserve_workspace(pkv_pool *pool, int32_t batch, int32_t n
  * its table is skipped and sets PKV_DEVERR_CTX_RANGE.  A block id outside the
  * pool counts as masked and sets PKV_DEVERR_BLOCK_RANGE.  A row that sees
  * nothing is zero, and a visible key whose score is -infinity weighs nothing.
- * Cached rows behind C_b are never used, whatever they hold; a node that some
- * of the sequence's nodes see and others do not has to have finite values, as
- * the others multiply them by 0.
+ * Cached rows behind C_b are never used, and the keys and values of a node not
+ * by the rows that do not see it, whatever they hold (where nodes have values
+ * that are not finite, the call takes longer: some microseconds a node).
  * The softmax statistics and the sums are held in fp32; weights are rounded
  * once, to bf16 (bf16 pools) or f16 (FP8 pools, whose queries are multiplied
  * as f16: |q| must stay in f16's range), and out once, to bf16.

@@ -9,7 +9,7 @@ import torch
 
 import gqa_decode_attention_paged_gb300 as pkv
 from test_gpu_beam_select import check as check_selection
-from tree_ref import BS, check, pack, parents_of, plain, tree_bits
+from tree_ref import BS, Cache, check, pack, parents_of, plain, tree_bits
 
 N_KV, G, D, LAYERS = 2, 4, 128, 2
 KINDS = {"bf16": pkv.BF16, "fp8": pkv.FP8_E4M3}
@@ -335,3 +335,52 @@ def test_rows_in_one_piece_are_summed_as_exactly():
         assert torch.equal(tokens[r].long(), at[:3])
         err = (best[r].double() - v[:3]).abs()
         assert (err <= 2.0 ** -21 + 2.0 ** -20 + 2.0 ** -24 * v[:3].abs()).all(), err
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,nodes", [([200, 90], [40, 10]), ([16, 300], [16, 129]), ([3000, 50], [100, 1])])
+def test_what_hidden_nodes_hold_does_not_matter(kv, d, lens, nodes):
+    """Keys and values of some nodes that are not finite (padding behind a tree, a branch that was not computed): rows
+    that see a node have its channels' NaN and infinities, all else is as with zeros there."""
+    rng = random.Random(13)
+    with Cache(kv, 2, d, lens, seed=13) as c:
+        bits = [m for n in nodes for m in tree_bits(parents_of(n, rng))]
+        pads = {}  # (sequence, node): KV head, channels whose values are not finite
+        for b, n in enumerate(nodes):
+            for j in sorted({n - 1, n // 2, n // 3 + 1} - {0}):
+                if j < n:
+                    pads[b, j] = (rng.randrange(2), sorted(rng.sample(range(d), rng.choice([1, d]))))
+        ip = np.cumsum([0] + nodes)
+        nan = torch.zeros(sum(nodes), 8, d, dtype=torch.bool)
+        for (b, j), (g, channels) in pads.items():
+            pos = lens[b] - nodes[b] + j
+            blk = int(c.tables[b, pos // BS])
+            bad = torch.tensor([math.nan if kv == "fp8" or i % 3 else math.inf for i in channels]).to(c.v.dtype)
+            c.v.view(torch.uint8).view(*c.v.shape, -1)[blk, g, pos % BS, channels] = bad.view(torch.uint8).view(len(channels), -1)
+            c.v64[blk, g, pos % BS, channels] = 0.0
+            for r in range(ip[b], ip[b + 1]):
+                if (bits[r] >> j) & 1:
+                    nan[r, 4 * g:4 * g + 4, channels] = True
+        c.upload()
+        q = torch.randn(sum(nodes), 8, d, generator=torch.Generator().manual_seed(14)).to(torch.bfloat16).cuda()
+        words = (max(nodes) + 63) // 64
+        call = lambda: pkv.paged_tree_attention(c.pool, q, i32(ip), pack(bits, words).cuda(), c.tables.cuda(), i32(lens), d ** -0.5)  # noqa: E731
+        got = call().cpu()
+        assert nan.any() and not nan.all()
+        assert torch.equal(~torch.isfinite(got), nan)
+        ref, bound = plain(c, q, ip, bits, lens, d ** -0.5)
+        check(torch.where(nan, 0, got), torch.where(nan, 0, ref), bound)
+        # and keys: NaN ones of nodes that no row sees change nothing
+        unseen = [(b, n - 1) for b, n in enumerate(nodes) if n > 1]
+        for b, j in unseen:
+            for r in range(ip[b], ip[b + 1]):
+                bits[r] &= ~(1 << j)
+        want = call()
+        for b, j in unseen:
+            pos = lens[b] - nodes[b] + j
+            c.k.view(torch.uint8)[int(c.tables[b, pos // BS]), :, pos % BS] = torch.full((d,), math.nan).to(c.k.dtype).view(torch.uint8)
+        c.upload()
+        assert torch.equal(call().nan_to_num(7, 8, 9), want.nan_to_num(7, 8, 9))
+        assert c.pool.get_error() == 0
