@@ -49,7 +49,7 @@
 //     their product: a weight of 0 does not cancel what is not finite.  Nodes that
 //     a row does not see may hold anything, too: what is not finite in the nodes'
 //     value rows becomes 0 there, and is added to the results of the rows that see
-//     it, when the slice is done (16 trees of 26 nodes on 1024..2048 tokens: 38 us
+//     it, when the slice is done (16 trees of 17..32 nodes on 1024..2048 tokens: 38 us
 //     without the look at the nodes' rows, 39 with it).
 // Every mbarrier wait is bounded; on a timeout the CTA records
 // PKV_DEVERR_TIMEOUT, every role stops, the MMA and copy pipes are drained
@@ -74,7 +74,7 @@ constexpr int kCopyWarp = 16, kMmaWarp = 17, kPrepWarp = 20;
 constexpr int kMaxWords = 16;
 constexpr int kMany = 4;                   // windows of 32 sequences whose lengths are read at a time
 // What a step costs in a unit of one tile (bound by HBM, or by the widening of its keys) and of two (by the products
-// and exponentials), and a unit besides its steps: about 1.4, 2 and 4 us.  (16 trees of 26 nodes on 1024..2048 tokens
+// and exponentials), and a unit besides its steps: about 1.4, 2 and 4 us.  (16 trees of 17..32 nodes on 1024..2048 tokens
 // and 64 of 1..60 on E4M3: 38.1 and 131 us so, 38.8 and 140 with 3, 4 and 6, 38.9 and 128..135 with units at half more.)
 constexpr int kCostOne = 2, kCostTwo = 3, kCostUnit = 6;
 constexpr int kMinShare = kCostUnit + 2 * kCostOne;  // of a slice
@@ -95,9 +95,10 @@ constexpr uint32_t kColO = 256;
 constexpr uint32_t kHalf = 128 * 128;      // bytes of a 64-column range of a 128-row tile
 constexpr float kSlack = 8.0f;             // log2 of the largest weight before the reference maximum is raised
 
-// The unit that begins in a CTA's slice and goes on in the next ones, for the merge.  more < 0: none.
+// The unit that a CTA's slice has a part of and that goes on in the next one, for the merge.  more < 0: none.
 struct Part {
-    int row0, r0, R, g, more;  // first token row, first local row, local rows, KV head, parts that follow
+    int row0, r0, R, g;  // first token row, first local row, local rows, KV head
+    int more, back;      // parts that follow the first; which of them this CTA's is
 };
 
 struct Args {
@@ -223,7 +224,7 @@ struct Piece {
     int b, g, r0;      // sequence, KV head, first local row
     int row0, T, R, C; // first token row, nodes, local rows (nodes x heads), cache length
     int S, s0, n;      // the unit's steps; this piece's
-    int more;          // pieces of the unit in the slices that follow
+    int more, back;    // pieces of the unit in the slices that follow, and in those before
     int next;          // where the stream goes on
     int blocks;        // of the sequence
     // the first of the piece's steps that has nodes, and the rows of a step's tile that are nodes
@@ -331,6 +332,7 @@ __device__ __forceinline__ bool find_piece(Walker &w, const Args &a, int f, int 
         // the last step's beginning, behind this slice's end
         const int left = (p.S == 1 ? 0 : kCostUnit + cost * (p.S - 1)) - e;
         p.more = left < 0 ? 0 : left / share + 1;
+        p.back = f / share - (f - x) / share;
         p.blocks = (p.C + kBlockSize - 1) / kBlockSize;
         if (p.n > 0) return true;
         f = p.next;
@@ -525,7 +527,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
             const uint32_t go = elect_one();  // one lane issues all copies, the warp running as one
             int u = 0, n = 0;                 // tiles of the ring, pieces
             bool ok = true;
-            Part begun = {0, 0, 0, 0, -1};
+            Part cut = {0, 0, 0, 0, -1, 0};
             for (int f = f0;;) {
                 if (*abort_flag) break;
                 Piece p;
@@ -557,7 +559,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                     return true;
                 };
                 static_assert(NS >= 2, "");
-                if (p.s0 == 0 && !p.whole()) begun = {p.row0, p.r0, p.R, p.g, p.more};
+                if (p.more > 0) cut = {p.row0, p.r0, p.R, p.g, p.back + p.more, p.back};
                 const int32_t *trow = a.block_tables + (int64_t)p.b * a.W;
                 // lane k < 8: the entry rows of block k of a step, or rows past the pool (zero filled)
                 auto rows_of = [&](int s) -> int {
@@ -601,7 +603,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                 if (!ok) break;
                 ++n;
             }
-            if (lane == 0) a.parts[blockIdx.x] = begun;
+            if (lane == 0) a.parts[blockIdx.x] = cut;
             // copies still in flight (after an abort) land before the CTA exits
             for (int i = max(0, u - NS); i < u; ++i)
                 mbar_wait_bounded(&bar[(F8 ? L::RAW : L::FULL) + i % NS], (i / NS) & 1);
@@ -1040,72 +1042,110 @@ struct MergeArgs {
     __nv_bfloat16 *out;
 };
 
-constexpr int kMergeWarps = 8;
+constexpr int kMergeWarps = 8, kMergeBlocks = 8;  // of a slice
+static_assert(kUnitRows <= 4 * kMergeWarps * kMergeBlocks, "a warp takes four rows at most");
 
-// Block (c, y): rows 8 y .. of the unit that begins in slice c and goes on in the next ones; a warp a row.
-template <int D, int G>
-__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ MergeArgs a)
+// Rows [i0, i0 + N) of a unit, those below i1: 32 parts at a time, a lane holding one's (m, l) of each row, and of the O
+// 8 / N parts of all rows read at once.
+template <int D, int G, int N>
+__device__ __forceinline__ void join_rows(const MergeArgs &a, const Part &p, int first, int i0, int i1, int lane)
 {
     constexpr int PL = D / 32;  // channels of a lane
-    griddep_wait();
-    griddep_launch_dependents();
-    const int c = blockIdx.x, lane = threadIdx.x & 31;
-    const Part p = a.parts[c];
-    const int i = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);  // row of the unit
-    const int r = p.r0 + i;
-    if (p.more < 0 || i >= kUnitRows || r >= p.R) return;
-    auto at = [&](int k) -> int64_t { return (int64_t)(k == 0 ? 2 * c + 1 : 2 * (c + k)) * a.slot_rows + i; };
-    // 32 parts at a time: a lane holds one's (m, l), and all of them read eight parts of O at once
-    float o[PL] = {}, l = 0.0f, M = -INFINITY;
+    constexpr int U = 8 / N;
+    auto at = [&](int w, int k) -> int64_t { return (int64_t)(k == 0 ? 2 * first + 1 : 2 * (first + k)) * a.slot_rows + i0 + w; };
+    float o[N][PL] = {}, l[N] = {}, M[N];
+#pragma unroll
+    for (int w = 0; w < N; ++w) M[w] = -INFINITY;
     for (int k0 = 0; k0 <= p.more; k0 += 32) {
         const int n = min(32, p.more + 1 - k0);
-        const float2 y = lane < n ? a.ws_ml[at(k0 + lane)] : make_float2(-INFINITY, 0.0f);
-        constexpr int U = 8;
-        float z[U][PL];
+        float2 y[N];
+#pragma unroll
+        for (int w = 0; w < N; ++w) y[w] = lane < n && i0 + w < i1 ? a.ws_ml[at(w, k0 + lane)] : make_float2(-INFINITY, 0.0f);
+        float z[N][U][PL];
         auto load = [&](int k1) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (k1 + u >= n) continue;
-                const float *src = a.ws_o + at(k0 + k1 + u) * D + lane * PL;
-                if constexpr (PL == 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(src);
-                    z[u][0] = v.x; z[u][1] = v.y; z[u][2] = v.z; z[u][3] = v.w;
-                } else {
-                    const float2 v = *reinterpret_cast<const float2 *>(src);
-                    z[u][0] = v.x; z[u][1] = v.y;
+            for (int w = 0; w < N; ++w) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (k1 + u >= n || i0 + w >= i1) continue;
+                    const float *src = a.ws_o + at(w, k0 + k1 + u) * D + lane * PL;
+                    if constexpr (PL == 4) {
+                        const float4 v = *reinterpret_cast<const float4 *>(src);
+                        z[w][u][0] = v.x; z[w][u][1] = v.y; z[w][u][2] = v.z; z[w][u][3] = v.w;
+                    } else {
+                        const float2 v = *reinterpret_cast<const float2 *>(src);
+                        z[w][u][0] = v.x; z[w][u][1] = v.y;
+                    }
                 }
             }
         };
         load(0);  // (does not wait for the statistics)
-        float top = y.x;
+        float f[N];
 #pragma unroll
-        for (int s = 16; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, s));
-        const float was = M;
-        M = fmaxf(M, top);
-        const float old = was == -INFINITY ? 0.0f : exp2f(was - M), f = y.x == -INFINITY ? 0.0f : exp2f(y.x - M);
-        float sum = y.y * f;
+        for (int w = 0; w < N; ++w) {
+            float top = y[w].x;
 #pragma unroll
-        for (int s = 16; s >= 1; s >>= 1) sum += __shfl_xor_sync(kFull, sum, s);
-        l = l * old + sum;
+            for (int s = 16; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, s));
+            const float was = M[w];
+            M[w] = fmaxf(was, top);
+            const float old = was == -INFINITY ? 0.0f : exp2f(was - M[w]);
+            f[w] = y[w].x == -INFINITY ? 0.0f : exp2f(y[w].x - M[w]);
+            float sum = y[w].y * f[w];
 #pragma unroll
-        for (int d = 0; d < PL; ++d) o[d] *= old;
+            for (int s = 16; s >= 1; s >>= 1) sum += __shfl_xor_sync(kFull, sum, s);
+            l[w] = l[w] * old + sum;
+#pragma unroll
+            for (int d = 0; d < PL; ++d) o[w][d] *= old;
+        }
         for (int k1 = 0; k1 < n; k1 += U) {
             if (k1) load(k1);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const float w = __shfl_sync(kFull, f, (k1 + u) & 31);
-                if (k1 + u >= n) continue;
+            for (int w = 0; w < N; ++w) {
 #pragma unroll
-                for (int d = 0; d < PL; ++d) o[d] = fmaf(z[u][d], w, o[d]);
+                for (int u = 0; u < U; ++u) {
+                    const float x = __shfl_sync(kFull, f[w], (k1 + u) & 31);
+                    if (k1 + u >= n || i0 + w >= i1) continue;
+#pragma unroll
+                    for (int d = 0; d < PL; ++d) o[w][d] = fmaf(z[w][u][d], x, o[w][d]);
+                }
             }
         }
     }
-    const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
-    __nv_bfloat16 *dst = a.out + (((int64_t)p.row0 + r / G) * a.n_q + p.g * G + r % G) * D + lane * PL;
-    if constexpr (PL == 4)
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-    else
-        *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(o[0] * inv, o[1] * inv);
+#pragma unroll
+    for (int w = 0; w < N; ++w) {
+        if (i0 + w >= i1) continue;
+        const float inv = l[w] > 0.0f ? 1.0f / l[w] : l[w] == 0.0f ? 0.0f : l[w];
+        const int r = p.r0 + i0 + w;
+        __nv_bfloat16 *dst = a.out + (((int64_t)p.row0 + r / G) * a.n_q + p.g * G + r % G) * D + lane * PL;
+        if constexpr (PL == 4)
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(o[w][0] * inv, o[w][1] * inv), pack_bf16x2(o[w][2] * inv, o[w][3] * inv));
+        else
+            *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(o[w][0] * inv, o[w][1] * inv);
+    }
+}
+
+// Blocks (c, ..) take a share of the rows of the unit that slice c has a part of and leaves to the next one: where it is
+// cut once, all rows, up to four a warp; where it is long, as many blocks as it has parts take few rows each.  (With a
+// block for eight rows of the unit that begins in its slice, 32 of a slice: 11.7 us cold for 16 trees of 17..32 nodes on
+// 1024..2048 tokens, 9.6 so; twice the blocks of half the rows: 8.4 cold, but a call took 1.5 us longer.)
+template <int D, int G>
+__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ MergeArgs a)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const Part p = a.parts[blockIdx.x];
+    if (p.more <= 0) return;
+    const int rows = min(kUnitRows, p.R - p.r0);
+    const int lo = rows * p.back / p.more, hi = rows * (p.back + 1) / p.more;
+    const int warps = gridDim.y * kMergeWarps, at = blockIdx.y * kMergeWarps + (threadIdx.x >> 5), first = blockIdx.x - p.back;
+    if (hi - lo <= warps) {
+        if (lo + at < hi) join_rows<D, G, 1>(a, p, first, lo + at, hi, lane);
+    } else if (hi - lo <= 2 * warps) {
+        if (lo + 2 * at < hi) join_rows<D, G, 2>(a, p, first, lo + 2 * at, hi, lane);
+    } else if (lo + 4 * at < hi) {
+        join_rows<D, G, 4>(a, p, first, lo + 4 * at, hi, lane);
+    }
 }
 
 // ------------------------------------------------------------- launch
@@ -1169,7 +1209,7 @@ pkv_status launch(pkv_pool *pool, const void *q, Args a, int ctas, cudaStream_t 
     m.n_q = a.n_q;
     m.out = a.out;
     LaunchScope ls(pool, kMerge, s);
-    cudaError_t e = launch_pdl(tree_merge_kernel<D, G>, dim3(ctas, (a.slot_rows + kMergeWarps - 1) / kMergeWarps),
+    cudaError_t e = launch_pdl(tree_merge_kernel<D, G>, dim3(ctas, std::min(kMergeBlocks, (a.slot_rows + kMergeWarps - 1) / kMergeWarps)),
                                dim3(kMergeWarps * 32), 0, s, m);
     ls.done();
     if (e != cudaSuccess) return cuda_fail(e, "paged_tree_attention merge launch");
