@@ -1125,9 +1125,9 @@ __device__ __forceinline__ void join_rows(const MergeArgs &a, const Part &p, int
 }
 
 // Blocks (c, ..) take a share of the rows of the unit that slice c has a part of and leaves to the next one: where it is
-// cut once, all rows, up to four a warp; where it is long, as many blocks as it has parts take few rows each.  (With a
-// block for eight rows of the unit that begins in its slice, 32 of a slice: 11.7 us cold for 16 trees of 17..32 nodes on
-// 1024..2048 tokens, 9.6 so; twice the blocks of half the rows: 8.4 cold, but a call took 1.5 us longer.)
+// cut once, all rows, up to four a warp; where it is long, as many blocks as it has parts take few rows each.  (One
+// sequence of 32768 tokens: 35.4 us a call so, 36.7 with 32 blocks for the rows of the unit that begins in a slice, 37.6
+// with 16 blocks here and two rows a warp, which spills.)
 template <int D, int G>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ MergeArgs a)
 {
