@@ -207,7 +207,7 @@ __device__ __forceinline__ Cand shfl_xor(const Cand &x, int o)
 constexpr int kHold = 8;                         // continuations of a thread, at a time
 constexpr int kMergeKeep = 1024;                 // kept between rounds
 constexpr int kMergeCap = kMergeKeep + kHold * kThreads / 4;
-constexpr int kFewLists = 16;                    // bisected by every continuation: 16 lists of 8 take 0.5 us, the bar 3 us
+constexpr int kFewLists = 16;                    // bisected by every continuation: 16 lists of 8 take 1.3 us, the bar 3 us
 
 struct MergeShared {
     Cand buf[kMergeCap];

@@ -555,8 +555,9 @@ pkv_status paged_diff_reserve_workspace(pkv_pool *pool, int32_t batch, int32_t n
  *   tree_mask  device uint64 [n_rows][mask_words], 8-byte aligned: bit j % 64
  *              of word j / 64 of a node's row is set where it sees node j.
  *   mask_words 1 .. 16 (up to 1024 nodes).
- *   out        device bf16 [n_rows][n_q][d_head], 32-byte aligned; rows of no
- *              sequence, or of one that is skipped, stay as they were.
+ *   out        device bf16 [n_rows][n_q][d_head], 32-byte aligned, q itself or
+ *              apart from it; rows of no sequence, or of one that is skipped,
+ *              stay as they were.
  * A sequence whose rows run backwards or leave [0, n_rows), with more nodes
  * than the masks have bits, more nodes than cached tokens, or a length past
  * its table is skipped and sets PKV_DEVERR_CTX_RANGE.  A block id outside the

@@ -384,3 +384,42 @@ def test_what_hidden_nodes_hold_does_not_matter(kv, d, lens, nodes):
         c.upload()
         assert torch.equal(call().nan_to_num(7, 8, 9), want.nan_to_num(7, 8, 9))
         assert c.pool.get_error() == 0
+
+
+@pytest.mark.gpu
+def test_the_result_may_replace_the_queries():
+    layer = Layer("bf16", 200, 0)
+    fill(layer, 15)
+    args = tree_args(layer, [40, 3, 64, 1], [3100, 70, 900, 16], 16)
+    want = pkv.paged_tree_attention(layer.pool, *args)
+    for _ in range(3):
+        q = args[0].clone()
+        assert pkv.paged_tree_attention(layer.pool, q, *args[1:], out=q) is q
+        assert torch.equal(q, want)
+    layer.pool.close()
+
+
+@pytest.mark.gpu
+def test_the_widest_selection():
+    """64 beams of 2^22 logits, 64 of their 2^28 continuations; more than that is refused."""
+    beams, vocab, k = 64, 1 << 22, 64
+    g = torch.Generator(device="cuda").manual_seed(17)
+    x = torch.empty(1, beams, vocab, device="cuda")
+    for j in range(beams):
+        x[0, j] = torch.randn(vocab, device="cuda", generator=g)
+    scores = -torch.rand(1, beams, device="cuda", generator=g)
+    with pkv.kv_pool_create(2, 16, 1, 64, pkv.BF16) as pool:
+        tokens, parents, best = pkv.paged_beam_select(pool, x, scores, k)
+        assert pool.get_error() == 0
+        for bad in (dict(logits=torch.zeros(1, 1, vocab + 1, device="cuda"), scores=scores[:, :1].contiguous(), k=1),
+                    dict(logits=x, scores=scores, k=65)):
+            with pytest.raises(pkv.PagedKVError):
+                pkv.paged_beam_select(pool, **bad)
+    lse = torch.stack([torch.logsumexp(x[0, j].double(), 0) for j in range(beams)])
+    top = torch.stack([x[0, j].topk(k).values.double() for j in range(beams)]) - lse[:, None] + scores[0].double()[:, None]
+    want = top.flatten().sort(descending=True).values[:k]
+    p, t = parents[0].long(), tokens[0].long()
+    mine = x[0, p, t].double() - lse[p] + scores[0, p].double()
+    # the sums of exponentials are within 2^-19 as in a row of one piece, and ranks by at most as much
+    assert ((mine - want).abs() <= 2.0 ** -18).all() and len({*zip(p.tolist(), t.tolist())}) == k
+    assert ((best[0].double() - mine).abs() <= 2.0 ** -19 + 2.0 ** -24 * mine.abs()).all()
