@@ -20,17 +20,18 @@
 //     whatever the lengths are, and one long sequence keeps all of them busy (64
 //     trees of 1..60 nodes on an E4M3 cache: 201 us with all steps weighed
 //     alike, 149 so).  A unit that a slice holds whole is finished by its CTA; of
-//     one that is cut each CTA leaves its part (reference maximum, sum, unnormalised O), which
-//     tree_merge_kernel joins.  A slice cuts at most two units, the one it
-//     starts inside of (partial slot 2 cta) and the one it ends inside of
-//     (2 cta + 1).
+//     one that is cut each CTA leaves its part (reference maximum, sum,
+//     unnormalised O), which tree_merge_kernel joins.  A slice cuts at most two
+//     units, the one it starts inside of (partial slot 2 cta) and the one it ends
+//     inside of (2 cta + 1).  Where units are small, or there is one per SM and
+//     they are about alike, none is cut (see kCostCut).
 //   * two streams of softmax, each with its own scores and accumulator in
 //     tensor memory and its own eight warps: while one forms weights, the tensor
 //     cores work for the other.  A unit of two tiles gives each stream a tile,
 //     and both use every key and value tile; in a unit of one tile the streams
 //     take alternate steps (the second one the first, as it is the first that
 //     joins the two by log-sum-exp at the end).
-//   * a softmax warp has 16 rows, all 128 keys of a step, read from tensor
+//   * a softmax warp has 16 rows, all 64 keys of a turn, read from tensor
 //     memory as a matrix product's result is laid out: four threads a row, which
 //     two shuffles reduce.  (A thread per row, four warps a stream, left every
 //     scheduler with two warps and their dependent chains.)
@@ -80,6 +81,17 @@ constexpr int kCostOne = 2, kCostTwo = 3, kCostUnit = 6;
 constexpr int kMinShare = kCostUnit + 2 * kCostOne;  // of a slice
 // (between two steps' beginnings: no slice inside a unit is without one)
 static_assert(kMinShare >= kCostUnit + kCostTwo, "");
+// Units are not cut where that would gain less than it costs (a second beginning and end, the parts, the join).  With 16
+// nodes on four heads, 8 KV heads, us a call, cut and whole:
+//   * no more units than CTAs, one each: where the costliest is above the even share by kCostCut at most.  128 units on
+//     1024, 2048, 4096 tokens: 28.3 / 19.7, 37.7 / 32.2, 53.7 / 52.2; 64 units on 1536 (18 above): 23.2 / 23.5; on 2048
+//     (23 above): 25.4 / 28.0; 8 on 1024 (21 above): 15.9 / 17.5.
+//   * more units than CTAs, to the slice in which they begin: where none costs more than kCostSmall.  512 units on 1024,
+//     1536, 2048 tokens (22, 30, 38): 73 / 65, 85.7 / 84.2, 99.9 / 102.9; 1024 units on 1536: 152 / 156.
+constexpr int kCostCut = 18, kCostSmall = 30;
+// And where tables have no more steps than this, so that the join need not be launched: with tables of 1024 tokens 8, 32,
+// 512 units take 15.9 / 15.9, 20.0 / 16.3, 73 / 66; with 1536, 15.2 / 20.1, 20.5 / 20.1, 86 / 86.
+constexpr int kWholeSteps = 8;
 template <bool F8>
 struct Warps {
     static constexpr int kWarps = F8 ? 24 : 20, kThreads = kWarps * 32;
@@ -114,6 +126,7 @@ struct Args {
     int oob_row;          // a row index past the end of the pool's entry rows (zero-filled box)
     float qscale;         // scale * log2(e)
     const float *scales;  // FP8 pools: [2 * n_kv] fp32, K scales then V scales
+    bool whole;           // no unit is cut, whatever they cost
     int slot_rows;        // rows of a partial slot
     Part *parts;          // [CTAs]
     float2 *ws_ml;        // [2 CTAs][slot_rows] (reference maximum in log2 units, sum)
@@ -147,7 +160,7 @@ struct Layout {
     static constexpr uint32_t kAbort = kTmemSlot + 4;
     static constexpr uint32_t kOdd = kAbort + 4;    // a value of a node was not finite
     static constexpr uint32_t kSlice = kOdd + 4;    // where the CTA's slice begins
-    static constexpr uint32_t kEnd = kSlice + 20;
+    static constexpr uint32_t kEnd = kSlice + 28;
     static constexpr size_t bytes = 1024 + kEnd;
     static_assert(bytes <= 232448, "shared memory beyond the 227 KiB a CTA may use");
 };
@@ -240,6 +253,9 @@ struct Walker {
     int wb = 0, wbase = 0, tot = 0;  // first sequence of the window, costs before it, its costs
     int incl = 0;                    // costs up to and with this lane's sequence
     int row0 = 0, T = 0, C = 0;      // this lane's sequence
+    int units = 0, most = 0;         // of the lane's sequences so far: units, and the cost of the costliest
+    bool whole = false;              // units belong to the slice in which they begin
+    bool index = false;              // and count one each
 };
 
 __device__ __forceinline__ int inclusive_sum(int x, int lane)
@@ -255,14 +271,16 @@ __device__ __forceinline__ int inclusive_sum(int x, int lane)
 // The units of a sequence and KV head with R rows and S steps: all but the last have two tiles.  In a unit of step cost
 // w, step 0 begins at 0 and step s at kCostUnit + w s.
 struct Units {
-    int n, full, last;  // units, cost of all but the last, step cost of the last
-    int all;            // cost of the whole
-    __device__ __forceinline__ Units(int R, int S)
+    int n, full, last;  // units, size of all but the last in the stream, of the last
+    int step;           // step cost of the last
+    int all;            // size of the whole
+    __device__ __forceinline__ Units(int R, int S, bool index)
     {
         n = (R + kUnitRows - 1) / kUnitRows;
-        full = S * kCostTwo + kCostUnit;
-        last = R - (n - 1) * kUnitRows > kRows ? kCostTwo : kCostOne;
-        all = (n - 1) * full + S * last + kCostUnit;
+        step = R - (n - 1) * kUnitRows > kRows ? kCostTwo : kCostOne;
+        full = index ? 1 : S * kCostTwo + kCostUnit;
+        last = index ? 1 : S * step + kCostUnit;
+        all = (n - 1) * full + last;
     }
     // steps that begin before x
     static __device__ __forceinline__ int begun(int x, int w)
@@ -271,7 +289,7 @@ struct Units {
     }
 };
 
-// Sequence b's nodes and length; its cost, none where it does not fit.
+// Sequence b's nodes and length; its size in the stream, none where it does not fit.
 template <int G>
 __device__ __forceinline__ int sequence(const Args &a, int b, Walker &w, bool flag)
 {
@@ -286,7 +304,10 @@ __device__ __forceinline__ int sequence(const Args &a, int b, Walker &w, bool fl
     w.row0 = lo;
     w.T = hi - lo;
     w.C = C;
-    return Units(w.T * G, (C + kKeys - 1) / kKeys).all * a.n_kv;
+    const Units u(w.T * G, (C + kKeys - 1) / kKeys, w.index);
+    w.units += u.n * a.n_kv;
+    w.most = max(w.most, u.n > 1 ? u.full : u.last);
+    return u.all * a.n_kv;
 }
 
 template <int G>
@@ -318,21 +339,32 @@ __device__ __forceinline__ bool find_piece(Walker &w, const Args &a, int f, int 
         p.C = __shfl_sync(kFull, w.C, l);
         p.S = (p.C + kKeys - 1) / kKeys;
         p.R = p.T * G;
-        const Units u(p.R, p.S);
+        const Units u(p.R, p.S, w.index);
         const int within = at - (__shfl_sync(kFull, w.incl, l) - u.all * a.n_kv);
         p.g = within / u.all;
         int x = within - p.g * u.all;  // in the KV head, then in the unit
-        const int unit = min(x / u.full, u.n - 1), cost = unit == u.n - 1 ? u.last : kCostTwo;
+        const int unit = min(x / u.full, u.n - 1);
         x -= unit * u.full;
         p.r0 = unit * kUnitRows;
-        const int size = p.S * cost + kCostUnit, e = min(size, x + (end - f));
-        p.s0 = Units::begun(x, cost);
-        p.n = (e == size ? p.S : Units::begun(e, cost)) - p.s0;
-        p.next = f + (e - x);
-        // the last step's beginning, behind this slice's end
-        const int left = (p.S == 1 ? 0 : kCostUnit + cost * (p.S - 1)) - e;
-        p.more = left < 0 ? 0 : left / share + 1;
-        p.back = f / share - (f - x) / share;
+        const int size = unit == u.n - 1 ? u.last : u.full;
+        if (w.whole) {
+            if (x > 0) {  // the slice before has it
+                f += size - x;
+                continue;
+            }
+            p.s0 = p.more = p.back = 0;
+            p.n = p.S;
+            p.next = f + size;
+        } else {
+            const int cost = unit == u.n - 1 ? u.step : kCostTwo, e = min(size, x + (end - f));
+            p.s0 = Units::begun(x, cost);
+            p.n = (e == size ? p.S : Units::begun(e, cost)) - p.s0;
+            p.next = f + (e - x);
+            // the last step's beginning, behind this slice's end
+            const int left = (p.S == 1 ? 0 : kCostUnit + cost * (p.S - 1)) - e;
+            p.more = left < 0 ? 0 : left / share + 1;
+            p.back = f / share - (f - x) / share;
+        }
         p.blocks = (p.C + kBlockSize - 1) / kBlockSize;
         if (p.n > 0) return true;
         f = p.next;
@@ -394,7 +426,7 @@ __device__ __forceinline__ void add_odd(const Args &a, const Piece &p, int t0, f
 
 // Where a CTA's slice begins and ends, and in which window of 32 sequences.
 struct Slice {
-    int f0, f1, share, wb, wbase;
+    int f0, f1, share, wb, wbase, whole, index;
 };
 
 // The same for all rows that a softmax warp (w8 of stream x) has stored.
@@ -404,6 +436,8 @@ __device__ __noinline__ void add_odd_rows(const Args &a, const Slice &from, int 
     Walker wk;
     wk.wb = from.wb;
     wk.wbase = from.wbase;
+    wk.whole = from.whole;
+    wk.index = from.index;
     load_window<G>(wk, a, lane, false);
     Piece p;
     for (int f = from.f0; find_piece<G>(wk, a, f, from.f1, from.share, p, lane); f = p.next) {
@@ -495,21 +529,33 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
             Walker wk;
             int total = 0, many0 = 0, many1 = 0, f0, f1, share;
             static_assert(kMaxBatch <= 64 * 32 * kMany, "");
-            if (a.batch <= 32) {
-                load_window<G>(wk, a, lane, blockIdx.x == 0);
-                total = wk.tot;
-            } else {
+            auto scan = [&](bool flag) {
+                total = 0;
+                if (a.batch <= 32) {
+                    load_window<G>(wk, a, lane, flag);
+                    total = wk.tot;
+                    return;
+                }
                 for (int b = 0; b < a.batch; b += 32 * kMany) {
                     int x = 0;
 #pragma unroll
-                    for (int i = 0; i < kMany; ++i) x += sequence<G>(a, b + 32 * i + lane, wk, blockIdx.x == 0);
+                    for (int i = 0; i < kMany; ++i) x += sequence<G>(a, b + 32 * i + lane, wk, flag);
                     x = __reduce_add_sync(kFull, x);
                     total += x;
                     const int i = b / (32 * kMany);  // lane i % 32 keeps it
                     if (lane == i % 32) (i < 32 ? many0 : many1) = x;
                 }
+            };
+            scan(blockIdx.x == 0);
+            share = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+            const int units = __reduce_add_sync(kFull, wk.units), most = __reduce_max_sync(kFull, wk.most);
+            wk.index = units <= (int)gridDim.x && (a.whole || most <= share + kCostCut);
+            wk.whole = wk.index || a.whole || (units > (int)gridDim.x && most <= kCostSmall);
+            share = max(share, kMinShare);
+            if (wk.index) {
+                scan(false);
+                share = 1;
             }
-            share = max(kMinShare, (total + (int)gridDim.x - 1) / (int)gridDim.x);
             f0 = min((int64_t)total, (int64_t)blockIdx.x * share);
             f1 = min((int64_t)total, (int64_t)f0 + share);
             if (a.batch > 32) {
@@ -522,7 +568,7 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                 wk.wbase = __shfl_sync(kFull, j < 32 ? incl0 - many0 : incl1 - many1, j % 32);
                 load_window<G>(wk, a, lane, false);
             }
-            if (lane == 0) *reinterpret_cast<Slice *>(sm + L::kSlice) = {f0, f1, share, wk.wb, wk.wbase};
+            if (lane == 0) *reinterpret_cast<Slice *>(sm + L::kSlice) = {f0, f1, share, wk.wb, wk.wbase, wk.whole, wk.index};
             const uint64_t policy = l2_policy_evict_normal();
             const uint32_t go = elect_one();  // one lane issues all copies, the warp running as one
             int u = 0, n = 0;                 // tiles of the ring, pieces
@@ -1201,6 +1247,7 @@ pkv_status launch(pkv_pool *pool, const void *q, Args a, int ctas, cudaStream_t 
         ls.done();
         if (e != cudaSuccess) return cuda_fail(e, "paged_tree_attention launch");
     }
+    if (a.whole) return PKV_OK;
     MergeArgs m;
     m.parts = a.parts;
     m.ws_ml = a.ws_ml;
@@ -1296,6 +1343,7 @@ extern "C" pkv_status paged_tree_attention(pkv_pool *pool, const void *q, int64_
     // (0 as 1e-30: the same scores to fp32, but -inf for hidden ones stays -inf)
     a.qscale = scale == 0.0f ? 1e-30f : scale * kLog2e;
     a.scales = pool->scales;
+    a.whole = steps <= kWholeSteps;
     a.slot_rows = sp.slot_rows;
     uint8_t *ws = static_cast<uint8_t *>(pool->ws);
     a.parts = reinterpret_cast<Part *>(ws);

@@ -571,7 +571,7 @@ pkv_status paged_diff_reserve_workspace(pkv_pool *pool, int32_t batch, int32_t n
  * as f16: |q| must stay in f16's range), and out once, to bf16.
  * bf16 and FP8 pools.  Two launches on the pool's workspace: equal slices of
  * the (sequence, KV head, step of 128 keys) stream on the tcgen05 tensor cores,
- * then a join of what was cut.  Results of a call do not depend on timing, but
+ * then a join of what was cut (tables of up to 64 blocks: the first alone).  Results of a call do not depend on timing, but
  * may differ in rounding between calls of different batches.  Other arguments,
  * group sizes and limits as paged_prefill_attention.
  * Errors: EINVAL (also a workspace that would have to grow while `stream` is

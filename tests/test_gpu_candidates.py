@@ -340,7 +340,7 @@ def test_rows_in_one_piece_are_summed_as_exactly():
 @pytest.mark.gpu
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("lens,nodes", [([200, 90], [40, 10]), ([16, 300], [16, 129]), ([3000, 50], [100, 1])])
+@pytest.mark.parametrize("lens,nodes", [([200, 90], [40, 10]), ([16, 300], [16, 129]), ([3000, 50], [100, 1]), ([9000, 1200], [90, 64])])
 def test_what_hidden_nodes_hold_does_not_matter(kv, d, lens, nodes):
     """Keys and values of some nodes that are not finite (padding behind a tree, a branch that was not computed): rows
     that see a node have its channels' NaN and infinities, all else is as with zeros there."""
@@ -423,3 +423,56 @@ def test_the_widest_selection():
     # the sums of exponentials are within 2^-19 as in a row of one piece, and ranks by at most as much
     assert ((mine - want).abs() <= 2.0 ** -18).all() and len({*zip(p.tolist(), t.tolist())}) == k
     assert ((best[0].double() - mine).abs() <= 2.0 ** -19 + 2.0 ** -24 * mine.abs()).all()
+
+
+def spread(lo, hi, n, seed):
+    rng = random.Random(seed)
+    return [rng.randint(lo, hi) for _ in range(n)]
+
+
+# lengths, nodes, KV heads: one unit a CTA (few and many sequences); small units, several a CTA; long ones among short
+# ones; few long ones; units of one tile and of two
+SLICES = [([1000, 1100, 900], [20, 60, 33], 2), (spread(800, 1300, 60, 1), spread(1, 40, 60, 2), 2),
+          (spread(20, 1000, 100, 3), spread(1, 20, 100, 4), 2), (spread(60, 300, 100, 5) + [6000], spread(1, 30, 101, 6), 2),
+          ([9000, 2000], [10, 64], 1), (spread(100, 1024, 41, 7), spread(33, 64, 41, 8), 4)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("extra", [0, 70])
+@pytest.mark.parametrize("case", range(len(SLICES)))
+def test_units_that_are_cut_and_that_are_not(kv, extra, case):
+    """The same trees with tables as wide as they need, and wider: what is cut depends on that, and on their lengths."""
+    lens, nodes, n_kv = SLICES[case]
+    with Cache(kv, n_kv, 64 if case % 2 else 128, lens, seed=case, table_extra=extra) as c:
+        rng = random.Random(case)
+        bits = [m for n in nodes for m in tree_bits(parents_of(n, rng))]
+        ip = np.cumsum([0] + nodes)
+        q = torch.randn(sum(nodes), 4 * n_kv, c.d, generator=torch.Generator().manual_seed(case)).to(torch.bfloat16).cuda()
+        got = pkv.paged_tree_attention(c.pool, q, i32(ip), pack(bits, 1).cuda(), c.tables.cuda(), i32(lens), c.d ** -0.5)
+        assert c.pool.get_error() == 0
+        check(got, *plain(c, q, ip, bits, lens, c.d ** -0.5))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_a_graph_whose_lengths_change_what_is_cut(kv):
+    lens, nodes = [4000, 500, 3900, 300], [20, 5, 40, 64]
+    with Cache(kv, 2, 128, lens, seed=18, table_extra=0) as c:
+        rng = random.Random(18)
+        bits = [m for n in nodes for m in tree_bits(parents_of(n, rng))]
+        ip = np.cumsum([0] + nodes)
+        q = torch.randn(sum(nodes), 8, 128, generator=torch.Generator().manual_seed(18)).to(torch.bfloat16).cuda()
+        args = [q, i32(ip), pack(bits, 1).cuda(), c.tables.cuda(), i32(lens), 128 ** -0.5]
+        c.pool.reserve_tree_workspace(sum(nodes), 8)
+        out = torch.zeros_like(q)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            pkv.paged_tree_attention(c.pool, *args, out=out)
+        for now in ([4000, 500, 3900, 300], [400, 500, 390, 300], [20, 5, 40, 64], [4000, 5, 40, 64], [1000, 500, 900, 300]):
+            args[4].copy_(i32(now))
+            out.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            check(out, *plain(c, q, ip, bits, now, 128 ** -0.5))
