@@ -1088,8 +1088,7 @@ struct MergeArgs {
     __nv_bfloat16 *out;
 };
 
-constexpr int kMergeWarps = 8, kMergeBlocks = 8;  // of a slice
-static_assert(kUnitRows <= 4 * kMergeWarps * kMergeBlocks, "a warp takes four rows at most");
+constexpr int kMergeWarps = 8, kMergeBlocks = 4;  // of a slice
 
 // Rows [i0, i0 + N) of a unit, those below i1: 32 parts at a time, a lane holding one's (m, l) of each row, and of the O
 // 8 / N parts of all rows read at once.
@@ -1171,9 +1170,9 @@ __device__ __forceinline__ void join_rows(const MergeArgs &a, const Part &p, int
 }
 
 // Blocks (c, ..) take a share of the rows of the unit that slice c has a part of and leaves to the next one: where it is
-// cut once, all rows, up to four a warp; where it is long, as many blocks as it has parts take few rows each.  (One
-// sequence of 32768 tokens: 35.4 us a call so, 36.7 with 32 blocks for the rows of the unit that begins in a slice, 37.6
-// with 16 blocks here and two rows a warp, which spills.)
+// cut once, all rows, up to four a warp at a time; where it is long, as many blocks as it has parts take few rows each.
+// (Four blocks a slice, eight, two: one sequence of 32768 tokens 35.5, 36.1, 35.6 us a call, 64 trees on an E4M3 cache
+// 132.3, 134.4, 134.3.  The first with 32 blocks for the rows of the unit that begins in a slice: 36.7.)
 template <int D, int G>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ MergeArgs a)
 {
@@ -1189,8 +1188,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __gr
         if (lo + at < hi) join_rows<D, G, 1>(a, p, first, lo + at, hi, lane);
     } else if (hi - lo <= 2 * warps) {
         if (lo + 2 * at < hi) join_rows<D, G, 2>(a, p, first, lo + 2 * at, hi, lane);
-    } else if (lo + 4 * at < hi) {
-        join_rows<D, G, 4>(a, p, first, lo + 4 * at, hi, lane);
+    } else {
+        for (int i = lo + 4 * at; i < hi; i += 4 * warps) join_rows<D, G, 4>(a, p, first, i, hi, lane);
     }
 }
 
