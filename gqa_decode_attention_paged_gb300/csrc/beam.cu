@@ -26,7 +26,10 @@
 // logits, reduced to 4 k groups or more, give a bar: the k-th greatest group
 // maximum, which at least k logits reach.  The warps then go through the rest
 // each for itself, and note the vectors that have a logit above the bar: about
-// k (n / n_1 - 1) where the logits come in any order.  At the end the logits of
+// 1.15 k (n / n_1 - 1) where the logits come in any order (n_1: those that the
+// bar is from).  Before that comes near what can be noted, the noted logits are
+// taken, and give the next bar (16 searches x 16 beams x 128256 in fp32, k = 24,
+// 32, 64: 129, 134, 68..185 us without, 49, 49, 69 so).  At the end the logits of
 // the noted vectors are taken out of them.  Where they rise along the row, or
 // many equal the bar, the notes or what is in them can be too many; the piece is
 // then read again, and every part raises the bar first: what reaches it belongs
@@ -61,6 +64,9 @@ constexpr int kMaxK = 64, kMaxBeams = 64;
 constexpr int kPartKeys = 2048;                  // of a part, that reach its bar, at most
 constexpr int kCap = 2304;                       // keys the buffer holds: those, k kept ones, some more
 constexpr int kNotes = 1280;                     // vectors that can be noted
+// The bar is raised after 1 + kRaise / k parts, then whenever there were as many times the parts before: about 1.15 kRaise
+// are noted until then, give or take 1 / sqrt(k) of it, as the bar is the k-th of a sample.
+constexpr int kRaise = 512;
 
 // How rows are cut: piece i of a row has parts [first(i), first(i + 1)).
 struct Cut {
@@ -207,7 +213,7 @@ __device__ __forceinline__ Cand shfl_xor(const Cand &x, int o)
 constexpr int kHold = 8;                         // continuations of a thread, at a time
 constexpr int kMergeKeep = 1024;                 // kept between rounds
 constexpr int kMergeCap = kMergeKeep + kHold * kThreads / 4;
-constexpr int kFewLists = 16;                    // bisected by every continuation: 16 lists of 8 take 1.3 us, the bar 3 us
+constexpr int kFewLists = 8;                     // bisected by every continuation: 4 lists of 8 take 11.6 us a call, with a bar 12.7; 16: 13.7, 11.5
 
 struct MergeShared {
     Cand buf[kMergeCap];
@@ -596,14 +602,34 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) beam_select_kernel(con
     fetch(0, v);
     float top = greatest(v, tops);
     raise_bar(sh, key_at(v, 0, top), k, p);
-    const uint64_t bar = sh.bar;
-    const float high = bar ? logit_of(bar) : -INFINITY;
+    uint64_t bar = sh.bar;
+    float high = bar ? logit_of(bar) : -INFINITY;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
         if (tops[i] > -INFINITY && tops[i] >= high) note(0, i);
     sum.add<T>(v, top);
+    auto read = [&](int i0) -> uint4 { return rw.elements(i0 / N, [&](int u) { return ldg_nc_v4(rw.at(u)); }); };
     // ---- the rest of the piece, every warp for itself ----
+    int raise = 1 + kRaise / k;
     for (int q = 1; q < parts; ++q) {
+        if (q == raise) {  // the notes taken so far give a higher bar
+            raise = q + q * (kRaise / k);
+            __syncthreads();
+            const int notes = sh.notes;
+            if (notes <= kNotes) {
+                for (int i = tid; i < notes; i += kThreads) add_keys(read(sh.note[i]), sh.note[i], bar);
+                __syncthreads();
+                const int have = sh.n;
+                __syncthreads();
+                if (have <= kCap) {  // (else the piece is read again, below)
+                    thin_out(sh, have, k, p, kMaxK);
+                    if (tid == 0) sh.notes = 0;
+                    __syncthreads();
+                    bar = sh.bar;
+                    high = bar ? logit_of(bar) : -INFINITY;
+                }
+            }
+        }
         fetch(q, v);
         top = greatest(v, tops);
         if (top > high) {  // (an equal one has a greater index than the bar's)
@@ -630,7 +656,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) beam_select_kernel(con
     for (int o = 16; o >= 1; o >>= 1) f += __shfl_xor_sync(kFull, f, o);
     if (lane == 0) sh.sums[warp] = f;
     const int notes = sh.notes;
-    auto read = [&](int i0) -> uint4 { return rw.elements(i0 / N, [&](int u) { return ldg_nc_v4(rw.at(u)); }); };
     if (notes <= kNotes)
         for (int i = tid; i < notes; i += kThreads) add_keys(read(sh.note[i]), sh.note[i], bar);
     __syncthreads();
@@ -698,14 +723,16 @@ static_assert(kBlocksPerSm * (sizeof(Shared) + 1024) <= 232448, "fewer blocks wo
 static_assert(sizeof(MergeShared) <= sizeof(Shared), "");
 
 // Pieces of a row: as many as all blocks that run at once have room for, of two parts each at least (the bar comes
-// from the first).
+// from the first).  Shorter rows are not cut: 4 and 8 beams x 32000 in bf16, four parts, take 11.6 and 14.3 us whole,
+// 12.3 and 16.2 in two; sixteen parts (128256), where the rows are few, 12.7 and 16.2 in eight, 16.2 and 16.0 in four.
+constexpr int kCutParts = 6;
 Cut cut_of(const pkv_pool *pool, int64_t rows, int vocab, int elem)
 {
     const int part = kPartVecs * (16 / elem);
     Cut c;
     c.parts = (vocab + part - 1) / part;
     const int64_t room = (int64_t)kBlocksPerSm * pool->num_sms / std::max<int64_t>(1, rows);
-    c.pieces = (int)std::max<int64_t>(1, std::min<int64_t>(room, c.parts / 2));
+    c.pieces = c.parts < kCutParts ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(room, c.parts / 2));
     return c;
 }
 

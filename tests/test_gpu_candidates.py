@@ -476,3 +476,26 @@ def test_a_graph_whose_lengths_change_what_is_cut(kv):
             graph.replay()
             torch.cuda.synchronize()
             check(out, *plain(c, q, ip, bits, now, 128 ** -0.5))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,vocab", [(torch.float32, 50001), (torch.bfloat16, 100003)])
+@pytest.mark.parametrize("kind", ["random", "rising", "late", "levels", "half"])
+@pytest.mark.parametrize("k", [20, 64])
+def test_selection_of_rows_in_one_piece(dtype, vocab, kind, k):
+    """More rows than blocks run at once, each read by one block, in more parts than its first bar is good for."""
+    S, beams = 115, 4
+    g = torch.Generator().manual_seed(k)
+    x = torch.randn(S, beams, vocab, generator=g)
+    at = torch.arange(vocab) / vocab
+    if kind == "rising":  # every part is above the one before
+        x = x * 0.01 + 8 * at
+    elif kind == "late":  # the best are at the end
+        x = x + (at > 0.9) * 4.0
+    elif kind == "levels":  # many equal ones
+        x = (x * 2).round() / 2
+    elif kind == "half":  # rising, behind where the second bar is from
+        x = x * 0.1 + (at > 0.75) * (at - 0.75) * 20
+    scores = -torch.rand(S, beams, generator=g).cuda()
+    with pkv.kv_pool_create(2, 16, 1, 64, pkv.BF16) as pool:
+        check_selection(pool, x.to(dtype).cuda(), scores, k)
