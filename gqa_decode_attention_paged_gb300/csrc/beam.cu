@@ -765,11 +765,6 @@ pkv_status check_beam(const pkv_pool *pool, const char *who, int batch, int beam
     return PKV_OK;
 }
 
-bool overlap(const void *x, size_t xn, const void *y, size_t yn)
-{
-    return (uintptr_t)x < (uintptr_t)y + yn && (uintptr_t)y < (uintptr_t)x + xn;
-}
-
 }  // namespace
 }  // namespace pkv
 

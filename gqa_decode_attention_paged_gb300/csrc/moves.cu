@@ -210,11 +210,6 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const __grid_con
             : pool->dtype == PKV_FP8_E4M3 ? launch_pdl(kern<64, PKV_FP8_E4M3>, grid, dim3(kThreads), 0, s, a)  \
                                           : launch_pdl(kern<64, PKV_INT4>, grid, dim3(kThreads), 0, s, a)))
 
-bool overlap(const void *x, size_t xn, const void *y, size_t yn)
-{
-    return (uintptr_t)x < (uintptr_t)y + yn && (uintptr_t)y < (uintptr_t)x + xn;
-}
-
 }  // namespace
 }  // namespace pkv
 

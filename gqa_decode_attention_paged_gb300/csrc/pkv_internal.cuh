@@ -181,6 +181,12 @@ pkv_status check_step_args(const pkv_pool *pool, const char *who, int n_q, int m
 // current device, where the pool's memory is not.
 pkv_status check_pool_device(const pkv_pool *pool, const char *who);
 
+// Whether xn bytes at x and yn bytes at y have any in common.
+inline bool overlap(const void *x, size_t xn, const void *y, size_t yn)
+{
+    return (uintptr_t)x < (uintptr_t)y + yn && (uintptr_t)y < (uintptr_t)x + xn;
+}
+
 // ---------------------------------------------------------------------------
 // Device helpers (inline PTX)
 // ---------------------------------------------------------------------------

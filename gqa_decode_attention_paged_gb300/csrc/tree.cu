@@ -1313,6 +1313,13 @@ extern "C" pkv_status paged_tree_attention(pkv_pool *pool, const void *q, int64_
         return fail(PKV_EINVAL, "%s: q must be 16-byte and out 32-byte aligned", who);
     if (((uintptr_t)qo_indptr | (uintptr_t)block_tables | (uintptr_t)context_lens) & 3u || ((uintptr_t)tree_mask & 7u))
         return fail(PKV_EINVAL, "%s: indptr, tables and lengths must be 4-byte, masks 8-byte aligned", who);
+    // a CTA stores a unit's rows while others have yet to read theirs: only a unit's own queries may be written over
+    const size_t nout = (size_t)n_rows * n_q * pool->d_head * 2, nseq = (size_t)batch * 4;
+    if (out != q && overlap(out, nout, q, nout)) return fail(PKV_EINVAL, "%s: out overlaps q without being q itself", who);
+    if (overlap(out, nout, qo_indptr, nseq + 4) || overlap(out, nout, tree_mask, (size_t)n_rows * mask_words * 8) ||
+        overlap(out, nout, block_tables, nseq * max_blocks_per_seq) || overlap(out, nout, context_lens, nseq) ||
+        overlap(out, nout, pool->k, pool->alloc_bytes))
+        return fail(PKV_EINVAL, "%s: out overlaps an input", who);
     st = check_pool_device(pool, who);
     if (st != PKV_OK) return st;
     // the most units and steps that the call can have: sequences may share rows (their indptr is not checked here)

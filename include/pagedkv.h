@@ -556,8 +556,8 @@ pkv_status paged_diff_reserve_workspace(pkv_pool *pool, int32_t batch, int32_t n
  *              of word j / 64 of a node's row is set where it sees node j.
  *   mask_words 1 .. 16 (up to 1024 nodes).
  *   out        device bf16 [n_rows][n_q][d_head], 32-byte aligned, q itself or
- *              apart from it; rows of no sequence, or of one that is skipped,
- *              stay as they were.
+ *              apart from it, and apart from all other inputs and the pool; rows
+ *              of no sequence, or of one that is skipped, stay as they were.
  * A sequence whose rows run backwards or leave [0, n_rows), with more nodes
  * than the masks have bits, more nodes than cached tokens, or a length past
  * its table is skipped and sets PKV_DEVERR_CTX_RANGE.  A block id outside the
@@ -574,9 +574,9 @@ pkv_status paged_diff_reserve_workspace(pkv_pool *pool, int32_t batch, int32_t n
  * then a join of what was cut (tables of up to 64 blocks: the first alone).  Results of a call do not depend on timing, but
  * may differ in rounding between calls of different batches.  Other arguments,
  * group sizes and limits as paged_prefill_attention.
- * Errors: EINVAL (also a workspace that would have to grow while `stream` is
- * captured), EUNSUPPORTED (4-bit pools, group size, mask_words, too many query
- * rows), ENOMEM, ECUDA. */
+ * Errors: EINVAL (also an out that overlaps an input without being q, and a
+ * workspace that would have to grow while `stream` is captured), EUNSUPPORTED
+ * (4-bit pools, group size, mask_words, too many query rows), ENOMEM, ECUDA. */
 pkv_status paged_tree_attention(pkv_pool *pool, const void *q, int64_t n_rows, int32_t n_q, const int32_t *qo_indptr,
                                 const uint64_t *tree_mask, int32_t mask_words, const int32_t *block_tables,
                                 int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t batch, float scale,

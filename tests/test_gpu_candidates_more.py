@@ -1,0 +1,90 @@
+"""The edges of the calls for several candidates a sequence: memory that two arguments share, values that are not
+finite, weights and scales at the ends of their types' ranges, beams that begin with one prompt."""
+import math
+import random
+
+import numpy as np
+import pytest
+import torch
+
+import gqa_decode_attention_paged_gb300 as pkv
+from tree_ref import BS, Cache, check, pack, parents_of, plain, tree_bits
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32).cuda()
+
+
+def trees(c, nodes, G, seed):
+    """Queries and what follows them in a call, the masks as numbers and the rows' offsets."""
+    rng = random.Random(seed)
+    bits = [m for n in nodes for m in tree_bits(parents_of(n, rng))]
+    q = torch.randn(sum(nodes), G * c.n_kv, c.d, generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16).cuda()
+    ip = np.cumsum([0] + list(nodes))
+    words = (max(nodes) + 63) // 64
+    return q, [i32(ip), pack(bits, words).cuda(), c.tables.cuda(), i32(c.lens), c.d ** -0.5], bits, ip
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("lens,nodes,extra", [([3100, 200, 900, 16], [150, 3, 64, 1], 0), ([9000], [1000], 0), ([700, 900, 1000], [200, 70, 130], 0),
+                                              ([700, 900, 1000], [200, 70, 130], 70)])
+def test_several_units_of_a_head_may_write_over_their_queries(kv, lens, nodes, extra):
+    """Eight query heads on a KV head: 256 rows are 32 nodes.  Tables of up to 64 blocks, whose units are whole, and
+    wider ones, whose units are cut."""
+    with Cache(kv, 2, 128, lens, seed=31, table_extra=extra) as c:
+        q, args, bits, ip = trees(c, nodes, 8, 31)
+        want = pkv.paged_tree_attention(c.pool, q, *args)
+        check(want, *plain(c, q, ip, bits, lens, args[-1]))
+        for _ in range(3):
+            x = q.clone()
+            assert pkv.paged_tree_attention(c.pool, x, *args, out=x) is x
+            assert torch.equal(x, want)
+        assert c.pool.get_error() == 0
+
+
+@pytest.mark.gpu
+def test_results_that_share_memory_with_an_input_are_refused():
+    lens, nodes = [100, 40, 20], [6, 3, 1]
+    with Cache("bf16", 2, 64, lens, seed=32) as c:
+        q, args, bits, ip = trees(c, nodes, 4, 32)
+        want = pkv.paged_tree_attention(c.pool, q, *args)
+        n = q.numel()
+        room = torch.zeros(3 * n + 512, dtype=torch.bfloat16, device="cuda")  # (the result's place is [n, 2 n))
+        out = room[n:2 * n].view(q.shape)
+
+        def put(x, at):
+            """x's values at an offset (in bytes) of the room."""
+            size = x.numel() * x.element_size()
+            y = room.view(torch.uint8)[at:at + size].view(x.dtype).view(x.shape)
+            y.copy_(x)
+            return y
+
+        row = 8 * 64 * 2
+        lo, hi = 2 * n, 4 * n  # of the result, in bytes
+        for at in (lo - row, lo + row, lo + 32, hi - row, lo - 2 * n + 16):  # (rows on and back, part of a row)
+            with pytest.raises(pkv.PagedKVError, match="out overlaps q"):
+                pkv.paged_tree_attention(c.pool, put(q, at), *args, out=out)
+        for i in range(4):  # indptr, masks, tables, lengths: their last element in the result, and their first
+            size = args[i].numel() * args[i].element_size()
+            step = 8 if i == 1 else 4
+            for at in (lo - size + step, lo + 64, hi - step):
+                moved = [put(x, at) if j == i else x for j, x in enumerate(args[:4])]
+                with pytest.raises(pkv.PagedKVError, match="out overlaps an input"):
+                    pkv.paged_tree_attention(c.pool, q, *moved, args[4], out=out)
+                with pytest.raises(pkv.PagedKVError, match="out overlaps an input"):  # and over the queries
+                    pkv.paged_tree_attention(c.pool, out, *moved, args[4], out=out)
+        inside = c.pool._alloc_bytes_view(c.pool.layout())[4096:][:q.numel() * 2].view(torch.bfloat16).view(q.shape)
+        with pytest.raises(pkv.PagedKVError, match="out overlaps an input"):
+            pkv.paged_tree_attention(c.pool, q, *args, out=inside)
+        # next to one another is apart
+        for at in (lo - 2 * n, hi):
+            pkv.paged_tree_attention(c.pool, put(q, at), *args, out=out)
+            assert torch.equal(out, want)
+        for i in range(4):
+            size = args[i].numel() * args[i].element_size()
+            for at in (lo - size, hi):
+                moved = [put(x, at) if j == i else x for j, x in enumerate(args[:4])]
+                pkv.paged_tree_attention(c.pool, q, *moved, args[4], out=out)
+                assert torch.equal(out, want)
+        assert c.pool.get_error() == 0
