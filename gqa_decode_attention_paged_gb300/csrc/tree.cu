@@ -42,7 +42,7 @@
 //     each: S = Q K^T, and when the weights are written over S, O += P V.
 //   * the reference maximum is raised lazily (O is rescaled only when a row's
 //     maximum grows by more than 2^8).  Weights are rounded to bf16 (FP8 pools:
-//     f16) for the MMA; the sum adds them in fp32 as they were (adding the
+//     f16, times 2^7) for the MMA; the sum adds them in fp32 as they were (adding the
 //     rounded ones takes twice the additions, and makes no measurable difference
 //     against 64 bits).
 //   * FP8 pools: the E4M3 tiles are widened to f16 in place by four warps.
@@ -106,6 +106,11 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;
 constexpr uint32_t kHalf = 128 * 128;      // bytes of a 64-column range of a 128-row tile
 constexpr float kSlack = 8.0f;             // log2 of the largest weight before the reference maximum is raised
+// FP8 pools: log2 of a factor of all weights, which their sum has too.  f16 ends at 2^16, and loses bits below 2^-14: so
+// what weighs down to 2^-21 of the reference is held to 2^-11 of itself (2^-14 without; of many keys that weighed 2^-25
+// of the first one, nothing was left).
+constexpr float kLift = 7.0f;
+static_assert(kSlack + kLift < 16.0f, "weights beyond f16's range");
 
 // The unit that a CTA's slice has a part of and that goes on in the next one, for the merge.  more < 0: none.
 struct Part {
@@ -925,7 +930,8 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
                             m[0] = top[0];
                             m[1] = top[1];
                         }
-                        const float nm[2] = {m[0] == -INFINITY ? 0.0f : -m[0], m[1] == -INFINITY ? 0.0f : -m[1]};
+                        constexpr float lift = F8 ? kLift : 0.0f;
+                        const float nm[2] = {m[0] == -INFINITY ? 0.0f : lift - m[0], m[1] == -INFINITY ? 0.0f : lift - m[1]};
                         float2 part[2][2] = {};
 #pragma unroll
                         for (int j = 0; j < kTurn / 8; ++j) {

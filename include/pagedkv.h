@@ -567,8 +567,9 @@ pkv_status paged_diff_reserve_workspace(pkv_pool *pool, int32_t batch, int32_t n
  * by the rows that do not see it, whatever they hold (where nodes have values
  * that are not finite, the call takes longer: some microseconds a node).
  * The softmax statistics and the sums are held in fp32; weights are rounded
- * once, to bf16 (bf16 pools) or f16 (FP8 pools, whose queries are multiplied
- * as f16: |q| must stay in f16's range), and out once, to bf16.
+ * once, to bf16 (bf16 pools) or f16 (FP8 pools: by 2^-11 of themselves down to
+ * 2^-21 of a row's largest so far, by 2^-32 of that below; queries are
+ * multiplied as f16, too: |q| must stay in f16's range), and out once, to bf16.
  * bf16 and FP8 pools.  Two launches on the pool's workspace: equal slices of
  * the (sequence, KV head, step of 128 keys) stream on the tcgen05 tensor cores,
  * then a join of what was cut (tables of up to 64 blocks: the first alone).  Results of a call do not depend on timing, but

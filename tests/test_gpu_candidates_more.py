@@ -88,3 +88,36 @@ def test_results_that_share_memory_with_an_input_are_refused():
                 pkv.paged_tree_attention(c.pool, q, *moved, args[4], out=out)
                 assert torch.equal(out, want)
         assert c.pool.get_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("gap", [9.0, 13.0, 15.0, 17.5])
+@pytest.mark.parametrize("extra", [0, 200])
+def test_what_little_weight_many_keys_have_next_to_one_that_has_most(kv, d, gap, extra):
+    """The first key's score is `gap` above all others', and its value zero: the result is what the others add.
+    Their weights, 2^-13 to 2^-25 of the first's, are bf16 on a bf16 pool (2^-8 of themselves, over its whole range).
+    On an FP8 pool they are f16 after a factor of 2^7: 2^-11 of themselves down to 2^-21 of the first's, and half of
+    f16's smallest step below, 2^-25 2^-7 of the first's.  The sum is at least the first's own weight."""
+    lens, nodes = [1024, 1000, 17], [5, 40, 1]
+    with Cache(kv, 2, d, lens, seed=33, table_extra=extra) as c:
+        if kv == "fp8":
+            c.pool.set_fp8_scales(np.ones(2, np.float32), np.ones(2, np.float32))
+        c.k = torch.zeros(c.k.shape).to(c.k.dtype)
+        c.v = (1 + torch.rand(c.v.shape, generator=torch.Generator().manual_seed(33))).to(c.v.dtype)
+        for b in range(len(lens)):
+            c.k[int(c.tables[b, 0]), :, 0, 0] = 16.0
+            c.v[int(c.tables[b, 0]), :, 0] = 0.0
+        c.k64, c.v64 = c.k.double(), c.v.double()
+        c.upload()
+        q, args, bits, ip = trees(c, nodes, 4, 33)
+        q = torch.zeros_like(q)
+        q[..., 0] = 1.0
+        scale = float(np.float32(gap / 16.0))
+        got = pkv.paged_tree_attention(c.pool, q, *args[:-1], scale)
+        assert c.pool.get_error() == 0
+        ref, _ = plain(c, q, ip, bits, lens, scale)
+        e = (2.0 ** -8 if kv == "bf16" else 2.0 ** -11) + 2.0 ** -12
+        small = 0.0 if kv == "bf16" else 2.0 ** -32 * max(lens) * 2  # (values are below 2)
+        check(got, ref, 1.1 * (e * 2 * ref.abs() + small) + 2.0 ** -8 * ref.abs() + 1e-30)
