@@ -56,6 +56,7 @@
 // PKV_DEVERR_TIMEOUT, every role stops, the MMA and copy pipes are drained
 // (bounded) and the tensor memory is released before the CTA exits.
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <mutex>
 
@@ -857,7 +858,8 @@ __global__ void __launch_bounds__(Warps<F8>::kThreads, 1)
             const int t0 = p.r0 + (two ? x * kRows : 0) + row0;  // the warp's first local row
             const bool live = t0 < p.R;
             const int rel0 = p.s0 * kKeys - (p.C - p.T);         // the first step's first key, against the first node
-            const float qs = fabsf(a.qscale) * (F8 ? a.scales[p.g] : 1.0f), vs = F8 ? a.scales[a.n_kv + p.g] : 1.0f;
+            // (never 0, which times a hidden key's -inf would be NaN: a product below fp32's range is its least normal number)
+            const float qs = F8 ? fmaxf(fabsf(a.qscale) * a.scales[p.g], FLT_MIN) : fabsf(a.qscale), vs = F8 ? a.scales[a.n_kv + p.g] : 1.0f;
             const int32_t *trow = a.block_tables + (int64_t)p.b * a.W + p.s0 * kStepBlocks;
             const int blocks = p.blocks - p.s0 * kStepBlocks;
             const int hop = two ? 1 : 2, s1 = two ? 0 : 1 - x;

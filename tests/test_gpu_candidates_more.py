@@ -121,3 +121,19 @@ def test_what_little_weight_many_keys_have_next_to_one_that_has_most(kv, d, gap,
         e = (2.0 ** -8 if kv == "bf16" else 2.0 ** -11) + 2.0 ** -12
         small = 0.0 if kv == "bf16" else 2.0 ** -32 * max(lens) * 2  # (values are below 2)
         check(got, ref, 1.1 * (e * 2 * ref.abs() + small) + 2.0 ** -8 * ref.abs() + 1e-30)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("k_scale,scale", [(1e-16, 0.0), (1e-26, 1e-20), (1e-26, -1e-20), (1e-38, 1e-38), (1.0, 1e-45)])
+def test_scales_whose_product_is_below_fp32(k_scale, scale):
+    """Scores of zero to all that counts: what is visible weighs alike, what is not weighs nothing."""
+    lens, nodes = [300, 20, 2100], [20, 20, 70]
+    with Cache("fp8", 2, 64, lens, seed=34) as c:
+        v_scale = np.array([0.01, 0.02], np.float32)
+        c.pool.set_fp8_scales(np.full(2, k_scale, np.float32), v_scale)
+        c.k64 = torch.zeros_like(c.k64)
+        c.v64 = c.v.double() * torch.tensor(v_scale).double().view(1, 2, 1, 1)
+        q, args, bits, ip = trees(c, nodes, 4, 34)
+        got = pkv.paged_tree_attention(c.pool, q, *args[:-1], scale)
+        assert c.pool.get_error() == 0
+        check(got, *plain(c, q, ip, bits, lens, scale))
