@@ -562,7 +562,9 @@ pkv_status paged_diff_reserve_workspace(pkv_pool *pool, int32_t batch, int32_t n
  * than the masks have bits, more nodes than cached tokens, or a length past
  * its table is skipped and sets PKV_DEVERR_CTX_RANGE.  A block id outside the
  * pool counts as masked and sets PKV_DEVERR_BLOCK_RANGE.  A row that sees
- * nothing is zero, and a visible key whose score is -infinity weighs nothing.
+ * nothing is zero.  A visible key whose score is -infinity weighs nothing where
+ * its value is finite; a channel in which any visible key's value is not finite
+ * is not finite in the row's result (NaN or an infinity), whatever the scores.
  * Cached rows behind C_b are never used, and the keys and values of a node not
  * by the rows that do not see it, whatever they hold (where nodes have values
  * that are not finite, the call takes longer: some microseconds a node).

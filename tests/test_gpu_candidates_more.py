@@ -137,3 +137,39 @@ def test_scales_whose_product_is_below_fp32(k_scale, scale):
         got = pkv.paged_tree_attention(c.pool, q, *args[:-1], scale)
         assert c.pool.get_error() == 0
         check(got, *plain(c, q, ip, bits, lens, scale))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("extra", [0, 200])
+def test_values_that_are_not_finite_under_scores_of_minus_infinity(d, extra):
+    """Of a key in the context, of a node, and where a sequence has no other scores: those channels are not finite in
+    the rows that may see the key, and all else is as if the values were zero."""
+    lens, nodes = [300, 2500, 40, 1000], [20, 40, 40, 9]
+    # sequence, position, channels
+    odd = [(0, 5, [3]), (0, 290, [7, 9]), (1, 2000, [0, 1, 2]), (1, 2461, [60]), (1, 2499, [4, 5]), (2, 3, [8]), (2, 39, range(20, 64)), (3, 998, [11])]
+    with Cache("bf16", 2, d, lens, seed=35, table_extra=extra) as c:
+        at = lambda b, pos: (int(c.tables[b, pos // BS]), slice(None), pos % BS)  # noqa: E731
+        for b, pos, _ in odd + [(2, p, None) for p in range(40)]:  # (all scores of sequence 2 are)
+            c.k[at(b, pos)] = c.k[at(b, pos)].index_fill(1, torch.tensor([0]), -math.inf)
+        c.k64, c.v64 = c.k.double(), c.v.double()
+        q, args, bits, ip = trees(c, nodes, 4, 35)
+        q[..., 0] = 1
+        hit = torch.zeros(sum(nodes), 8, d, dtype=torch.bool)
+        for i, (b, pos, channels) in enumerate(odd):
+            v = torch.zeros(2, d)
+            v[:, list(channels)] = [math.inf, -math.inf, math.nan][i % 3]
+            c.v[at(b, pos)] = torch.where(v == 0, c.v[at(b, pos)].float(), v).to(torch.bfloat16)
+            c.v64[at(b, pos)] = torch.where(v == 0, c.v64[at(b, pos)], 0.0)
+            node = pos - (lens[b] - nodes[b])
+            for r in range(ip[b], ip[b + 1]):
+                if node < 0 or (bits[r] >> node) & 1:
+                    hit[r][:, list(channels)] = True
+        c.upload()
+        got = pkv.paged_tree_attention(c.pool, q, *args).cpu()
+        assert c.pool.get_error() == 0
+        assert hit.any() and not hit.all()
+        assert torch.equal(~torch.isfinite(got), hit)
+        ref, bound = plain(c, q, ip, bits, lens, args[-1])
+        check(torch.where(hit, 0, got), torch.where(hit, 0, ref), bound)
+        assert (got[ip[2]:ip[3]][~hit[ip[2]:ip[3]]] == 0).all()
