@@ -793,7 +793,9 @@ def paged_beam_reorder(pool: Pool, parents, block_tables, context_lens, spare_bl
     beam that each new one goes on from (-1: none); block_tables: int32
     [B * beams, W]; context_lens: int32 [B * beams]; spare_blocks: int32
     [B * k].  A parent's first new beam keeps its unfilled block, the others get
-    their spare block, into which the filled rows are copied.  Returns
+    their spare block, into which the filled rows are copied; different parents
+    must not have the same unfilled block (a prompt's, copied to every beam's
+    table: one of them alone goes on at the first step).  Returns
     (tables_out int32 [B * k, W], lens_out int32 [B * k]), allocated if not
     given."""
     import torch

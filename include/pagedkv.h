@@ -656,14 +656,19 @@ pkv_status paged_beam_reserve_workspace(pkv_pool *pool, int32_t batch, int32_t b
  * next, must be its own: the parent's first new beam keeps the parent's entry
  * (filled or not yet given); every other one gets spare_blocks[b][i], into
  * which the L % 16 filled rows are copied.  Entries behind it become -1.
+ * Beams that new ones go on from must not have the same block there (unchecked:
+ * the first child of each would keep it, and what one appends would overwrite
+ * the other's): a table that is copied to several beams, as a prompt's is, may
+ * be gone on from by one of them alone (scores of -infinity for the others in
+ * paged_beam_select), or gets blocks of its own first (kv_block_copy).
  *   parents       device int32 [batch][k]; -1: no beam (its table becomes -1,
  *                 its length 0).
  *   block_tables  device int32 [batch * beams][max_blocks_per_seq].
  *   context_lens  device int32 [batch * beams].
  *   spare_blocks  device int32 [batch * k]: free blocks, no id twice, none in a
  *                 table (unchecked).  Which were taken follows from parents: a
- *                 first new beam's, and a full table's (L / 16 =
- *                 max_blocks_per_seq), stays free.
+ *                 first new beam's, that of one with no parent, and a full
+ *                 table's (L / 16 = max_blocks_per_seq) stay free.
  *   tables_out    device int32 [batch * k][max_blocks_per_seq], lens_out device
  *                 int32 [batch * k]; must overlap neither each other nor an
  *                 input.

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import gqa_decode_attention_paged_gb300 as pkv
+from test_gpu_moves import Bytes, reorder
 from tree_ref import BS, Cache, check, pack, parents_of, plain, tree_bits
 
 
@@ -173,3 +174,33 @@ def test_values_that_are_not_finite_under_scores_of_minus_infinity(d, extra):
         ref, bound = plain(c, q, ip, bits, lens, args[-1])
         check(torch.where(hit, 0, got), torch.where(hit, 0, ref), bound)
         assert (got[ip[2]:ip[3]][~hit[ip[2]:ip[3]]] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "int4"])
+@pytest.mark.parametrize("length", [1, 16, 37, 80])
+def test_the_first_step_of_beams_that_share_a_prompt(kv, length):
+    """Every beam's table is the prompt's, its unfilled block among them; one beam goes on, the others' scores are
+    -infinity.  Afterwards each new beam has a block of its own to write."""
+    searches, beams = 3, 4
+    rng = random.Random(36)
+    W = length // BS + 1
+    ids = rng.sample(range(40), 40)
+    table = np.array([ids[b * W:(b + 1) * W] for b in range(searches) for _ in range(beams)], np.int32)
+    spare = ids[searches * W:searches * W + searches * beams]
+    scores = torch.full((searches, beams), -math.inf)
+    logits = torch.randn(searches, 1, 50, generator=torch.Generator().manual_seed(36)).expand(-1, beams, -1).contiguous()
+    alive = [0, 2, 3]
+    for b, j in enumerate(alive):
+        scores[b, j] = 0.0
+    with Bytes(kv, 2, 64, 40) as m:
+        tokens, parents, _ = pkv.paged_beam_select(m.pool, logits.cuda(), scores.cuda(), beams)
+        assert parents.tolist() == [[j] * beams for j in alive]
+        assert tokens.tolist() == logits[:, 0].double().sort(dim=-1, descending=True, stable=True)[1][:, :beams].tolist()
+        got, after = pkv.paged_beam_reorder(m.pool, parents, i32(table), i32([length] * len(table)), i32(spare))
+        want, lens = reorder(m, parents.tolist(), table, [length] * len(table), spare, beams)
+        m.check()
+        assert got.tolist() == want and after.tolist() == lens == [length] * len(table)
+        writes = [t[length // BS] for t in got.tolist()]
+        assert len(set(writes)) == len(writes)
+        assert m.pool.get_error() == 0
