@@ -150,7 +150,7 @@ struct Shared {
 
 __device__ __forceinline__ uint64_t max64(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
-// Raises sh.bar to the k-th greatest of the groups' greatest keys (of `mine`, 0: none; 16 p groups of 32 / p
+// Raises sh.bar to the k-th greatest of the groups' greatest keys (of `mine`, 0: none; 8 p groups of 32 / p
 // neighbouring threads), if that many groups have one.  At least k of the threads' keys reach it, and those that
 // do belong to k groups.
 __device__ __forceinline__ void raise_bar(Shared &sh, uint64_t mine, int k, int p)

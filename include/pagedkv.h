@@ -574,9 +574,10 @@ pkv_status paged_diff_reserve_workspace(pkv_pool *pool, int32_t batch, int32_t n
  * multiplied as f16, too: |q| must stay in f16's range), and out once, to bf16.
  * bf16 and FP8 pools.  Two launches on the pool's workspace: equal slices of
  * the (sequence, KV head, step of 128 keys) stream on the tcgen05 tensor cores,
- * then a join of what was cut (tables of up to 64 blocks: the first alone).  Results of a call do not depend on timing, but
- * may differ in rounding between calls of different batches.  Other arguments,
- * group sizes and limits as paged_prefill_attention.
+ * then a join of what was cut (tables of up to 64 blocks: the first alone).
+ * Results of a call do not depend on timing, but may differ in rounding between
+ * calls of different batches and of tables of different widths.  Other
+ * arguments, group sizes and limits as paged_prefill_attention.
  * Errors: EINVAL (also an out that overlaps an input without being q, and a
  * workspace that would have to grow while `stream` is captured), EUNSUPPORTED
  * (4-bit pools, group size, mask_words, too many query rows), ENOMEM, ECUDA. */
@@ -610,7 +611,9 @@ pkv_status paged_tree_reserve_workspace(pkv_pool *pool, int64_t n_rows, int32_t 
  * clamped to the table) and sets PKV_DEVERR_CTX_RANGE; a row from or to a block
  * outside the pool is not moved and sets PKV_DEVERR_BLOCK_RANGE.  The blocks of
  * a sequence's nodes must not be shared with another sequence (as for any
- * append).  All pool types.  One launch, counted with the block launches.
+ * append).  All pool types; there is no attention of trees on a 4-bit pool here
+ * (paged_tree_attention refuses it): there the call serves who verifies them
+ * otherwise.  One launch, counted with the block launches.
  * Errors: EINVAL, ECUDA. */
 pkv_status paged_tree_commit(pkv_pool *pool, const int32_t *qo_indptr, const int32_t *accepted, int32_t max_accepted,
                              const int32_t *n_accepted, const int32_t *block_tables, int32_t max_blocks_per_seq,
