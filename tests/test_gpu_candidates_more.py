@@ -204,3 +204,15 @@ def test_the_first_step_of_beams_that_share_a_prompt(kv, length):
         writes = [t[length // BS] for t in got.tolist()]
         assert len(set(writes)) == len(writes)
         assert m.pool.get_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("lens,nodes,G", [([131072], [2], 4), ([70000], [90], 4), ([66000, 40000], [3, 40], 1)])
+def test_units_in_more_parts_than_a_warp_joins_at_once(kv, lens, nodes, G):
+    """One KV head and few rows: a unit's parts are in tens of slices, up to all of them."""
+    with Cache(kv, 1, 64, lens, seed=37) as c:
+        q, args, bits, ip = trees(c, nodes, G, 37)
+        got = pkv.paged_tree_attention(c.pool, q, *args)
+        assert c.pool.get_error() == 0
+        check(got, *plain(c, q, ip, bits, lens, args[-1]))
