@@ -6,12 +6,15 @@
 // a row v grows with x, so a row's candidates are its k greatest logits, and
 // only those need v.
 //
-// What bounds it: HBM, the logits read once; close behind it the instructions
-// (about five per logit).  One launch: a scan of the rows, cut into pieces so that
-// every SM has three blocks where the rows are few, leaves each piece's maximum,
-// sum of exponentials and k greatest logits; the block that is the last of a
-// search to get there merges them (as a second launch that took the GPU as long,
-// and the host 20 us a call instead of 15).
+// What bounds it: HBM, the logits read once, and the instructions: 11 per logit in
+// bf16 (64 x 4 x 128256), 19 in fp32 where rows begin anywhere (32 x 10 x 100277),
+// all steps counted, 43 and 47 % of the issue slots while an SM has work, which it
+// has for 70 and 65 % of the time: with more rows than SMs they are not cut, and
+// some SMs have one more than others.  One launch: a scan of the rows, cut into
+// pieces so that every SM has three blocks where the rows are few, leaves each
+// piece's maximum, sum of exponentials and k greatest logits; the block that is
+// the last of a search to get there merges them (as a second launch that took the
+// GPU as long, and the host 20 us a call instead of 15).
 //
 // Reading.  A piece streams through a ring of three parts of 16 KiB in shared
 // memory (bulk copies: a vector a thread ahead kept 64 KiB in flight on an SM and

@@ -9,9 +9,12 @@
 // i * G + h.  One pass over the keys with a running maximum and sum; a key
 // that a row does not see has score -infinity.
 //
-// What bounds it: HBM, while a KV head's rows are few (the cache is read once,
-// 4 d rows operations for every 4 d bytes of a bf16 key and value), the tensor
-// cores and the exponentials from about 256 rows on.
+// What bounds it: HBM, while a KV head's rows are few (up to 256 of them read the
+// cache once, 4 d rows operations for every 4 d bytes of a bf16 key and value),
+// the tensor cores and the exponentials from about 256 rows on.  Every further
+// 256 rows of a KV head read the cache again: they follow one another in the
+// stream, and the L2 has little left of what the first ones read (64 nodes on
+// 16 x 8192 tokens, 512 rows a KV head: 1087 MB from HBM for 531 MB of cache).
 //
 // Design (one persistent CTA per SM, warp-specialised):
 //   * a unit is up to 256 rows (two tiles of 128) of one (sequence, KV head).
@@ -91,7 +94,9 @@ static_assert(kMinShare >= kCostUnit + kCostTwo, "");
 //     1536, 2048 tokens (22, 30, 38): 73 / 65, 85.7 / 84.2, 99.9 / 102.9; 1024 units on 1536: 152 / 156.
 constexpr int kCostCut = 18, kCostSmall = 30;
 // And where tables have no more steps than this, so that the join need not be launched: with tables of 1024 tokens 8, 32,
-// 512 units take 15.9 / 15.9, 20.0 / 16.3, 73 / 66; with 1536, 15.2 / 20.1, 20.5 / 20.1, 86 / 86.
+// 512 units take 15.9 / 15.9, 20.0 / 16.3, 73 / 66; with 1536, 15.2 / 20.1, 20.5 / 20.1, 86 / 86.  (The table's width decides,
+// as the host does not see the lengths: 8 nodes on 300 tokens take 8.7 us in a graph with a table of 19 blocks, 9.0 with 64,
+// 10.0 with 65 and 10.3 with 2048.)
 constexpr int kWholeSteps = 8;
 template <bool F8>
 struct Warps {
