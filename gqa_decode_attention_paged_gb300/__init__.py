@@ -706,7 +706,8 @@ def paged_tree_attention(pool: Pool, q, qo_indptr, tree_mask, block_tables, cont
     where the row sees its sequence's node j (all see the context before the
     nodes); block_tables: int32 [B, W]; context_lens: int32 [B] (including the
     nodes, which are the last entries of the cache).  Returns ``out`` (bf16
-    [rows, n_q, d_head], allocated if not given)."""
+    [rows, n_q, d_head], allocated if not given; ``q`` itself, or apart from all
+    inputs)."""
     import torch
 
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
